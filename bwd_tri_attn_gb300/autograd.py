@@ -14,7 +14,10 @@ backward passes are differentiable once (no second derivatives).
 - ``triangle_attention_block(z, gamma, beta, W, wb, Wo, mask, H, d, node, eps)`` and
   ``TriangleAttentionBlock``: the surrounding block (include/tri_module.h). The weights may be FP32
   masters: the forward uses their BF16 rounding (as mixed-precision training does) and the
-  backward returns the library's FP32 weight gradients in the masters' dtype.
+  backward returns the library's FP32 weight gradients in the masters' dtype. With ``checkpoint``
+  the block keeps its input in 8 bits and recomputes.
+- ``layer_norm(x, gamma, beta, eps, checkpoint=False)``: LayerNorm (include/tri_norm.h), gradients
+  for x and the weights; with ``checkpoint`` it keeps x in 8 bits for the backward pass.
 """
 from __future__ import annotations
 
@@ -78,43 +81,84 @@ def triangle_multiplication(Pa, Ga, Pb, Gb, incoming=False, layout=tb.LAYOUT_PAI
 
 class _TriangleAttentionBlock(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, z, gamma, beta, W, wb, Wo, mask, H, d, node, eps):
+    def forward(ctx, z, gamma, beta, W, wb, Wo, mask, H, d, node, eps, checkpoint):
         z = z.contiguous()
         mask = None if mask is None else mask.contiguous()
         bf = [t.to(torch.bfloat16).contiguous() for t in (W, wb, Wo)]
         g32, b32 = gamma.float().contiguous(), beta.float().contiguous()
         out, saved = tb.module_forward(z, g32, b32, *bf, mask, H, d, node=node, eps=eps)
         ctx.meta = (H, d, node, eps, [t.dtype for t in (gamma, beta, W, wb, Wo)])
-        ctx.save_for_backward(z, g32, b32, *bf, mask, saved)
+        ctx.kept_in_8_bits = checkpoint
+        ctx.save_for_backward(g32, b32, *bf, mask, *(tb.checkpoint_pack(z) if checkpoint else (z, saved)))
         return out
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dout):
-        z, g32, b32, W, wb, Wo, mask, saved = ctx.saved_tensors
+        g32, b32, W, wb, Wo, mask, *kept = ctx.saved_tensors
         H, d, node, eps, dtypes = ctx.meta
+        if ctx.kept_in_8_bits:
+            z = tb.checkpoint_unpack(kept)
+            _, saved = tb.module_forward(z, g32, b32, W, wb, Wo, mask, H, d, node=node, eps=eps)
+        else:
+            z, saved = kept
         grads = tb.module_backward(z, g32, b32, W, wb, Wo, mask, saved, dout.to(torch.bfloat16).contiguous(),
                                    H, d, node=node, eps=eps)
         dz = grads[0]
         wgrads = [g.to(dt) for g, dt in zip(grads[1:], dtypes)]
-        return (dz, *wgrads, None, None, None, None, None)
+        return (dz, *wgrads, None, None, None, None, None, None)
 
 
-def triangle_attention_block(z, gamma, beta, W, wb, Wo, mask, H, d, node=tb.NODE_STARTING, eps=1e-5):
+def triangle_attention_block(z, gamma, beta, W, wb, Wo, mask, H, d, node=tb.NODE_STARTING, eps=1e-5,
+                             checkpoint=False):
     """The triangle-attention block on the BF16 pair representation z [B, N, N, c]: LayerNorm
     (gamma, beta [c]), projections W [4 H d, c] (q, k, v, gate rows) and wb [H, c], the attention,
-    the sigmoid gate and the output projection Wo [c, H d]."""
-    return _TriangleAttentionBlock.apply(z, gamma, beta, W, wb, Wo, mask, H, d, node, eps)
+    the sigmoid gate and the output projection Wo [c, H d].
+
+    With ``checkpoint`` the block keeps z in 8 bits (one byte and 1/32 of an FP32 scale a value) in
+    the place of z and its activations (at least 4 c + 14 H d bytes a pair position), and the backward
+    pass recomputes them: its gradients are those of the block at the checkpoint's values of z."""
+    return _TriangleAttentionBlock.apply(z, gamma, beta, W, wb, Wo, mask, H, d, node, eps, checkpoint)
+
+
+class _LayerNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, gamma, beta, eps, checkpoint):
+        x = x.contiguous()
+        g32, b32 = (None if t is None else t.float().contiguous() for t in (gamma, beta))
+        y, mean, rstd, *kept = tb.norm_forward(x, g32, b32, eps=eps, checkpoint=checkpoint)
+        ctx.kept_in_8_bits = checkpoint
+        ctx.dtypes = tuple(None if t is None else t.dtype for t in (gamma, beta))
+        ctx.save_for_backward(g32, mean, rstd, *(kept[0] if checkpoint else (x,)))
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        g32, mean, rstd, *kept = ctx.saved_tensors
+        x = tb.Checkpoint(*kept) if ctx.kept_in_8_bits else kept[0]
+        if g32 is None and ctx.dtypes[1] is not None:  # (beta alone: its gradient is taken with gamma = 1)
+            g32 = torch.ones(dy.shape[-1], dtype=torch.float32, device=dy.device)
+        grads = tb.norm_backward(x, g32, mean, rstd, dy.contiguous())
+        wgrads = (None if dt is None else g.to(dt) for g, dt in zip(grads[1:], ctx.dtypes))
+        return (grads[0], *wgrads, None, None)
+
+
+def layer_norm(x, gamma=None, beta=None, eps=1e-5, checkpoint=False):
+    """LayerNorm over the last axis of x [..., C] (BF16, FP16 or FP32; FP32 statistics and weights).
+    With ``checkpoint`` the backward pass reads an 8-bit checkpoint of x in the place of x."""
+    return _LayerNorm.apply(x, gamma, beta, eps, checkpoint)
 
 
 class TriangleAttentionBlock(torch.nn.Module):
     """The triangle-attention block as a module with FP32 master parameters (initialised like the
-    seeded test inputs: gamma 1, beta 0, W and wb normal / sqrt(c), Wo normal / sqrt(H d))."""
+    seeded test inputs: gamma 1, beta 0, W and wb normal / sqrt(c), Wo normal / sqrt(H d)).
+    ``checkpoint``: keep the input in 8 bits and recompute the activations in the backward pass."""
 
     def __init__(self, c: int = 128, H: int = 4, d: int = 32, node: int = tb.NODE_STARTING, eps: float = 1e-5,
-                 device=None):
+                 device=None, checkpoint: bool = False):
         super().__init__()
-        self.c, self.H, self.d, self.node, self.eps = c, H, d, node, eps
+        self.c, self.H, self.d, self.node, self.eps, self.checkpoint = c, H, d, node, eps, checkpoint
         f32 = dict(dtype=torch.float32, device=device)
         self.gamma = torch.nn.Parameter(torch.ones(c, **f32))
         self.beta = torch.nn.Parameter(torch.zeros(c, **f32))
@@ -124,4 +168,4 @@ class TriangleAttentionBlock(torch.nn.Module):
 
     def forward(self, z, mask=None):
         return triangle_attention_block(z, self.gamma, self.beta, self.W, self.wb, self.Wo, mask, self.H, self.d,
-                                        self.node, self.eps)
+                                        self.node, self.eps, self.checkpoint)

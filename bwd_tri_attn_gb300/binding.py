@@ -1,5 +1,5 @@
-"""Thin ctypes binding of the C ABI in ``include/tri_attn.h``, ``include/tri_mul.h`` and
-``include/tri_module.h``.
+"""Thin ctypes binding of the C ABI in ``include/tri_attn.h``, ``include/tri_mul.h``,
+``include/tri_module.h`` and ``include/tri_norm.h``.
 
 Argument marshalling only: PyTorch tensors supply device pointers and the
 current CUDA stream; every step of the computation runs in the library's
@@ -12,6 +12,7 @@ import ctypes
 import math
 import os
 import threading
+from typing import NamedTuple
 
 import torch
 
@@ -44,7 +45,8 @@ _VP = ctypes.c_void_p
 EXPORTS = ("tri_attn_strerror", "tri_attn_fwd", "tri_attn_bwd_workspace_size", "tri_attn_bwd_split", "tri_attn_bwd",
            "tri_attn_device_status", "tri_attn_set_timing_events", "tri_attn_bwd_static", "tri_mul_fwd",
            "tri_mul_bwd_workspace_size", "tri_mul_bwd", "tri_module_saved_size", "tri_module_bwd_workspace_size",
-           "tri_module_fwd", "tri_module_bwd")
+           "tri_module_fwd", "tri_module_bwd", "tri_norm_fwd", "tri_norm_bwd_workspace_size", "tri_norm_bwd",
+           "tri_ckpt_pack", "tri_ckpt_unpack")
 
 
 LAYOUT_PAIR, LAYOUT_CHANNEL_MAJOR = 0, 1  # tri_mul_shape.layout
@@ -69,6 +71,27 @@ class ModuleShape(ctypes.Structure):
     def __repr__(self):
         return (f"ModuleShape(B={self.B}, N={self.N}, c={self.c}, H={self.H}, d={self.d}, node={self.node}, "
                 f"eps={self.eps})")
+
+
+DTYPE_BF16, DTYPE_FP16, DTYPE_FP32 = 0, 1, 2  # tri_norm_shape.dtype
+CKPT_GROUP = 128  # channels that share a scale in an 8-bit checkpoint
+
+
+class NormShape(ctypes.Structure):
+    """tri_norm_shape: rows, row strides of x and dy in elements (0: C), channels, dtype, LayerNorm eps."""
+    _fields_ = [("M", ctypes.c_int64), ("ldx", ctypes.c_int64), ("lddy", ctypes.c_int64), ("C", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("eps", ctypes.c_float)]
+
+    def __repr__(self):
+        return (f"NormShape(M={self.M}, ldx={self.ldx}, lddy={self.lddy}, C={self.C}, dtype={self.dtype}, "
+                f"eps={self.eps})")
+
+
+class Checkpoint(NamedTuple):
+    """An activation kept in 8 bits: q8 (int8, the activation's shape) and the FP32 scales of its groups of 128
+    channels ([..., (C + 127) // 128]); it stands for q8 * scale."""
+    q8: torch.Tensor
+    scale: torch.Tensor
 
 
 def lib_path() -> str:
@@ -116,6 +139,16 @@ def load(path: str | None = None):
         lib.tri_module_fwd.restype = ctypes.c_int
         lib.tri_module_bwd.argtypes = [ModuleShape] + [_VP] * 8 + [ctypes.c_size_t] + [_VP] * 8 + [ctypes.c_size_t, _VP]
         lib.tri_module_bwd.restype = ctypes.c_int
+        lib.tri_norm_fwd.argtypes = [NormShape] + [_VP] * 9
+        lib.tri_norm_fwd.restype = ctypes.c_int
+        lib.tri_norm_bwd_workspace_size.argtypes = [NormShape]
+        lib.tri_norm_bwd_workspace_size.restype = ctypes.c_size_t
+        lib.tri_norm_bwd.argtypes = [NormShape] + [_VP] * 11 + [ctypes.c_size_t, _VP]
+        lib.tri_norm_bwd.restype = ctypes.c_int
+        lib.tri_ckpt_pack.argtypes = [NormShape] + [_VP] * 4
+        lib.tri_ckpt_pack.restype = ctypes.c_int
+        lib.tri_ckpt_unpack.argtypes = [NormShape] + [_VP] * 4
+        lib.tri_ckpt_unpack.restype = ctypes.c_int
         _lib = lib
     return _lib
 
@@ -295,6 +328,109 @@ def tri_module_bwd(shape: ModuleShape, z, gamma, beta, W, wb, Wo, mask, saved, d
     _check("tri_module_bwd", rc)
 
 
+_NORM_DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_FP16, torch.float32: DTYPE_FP32}
+
+
+def _norm_dtype(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
+    if t.dtype not in _NORM_DTYPES:
+        raise TypeError(f"{name} must be bfloat16, float16 or float32, got {t.dtype}")
+    return _NORM_DTYPES[t.dtype]
+
+
+def _row_stride(t, name):
+    """Elements between the rows of `t` [..., C] when its rows are contiguous and evenly spaced."""
+    if t.is_contiguous():
+        return t.shape[-1]
+    ld, expect = None, None
+    if t.shape[-1] == 1 or t.stride(-1) == 1:
+        for n, s in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+            if n == 1:
+                continue
+            if ld is None:
+                ld = s
+            elif s != expect:
+                ld = -1
+                break
+            expect = s * n
+    if ld is None or ld < t.shape[-1]:
+        raise ValueError(f"{name} must have contiguous, evenly spaced rows, got strides {t.stride()} for shape "
+                         f"{tuple(t.shape)}")
+    return ld
+
+
+def _rows_arg(t, name, dtype, numel):
+    """As _arg, for a tensor whose rows may be spaced apart (_row_stride has checked them)."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.numel() != numel:
+        raise ValueError(f"{name} has {t.numel()} elements, the shape needs {numel}")
+    return (name, t)
+
+
+def _norm_counts(shape):
+    return shape.M * shape.C, shape.M * ((shape.C + CKPT_GROUP - 1) // CKPT_GROUP)
+
+
+_TORCH_DTYPES = {v: k for k, v in _NORM_DTYPES.items()}
+
+
+def _spaced_arg(t, name, dtype, shape, ld):
+    """An [M, C] tensor argument with `ld` elements between its rows (0: C)."""
+    if ld in (0, shape.C):
+        return _arg(t, name, dtype, shape.M * shape.C)
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
+    if _row_stride(t, name) != ld or t.shape[-1] != shape.C:
+        raise ValueError(f"{name}'s rows are not the {ld} elements apart that the shape gives")
+    return _rows_arg(t, name, dtype, shape.M * shape.C)
+
+
+def tri_norm_fwd(shape: NormShape, x, gamma, beta, y, mean, rstd, q8=None, scale=None, stream=None):
+    n, ng = _norm_counts(shape)
+    dt = _TORCH_DTYPES.get(shape.dtype)
+    ptrs = _ptrs(_spaced_arg(x, "x", dt, shape, shape.ldx), _arg(gamma, "gamma", _F32, shape.C, True),
+                 _arg(beta, "beta", _F32, shape.C, True), _arg(y, "y", dt, n), _arg(mean, "mean", _F32, shape.M),
+                 _arg(rstd, "rstd", _F32, shape.M), _arg(q8, "q8", torch.int8, n, True),
+                 _arg(scale, "scale", _F32, ng, True))
+    rc = load().tri_norm_fwd(shape, *ptrs, _stream(stream))
+    _check("tri_norm_fwd", rc)
+
+
+def tri_norm_bwd_workspace_size(shape: NormShape) -> int:
+    return int(load().tri_norm_bwd_workspace_size(shape))
+
+
+def tri_norm_bwd(shape: NormShape, x, q8, scale, gamma, mean, rstd, dy, dx, dgamma, dbeta, workspace, stream=None):
+    n, ng = _norm_counts(shape)
+    dt = _TORCH_DTYPES.get(shape.dtype)
+    ptrs = _ptrs(None if x is None else _spaced_arg(x, "x", dt, shape, shape.ldx),
+                 _arg(q8, "q8", torch.int8, n, True), _arg(scale, "scale", _F32, ng, True),
+                 _arg(gamma, "gamma", _F32, shape.C, True), _arg(mean, "mean", _F32, shape.M),
+                 _arg(rstd, "rstd", _F32, shape.M), _spaced_arg(dy, "dy", dt, shape, shape.lddy),
+                 _arg(dx, "dx", dt, n), _arg(dgamma, "dgamma", _F32, shape.C, True),
+                 _arg(dbeta, "dbeta", _F32, shape.C, True), _arg(workspace, "workspace", None, None, True))
+    rc = load().tri_norm_bwd(shape, *ptrs, _nbytes(workspace), _stream(stream))
+    _check("tri_norm_bwd", rc)
+
+
+def tri_ckpt_pack(shape: NormShape, x, q8, scale, stream=None):
+    n, ng = _norm_counts(shape)
+    ptrs = _ptrs(_spaced_arg(x, "x", _TORCH_DTYPES.get(shape.dtype), shape, shape.ldx),
+                 _arg(q8, "q8", torch.int8, n), _arg(scale, "scale", _F32, ng))
+    rc = load().tri_ckpt_pack(shape, *ptrs, _stream(stream))
+    _check("tri_ckpt_pack", rc)
+
+
+def tri_ckpt_unpack(shape: NormShape, q8, scale, x, stream=None):
+    n, ng = _norm_counts(shape)
+    ptrs = _ptrs(_arg(q8, "q8", torch.int8, n), _arg(scale, "scale", _F32, ng),
+                 _arg(x, "x", _TORCH_DTYPES.get(shape.dtype), n))
+    rc = load().tri_ckpt_unpack(shape, *ptrs, _stream(stream))
+    _check("tri_ckpt_unpack", rc)
+
+
 def tri_attn_device_status(stream=None) -> int:
     return int(load().tri_attn_device_status(_stream(stream)))
 
@@ -409,3 +545,75 @@ def module_backward(z, gamma, beta, W, wb, Wo, mask, saved, dout, H, d, node=NOD
     tri_module_bwd(shape, z, gamma, beta, W, wb, Wo, mask, saved, dout, dz, dgamma, dbeta, dW, dwb, dWo, workspace,
                    stream)
     return dz, dgamma, dbeta, dW, dwb, dWo
+
+
+def norm_shape_of(x: torch.Tensor, eps: float = 1e-5, dy: torch.Tensor | None = None) -> NormShape:
+    """Shape of LayerNorm over the last axis of x [..., C] (and of the row strides of x and dy)."""
+    dtype = _norm_dtype(x, "x")
+    if x.dim() < 1 or x.numel() == 0:
+        raise ValueError(f"x must have at least one row and one channel, got shape {tuple(x.shape)}")
+    C = x.shape[-1]
+    return NormShape(x.numel() // C, _row_stride(x, "x"), C if dy is None else _row_stride(dy, "dy"), C, dtype,
+                     float(eps))
+
+
+def _empty_checkpoint(x):
+    return Checkpoint(torch.empty(x.shape, dtype=torch.int8, device=x.device),
+                      torch.empty((*x.shape[:-1], (x.shape[-1] + CKPT_GROUP - 1) // CKPT_GROUP), dtype=torch.float32,
+                                  device=x.device))
+
+
+def norm_forward(x, gamma=None, beta=None, eps=1e-5, checkpoint=False, stream=None):
+    """LayerNorm over the last axis of x [..., C]: returns (y, mean, rstd), y in x's dtype and the FP32 statistics
+    [...]; with ``checkpoint`` also the 8-bit checkpoint of x, written in the same pass."""
+    shape = norm_shape_of(x, eps)
+    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    stats = torch.empty((2, *x.shape[:-1]), dtype=torch.float32, device=x.device)
+    mean, rstd = stats[0], stats[1]
+    if not checkpoint:
+        tri_norm_fwd(shape, x, gamma, beta, y, mean, rstd, stream=stream)
+        return y, mean, rstd
+    kept = _empty_checkpoint(x)
+    tri_norm_fwd(shape, x, gamma, beta, y, mean, rstd, kept.q8, kept.scale, stream)
+    return y, mean, rstd, kept
+
+
+def norm_backward(x, gamma, mean, rstd, dy, workspace=None, stream=None):
+    """Returns (dx, dgamma, dbeta): dx in dy's dtype, the weight gradients FP32 (None when gamma is None, the
+    LayerNorm without weights). ``x`` is the forward's input or its ``Checkpoint``; mean and rstd are the forward's."""
+    dtype = _norm_dtype(dy, "dy")
+    kept = x if isinstance(x, tuple) else None
+    like = kept[0] if kept is not None else x
+    if not isinstance(like, torch.Tensor) or like.shape != dy.shape:
+        raise ValueError(f"dy {tuple(dy.shape)} must have x's shape")
+    if dy.dim() < 1 or dy.numel() == 0:
+        raise ValueError(f"dy must have at least one row and one channel, got shape {tuple(dy.shape)}")
+    C = dy.shape[-1]
+    shape = NormShape(dy.numel() // C, C if kept is not None else _row_stride(x, "x"), _row_stride(dy, "dy"), C, dtype,
+                      0.0)
+    dx = torch.empty(dy.shape, dtype=dy.dtype, device=dy.device)
+    dgamma = dbeta = None
+    if gamma is not None:
+        grads = torch.empty((2, C), dtype=torch.float32, device=dy.device)
+        dgamma, dbeta = grads[0], grads[1]
+        if workspace is None:
+            workspace = torch.empty(max(tri_norm_bwd_workspace_size(shape), 16), dtype=torch.uint8, device=dy.device)
+    tri_norm_bwd(shape, None if kept is not None else x, *(kept if kept is not None else (None, None)), gamma, mean,
+                 rstd, dy, dx, dgamma, dbeta, workspace, stream)
+    return dx, dgamma, dbeta
+
+
+def checkpoint_pack(x, stream=None) -> Checkpoint:
+    """x [..., C] kept in 8 bits: int8 values and one FP32 scale for every 128 channels of a row."""
+    shape = norm_shape_of(x)
+    kept = _empty_checkpoint(x)
+    tri_ckpt_pack(shape, x, kept.q8, kept.scale, stream)
+    return kept
+
+
+def checkpoint_unpack(kept, dtype=torch.bfloat16, stream=None) -> torch.Tensor:
+    """The values a checkpoint stands for, rounded once to ``dtype``."""
+    q8, scale = kept
+    x = torch.empty(q8.shape, dtype=dtype, device=q8.device)
+    tri_ckpt_unpack(norm_shape_of(x), q8, scale, x, stream)
+    return x

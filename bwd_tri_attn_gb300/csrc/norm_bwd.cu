@@ -1,0 +1,290 @@
+// LayerNorm backward (include/tri_norm.h states the formulas), reading x or its 8-bit checkpoint.
+//
+// A CTA takes a fixed chunk of rows. A row's x (or checkpoint) and dy are read once into registers,
+// the two row sums of dx come from there, and every thread adds dy xh and dy of its own columns
+// into registers: dgamma and dbeta cost no second pass. The CTAs' partial sums are added by a
+// second kernel in a fixed order, without atomics, so the same call gives the same bits. The next
+// row's loads are issued before the current row's sums (memory bandwidth bounds the kernel).
+#include <algorithm>
+
+#include "norm.cuh"
+
+namespace triattn {
+namespace {
+
+template <typename XT, int T, int NV, bool AL>
+__global__ void __launch_bounds__(T > 32 ? T : 256)
+    norm_bwd_kernel(const XT *__restrict__ x, int64_t ldx, const int8_t *__restrict__ q8, const float *__restrict__ s8,
+                    const float *__restrict__ gamma, const float *__restrict__ mean, const float *__restrict__ rstd,
+                    const XT *__restrict__ dy, int64_t lddy, int64_t M, int C, int64_t rpc, XT *__restrict__ dx,
+                    float *__restrict__ part) {
+  constexpr int VEC = Chunk<XT>::VEC, NT = T > 32 ? T : 256, RPC = NT / T;
+  __shared__ float red[T > 32 ? 2 * T / 32 : 1][2];
+  __shared__ float col[T > 32 ? 1 : 2 * NV * T * VEC];
+  RowSum<T, 2> row_sum{red, 0};
+  const int t = threadIdx.x % T, g = threadIdx.x / T;
+  const float inv_c = 1.f / (float)C;
+  const int groups = (C + TRI_CKPT_GROUP - 1) / TRI_CKPT_GROUP;
+  float gm[NV][VEC], ag[NV][VEC], ab[NV][VEC];
+#pragma unroll
+  for (int v = 0; v < NV; ++v)
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      const int c = (v * T + t) * VEC + j;
+      gm[v][j] = gamma && c < C ? __ldg(gamma + c) : 1.f;
+      ag[v][j] = 0.f;
+      ab[v][j] = 0.f;
+    }
+  const int64_t r0 = (int64_t)blockIdx.x * rpc, r1 = min(M, r0 + rpc);
+  // rows past the chunk are zeros, which add nothing and are not written (their threads still
+  // join the sums)
+  auto load = [&](int64_t m, uint4(&rx)[NV], uint4(&rd)[NV], float(&sc)[NV], float &mu, float &rs) {
+    const bool live = m < r1;
+    mu = live ? __ldg(mean + m) : 0.f;
+    rs = live ? __ldg(rstd + m) : 0.f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = (v * T + t) * VEC;
+      rx[v] = rd[v] = make_uint4(0u, 0u, 0u, 0u);
+      sc[v] = 0.f;
+      if (live) {
+        if (q8) {  // (uniform: a kernel argument)
+          uint32_t w[VEC / 4];
+          q8_load<VEC, AL>(q8 + m * C, c, C, w);
+          rx[v].x = w[0];
+          if constexpr (VEC == 8) rx[v].y = w[1];
+          if (c < C) sc[v] = __ldg(s8 + m * groups + c / TRI_CKPT_GROUP);
+        } else {
+          rx[v] = chunk_load<XT, AL>(x + m * ldx, c, C);
+        }
+        rd[v] = chunk_load<XT, AL>(dy + m * lddy, c, C);
+      }
+    }
+  };
+  uint4 rx[NV], rd[NV];
+  float sc[NV], mu, rs;
+  load(r0 + g, rx, rd, sc, mu, rs);
+  for (int64_t b0 = r0; b0 < r1; b0 += RPC) {
+    uint4 nx[NV], nd[NV];
+    float nsc[NV], nmu, nrs;
+    load(b0 + RPC + g, nx, nd, nsc, nmu, nrs);
+    float xh[NV][VEC], dz[NV][VEC], s[2] = {0.f, 0.f};
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      float d[VEC];
+      if (q8) {
+        uint32_t w[VEC / 4];
+        w[0] = rx[v].x;
+        if constexpr (VEC == 8) w[1] = rx[v].y;
+        q8_values<VEC>(w, sc[v], xh[v]);
+      } else {
+        chunk_unpack(rx[v], xh[v], XT());
+      }
+      chunk_unpack(rd[v], d, XT());
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        // (columns past C: dy is zero there, so they add nothing to any sum)
+        xh[v][j] = (xh[v][j] - mu) * rs;
+        ag[v][j] = fmaf(d[j], xh[v][j], ag[v][j]);
+        ab[v][j] += d[j];
+        dz[v][j] = d[j] * gm[v][j];
+        s[0] += dz[v][j];
+        s[1] = fmaf(dz[v][j], xh[v][j], s[1]);
+      }
+    }
+    row_sum(s);
+    const float a = s[0] * inv_c, b = s[1] * inv_c;
+    const int64_t m = b0 + g;
+    if (m < r1) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        float o[VEC];
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) o[j] = rs * (dz[v][j] - a - xh[v][j] * b);
+        chunk_store<XT, AL>(dx + m * C, (v * T + t) * VEC, C, chunk_pack(o, XT()));
+      }
+    }
+#pragma unroll
+    for (int v = 0; v < NV; ++v) rx[v] = nx[v], rd[v] = nd[v], sc[v] = nsc[v];
+    mu = nmu;
+    rs = nrs;
+  }
+  if (!part) return;
+  float *out = part + (int64_t)blockIdx.x * 2 * C;
+  if constexpr (T > 32) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        const int c = (v * T + t) * VEC + j;
+        if (c < C) {
+          out[c] = ag[v][j];
+          out[C + c] = ab[v][j];
+        }
+      }
+  } else {
+    // a warp's lane groups by an xor tree, then the warps in warp order
+#pragma unroll
+    for (int o = T; o < 32; o <<= 1)
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+          ag[v][j] += __shfl_xor_sync(0xffffffffu, ag[v][j], o);
+          ab[v][j] += __shfl_xor_sync(0xffffffffu, ab[v][j], o);
+        }
+    constexpr int W = NV * T * VEC;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int w = 0; w < 8; ++w) {
+      if (warp == w && lane < T) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) {
+            const int c = (v * T + t) * VEC + j;
+            col[c] = w ? col[c] + ag[v][j] : ag[v][j];
+            col[W + c] = w ? col[W + c] + ab[v][j] : ab[v][j];
+          }
+      }
+      __syncthreads();
+    }
+    for (int c = threadIdx.x; c < C; c += NT) {
+      out[c] = col[c];
+      out[C + c] = col[W + c];
+    }
+  }
+}
+
+// dgamma and dbeta: the sums over the CTAs' partials part[p][2][C]. A CTA takes 32 of the 2 C
+// columns; lane row y adds p = y, y + 32, ... in order, then the 32 sums are added in order.
+__global__ void __launch_bounds__(1024) norm_reduce_kernel(const float *__restrict__ part, int parts, int C,
+                                                           float *__restrict__ dgamma, float *__restrict__ dbeta) {
+  __shared__ float acc[32][33];
+  const int i = blockIdx.x * 32 + threadIdx.x, n = 2 * C;
+  float s = 0.f;
+  if (i < n) {
+    int p = threadIdx.y;
+    for (; p + 96 < parts; p += 128) {  // four loads in flight, added in order
+      const float a0 = part[(int64_t)p * n + i], a1 = part[(int64_t)(p + 32) * n + i];
+      const float a2 = part[(int64_t)(p + 64) * n + i], a3 = part[(int64_t)(p + 96) * n + i];
+      s = (((s + a0) + a1) + a2) + a3;
+    }
+    for (; p < parts; p += 32) s += part[(int64_t)p * n + i];
+  }
+  acc[threadIdx.y][threadIdx.x] = s;
+  __syncthreads();
+  // row y of the transposed sums: an xor tree over 32 lanes
+  float r = acc[threadIdx.x][threadIdx.y];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
+  const int k = blockIdx.x * 32 + threadIdx.y;
+  if (threadIdx.x == 0 && k < n) {
+    if (k < C)
+      dgamma[k] = r;
+    else
+      dbeta[k - C] = r;
+  }
+}
+
+struct BwdSplitRows {
+  int64_t rpc;  // rows per CTA
+  int parts;    // CTAs
+};
+
+// The split of the rows over CTAs, from the shape alone: about 4 CTAs of 256 (8 of 128) threads for
+// each of 152 SMs, at least two rows per lane group.
+BwdSplitRows split_rows(const tri_norm_shape &s, int geo) {
+  const int T = norm_threads_per_row(geo), RPC = T > 32 ? 1 : 256 / T;
+  const int64_t target = T == 128 ? 152 * 8 : 152 * 4;
+  int64_t rpc = (s.M + target - 1) / target;
+  rpc = std::max<int64_t>((rpc + RPC - 1) / RPC * RPC, 2 * RPC);
+  return {rpc, (int)((s.M + rpc - 1) / rpc)};
+}
+
+template <typename XT>
+int geometry_of(const tri_norm_shape &s, const void *x, const int8_t *q8, const void *dy, const void *dx, bool *al) {
+  constexpr int VEC = Chunk<XT>::VEC;
+  const int64_t ldx = s.ldx ? s.ldx : s.C, lddy = s.lddy ? s.lddy : s.C;
+  *al = s.C % VEC == 0 && (q8 || ldx % VEC == 0) && lddy % VEC == 0 &&
+        ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(dy) | reinterpret_cast<uintptr_t>(dx)) & 15u) == 0 &&
+        (reinterpret_cast<uintptr_t>(q8) & (VEC - 1)) == 0;
+  return norm_geometry((s.C + VEC - 1) / VEC, *al);
+}
+
+template <typename XT>
+cudaError_t launch_bwd_t(const tri_norm_shape &s, const void *x, const int8_t *q8, const float *s8, const float *gamma,
+                         const float *mean, const float *rstd, const void *dy, void *dx, float *dgamma, float *dbeta,
+                         float *part, cudaStream_t st) {
+  constexpr int VEC = Chunk<XT>::VEC;
+  bool al;
+  const int geo = geometry_of<XT>(s, x, q8, dy, dx, &al);
+  const BwdSplitRows sp = split_rows(s, geo);
+  const int64_t ldx = s.ldx ? s.ldx : s.C, lddy = s.lddy ? s.lddy : s.C;
+#define LAUNCH(T, NV, AL)                                                                                               \
+  if constexpr (T * NV * VEC <= TRI_NORM_MAX_C) {                                                                       \
+    constexpr int NT = T > 32 ? T : 256;                                                                                \
+    norm_bwd_kernel<XT, T, NV, AL><<<sp.parts, NT, 0, st>>>(static_cast<const XT *>(x), ldx, q8, s8, gamma, mean, rstd, \
+                                                            static_cast<const XT *>(dy), lddy, s.M, s.C, sp.rpc,        \
+                                                            static_cast<XT *>(dx), part);                               \
+  }
+  NORM_DISPATCH(geo, al, LAUNCH);
+#undef LAUNCH
+  cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess && part) {
+    norm_reduce_kernel<<<(2 * s.C + 31) / 32, dim3(32, 32), 0, st>>>(part, sp.parts, s.C, dgamma, dbeta);
+    e = cudaGetLastError();
+  }
+  return e;
+}
+
+// The largest number of partial sums any alignment of the call's pointers can lead to.
+size_t workspace_bytes_of(const tri_norm_shape &s) {
+  const int vec = s.dtype == TRI_DTYPE_FP32 ? 4 : 8, chunks = (s.C + vec - 1) / vec;
+  const int parts = std::max(split_rows(s, norm_geometry(chunks, true)).parts, split_rows(s, norm_geometry(chunks, false)).parts);
+  return sizeof(float) * (size_t)parts * 2 * s.C;
+}
+
+}  // namespace
+}  // namespace triattn
+
+using namespace triattn;
+
+extern "C" {
+
+size_t tri_norm_bwd_workspace_size(tri_norm_shape shape) {
+  if (norm_check_shape(shape) || shape.C > TRI_NORM_MAX_C) return 0;
+  return workspace_bytes_of(shape);
+}
+
+int tri_norm_bwd(tri_norm_shape shape, const void *x, const int8_t *q8, const float *scale8, const float *gamma,
+                 const float *mean, const float *rstd, const void *dy, void *dx, float *dgamma, float *dbeta,
+                 void *workspace, size_t workspace_bytes, void *stream) {
+  const int rc = norm_check_shape(shape);
+  if (rc) return rc;
+  if ((x != nullptr) == (q8 != nullptr) || (q8 != nullptr) != (scale8 != nullptr) || !mean || !rstd || !dy || !dx ||
+      (dgamma != nullptr) != (dbeta != nullptr))
+    return TRI_ATTN_ERR_INVALID_ARG;
+  if (shape.C > TRI_NORM_MAX_C) return TRI_ATTN_ERR_UNSUPPORTED;
+  const uintptr_t es = shape.dtype == TRI_DTYPE_FP32 ? 4 : 2;
+  if ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(dy) | reinterpret_cast<uintptr_t>(dx)) & (es - 1))
+    return TRI_ATTN_ERR_UNSUPPORTED;
+  for (const void *p : {(const void *)scale8, (const void *)gamma, (const void *)mean, (const void *)rstd,
+                        (const void *)dgamma, (const void *)dbeta, (const void *)workspace})
+    if (reinterpret_cast<uintptr_t>(p) & 3u) return TRI_ATTN_ERR_UNSUPPORTED;
+  if (dgamma && (!workspace || workspace_bytes < workspace_bytes_of(shape))) return TRI_ATTN_ERR_WORKSPACE;
+  float *part = dgamma ? static_cast<float *>(workspace) : nullptr;
+  const auto st = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  switch (shape.dtype) {
+    case TRI_DTYPE_BF16:
+      e = launch_bwd_t<__nv_bfloat16>(shape, x, q8, scale8, gamma, mean, rstd, dy, dx, dgamma, dbeta, part, st);
+      break;
+    case TRI_DTYPE_FP16:
+      e = launch_bwd_t<__half>(shape, x, q8, scale8, gamma, mean, rstd, dy, dx, dgamma, dbeta, part, st);
+      break;
+    default: e = launch_bwd_t<float>(shape, x, q8, scale8, gamma, mean, rstd, dy, dx, dgamma, dbeta, part, st); break;
+  }
+  return e == cudaSuccess ? TRI_ATTN_OK : TRI_ATTN_ERR_CUDA;
+}
+
+}  // extern "C"

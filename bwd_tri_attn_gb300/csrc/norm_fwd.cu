@@ -1,0 +1,167 @@
+// LayerNorm forward, with the 8-bit checkpoint of its input written in the same pass
+// (include/tri_norm.h states the formulas).
+//
+// A row is read once into registers; its mean and then the mean of the squared differences are
+// summed from there (no cancellation for rows far from zero), and y, the statistics and the
+// checkpoint leave in the same pass: the kernel reads x and writes y (plus one byte and 1/32 of an
+// FP32 scale per value for the checkpoint), and memory bandwidth bounds it.
+#include <math.h>
+
+#include <algorithm>
+
+#include "norm.cuh"
+
+namespace triattn {
+namespace {
+
+// Rows per lane group whose loads are issued together: enough bytes in flight at one chunk a lane.
+template <int T, int NV>
+constexpr int fwd_rows_in_flight() {
+  return T > 32 ? 1 : NV == 1 ? 4 : 2;
+}
+
+template <typename XT, int T, int NV, bool AL>
+__global__ void __launch_bounds__(T > 32 ? T : 256)
+    norm_fwd_kernel(const XT *__restrict__ x, int64_t ldx, const float *__restrict__ gamma,
+                    const float *__restrict__ beta, float eps, int64_t M, int C, XT *__restrict__ y,
+                    float *__restrict__ mean, float *__restrict__ rstd, int8_t *__restrict__ q8,
+                    float *__restrict__ s8) {
+  constexpr int VEC = Chunk<XT>::VEC, NT = T > 32 ? T : 256, RPC = NT / T, U = fwd_rows_in_flight<T, NV>();
+  constexpr int GL = (TRI_CKPT_GROUP / VEC) < T ? (TRI_CKPT_GROUP / VEC) : T;  // lanes per checkpoint group
+  __shared__ float red[T > 32 ? 2 * T / 32 : 1][1];
+  RowSum<T, 1> row_sum{red, 0};
+  const int t = threadIdx.x % T, g = threadIdx.x / T;
+  const float inv_c = 1.f / (float)C;
+  const int groups = (C + TRI_CKPT_GROUP - 1) / TRI_CKPT_GROUP;
+  float gm[NV][VEC], bt[NV][VEC];
+#pragma unroll
+  for (int v = 0; v < NV; ++v)
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      const int c = (v * T + t) * VEC + j;
+      gm[v][j] = gamma && c < C ? __ldg(gamma + c) : 1.f;
+      bt[v][j] = beta && c < C ? __ldg(beta + c) : 0.f;
+    }
+  // (every thread of a warp, and of a CTA that holds a row, makes the same number of iterations:
+  // rows past the last one are zeros that are not written)
+  const int64_t step = (int64_t)gridDim.x * RPC * U;
+  for (int64_t m0 = (int64_t)blockIdx.x * RPC * U; m0 < M; m0 += step) {
+    uint4 raw[U][NV];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t m = m0 + u * RPC + g;
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+        raw[u][v] = m < M ? chunk_load<XT, AL>(x + m * ldx, (v * T + t) * VEC, C) : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t m = m0 + u * RPC + g;
+      float s[1] = {0.f};
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        float f[VEC];
+        chunk_unpack(raw[u][v], f, XT());
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) s[0] += f[j];
+      }
+      row_sum(s);
+      const float mu = s[0] * inv_c;
+      float q[1] = {0.f};
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        float f[VEC];
+        chunk_unpack(raw[u][v], f, XT());
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+          const float d = (v * T + t) * VEC + j < C ? f[j] - mu : 0.f;
+          q[0] = fmaf(d, d, q[0]);
+        }
+      }
+      row_sum(q);
+      const float r = __frsqrt_rn(fmaf(q[0], inv_c, eps));
+      if (m < M && t == 0) {
+        mean[m] = mu;
+        rstd[m] = r;
+      }
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        const int ch = v * T + t, c = ch * VEC;
+        float f[VEC], o[VEC];
+        chunk_unpack(raw[u][v], f, XT());
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) o[j] = fmaf((f[j] - mu) * r, gm[v][j], bt[v][j]);
+        if (m < M) chunk_store<XT, AL>(y + m * C, c, C, chunk_pack(o, XT()));
+        if (q8) {  // (uniform: a kernel argument)
+          const uint32_t top = group_top<GL>(top_bits<VEC>(f));
+          float sc, inv;
+          q8_scales(top, sc, inv);
+          uint32_t w[VEC / 4];
+          q8_round<VEC>(f, inv, w);
+          if (m < M) {
+            q8_store<VEC, AL>(q8 + m * C, c, C, w);
+            if (ch % GL == 0 && c < C) s8[m * groups + c / TRI_CKPT_GROUP] = sc;
+          }
+        }
+      }
+    }
+  }
+}
+
+template <typename XT>
+cudaError_t launch_fwd_t(const tri_norm_shape &s, const void *x, const float *gamma, const float *beta, void *y,
+                         float *mean, float *rstd, int8_t *q8, float *s8, cudaStream_t st) {
+  constexpr int VEC = Chunk<XT>::VEC;
+  const int64_t ldx = s.ldx ? s.ldx : s.C;
+  const bool al = s.C % VEC == 0 && ldx % VEC == 0 && ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(y)) & 15u) == 0 &&
+                  (reinterpret_cast<uintptr_t>(q8) & (VEC - 1)) == 0;
+  const int geo = norm_geometry((s.C + VEC - 1) / VEC, al);
+#define LAUNCH(T, NV, AL)                                                                                         \
+  if constexpr (T * NV * VEC <= TRI_NORM_MAX_C) {                                                                 \
+    constexpr int NT = T > 32 ? T : 256, per = NT / T * fwd_rows_in_flight<T, NV>();                              \
+    const int grid = (int)std::min<int64_t>((s.M + per - 1) / per, 152 * (2048 / NT) * 4);                        \
+    norm_fwd_kernel<XT, T, NV, AL><<<grid, NT, 0, st>>>(static_cast<const XT *>(x), ldx, gamma, beta, s.eps, s.M, \
+                                                       s.C, static_cast<XT *>(y), mean, rstd, q8, s8);            \
+  }
+  NORM_DISPATCH(geo, al, LAUNCH);
+#undef LAUNCH
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+int norm_check_shape(const tri_norm_shape &s) {
+  if (s.M < 1 || s.C < 1 || (s.ldx != 0 && s.ldx < s.C) || (s.lddy != 0 && s.lddy < s.C) || !(s.eps >= 0.f) ||
+      !isfinite(s.eps))
+    return TRI_ATTN_ERR_INVALID_ARG;
+  if (s.dtype != TRI_DTYPE_BF16 && s.dtype != TRI_DTYPE_FP16 && s.dtype != TRI_DTYPE_FP32)
+    return TRI_ATTN_ERR_INVALID_ARG;
+  // every element offset (the largest row stride included) fits 62 bits
+  const int64_t ld = std::max<int64_t>(std::max<int64_t>(s.ldx, s.lddy), s.C);
+  if (s.M > (int64_t{1} << 40) || ld > (int64_t{1} << 62) / s.M) return TRI_ATTN_ERR_UNSUPPORTED;
+  return TRI_ATTN_OK;
+}
+
+}  // namespace triattn
+
+using namespace triattn;
+
+extern "C" int tri_norm_fwd(tri_norm_shape shape, const void *x, const float *gamma, const float *beta, void *y,
+                            float *mean, float *rstd, int8_t *q8, float *scale8, void *stream) {
+  const int rc = norm_check_shape(shape);
+  if (rc) return rc;
+  if (!x || !y || !mean || !rstd || (q8 != nullptr) != (scale8 != nullptr)) return TRI_ATTN_ERR_INVALID_ARG;
+  if (shape.C > TRI_NORM_MAX_C) return TRI_ATTN_ERR_UNSUPPORTED;
+  const uintptr_t es = shape.dtype == TRI_DTYPE_FP32 ? 4 : 2;
+  if ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(y)) & (es - 1)) return TRI_ATTN_ERR_UNSUPPORTED;
+  for (const void *p : {(const void *)gamma, (const void *)beta, (const void *)mean, (const void *)rstd, (const void *)scale8})
+    if (reinterpret_cast<uintptr_t>(p) & 3u) return TRI_ATTN_ERR_UNSUPPORTED;
+  const auto st = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  switch (shape.dtype) {
+    case TRI_DTYPE_BF16: e = launch_fwd_t<__nv_bfloat16>(shape, x, gamma, beta, y, mean, rstd, q8, scale8, st); break;
+    case TRI_DTYPE_FP16: e = launch_fwd_t<__half>(shape, x, gamma, beta, y, mean, rstd, q8, scale8, st); break;
+    default: e = launch_fwd_t<float>(shape, x, gamma, beta, y, mean, rstd, q8, scale8, st); break;
+  }
+  return e == cudaSuccess ? TRI_ATTN_OK : TRI_ATTN_ERR_CUDA;
+}

@@ -1,0 +1,193 @@
+// Row-wise access to [M, C] tensors for the LayerNorm and checkpoint kernels: 16-byte chunks of a
+// row (8 BF16/FP16 or 4 FP32 values) per thread, and the 8-bit checkpoint's rounding.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "sm100.cuh"
+#include "tri_norm.h"
+
+namespace triattn {
+
+template <typename XT>
+struct Chunk {
+  static constexpr int VEC = 16 / (int)sizeof(XT);  // values per chunk
+};
+
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+__device__ __forceinline__ float to_f32(float v) { return v; }
+
+__device__ __forceinline__ void chunk_unpack(const uint4 &w, float (&v)[8], __nv_bfloat16) {
+  const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    v[2 * j] = __uint_as_float(ww[j] << 16);
+    v[2 * j + 1] = __uint_as_float(ww[j] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void chunk_unpack(const uint4 &w, float (&v)[8], __half) {
+  const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&ww[j]));
+    v[2 * j] = f.x;
+    v[2 * j + 1] = f.y;
+  }
+}
+__device__ __forceinline__ void chunk_unpack(const uint4 &w, float (&v)[4], float) {
+  v[0] = __uint_as_float(w.x), v[1] = __uint_as_float(w.y), v[2] = __uint_as_float(w.z), v[3] = __uint_as_float(w.w);
+}
+
+__device__ __forceinline__ uint4 chunk_pack(const float (&v)[8], __nv_bfloat16) {
+  return make_uint4(sm100::pack_bf16x2(v[0], v[1]), sm100::pack_bf16x2(v[2], v[3]), sm100::pack_bf16x2(v[4], v[5]),
+                    sm100::pack_bf16x2(v[6], v[7]));
+}
+__device__ __forceinline__ uint4 chunk_pack(const float (&v)[8], __half) {
+  return make_uint4(sm100::pack_f16x2(v[0], v[1]), sm100::pack_f16x2(v[2], v[3]), sm100::pack_f16x2(v[4], v[5]),
+                    sm100::pack_f16x2(v[6], v[7]));
+}
+__device__ __forceinline__ uint4 chunk_pack(const float (&v)[4], float) {
+  return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+}
+
+// The chunk of values c .. c + VEC - 1 of a row (zeros past C). AL: the row starts on a 16-byte
+// boundary and C is a multiple of VEC, so a chunk is whole or absent; else value by value.
+template <typename XT, bool AL>
+__device__ __forceinline__ uint4 chunk_load(const XT *row, int c, int C) {
+  constexpr int VEC = Chunk<XT>::VEC;
+  if constexpr (AL) {
+    return c < C ? ld_stream(reinterpret_cast<const uint4 *>(row + c)) : make_uint4(0u, 0u, 0u, 0u);
+  } else {
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+    if constexpr (sizeof(XT) == 2) {
+      const uint16_t *p = reinterpret_cast<const uint16_t *>(row);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j)
+        if (c + j < C) w[j / 2] |= (uint32_t)p[c + j] << (16 * (j & 1));
+    } else {
+      const uint32_t *p = reinterpret_cast<const uint32_t *>(row);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j)
+        if (c + j < C) w[j] = p[c + j];
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+template <typename XT, bool AL>
+__device__ __forceinline__ void chunk_store(XT *row, int c, int C, const uint4 &v) {
+  constexpr int VEC = Chunk<XT>::VEC;
+  if constexpr (AL) {
+    if (c < C) *reinterpret_cast<uint4 *>(row + c) = v;
+  } else {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    if constexpr (sizeof(XT) == 2) {
+      uint16_t *p = reinterpret_cast<uint16_t *>(row);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j)
+        if (c + j < C) p[c + j] = (uint16_t)(w[j / 2] >> (16 * (j & 1)));
+    } else {
+      uint32_t *p = reinterpret_cast<uint32_t *>(row);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j)
+        if (c + j < C) p[c + j] = w[j];
+    }
+  }
+}
+
+// VEC 8-bit values of a row, packed into VEC / 4 words (zeros past C).
+template <int VEC, bool AL>
+__device__ __forceinline__ void q8_load(const int8_t *row, int c, int C, uint32_t (&w)[VEC / 4]) {
+#pragma unroll
+  for (int i = 0; i < VEC / 4; ++i) w[i] = 0u;
+  if constexpr (AL) {
+    if (c < C) {
+      if constexpr (VEC == 8) {
+        const uint2 v = __ldg(reinterpret_cast<const uint2 *>(row + c));
+        w[0] = v.x, w[1] = v.y;
+      } else {
+        w[0] = __ldg(reinterpret_cast<const uint32_t *>(row + c));
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j)
+      if (c + j < C) w[j / 4] |= (uint32_t)(uint8_t)row[c + j] << (8 * (j & 3));
+  }
+}
+
+template <int VEC, bool AL>
+__device__ __forceinline__ void q8_store(int8_t *row, int c, int C, const uint32_t (&w)[VEC / 4]) {
+  if constexpr (AL) {
+    if (c < C) {
+      if constexpr (VEC == 8)
+        *reinterpret_cast<uint2 *>(row + c) = make_uint2(w[0], w[1]);
+      else
+        *reinterpret_cast<uint32_t *>(row + c) = w[0];
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j)
+      if (c + j < C) row[c + j] = (int8_t)(uint8_t)(w[j / 4] >> (8 * (j & 3)));
+  }
+}
+
+template <int VEC>
+__device__ __forceinline__ void q8_values(const uint32_t (&w)[VEC / 4], float s, float (&v)[VEC]) {
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) v[j] = (float)(int8_t)(uint8_t)(w[j / 4] >> (8 * (j & 3))) * s;
+}
+
+// A checkpoint group's scale and inverse scale from the bits of its largest magnitude (as
+// unsigned numbers the bits of |x| order as |x| does, an infinity above every number and a NaN
+// above it). A NaN scale makes every value of the group NaN, whatever q holds.
+__device__ __forceinline__ void q8_scales(uint32_t top_bits, float &s, float &inv) {
+  const float top = __uint_as_float(top_bits);
+  if (top_bits >= 0x7f800000u) {
+    s = __uint_as_float(0x7fffffffu);
+    inv = 0.f;
+  } else if (top < 0x1p-120f) {  // (the inverse scale of anything larger is finite)
+    s = 0.f;
+    inv = 0.f;
+  } else {
+    s = __fdiv_rn(top, 127.f);
+    if (__fmul_rn(s, 127.f) > 3.4028234663852886e38f) s = __uint_as_float(__float_as_uint(s) - 1u);  // (finite again)
+    inv = __fdiv_rn(127.f, top);
+  }
+}
+
+// Largest |v| of a chunk, as bits.
+template <int VEC>
+__device__ __forceinline__ uint32_t top_bits(const float (&v)[VEC]) {
+  uint32_t m = 0u;
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
+  return m;
+}
+
+// VEC values to packed 8-bit ones. |x| inv is at most 127 (1 + 2^-23), which rounds to 127; a
+// group with an infinity or NaN has inv = 0 and its q's (0, or the conversion of a NaN, also 0)
+// do not matter.
+template <int VEC>
+__device__ __forceinline__ void q8_round(const float (&v)[VEC], float inv, uint32_t (&w)[VEC / 4]) {
+#pragma unroll
+  for (int i = 0; i < VEC / 4; ++i) {
+    uint32_t x = 0u;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x |= ((uint32_t)__float2int_rn(__fmul_rn(v[4 * i + j], inv)) & 0xffu) << (8 * j);
+    w[i] = x;
+  }
+}
+
+// The maximum over the LANES consecutive lanes that hold one checkpoint group.
+template <int LANES>
+__device__ __forceinline__ uint32_t group_top(uint32_t m) {
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+  return m;
+}
+
+}  // namespace triattn
