@@ -18,6 +18,8 @@ backward passes are differentiable once (no second derivatives).
   the block keeps its input in 8 bits and recomputes.
 - ``layer_norm(x, gamma, beta, eps, checkpoint=False)``: LayerNorm (include/tri_norm.h), gradients
   for x and the weights; with ``checkpoint`` it keeps x in 8 bits for the backward pass.
+- ``cross_attention(Q, K, V, mask=None, kv_lens=None, scale=None)``: cross attention to an encoder's
+  states of another length (include/tri_cross.h), gradients for Q, K and V.
 """
 from __future__ import annotations
 
@@ -148,6 +150,42 @@ def layer_norm(x, gamma=None, beta=None, eps=1e-5, checkpoint=False):
     """LayerNorm over the last axis of x [..., C] (BF16, FP16 or FP32; FP32 statistics and weights).
     With ``checkpoint`` the backward pass reads an 8-bit checkpoint of x in the place of x."""
     return _LayerNorm.apply(x, gamma, beta, eps, checkpoint)
+
+
+class _CrossAttention(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, Q, K, V, mask, kv_lens, scale):
+        Q, K, V = (_spaced(t) for t in (Q, K, V))
+        mask, kv_lens = (None if t is None else t.contiguous() for t in (mask, kv_lens))
+        O, LSE = tb.cross_forward(Q, K, V, mask, kv_lens, scale)
+        ctx.scale = scale
+        ctx.save_for_backward(Q, K, V, mask, kv_lens, O, LSE)
+        return O
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dO):
+        Q, K, V, mask, kv_lens, O, LSE = ctx.saved_tensors
+        grads = tb.cross_backward(Q, K, V, O, LSE, dO.to(torch.bfloat16).contiguous(), mask, kv_lens, ctx.scale)
+        return (*grads, None, None, None)
+
+
+def _spaced(t):
+    """t as the kernels read it in place (channels contiguous, the other strides multiples of 8 elements and not
+    zero, a 16-byte aligned start), else a contiguous copy."""
+    fits = t.dim() == 4 and (t.stride(3) == 1 or t.shape[3] == 1) and t.data_ptr() % 16 == 0 and all(
+        n == 1 or (s >= t.shape[3] and s % 8 == 0) for n, s in zip(t.shape[:3], t.stride()[:3]))
+    if fits:
+        return t
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
+def cross_attention(Q, K, V, mask=None, kv_lens=None, scale=None):
+    """Cross attention of BF16 CUDA queries Q [B, T, H, d] to encoder states K, V [B, S, Hk, d] (H a multiple of
+    Hk; include/tri_cross.h): mask [B, S] False where a key is not attended, kv_lens int32 [B]. Parts of fused
+    projections and transposed heads are read in place."""
+    return _CrossAttention.apply(Q, K, V, mask, kv_lens, scale)
 
 
 class TriangleAttentionBlock(torch.nn.Module):

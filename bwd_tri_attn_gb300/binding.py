@@ -1,5 +1,5 @@
 """Thin ctypes binding of the C ABI in ``include/tri_attn.h``, ``include/tri_mul.h``,
-``include/tri_module.h`` and ``include/tri_norm.h``.
+``include/tri_module.h``, ``include/tri_norm.h`` and ``include/tri_cross.h``.
 
 Argument marshalling only: PyTorch tensors supply device pointers and the
 current CUDA stream; every step of the computation runs in the library's
@@ -46,7 +46,8 @@ EXPORTS = ("tri_attn_strerror", "tri_attn_fwd", "tri_attn_bwd_workspace_size", "
            "tri_attn_device_status", "tri_attn_set_timing_events", "tri_attn_bwd_static", "tri_mul_fwd",
            "tri_mul_bwd_workspace_size", "tri_mul_bwd", "tri_module_saved_size", "tri_module_bwd_workspace_size",
            "tri_module_fwd", "tri_module_bwd", "tri_norm_fwd", "tri_norm_bwd_workspace_size", "tri_norm_bwd",
-           "tri_ckpt_pack", "tri_ckpt_unpack")
+           "tri_ckpt_pack", "tri_ckpt_unpack", "tri_cross_fwd_workspace_size", "tri_cross_fwd",
+           "tri_cross_bwd_workspace_size", "tri_cross_bwd")
 
 
 LAYOUT_PAIR, LAYOUT_CHANNEL_MAJOR = 0, 1  # tri_mul_shape.layout
@@ -92,6 +93,19 @@ class Checkpoint(NamedTuple):
     channels ([..., (C + 127) // 128]); it stands for q8 * scale."""
     q8: torch.Tensor
     scale: torch.Tensor
+
+
+class CrossShape(ctypes.Structure):
+    """tri_cross_shape: batch, queries, encoder states, query heads, key heads, head dimension, scale, and the
+    strides (batch, position, head; in elements) of Q, K and V."""
+    _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("S", ctypes.c_int), ("H", ctypes.c_int),
+                ("Hk", ctypes.c_int), ("d", ctypes.c_int), ("scale", ctypes.c_float),
+                ("q_stride", ctypes.c_int64 * 3), ("k_stride", ctypes.c_int64 * 3), ("v_stride", ctypes.c_int64 * 3)]
+
+    def __repr__(self):
+        return (f"CrossShape(B={self.B}, T={self.T}, S={self.S}, H={self.H}, Hk={self.Hk}, d={self.d}, "
+                f"scale={self.scale}, q_stride={list(self.q_stride)}, k_stride={list(self.k_stride)}, "
+                f"v_stride={list(self.v_stride)})")
 
 
 def lib_path() -> str:
@@ -149,6 +163,14 @@ def load(path: str | None = None):
         lib.tri_ckpt_pack.restype = ctypes.c_int
         lib.tri_ckpt_unpack.argtypes = [NormShape] + [_VP] * 4
         lib.tri_ckpt_unpack.restype = ctypes.c_int
+        lib.tri_cross_fwd_workspace_size.argtypes = [CrossShape]
+        lib.tri_cross_fwd_workspace_size.restype = ctypes.c_size_t
+        lib.tri_cross_fwd.argtypes = [CrossShape] + [_VP] * 8 + [ctypes.c_size_t, _VP]
+        lib.tri_cross_fwd.restype = ctypes.c_int
+        lib.tri_cross_bwd_workspace_size.argtypes = [CrossShape]
+        lib.tri_cross_bwd_workspace_size.restype = ctypes.c_size_t
+        lib.tri_cross_bwd.argtypes = [CrossShape] + [_VP] * 12 + [ctypes.c_size_t, _VP]
+        lib.tri_cross_bwd.restype = ctypes.c_int
         _lib = lib
     return _lib
 
@@ -431,6 +453,56 @@ def tri_ckpt_unpack(shape: NormShape, q8, scale, x, stream=None):
     _check("tri_ckpt_unpack", rc)
 
 
+def _strided_arg(t, name, shape, strides):
+    """A BF16 [B, n, heads, d] argument with the given strides (batch, position, head)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
+    if t.dtype != _BF16:
+        raise TypeError(f"{name} must be {_BF16}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, the call needs {tuple(shape)}")
+    if t.stride(3) != 1 and shape[3] != 1:
+        raise ValueError(f"{name}'s last axis must be contiguous, got strides {t.stride()}")
+    for n, have, given in zip(shape, t.stride(), strides):
+        if n > 1 and have != given:
+            raise ValueError(f"{name} has strides {t.stride()}, the shape gives {tuple(strides)}")
+    return (name, t)
+
+
+def _cross_args(shape, Q, K, V, mask, kv_lens):
+    B, T, S, H, Hk, d = shape.B, shape.T, shape.S, shape.H, shape.Hk, shape.d
+    m = None if mask is None else mask.view(torch.uint8) if isinstance(mask, torch.Tensor) and mask.dtype == torch.bool else mask
+    return [_strided_arg(Q, "Q", (B, T, H, d), shape.q_stride), _strided_arg(K, "K", (B, S, Hk, d), shape.k_stride),
+            _strided_arg(V, "V", (B, S, Hk, d), shape.v_stride), _arg(m, "mask", torch.uint8, B * S, True),
+            _arg(kv_lens, "kv_lens", torch.int32, B, True)]
+
+
+def tri_cross_fwd_workspace_size(shape: CrossShape) -> int:
+    return int(load().tri_cross_fwd_workspace_size(shape))
+
+
+def tri_cross_fwd(shape: CrossShape, Q, K, V, mask, kv_lens, O, LSE, workspace, stream=None):
+    rows = shape.B * shape.T * shape.H
+    ptrs = _ptrs(*_cross_args(shape, Q, K, V, mask, kv_lens), _arg(O, "O", _BF16, rows * shape.d),
+                 _arg(LSE, "LSE", _F32, rows), _arg(workspace, "workspace", None, None, True))
+    rc = load().tri_cross_fwd(shape, *ptrs, _nbytes(workspace), _stream(stream))
+    _check("tri_cross_fwd", rc)
+
+
+def tri_cross_bwd_workspace_size(shape: CrossShape) -> int:
+    return int(load().tri_cross_bwd_workspace_size(shape))
+
+
+def tri_cross_bwd(shape: CrossShape, Q, K, V, mask, kv_lens, O, LSE, dO, dQ, dK, dV, workspace, stream=None):
+    rows, keys = shape.B * shape.T * shape.H, shape.B * shape.S * shape.Hk * shape.d
+    ptrs = _ptrs(*_cross_args(shape, Q, K, V, mask, kv_lens), _arg(O, "O", _BF16, rows * shape.d),
+                 _arg(LSE, "LSE", _F32, rows), _arg(dO, "dO", _BF16, rows * shape.d),
+                 _arg(dQ, "dQ", _BF16, rows * shape.d), _arg(dK, "dK", _BF16, keys), _arg(dV, "dV", _BF16, keys),
+                 _arg(workspace, "workspace", None, None, True))
+    rc = load().tri_cross_bwd(shape, *ptrs, _nbytes(workspace), _stream(stream))
+    _check("tri_cross_bwd", rc)
+
+
 def tri_attn_device_status(stream=None) -> int:
     return int(load().tri_attn_device_status(_stream(stream)))
 
@@ -617,3 +689,46 @@ def checkpoint_unpack(kept, dtype=torch.bfloat16, stream=None) -> torch.Tensor:
     x = torch.empty(q8.shape, dtype=dtype, device=q8.device)
     tri_ckpt_unpack(norm_shape_of(x), q8, scale, x, stream)
     return x
+
+
+def cross_shape_of(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, scale: float | None = None) -> CrossShape:
+    """Shape of the cross attention of Q [B, T, H, d] to K, V [B, S, Hk, d], with their strides."""
+    for t, name in ((Q, "Q"), (K, "K"), (V, "V")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
+        if t.dim() != 4:
+            raise ValueError(f"{name} must have four axes (batch, position, head, channel), got shape {tuple(t.shape)}")
+    B, T, H, d = Q.shape
+    S, Hk = K.shape[1], K.shape[2]
+    if scale is None:
+        scale = 1.0 / math.sqrt(d) if d else 0.0
+    three = ctypes.c_int64 * 3
+    return CrossShape(B, T, S, H, Hk, d, float(scale), three(*Q.stride()[:3]), three(*K.stride()[:3]),
+                      three(*V.stride()[:3]))
+
+
+def _workspace(nbytes, device):
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+
+
+def cross_forward(Q, K, V, mask=None, kv_lens=None, scale=None, workspace=None, stream=None):
+    """Cross attention of the queries Q [B, T, H, d] to the encoder states K, V [B, S, Hk, d] (BF16; heads, positions
+    and batches may be spaced apart). mask: bool or uint8 [B, S], False where a key is not to be attended; kv_lens:
+    int32 [B]. Returns (O, LSE): O [B, T, H, d] and the FP32 log-sum-exp [B, H, T] that cross_backward reads."""
+    shape = cross_shape_of(Q, K, V, scale)
+    O = torch.empty(Q.shape, dtype=torch.bfloat16, device=Q.device)
+    LSE = torch.empty((shape.B, shape.H, shape.T), dtype=torch.float32, device=Q.device)
+    if workspace is None:
+        workspace = _workspace(tri_cross_fwd_workspace_size(shape), Q.device)
+    tri_cross_fwd(shape, Q, K, V, mask, kv_lens, O, LSE, workspace, stream)
+    return O, LSE
+
+
+def cross_backward(Q, K, V, O, LSE, dO, mask=None, kv_lens=None, scale=None, workspace=None, stream=None):
+    """Returns (dQ, dK, dV), without gaps, for the gradient dO of cross_forward's O."""
+    shape = cross_shape_of(Q, K, V, scale)
+    dQ, dK, dV = (torch.empty(t.shape, dtype=torch.bfloat16, device=Q.device) for t in (Q, K, V))
+    if workspace is None:
+        workspace = _workspace(tri_cross_bwd_workspace_size(shape), Q.device)
+    tri_cross_bwd(shape, Q, K, V, mask, kv_lens, O, LSE, dO, dQ, dK, dV, workspace, stream)
+    return dQ, dK, dV

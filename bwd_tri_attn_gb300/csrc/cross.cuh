@@ -1,0 +1,241 @@
+// What the cross-attention kernels share: tensor maps, the division of the work over CTAs, and the
+// key masks.
+//
+// Rows. GB query heads that share a key head (the largest power of two that divides H / Hk, at
+// most 128) are rows of one tile: row r of a tile that starts at query t0 is query t0 + r / GB of
+// head head0 + r mod GB, which is how a TMA box (64 channels, GB heads, 128 / GB queries) lands in shared memory.
+// One query of grouped heads so fills GB rows and reads K and V once.
+//
+// Work. An item is a set of output rows (a row tile of a head block for the forward and dQ, a key tile
+// of a key head for dK and dV), a unit one step of its inner loop (a key tile, or a query tile). The
+// units of all items, in order, are divided evenly over one CTA per SM: CTA k takes
+// [U k / n, U (k + 1) / n). An item whose units fall to several CTAs leaves FP32 partial results in the workspace,
+// at most two per CTA (slot 2 k: the CTA begins inside the item, slot 2 k + 1: it ends inside an
+// item that it began), and a second kernel adds them in CTA order. No SM idles in a last wave,
+// long key lengths are split without a tuned rule, and the order of every sum follows from the shape, the lengths
+// and the SM count.
+#pragma once
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "launch.cuh"
+#include "plan.cuh"
+#include "sm100.cuh"
+#include "sync.cuh"
+#include "tmap.cuh"
+#include "tri_cross.h"
+
+namespace triattn {
+
+constexpr int kTile = 128;                 // rows and keys of a tile
+constexpr int kBoxBytes = kTile * 128;     // one TMA box: 128 rows of 64 BF16 channels, 128-byte swizzled
+
+struct CrossSched {
+  int B, S;
+  const int32_t *lens;  // may be NULL
+  bool by_keys;         // items are key tiles (dK, dV), else row tiles
+  int heads;            // head blocks (rows) or key heads (keys) of a batch
+  int rows;             // row tiles of a head block, or units of a key tile
+  int *status;
+
+  __device__ __forceinline__ int len(int b) const { return lens ? min(max(__ldg(lens + b), 0), S) : S; }
+  // (a sequence without keys still has one tile, all of it masked: it writes the zeros)
+  __device__ __forceinline__ int tiles(int b) const { return max(1, (len(b) + kTile - 1) / kTile); }
+  __device__ __forceinline__ int items(int nt) const { return heads * (by_keys ? nt : rows); }
+  __device__ __forceinline__ int inner(int nt) const { return by_keys ? rows : nt; }
+};
+
+// Position in the list of units. b, item (within the batch), k (unit within the item).
+struct CrossPos {
+  int b, item, k;
+  int nt, items, inner;  // of batch b
+  __device__ __forceinline__ void load(const CrossSched &s) {
+    nt = s.tiles(b);
+    items = s.items(nt);
+    inner = s.inner(nt);
+  }
+  __device__ __forceinline__ void next(const CrossSched &s) {
+    if (++k < inner) return;
+    k = 0;
+    if (++item < items) return;
+    item = 0;
+    if (++b < s.B) load(s);
+  }
+};
+
+// Sum of the units of all batches (the whole warp calls it; every lane gets the result).
+__device__ __forceinline__ int64_t cross_units(const CrossSched &s) {
+  const int64_t per = (int64_t)s.heads * s.rows;  // units of a batch are per x its key tiles, either way
+  if (!s.lens) return per * s.B * s.tiles(0);
+  int64_t n = 0;
+  for (int b = threadIdx.x & 31; b < s.B; b += 32) n += s.tiles(b);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+  return n * per;
+}
+
+// The position of unit u < cross_units(s) (the whole warp calls it).
+__device__ __forceinline__ CrossPos cross_locate(const CrossSched &s, int64_t u) {
+  const int64_t per = (int64_t)s.heads * s.rows;
+  CrossPos p;
+  if (!s.lens) {
+    p.b = (int)(u / (per * s.tiles(0)));
+    u -= (int64_t)p.b * per * s.tiles(0);
+  } else {
+    const int lane = threadIdx.x & 31;
+    p.b = 0;
+    for (int b0 = 0; b0 < s.B; b0 += 32) {
+      const int64_t n = b0 + lane < s.B ? per * s.tiles(b0 + lane) : 0;
+      int64_t upto = n;  // inclusive prefix sum
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, upto > u && b0 + lane < s.B);
+      if (past) {
+        const int l = __ffs(past) - 1;
+        p.b = b0 + l;
+        u -= __shfl_sync(0xffffffffu, upto - n, l);
+        break;
+      }
+      u -= __shfl_sync(0xffffffffu, upto, 31);
+    }
+  }
+  p.load(s);
+  p.item = (int)(u / p.inner);
+  p.k = (int)(u - (int64_t)p.item * p.inner);
+  return p;
+}
+
+// A CTA's share of the units: where it begins and how many there are.
+struct CrossShare {
+  CrossPos pos;
+  int n;
+};
+
+__device__ __forceinline__ int64_t cross_bound(int64_t units, int cta, int ctas) {
+  return units / ctas * cta + units % ctas * cta / ctas;
+}
+
+// The CTA's share (the whole warp calls it).
+__device__ __forceinline__ CrossShare cross_share(const CrossSched &s) {
+  const int64_t units = cross_units(s);
+  const int64_t u0 = cross_bound(units, blockIdx.x, gridDim.x), u1 = cross_bound(units, blockIdx.x + 1, gridDim.x);
+  CrossShare sh;
+  sh.n = (int)(u1 - u0);
+  if (sh.n > 0) sh.pos = cross_locate(s, u0);
+  return sh;
+}
+
+// The run of units of one item within a share that begins at position p with `left` units: how many
+// units it has, and where its results go (-1: the item is whole, else the partial slot).
+struct CrossRun {
+  int n, slot;
+};
+__device__ __forceinline__ CrossRun cross_run(const CrossPos &p, int left) {
+  CrossRun r;
+  r.n = min(p.inner - p.k, left);
+  r.slot = p.k != 0 ? 2 * (int)blockIdx.x : r.n < p.inner ? 2 * (int)blockIdx.x + 1 : -1;
+  return r;
+}
+
+// Live keys of the 128-key tile at k0, one bit a key, in four words. all: the tile is whole and
+// there is no mask. The whole warp calls load() (its reads can be issued early) and then words().
+struct KeyWords {
+  bool all;
+  uint32_t bits;  // this lane's four keys: k0 + 32 i + lane
+  __device__ __forceinline__ void load(const uint8_t *mask, int len, int b, int S, int k0) {
+    const int lane = threadIdx.x & 31;
+    all = !mask && k0 + kTile <= len;
+    bits = 0u;
+    if (all) return;
+    const uint8_t *m = mask ? mask + (int64_t)b * S + k0 : nullptr;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int j = 32 * i + lane;
+      const bool live = k0 + j < len && (!m || __ldg(m + j) != 0);
+      bits |= (live ? 1u : 0u) << i;
+    }
+  }
+  __device__ __forceinline__ void words(uint32_t (&w)[4]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __ballot_sync(0xffffffffu, (bits >> i) & 1u);
+  }
+};
+
+// Zeroes the rows of a [128 rows][boxes of 64 channels] tile whose bit is clear: 0 x NaN would reach
+// the accumulator otherwise (the whole warp calls it, before the products that read the tile).
+template <int BOXES>
+__device__ __forceinline__ void zero_dead_rows(uint8_t *tile, const uint32_t (&w)[4]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    for (uint32_t dead = ~w[i]; dead;) {
+      // four rows at a time, eight lanes (16 bytes each) per row
+      int row = -1;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int r = dead ? __ffs(dead) - 1 : -1;
+        if (r >= 0) dead &= dead - 1;
+        if ((lane >> 3) == g) row = r;
+      }
+      if (row >= 0)
+#pragma unroll
+        for (int x = 0; x < BOXES; ++x)
+          *reinterpret_cast<uint4 *>(tile + x * kBoxBytes + (32 * i + row) * 128 + (lane & 7) * 16) =
+              make_uint4(0u, 0u, 0u, 0u);
+    }
+  sm100::fence_proxy_async_smem();
+  __syncwarp();
+}
+
+// Descriptors of a 128-row tile of boxes (64 channels x 128 rows, 128-byte swizzled). K-major: the
+// product runs over the channels, 16 at a time (step k at k_off(k)); MN-major: over the rows, 16
+// rows a step, the channels being the operand's free index (64 per box).
+__device__ __forceinline__ uint64_t desc_k(uint32_t tile, int k) {
+  return sm100::smem_desc(tile + (k >> 2) * kBoxBytes + (k & 3) * 32, 16, 1024, sm100::kSwizzle128B);
+}
+__device__ __forceinline__ uint64_t desc_mn(uint32_t tile) {
+  return sm100::smem_desc(tile, kBoxBytes, 1024, sm100::kSwizzle128B);
+}
+constexpr uint64_t kMnStep = (16 * 128) >> 4;  // 16 rows further
+
+// ---------------------------------------------------------------- host side
+// Tensor map of a [B, n, heads, d] BF16 tensor (strides in elements), boxes of 64 channels x `hb` heads
+// x `rows` positions. Channels past d, positions past n: zeros.
+inline cudaError_t make_cross_map(CUtensorMap *m, const void *p, int B, int n, int heads, int d, const int64_t (&st)[3],
+                                  int hb, int rows) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return cudaErrorNotSupported;
+  // (a dimension of one element has no stride; the encoder wants a valid one all the same)
+  const cuuint64_t any = 2ull * (cuuint64_t)((d + 7) / 8 * 8);
+  const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)n, (cuuint64_t)B};
+  const cuuint64_t strides[3] = {heads > 1 ? 2ull * st[2] : any, n > 1 ? 2ull * st[1] : any, B > 1 ? 2ull * st[0] : any};
+  const cuuint32_t box[4] = {64, (cuuint32_t)hb, (cuuint32_t)rows, 1};
+  const cuuint32_t es[4] = {1, 1, 1, 1};
+  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(p), dims, strides, box, es,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// Head block size, its log2, and the sizes every launch needs.
+struct CrossSizes {
+  int G, GB, lg, kd, key_tiles;
+};
+inline CrossSizes cross_sizes(const tri_cross_shape &s) {
+  CrossSizes z;
+  z.G = s.H / s.Hk;
+  z.lg = 0;
+  while (z.lg < 7 && z.G % (2 << z.lg) == 0) ++z.lg;
+  z.GB = 1 << z.lg;
+  z.kd = (s.d + 15) / 16;
+  z.key_tiles = (s.S + kTile - 1) / kTile;
+  return z;
+}
+
+int cross_check_shape(const tri_cross_shape &s);
+
+}  // namespace triattn
