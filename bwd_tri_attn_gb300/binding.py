@@ -115,6 +115,8 @@ def lib_path() -> str:
 def load(path: str | None = None):
     """Loads ``libtriattn.so`` (built by ``__graft_entry__.build()``)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -237,6 +239,33 @@ def _stream(stream):
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+
+
+_raw_stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _on_device(device, *checked):
+    """Raises unless every argument that passed _arg is a CUDA tensor on the current device, and returns that
+    device's index (device: the first argument's get_device())."""
+    for c in checked:
+        if c is not None and (c[1].get_device() != device or device < 0):
+            break
+    else:
+        if device >= 0 and device == torch.cuda.current_device():
+            return device
+    _ptrs(*checked)  # (names the argument)
+    return device
+
+
+def _stream_on(device, stream):
+    """The raw handle of `stream`, or of the device's current stream (as _stream, with less work on the host)."""
+    if stream is None:
+        return _raw_stream_of(device) if _raw_stream_of is not None else torch.cuda.current_stream().cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _check(fn, rc):
@@ -630,24 +659,25 @@ def norm_shape_of(x: torch.Tensor, eps: float = 1e-5, dy: torch.Tensor | None = 
 
 
 def _empty_checkpoint(x):
-    return Checkpoint(torch.empty(x.shape, dtype=torch.int8, device=x.device),
-                      torch.empty((*x.shape[:-1], (x.shape[-1] + CKPT_GROUP - 1) // CKPT_GROUP), dtype=torch.float32,
-                                  device=x.device))
+    *rows, C = x.shape
+    return Checkpoint(x.new_empty(x.shape, dtype=torch.int8),
+                      x.new_empty((*rows, (C + CKPT_GROUP - 1) // CKPT_GROUP), dtype=_F32))
 
 
 def norm_forward(x, gamma=None, beta=None, eps=1e-5, checkpoint=False, stream=None):
     """LayerNorm over the last axis of x [..., C]: returns (y, mean, rstd), y in x's dtype and the FP32 statistics
     [...]; with ``checkpoint`` also the 8-bit checkpoint of x, written in the same pass."""
     shape = norm_shape_of(x, eps)
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    stats = torch.empty((2, *x.shape[:-1]), dtype=torch.float32, device=x.device)
-    mean, rstd = stats[0], stats[1]
-    if not checkpoint:
-        tri_norm_fwd(shape, x, gamma, beta, y, mean, rstd, stream=stream)
-        return y, mean, rstd
-    kept = _empty_checkpoint(x)
-    tri_norm_fwd(shape, x, gamma, beta, y, mean, rstd, kept.q8, kept.scale, stream)
-    return y, mean, rstd, kept
+    device = _on_device(x.get_device(), ("x", x), _arg(gamma, "gamma", _F32, shape.C, True),
+                        _arg(beta, "beta", _F32, shape.C, True))
+    rows = x.shape[:-1]
+    y, mean, rstd = x.new_empty(x.shape), x.new_empty(rows, dtype=_F32), x.new_empty(rows, dtype=_F32)
+    kept = _empty_checkpoint(x) if checkpoint else None
+    q8, scale = (kept.q8.data_ptr(), kept.scale.data_ptr()) if checkpoint else (None, None)
+    rc = load().tri_norm_fwd(shape, x.data_ptr(), _ptr(gamma), _ptr(beta), y.data_ptr(), mean.data_ptr(),
+                             rstd.data_ptr(), q8, scale, _stream_on(device, stream))
+    _check("tri_norm_fwd", rc)
+    return (y, mean, rstd, kept) if checkpoint else (y, mean, rstd)
 
 
 def norm_backward(x, gamma, mean, rstd, dy, workspace=None, stream=None):
@@ -658,28 +688,40 @@ def norm_backward(x, gamma, mean, rstd, dy, workspace=None, stream=None):
     like = kept[0] if kept is not None else x
     if not isinstance(like, torch.Tensor) or like.shape != dy.shape:
         raise ValueError(f"dy {tuple(dy.shape)} must have x's shape")
-    if dy.dim() < 1 or dy.numel() == 0:
+    n = dy.numel()
+    if dy.dim() < 1 or n == 0:
         raise ValueError(f"dy must have at least one row and one channel, got shape {tuple(dy.shape)}")
     C = dy.shape[-1]
-    shape = NormShape(dy.numel() // C, C if kept is not None else _row_stride(x, "x"), _row_stride(dy, "dy"), C, dtype,
-                      0.0)
-    dx = torch.empty(dy.shape, dtype=dy.dtype, device=dy.device)
+    M = n // C
+    shape = NormShape(M, C if kept is not None else _row_stride(x, "x"), _row_stride(dy, "dy"), C, dtype, 0.0)
+    if kept is not None:
+        given = [_arg(kept[0], "q8", torch.int8, n), _arg(kept[1], "scale", _F32, _norm_counts(shape)[1])]
+    else:
+        given = [_rows_arg(x, "x", dy.dtype, n)]
+    device = _on_device(dy.get_device(), *given, _arg(gamma, "gamma", _F32, C, True), _arg(mean, "mean", _F32, M),
+                        _arg(rstd, "rstd", _F32, M), ("dy", dy), _arg(workspace, "workspace", None, None, True))
+    dx = dy.new_empty(dy.shape)
     dgamma = dbeta = None
     if gamma is not None:
-        grads = torch.empty((2, C), dtype=torch.float32, device=dy.device)
-        dgamma, dbeta = grads[0], grads[1]
+        dgamma, dbeta = dy.new_empty(C, dtype=_F32), dy.new_empty(C, dtype=_F32)
         if workspace is None:
-            workspace = torch.empty(max(tri_norm_bwd_workspace_size(shape), 16), dtype=torch.uint8, device=dy.device)
-    tri_norm_bwd(shape, None if kept is not None else x, *(kept if kept is not None else (None, None)), gamma, mean,
-                 rstd, dy, dx, dgamma, dbeta, workspace, stream)
+            workspace = _workspace(tri_norm_bwd_workspace_size(shape), dy)
+    xp, q8, scale = (None, kept[0].data_ptr(), kept[1].data_ptr()) if kept is not None else (x.data_ptr(), None, None)
+    rc = load().tri_norm_bwd(shape, xp, q8, scale, _ptr(gamma), mean.data_ptr(), rstd.data_ptr(), dy.data_ptr(),
+                             dx.data_ptr(), _ptr(dgamma), _ptr(dbeta), _ptr(workspace), _nbytes(workspace),
+                             _stream_on(device, stream))
+    _check("tri_norm_bwd", rc)
     return dx, dgamma, dbeta
 
 
 def checkpoint_pack(x, stream=None) -> Checkpoint:
     """x [..., C] kept in 8 bits: int8 values and one FP32 scale for every 128 channels of a row."""
     shape = norm_shape_of(x)
+    device = _on_device(x.get_device(), ("x", x))
     kept = _empty_checkpoint(x)
-    tri_ckpt_pack(shape, x, kept.q8, kept.scale, stream)
+    rc = load().tri_ckpt_pack(shape, x.data_ptr(), kept.q8.data_ptr(), kept.scale.data_ptr(),
+                              _stream_on(device, stream))
+    _check("tri_ckpt_pack", rc)
     return kept
 
 
@@ -687,7 +729,11 @@ def checkpoint_unpack(kept, dtype=torch.bfloat16, stream=None) -> torch.Tensor:
     """The values a checkpoint stands for, rounded once to ``dtype``."""
     q8, scale = kept
     x = torch.empty(q8.shape, dtype=dtype, device=q8.device)
-    tri_ckpt_unpack(norm_shape_of(x), q8, scale, x, stream)
+    shape = norm_shape_of(x)
+    n, ng = _norm_counts(shape)
+    device = _on_device(x.get_device(), _arg(q8, "q8", torch.int8, n), _arg(scale, "scale", _F32, ng))
+    rc = load().tri_ckpt_unpack(shape, q8.data_ptr(), scale.data_ptr(), x.data_ptr(), _stream_on(device, stream))
+    _check("tri_ckpt_unpack", rc)
     return x
 
 
@@ -699,36 +745,53 @@ def cross_shape_of(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, scale: flo
         if t.dim() != 4:
             raise ValueError(f"{name} must have four axes (batch, position, head, channel), got shape {tuple(t.shape)}")
     B, T, H, d = Q.shape
-    S, Hk = K.shape[1], K.shape[2]
+    _, S, Hk, _ = K.shape
     if scale is None:
         scale = 1.0 / math.sqrt(d) if d else 0.0
-    three = ctypes.c_int64 * 3
-    return CrossShape(B, T, S, H, Hk, d, float(scale), three(*Q.stride()[:3]), three(*K.stride()[:3]),
-                      three(*V.stride()[:3]))
+    return CrossShape(B, T, S, H, Hk, d, scale, Q.stride()[:3], K.stride()[:3], V.stride()[:3])
 
 
-def _workspace(nbytes, device):
-    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+def _workspace(nbytes, like):
+    return like.new_empty(nbytes, dtype=torch.uint8) if nbytes else None
+
+
+def _cross_checked(Q, K, V, mask, kv_lens, scale, *more):
+    """The call's shape and its device, with every argument checked (more: arguments that have passed _arg)."""
+    shape = cross_shape_of(Q, K, V, scale)
+    kv = K.shape
+    if not (Q.dtype is _BF16 and K.dtype is _BF16 and V.dtype is _BF16 and V.shape == kv and kv[0] == shape.B
+            and kv[3] == shape.d and Q.stride(3) == K.stride(3) == V.stride(3) == 1 and mask is None and kv_lens is None):
+        more = (*_cross_args(shape, Q, K, V, mask, kv_lens), *more)  # (names what is wrong)
+    return shape, _on_device(Q.get_device(), ("Q", Q), ("K", K), ("V", V), *more)
 
 
 def cross_forward(Q, K, V, mask=None, kv_lens=None, scale=None, workspace=None, stream=None):
     """Cross attention of the queries Q [B, T, H, d] to the encoder states K, V [B, S, Hk, d] (BF16; heads, positions
     and batches may be spaced apart). mask: bool or uint8 [B, S], False where a key is not to be attended; kv_lens:
     int32 [B]. Returns (O, LSE): O [B, T, H, d] and the FP32 log-sum-exp [B, H, T] that cross_backward reads."""
-    shape = cross_shape_of(Q, K, V, scale)
-    O = torch.empty(Q.shape, dtype=torch.bfloat16, device=Q.device)
-    LSE = torch.empty((shape.B, shape.H, shape.T), dtype=torch.float32, device=Q.device)
+    shape, device = _cross_checked(Q, K, V, mask, kv_lens, scale, _arg(workspace, "workspace", None, None, True))
+    B, T, H, _ = Q.shape
+    O, LSE = Q.new_empty(Q.shape), Q.new_empty((B, H, T), dtype=_F32)
     if workspace is None:
-        workspace = _workspace(tri_cross_fwd_workspace_size(shape), Q.device)
-    tri_cross_fwd(shape, Q, K, V, mask, kv_lens, O, LSE, workspace, stream)
+        workspace = _workspace(tri_cross_fwd_workspace_size(shape), Q)
+    rc = load().tri_cross_fwd(shape, Q.data_ptr(), K.data_ptr(), V.data_ptr(), _ptr(mask), _ptr(kv_lens),
+                              O.data_ptr(), LSE.data_ptr(), _ptr(workspace), _nbytes(workspace),
+                              _stream_on(device, stream))
+    _check("tri_cross_fwd", rc)
     return O, LSE
 
 
 def cross_backward(Q, K, V, O, LSE, dO, mask=None, kv_lens=None, scale=None, workspace=None, stream=None):
     """Returns (dQ, dK, dV), without gaps, for the gradient dO of cross_forward's O."""
-    shape = cross_shape_of(Q, K, V, scale)
-    dQ, dK, dV = (torch.empty(t.shape, dtype=torch.bfloat16, device=Q.device) for t in (Q, K, V))
+    n = Q.numel() if isinstance(Q, torch.Tensor) else None
+    rows = n // Q.shape[-1] if n else None
+    shape, device = _cross_checked(Q, K, V, mask, kv_lens, scale, _arg(O, "O", _BF16, n), _arg(LSE, "LSE", _F32, rows),
+                                   _arg(dO, "dO", _BF16, n), _arg(workspace, "workspace", None, None, True))
+    dQ, dK, dV = Q.new_empty(Q.shape), K.new_empty(K.shape), V.new_empty(V.shape)
     if workspace is None:
-        workspace = _workspace(tri_cross_bwd_workspace_size(shape), Q.device)
-    tri_cross_bwd(shape, Q, K, V, mask, kv_lens, O, LSE, dO, dQ, dK, dV, workspace, stream)
+        workspace = _workspace(tri_cross_bwd_workspace_size(shape), Q)
+    rc = load().tri_cross_bwd(shape, Q.data_ptr(), K.data_ptr(), V.data_ptr(), _ptr(mask), _ptr(kv_lens),
+                              O.data_ptr(), LSE.data_ptr(), dO.data_ptr(), dQ.data_ptr(), dK.data_ptr(),
+                              dV.data_ptr(), _ptr(workspace), _nbytes(workspace), _stream_on(device, stream))
+    _check("tri_cross_bwd", rc)
     return dQ, dK, dV

@@ -64,6 +64,11 @@ struct CrossPos {
   }
 };
 
+// n / d, in 32 bits where both fit (a 64-bit division costs some hundred cycles).
+__device__ __forceinline__ int64_t div_units(int64_t n, int64_t d) {
+  return ((n | d) >> 31) == 0 ? (int64_t)((uint32_t)n / (uint32_t)d) : n / d;
+}
+
 // Sum of the units of all batches (the whole warp calls it; every lane gets the result).
 __device__ __forceinline__ int64_t cross_units(const CrossSched &s) {
   const int64_t per = (int64_t)s.heads * s.rows;  // units of a batch are per x its key tiles, either way
@@ -80,7 +85,7 @@ __device__ __forceinline__ CrossPos cross_locate(const CrossSched &s, int64_t u)
   const int64_t per = (int64_t)s.heads * s.rows;
   CrossPos p;
   if (!s.lens) {
-    p.b = (int)(u / (per * s.tiles(0)));
+    p.b = (int)div_units(u, per * s.tiles(0));
     u -= (int64_t)p.b * per * s.tiles(0);
   } else {
     const int lane = threadIdx.x & 31;
@@ -104,7 +109,7 @@ __device__ __forceinline__ CrossPos cross_locate(const CrossSched &s, int64_t u)
     }
   }
   p.load(s);
-  p.item = (int)(u / p.inner);
+  p.item = (int)div_units(u, p.inner);
   p.k = (int)(u - (int64_t)p.item * p.inner);
   return p;
 }
@@ -116,7 +121,8 @@ struct CrossShare {
 };
 
 __device__ __forceinline__ int64_t cross_bound(int64_t units, int cta, int ctas) {
-  return units / ctas * cta + units % ctas * cta / ctas;
+  const int64_t q = div_units(units, ctas);  // floor(units cta / ctas)
+  return q * cta + (uint32_t)((int)(units - q * ctas) * cta) / (uint32_t)ctas;
 }
 
 // The CTA's share (the whole warp calls it).
@@ -139,6 +145,51 @@ __device__ __forceinline__ CrossRun cross_run(const CrossPos &p, int left) {
   r.n = min(p.inner - p.k, left);
   r.slot = p.k != 0 ? 2 * (int)blockIdx.x : r.n < p.inner ? 2 * (int)blockIdx.x + 1 : -1;
   return r;
+}
+
+// ---------------------------------------------------------------- partial results
+// The join kernels' view of one item that several CTAs share: block x looks at the boundary between
+// CTAs x and x + 1 and has work if that is the first boundary inside an item. CTA `first` ended inside the item (its slot 2 first + 1),
+// the CTAs after it, up to `last`, began inside it (slots 2 c); CTAs without units are left out.
+constexpr int kMaxCtas = 256;
+struct CrossJoin {
+  CrossPos pos;
+  int first, count;
+  int slot[kMaxCtas];  // the item's partial slots, in order
+};
+
+// Fills j (shared memory; all threads of the block call it); false: nothing to do here.
+__device__ __forceinline__ bool cross_join_setup(const CrossSched &s, int ctas, CrossJoin &j) {
+  if (threadIdx.x < 32) {
+    const int64_t units = cross_units(s);
+    const int k = blockIdx.x + 1, lane = threadIdx.x;
+    const int64_t u = cross_bound(units, k, ctas);
+    int count = 0;
+    CrossPos p;
+    p.k = 0;
+    if (u < units) p = cross_locate(s, u);
+    if (p.k > 0 && cross_bound(units, k - 1, ctas) <= u - p.k) {
+      const int64_t u1 = u - p.k + p.inner;
+      if (lane == 0) j.slot[0] = 2 * k - 1;
+      count = 1;
+      for (int c0 = k; c0 < ctas; c0 += 32) {
+        const int c = c0 + lane;
+        const int64_t b0 = c < ctas ? cross_bound(units, c, ctas) : u1;
+        const uint32_t in = __ballot_sync(0xffffffffu, b0 < u1);
+        const bool has = b0 < u1 && cross_bound(units, c + 1, ctas) > b0;
+        const uint32_t take = __ballot_sync(0xffffffffu, has);
+        if (has) j.slot[count + __popc(take & ((1u << lane) - 1u))] = 2 * c;
+        count += __popc(take);
+        if (in != 0xffffffffu) break;
+      }
+    }
+    if (lane == 0) {
+      j.pos = p;
+      j.count = count;
+    }
+  }
+  __syncthreads();
+  return j.count > 0;
 }
 
 // Live keys of the 128-key tile at k0, one bit a key, in four words. all: the tile is whole and
@@ -192,15 +243,23 @@ __device__ __forceinline__ void zero_dead_rows(uint8_t *tile, const uint32_t (&w
 }
 
 // Descriptors of a 128-row tile of boxes (64 channels x 128 rows, 128-byte swizzled). K-major: the
-// product runs over the channels, 16 at a time (step k at k_off(k)); MN-major: over the rows, 16
-// rows a step, the channels being the operand's free index (64 per box).
-__device__ __forceinline__ uint64_t desc_k(uint32_t tile, int k) {
-  return sm100::smem_desc(tile + (k >> 2) * kBoxBytes + (k & 3) * 32, 16, 1024, sm100::kSwizzle128B);
-}
+// product runs over the channels, 16 at a time; MN-major: over the rows, 16 rows a step, the
+// channels being the operand's free index (64 per box).
+__device__ __forceinline__ uint64_t desc_k(uint32_t tile) { return sm100::smem_desc(tile, 16, 1024, sm100::kSwizzle128B); }
 __device__ __forceinline__ uint64_t desc_mn(uint32_t tile) {
   return sm100::smem_desc(tile, kBoxBytes, 1024, sm100::kSwizzle128B);
 }
 constexpr uint64_t kMnStep = (16 * 128) >> 4;  // 16 rows further
+
+// D = A B^T over the 16 kd channels of two K-major tiles (the products of scores). Precomputed
+// descriptors and one elect per four MMAs: built one by one in a loop, eight MMAs took 1100 cycles
+// to issue, twice what the tensor cores need for them.
+template <int BOXES>
+__device__ __forceinline__ void mma_channels(uint32_t d, uint32_t tile_a, uint32_t tile_b, uint32_t idesc, int kd) {
+  sm100::mma_ss_box_e(d, desc_k(tile_a), desc_k(tile_b), idesc, kd, 0u);
+  if (BOXES > 1 && kd > 4)
+    sm100::mma_ss_box_e(d, desc_k(tile_a + kBoxBytes), desc_k(tile_b + kBoxBytes), idesc, kd - 4, 1u);
+}
 
 // ---------------------------------------------------------------- host side
 // Tensor map of a [B, n, heads, d] BF16 tensor (strides in elements), boxes of 64 channels x `hb` heads

@@ -43,8 +43,8 @@ __global__ void __launch_bounds__(256) cross_bwd_prep_kernel(const CBwdArgs a, c
   if ((int)blockIdx.x < row_blocks) {
     const int64_t per = (int64_t)a.tiles * kTile, n = per * (a.H >> a.lg) * a.sc.B;
     for (int64_t i = (int64_t)blockIdx.x * 16 + g; i < n; i += (int64_t)row_blocks * 16) {
-      const int64_t bh = i / per;
-      const int r = (int)(i - bh * per), b = (int)(bh / (a.H >> a.lg)), hb = (int)(bh - (int64_t)b * (a.H >> a.lg));
+      const int64_t bh = div_units(i, per);
+      const int r = (int)(i - bh * per), b = (int)div_units(bh, a.H >> a.lg), hb = (int)(bh - (int64_t)b * (a.H >> a.lg));
       const int t = r >> a.lg, h = hb * a.GB + (r & (a.GB - 1));
       float s = 0.f;
       if (t < a.T && 8 * t16 < a.d) {
@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(CDkv<DP>::NTHREADS, 1)
       if (!wait_bar_warp(bar(C::B_QF + u % C::NST), phase(u), ab)) return false;
       tc_fence_after();
       const uint32_t sq = stage(u);
-      for (int k = 0; k < a.kd; ++k) mma_ss_e(tb + C::T_S, desc_k(sk, k), desc_k(sq, k), id_s, k > 0);
+      mma_channels<C::BOXES>(tb + C::T_S, sk, sq, id_s, a.kd);
       mma_commit_e(bar(C::B_S));
       return true;
     };
@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(CDkv<DP>::NTHREADS, 1)
       if (!wait_bar_warp(bar(C::B_DF + u % C::NST), phase(u), ab)) return false;
       tc_fence_after();
       const uint32_t sd = stage(u) + C::TILE;
-      for (int k = 0; k < a.kd; ++k) mma_ss_e(tb + C::T_DP, desc_k(sv, k), desc_k(sd, k), id_s, k > 0);
+      mma_channels<C::BOXES>(tb + C::T_DP, sv, sd, id_s, a.kd);
       mma_commit_e(bar(C::B_DP));
       if (left_next == 0) mma_commit_e(bar(C::B_KE));
       return true;
@@ -499,14 +499,14 @@ __global__ void __launch_bounds__(CDq<DP>::NTHREADS, 1)
         zero_dead_rows<C::BOXES>(sm + kst(u), w);
       }
       tc_fence_after();
-      for (int k = 0; k < a.kd; ++k) mma_ss_e(tb + C::T_S + 128 * (u & 1), desc_k(sq, k), desc_k(sb0 + kst(u), k), id_s, k > 0);
+      mma_channels<C::BOXES>(tb + C::T_S + 128 * (u & 1), sq, sb0 + kst(u), id_s, a.kd);
       mma_commit_e(bar(C::B_S + (u & 1)));
       return true;
     };
     auto dp_n = [&](int u) -> bool {  // dP of unit u; the last of a run hands Q and dO back
       if (!wait_bar_warp(bar(C::B_VF + u % C::NV), vph(u), ab)) return false;
       tc_fence_after();
-      for (int k = 0; k < a.kd; ++k) mma_ss_e(tb + C::T_DP, desc_k(sd, k), desc_k(sb0 + vst(u), k), id_s, k > 0);
+      mma_channels<C::BOXES>(tb + C::T_DP, sd, sb0 + vst(u), id_s, a.kd);
       mma_commit_e(bar(C::B_DP));
       mma_commit_e(bar(C::B_VE + u % C::NV));
       if (left_next == 0) mma_commit_e(bar(C::B_QE));
@@ -618,42 +618,58 @@ __global__ void __launch_bounds__(CDq<DP>::NTHREADS, 1)
 }
 
 // ================================================================ partial results
-// Block (k, y): the item that the boundary between CTAs k and k + 1 cuts, if that is its first cut;
-// eight rows of its outputs (dQ: 128 rows; dV, dK: 256), a warp each.
+// cross_join_setup says which item a block has. W warps take the partial results of four rows of its
+// outputs (dQ: 128 rows; dV, dK: 256) in turn, as in the forward's join, and the first of them adds
+// the W sums in order.
 __global__ void __launch_bounds__(256) cross_join_kernel(const CBwdArgs a, int ctas) {
+  __shared__ CrossJoin j;
+  __shared__ float4 acc_s[8][4][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t units = cross_units(a.sc);
-  const int k = blockIdx.x + 1;
-  const int64_t u = cross_bound(units, k, ctas);
-  if (u >= units) return;
-  const CrossPos p = cross_locate(a.sc, u);
-  if (p.k == 0) return;
-  const int64_t u0 = u - p.k, u1 = u0 + p.inner;
-  if (cross_bound(units, k - 1, ctas) > u0) return;
-  const int r = blockIdx.y * 8 + warp, which = r / kTile, row = r % kTile;
-  const int pitch = 16 * a.kd;
-  uint16_t *out;
-  if (a.sc.by_keys) {
-    const int hk = p.item / p.nt, key = (p.item % p.nt) * kTile + row;
-    if (key >= a.sc.S) return;
-    out = (which ? a.dK : a.dV) + (((int64_t)p.b * a.sc.S + key) * a.Hk + hk) * a.d;
-  } else {
-    const int hb = p.item / a.tiles, mt = p.item % a.tiles;
-    const int t = mt * (kTile >> a.lg) + (row >> a.lg), h = hb * a.GB + (row & (a.GB - 1));
-    if (t >= a.T) return;
-    out = a.dQ + (((int64_t)p.b * a.T + t) * a.H + h) * a.d;
+  const bool work = cross_join_setup(a.sc, ctas, j);
+  wait_previous_kernel();  // (every block: the next kernel of the stream relies on this one's end alone)
+  if (!work) return;
+  const int W = j.count > 4 ? 8 : j.count > 2 ? 4 : 2, w = warp & (W - 1), per = 8 / W;
+  const int pitch = 16 * a.kd, rows = (a.sc.by_keys ? 2 : 1) * kTile;
+  const int64_t slot = (int64_t)rows * pitch;
+  for (int r0 = (blockIdx.y * per + warp / W) * 4; r0 - warp / W * 4 < rows; r0 += gridDim.y * per * 4) {
+    // (every warp of the block makes the same number of rounds; r0 may pass the rows for some)
+    float4 acc[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r0 < rows && 4 * lane < pitch)
+      for (int c = w; c < j.count; c += W) {
+        const float *base = a.part + j.slot[c] * slot + (int64_t)r0 * pitch + 4 * lane;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const float4 v = *reinterpret_cast<const float4 *>(base + x * pitch);
+          acc[x].x += v.x, acc[x].y += v.y, acc[x].z += v.z, acc[x].w += v.w;
+        }
+      }
+#pragma unroll
+    for (int x = 0; x < 4; ++x) acc_s[warp][x][lane] = acc[x];
+    __syncthreads();
+    if (w == 0 && r0 < rows && 4 * lane < a.d)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        for (int y = 1; y < W; ++y) {
+          const float4 v = acc_s[warp + y][x][lane];
+          acc[x].x += v.x, acc[x].y += v.y, acc[x].z += v.z, acc[x].w += v.w;
+        }
+        const int row = (r0 + x) % kTile;
+        uint16_t *out;
+        if (a.sc.by_keys) {
+          const int hk = j.pos.item / j.pos.nt, key = (j.pos.item % j.pos.nt) * kTile + row;
+          if (key >= a.sc.S) continue;
+          out = ((r0 + x) / kTile ? a.dK : a.dV) + (((int64_t)j.pos.b * a.sc.S + key) * a.Hk + hk) * a.d;
+        } else {
+          const int hb = j.pos.item / a.tiles, t = (j.pos.item % a.tiles) * (kTile >> a.lg) + (row >> a.lg);
+          if (t >= a.T) continue;
+          out = a.dQ + (((int64_t)j.pos.b * a.T + t) * a.H + hb * a.GB + (row & (a.GB - 1))) * a.d;
+        }
+        *reinterpret_cast<uint2 *>(out + 4 * lane) = make_uint2(pack_bf16x2(acc[x].x, acc[x].y), pack_bf16x2(acc[x].z, acc[x].w));
+      }
+    __syncthreads();
   }
-  const int64_t slot = (int64_t)(a.sc.by_keys ? 2 : 1) * kTile * pitch;
-  const float *base = a.part + ((int64_t)which * kTile + row) * pitch + 4 * lane;
-  if (4 * lane >= a.d) return;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  // CTA k - 1 ended inside the item (slot 2 (k - 1) + 1), CTAs k, k + 1, ... began inside it (slot 2 k, ...)
-  for (int c = k - 1; c < ctas && (c < k || cross_bound(units, c, ctas) < u1); ++c) {
-    if (cross_bound(units, c, ctas) == cross_bound(units, c + 1, ctas)) continue;
-    const float4 v = *reinterpret_cast<const float4 *>(base + (c < k ? 2 * (int64_t)c + 1 : 2 * (int64_t)c) * slot);
-    acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
-  }
-  *reinterpret_cast<uint2 *>(out + 4 * lane) = make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
 }
 
 // ================================================================ host side
@@ -671,7 +687,7 @@ BwdGeo bwd_geo(const tri_cross_shape &s, int nsm) {
   g.tiles = (int)((((int64_t)s.T << z.lg) + kTile - 1) / kTile);
   const int64_t per = (int64_t)s.B * (s.H / z.GB) * g.tiles;  // row tiles
   const int64_t units = per * z.key_tiles;                    // of either kernel
-  g.dq_ctas = g.dkv_ctas = (int)std::min<int64_t>(units, nsm);
+  g.dq_ctas = g.dkv_ctas = (int)std::min<int64_t>(units, std::min(nsm, kMaxCtas));
   g.dq_split = z.key_tiles > 1;
   g.dkv_split = (int64_t)(z.G / z.GB) * g.tiles > 1;
   g.rows = per * kTile;
@@ -698,16 +714,14 @@ cudaError_t launch_bwd(const CUtensorMap &mq, const CUtensorMap &mdo, const CUte
   cross_dkv_kernel<DP><<<g.dkv_ctas, CDkv<DP>::NTHREADS, CDkv<DP>::SMEM, st>>>(mq, mdo, mk, mv, dkv);
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess && g.dkv_split && g.dkv_ctas > 1) {
-    cross_join_kernel<<<dim3(g.dkv_ctas - 1, 2 * kTile / 8), 256, 0, st>>>(dkv, g.dkv_ctas);
-    e = cudaGetLastError();
+    e = launch_after(cross_join_kernel, dim3(g.dkv_ctas - 1, 8), 256, st, dkv, g.dkv_ctas);
   }
   if (e == cudaSuccess) {
     cross_dq_kernel<DP><<<g.dq_ctas, CDq<DP>::NTHREADS, CDq<DP>::SMEM, st>>>(mq, mdo, mk, mv, dq);
     e = cudaGetLastError();
   }
   if (e == cudaSuccess && g.dq_split && g.dq_ctas > 1) {
-    cross_join_kernel<<<dim3(g.dq_ctas - 1, kTile / 8), 256, 0, st>>>(dq, g.dq_ctas);
-    e = cudaGetLastError();
+    e = launch_after(cross_join_kernel, dim3(g.dq_ctas - 1, 4), 256, st, dq, g.dq_ctas);
   }
   return e;
 }

@@ -2,13 +2,14 @@
 // division of the work).
 //
 // One CTA per SM works through its units; a unit is one 128-key tile against up to two tiles of 128
-// rows. Warps 0-3 and 4-7 are the softmax of row tiles 0 and 1 (thread = row), warp 8 loads K and V
-// through a TMA ring, warp 9 issues the MMAs, warp 10 loads Q. TMEM: S0, S1 (128 columns each;
-// P, as BF16 pairs, over the first half of S once S is in registers), O0, O1. The MMA warp issues
-//     P0 V (unit u), Q0 K (u + 1), P1 V (u), Q1 K (u + 1), ...
-// so the products of one row tile run while the other's softmax does. The running maximum is only
-// moved (and O rescaled) when it grows by more than 2^8: the reference value cancels in O / l, and P
-// up to 2^8 costs no precision.
+// rows. Two streams run side by side, each with a softmax warpgroup (warps 0-3 and 4-7, thread =
+// row) and an MMA warp (9 and 11): the two row tiles, or, where an item has one row tile (single tokens),
+// its even and odd key tiles, merged at the end of a run. Warp 8 loads K and V through a TMA ring; warp 10 loads Q and zeroes
+// masked rows of V. TMEM: S0, S1 (128 columns each; P, as BF16 pairs, over the first half of S once
+// S is in registers), O0, O1. A stream's MMA warp issues P V of unit u (in two halves, as P comes) and Q K of
+// unit u + 1 behind it, so the products of one stream run while the other's softmax does. The running
+// maximum is only moved (and O rescaled) when it grows by more than 2^8: the reference value cancels
+// in O / l, and P up to 2^8 costs no precision.
 #include <math.h>
 
 #include "cross.cuh"
@@ -23,12 +24,17 @@ struct CFwd {
   static constexpr int BOXES = DP / 64, TILE = BOXES * kBoxBytes;
   static constexpr int NST = DP == 128 ? 5 : 10;  // ring of K and V tiles, in turn
   static constexpr int OFF_RING = 2 * TILE, OFF_BAR = OFF_RING + NST * TILE;
-  static constexpr int B_FULL = 0, B_EMPTY = NST, B_QF = 2 * NST, B_QE = B_QF + 1, B_S = B_QE + 1, B_P = B_S + 2,
-                       B_O = B_P + 2, B_DONE = B_O + 2, NBAR = B_DONE + 1;
+  static constexpr int B_FULL = 0, B_EMPTY = NST, B_CLEAN = 2 * NST, B_QF = 3 * NST, B_QE = B_QF + 1, B_S = B_QE + 1,
+                       B_P = B_S + 2, B_O = B_P + 4, B_MERGE = B_O + 2, B_MERGED = B_MERGE + 1,
+                       B_DONE = B_MERGED + 1, NBAR = B_DONE + 2;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int OFF_SHARE = OFF_MISC + 16;
-  static constexpr int SMEM = OFF_SHARE + (int)sizeof(CrossShare) + 1024;
-  static constexpr int NTHREADS = 352;
+  static constexpr int OFF_ML = (OFF_SHARE + (int)sizeof(CrossShare) + 15) / 16 * 16;  // stream 1's maxima and sums
+  static constexpr int SMEM = OFF_ML + kTile * 8 + 1024;
+  static constexpr int NTHREADS = 384;
+  // 168 registers a thread at launch: 256 of them take 216, the other 128 give down to 72
+  static constexpr uint32_t REG_LAUNCH = 168, REG_SOFT = 216, REG_OTHER = 72;
+  static_assert(256 * REG_SOFT + (NTHREADS - 256) * REG_OTHER == NTHREADS * REG_LAUNCH, "register split");
   static constexpr int T_S = 0, T_O = 256;  // TMEM columns; row tile i: + 128 i
   static_assert(SMEM <= 227 * 1024, "shared memory budget");
   static_assert(OFF_SHARE % 4 == 0, "alignment");
@@ -40,6 +46,7 @@ struct CFwdArgs {
   int two;        // row tiles per item: 1 or 2
   float c;        // |scale| log2(e)
   bool negate;    // scale < 0
+  bool clean;     // there may be masked keys: warp 10 passes every tile on
   const uint8_t *mask;
   uint16_t *O;
   float *LSE;
@@ -60,55 +67,20 @@ __device__ __forceinline__ RowTile row_tile(const CFwdArgs &a, int item, int i) 
   return r;
 }
 
-// The largest of a thread's 128 scores in TMEM; kMasked: those of keys whose bit in w is clear are -inf.
-template <bool kMasked>
-__device__ __forceinline__ float tile_max(uint32_t ts, const uint32_t (&w)[4]) {
-  uint32_t s[2][32];
-  float mx[4];
-  tmem_ld32(ts, s[0]);
-#pragma unroll
+// Scores of keys whose bit in w is clear become -inf, in place (the rare tiles with such keys take
+// this extra pass, so that the others run one and the same code).
+__device__ __forceinline__ void mask_scores(uint32_t ts, const uint32_t (&w)[4]) {
+#pragma unroll 1
   for (int q = 0; q < 4; ++q) {
-    tmem_wait_ld(s[q & 1]);
-    if (q < 3) tmem_ld32(ts + 32 * (q + 1), s[(q + 1) & 1]);
-    auto at = [&](int j) {
-      return !kMasked || ((w[q] >> j) & 1u) ? __uint_as_float(s[q & 1][j]) : -INFINITY;
-    };
-    mx[q] = at(0);
+    const uint32_t m = q == 0 ? w[0] : q == 1 ? w[1] : q == 2 ? w[2] : w[3];
+    uint32_t s[32];
+    tmem_ld32(ts + 32 * q, s);
+    tmem_wait_ld(s);
 #pragma unroll
-    for (int j = 1; j < 31; j += 2) mx[q] = fmax3(mx[q], at(j), at(j + 1));
-    mx[q] = fmaxf(mx[q], at(31));
+    for (int j = 0; j < 32; ++j) s[j] = (m >> j) & 1u ? s[j] : 0xff800000u;
+    tmem_st32(ts + 32 * q, s);
   }
-  return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-}
-
-// P = 2^(c s + mu) of a thread's 128 scores, written over the first 64 columns of S as BF16 pairs
-// (each 16 columns once the 32 of S that they come from, and all before, are in registers);
-// returns their FP32 sum.
-template <bool kMasked>
-__device__ __forceinline__ float tile_exp(uint32_t ts, const uint32_t (&w)[4], float c, float mu) {
-  uint32_t s[2][32];
-  const float2 c2 = make_float2(c, c), mu2 = make_float2(mu, mu);
-  float2 sum[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-  tmem_ld32(ts, s[0]);
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    tmem_wait_ld(s[q & 1]);
-    if (q < 3) tmem_ld32(ts + 32 * (q + 1), s[(q + 1) & 1]);
-    auto at = [&](int j) {
-      return !kMasked || ((w[q] >> j) & 1u) ? __uint_as_float(s[q & 1][j]) : -INFINITY;
-    };
-    uint32_t pk[16];
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const float2 y = __ffma2_rn(make_float2(at(2 * j), at(2 * j + 1)), c2, mu2);
-      const float2 pv = make_float2(ex2(y.x), ex2(y.y));
-      sum[j & 3] = __fadd2_rn(sum[j & 3], pv);
-      pk[j] = pack_bf16x2(pv.x, pv.y);
-    }
-    tmem_st16(ts + 16 * q, pk);
-  }
-  const float2 t = __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3]));
-  return t.x + t.y;
+  tmem_wait_st();
 }
 
 template <int DP>
@@ -126,16 +98,20 @@ __global__ void __launch_bounds__(CFwd<DP>::NTHREADS, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::NST; ++s) {
       mbar_init(bar(C::B_FULL + s), 1);
-      mbar_init(bar(C::B_EMPTY + s), 1);
+      mbar_init(bar(C::B_EMPTY + s), 2);
+      mbar_init(bar(C::B_CLEAN + s), 1);
     }
     mbar_init(bar(C::B_QF), 1);
-    mbar_init(bar(C::B_QE), 1);
+    mbar_init(bar(C::B_QE), 2);
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(C::B_S + i), 1);
       mbar_init(bar(C::B_P + i), 128);
+      mbar_init(bar(C::B_P + 2 + i), 128);
       mbar_init(bar(C::B_O + i), 1);
+      mbar_init(bar(C::B_DONE + i), 1);
     }
-    mbar_init(bar(C::B_DONE), 1);
+    mbar_init(bar(C::B_MERGE), 128);
+    mbar_init(bar(C::B_MERGED), 128);
     misc[1] = 0;
     fence_barrier_init();
   }
@@ -153,11 +129,13 @@ __global__ void __launch_bounds__(CFwd<DP>::NTHREADS, 1)
   const uint32_t tb = misc[0];
   const CrossShare share = *reinterpret_cast<const CrossShare *>(sm + C::OFF_SHARE);
   const int n = share.n;
+  const bool alt = a.two == 1;  // the streams are the even and odd units of a run
   // ring positions of unit u: K at 2 u, V at 2 u + 1
   auto stage = [&](int x) { return sb0 + C::OFF_RING + (uint32_t)(x % C::NST) * C::TILE; };
   auto phase = [&](int x) { return (uint32_t)(x / C::NST) & 1u; };
 
   if (warp == 8) {
+    reg_dealloc<C::REG_OTHER>();
     // ------------------------------------------------------------ K and V
     CrossPos p = share.pos;
     bool ok = true;
@@ -180,7 +158,8 @@ __global__ void __launch_bounds__(CFwd<DP>::NTHREADS, 1)
     if (!ok && lane == 0)  // let the copies in flight land before the CTA exits
       for (int y = max(0, x - C::NST); y < x; ++y) drain_bar(bar(C::B_FULL + y % C::NST), phase(y));
   } else if (warp == 10) {
-    // ------------------------------------------------------------ Q, once per run of units of an item
+    reg_dealloc<C::REG_OTHER>();
+    // ------------------------------------------------------------ Q of a run; rows of V that are masked
     CrossPos p = share.pos;
     bool ok = true;
     int q = 0;
@@ -199,124 +178,147 @@ __global__ void __launch_bounds__(CFwd<DP>::NTHREADS, 1)
             tma_load_4d(sb0 + C::TILE + y * kBoxBytes, &mQ, bar(C::B_QF), 64 * y, r1.head0, r1.t0, p.b);
       }
       __syncwarp();
-      for (int k = 0; k < run.n; ++k) p.next(a.sc);
-      u += run.n;
+      for (int k = 0; k < run.n && ok; ++k, ++u) {
+        for (int x = 2 * u; a.clean && x < 2 * u + 2 && ok; ++x) {
+          KeyWords kw;
+          kw.load(a.mask, a.sc.len(p.b), p.b, a.sc.S, p.k * kTile);
+          ok = wait_bar_warp(bar(C::B_FULL + x % C::NST), phase(x), ab);
+          if (!ok) break;
+          if ((x & 1) && !kw.all) {
+            uint32_t w[4];
+            kw.words(w);
+            zero_dead_rows<C::BOXES>(sm + C::OFF_RING + (x % C::NST) * C::TILE, w);
+          }
+          if (lane == 0) mbar_arrive(bar(C::B_CLEAN + x % C::NST));
+        }
+        p.next(a.sc);
+      }
     }
     if (!ok && q > 0 && lane == 0) drain_bar(bar(C::B_QF), (q - 1) & 1);
-  } else if (warp == 9) {
-    // ------------------------------------------------------------ MMA issuer (whole warp, elect.sync)
+  } else if (warp == 9 || warp == 11) {
+    reg_dealloc<C::REG_OTHER>();
+    // ------------------------------------------------------------ MMA issuer of stream i (whole warp, elect.sync)
+    const int i = warp == 11;
     const uint32_t id_s = idesc_f16(128, 128, true, true, false, false) | (a.negate ? 1u << 13 : 0u);  // (bit 13: -A)
     const uint32_t id_o = idesc_f16(128, 16, true, true, false, true) + ((uint32_t)(2 * (a.kd - 1)) << 17);
-    CrossPos pc = share.pos, pn = share.pos;  // units u (P V) and u + 1 (Q K)
-    int runs = 0, run_left = 0;               // runs begun by the Q K side, units left of the current one
-    int np[2] = {0, 0};                       // units whose P V is issued, by row tile
-    bool ok = true;
-    // Q K of unit u at position pn for row tile i
-    auto qk = [&](int u, int i, bool last_tile) -> bool {
-      if (i == 0) {
-        if (run_left == 0) {
-          run_left = cross_run(pn, n - u).n;
-          if (!wait_bar_warp(bar(C::B_QF), runs & 1, ab)) return false;
-          ++runs;
-        }
-        --run_left;
-        if (!wait_bar_warp(bar(C::B_FULL + 2 * u % C::NST), phase(2 * u), ab)) return false;
-        tc_fence_after();
-      }
-      const uint32_t d = tb + C::T_S + 128 * i, sq = sb0 + i * C::TILE, sk = stage(2 * u);
-      for (int k = 0; k < a.kd; ++k) mma_ss_e(d, desc_k(sq, k), desc_k(sk, k), id_s, k > 0);
-      mma_commit_e(bar(C::B_S + i));
-      if (last_tile) {
-        mma_commit_e(bar(C::B_EMPTY + 2 * u % C::NST));
-        if (run_left == 0) mma_commit_e(bar(C::B_QE));
-      }
-      return true;
-    };
-    if (n > 0) {
-      const bool two = row_tile(a, pn.item, 1).live;
-      ok = qk(0, 0, !two);
-      if (ok && two) ok = qk(0, 1, true);
-      pn.next(a.sc);
-    }
-    bool first = true;  // the first unit of a run: P V starts the accumulator
-    int pv_left = n > 0 ? cross_run(pc, n).n : 0;
-    for (int u = 0; u < n && ok; ++u) {
-      const bool two = row_tile(a, pc.item, 1).live, more = u + 1 < n;
-      const bool two_next = more && row_tile(a, pn.item, 1).live;
-      KeyWords kw;
-      kw.load(a.mask, a.sc.len(pc.b), pc.b, a.sc.S, pc.k * kTile);
-      for (int i = 0; i < 2 && ok; ++i) {
-        if (i == 0 || two) {
-          if (i == 0) {
-            ok = wait_bar_warp(bar(C::B_FULL + (2 * u + 1) % C::NST), phase(2 * u + 1), ab);
-            if (!ok) break;
-            if (!kw.all) {
-              uint32_t w[4];
-              kw.words(w);
-              zero_dead_rows<C::BOXES>(sm + C::OFF_RING + ((2 * u + 1) % C::NST) * C::TILE, w);
-            }
-          }
-          ok = wait_bar_warp(bar(C::B_P + i), np[i] & 1, ab);
+    const uint32_t ds = tb + C::T_S + 128 * i, dO = tb + C::T_O + 128 * i, sq = sb0 + (alt ? 0 : i * C::TILE);
+    const int full = a.clean ? C::B_CLEAN : C::B_FULL;
+    CrossPos p = share.pos;   // of unit u + 1
+    int runs = 0, units = 0;  // runs begun, units of this stream whose P V is issued
+    int left = 0, k = 0;      // of unit u + 1: units left of its run (itself included), its place in the run
+    bool ok = true, live = false, first = false;  // of unit u: this stream's, the stream's first of a run
+    // Round u: P V of unit u, then Q K of unit u + 1. A unit that is not this stream's is handed back
+    // at once, but not before it is there: its slot's barrier counts both streams.
+#pragma unroll 1
+    for (int u = -1; u < n; ++u) {
+      if (u >= 0) {
+        const int x = 2 * u + 1;
+        ok = wait_bar_warp(bar(full + x % C::NST), phase(x), ab);
+        if (!ok) break;
+        if (live) {
+          // P comes in two halves of 64 keys
+          const uint64_t dv = desc_mn(stage(x));
+          ok = wait_bar_warp(bar(C::B_P + i), units & 1, ab);
           if (!ok) break;
-          ++np[i];
           tc_fence_after();
-          const uint32_t d = tb + C::T_O + 128 * i, p = tb + C::T_S + 128 * i;
-          const uint64_t dv = desc_mn(stage(2 * u + 1));
-          mma_ts_x8_e<0, 8, 16, 24, 32, 40, 48, 56>(d, p, dv, kMnStep, id_o, first ? 0u : 1u);
+          mma_ts_x4_e(dO, ds, dv, kMnStep, id_o, first ? 0u : 1u);
+          ok = wait_bar_warp(bar(C::B_P + 2 + i), units & 1, ab);
+          if (!ok) break;
+          tc_fence_after();
+          mma_ts_x4_e(dO, ds + 32, dv + 4 * kMnStep, kMnStep, id_o, 1u);
           mma_commit_e(bar(C::B_O + i));
-          if (i == 1 || !two) mma_commit_e(bar(C::B_EMPTY + (2 * u + 1) % C::NST));
+          mma_commit_e(bar(C::B_EMPTY + x % C::NST));
+          ++units;
+        } else if (lane == 0) {
+          mbar_arrive(bar(C::B_EMPTY + x % C::NST));
         }
-        if (more && (i == 0 || two_next)) ok = qk(u + 1, i, i == 1 || !two_next);
       }
-      first = --pv_left == 0;
-      pc.next(a.sc);
-      if (more) {
-        pn.next(a.sc);
-        if (first) pv_left = cross_run(pc, n - u - 1).n;
+      if (u + 1 == n) break;
+      const int x = 2 * (u + 1);
+      if (left == 0) {
+        left = cross_run(p, n - u - 1).n;
+        k = 0;
+        ok = wait_bar_warp(bar(C::B_QF), runs & 1, ab);
+        if (!ok) break;
+        ++runs;
       }
+      ok = wait_bar_warp(bar(full + x % C::NST), phase(x), ab);
+      if (!ok) break;
+      live = alt ? (k & 1) == i : row_tile(a, p.item, i).live;
+      first = k == (alt ? i : 0);
+      if (live) {
+        tc_fence_after();
+        mma_channels<C::BOXES>(ds, sq, stage(x), id_s, a.kd);
+        mma_commit_e(bar(C::B_S + i));
+        mma_commit_e(bar(C::B_EMPTY + x % C::NST));
+      } else if (lane == 0) {
+        mbar_arrive(bar(C::B_EMPTY + x % C::NST));
+      }
+      if (--left == 0) mma_commit_e(bar(C::B_QE));
+      ++k;
+      p.next(a.sc);
     }
-    mma_commit_e(bar(C::B_DONE));
-    if (lane == 0) drain_bar(bar(C::B_DONE), 0);
+    mma_commit_e(bar(C::B_DONE + i));
+    if (lane == 0) drain_bar(bar(C::B_DONE + i), 0);
     __syncwarp();
   } else {
-    // ------------------------------------------------------------ softmax of row tile i, thread = row
+    reg_alloc<C::REG_SOFT>();
+    // ------------------------------------------------------------ softmax of stream i, thread = row
     const int i = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tb + lanes + C::T_S + 128 * i, to = tb + lanes + C::T_O + 128 * i;
+    float2 *ml = reinterpret_cast<float2 *>(sm + C::OFF_ML);
     CrossPos p = share.pos;
     bool ok = true;
-    int x = 0;  // units of this row tile
+    int x = 0;       // units of this stream
+    int merges = 0;  // runs of two streams
     for (int u = 0; u < n && ok;) {
       const CrossRun run = cross_run(p, n - u);
-      const RowTile rt = row_tile(a, p.item, i);
+      const RowTile rt = row_tile(a, p.item, alt ? 0 : i);
       const int b = p.b;
-      if (!rt.live) {
+      if (!rt.live || (alt && run.n <= i)) {
         for (int k = 0; k < run.n; ++k) p.next(a.sc);
         u += run.n;
         continue;
       }
       const int len = a.sc.len(b);
       float m = -INFINITY, l = 0.f;  // the reference value (log2 units) and the sum of exponentials above it
-      for (int k = 0; k < run.n; ++k, ++u, ++x) {
+      bool first = true;             // O of this stream holds nothing yet
+      for (int k = 0; k < run.n; ++k, ++u) {
+        const int key0 = p.k * kTile;
+        p.next(a.sc);
+        if (alt && (k & 1) != i) continue;
         KeyWords kw;
-        kw.load(a.mask, len, b, a.sc.S, p.k * kTile);
+        kw.load(a.mask, len, b, a.sc.S, key0);
         ok = wait_bar_warp(bar(C::B_S + i), x & 1, ab);
         if (!ok) break;
+        ++x;
         tc_fence_after();
-        // S is read twice, 32 columns at a time (its 128 values and P's would not fit in registers):
-        // for the maximum, then for the exponentials
-        uint32_t w[4] = {~0u, ~0u, ~0u, ~0u};
-        if (!kw.all) kw.words(w);
-        const float top = (kw.all ? tile_max<false>(ts, w) : tile_max<true>(ts, w)) * a.c;
+        if (!kw.all) {
+          uint32_t w[4];
+          kw.words(w);
+          mask_scores(ts, w);
+        }
+        uint32_t s[4][32];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_ld32(ts + 32 * q, s[q]);
+        tmem_wait_ld(s);
+        float mx[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          mx[q] = __uint_as_float(s[q][0]);
+#pragma unroll
+          for (int j = 1; j < 31; j += 2) mx[q] = fmax3(mx[q], __uint_as_float(s[q][j]), __uint_as_float(s[q][j + 1]));
+          mx[q] = fmaxf(mx[q], __uint_as_float(s[q][31]));
+        }
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.c;
         if (__any_sync(0xffffffffu, top > m + 8.f)) {  // (from m = -inf: any finite top)
           const float m1 = fmaxf(m, top);
           const float f = m1 == -INFINITY ? 1.f : ex2(m - m1);
           m = m1;
           l *= f;
-          if (k > 0) {  // O holds earlier tiles: wait for the last of them and rescale
-            ok = wait_bar_warp(bar(C::B_O + i), (x - 1) & 1, ab);
-            if (!ok) break;
-            tc_fence_after();
+          if (!first) {
+            // O holds earlier tiles (the products that S came with were issued after theirs, so they are done)
             for (int q = 0; q < a.kd; ++q) {
               uint32_t o[16];
               tmem_ld16(to + 16 * q, o);
@@ -327,32 +329,84 @@ __global__ void __launch_bounds__(CFwd<DP>::NTHREADS, 1)
             }
           }
         }
+        first = false;
         const float mu = m == -INFINITY ? 0.f : -m;
-        l += kw.all ? tile_exp<false>(ts, w, a.c, mu) : tile_exp<true>(ts, w, a.c, mu);
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(bar(C::B_P + i));
-        p.next(a.sc);
+        const float2 c2 = make_float2(a.c, a.c), mu2 = make_float2(mu, mu);
+        float2 sum[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float2 y = __ffma2_rn(make_float2(__uint_as_float(s[q][2 * j]), __uint_as_float(s[q][2 * j + 1])), c2, mu2);
+            const float2 pv = make_float2(ex2(y.x), ex2(y.y));
+            sum[j & 3] = __fadd2_rn(sum[j & 3], pv);
+            pk[j] = pack_bf16x2(pv.x, pv.y);
+          }
+          tmem_st16(ts + 16 * q, pk);
+          if (q & 1) {  // half of P is there
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(bar(C::B_P + (q == 1 ? 0 : 2) + i));
+          }
+        }
+        const float2 t2 = __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3]));
+        l += t2.x + t2.y;
       }
       if (!ok) break;
-      // the item's rows: O / l, and the log-sum-exp
+      // the run's rows: O / l, and the log-sum-exp
       ok = wait_bar_warp(bar(C::B_O + i), (x - 1) & 1, ab);
       if (!ok) break;
       tc_fence_after();
+      float w0 = 1.f, w1 = 0.f;  // weights of the streams' O
+      const bool merge = alt && run.n > 1;
+      if (merge) {
+        if (i == 1) {  // stream 0's threads of the same rows read O1, and m and l from here
+          ml[row] = make_float2(m, l);
+          tc_fence_before();
+          mbar_arrive(bar(C::B_MERGE));
+          ok = wait_bar_warp(bar(C::B_MERGED), merges & 1, ab);
+          if (!ok) break;
+          tc_fence_after();
+          ++merges;
+          continue;
+        }
+        ok = wait_bar_warp(bar(C::B_MERGE), merges & 1, ab);
+        if (!ok) break;
+        tc_fence_after();
+        ++merges;
+        const float2 o = ml[row];
+        const float m1 = fmaxf(m, o.x);
+        if (m1 != -INFINITY) {
+          w0 = ex2(m - m1);
+          w1 = ex2(o.x - m1);
+        }
+        l = l * w0 + o.y * w1;
+        m = m1;
+      }
       const float inv = l > 0.f ? __fdividef(1.f, l) : 0.f;
       const float lse2 = l > 0.f ? m + __log2f(l) : -INFINITY;
       const int t = rt.t0 + (row >> a.lg), h = rt.head0 + (row & (a.GB - 1));
       const bool mine = t < a.T;
       const int pitch = 16 * a.kd;
-      float *part = a.part + ((int64_t)max(run.slot, 0) * a.two + i) * kTile * (pitch + 4) + row * pitch;
+      float *tile = a.part + ((int64_t)max(run.slot, 0) * a.two + (alt ? 0 : i)) * kTile * (pitch + 4);
+      float *part = tile + row * pitch;
       uint16_t *out = a.O + (((int64_t)b * a.T + t) * a.H + h) * a.d;
+      w0 *= inv;
+      w1 *= inv;
       for (int q = 0; q < a.kd; ++q) {
         uint32_t o[16];
         tmem_ld16(to + 16 * q, o);
         tmem_wait_ld(o);
         float f[16];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) f[j] = __uint_as_float(o[j]) * inv;
+        for (int j = 0; j < 16; ++j) f[j] = __uint_as_float(o[j]) * w0;
+        if (merge) {
+          tmem_ld16(to + 128 + 16 * q, o);
+          tmem_wait_ld(o);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) f[j] = fmaf(__uint_as_float(o[j]), w1, f[j]);
+        }
         if (mine && run.slot < 0) {
 #pragma unroll
           for (int j = 0; j < 2; ++j)
@@ -371,9 +425,10 @@ __global__ void __launch_bounds__(CFwd<DP>::NTHREADS, 1)
         if (run.slot < 0)
           a.LSE[((int64_t)b * a.H + h) * a.T + t] = lse2 * kLn2;
         else
-          (part - row * pitch + kTile * pitch)[row] = lse2;
+          tile[kTile * pitch + row] = lse2;
       }
       tc_fence_before();
+      if (merge) mbar_arrive(bar(C::B_MERGED));
     }
   }
   tc_fence_before();
@@ -384,50 +439,84 @@ __global__ void __launch_bounds__(CFwd<DP>::NTHREADS, 1)
   }
 }
 
-// Adds the partial results of the items that several CTAs share. Block (k, y): the item that the
-// boundary between CTAs k and k + 1 cuts, if that is its first cut; eight of its rows, a warp each.
+// Adds the partial results of the items that several CTAs share (cross_join_setup says which item a
+// block has). W warps take the partial results of four rows in turn (W: the power of two that covers
+// them, at most 8: two partial results are the rule, many the case of few rows over long keys), then
+// the first of them adds the W results in order.
 __global__ void __launch_bounds__(256) cross_fwd_join_kernel(const CFwdArgs a, int ctas) {
+  __shared__ CrossJoin j;
+  __shared__ float4 acc_s[8][4][32];
+  __shared__ float2 ml_s[8][4];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t units = cross_units(a.sc);
-  const int k = blockIdx.x + 1;
-  const int64_t u = cross_bound(units, k, ctas);
-  if (u >= units) return;
-  const CrossPos p = cross_locate(a.sc, u);
-  if (p.k == 0) return;
-  const int64_t u0 = u - p.k, u1 = u0 + p.inner;
-  if (cross_bound(units, k - 1, ctas) > u0) return;
-  const int r = blockIdx.y * 8 + warp, i = r / kTile, row = r % kTile;
-  const RowTile rt = row_tile(a, p.item, i);
-  const int t = rt.t0 + (row >> a.lg), h = rt.head0 + (row & (a.GB - 1));
-  if (!rt.live || t >= a.T) return;
-  const int pitch = 16 * a.kd;
-  const int64_t slot = (int64_t)a.two * kTile * (pitch + 4);
-  const float *base = a.part + (int64_t)i * kTile * (pitch + 4);
-  // CTA k - 1 ended inside the item (slot 2 (k - 1) + 1), CTAs k, k + 1, ... began inside it (slot 2 k, ...)
-  auto at = [&](int c) { return base + (c < k ? 2 * (int64_t)c + 1 : 2 * (int64_t)c) * slot; };
-  float top = -INFINITY;
-  int last = k - 1;
-  for (int c = k - 1; c < ctas && (c < k || cross_bound(units, c, ctas) < u1); ++c) {
-    if (cross_bound(units, c, ctas) == cross_bound(units, c + 1, ctas)) continue;
-    top = fmaxf(top, at(c)[kTile * pitch + row]);
-    last = c;
-  }
-  float l = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int c = k - 1; c <= last && top > -INFINITY; ++c) {
-    if (cross_bound(units, c, ctas) == cross_bound(units, c + 1, ctas)) continue;
-    const float w = ex2(at(c)[kTile * pitch + row] - top);
-    l += w;
-    if (4 * lane < pitch) {
-      const float4 v = *reinterpret_cast<const float4 *>(at(c) + row * pitch + 4 * lane);
-      acc.x = fmaf(w, v.x, acc.x), acc.y = fmaf(w, v.y, acc.y), acc.z = fmaf(w, v.z, acc.z), acc.w = fmaf(w, v.w, acc.w);
+  const bool work = cross_join_setup(a.sc, ctas, j);
+  wait_previous_kernel();  // (every block: the next kernel of the stream relies on this one's end alone)
+  if (!work) return;
+  const int W = j.count > 4 ? 8 : j.count > 2 ? 4 : 2, w = warp & (W - 1), per = 8 / W;
+  const int pitch = 16 * a.kd, tile = kTile * (pitch + 4);
+  const int64_t slot = (int64_t)a.two * tile;
+  const int rows = a.two * kTile;
+  for (int r0 = (blockIdx.y * per + warp / W) * 4; r0 - warp / W * 4 < rows; r0 += gridDim.y * per * 4) {
+    // (every warp of the block makes the same number of rounds; r0 may pass the rows for some)
+    const int i = r0 / kTile, row = r0 % kTile;  // four rows of one tile
+    const RowTile rt = row_tile(a, j.pos.item, i);
+    const bool live = r0 < rows && rt.live && rt.t0 + (row >> a.lg) < a.T;
+    float4 acc[4];
+    float m[4], l[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+      m[x] = -INFINITY;
+      l[x] = 0.f;
     }
+    for (int c = w; c < j.count && live; c += W) {
+      const float *base = a.part + j.slot[c] * slot + (int64_t)i * tile;
+      const float4 lse = *reinterpret_cast<const float4 *>(base + kTile * pitch + row);
+      const float ls[4] = {lse.x, lse.y, lse.z, lse.w};
+      float4 v[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        v[x] = 4 * lane < pitch ? *reinterpret_cast<const float4 *>(base + (row + x) * pitch + 4 * lane)
+                                : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const float m1 = fmaxf(m[x], ls[x]);
+        const float f = m1 == -INFINITY ? 0.f : ex2(m[x] - m1), g = m1 == -INFINITY ? 0.f : ex2(ls[x] - m1);
+        // (rows past T hold nothing: their weight is whatever it is, and they are not written)
+        acc[x] = make_float4(acc[x].x * f + v[x].x * g, acc[x].y * f + v[x].y * g, acc[x].z * f + v[x].z * g, acc[x].w * f + v[x].w * g);
+        l[x] = l[x] * f + g;
+        m[x] = m1;
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      acc_s[warp][x][lane] = acc[x];
+      if (lane == 0) ml_s[warp][x] = make_float2(m[x], l[x]);
+    }
+    __syncthreads();
+    if (w == 0 && live) {
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        for (int y = 1; y < W; ++y) {
+          const float2 ml = ml_s[warp + y][x];
+          const float4 v = acc_s[warp + y][x][lane];
+          const float m1 = fmaxf(m[x], ml.x);
+          const float f = m1 == -INFINITY ? 0.f : ex2(m[x] - m1), g = m1 == -INFINITY ? 0.f : ex2(ml.x - m1);
+          acc[x] = make_float4(acc[x].x * f + v.x * g, acc[x].y * f + v.y * g, acc[x].z * f + v.z * g, acc[x].w * f + v.w * g);
+          l[x] = l[x] * f + ml.y * g;
+          m[x] = m1;
+        }
+        const int t = rt.t0 + ((row + x) >> a.lg), h = rt.head0 + ((row + x) & (a.GB - 1));
+        if (t >= a.T) continue;
+        const float inv = l[x] > 0.f ? 1.f / l[x] : 0.f;
+        if (4 * lane < a.d)
+          *reinterpret_cast<uint2 *>(a.O + (((int64_t)j.pos.b * a.T + t) * a.H + h) * a.d + 4 * lane) =
+              make_uint2(pack_bf16x2(acc[x].x * inv, acc[x].y * inv), pack_bf16x2(acc[x].z * inv, acc[x].w * inv));
+        if (lane == 0)
+          a.LSE[((int64_t)j.pos.b * a.H + h) * a.T + t] = l[x] > 0.f ? (m[x] + __log2f(l[x])) * kLn2 : -INFINITY;
+      }
+    }
+    __syncthreads();
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  if (4 * lane < a.d)
-    *reinterpret_cast<uint2 *>(a.O + (((int64_t)p.b * a.T + t) * a.H + h) * a.d + 4 * lane) =
-        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-  if (lane == 0) a.LSE[((int64_t)p.b * a.H + h) * a.T + t] = l > 0.f ? (top + __log2f(l)) * kLn2 : -INFINITY;
 }
 
 // Launch geometry, from the shape and the SM count.
@@ -443,7 +532,7 @@ FwdGeo fwd_geo(const tri_cross_shape &s, int nsm) {
   g.two = r > kTile ? 2 : 1;
   g.rows = (int)((r + g.two * kTile - 1) / (g.two * kTile));
   const int64_t items = (int64_t)s.B * (s.H / z.GB) * g.rows, units = items * z.key_tiles;
-  g.ctas = (int)std::min<int64_t>(units, nsm);
+  g.ctas = (int)std::min<int64_t>(units, std::min(nsm, kMaxCtas));
   g.split = z.key_tiles > 1;
   g.bytes = g.split ? (size_t)2 * g.ctas * g.two * kTile * (16 * z.kd + 4) * sizeof(float) : 0;
   return g;
@@ -455,9 +544,12 @@ cudaError_t launch_fwd(const CUtensorMap &mq, const CUtensorMap &mk, const CUten
   using C = CFwd<DP>;
   static DeviceOnce ready;
   if (!ready.done(dev)) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(cross_fwd_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    cudaError_t e = cudaFuncSetAttribute(cross_fwd_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    cudaFuncAttributes fa;
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, cross_fwd_kernel<DP>);
     if (e != cudaSuccess) return e;
+    // the register split only balances if the kernel was built with exactly REG_LAUNCH
+    if (fa.numRegs != (int)C::REG_LAUNCH) return cudaErrorInvalidConfiguration;
     ready.mark(dev);
   }
   cross_fwd_kernel<DP><<<ctas, C::NTHREADS, C::SMEM, st>>>(mq, mk, mv, a);
@@ -470,8 +562,8 @@ int cross_check_shape(const tri_cross_shape &s) {
   if (s.B < 1 || s.T < 1 || s.S < 1 || s.H < 1 || s.Hk < 1 || s.d < 1 || s.H % s.Hk || !isfinite(s.scale))
     return TRI_ATTN_ERR_INVALID_ARG;
   if (s.d % 8 || s.d > 128 || s.B > 65535 || s.H > 1024 || s.T > (1 << 30) || s.S > (1 << 30)) return TRI_ATTN_ERR_UNSUPPORTED;
-  // unit counts and their products with the CTA count fit 64 bits
-  if ((double)s.B * s.H * (s.T / 128 + 1.0) * (s.S / 128 + 1.0) > 0x1p44) return TRI_ATTN_ERR_UNSUPPORTED;
+  // a CTA's units, and twice their number, fit 32 bits
+  if ((double)s.B * s.H * (s.T / 128 + 1.0) * (s.S / 128 + 1.0) > 0x1p36) return TRI_ATTN_ERR_UNSUPPORTED;
   const int64_t *st[3] = {s.q_stride, s.k_stride, s.v_stride};
   const int64_t heads[3] = {s.H, s.Hk, s.Hk}, n[3] = {s.T, s.S, s.S};
   for (int x = 0; x < 3; ++x) {
@@ -529,6 +621,7 @@ int tri_cross_fwd(tri_cross_shape shape, const tri_attn_bf16 *Q, const tri_attn_
   // (a scale of 0 as the smallest normal number: masked scores stay -inf and all others come to 0)
   a.c = fmaxf(fabsf(shape.scale) * kLog2e, 1.17549435e-38f);
   a.negate = shape.scale < 0.f;
+  a.clean = mask || kv_lens;
   a.mask = mask;
   a.O = O;
   a.LSE = LSE;
@@ -536,8 +629,7 @@ int tri_cross_fwd(tri_cross_shape shape, const tri_attn_bf16 *Q, const tri_attn_
   const auto st = static_cast<cudaStream_t>(stream);
   cudaError_t e = shape.d <= 64 ? launch_fwd<64>(mq, mk, mv, a, g.ctas, dev, st) : launch_fwd<128>(mq, mk, mv, a, g.ctas, dev, st);
   if (e == cudaSuccess && g.split && g.ctas > 1) {
-    cross_fwd_join_kernel<<<dim3(g.ctas - 1, g.two * kTile / 8), 256, 0, st>>>(a, g.ctas);
-    e = cudaGetLastError();
+    e = launch_after(cross_fwd_join_kernel, dim3(g.ctas - 1, g.two * 4), 256, st, a, g.ctas);
   }
   return e == cudaSuccess ? TRI_ATTN_OK : TRI_ATTN_ERR_CUDA;
 }

@@ -33,4 +33,27 @@ struct DeviceValue {
   void set(int dev, int x) { v[dev].store(x, std::memory_order_release); }
 };
 
+// Launch of a kernel that may be set up while the stream's previous kernel still runs (programmatic
+// dependent launch): it calls wait_previous_kernel() before it reads what that kernel wrote.
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, dim3 block, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
+// Until every thread of the stream's previous kernel is done and what it wrote can be read (at once
+// where the launch was an ordinary one).
+__device__ __forceinline__ void wait_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Lets the next kernel of the stream be set up (every CTA calls it once, or exits).
+__device__ __forceinline__ void allow_next_kernel() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 }  // namespace triattn
