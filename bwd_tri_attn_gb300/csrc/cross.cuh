@@ -62,6 +62,11 @@ struct CrossPos {
     item = 0;
     if (++b < s.B) load(s);
   }
+  // n units further, none of them but the last one the end of an item
+  __device__ __forceinline__ void skip(const CrossSched &s, int n) {
+    k += n - 1;
+    next(s);
+  }
 };
 
 // n / d, in 32 bits where both fit (a 64-bit division costs some hundred cycles).
@@ -192,27 +197,28 @@ __device__ __forceinline__ bool cross_join_setup(const CrossSched &s, int ctas, 
   return j.count > 0;
 }
 
-// Live keys of the 128-key tile at k0, one bit a key, in four words. all: the tile is whole and
-// there is no mask. The whole warp calls load() (its reads can be issued early) and then words().
+// Live keys of the 32 N keys from k0 on, one bit a key. all: every one of them is live and there is no mask. The
+// whole warp calls load() (its reads can be issued early) and then words().
+template <int N>
 struct KeyWords {
   bool all;
-  uint32_t bits;  // this lane's four keys: k0 + 32 i + lane
+  uint32_t bits;  // this lane's keys: k0 + 32 i + lane
   __device__ __forceinline__ void load(const uint8_t *mask, int len, int b, int S, int k0) {
     const int lane = threadIdx.x & 31;
-    all = !mask && k0 + kTile <= len;
+    all = !mask && k0 + 32 * N <= len;
     bits = 0u;
     if (all) return;
     const uint8_t *m = mask ? mask + (int64_t)b * S + k0 : nullptr;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < N; ++i) {
       const int j = 32 * i + lane;
       const bool live = k0 + j < len && (!m || __ldg(m + j) != 0);
       bits |= (live ? 1u : 0u) << i;
     }
   }
-  __device__ __forceinline__ void words(uint32_t (&w)[4]) const {
+  __device__ __forceinline__ void words(uint32_t (&w)[N]) const {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = __ballot_sync(0xffffffffu, (bits >> i) & 1u);
+    for (int i = 0; i < N; ++i) w[i] = __ballot_sync(0xffffffffu, (bits >> i) & 1u);
   }
 };
 
@@ -251,14 +257,34 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t tile) {
 }
 constexpr uint64_t kMnStep = (16 * 128) >> 4;  // 16 rows further
 
-// D = A B^T over the 16 kd channels of two K-major tiles (the products of scores). Precomputed
-// descriptors and one elect per four MMAs: built one by one in a loop, eight MMAs took 1100 cycles
-// to issue, twice what the tensor cores need for them.
+constexpr uint64_t kBoxStep = kBoxBytes >> 4;  // the next 64 channels of a K-major tile
+
+// D = A B^T over the 16 kd channels of two K-major tiles (the products of scores). Descriptors are built
+// ahead and elected once per four MMAs: built one by one in a loop, eight MMAs took 1100 cycles to
+// issue, twice what the tensor cores need for them.
 template <int BOXES>
-__device__ __forceinline__ void mma_channels(uint32_t d, uint32_t tile_a, uint32_t tile_b, uint32_t idesc, int kd) {
-  sm100::mma_ss_box_e(d, desc_k(tile_a), desc_k(tile_b), idesc, kd, 0u);
-  if (BOXES > 1 && kd > 4)
-    sm100::mma_ss_box_e(d, desc_k(tile_a + kBoxBytes), desc_k(tile_b + kBoxBytes), idesc, kd - 4, 1u);
+__device__ __forceinline__ void mma_channels(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, int kd) {
+  sm100::mma_ss_box_e(d, a, b, idesc, kd, 0u);
+  if (BOXES > 1 && kd > 4) sm100::mma_ss_box_e(d, a + kBoxStep, b + kBoxStep, idesc, kd - 4, 1u);
+}
+
+// A place in a ring of N slots and the phase parity of its barriers.
+template <int N>
+struct Ring {
+  int slot = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == N) {
+      slot = 0;
+      parity ^= 1u;
+    }
+  }
+};
+
+// One arrival for the whole warp, after every lane's work.
+__device__ __forceinline__ void warp_arrive(uint32_t bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) sm100::mbar_arrive(bar);
 }
 
 // ---------------------------------------------------------------- host side

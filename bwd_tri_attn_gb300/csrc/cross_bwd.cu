@@ -9,8 +9,8 @@
 //   cross_dkv_kernel        items are key tiles: S^T = K Q^T, dP^T = V dO^T, dV += P^T dO, dK += dS^T Q
 //   cross_dq_kernel         items are row tiles: S = Q K^T, dP = dO V^T, dQ += dS K
 //   cross_join_kernel       adds the partial results of items that several CTAs share, in CTA order
-// In both main kernels P and dS never leave TMEM: the element-wise warps (two warpgroups, thread = tile row,
-// 64 columns each) read the accumulators, and write P or dS as BF16 pairs over the columns they have
+// In both main kernels P and dS never leave TMEM: the element-wise warps (four warpgroups, thread = tile row,
+// 32 columns each) read the accumulators, and write P or dS as BF16 pairs over the columns they have
 // read, from where the next product takes its A operand. The second operands are the tiles that the
 // first products read, through MN-major descriptors.
 #include <math.h>
@@ -27,6 +27,7 @@ struct CBwdArgs {
   int T, H, Hk, d, kd, G, GB, lg;
   int tiles;        // row tiles of a head block
   float c, scale;   // scale log2(e), scale
+  bool clean;       // there may be masked keys
   const uint8_t *mask;
   const float *nl, *nd;  // [B][H / GB][tiles][128]: -LSE log2(e) (-inf: row without keys or past T), -D
   uint16_t *dQ, *dK, *dV;
@@ -83,6 +84,7 @@ __global__ void __launch_bounds__(256) cross_bwd_prep_kernel(const CBwdArgs a, c
 // 16 kd columns of a thread's accumulator row, chunks [q0, q1) of 16: times f to `out` (BF16, d
 // columns) or `part` (FP32). The whole warp calls it; rows with mine = false write nothing.
 __device__ __forceinline__ void store_row(uint32_t tm, int q0, int q1, int d, float f, bool mine, uint16_t *out, float *part) {
+#pragma unroll 1
   for (int q = q0; q < q1; ++q) {
     uint32_t o[16];
     tmem_ld16(tm + 16 * q, o);
@@ -106,45 +108,61 @@ __device__ __forceinline__ void store_row(uint32_t tm, int q0, int q1, int d, fl
   }
 }
 
+// The element-wise warps of both kernels: four warpgroups, thread = tile row, 32 columns each.
+constexpr int kEw = 16;
+constexpr int kBwdThreads = 32 * (kEw + 4);
+constexpr int kWarpLoad = kEw, kWarpMma = kEw + 1, kWarpRun = kEw + 2;
+
+// D (+)= A B over 128 rows of B, A the BF16 pairs that the four warpgroups wrote over the first half of
+// their 32 columns.
+__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool start) {
+  mma_ts_x8_e<0, 8, 32, 40, 64, 72, 96, 104>(d, a, b, kMnStep, idesc, start ? 0u : 1u);
+}
+
 // ================================================================ dK and dV
 template <int DP>
 struct CDkv {
   static constexpr int BOXES = DP / 64, TILE = BOXES * kBoxBytes;
-  static constexpr int NST = DP == 128 ? 2 : 4;  // stages of Q, dO and the rows' -LSE, -D
-  static constexpr int STAGE = 2 * TILE + 1024;
-  static constexpr int OFF_STAGE = 2 * TILE, OFF_BAR = OFF_STAGE + NST * STAGE;
-  static constexpr int B_QF = 0, B_QE = NST, B_DF = 2 * NST, B_DE = 3 * NST, B_KF = 4 * NST, B_KE = B_KF + 1,
-                       B_S = B_KE + 1, B_DP = B_S + 1, B_P = B_DP + 1, B_DS = B_P + 1, B_ACC = B_DS + 1,
-                       B_DONE = B_ACC + 1, NBAR = B_DONE + 1;
+  // Rings of Q, dO, and the rows' -LSE and -D. Q of unit u is read last (dK), one unit after Q of u + 1 is
+  // wanted: three slots. (K, V, three of Q and two of dO leave 3 KB: no room to align by hand.)
+  static constexpr int NQ = DP == 128 ? 3 : 5, ND = DP == 128 ? 2 : 4, NR = ND;
+  static constexpr int OFF_Q = 2 * TILE, OFF_D = OFF_Q + NQ * TILE, OFF_R = OFF_D + ND * TILE, OFF_BAR = OFF_R + NR * 1024;
+  static constexpr int B_QF = 0, B_QE = B_QF + NQ, B_DF = B_QE + NQ, B_DE = B_DF + ND, B_RF = B_DE + ND, B_RE = B_RF + NR,
+                       B_KF = B_RE + NR, B_KE = B_KF + 1, B_S = B_KE + 1, B_DP = B_S + 1, B_P = B_DP + 1, B_DS = B_P + 1,
+                       B_ACC = B_DS + 1, B_DONE = B_ACC + 1, NBAR = B_DONE + 1;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8, OFF_SHARE = OFF_MISC + 16;
-  static constexpr int SMEM = OFF_SHARE + (int)sizeof(CrossShare) + 1024;
-  static constexpr int NTHREADS = 352;
+  static constexpr int SMEM = OFF_SHARE + (int)sizeof(CrossShare);
   static constexpr int T_S = 0, T_DP = 128, T_DV = 256, T_DK = 384;
-  static_assert(SMEM <= 227 * 1024 && STAGE % 1024 == 0 && OFF_SHARE % 4 == 0, "shared memory");
+  static_assert(SMEM <= 227 * 1024 && OFF_SHARE % 4 == 0, "shared memory");
 };
 
 template <int DP>
-__global__ void __launch_bounds__(CDkv<DP>::NTHREADS, 1)
+__global__ void __launch_bounds__(kBwdThreads, 1)
     cross_dkv_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mDO,
                      const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mV, const CBwdArgs a) {
   using C = CDkv<DP>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t sm[];
   const uint32_t sb0 = smem_u32(sm);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (sb0 & 1023u) {  // (swizzled tiles need it; the declaration asks for it)
+    if (threadIdx.x == 0) atomicExch(a.sc.status, kStatusTimeout);
+    return;
+  }
+  // (the hardware's first four warps, which the schedulers prefer, are those that feed the others)
+  const int warp = ((threadIdx.x >> 5) + kEw) % (kEw + 4), lane = threadIdx.x & 31;
   auto bar = [&](int k) { return sb0 + C::OFF_BAR + 8u * (uint32_t)k; };
   volatile uint32_t *misc = reinterpret_cast<volatile uint32_t *>(sm + C::OFF_MISC);
   const Abort ab{reinterpret_cast<volatile int *>(misc + 1), a.sc.status};
   if (threadIdx.x == 0) {
-    for (int k = 0; k < C::NBAR; ++k) mbar_init(bar(k), k == C::B_P || k == C::B_DS ? 256 : 1);
+    for (int k = 0; k < C::NBAR; ++k)
+      mbar_init(bar(k), k == C::B_P || k == C::B_DS || (k >= C::B_RE && k < C::B_RE + C::NR) ? kEw : 1);
     misc[1] = 0;
     fence_barrier_init();
   }
-  if (warp == 9) {
+  if (warp == kWarpMma) {
     tmem_alloc(sb0 + C::OFF_MISC, 512);
     tmem_relinquish();
   }
-  if (warp == 8) {
+  if (warp == kWarpLoad) {
     const CrossShare sh = cross_share(a.sc);
     if (lane == 0) *reinterpret_cast<CrossShare *>(sm + C::OFF_SHARE) = sh;
   }
@@ -155,46 +173,58 @@ __global__ void __launch_bounds__(CDkv<DP>::NTHREADS, 1)
   const CrossShare share = *reinterpret_cast<const CrossShare *>(sm + C::OFF_SHARE);
   const int n = share.n;
   const int groups = a.G >> a.lg;  // head blocks of a key head
-  auto stage = [&](int u) { return sb0 + C::OFF_STAGE + (uint32_t)(u % C::NST) * C::STAGE; };
-  auto phase = [&](int u) { return (uint32_t)(u / C::NST) & 1u; };
 
-  if (warp == 8) {
-    // ------------------------------------------------------------ Q with -LSE and -D, and dO
+  if (warp == kWarpLoad) {
+    // ------------------------------------------------------------ the rows' -LSE and -D, Q, and dO
     CrossPos p = share.pos;
+    Ring<C::NQ> q;
+    Ring<C::ND> d;
+    Ring<C::NR> r;
     bool ok = true;
-    int u = 0, dq = 0, dd = 0;  // units, Q loads and dO loads issued
-    for (; u < n && ok; ++u) {
+    int lr = 0, lq = 0, ld = 0;  // loads issued
+    for (int u = 0; u < n && ok; ++u) {
       const int hk = p.item / p.nt, hb = hk * groups + p.k / a.tiles, mt = p.k % a.tiles;
       const int head0 = hb * a.GB, t0 = mt * (kTile >> a.lg);
       const int64_t rows = (((int64_t)p.b * (a.H >> a.lg) + hb) * a.tiles + mt) * kTile;
-      if (u >= C::NST) ok = wait_bar_warp(bar(C::B_QE + u % C::NST), phase(u) ^ 1u, ab);
+      if (u >= C::NQ) ok = wait_bar_warp(bar(C::B_QE + q.slot), q.parity ^ 1u, ab);
       if (!ok) break;
       if (lane == 0) {
-        const uint32_t fb = bar(C::B_QF + u % C::NST);
-        mbar_arrive_expect_tx(fb, C::TILE + 1024);
-#pragma unroll
-        for (int y = 0; y < C::BOXES; ++y) tma_load_4d(stage(u) + y * kBoxBytes, &mQ, fb, 64 * y, head0, t0, p.b);
-        bulk_load(stage(u) + 2 * C::TILE, a.nl + rows, 512, fb);
-        bulk_load(stage(u) + 2 * C::TILE + 512, a.nd + rows, 512, fb);
-      }
-      ++dq;
-      if (u >= C::NST) ok = wait_bar_warp(bar(C::B_DE + u % C::NST), phase(u) ^ 1u, ab);
-      if (!ok) break;
-      if (lane == 0) {
-        const uint32_t fb = bar(C::B_DF + u % C::NST);
+        const uint32_t fb = bar(C::B_QF + q.slot), dst = sb0 + C::OFF_Q + (uint32_t)(q.slot * C::TILE);
         mbar_arrive_expect_tx(fb, C::TILE);
 #pragma unroll
-        for (int y = 0; y < C::BOXES; ++y) tma_load_4d(stage(u) + C::TILE + y * kBoxBytes, &mDO, fb, 64 * y, head0, t0, p.b);
+        for (int y = 0; y < C::BOXES; ++y) tma_load_4d(dst + y * kBoxBytes, &mQ, fb, 64 * y, head0, t0, p.b);
       }
-      ++dd;
+      ++lq;
+      q.next();
+      if (u >= C::NR) ok = wait_bar_warp(bar(C::B_RE + r.slot), r.parity ^ 1u, ab);
+      if (!ok) break;
+      if (lane == 0) {
+        const uint32_t fb = bar(C::B_RF + r.slot), dst = sb0 + C::OFF_R + (uint32_t)(r.slot * 1024);
+        mbar_arrive_expect_tx(fb, 1024);
+        bulk_load(dst, a.nl + rows, 512, fb);
+        bulk_load(dst + 512, a.nd + rows, 512, fb);
+      }
+      ++lr;
+      r.next();
+      if (u >= C::ND) ok = wait_bar_warp(bar(C::B_DE + d.slot), d.parity ^ 1u, ab);
+      if (!ok) break;
+      if (lane == 0) {
+        const uint32_t fb = bar(C::B_DF + d.slot), dst = sb0 + C::OFF_D + (uint32_t)(d.slot * C::TILE);
+        mbar_arrive_expect_tx(fb, C::TILE);
+#pragma unroll
+        for (int y = 0; y < C::BOXES; ++y) tma_load_4d(dst + y * kBoxBytes, &mDO, fb, 64 * y, head0, t0, p.b);
+      }
+      ++ld;
+      d.next();
       __syncwarp();
       p.next(a.sc);
     }
     if (!ok && lane == 0) {  // let the copies in flight land before the CTA exits
-      for (int y = max(0, dq - C::NST); y < dq; ++y) drain_bar(bar(C::B_QF + y % C::NST), phase(y));
-      for (int y = max(0, dd - C::NST); y < dd; ++y) drain_bar(bar(C::B_DF + y % C::NST), phase(y));
+      for (int y = max(0, lq - C::NQ); y < lq; ++y) drain_bar(bar(C::B_QF + y % C::NQ), (y / C::NQ) & 1);
+      for (int y = max(0, lr - C::NR); y < lr; ++y) drain_bar(bar(C::B_RF + y % C::NR), (y / C::NR) & 1);
+      for (int y = max(0, ld - C::ND); y < ld; ++y) drain_bar(bar(C::B_DF + y % C::ND), (y / C::ND) & 1);
     }
-  } else if (warp == 10) {
+  } else if (warp == kWarpRun) {
     // ------------------------------------------------------------ K and V of a run
     CrossPos p = share.pos;
     bool ok = true;
@@ -213,81 +243,93 @@ __global__ void __launch_bounds__(CDkv<DP>::NTHREADS, 1)
         }
       }
       __syncwarp();
-      for (int k = 0; k < run.n; ++k) p.next(a.sc);
+      p.skip(a.sc, run.n);
       u += run.n;
     }
     if (!ok && q > 0 && lane == 0) drain_bar(bar(C::B_KF), (q - 1) & 1);
-  } else if (warp == 9) {
+  } else if (warp == kWarpMma) {
     // ------------------------------------------------------------ MMA issuer (whole warp, elect.sync)
     const uint32_t id_s = idesc_f16(128, 128, true, true, false, false);
     const uint32_t id_o = idesc_f16(128, 16, true, true, false, true) + ((uint32_t)(2 * (a.kd - 1)) << 17);
-    const uint32_t sk = sb0, sv = sb0 + C::TILE;
-    CrossPos p = share.pos;
-    int runs = 0, left = 0, left_next = 0;  // runs begun; units left of the run of unit u, and of unit u + 1
+    const uint64_t dk = desc_k(sb0), dv = desc_k(sb0 + C::TILE), q_k = desc_k(sb0 + C::OFF_Q), q_mn = desc_mn(sb0 + C::OFF_Q),
+                   d_k = desc_k(sb0 + C::OFF_D), d_mn = desc_mn(sb0 + C::OFF_D);
+    constexpr uint64_t kTileStep = C::TILE >> 4;
+    Ring<C::NQ> q;  // of unit u + 1
+    Ring<C::ND> d;
+    int q_slot = 0, d_slot = 0;  // of unit u
+    int runs = 0;
     bool ok = true;
-    auto s_t = [&](int u) -> bool {  // S^T of unit u (its run's K has to be there)
-      if (left_next == 0) {
-        left_next = cross_run(p, n - u).n;
-        if (!wait_bar_warp(bar(C::B_KF), runs & 1, ab)) return false;
-        ++runs;
-      }
-      --left_next;
-      if (!wait_bar_warp(bar(C::B_QF + u % C::NST), phase(u), ab)) return false;
-      tc_fence_after();
-      const uint32_t sq = stage(u);
-      mma_channels<C::BOXES>(tb + C::T_S, sk, sq, id_s, a.kd);
-      mma_commit_e(bar(C::B_S));
-      return true;
-    };
-    auto dp_t = [&](int u) -> bool {  // dP^T of unit u; the last of a run hands K and V back
-      if (!wait_bar_warp(bar(C::B_DF + u % C::NST), phase(u), ab)) return false;
-      tc_fence_after();
-      const uint32_t sd = stage(u) + C::TILE;
-      mma_channels<C::BOXES>(tb + C::T_DP, sv, sd, id_s, a.kd);
-      mma_commit_e(bar(C::B_DP));
-      if (left_next == 0) mma_commit_e(bar(C::B_KE));
-      return true;
-    };
-    if (n > 0) {
-      ok = s_t(0) && dp_t(0);
+    // What a unit needs to know about the next one is worked out ahead: what stands between a wait and
+    // the products behind it is on the critical path.
+    CrossPos p = share.pos;
+    int left = 0;  // units left of unit u + 1's run after it
+    bool first = true, last = false, begin1 = false, end1 = false;
+    auto ahead = [&](int u1) {
+      begin1 = left == 0;
+      if (begin1) left = cross_run(p, n - u1).n;
+      end1 = --left == 0;
       p.next(a.sc);
-      left = left_next + 1;
-    }
-    bool first = true;
-    for (int u = 0; u < n && ok; ++u) {
+    };
+    if (n > 0) ahead(0);
+    // Round u: dV of unit u and S^T of unit u + 1 (its columns are P's) while the warps work on dS; dK of
+    // unit u and dP^T of unit u + 1 (its columns are dS's) while they work on the next P. Round -1: S^T
+    // and dP^T of unit 0.
+#pragma unroll 1
+    for (int u = -1; u < n; ++u) {
       const bool more = u + 1 < n;
-      --left;
-      // dV of unit u, then S^T of unit u + 1 (its columns are P's): while the warps work on dS
-      ok = wait_bar_warp(bar(C::B_P), u & 1, ab);
-      if (!ok) break;
-      tc_fence_after();
-      mma_ts_x8_e<0, 8, 16, 24, 64, 72, 80, 88>(tb + C::T_DV, tb + C::T_S, desc_mn(stage(u) + C::TILE), kMnStep, id_o, first ? 0u : 1u);
-      mma_commit_e(bar(C::B_DE + u % C::NST));
-      if (more) ok = s_t(u + 1);
-      if (!ok) break;
-      // dK of unit u, then dP^T of unit u + 1: while the warps work on the next P
-      ok = wait_bar_warp(bar(C::B_DS), u & 1, ab);
-      if (!ok) break;
-      tc_fence_after();
-      mma_ts_x8_e<0, 8, 16, 24, 64, 72, 80, 88>(tb + C::T_DK, tb + C::T_DP, desc_mn(stage(u)), kMnStep, id_o, first ? 0u : 1u);
-      mma_commit_e(bar(C::B_QE + u % C::NST));
-      first = left == 0;
-      if (first) mma_commit_e(bar(C::B_ACC));
-      if (more) {
-        ok = dp_t(u + 1);
-        p.next(a.sc);
-        if (first) left = left_next + 1;
+      if (u >= 0) {
+        ok = wait_bar_warp(bar(C::B_P), u & 1, ab);
+        if (!ok) break;
+        tc_fence_after();
+        mma_rows(tb + C::T_DV, tb + C::T_S, d_mn + d_slot * kTileStep, id_o, first);
       }
+      if (more) {
+        if (begin1) {
+          ok = wait_bar_warp(bar(C::B_KF), runs & 1, ab);
+          if (!ok) break;
+          ++runs;
+        }
+        ok = wait_bar_warp(bar(C::B_QF + q.slot), q.parity, ab);
+        if (!ok) break;
+        tc_fence_after();
+        mma_channels<C::BOXES>(tb + C::T_S, dk, q_k + q.slot * kTileStep, id_s, a.kd);
+        mma_commit_e(bar(C::B_S));
+      }
+      if (u >= 0) {
+        mma_commit_e(bar(C::B_DE + d_slot));
+        ok = wait_bar_warp(bar(C::B_DS), u & 1, ab);
+        if (!ok) break;
+        tc_fence_after();
+        mma_rows(tb + C::T_DK, tb + C::T_DP, q_mn + q_slot * kTileStep, id_o, first);
+        if (last) mma_commit_e(bar(C::B_ACC));
+      }
+      if (more) {
+        ok = wait_bar_warp(bar(C::B_DF + d.slot), d.parity, ab);
+        if (!ok) break;
+        tc_fence_after();
+        mma_channels<C::BOXES>(tb + C::T_DP, dv, d_k + d.slot * kTileStep, id_s, a.kd);
+        mma_commit_e(bar(C::B_DP));
+        if (end1) mma_commit_e(bar(C::B_KE));
+      }
+      if (u >= 0) mma_commit_e(bar(C::B_QE + q_slot));
+      q_slot = q.slot;
+      d_slot = d.slot;
+      q.next();
+      d.next();
+      first = begin1;
+      last = end1;
+      if (u + 2 < n) ahead(u + 2);
     }
     mma_commit_e(bar(C::B_DONE));
     if (lane == 0) drain_bar(bar(C::B_DONE), 0);
     __syncwarp();
-  } else {
-    // ------------------------------------------------------------ P and dS, thread = key, 64 queries a warpgroup
-    const int half = warp >> 2, row = (warp & 3) * 32 + lane;
+  } else if (warp < kEw) {
+    // ------------------------------------------------------------ P and dS, thread = key, 32 queries a warpgroup
+    const int part4 = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t ts = tb + lanes + C::T_S + 64 * half, tdp = tb + lanes + C::T_DP + 64 * half;
+    const uint32_t ts = tb + lanes + C::T_S + 32 * part4, tdp = tb + lanes + C::T_DP + 32 * part4;
     CrossPos p = share.pos;
+    Ring<C::NR> r;
     bool ok = true;
     int runs = 0;
     const float2 c2 = make_float2(a.c, a.c);
@@ -297,72 +339,66 @@ __global__ void __launch_bounds__(CDkv<DP>::NTHREADS, 1)
       const bool live = key < a.sc.len(b) && (!a.mask || __ldg(a.mask + (int64_t)b * a.sc.S + key) != 0);
       const uint32_t keep = live ? ~0u : 0u;
       for (int k = 0; k < run.n; ++k, ++u) {
-        const float4 *nl = reinterpret_cast<const float4 *>(sm + C::OFF_STAGE + (u % C::NST) * C::STAGE + 2 * C::TILE) + 16 * half;
+        const float4 *nl = reinterpret_cast<const float4 *>(sm + C::OFF_R + r.slot * 1024) + 8 * part4;
         const float4 *nd = nl + 32;
-        // (-LSE and -D came with Q: the copy is visible to the threads that have seen its barrier)
-        ok = wait_bar_warp(bar(C::B_QF + u % C::NST), phase(u), ab) && wait_bar_warp(bar(C::B_S), u & 1, ab);
+        ok = wait_bar_warp(bar(C::B_RF + r.slot), r.parity, ab) && wait_bar_warp(bar(C::B_S), u & 1, ab);
         if (!ok) break;
         tc_fence_after();
-        float2 pr[2][16];
+        float2 pr[16];
+        uint32_t s[32], pk[16];
+        tmem_ld32(ts, s);
+        tmem_wait_ld(s);
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          uint32_t s[32], pk[16];
-          tmem_ld32(ts + 32 * q, s);
-          tmem_wait_ld(s);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float4 l4 = nl[8 * q + j];
-            const float2 y0 = __ffma2_rn(make_float2(__uint_as_float(s[4 * j]), __uint_as_float(s[4 * j + 1])), c2, make_float2(l4.x, l4.y));
-            const float2 y1 = __ffma2_rn(make_float2(__uint_as_float(s[4 * j + 2]), __uint_as_float(s[4 * j + 3])), c2, make_float2(l4.z, l4.w));
-            pr[q][2 * j] = make_float2(ex2(y0.x), ex2(y0.y));
-            pr[q][2 * j + 1] = make_float2(ex2(y1.x), ex2(y1.y));
-            pk[2 * j] = pack_bf16x2(pr[q][2 * j].x, pr[q][2 * j].y) & keep;
-            pk[2 * j + 1] = pack_bf16x2(pr[q][2 * j + 1].x, pr[q][2 * j + 1].y) & keep;
-          }
-          tmem_st16(ts + 16 * q, pk);
+        for (int j = 0; j < 8; ++j) {
+          const float4 l4 = nl[j];
+          const float2 y0 = __ffma2_rn(make_float2(__uint_as_float(s[4 * j]), __uint_as_float(s[4 * j + 1])), c2, make_float2(l4.x, l4.y));
+          const float2 y1 = __ffma2_rn(make_float2(__uint_as_float(s[4 * j + 2]), __uint_as_float(s[4 * j + 3])), c2, make_float2(l4.z, l4.w));
+          pr[2 * j] = make_float2(ex2(y0.x), ex2(y0.y));
+          pr[2 * j + 1] = make_float2(ex2(y1.x), ex2(y1.y));
+          pk[2 * j] = pack_bf16x2(pr[2 * j].x, pr[2 * j].y) & keep;
+          pk[2 * j + 1] = pack_bf16x2(pr[2 * j + 1].x, pr[2 * j + 1].y) & keep;
         }
+        tmem_st16(ts, pk);
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(bar(C::B_P));
+        warp_arrive(bar(C::B_P));
         ok = wait_bar_warp(bar(C::B_DP), u & 1, ab);
         if (!ok) break;
         tc_fence_after();
+        tmem_ld32(tdp, s);
+        tmem_wait_ld(s);
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          uint32_t s[32], pk[16];
-          tmem_ld32(tdp + 32 * q, s);
-          tmem_wait_ld(s);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float4 d4 = nd[8 * q + j];
-            const float2 y0 = __fmul2_rn(pr[q][2 * j], __fadd2_rn(make_float2(__uint_as_float(s[4 * j]), __uint_as_float(s[4 * j + 1])), make_float2(d4.x, d4.y)));
-            const float2 y1 = __fmul2_rn(pr[q][2 * j + 1], __fadd2_rn(make_float2(__uint_as_float(s[4 * j + 2]), __uint_as_float(s[4 * j + 3])), make_float2(d4.z, d4.w)));
-            pk[2 * j] = pack_bf16x2(y0.x, y0.y) & keep;
-            pk[2 * j + 1] = pack_bf16x2(y1.x, y1.y) & keep;
-          }
-          tmem_st16(tdp + 16 * q, pk);
+        for (int j = 0; j < 8; ++j) {
+          const float4 d4 = nd[j];
+          const float2 y0 = __fmul2_rn(pr[2 * j], __fadd2_rn(make_float2(__uint_as_float(s[4 * j]), __uint_as_float(s[4 * j + 1])), make_float2(d4.x, d4.y)));
+          const float2 y1 = __fmul2_rn(pr[2 * j + 1], __fadd2_rn(make_float2(__uint_as_float(s[4 * j + 2]), __uint_as_float(s[4 * j + 3])), make_float2(d4.z, d4.w)));
+          pk[2 * j] = pack_bf16x2(y0.x, y0.y) & keep;
+          pk[2 * j + 1] = pack_bf16x2(y1.x, y1.y) & keep;
         }
+        tmem_st16(tdp, pk);
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(bar(C::B_DS));
+        warp_arrive(bar(C::B_DS));
+        if (lane == 0) mbar_arrive(bar(C::B_RE + r.slot));
+        r.next();
         p.next(a.sc);
       }
       if (!ok) break;
-      // the run's sums: warpgroup 0 stores dV, warpgroup 1 dK
+      // the run's sums: warpgroups 0 and 1 store the halves of dV's channels, 2 and 3 dK's
       ok = wait_bar_warp(bar(C::B_ACC), runs & 1, ab);
       if (!ok) break;
       tc_fence_after();
       const int64_t off = (((int64_t)b * a.sc.S + key) * a.Hk + hk) * a.d;
-      const int pitch = 16 * a.kd;
-      float *part = a.part + (((int64_t)max(run.slot, 0) * 2 + half) * kTile + row) * pitch;
-      store_row(tb + lanes + (half ? C::T_DK : C::T_DV), 0, a.kd, a.d, half ? a.scale : 1.f, key < a.sc.S,
-                run.slot < 0 ? (half ? a.dK : a.dV) + off : nullptr, part);
+      const int pitch = 16 * a.kd, which = part4 >> 1, mid = (a.kd + 1) / 2;
+      float *part = a.part + (((int64_t)max(run.slot, 0) * 2 + which) * kTile + row) * pitch;
+      store_row(tb + lanes + (which ? C::T_DK : C::T_DV), part4 & 1 ? mid : 0, part4 & 1 ? a.kd : mid, a.d, which ? a.scale : 1.f,
+                key < a.sc.S, run.slot < 0 ? (which ? a.dK : a.dV) + off : nullptr, part);
       tc_fence_before();
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == kWarpMma) {
     tc_fence_after();
     tmem_dealloc(tb, 512);
   }
@@ -374,38 +410,38 @@ struct CDq {
   static constexpr int BOXES = DP / 64, TILE = BOXES * kBoxBytes;
   static constexpr int NK = DP == 128 ? 3 : 6, NV = DP == 128 ? 2 : 4;
   static constexpr int OFF_K = 2 * TILE, OFF_V = OFF_K + NK * TILE, OFF_BAR = OFF_V + NV * TILE;
-  static constexpr int B_KF = 0, B_KE = NK, B_VF = 2 * NK, B_VE = B_VF + NV, B_QF = B_VE + NV, B_QE = B_QF + 1,
+  static constexpr int B_KF = 0, B_KE = NK, B_KC = 2 * NK, B_VF = 3 * NK, B_VE = B_VF + NV, B_QF = B_VE + NV, B_QE = B_QF + 1,
                        B_S = B_QE + 1, B_DP = B_S + 2, B_DPE = B_DP + 1, B_DS = B_DPE + 1, B_ACC = B_DS + 1,
                        B_DONE = B_ACC + 1, NBAR = B_DONE + 1;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8, OFF_SHARE = OFF_MISC + 16;
   static constexpr int SMEM = OFF_SHARE + (int)sizeof(CrossShare) + 1024;
-  static constexpr int NTHREADS = 352;
   static constexpr int T_S = 0, T_DP = 256, T_DQ = 384;  // (S twice: units in turn)
   static_assert(SMEM <= 227 * 1024 && OFF_SHARE % 4 == 0, "shared memory");
 };
 
 template <int DP>
-__global__ void __launch_bounds__(CDq<DP>::NTHREADS, 1)
+__global__ void __launch_bounds__(kBwdThreads, 1)
     cross_dq_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mDO,
                     const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mV, const CBwdArgs a) {
   using C = CDq<DP>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sb0 = smem_u32(sm);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (the hardware's first four warps, which the schedulers prefer, are those that feed the others)
+  const int warp = ((threadIdx.x >> 5) + kEw) % (kEw + 4), lane = threadIdx.x & 31;
   auto bar = [&](int k) { return sb0 + C::OFF_BAR + 8u * (uint32_t)k; };
   volatile uint32_t *misc = reinterpret_cast<volatile uint32_t *>(sm + C::OFF_MISC);
   const Abort ab{reinterpret_cast<volatile int *>(misc + 1), a.sc.status};
   if (threadIdx.x == 0) {
-    for (int k = 0; k < C::NBAR; ++k) mbar_init(bar(k), k == C::B_DPE || k == C::B_DS ? 256 : 1);
+    for (int k = 0; k < C::NBAR; ++k) mbar_init(bar(k), k == C::B_DPE || k == C::B_DS ? kEw : 1);
     misc[1] = 0;
     fence_barrier_init();
   }
-  if (warp == 9) {
+  if (warp == kWarpMma) {
     tmem_alloc(sb0 + C::OFF_MISC, 512);
     tmem_relinquish();
   }
-  if (warp == 8) {
+  if (warp == kWarpLoad) {
     const CrossShare sh = cross_share(a.sc);
     if (lane == 0) *reinterpret_cast<CrossShare *>(sm + C::OFF_SHARE) = sh;
   }
@@ -415,46 +451,47 @@ __global__ void __launch_bounds__(CDq<DP>::NTHREADS, 1)
   const uint32_t tb = misc[0];
   const CrossShare share = *reinterpret_cast<const CrossShare *>(sm + C::OFF_SHARE);
   const int n = share.n;
-  auto kst = [&](int u) { return (uint32_t)(C::OFF_K + (u % C::NK) * C::TILE); };
-  auto vst = [&](int u) { return (uint32_t)(C::OFF_V + (u % C::NV) * C::TILE); };
-  auto kph = [&](int u) { return (uint32_t)(u / C::NK) & 1u; };
-  auto vph = [&](int u) { return (uint32_t)(u / C::NV) & 1u; };
 
-  if (warp == 8) {
+  if (warp == kWarpLoad) {
     // ------------------------------------------------------------ K and V
     CrossPos p = share.pos;
+    Ring<C::NK> k;
+    Ring<C::NV> v;
     bool ok = true;
     int lk = 0, lv = 0;
     for (int u = 0; u < n && ok; ++u) {
       const int hk = (p.item / a.tiles) * a.GB / a.G, k0 = p.k * kTile;
-      if (u >= C::NK) ok = wait_bar_warp(bar(C::B_KE + u % C::NK), kph(u) ^ 1u, ab);
+      if (u >= C::NK) ok = wait_bar_warp(bar(C::B_KE + k.slot), k.parity ^ 1u, ab);
       if (!ok) break;
       if (lane == 0) {
-        const uint32_t fb = bar(C::B_KF + u % C::NK);
+        const uint32_t fb = bar(C::B_KF + k.slot), dst = sb0 + C::OFF_K + (uint32_t)(k.slot * C::TILE);
         mbar_arrive_expect_tx(fb, C::TILE);
 #pragma unroll
-        for (int y = 0; y < C::BOXES; ++y) tma_load_4d(sb0 + kst(u) + y * kBoxBytes, &mK, fb, 64 * y, hk, k0, p.b);
+        for (int y = 0; y < C::BOXES; ++y) tma_load_4d(dst + y * kBoxBytes, &mK, fb, 64 * y, hk, k0, p.b);
       }
       ++lk;
-      if (u >= C::NV) ok = wait_bar_warp(bar(C::B_VE + u % C::NV), vph(u) ^ 1u, ab);
+      k.next();
+      if (u >= C::NV) ok = wait_bar_warp(bar(C::B_VE + v.slot), v.parity ^ 1u, ab);
       if (!ok) break;
       if (lane == 0) {
-        const uint32_t fb = bar(C::B_VF + u % C::NV);
+        const uint32_t fb = bar(C::B_VF + v.slot), dst = sb0 + C::OFF_V + (uint32_t)(v.slot * C::TILE);
         mbar_arrive_expect_tx(fb, C::TILE);
 #pragma unroll
-        for (int y = 0; y < C::BOXES; ++y) tma_load_4d(sb0 + vst(u) + y * kBoxBytes, &mV, fb, 64 * y, hk, k0, p.b);
+        for (int y = 0; y < C::BOXES; ++y) tma_load_4d(dst + y * kBoxBytes, &mV, fb, 64 * y, hk, k0, p.b);
       }
       ++lv;
+      v.next();
       __syncwarp();
       p.next(a.sc);
     }
     if (!ok && lane == 0) {  // let the copies in flight land before the CTA exits
-      for (int y = max(0, lk - C::NK); y < lk; ++y) drain_bar(bar(C::B_KF + y % C::NK), kph(y));
-      for (int y = max(0, lv - C::NV); y < lv; ++y) drain_bar(bar(C::B_VF + y % C::NV), vph(y));
+      for (int y = max(0, lk - C::NK); y < lk; ++y) drain_bar(bar(C::B_KF + y % C::NK), (y / C::NK) & 1);
+      for (int y = max(0, lv - C::NV); y < lv; ++y) drain_bar(bar(C::B_VF + y % C::NV), (y / C::NV) & 1);
     }
-  } else if (warp == 10) {
-    // ------------------------------------------------------------ Q and dO of a run
+  } else if (warp == kWarpRun) {
+    // ------------------------------------------------------------ Q and dO of a run; rows of K that are masked
     CrossPos p = share.pos;
+    Ring<C::NK> r;
     bool ok = true;
     int q = 0;
     for (int u = 0; u < n && ok; ++q) {
@@ -471,81 +508,95 @@ __global__ void __launch_bounds__(CDq<DP>::NTHREADS, 1)
         }
       }
       __syncwarp();
-      for (int k = 0; k < run.n; ++k) p.next(a.sc);
-      u += run.n;
+      for (int k = 0; k < run.n && ok; ++k, ++u) {
+        if (a.clean) {
+          KeyWords<4> kw;
+          kw.load(a.mask, a.sc.len(p.b), p.b, a.sc.S, p.k * kTile);
+          ok = wait_bar_warp(bar(C::B_KF + r.slot), r.parity, ab);
+          if (!ok) break;
+          if (!kw.all) {
+            uint32_t w[4];
+            kw.words(w);
+            zero_dead_rows<C::BOXES>(sm + C::OFF_K + r.slot * C::TILE, w);
+          }
+          if (lane == 0) mbar_arrive(bar(C::B_KC + r.slot));
+          r.next();
+        }
+        p.next(a.sc);
+      }
     }
     if (!ok && q > 0 && lane == 0) drain_bar(bar(C::B_QF), (q - 1) & 1);
-  } else if (warp == 9) {
+  } else if (warp == kWarpMma) {
     // ------------------------------------------------------------ MMA issuer (whole warp, elect.sync)
     const uint32_t id_s = idesc_f16(128, 128, true, true, false, false);
     const uint32_t id_o = idesc_f16(128, 16, true, true, false, true) + ((uint32_t)(2 * (a.kd - 1)) << 17);
-    const uint32_t sq = sb0, sd = sb0 + C::TILE;
-    CrossPos p = share.pos;
-    int runs = 0, left = 0, left_next = 0;
+    const uint64_t dq = desc_k(sb0), dd = desc_k(sb0 + C::TILE), k_k = desc_k(sb0 + C::OFF_K), k_mn = desc_mn(sb0 + C::OFF_K),
+                   v_k = desc_k(sb0 + C::OFF_V);
+    constexpr uint64_t kTileStep = C::TILE >> 4;
+    const int full = a.clean ? C::B_KC : C::B_KF;
+    Ring<C::NK> k;  // of unit u + 1
+    Ring<C::NV> v;
+    int k_slot = 0;  // of unit u
+    int runs = 0;
     bool ok = true;
-    auto s_n = [&](int u) -> bool {  // S of unit u (its run's Q and dO have to be there)
-      if (left_next == 0) {
-        left_next = cross_run(p, n - u).n;
-        if (!wait_bar_warp(bar(C::B_QF), runs & 1, ab)) return false;
-        ++runs;
-      }
-      --left_next;
-      KeyWords kw;
-      kw.load(a.mask, a.sc.len(p.b), p.b, a.sc.S, p.k * kTile);
-      if (!wait_bar_warp(bar(C::B_KF + u % C::NK), kph(u), ab)) return false;
-      if (!kw.all) {
-        uint32_t w[4];
-        kw.words(w);
-        zero_dead_rows<C::BOXES>(sm + kst(u), w);
-      }
-      tc_fence_after();
-      mma_channels<C::BOXES>(tb + C::T_S + 128 * (u & 1), sq, sb0 + kst(u), id_s, a.kd);
-      mma_commit_e(bar(C::B_S + (u & 1)));
-      return true;
-    };
-    auto dp_n = [&](int u) -> bool {  // dP of unit u; the last of a run hands Q and dO back
-      if (!wait_bar_warp(bar(C::B_VF + u % C::NV), vph(u), ab)) return false;
-      tc_fence_after();
-      mma_channels<C::BOXES>(tb + C::T_DP, sd, sb0 + vst(u), id_s, a.kd);
-      mma_commit_e(bar(C::B_DP));
-      mma_commit_e(bar(C::B_VE + u % C::NV));
-      if (left_next == 0) mma_commit_e(bar(C::B_QE));
-      return true;
-    };
-    if (n > 0) {
-      ok = s_n(0) && dp_n(0);
+    CrossPos p = share.pos;
+    int left = 0;  // units left of unit u + 1's run after it
+    bool first = true, last = false, begin1 = false, end1 = false;
+    auto ahead = [&](int u1) {
+      begin1 = left == 0;
+      if (begin1) left = cross_run(p, n - u1).n;
+      end1 = --left == 0;
       p.next(a.sc);
-      left = left_next + 1;
-    }
-    bool first = true;
-    for (int u = 0; u < n && ok; ++u) {
-      const bool more = u + 1 < n;
-      --left;
-      if (more) ok = s_n(u + 1);  // (the columns of S, and of dS, of unit u - 1: dQ of it is issued)
-      if (!ok) break;
-      if (more) {
-        ok = wait_bar_warp(bar(C::B_DPE), u & 1, ab) && dp_n(u + 1);  // dP of unit u is in registers
+    };
+    if (n > 0) ahead(0);
+    // Round u: S and dP of unit u + 1 while the warps work on dS of unit u, then dQ of unit u. (S of u + 1
+    // takes the columns of S and dS of unit u - 1, whose dQ is issued.)
+#pragma unroll 1
+    for (int u = -1; u < n; ++u) {
+      if (u + 1 < n) {
+        const int odd = (u + 1) & 1;
+        if (begin1) {
+          ok = wait_bar_warp(bar(C::B_QF), runs & 1, ab);
+          if (!ok) break;
+          ++runs;
+        }
+        ok = wait_bar_warp(bar(full + k.slot), k.parity, ab);
         if (!ok) break;
+        tc_fence_after();
+        mma_channels<C::BOXES>(tb + C::T_S + 128 * odd, dq, k_k + k.slot * kTileStep, id_s, a.kd);
+        mma_commit_e(bar(C::B_S + odd));
+        if (u >= 0) ok = wait_bar_warp(bar(C::B_DPE), u & 1, ab);  // dP of unit u is in registers
+        ok = ok && wait_bar_warp(bar(C::B_VF + v.slot), v.parity, ab);
+        if (!ok) break;
+        tc_fence_after();
+        mma_channels<C::BOXES>(tb + C::T_DP, dd, v_k + v.slot * kTileStep, id_s, a.kd);
+        mma_commit_e(bar(C::B_DP));
+        mma_commit_e(bar(C::B_VE + v.slot));
+        if (end1) mma_commit_e(bar(C::B_QE));
+        v.next();
       }
-      ok = wait_bar_warp(bar(C::B_DS), u & 1, ab);
-      if (!ok) break;
-      tc_fence_after();
-      mma_ts_x8_e<0, 8, 16, 24, 64, 72, 80, 88>(tb + C::T_DQ, tb + C::T_S + 128 * (u & 1), desc_mn(sb0 + kst(u)), kMnStep, id_o, first ? 0u : 1u);
-      mma_commit_e(bar(C::B_KE + u % C::NK));
-      first = left == 0;
-      if (first) mma_commit_e(bar(C::B_ACC));
-      if (more) {
-        p.next(a.sc);
-        if (first) left = left_next + 1;
+      if (u >= 0) {
+        ok = wait_bar_warp(bar(C::B_DS), u & 1, ab);
+        if (!ok) break;
+        tc_fence_after();
+        mma_rows(tb + C::T_DQ, tb + C::T_S + 128 * (u & 1), k_mn + k_slot * kTileStep, id_o, first);
+        mma_commit_e(bar(C::B_KE + k_slot));
+        if (last) mma_commit_e(bar(C::B_ACC));
       }
+      k_slot = k.slot;
+      k.next();
+      first = begin1;
+      last = end1;
+      if (u + 2 < n) ahead(u + 2);
     }
     mma_commit_e(bar(C::B_DONE));
     if (lane == 0) drain_bar(bar(C::B_DONE), 0);
     __syncwarp();
-  } else {
-    // ------------------------------------------------------------ dS, thread = query row, 64 keys a warpgroup
-    const int half = warp >> 2, row = (warp & 3) * 32 + lane;
+  } else if (warp < kEw) {
+    // ------------------------------------------------------------ dS, thread = query row, 32 keys a warpgroup
+    const int part4 = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tdp = tb + lanes + C::T_DP + 32 * part4;
     CrossPos p = share.pos;
     bool ok = true;
     int runs = 0;
@@ -557,53 +608,48 @@ __global__ void __launch_bounds__(CDq<DP>::NTHREADS, 1)
       const float nl = __ldg(a.nl + r), nd = __ldg(a.nd + r);
       const float2 nl2 = make_float2(nl, nl), nd2 = make_float2(nd, nd);
       for (int k = 0; k < run.n; ++k, ++u) {
-        KeyWords kw;
-        kw.load(a.mask, len, b, a.sc.S, p.k * kTile);
-        const uint32_t ts = tb + lanes + C::T_S + 128 * (u & 1) + 64 * half, tdp = tb + lanes + C::T_DP + 64 * half;
-        ok = wait_bar_warp(bar(C::B_S + (u & 1)), (u >> 1) & 1, ab) && wait_bar_warp(bar(C::B_DP), u & 1, ab);
+        // this warpgroup's 32 keys, one bit each
+        const int key = p.k * kTile + 32 * part4 + lane;
+        const bool all = !a.mask && key - lane + 32 <= len;
+        const bool live = all || (key < len && (!a.mask || __ldg(a.mask + (int64_t)b * a.sc.S + key) != 0));
+        const uint32_t ts = tb + lanes + C::T_S + 128 * (u & 1) + 32 * part4;
+        ok = wait_bar_warp(bar(C::B_DP), u & 1, ab) && wait_bar_warp(bar(C::B_S + (u & 1)), (u >> 1) & 1, ab);
         if (!ok) break;
         tc_fence_after();
-        uint32_t dp[2][32];
-        tmem_ld32(tdp, dp[0]);
-        tmem_ld32(tdp + 32, dp[1]);
+        uint32_t dp[32], s[32], pk[16];
+        tmem_ld32(tdp, dp);
+        tmem_ld32(ts, s);
         tmem_wait_ld(dp);
+        tmem_wait_ld(s);
         tc_fence_before();
-        mbar_arrive(bar(C::B_DPE));
-        uint32_t w[4] = {~0u, ~0u, ~0u, ~0u};
-        if (!kw.all) kw.words(w);
+        warp_arrive(bar(C::B_DPE));
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          uint32_t s[32], pk[16];
-          tmem_ld32(ts + 32 * q, s);
-          tmem_wait_ld(s);
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float2 y = __ffma2_rn(make_float2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), c2, nl2);
-            const float2 x = __fmul2_rn(make_float2(ex2(y.x), ex2(y.y)),
-                                        __fadd2_rn(make_float2(__uint_as_float(dp[q][2 * j]), __uint_as_float(dp[q][2 * j + 1])), nd2));
-            pk[j] = pack_bf16x2(x.x, x.y);
-          }
-          if (!kw.all) {
-            const uint32_t m = half ? (q ? w[3] : w[2]) : (q ? w[1] : w[0]);
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-              pk[j] &= ((m >> (2 * j)) & 1u ? 0xffffu : 0u) | ((m >> (2 * j + 1)) & 1u ? 0xffff0000u : 0u);
-          }
-          tmem_st16(ts + 16 * q, pk);
+        for (int j = 0; j < 16; ++j) {
+          const float2 y = __ffma2_rn(make_float2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), c2, nl2);
+          const float2 x = __fmul2_rn(make_float2(ex2(y.x), ex2(y.y)),
+                                      __fadd2_rn(make_float2(__uint_as_float(dp[2 * j]), __uint_as_float(dp[2 * j + 1])), nd2));
+          pk[j] = pack_bf16x2(x.x, x.y);
         }
+        if (!all) {
+          const uint32_t w = __ballot_sync(0xffffffffu, live);
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            pk[j] &= ((w >> (2 * j)) & 1u ? 0xffffu : 0u) | ((w >> (2 * j + 1)) & 1u ? 0xffff0000u : 0u);
+        }
+        tmem_st16(ts, pk);
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(bar(C::B_DS));
+        warp_arrive(bar(C::B_DS));
         p.next(a.sc);
       }
       if (!ok) break;
-      // the run's dQ: the warpgroups take half of the channels each
+      // the run's dQ: the warpgroups take a quarter of the channels each
       ok = wait_bar_warp(bar(C::B_ACC), runs & 1, ab);
       if (!ok) break;
       tc_fence_after();
-      const int t = mt * (kTile >> a.lg) + (row >> a.lg), h = hb * a.GB + (row & (a.GB - 1)), mid = (a.kd + 1) / 2;
+      const int t = mt * (kTile >> a.lg) + (row >> a.lg), h = hb * a.GB + (row & (a.GB - 1)), quarter = (a.kd + 3) / 4;
       const int pitch = 16 * a.kd;
-      store_row(tb + lanes + C::T_DQ, half ? mid : 0, half ? a.kd : mid, a.d, a.scale, t < a.T,
+      store_row(tb + lanes + C::T_DQ, min(part4 * quarter, a.kd), min((part4 + 1) * quarter, a.kd), a.d, a.scale, t < a.T,
                 run.slot < 0 ? a.dQ + (((int64_t)b * a.T + t) * a.H + h) * a.d : nullptr,
                 a.part + ((int64_t)max(run.slot, 0) * kTile + row) * pitch);
       tc_fence_before();
@@ -611,16 +657,15 @@ __global__ void __launch_bounds__(CDq<DP>::NTHREADS, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == kWarpMma) {
     tc_fence_after();
     tmem_dealloc(tb, 512);
   }
 }
 
 // ================================================================ partial results
-// cross_join_setup says which item a block has. W warps take the partial results of four rows of its
-// outputs (dQ: 128 rows; dV, dK: 256) in turn, as in the forward's join, and the first of them adds
-// the W sums in order.
+// cross_join_setup says which item a block has. A warp takes four rows of its outputs (dQ: 128 rows;
+// dV, dK: 256) and the partial results in order, or every eighth of many, as in the forward's join.
 __global__ void __launch_bounds__(256) cross_join_kernel(const CBwdArgs a, int ctas) {
   __shared__ CrossJoin j;
   __shared__ float4 acc_s[8][4][32];
@@ -628,16 +673,18 @@ __global__ void __launch_bounds__(256) cross_join_kernel(const CBwdArgs a, int c
   const bool work = cross_join_setup(a.sc, ctas, j);
   wait_previous_kernel();  // (every block: the next kernel of the stream relies on this one's end alone)
   if (!work) return;
-  const int W = j.count > 4 ? 8 : j.count > 2 ? 4 : 2, w = warp & (W - 1), per = 8 / W;
+  const bool many = j.count > 4;
   const int pitch = 16 * a.kd, rows = (a.sc.by_keys ? 2 : 1) * kTile;
   const int64_t slot = (int64_t)rows * pitch;
-  for (int r0 = (blockIdx.y * per + warp / W) * 4; r0 - warp / W * 4 < rows; r0 += gridDim.y * per * 4) {
-    // (every warp of the block makes the same number of rounds; r0 may pass the rows for some)
+  const int step = many ? 4 : 32;  // rows a block takes at a time
+  for (int b0 = blockIdx.y * step; b0 < rows; b0 += gridDim.y * step) {
+    const int r0 = b0 + (many ? 0 : 4 * warp);
     float4 acc[4];
 #pragma unroll
     for (int x = 0; x < 4; ++x) acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (r0 < rows && 4 * lane < pitch)
-      for (int c = w; c < j.count; c += W) {
+    if (4 * lane < pitch)
+#pragma unroll 2
+      for (int c = many ? warp : 0; c < j.count; c += many ? 8 : 1) {
         const float *base = a.part + j.slot[c] * slot + (int64_t)r0 * pitch + 4 * lane;
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
@@ -645,30 +692,35 @@ __global__ void __launch_bounds__(256) cross_join_kernel(const CBwdArgs a, int c
           acc[x].x += v.x, acc[x].y += v.y, acc[x].z += v.z, acc[x].w += v.w;
         }
       }
+    if (many) {
 #pragma unroll
-    for (int x = 0; x < 4; ++x) acc_s[warp][x][lane] = acc[x];
-    __syncthreads();
-    if (w == 0 && r0 < rows && 4 * lane < a.d)
+      for (int x = 0; x < 4; ++x) acc_s[warp][x][lane] = acc[x];
+      __syncthreads();
+      if (warp == 0)
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        for (int y = 1; y < W; ++y) {
-          const float4 v = acc_s[warp + y][x][lane];
-          acc[x].x += v.x, acc[x].y += v.y, acc[x].z += v.z, acc[x].w += v.w;
-        }
-        const int row = (r0 + x) % kTile;
-        uint16_t *out;
-        if (a.sc.by_keys) {
-          const int hk = j.pos.item / j.pos.nt, key = (j.pos.item % j.pos.nt) * kTile + row;
-          if (key >= a.sc.S) continue;
-          out = ((r0 + x) / kTile ? a.dK : a.dV) + (((int64_t)j.pos.b * a.sc.S + key) * a.Hk + hk) * a.d;
-        } else {
-          const int hb = j.pos.item / a.tiles, t = (j.pos.item % a.tiles) * (kTile >> a.lg) + (row >> a.lg);
-          if (t >= a.T) continue;
-          out = a.dQ + (((int64_t)j.pos.b * a.T + t) * a.H + hb * a.GB + (row & (a.GB - 1))) * a.d;
-        }
-        *reinterpret_cast<uint2 *>(out + 4 * lane) = make_uint2(pack_bf16x2(acc[x].x, acc[x].y), pack_bf16x2(acc[x].z, acc[x].w));
+        for (int x = 0; x < 4; ++x)
+          for (int y = 1; y < 8; ++y) {
+            const float4 v = acc_s[y][x][lane];
+            acc[x].x += v.x, acc[x].y += v.y, acc[x].z += v.z, acc[x].w += v.w;
+          }
+      __syncthreads();
+    }
+    if (4 * lane >= a.d || (many && warp > 0)) continue;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int row = (r0 + x) % kTile;
+      uint16_t *out;
+      if (a.sc.by_keys) {
+        const int hk = j.pos.item / j.pos.nt, key = (j.pos.item % j.pos.nt) * kTile + row;
+        if (key >= a.sc.S) continue;
+        out = (r0 / kTile ? a.dK : a.dV) + (((int64_t)j.pos.b * a.sc.S + key) * a.Hk + hk) * a.d;
+      } else {
+        const int hb = j.pos.item / a.tiles, t = (j.pos.item % a.tiles) * (kTile >> a.lg) + (row >> a.lg);
+        if (t >= a.T) continue;
+        out = a.dQ + (((int64_t)j.pos.b * a.T + t) * a.H + hb * a.GB + (row & (a.GB - 1))) * a.d;
       }
-    __syncthreads();
+      *reinterpret_cast<uint2 *>(out + 4 * lane) = make_uint2(pack_bf16x2(acc[x].x, acc[x].y), pack_bf16x2(acc[x].z, acc[x].w));
+    }
   }
 }
 
@@ -711,13 +763,13 @@ cudaError_t launch_bwd(const CUtensorMap &mq, const CUtensorMap &mdo, const CUte
     if (e != cudaSuccess) return e;
     ready.mark(dev);
   }
-  cross_dkv_kernel<DP><<<g.dkv_ctas, CDkv<DP>::NTHREADS, CDkv<DP>::SMEM, st>>>(mq, mdo, mk, mv, dkv);
+  cross_dkv_kernel<DP><<<g.dkv_ctas, kBwdThreads, CDkv<DP>::SMEM, st>>>(mq, mdo, mk, mv, dkv);
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess && g.dkv_split && g.dkv_ctas > 1) {
     e = launch_after(cross_join_kernel, dim3(g.dkv_ctas - 1, 8), 256, st, dkv, g.dkv_ctas);
   }
   if (e == cudaSuccess) {
-    cross_dq_kernel<DP><<<g.dq_ctas, CDq<DP>::NTHREADS, CDq<DP>::SMEM, st>>>(mq, mdo, mk, mv, dq);
+    cross_dq_kernel<DP><<<g.dq_ctas, kBwdThreads, CDq<DP>::SMEM, st>>>(mq, mdo, mk, mv, dq);
     e = cudaGetLastError();
   }
   if (e == cudaSuccess && g.dq_split && g.dq_ctas > 1) {
@@ -778,6 +830,7 @@ int tri_cross_bwd(tri_cross_shape shape, const tri_attn_bf16 *Q, const tri_attn_
   a.c = shape.scale * kLog2e;
   a.scale = shape.scale;
   a.mask = mask;
+  a.clean = mask || kv_lens;
   float *nl = reinterpret_cast<float *>(ws + g.nl), *nd = reinterpret_cast<float *>(ws + g.nd);
   a.nl = nl;
   a.nd = nd;

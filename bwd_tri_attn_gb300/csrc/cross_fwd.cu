@@ -2,14 +2,15 @@
 // division of the work).
 //
 // One CTA per SM works through its units; a unit is one 128-key tile against up to two tiles of 128
-// rows. Two streams run side by side, each with a softmax warpgroup (warps 0-3 and 4-7, thread =
-// row) and an MMA warp (9 and 11): the two row tiles, or, where an item has one row tile (single tokens),
-// its even and odd key tiles, merged at the end of a run. Warp 8 loads K and V through a TMA ring; warp 10 loads Q and zeroes
+// rows. Two streams run side by side, each with a softmax warpgroup (warps 0-3 and 4-7, thread = row): the
+// two row tiles of an item, or, where it has one (single tokens, a last odd tile), its even and odd key tiles,
+// merged at the end of a run. Warp 8 loads K and V through a TMA ring; warp 10 loads Q and zeroes
 // masked rows of V. TMEM: S0, S1 (128 columns each; P, as BF16 pairs, over the first half of S once
-// S is in registers), O0, O1. A stream's MMA warp issues P V of unit u (in two halves, as P comes) and Q K of
-// unit u + 1 behind it, so the products of one stream run while the other's softmax does. The running
-// maximum is only moved (and O rescaled) when it grows by more than 2^8: the reference value cancels
-// in O / l, and P up to 2^8 costs no precision.
+// S is in registers), O0, O1. Warp 9 issues all products, stream by stream: P V of a stream's step (in two
+// halves, as P comes) and Q K of its next step behind it, so that they run during the softmax of the other
+// stream. (Two issuing warps mixed the streams' products: both softmaxes then ran at the same time, and the
+// tensor cores waited for them.) The running maximum is only moved (and O rescaled) when it grows by more
+// than 2^8: the reference value cancels in O / l, and P up to 2^8 costs no precision.
 #include <math.h>
 
 #include "cross.cuh"
@@ -26,7 +27,7 @@ struct CFwd {
   static constexpr int OFF_RING = 2 * TILE, OFF_BAR = OFF_RING + NST * TILE;
   static constexpr int B_FULL = 0, B_EMPTY = NST, B_CLEAN = 2 * NST, B_QF = 3 * NST, B_QE = B_QF + 1, B_S = B_QE + 1,
                        B_P = B_S + 2, B_O = B_P + 4, B_MERGE = B_O + 2, B_MERGED = B_MERGE + 1,
-                       B_DONE = B_MERGED + 1, NBAR = B_DONE + 2;
+                       B_DONE = B_MERGED + 1, NBAR = B_DONE + 1;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int OFF_SHARE = OFF_MISC + 16;
   static constexpr int OFF_ML = (OFF_SHARE + (int)sizeof(CrossShare) + 15) / 16 * 16;  // stream 1's maxima and sums
@@ -91,24 +92,25 @@ __global__ void __launch_bounds__(CFwd<DP>::NTHREADS, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sb0 = smem_u32(sm);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (the hardware's first four warps, which the schedulers prefer, are those that feed the others)
+  const int warp = ((threadIdx.x >> 5) + 8) % 12, lane = threadIdx.x & 31;
   auto bar = [&](int k) { return sb0 + C::OFF_BAR + 8u * (uint32_t)k; };
   volatile uint32_t *misc = reinterpret_cast<volatile uint32_t *>(sm + C::OFF_MISC);
   const Abort ab{reinterpret_cast<volatile int *>(misc + 1), a.sc.status};
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::NST; ++s) {
       mbar_init(bar(C::B_FULL + s), 1);
-      mbar_init(bar(C::B_EMPTY + s), 2);
+      mbar_init(bar(C::B_EMPTY + s), 1);
       mbar_init(bar(C::B_CLEAN + s), 1);
     }
     mbar_init(bar(C::B_QF), 1);
-    mbar_init(bar(C::B_QE), 2);
+    mbar_init(bar(C::B_QE), 1);
+    mbar_init(bar(C::B_DONE), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(C::B_S + i), 1);
-      mbar_init(bar(C::B_P + i), 128);
-      mbar_init(bar(C::B_P + 2 + i), 128);
+      mbar_init(bar(C::B_P + i), 4);
+      mbar_init(bar(C::B_P + 2 + i), 4);
       mbar_init(bar(C::B_O + i), 1);
-      mbar_init(bar(C::B_DONE + i), 1);
     }
     mbar_init(bar(C::B_MERGE), 128);
     mbar_init(bar(C::B_MERGED), 128);
@@ -129,7 +131,6 @@ __global__ void __launch_bounds__(CFwd<DP>::NTHREADS, 1)
   const uint32_t tb = misc[0];
   const CrossShare share = *reinterpret_cast<const CrossShare *>(sm + C::OFF_SHARE);
   const int n = share.n;
-  const bool alt = a.two == 1;  // the streams are the even and odd units of a run
   // ring positions of unit u: K at 2 u, V at 2 u + 1
   auto stage = [&](int x) { return sb0 + C::OFF_RING + (uint32_t)(x % C::NST) * C::TILE; };
   auto phase = [&](int x) { return (uint32_t)(x / C::NST) & 1u; };
@@ -180,7 +181,7 @@ __global__ void __launch_bounds__(CFwd<DP>::NTHREADS, 1)
       __syncwarp();
       for (int k = 0; k < run.n && ok; ++k, ++u) {
         for (int x = 2 * u; a.clean && x < 2 * u + 2 && ok; ++x) {
-          KeyWords kw;
+          KeyWords<4> kw;
           kw.load(a.mask, a.sc.len(p.b), p.b, a.sc.S, p.k * kTile);
           ok = wait_bar_warp(bar(C::B_FULL + x % C::NST), phase(x), ab);
           if (!ok) break;
@@ -195,72 +196,119 @@ __global__ void __launch_bounds__(CFwd<DP>::NTHREADS, 1)
       }
     }
     if (!ok && q > 0 && lane == 0) drain_bar(bar(C::B_QF), (q - 1) & 1);
-  } else if (warp == 9 || warp == 11) {
+  } else if (warp == 9) {
     reg_dealloc<C::REG_OTHER>();
-    // ------------------------------------------------------------ MMA issuer of stream i (whole warp, elect.sync)
-    const int i = warp == 11;
+    // ------------------------------------------------------------ MMA issuer (whole warp, elect.sync)
     const uint32_t id_s = idesc_f16(128, 128, true, true, false, false) | (a.negate ? 1u << 13 : 0u);  // (bit 13: -A)
     const uint32_t id_o = idesc_f16(128, 16, true, true, false, true) + ((uint32_t)(2 * (a.kd - 1)) << 17);
-    const uint32_t ds = tb + C::T_S + 128 * i, dO = tb + C::T_O + 128 * i, sq = sb0 + (alt ? 0 : i * C::TILE);
-    const int full = a.clean ? C::B_CLEAN : C::B_FULL;
-    CrossPos p = share.pos;   // of unit u + 1
-    int runs = 0, units = 0;  // runs begun, units of this stream whose P V is issued
-    int left = 0, k = 0;      // of unit u + 1: units left of its run (itself included), its place in the run
-    bool ok = true, live = false, first = false;  // of unit u: this stream's, the stream's first of a run
-    // Round u: P V of unit u, then Q K of unit u + 1. A unit that is not this stream's is handed back
-    // at once, but not before it is there: its slot's barrier counts both streams.
-#pragma unroll 1
-    for (int u = -1; u < n; ++u) {
-      if (u >= 0) {
-        const int x = 2 * u + 1;
-        ok = wait_bar_warp(bar(full + x % C::NST), phase(x), ab);
-        if (!ok) break;
-        if (live) {
-          // P comes in two halves of 64 keys
-          const uint64_t dv = desc_mn(stage(x));
-          ok = wait_bar_warp(bar(C::B_P + i), units & 1, ab);
-          if (!ok) break;
-          tc_fence_after();
-          mma_ts_x4_e(dO, ds, dv, kMnStep, id_o, first ? 0u : 1u);
-          ok = wait_bar_warp(bar(C::B_P + 2 + i), units & 1, ab);
-          if (!ok) break;
-          tc_fence_after();
-          mma_ts_x4_e(dO, ds + 32, dv + 4 * kMnStep, kMnStep, id_o, 1u);
-          mma_commit_e(bar(C::B_O + i));
-          mma_commit_e(bar(C::B_EMPTY + x % C::NST));
-          ++units;
-        } else if (lane == 0) {
-          mbar_arrive(bar(C::B_EMPTY + x % C::NST));
-        }
-      }
-      if (u + 1 == n) break;
-      const int x = 2 * (u + 1);
-      if (left == 0) {
-        left = cross_run(p, n - u - 1).n;
-        k = 0;
-        ok = wait_bar_warp(bar(C::B_QF), runs & 1, ab);
-        if (!ok) break;
+    const uint64_t dq0 = desc_k(sb0), dk0 = desc_k(sb0 + C::OFF_RING), dv0 = desc_mn(sb0 + C::OFF_RING);
+    constexpr uint64_t kTileStep = C::TILE >> 4;
+    const uint32_t full = bar(a.clean ? C::B_CLEAN : C::B_FULL), empty = bar(C::B_EMPTY);
+    Ring<C::NST> rk, rv;  // the next K and the next V
+    rv.next();            // (K of unit 0, V of unit 0, K of unit 1, ...)
+    CrossPos p = share.pos;
+    uint32_t par0 = 0, par1 = 0;  // phases of the streams' P barriers
+    int runs = 0;                 // runs whose Q K has begun
+    bool ok = true, begun = false;  // the coming run's first Q K is issued
+    auto wait_k = [&](bool begins) {  // (and for Q of a run that begins)
+      if (begins) {
+        ok = ok && wait_bar_warp(bar(C::B_QF), runs & 1, ab);
         ++runs;
       }
-      ok = wait_bar_warp(bar(full + x % C::NST), phase(x), ab);
-      if (!ok) break;
-      live = alt ? (k & 1) == i : row_tile(a, p.item, i).live;
-      first = k == (alt ? i : 0);
-      if (live) {
-        tc_fence_after();
-        mma_channels<C::BOXES>(ds, sq, stage(x), id_s, a.kd);
-        mma_commit_e(bar(C::B_S + i));
-        mma_commit_e(bar(C::B_EMPTY + x % C::NST));
-      } else if (lane == 0) {
-        mbar_arrive(bar(C::B_EMPTY + x % C::NST));
+      ok = ok && wait_bar_warp(full + 8 * rk.slot, rk.parity, ab);
+      tc_fence_after();
+    };
+    auto qk = [&](int i, int tile) {
+      mma_channels<C::BOXES>(tb + C::T_S + 128 * i, dq0 + tile * kTileStep, dk0 + rk.slot * kTileStep, id_s, a.kd);
+      mma_commit_e(bar(C::B_S + i));
+    };
+    auto k_done = [&](bool ends) {  // K (and Q of a run that ends) may be overwritten
+      mma_commit_e(empty + 8 * rk.slot);
+      if (ends) mma_commit_e(bar(C::B_QE));
+      rk.next();
+      rk.next();
+    };
+    auto pv = [&](int i, uint32_t &parity, bool begins, bool ends) {
+      const uint32_t ds = tb + C::T_S + 128 * i, dO = tb + C::T_O + 128 * i;
+      const uint64_t dv = dv0 + rv.slot * kTileStep;
+      ok = ok && wait_bar_warp(bar(C::B_P + i), parity, ab);  // (P comes in two halves of 64 keys)
+      tc_fence_after();
+      if (ok) mma_ts_x4_e(dO, ds, dv, kMnStep, id_o, begins ? 0u : 1u);
+      ok = ok && wait_bar_warp(bar(C::B_P + 2 + i), parity, ab);
+      tc_fence_after();
+      if (ok) mma_ts_x4_e(dO, ds + 32, dv + 4 * kMnStep, kMnStep, id_o, 1u);
+      parity ^= 1u;
+      if (ends) mma_commit_e(bar(C::B_O + i));
+    };
+    auto v_done = [&] {
+      mma_commit_e(empty + 8 * rv.slot);
+      rv.next();
+      rv.next();
+    };
+    for (int u = 0; u < n && ok;) {
+      const CrossRun run = cross_run(p, n - u);
+      const bool pair = row_tile(a, p.item, 1).live;
+      p.skip(a.sc, run.n);
+      u += run.n;
+      // the run after this one: if it has two row tiles too, its first Q K follow this run's last P V
+      const int next_n = u < n ? cross_run(p, n - u).n : 0;
+      const bool next_pair = pair && u < n && row_tile(a, p.item, 1).live;
+      if (!begun) {  // the first Q K of both streams
+        wait_k(true);
+        if (!ok) break;
+        qk(0, 0);
+        if (pair) {
+          qk(1, 1);
+          k_done(run.n == 1);
+        } else {
+          k_done(run.n == 1);
+          if (run.n > 1) {
+            wait_k(false);
+            if (!ok) break;
+            qk(1, 0);
+            k_done(run.n == 2);
+          }
+        }
       }
-      if (--left == 0) mma_commit_e(bar(C::B_QE));
-      ++k;
-      p.next(a.sc);
+      begun = next_pair;
+      if (pair) {
+#pragma unroll 1
+        for (int k = 0; k < run.n; ++k) {
+          const bool last = k + 1 == run.n, more = !last || next_pair;
+          ok = ok && wait_bar_warp(full + 8 * rv.slot, rv.parity, ab);
+          pv(0, par0, k == 0, last);
+          if (more) {
+            wait_k(last);
+            if (ok) qk(0, 0);
+          }
+          pv(1, par1, k == 0, last);
+          if (more && ok) qk(1, 1);
+          if (!ok) break;
+          v_done();
+          if (more) k_done(last ? next_n == 1 : k + 2 == run.n);
+        }
+      } else {
+#pragma unroll 1
+        for (int k = 0; k < run.n; ++k) {
+          const int i = k & 1;
+          ok = ok && wait_bar_warp(full + 8 * rv.slot, rv.parity, ab);
+          pv(i, i ? par1 : par0, k < 2, k + 2 >= run.n);
+          if (!ok) break;
+          v_done();
+          if (k + 2 < run.n) {
+            wait_k(false);
+            if (!ok) break;
+            qk(i, 0);
+            k_done(k + 3 == run.n);
+          }
+        }
+      }
     }
-    mma_commit_e(bar(C::B_DONE + i));
-    if (lane == 0) drain_bar(bar(C::B_DONE + i), 0);
+    mma_commit_e(bar(C::B_DONE));
+    if (lane == 0) drain_bar(bar(C::B_DONE), 0);
     __syncwarp();
+  } else if (warp == 11) {
+    reg_dealloc<C::REG_OTHER>();  // (only gives its registers)
   } else {
     reg_alloc<C::REG_SOFT>();
     // ------------------------------------------------------------ softmax of stream i, thread = row
@@ -271,13 +319,15 @@ __global__ void __launch_bounds__(CFwd<DP>::NTHREADS, 1)
     CrossPos p = share.pos;
     bool ok = true;
     int x = 0;       // units of this stream
+    int outs = 0;    // runs in which it has units
     int merges = 0;  // runs of two streams
     for (int u = 0; u < n && ok;) {
       const CrossRun run = cross_run(p, n - u);
+      const bool alt = !row_tile(a, p.item, 1).live;
       const RowTile rt = row_tile(a, p.item, alt ? 0 : i);
       const int b = p.b;
-      if (!rt.live || (alt && run.n <= i)) {
-        for (int k = 0; k < run.n; ++k) p.next(a.sc);
+      if (alt && run.n <= i) {
+        p.skip(a.sc, run.n);
         u += run.n;
         continue;
       }
@@ -288,7 +338,7 @@ __global__ void __launch_bounds__(CFwd<DP>::NTHREADS, 1)
         const int key0 = p.k * kTile;
         p.next(a.sc);
         if (alt && (k & 1) != i) continue;
-        KeyWords kw;
+        KeyWords<4> kw;
         kw.load(a.mask, len, b, a.sc.S, key0);
         ok = wait_bar_warp(bar(C::B_S + i), x & 1, ab);
         if (!ok) break;
@@ -319,6 +369,7 @@ __global__ void __launch_bounds__(CFwd<DP>::NTHREADS, 1)
           l *= f;
           if (!first) {
             // O holds earlier tiles (the products that S came with were issued after theirs, so they are done)
+#pragma unroll 1
             for (int q = 0; q < a.kd; ++q) {
               uint32_t o[16];
               tmem_ld16(to + 16 * q, o);
@@ -347,7 +398,7 @@ __global__ void __launch_bounds__(CFwd<DP>::NTHREADS, 1)
           if (q & 1) {  // half of P is there
             tmem_wait_st();
             tc_fence_before();
-            mbar_arrive(bar(C::B_P + (q == 1 ? 0 : 2) + i));
+            warp_arrive(bar(C::B_P + (q == 1 ? 0 : 2) + i));
           }
         }
         const float2 t2 = __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3]));
@@ -355,8 +406,9 @@ __global__ void __launch_bounds__(CFwd<DP>::NTHREADS, 1)
       }
       if (!ok) break;
       // the run's rows: O / l, and the log-sum-exp
-      ok = wait_bar_warp(bar(C::B_O + i), (x - 1) & 1, ab);
+      ok = wait_bar_warp(bar(C::B_O + i), outs & 1, ab);
       if (!ok) break;
+      ++outs;
       tc_fence_after();
       float w0 = 1.f, w1 = 0.f;  // weights of the streams' O
       const bool merge = alt && run.n > 1;
@@ -394,6 +446,7 @@ __global__ void __launch_bounds__(CFwd<DP>::NTHREADS, 1)
       uint16_t *out = a.O + (((int64_t)b * a.T + t) * a.H + h) * a.d;
       w0 *= inv;
       w1 *= inv;
+#pragma unroll 1
       for (int q = 0; q < a.kd; ++q) {
         uint32_t o[16];
         tmem_ld16(to + 16 * q, o);
@@ -439,10 +492,20 @@ __global__ void __launch_bounds__(CFwd<DP>::NTHREADS, 1)
   }
 }
 
+// Two results of softmax over parts of a row's keys, (m, l, acc) and (m2, l2, v): acc a sum weighted by
+// l exp(m).
+__device__ __forceinline__ void join_add(float &m, float &l, float4 &acc, float m2, float l2, const float4 &v) {
+  const float m1 = fmaxf(m, m2);
+  const float f = m1 == -INFINITY ? 0.f : ex2(m - m1), g = m1 == -INFINITY ? 0.f : ex2(m2 - m1);
+  acc = make_float4(acc.x * f + v.x * g, acc.y * f + v.y * g, acc.z * f + v.z * g, acc.w * f + v.w * g);
+  l = l * f + l2 * g;
+  m = m1;
+}
+
 // Adds the partial results of the items that several CTAs share (cross_join_setup says which item a
-// block has). W warps take the partial results of four rows in turn (W: the power of two that covers
-// them, at most 8: two partial results are the rule, many the case of few rows over long keys), then
-// the first of them adds the W results in order.
+// block has). A warp takes four rows; of few partial results (two is the rule) it adds all, in
+// order; of many (few rows over long keys) the eight warps of a block take every eighth, and the first
+// adds the eight sums in order.
 __global__ void __launch_bounds__(256) cross_fwd_join_kernel(const CFwdArgs a, int ctas) {
   __shared__ CrossJoin j;
   __shared__ float4 acc_s[8][4][32];
@@ -451,15 +514,14 @@ __global__ void __launch_bounds__(256) cross_fwd_join_kernel(const CFwdArgs a, i
   const bool work = cross_join_setup(a.sc, ctas, j);
   wait_previous_kernel();  // (every block: the next kernel of the stream relies on this one's end alone)
   if (!work) return;
-  const int W = j.count > 4 ? 8 : j.count > 2 ? 4 : 2, w = warp & (W - 1), per = 8 / W;
-  const int pitch = 16 * a.kd, tile = kTile * (pitch + 4);
+  const bool many = j.count > 4;
+  const int pitch = 16 * a.kd, tile = kTile * (pitch + 4), rows = a.two * kTile;
   const int64_t slot = (int64_t)a.two * tile;
-  const int rows = a.two * kTile;
-  for (int r0 = (blockIdx.y * per + warp / W) * 4; r0 - warp / W * 4 < rows; r0 += gridDim.y * per * 4) {
-    // (every warp of the block makes the same number of rounds; r0 may pass the rows for some)
-    const int i = r0 / kTile, row = r0 % kTile;  // four rows of one tile
+  const int step = many ? 4 : 32;  // rows a block takes at a time
+  for (int b0 = blockIdx.y * step; b0 < rows; b0 += gridDim.y * step) {
+    const int r0 = b0 + (many ? 0 : 4 * warp), i = r0 / kTile, row = r0 % kTile;  // four rows of one tile
     const RowTile rt = row_tile(a, j.pos.item, i);
-    const bool live = r0 < rows && rt.live && rt.t0 + (row >> a.lg) < a.T;
+    const bool live = rt.live && rt.t0 + (row >> a.lg) < a.T;
     float4 acc[4];
     float m[4], l[4];
 #pragma unroll
@@ -468,54 +530,46 @@ __global__ void __launch_bounds__(256) cross_fwd_join_kernel(const CFwdArgs a, i
       m[x] = -INFINITY;
       l[x] = 0.f;
     }
-    for (int c = w; c < j.count && live; c += W) {
-      const float *base = a.part + j.slot[c] * slot + (int64_t)i * tile;
-      const float4 lse = *reinterpret_cast<const float4 *>(base + kTile * pitch + row);
-      const float ls[4] = {lse.x, lse.y, lse.z, lse.w};
-      float4 v[4];
+    if (live)
+#pragma unroll 2
+      for (int c = many ? warp : 0; c < j.count; c += many ? 8 : 1) {
+        const float *base = a.part + j.slot[c] * slot + (int64_t)i * tile;
+        const float4 lse = *reinterpret_cast<const float4 *>(base + kTile * pitch + row);
+        const float ls[4] = {lse.x, lse.y, lse.z, lse.w};
+        float4 v[4];
 #pragma unroll
-      for (int x = 0; x < 4; ++x)
-        v[x] = 4 * lane < pitch ? *reinterpret_cast<const float4 *>(base + (row + x) * pitch + 4 * lane)
-                                : make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int x = 0; x < 4; ++x)
+          v[x] = 4 * lane < pitch ? *reinterpret_cast<const float4 *>(base + (row + x) * pitch + 4 * lane)
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+        // (rows past T hold nothing: whatever comes out for them is not written)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) join_add(m[x], l[x], acc[x], ls[x], 1.f, v[x]);
+      }
+    if (many) {
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
-        const float m1 = fmaxf(m[x], ls[x]);
-        const float f = m1 == -INFINITY ? 0.f : ex2(m[x] - m1), g = m1 == -INFINITY ? 0.f : ex2(ls[x] - m1);
-        // (rows past T hold nothing: their weight is whatever it is, and they are not written)
-        acc[x] = make_float4(acc[x].x * f + v[x].x * g, acc[x].y * f + v[x].y * g, acc[x].z * f + v[x].z * g, acc[x].w * f + v[x].w * g);
-        l[x] = l[x] * f + g;
-        m[x] = m1;
+        acc_s[warp][x][lane] = acc[x];
+        if (lane == 0) ml_s[warp][x] = make_float2(m[x], l[x]);
       }
+      __syncthreads();
+      if (warp == 0)
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          for (int y = 1; y < 8; ++y) join_add(m[x], l[x], acc[x], ml_s[y][x].x, ml_s[y][x].y, acc_s[y][x][lane]);
+      __syncthreads();
     }
+    if (!live || (many && warp > 0)) continue;
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
-      acc_s[warp][x][lane] = acc[x];
-      if (lane == 0) ml_s[warp][x] = make_float2(m[x], l[x]);
+      const int t = rt.t0 + ((row + x) >> a.lg), h = rt.head0 + ((row + x) & (a.GB - 1));
+      if (t >= a.T) continue;
+      const float inv = l[x] > 0.f ? 1.f / l[x] : 0.f;
+      if (4 * lane < a.d)
+        *reinterpret_cast<uint2 *>(a.O + (((int64_t)j.pos.b * a.T + t) * a.H + h) * a.d + 4 * lane) =
+            make_uint2(pack_bf16x2(acc[x].x * inv, acc[x].y * inv), pack_bf16x2(acc[x].z * inv, acc[x].w * inv));
+      if (lane == 0)
+        a.LSE[((int64_t)j.pos.b * a.H + h) * a.T + t] = l[x] > 0.f ? (m[x] + __log2f(l[x])) * kLn2 : -INFINITY;
     }
-    __syncthreads();
-    if (w == 0 && live) {
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        for (int y = 1; y < W; ++y) {
-          const float2 ml = ml_s[warp + y][x];
-          const float4 v = acc_s[warp + y][x][lane];
-          const float m1 = fmaxf(m[x], ml.x);
-          const float f = m1 == -INFINITY ? 0.f : ex2(m[x] - m1), g = m1 == -INFINITY ? 0.f : ex2(ml.x - m1);
-          acc[x] = make_float4(acc[x].x * f + v.x * g, acc[x].y * f + v.y * g, acc[x].z * f + v.z * g, acc[x].w * f + v.w * g);
-          l[x] = l[x] * f + ml.y * g;
-          m[x] = m1;
-        }
-        const int t = rt.t0 + ((row + x) >> a.lg), h = rt.head0 + ((row + x) & (a.GB - 1));
-        if (t >= a.T) continue;
-        const float inv = l[x] > 0.f ? 1.f / l[x] : 0.f;
-        if (4 * lane < a.d)
-          *reinterpret_cast<uint2 *>(a.O + (((int64_t)j.pos.b * a.T + t) * a.H + h) * a.d + 4 * lane) =
-              make_uint2(pack_bf16x2(acc[x].x * inv, acc[x].y * inv), pack_bf16x2(acc[x].z * inv, acc[x].w * inv));
-        if (lane == 0)
-          a.LSE[((int64_t)j.pos.b * a.H + h) * a.T + t] = l[x] > 0.f ? (m[x] + __log2f(l[x])) * kLn2 : -INFINITY;
-      }
-    }
-    __syncthreads();
   }
 }
 
