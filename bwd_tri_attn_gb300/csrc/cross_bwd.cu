@@ -40,6 +40,7 @@ __global__ void __launch_bounds__(256) cross_bwd_prep_kernel(const CBwdArgs a, c
                                                              const float *__restrict__ LSE,
                                                              const uint16_t *__restrict__ dO, float *nl, float *nd,
                                                              int row_blocks) {
+  allow_next_kernel();
   const int t16 = threadIdx.x & 15, g = threadIdx.x >> 4;
   if ((int)blockIdx.x < row_blocks) {
     const int64_t per = (int64_t)a.tiles * kTile, n = per * (a.H >> a.lg) * a.sc.B;
@@ -166,6 +167,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const CrossShare sh = cross_share(a.sc);
     if (lane == 0) *reinterpret_cast<CrossShare *>(sm + C::OFF_SHARE) = sh;
   }
+  // -LSE and -D. Only then the next kernels may start: on a free SM one of them could be ahead of the preparation.
+  wait_previous_kernel();
+  allow_next_kernel();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -441,6 +445,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     tmem_alloc(sb0 + C::OFF_MISC, 512);
     tmem_relinquish();
   }
+  allow_next_kernel();
   if (warp == kWarpLoad) {
     const CrossShare sh = cross_share(a.sc);
     if (lane == 0) *reinterpret_cast<CrossShare *>(sm + C::OFF_SHARE) = sh;
@@ -647,6 +652,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       ok = wait_bar_warp(bar(C::B_ACC), runs & 1, ab);
       if (!ok) break;
       tc_fence_after();
+      // The kernel before, the join of dK and dV, reads the partial results' space: nothing is written
+      // before it has ended. (What this kernel reads was complete before that one's predecessor read it.)
+      if (runs == 0) wait_previous_kernel();
       const int t = mt * (kTile >> a.lg) + (row >> a.lg), h = hb * a.GB + (row & (a.GB - 1)), quarter = (a.kd + 3) / 4;
       const int pitch = 16 * a.kd;
       store_row(tb + lanes + C::T_DQ, min(part4 * quarter, a.kd), min((part4 + 1) * quarter, a.kd), a.d, a.scale, t < a.T,
@@ -655,6 +663,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       tc_fence_before();
     }
   }
+  wait_previous_kernel();  // (every CTA, whatever its share: the next kernel relies on this one's end alone)
   tc_fence_before();
   __syncthreads();
   if (warp == kWarpMma) {
@@ -666,10 +675,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 // ================================================================ partial results
 // cross_join_setup says which item a block has. A warp takes four rows of its outputs (dQ: 128 rows;
 // dV, dK: 256) and the partial results in order, or every eighth of many, as in the forward's join.
-__global__ void __launch_bounds__(256) cross_join_kernel(const CBwdArgs a, int ctas) {
+__global__ void __launch_bounds__(256, 4) cross_join_kernel(const CBwdArgs a, int ctas) {
   __shared__ CrossJoin j;
   __shared__ float4 acc_s[8][4][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  allow_next_kernel();
   const bool work = cross_join_setup(a.sc, ctas, j);
   wait_previous_kernel();  // (every block: the next kernel of the stream relies on this one's end alone)
   if (!work) return;
@@ -763,17 +773,15 @@ cudaError_t launch_bwd(const CUtensorMap &mq, const CUtensorMap &mdo, const CUte
     if (e != cudaSuccess) return e;
     ready.mark(dev);
   }
-  cross_dkv_kernel<DP><<<g.dkv_ctas, kBwdThreads, CDkv<DP>::SMEM, st>>>(mq, mdo, mk, mv, dkv);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = launch_after(cross_dkv_kernel<DP>, dim3(g.dkv_ctas), dim3(kBwdThreads), CDkv<DP>::SMEM, st, mq, mdo, mk, mv, dkv);
   if (e == cudaSuccess && g.dkv_split && g.dkv_ctas > 1) {
-    e = launch_after(cross_join_kernel, dim3(g.dkv_ctas - 1, 8), 256, st, dkv, g.dkv_ctas);
+    e = launch_after(cross_join_kernel, dim3(g.dkv_ctas - 1, 4), dim3(256), 0, st, dkv, g.dkv_ctas);
   }
   if (e == cudaSuccess) {
-    cross_dq_kernel<DP><<<g.dq_ctas, kBwdThreads, CDq<DP>::SMEM, st>>>(mq, mdo, mk, mv, dq);
-    e = cudaGetLastError();
+    e = launch_after(cross_dq_kernel<DP>, dim3(g.dq_ctas), dim3(kBwdThreads), CDq<DP>::SMEM, st, mq, mdo, mk, mv, dq);
   }
   if (e == cudaSuccess && g.dq_split && g.dq_ctas > 1) {
-    e = launch_after(cross_join_kernel, dim3(g.dq_ctas - 1, 4), 256, st, dq, g.dq_ctas);
+    e = launch_after(cross_join_kernel, dim3(g.dq_ctas - 1, 2), dim3(256), 0, st, dq, g.dq_ctas);
   }
   return e;
 }

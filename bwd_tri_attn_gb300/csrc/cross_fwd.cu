@@ -121,6 +121,7 @@ __global__ void __launch_bounds__(CFwd<DP>::NTHREADS, 1)
     tmem_alloc(sb0 + C::OFF_MISC, 512);
     tmem_relinquish();
   }
+  allow_next_kernel();  // (the join waits for all of this one before it reads)
   if (warp == 8) {
     const CrossShare sh = cross_share(a.sc);
     if (lane == 0) *reinterpret_cast<CrossShare *>(sm + C::OFF_SHARE) = sh;
@@ -506,7 +507,7 @@ __device__ __forceinline__ void join_add(float &m, float &l, float4 &acc, float 
 // block has). A warp takes four rows; of few partial results (two is the rule) it adds all, in
 // order; of many (few rows over long keys) the eight warps of a block take every eighth, and the first
 // adds the eight sums in order.
-__global__ void __launch_bounds__(256) cross_fwd_join_kernel(const CFwdArgs a, int ctas) {
+__global__ void __launch_bounds__(256, 4) cross_fwd_join_kernel(const CFwdArgs a, int ctas) {
   __shared__ CrossJoin j;
   __shared__ float4 acc_s[8][4][32];
   __shared__ float2 ml_s[8][4];
@@ -683,7 +684,7 @@ int tri_cross_fwd(tri_cross_shape shape, const tri_attn_bf16 *Q, const tri_attn_
   const auto st = static_cast<cudaStream_t>(stream);
   cudaError_t e = shape.d <= 64 ? launch_fwd<64>(mq, mk, mv, a, g.ctas, dev, st) : launch_fwd<128>(mq, mk, mv, a, g.ctas, dev, st);
   if (e == cudaSuccess && g.split && g.ctas > 1) {
-    e = launch_after(cross_fwd_join_kernel, dim3(g.ctas - 1, g.two * 4), 256, st, a, g.ctas);
+    e = launch_after(cross_fwd_join_kernel, dim3(g.ctas - 1, g.two * 2), dim3(256), 0, st, a, g.ctas);
   }
   return e == cudaSuccess ? TRI_ATTN_OK : TRI_ATTN_ERR_CUDA;
 }
