@@ -15,7 +15,7 @@ constexpr int kU = 4;
 
 // The row and first channel of group k.
 __device__ __forceinline__ void group_of(int64_t k, int groups, int64_t &m, int &c0) {
-  m = groups == 1 ? k : k / groups;
+  m = groups == 1 ? k : (k >> 31) == 0 ? (int64_t)((uint32_t)k / (uint32_t)groups) : k / groups;
   c0 = (int)(k - m * groups) * TRI_CKPT_GROUP;
 }
 
@@ -24,6 +24,7 @@ __global__ void __launch_bounds__(256) ckpt_pack_kernel(const XT *__restrict__ x
                                                         int groups, int8_t *__restrict__ q8, float *__restrict__ s8) {
   constexpr int VEC = Chunk<XT>::VEC, GL = TRI_CKPT_GROUP / VEC, PER = 256 / GL;
   const int t = threadIdx.x % GL, g = threadIdx.x / GL;
+  const Span span = span_of(x, M, ldx, C);
   const int64_t n = M * groups, step = (int64_t)gridDim.x * PER * kU;
   for (int64_t k0 = (int64_t)blockIdx.x * PER * kU; k0 < n; k0 += step) {
     uint4 raw[kU];
@@ -34,7 +35,7 @@ __global__ void __launch_bounds__(256) ckpt_pack_kernel(const XT *__restrict__ x
       const int64_t k = k0 + u * PER + g;
       group_of(min(k, n - 1), groups, m[u], c[u]);
       c[u] += t * VEC;
-      raw[u] = k < n ? chunk_load<XT, AL>(x + m[u] * ldx, c[u], C) : make_uint4(0u, 0u, 0u, 0u);
+      raw[u] = k < n ? chunk_load<XT, AL>(x + m[u] * ldx, c[u], C, span) : make_uint4(0u, 0u, 0u, 0u);
     }
 #pragma unroll
     for (int u = 0; u < kU; ++u) {

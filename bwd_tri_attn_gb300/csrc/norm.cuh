@@ -94,6 +94,22 @@ struct RowSum {
   }
 };
 
+// VEC of a row's weights from channel c on (`other` past C, and everywhere without weights). Read
+// again for every row from the first-level cache: registers are better spent on rows in flight.
+template <int VEC, bool AL>
+__device__ __forceinline__ void row_weights(const float *w, int c, int C, float other, float (&v)[VEC]) {
+  if (AL && w && c < C) {
+#pragma unroll
+    for (int j = 0; j < VEC; j += 4) {
+      const float4 f = __ldg(reinterpret_cast<const float4 *>(w + c + j));
+      v[j] = f.x, v[j + 1] = f.y, v[j + 2] = f.z, v[j + 3] = f.w;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) v[j] = w && c + j < C ? __ldg(w + c + j) : other;
+  }
+}
+
 int norm_check_shape(const tri_norm_shape &s);
 cudaError_t launch_norm_reduce(const float *part, int parts, int C, float *dgamma, float *dbeta, cudaStream_t st);
 

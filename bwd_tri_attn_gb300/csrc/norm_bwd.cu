@@ -12,8 +12,14 @@
 namespace triattn {
 namespace {
 
-template <typename XT, int T, int NV, bool AL>
-__global__ void __launch_bounds__(T > 32 ? T : 256)
+// CTAs of 256 threads per SM that the registers are kept to.
+template <int NV>
+constexpr int bwd_ctas() {
+  return NV == 1 ? 3 : NV == 2 ? 2 : 1;
+}
+
+template <typename XT, int T, int NV, bool AL, bool Q8>
+__global__ void __launch_bounds__(T > 32 ? T : 256, bwd_ctas<NV>() * (T == 128 ? 2 : 1))
     norm_bwd_kernel(const XT *__restrict__ x, int64_t ldx, const int8_t *__restrict__ q8, const float *__restrict__ s8,
                     const float *__restrict__ gamma, const float *__restrict__ mean, const float *__restrict__ rstd,
                     const XT *__restrict__ dy, int64_t lddy, int64_t M, int C, int64_t rpc, XT *__restrict__ dx,
@@ -22,6 +28,7 @@ __global__ void __launch_bounds__(T > 32 ? T : 256)
   __shared__ float red[T > 32 ? 2 * T / 32 : 1][2];
   __shared__ float col[T > 32 ? 1 : 2 * NV * T * VEC];
   RowSum<T, 2> row_sum{red, 0};
+  const Span span_x = span_of(x, M, ldx, C), span_dy = span_of(dy, M, lddy, C);
   const int t = threadIdx.x % T, g = threadIdx.x / T;
   const float inv_c = 1.f / (float)C;
   const int groups = (C + TRI_CKPT_GROUP - 1) / TRI_CKPT_GROUP;
@@ -48,16 +55,16 @@ __global__ void __launch_bounds__(T > 32 ? T : 256)
       rx[v] = rd[v] = make_uint4(0u, 0u, 0u, 0u);
       sc[v] = 0.f;
       if (live) {
-        if (q8) {  // (uniform: a kernel argument)
+        if constexpr (Q8) {
           uint32_t w[VEC / 4];
           q8_load<VEC, AL>(q8 + m * C, c, C, w);
           rx[v].x = w[0];
           if constexpr (VEC == 8) rx[v].y = w[1];
           if (c < C) sc[v] = __ldg(s8 + m * groups + c / TRI_CKPT_GROUP);
         } else {
-          rx[v] = chunk_load<XT, AL>(x + m * ldx, c, C);
+          rx[v] = chunk_load<XT, AL>(x + m * ldx, c, C, span_x);
         }
-        rd[v] = chunk_load<XT, AL>(dy + m * lddy, c, C);
+        rd[v] = chunk_load<XT, AL>(dy + m * lddy, c, C, span_dy);
       }
     }
   };
@@ -72,7 +79,7 @@ __global__ void __launch_bounds__(T > 32 ? T : 256)
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       float d[VEC];
-      if (q8) {
+      if constexpr (Q8) {
         uint32_t w[VEC / 4];
         w[0] = rx[v].x;
         if constexpr (VEC == 8) w[1] = rx[v].y;
@@ -191,22 +198,26 @@ struct BwdSplitRows {
   int parts;    // CTAs
 };
 
-// The split of the rows over CTAs, from the shape alone: about 4 CTAs of 256 (8 of 128) threads for
-// each of 152 SMs, at least two rows per lane group.
+// The split of the rows over CTAs, from the shape alone: the CTAs that 152 SMs hold at once (a second,
+// shorter wave of them took as long as the first: 102 against 77 us for 768 x 768 rows of 128),
+// at least two rows for each group of threads that holds a row.
 BwdSplitRows split_rows(const tri_norm_shape &s, int geo) {
   const int T = norm_threads_per_row(geo), RPC = T > 32 ? 1 : 256 / T;
-  const int64_t target = T == 128 ? 152 * 8 : 152 * 4;
+  const int per_sm = geo == kNormT32x2 || geo == kNormT256x2 ? 2 : geo == kNormT256x4 || geo == kNormT256x8 ? 1 : T == 128 ? 6 : 3;
+  const int64_t target = 152 * per_sm;
   int64_t rpc = (s.M + target - 1) / target;
   rpc = std::max<int64_t>((rpc + RPC - 1) / RPC * RPC, 2 * RPC);
   return {rpc, (int)((s.M + rpc - 1) / rpc)};
 }
 
 template <typename XT>
-int geometry_of(const tri_norm_shape &s, const void *x, const int8_t *q8, const void *dy, const void *dx, bool *al) {
+int geometry_of(const tri_norm_shape &s, const void *x, const int8_t *q8, const float *gamma, const void *dy,
+                const void *dx, bool *al) {
   constexpr int VEC = Chunk<XT>::VEC;
   const int64_t ldx = s.ldx ? s.ldx : s.C, lddy = s.lddy ? s.lddy : s.C;
   *al = s.C % VEC == 0 && (q8 || ldx % VEC == 0) && lddy % VEC == 0 &&
-        ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(dy) | reinterpret_cast<uintptr_t>(dx)) & 15u) == 0 &&
+        ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(gamma) | reinterpret_cast<uintptr_t>(dy) |
+          reinterpret_cast<uintptr_t>(dx)) & 15u) == 0 &&
         (reinterpret_cast<uintptr_t>(q8) & (VEC - 1)) == 0;
   return norm_geometry((s.C + VEC - 1) / VEC, *al);
 }
@@ -217,15 +228,21 @@ cudaError_t launch_bwd_t(const tri_norm_shape &s, const void *x, const int8_t *q
                          float *part, cudaStream_t st) {
   constexpr int VEC = Chunk<XT>::VEC;
   bool al;
-  const int geo = geometry_of<XT>(s, x, q8, dy, dx, &al);
+  const int geo = geometry_of<XT>(s, x, q8, gamma, dy, dx, &al);
   const BwdSplitRows sp = split_rows(s, geo);
   const int64_t ldx = s.ldx ? s.ldx : s.C, lddy = s.lddy ? s.lddy : s.C;
-#define LAUNCH(T, NV, AL)                                                                                               \
-  if constexpr (T * NV * VEC <= TRI_NORM_MAX_C) {                                                                       \
-    constexpr int NT = T > 32 ? T : 256;                                                                                \
-    norm_bwd_kernel<XT, T, NV, AL><<<sp.parts, NT, 0, st>>>(static_cast<const XT *>(x), ldx, q8, s8, gamma, mean, rstd, \
-                                                            static_cast<const XT *>(dy), lddy, s.M, s.C, sp.rpc,        \
-                                                            static_cast<XT *>(dx), part);                               \
+  const XT *dyp = static_cast<const XT *>(dy);
+  XT *dxp = static_cast<XT *>(dx);
+#define LAUNCH(T, NV, AL)                                                                                                \
+  if constexpr (T * NV * VEC <= TRI_NORM_MAX_C) {                                                                        \
+    constexpr int NT = T > 32 ? T : 256;                                                                                 \
+    if (q8)                                                                                                              \
+      norm_bwd_kernel<XT, T, NV, AL, true><<<sp.parts, NT, 0, st>>>(nullptr, 0, q8, s8, gamma, mean, rstd, dyp, lddy, s.M, \
+                                                                    s.C, sp.rpc, dxp, part);                             \
+    else                                                                                                                 \
+      norm_bwd_kernel<XT, T, NV, AL, false><<<sp.parts, NT, 0, st>>>(static_cast<const XT *>(x), ldx, nullptr, nullptr,  \
+                                                                     gamma, mean, rstd, dyp, lddy, s.M, s.C, sp.rpc, dxp, \
+                                                                     part);                                              \
   }
   NORM_DISPATCH(geo, al, LAUNCH);
 #undef LAUNCH

@@ -53,16 +53,57 @@ __device__ __forceinline__ uint4 chunk_pack(const float (&v)[4], float) {
   return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
 }
 
+// The bytes [begin, end) that a tensor's rows lie in: wide loads of unaligned rows stay inside.
+struct Span {
+  uintptr_t begin, end;
+};
+template <typename T>
+__host__ __device__ __forceinline__ Span span_of(const T *p, int64_t rows, int64_t ld, int C) {
+  return Span{reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p + (rows - 1) * ld + C)};
+}
+
+// The 16 bytes at any address, from the two aligned 16-byte words around them (both inside the tensor).
+__device__ __forceinline__ uint4 ld_shifted(uintptr_t addr) {
+  const uint4 *at = reinterpret_cast<const uint4 *>(addr & ~uintptr_t(15));
+  const uint4 lo = __ldg(at), hi = __ldg(at + 1);
+  const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  const bool one = (addr & 4) != 0, two = (addr & 8) != 0;
+  const uint32_t bits = 8 * (uint32_t)(addr & 3);
+  uint32_t t[7], u[5];
+#pragma unroll
+  for (int i = 0; i < 7; ++i) t[i] = one ? w[i + 1] : w[i];
+#pragma unroll
+  for (int i = 0; i < 5; ++i) u[i] = two ? t[i + 2] : t[i];
+  return make_uint4(__funnelshift_r(u[0], u[1], bits), __funnelshift_r(u[1], u[2], bits),
+                    __funnelshift_r(u[2], u[3], bits), __funnelshift_r(u[3], u[4], bits));
+}
+
 // The chunk of values c .. c + VEC - 1 of a row (zeros past C). AL: the row starts on a 16-byte
-// boundary and C is a multiple of VEC, so a chunk is whole or absent; else value by value.
+// boundary and C is a multiple of VEC, so a chunk is whole or absent. Else two aligned words and a
+// shift, or value by value at the ends of the tensor.
 template <typename XT, bool AL>
-__device__ __forceinline__ uint4 chunk_load(const XT *row, int c, int C) {
+__device__ __forceinline__ uint4 chunk_load(const XT *row, int c, int C, const Span &span) {
   constexpr int VEC = Chunk<XT>::VEC;
   if constexpr (AL) {
     return c < C ? ld_stream(reinterpret_cast<const uint4 *>(row + c)) : make_uint4(0u, 0u, 0u, 0u);
   } else {
+    if (c >= C) return make_uint4(0u, 0u, 0u, 0u);
     uint32_t w[4] = {0u, 0u, 0u, 0u};
-    if constexpr (sizeof(XT) == 2) {
+    const uintptr_t addr = reinterpret_cast<uintptr_t>(row + c), at = addr & ~uintptr_t(15);
+    if (at >= span.begin && at + 32 <= span.end) {
+      const uint4 v = ld_shifted(addr);
+      w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+      if (c + VEC > C) {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+          if constexpr (sizeof(XT) == 2) {
+            if (c + j >= C) w[j / 2] &= (j & 1) ? 0x0000ffffu : 0xffff0000u;
+          } else {
+            if (c + j >= C) w[j] = 0u;
+          }
+        }
+      }
+    } else if constexpr (sizeof(XT) == 2) {
       const uint16_t *p = reinterpret_cast<const uint16_t *>(row);
 #pragma unroll
       for (int j = 0; j < VEC; ++j)
@@ -85,10 +126,22 @@ __device__ __forceinline__ void chunk_store(XT *row, int c, int C, const uint4 &
   } else {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     if constexpr (sizeof(XT) == 2) {
-      uint16_t *p = reinterpret_cast<uint16_t *>(row);
+      uint16_t *p = reinterpret_cast<uint16_t *>(row) + c;
+      if (c + VEC <= C) {
+        if (reinterpret_cast<uintptr_t>(p) & 2) {  // a value, three pairs, a value
+          p[0] = (uint16_t)w[0];
 #pragma unroll
-      for (int j = 0; j < VEC; ++j)
-        if (c + j < C) p[c + j] = (uint16_t)(w[j / 2] >> (16 * (j & 1)));
+          for (int j = 0; j < 3; ++j) reinterpret_cast<uint32_t *>(p + 1)[j] = __funnelshift_r(w[j], w[j + 1], 16);
+          p[7] = (uint16_t)(w[3] >> 16);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) reinterpret_cast<uint32_t *>(p)[j] = w[j];
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j)
+          if (c + j < C) p[j] = (uint16_t)(w[j / 2] >> (16 * (j & 1)));
+      }
     } else {
       uint32_t *p = reinterpret_cast<uint32_t *>(row);
 #pragma unroll
@@ -168,17 +221,17 @@ __device__ __forceinline__ uint32_t top_bits(const float (&v)[VEC]) {
   return m;
 }
 
-// VEC values to packed 8-bit ones. |x| inv is at most 127 (1 + 2^-23), which rounds to 127; a
-// group with an infinity or NaN has inv = 0 and its q's (0, or the conversion of a NaN, also 0)
-// do not matter.
+// VEC values to packed 8-bit ones: added to 1.5 x 2^23 a product is rounded to a whole number, half to
+// even, that is the sum's low byte. |x| inv is at most 127 (1 + 2^-23), which rounds to 127; the
+// bytes of a group with an infinity or NaN (inv = 0) do not matter.
 template <int VEC>
 __device__ __forceinline__ void q8_round(const float (&v)[VEC], float inv, uint32_t (&w)[VEC / 4]) {
 #pragma unroll
   for (int i = 0; i < VEC / 4; ++i) {
-    uint32_t x = 0u;
+    uint32_t r[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) x |= ((uint32_t)__float2int_rn(__fmul_rn(v[4 * i + j], inv)) & 0xffu) << (8 * j);
-    w[i] = x;
+    for (int j = 0; j < 4; ++j) r[j] = __float_as_uint(__fadd_rn(__fmul_rn(v[4 * i + j], inv), 12582912.f));
+    w[i] = __byte_perm(__byte_perm(r[0], r[1], 0x0040u), __byte_perm(r[2], r[3], 0x0040u), 0x5410u);
   }
 }
 
