@@ -37,17 +37,21 @@ __global__ void __launch_bounds__(256) ckpt_pack_kernel(const XT *__restrict__ x
       c[u] += t * VEC;
       raw[u] = k < n ? chunk_load<XT, AL>(x + m[u] * ldx, c[u], C, span) : make_uint4(0u, 0u, 0u, 0u);
     }
+    uint32_t top[kU];
+    float sc[kU], inv[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) top[u] = top_f32(group_top<GL>(chunk_top(raw[u], XT())), XT());
+    q8_group_scales<GL>(top, sc, inv);
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       const int64_t k = k0 + u * PER + g;
-      float f[VEC], sc, inv;
-      chunk_unpack(raw[u], f, XT());
-      q8_scales(group_top<GL>(top_bits<VEC>(f)), sc, inv);
+      Pairs<XT> f;
+      chunk_unpack(raw[u], f);
       uint32_t w[VEC / 4];
-      q8_round<VEC>(f, inv, w);
+      q8_round(f, inv[u], w);
       if (k < n) {
         q8_store<VEC, AL>(q8 + m[u] * C, c[u], C, w);
-        if (t == 0) s8[k] = sc;
+        if (t == 0) s8[k] = sc[u];
       }
     }
   }
@@ -74,9 +78,9 @@ __global__ void __launch_bounds__(256) ckpt_unpack_kernel(const int8_t *__restri
     }
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-      float f[VEC];
-      q8_values<VEC>(w[u], sc[u], f);
-      if (k0 + u * PER + g < n) chunk_store<XT, AL>(x + m[u] * C, c[u], C, chunk_pack(f, XT()));
+      Pairs<XT> f;
+      q8_values<XT>(w[u], sc[u], f);
+      if (k0 + u * PER + g < n) chunk_store<XT, AL>(x + m[u] * C, c[u], C, chunk_pack(f));
     }
   }
 }

@@ -94,19 +94,21 @@ struct RowSum {
   }
 };
 
-// VEC of a row's weights from channel c on (`other` past C, and everywhere without weights). Read
-// again for every row from the first-level cache: registers are better spent on rows in flight.
-template <int VEC, bool AL>
-__device__ __forceinline__ void row_weights(const float *w, int c, int C, float other, float (&v)[VEC]) {
+// A chunk of the weights from channel c on (`other` past C, and everywhere without weights). The forward reads
+// them again for every row from the first-level cache: its registers are better spent on rows in flight.
+template <typename XT, bool AL>
+__device__ __forceinline__ void row_weights(const float *w, int c, int C, float other, Pairs<XT> &f) {
   if (AL && w && c < C) {
 #pragma unroll
-    for (int j = 0; j < VEC; j += 4) {
-      const float4 f = __ldg(reinterpret_cast<const float4 *>(w + c + j));
-      v[j] = f.x, v[j + 1] = f.y, v[j + 2] = f.z, v[j + 3] = f.w;
+    for (int j = 0; j < Pairs<XT>::N; j += 2) {
+      const float4 x = __ldg(reinterpret_cast<const float4 *>(w + c + 2 * j));
+      f.v[j] = make_float2(x.x, x.y);
+      f.v[j + 1] = make_float2(x.z, x.w);
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) v[j] = w && c + j < C ? __ldg(w + c + j) : other;
+    for (int j = 0; j < Pairs<XT>::N; ++j)
+      f.v[j] = make_float2(w && c + 2 * j < C ? __ldg(w + c + 2 * j) : other, w && c + 2 * j + 1 < C ? __ldg(w + c + 2 * j + 1) : other);
   }
 }
 

@@ -7,6 +7,7 @@
 // row's loads are issued before the current row's sums (memory bandwidth bounds the kernel).
 #include <algorithm>
 
+#include "launch.cuh"
 #include "norm.cuh"
 
 namespace triattn {
@@ -24,24 +25,22 @@ __global__ void __launch_bounds__(T > 32 ? T : 256, bwd_ctas<NV>() * (T == 128 ?
                     const float *__restrict__ gamma, const float *__restrict__ mean, const float *__restrict__ rstd,
                     const XT *__restrict__ dy, int64_t lddy, int64_t M, int C, int64_t rpc, XT *__restrict__ dx,
                     float *__restrict__ part) {
-  constexpr int VEC = Chunk<XT>::VEC, NT = T > 32 ? T : 256, RPC = NT / T;
+  constexpr int VEC = Chunk<XT>::VEC, P = VEC / 2, NT = T > 32 ? T : 256, RPC = NT / T;
   __shared__ float red[T > 32 ? 2 * T / 32 : 1][2];
-  __shared__ float col[T > 32 ? 1 : 2 * NV * T * VEC];
+  __shared__ __align__(8) float col[T > 32 ? 2 : 2 * NV * T * VEC];
   RowSum<T, 2> row_sum{red, 0};
+  allow_next_kernel();  // (the sum of the partial results waits for all of this one before it reads)
   const Span span_x = span_of(x, M, ldx, C), span_dy = span_of(dy, M, lddy, C);
   const int t = threadIdx.x % T, g = threadIdx.x / T;
   const float inv_c = 1.f / (float)C;
   const int groups = (C + TRI_CKPT_GROUP - 1) / TRI_CKPT_GROUP;
-  float gm[NV][VEC], ag[NV][VEC], ab[NV][VEC];
+  Pairs<XT> gm[NV], ag[NV], ab[NV];
 #pragma unroll
-  for (int v = 0; v < NV; ++v)
+  for (int v = 0; v < NV; ++v) {
+    row_weights<XT, AL>(gamma, (v * T + t) * VEC, C, 1.f, gm[v]);
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      const int c = (v * T + t) * VEC + j;
-      gm[v][j] = gamma && c < C ? __ldg(gamma + c) : 1.f;
-      ag[v][j] = 0.f;
-      ab[v][j] = 0.f;
-    }
+    for (int j = 0; j < P; ++j) ag[v].v[j] = ab[v].v[j] = make_float2(0.f, 0.f);
+  }
   const int64_t r0 = (int64_t)blockIdx.x * rpc, r1 = min(M, r0 + rpc);
   // rows past the chunk are zeros, which add nothing and are not written (their threads still
   // join the sums)
@@ -75,40 +74,45 @@ __global__ void __launch_bounds__(T > 32 ? T : 256, bwd_ctas<NV>() * (T == 128 ?
     uint4 nx[NV], nd[NV];
     float nsc[NV], nmu, nrs;
     load(b0 + RPC + g, nx, nd, nsc, nmu, nrs);
-    float xh[NV][VEC], dz[NV][VEC], s[2] = {0.f, 0.f};
+    Pairs<XT> xh[NV], dz[NV];
+    float2 s0 = make_float2(0.f, 0.f), s1 = s0;
+    const float2 neg = make_float2(-mu, -mu), rs2 = make_float2(rs, rs);
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      float d[VEC];
       if constexpr (Q8) {
         uint32_t w[VEC / 4];
         w[0] = rx[v].x;
         if constexpr (VEC == 8) w[1] = rx[v].y;
-        q8_values<VEC>(w, sc[v], xh[v]);
+        q8_values<XT>(w, sc[v], xh[v]);
       } else {
-        chunk_unpack(rx[v], xh[v], XT());
+        chunk_unpack(rx[v], xh[v]);
       }
-      chunk_unpack(rd[v], d, XT());
+      Pairs<XT> d;
+      chunk_unpack(rd[v], d);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
+      for (int j = 0; j < P; ++j) {
         // (columns past C: dy is zero there, so they add nothing to any sum)
-        xh[v][j] = (xh[v][j] - mu) * rs;
-        ag[v][j] = fmaf(d[j], xh[v][j], ag[v][j]);
-        ab[v][j] += d[j];
-        dz[v][j] = d[j] * gm[v][j];
-        s[0] += dz[v][j];
-        s[1] = fmaf(dz[v][j], xh[v][j], s[1]);
+        xh[v].v[j] = __fmul2_rn(__fadd2_rn(xh[v].v[j], neg), rs2);
+        ag[v].v[j] = __ffma2_rn(d.v[j], xh[v].v[j], ag[v].v[j]);
+        ab[v].v[j] = __fadd2_rn(ab[v].v[j], d.v[j]);
+        dz[v].v[j] = __fmul2_rn(d.v[j], gm[v].v[j]);
+        s0 = __fadd2_rn(s0, dz[v].v[j]);
+        s1 = __ffma2_rn(dz[v].v[j], xh[v].v[j], s1);
       }
     }
+    float s[2] = {s0.x + s0.y, s1.x + s1.y};
     row_sum(s);
-    const float a = s[0] * inv_c, b = s[1] * inv_c;
+    const float a = -s[0] * inv_c, b = -s[1] * inv_c;
+    const float2 a2 = make_float2(a, a), b2 = make_float2(b, b);
     const int64_t m = b0 + g;
     if (m < r1) {
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
-        float o[VEC];
+        Pairs<XT> o;
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) o[j] = rs * (dz[v][j] - a - xh[v][j] * b);
-        chunk_store<XT, AL>(dx + m * C, (v * T + t) * VEC, C, chunk_pack(o, XT()));
+        for (int j = 0; j < P; ++j)
+          o.v[j] = __fmul2_rn(rs2, __ffma2_rn(xh[v].v[j], b2, __fadd2_rn(dz[v].v[j], a2)));
+        chunk_store<XT, AL>(dx + m * C, (v * T + t) * VEC, C, chunk_pack(o));
       }
     }
 #pragma unroll
@@ -122,11 +126,15 @@ __global__ void __launch_bounds__(T > 32 ? T : 256, bwd_ctas<NV>() * (T == 128 ?
 #pragma unroll
     for (int v = 0; v < NV; ++v)
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        const int c = (v * T + t) * VEC + j;
+      for (int j = 0; j < P; ++j) {
+        const int c = (v * T + t) * VEC + 2 * j;
         if (c < C) {
-          out[c] = ag[v][j];
-          out[C + c] = ab[v][j];
+          out[c] = ag[v].v[j].x;
+          out[C + c] = ab[v].v[j].x;
+        }
+        if (c + 1 < C) {
+          out[c + 1] = ag[v].v[j].y;
+          out[C + c + 1] = ab[v].v[j].y;
         }
       }
   } else {
@@ -136,21 +144,24 @@ __global__ void __launch_bounds__(T > 32 ? T : 256, bwd_ctas<NV>() * (T == 128 ?
 #pragma unroll
       for (int v = 0; v < NV; ++v)
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          ag[v][j] += __shfl_xor_sync(0xffffffffu, ag[v][j], o);
-          ab[v][j] += __shfl_xor_sync(0xffffffffu, ab[v][j], o);
+        for (int j = 0; j < P; ++j) {
+          ag[v].v[j].x += __shfl_xor_sync(0xffffffffu, ag[v].v[j].x, o);
+          ag[v].v[j].y += __shfl_xor_sync(0xffffffffu, ag[v].v[j].y, o);
+          ab[v].v[j].x += __shfl_xor_sync(0xffffffffu, ab[v].v[j].x, o);
+          ab[v].v[j].y += __shfl_xor_sync(0xffffffffu, ab[v].v[j].y, o);
         }
     constexpr int W = NV * T * VEC;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float2 *col2 = reinterpret_cast<float2 *>(col);
     for (int w = 0; w < 8; ++w) {
       if (warp == w && lane < T) {
 #pragma unroll
         for (int v = 0; v < NV; ++v)
 #pragma unroll
-          for (int j = 0; j < VEC; ++j) {
-            const int c = (v * T + t) * VEC + j;
-            col[c] = w ? col[c] + ag[v][j] : ag[v][j];
-            col[W + c] = w ? col[W + c] + ab[v][j] : ab[v][j];
+          for (int j = 0; j < P; ++j) {
+            const int c = (v * T + t) * P + j;
+            col2[c] = w ? __fadd2_rn(col2[c], ag[v].v[j]) : ag[v].v[j];
+            col2[W / 2 + c] = w ? __fadd2_rn(col2[W / 2 + c], ab[v].v[j]) : ab[v].v[j];
           }
       }
       __syncthreads();
@@ -169,15 +180,15 @@ __global__ void __launch_bounds__(1024) norm_reduce_kernel(const float *__restri
   __shared__ float acc[32][33];
   const int i = blockIdx.x * 32 + threadIdx.x, n = 2 * C;
   float s = 0.f;
-  if (i < n) {
-    int p = threadIdx.y;
-    for (; p + 96 < parts; p += 128) {  // four loads in flight, added in order
-      const float a0 = part[(int64_t)p * n + i], a1 = part[(int64_t)(p + 32) * n + i];
-      const float a2 = part[(int64_t)(p + 64) * n + i], a3 = part[(int64_t)(p + 96) * n + i];
-      s = (((s + a0) + a1) + a2) + a3;
+  wait_previous_kernel();
+  if (i < n)
+    for (int p = threadIdx.y; p < parts; p += 256) {  // eight loads in flight, added in order
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = p + 32 * k < parts ? part[(int64_t)(p + 32 * k) * n + i] : 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s += v[k];
     }
-    for (; p < parts; p += 32) s += part[(int64_t)p * n + i];
-  }
   acc[threadIdx.y][threadIdx.x] = s;
   __syncthreads();
   // row y of the transposed sums: an xor tree over 32 lanes
@@ -248,8 +259,7 @@ cudaError_t launch_bwd_t(const tri_norm_shape &s, const void *x, const int8_t *q
 #undef LAUNCH
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess && part) {
-    norm_reduce_kernel<<<(2 * s.C + 31) / 32, dim3(32, 32), 0, st>>>(part, sp.parts, s.C, dgamma, dbeta);
-    e = cudaGetLastError();
+    e = launch_after(norm_reduce_kernel, dim3((2 * s.C + 31) / 32), dim3(32, 32), 0, st, part, sp.parts, s.C, dgamma, dbeta);
   }
   return e;
 }

@@ -33,7 +33,7 @@ __global__ void __launch_bounds__(T > 32 ? T : 256, fwd_ctas<NV>() * (T == 128 ?
                     const float *__restrict__ beta, float eps, int64_t M, int C, XT *__restrict__ y,
                     float *__restrict__ mean, float *__restrict__ rstd, int8_t *__restrict__ q8,
                     float *__restrict__ s8) {
-  constexpr int VEC = Chunk<XT>::VEC, NT = T > 32 ? T : 256, RPC = NT / T, U = fwd_rows<NV>();
+  constexpr int VEC = Chunk<XT>::VEC, P = VEC / 2, NT = T > 32 ? T : 256, RPC = NT / T, U = fwd_rows<NV>();
   constexpr int GL = (TRI_CKPT_GROUP / VEC) < T ? (TRI_CKPT_GROUP / VEC) : T;  // lanes per checkpoint group
   __shared__ float red[T > 32 ? 2 * T / 32 : 1][U];
   RowSum<T, U> row_sum{red, 0};
@@ -45,49 +45,83 @@ __global__ void __launch_bounds__(T > 32 ? T : 256, fwd_ctas<NV>() * (T == 128 ?
   // rows past the last one are zeros that are not written)
   const int64_t step = (int64_t)gridDim.x * RPC * U;
   for (int64_t m0 = (int64_t)blockIdx.x * RPC * U; m0 < M; m0 += step) {
-    uint4 raw[U][NV];
+    Pairs<XT> f[U][NV];
+    {
+      uint4 raw[U][NV];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t m = m0 + u * RPC + g;
+      for (int u = 0; u < U; ++u) {
+        const int64_t m = m0 + u * RPC + g;
 #pragma unroll
-      for (int v = 0; v < NV; ++v)
-        raw[u][v] = m < M ? chunk_load<XT, AL>(x + m * ldx, (v * T + t) * VEC, C, span) : make_uint4(0u, 0u, 0u, 0u);
+        for (int v = 0; v < NV; ++v)
+          raw[u][v] = m < M ? chunk_load<XT, AL>(x + m * ldx, (v * T + t) * VEC, C, span) : make_uint4(0u, 0u, 0u, 0u);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int v = 0; v < NV; ++v) chunk_unpack(raw[u][v], f[u][v]);
+      if (q8) {  // (uniform: a kernel argument)
+        uint32_t top[U * NV];
+        float sc[U * NV], inv[U * NV];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int v = 0; v < NV; ++v) top[u * NV + v] = top_f32(group_top<GL>(chunk_top(raw[u][v], XT())), XT());
+        q8_group_scales<GL>(top, sc, inv);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int64_t m = m0 + u * RPC + g;
+#pragma unroll
+          for (int v = 0; v < NV; ++v) {
+            const int ch = v * T + t, c = ch * VEC;
+            uint32_t w[VEC / 4];
+            q8_round(f[u][v], inv[u * NV + v], w);
+            if (m < M) {
+              q8_store<VEC, AL>(q8 + m * C, c, C, w);
+              if (ch % GL == 0 && c < C) s8[m * groups + c / TRI_CKPT_GROUP] = sc[u * NV + v];
+            }
+          }
+        }
+      }
     }
     float mu[U], q[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      mu[u] = 0.f;
+      float2 s = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        float f[VEC];
-        chunk_unpack(raw[u][v], f, XT());
+      for (int v = 0; v < NV; ++v)
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) mu[u] += f[j];
-      }
+        for (int j = 0; j < P; ++j) s = __fadd2_rn(s, f[u][v].v[j]);
+      mu[u] = s.x + s.y;
     }
     row_sum(mu);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       mu[u] *= inv_c;
+      const float2 neg = make_float2(-mu[u], -mu[u]);
       q[u] = 0.f;
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
-        float f[VEC];
-        chunk_unpack(raw[u][v], f, XT());
+        const int c = (v * T + t) * VEC;
+        float2 s = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          const float d = (v * T + t) * VEC + j < C ? f[j] - mu[u] : 0.f;
-          q[u] = fmaf(d, d, q[u]);
+        for (int j = 0; j < P; ++j) {
+          f[u][v].v[j] = __fadd2_rn(f[u][v].v[j], neg);
+          if constexpr (!AL) {  // (values past C are 0 - mean)
+            if (c + 2 * j >= C) f[u][v].v[j].x = 0.f;
+            if (c + 2 * j + 1 >= C) f[u][v].v[j].y = 0.f;
+          }
+          s = __ffma2_rn(f[u][v].v[j], f[u][v].v[j], s);
         }
+        if (c < C) q[u] += s.x + s.y;
       }
     }
     row_sum(q);
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int ch = v * T + t, c = ch * VEC;
-      float gm[VEC], bt[VEC];
-      row_weights<VEC, AL>(gamma, c, C, 1.f, gm);
-      row_weights<VEC, AL>(beta, c, C, 0.f, bt);
+      const int c = (v * T + t) * VEC;
+      Pairs<XT> gm, bt;
+      row_weights<XT, AL>(gamma, c, C, 1.f, gm);
+      row_weights<XT, AL>(beta, c, C, 0.f, bt);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int64_t m = m0 + u * RPC + g;
@@ -96,22 +130,11 @@ __global__ void __launch_bounds__(T > 32 ? T : 256, fwd_ctas<NV>() * (T == 128 ?
           mean[m] = mu[u];
           rstd[m] = r;
         }
-        float f[VEC], o[VEC];
-        chunk_unpack(raw[u][v], f, XT());
+        const float2 r2 = make_float2(r, r);
+        Pairs<XT> o;
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) o[j] = fmaf((f[j] - mu[u]) * r, gm[j], bt[j]);
-        if (m < M) chunk_store<XT, AL>(y + m * C, c, C, chunk_pack(o, XT()));
-        if (q8) {  // (uniform: a kernel argument)
-          const uint32_t top = group_top<GL>(top_bits<VEC>(f));
-          float sc, inv;
-          q8_scales(top, sc, inv);
-          uint32_t w[VEC / 4];
-          q8_round<VEC>(f, inv, w);
-          if (m < M) {
-            q8_store<VEC, AL>(q8 + m * C, c, C, w);
-            if (ch % GL == 0 && c < C) s8[m * groups + c / TRI_CKPT_GROUP] = sc;
-          }
-        }
+        for (int j = 0; j < P; ++j) o.v[j] = __ffma2_rn(__fmul2_rn(f[u][v].v[j], r2), gm.v[j], bt.v[j]);
+        if (m < M) chunk_store<XT, AL>(y + m * C, c, C, chunk_pack(o));
       }
     }
   }

@@ -20,38 +20,59 @@ __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162flo
 __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
 __device__ __forceinline__ float to_f32(float v) { return v; }
 
-__device__ __forceinline__ void chunk_unpack(const uint4 &w, float (&v)[8], __nv_bfloat16) {
+// A chunk's values as pairs (the arithmetic on them is packed, two values an instruction).
+template <typename XT>
+struct Pairs {
+  static constexpr int N = Chunk<XT>::VEC / 2;
+  float2 v[N];
+};
+
+__device__ __forceinline__ void chunk_unpack(const uint4 &w, Pairs<__nv_bfloat16> &f) {
   const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    v[2 * j] = __uint_as_float(ww[j] << 16);
-    v[2 * j + 1] = __uint_as_float(ww[j] & 0xffff0000u);
-  }
+  for (int j = 0; j < 4; ++j) f.v[j] = make_float2(__uint_as_float(ww[j] << 16), __uint_as_float(ww[j] & 0xffff0000u));
 }
-__device__ __forceinline__ void chunk_unpack(const uint4 &w, float (&v)[8], __half) {
+__device__ __forceinline__ void chunk_unpack(const uint4 &w, Pairs<__half> &f) {
   const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&ww[j]));
-    v[2 * j] = f.x;
-    v[2 * j + 1] = f.y;
-  }
+  for (int j = 0; j < 4; ++j) f.v[j] = __half22float2(*reinterpret_cast<const __half2 *>(&ww[j]));
 }
-__device__ __forceinline__ void chunk_unpack(const uint4 &w, float (&v)[4], float) {
-  v[0] = __uint_as_float(w.x), v[1] = __uint_as_float(w.y), v[2] = __uint_as_float(w.z), v[3] = __uint_as_float(w.w);
+__device__ __forceinline__ void chunk_unpack(const uint4 &w, Pairs<float> &f) {
+  f.v[0] = make_float2(__uint_as_float(w.x), __uint_as_float(w.y));
+  f.v[1] = make_float2(__uint_as_float(w.z), __uint_as_float(w.w));
 }
 
-__device__ __forceinline__ uint4 chunk_pack(const float (&v)[8], __nv_bfloat16) {
-  return make_uint4(sm100::pack_bf16x2(v[0], v[1]), sm100::pack_bf16x2(v[2], v[3]), sm100::pack_bf16x2(v[4], v[5]),
-                    sm100::pack_bf16x2(v[6], v[7]));
+__device__ __forceinline__ uint4 chunk_pack(const Pairs<__nv_bfloat16> &f) {
+  return make_uint4(sm100::pack_bf16x2(f.v[0].x, f.v[0].y), sm100::pack_bf16x2(f.v[1].x, f.v[1].y),
+                    sm100::pack_bf16x2(f.v[2].x, f.v[2].y), sm100::pack_bf16x2(f.v[3].x, f.v[3].y));
 }
-__device__ __forceinline__ uint4 chunk_pack(const float (&v)[8], __half) {
-  return make_uint4(sm100::pack_f16x2(v[0], v[1]), sm100::pack_f16x2(v[2], v[3]), sm100::pack_f16x2(v[4], v[5]),
-                    sm100::pack_f16x2(v[6], v[7]));
+__device__ __forceinline__ uint4 chunk_pack(const Pairs<__half> &f) {
+  return make_uint4(sm100::pack_f16x2(f.v[0].x, f.v[0].y), sm100::pack_f16x2(f.v[1].x, f.v[1].y),
+                    sm100::pack_f16x2(f.v[2].x, f.v[2].y), sm100::pack_f16x2(f.v[3].x, f.v[3].y));
 }
-__device__ __forceinline__ uint4 chunk_pack(const float (&v)[4], float) {
-  return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+__device__ __forceinline__ uint4 chunk_pack(const Pairs<float> &f) {
+  return make_uint4(__float_as_uint(f.v[0].x), __float_as_uint(f.v[0].y), __float_as_uint(f.v[1].x), __float_as_uint(f.v[1].y));
 }
+
+// Bits of the largest magnitude in a chunk, in the type's own format: as unsigned numbers they order
+// as the magnitudes do, an infinity above every number and a NaN above it. top_f32 makes them FP32's.
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t chunk_top16(const uint4 &w) {
+  const uint32_t m = max_u16x2(max_u16x2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), max_u16x2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
+  return max(m & 0xffffu, m >> 16);
+}
+__device__ __forceinline__ uint32_t chunk_top(const uint4 &w, __nv_bfloat16) { return chunk_top16(w); }
+__device__ __forceinline__ uint32_t chunk_top(const uint4 &w, __half) { return chunk_top16(w); }
+__device__ __forceinline__ uint32_t chunk_top(const uint4 &w, float) {
+  return max(max(w.x & 0x7fffffffu, w.y & 0x7fffffffu), max(w.z & 0x7fffffffu, w.w & 0x7fffffffu));
+}
+__device__ __forceinline__ uint32_t top_f32(uint32_t t, __nv_bfloat16) { return t << 16; }
+__device__ __forceinline__ uint32_t top_f32(uint32_t t, __half) { return __float_as_uint(__half2float(__ushort_as_half((unsigned short)t))); }
+__device__ __forceinline__ uint32_t top_f32(uint32_t t, float) { return t; }
 
 // The bytes [begin, end) that a tensor's rows lie in: wide loads of unaligned rows stay inside.
 struct Span {
@@ -188,10 +209,14 @@ __device__ __forceinline__ void q8_store(int8_t *row, int c, int C, const uint32
   }
 }
 
-template <int VEC>
-__device__ __forceinline__ void q8_values(const uint32_t (&w)[VEC / 4], float s, float (&v)[VEC]) {
+template <typename XT>
+__device__ __forceinline__ void q8_values(const uint32_t (&w)[Chunk<XT>::VEC / 4], float s, Pairs<XT> &f) {
+  const float2 s2 = make_float2(s, s);
 #pragma unroll
-  for (int j = 0; j < VEC; ++j) v[j] = (float)(int8_t)(uint8_t)(w[j / 4] >> (8 * (j & 3))) * s;
+  for (int j = 0; j < Pairs<XT>::N; ++j) {
+    const uint32_t x = w[j / 2] >> (16 * (j & 1));
+    f.v[j] = __fmul2_rn(make_float2((float)(int8_t)(uint8_t)x, (float)(int8_t)(uint8_t)(x >> 8)), s2);
+  }
 }
 
 // A checkpoint group's scale and inverse scale from the bits of its largest magnitude (as
@@ -212,27 +237,39 @@ __device__ __forceinline__ void q8_scales(uint32_t top_bits, float &s, float &in
   }
 }
 
-// Largest |v| of a chunk, as bits.
-template <int VEC>
-__device__ __forceinline__ uint32_t top_bits(const float (&v)[VEC]) {
-  uint32_t m = 0u;
+// The scales of the N groups whose largest magnitudes (FP32 bits) the LANES lanes of a group hold in top[]:
+// lane k works out the k-th group's two quotients, and all lanes get them from there.
+template <int LANES, int N>
+__device__ __forceinline__ void q8_group_scales(const uint32_t (&top)[N], float (&s)[N], float (&inv)[N]) {
+  if constexpr (N == 1 || N > LANES) {
 #pragma unroll
-  for (int j = 0; j < VEC; ++j) m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
-  return m;
+    for (int k = 0; k < N; ++k) q8_scales(top[k], s[k], inv[k]);
+  } else {
+    const int sl = threadIdx.x % LANES, base = (threadIdx.x & 31) - sl;
+    uint32_t t = top[0];
+#pragma unroll
+    for (int k = 1; k < N; ++k) t = sl == k ? top[k] : t;
+    float a, b;
+    q8_scales(t, a, b);
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      s[k] = __shfl_sync(0xffffffffu, a, base + k);
+      inv[k] = __shfl_sync(0xffffffffu, b, base + k);
+    }
+  }
 }
 
-// VEC values to packed 8-bit ones: added to 1.5 x 2^23 a product is rounded to a whole number, half to
+// A chunk's values to packed 8-bit ones: added to 1.5 x 2^23 a product is rounded to a whole number, half to
 // even, that is the sum's low byte. |x| inv is at most 127 (1 + 2^-23), which rounds to 127; the
-// bytes of a group with an infinity or NaN (inv = 0) do not matter.
-template <int VEC>
-__device__ __forceinline__ void q8_round(const float (&v)[VEC], float inv, uint32_t (&w)[VEC / 4]) {
+// bytes of a group with an infinity or NaN (inv = 0) do not matter. (The product is an FP32 number by
+// the format's definition: the packed multiply and add were fused into one rounding.)
+template <typename XT>
+__device__ __forceinline__ void q8_round(const Pairs<XT> &f, float inv, uint32_t (&w)[Chunk<XT>::VEC / 4]) {
+  auto r = [&](float x) { return __float_as_uint(__fadd_rn(__fmul_rn(x, inv), 12582912.f)); };
 #pragma unroll
-  for (int i = 0; i < VEC / 4; ++i) {
-    uint32_t r[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) r[j] = __float_as_uint(__fadd_rn(__fmul_rn(v[4 * i + j], inv), 12582912.f));
-    w[i] = __byte_perm(__byte_perm(r[0], r[1], 0x0040u), __byte_perm(r[2], r[3], 0x0040u), 0x5410u);
-  }
+  for (int i = 0; i < Chunk<XT>::VEC / 4; ++i)
+    w[i] = __byte_perm(__byte_perm(r(f.v[2 * i].x), r(f.v[2 * i].y), 0x0040u),
+                       __byte_perm(r(f.v[2 * i + 1].x), r(f.v[2 * i + 1].y), 0x0040u), 0x5410u);
 }
 
 // The maximum over the LANES consecutive lanes that hold one checkpoint group.
