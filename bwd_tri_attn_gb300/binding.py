@@ -658,10 +658,16 @@ def norm_shape_of(x: torch.Tensor, eps: float = 1e-5, dy: torch.Tensor | None = 
                      float(eps))
 
 
+def _dense_like(x):
+    """An empty tensor of x's shape and dtype without gaps (empty_like is the cheapest call for it, but keeps the
+    order of a strided tensor's axes)."""
+    return torch.empty_like(x) if x.is_contiguous() else torch.empty(x.shape, dtype=x.dtype, device=x.device)
+
+
 def _empty_checkpoint(x):
     *rows, C = x.shape
-    return Checkpoint(x.new_empty(x.shape, dtype=torch.int8),
-                      x.new_empty((*rows, (C + CKPT_GROUP - 1) // CKPT_GROUP), dtype=_F32))
+    return Checkpoint(torch.empty(x.shape, dtype=torch.int8, device=x.device),
+                      torch.empty((*rows, (C + CKPT_GROUP - 1) // CKPT_GROUP), dtype=_F32, device=x.device))
 
 
 def norm_forward(x, gamma=None, beta=None, eps=1e-5, checkpoint=False, stream=None):
@@ -671,7 +677,7 @@ def norm_forward(x, gamma=None, beta=None, eps=1e-5, checkpoint=False, stream=No
     device = _on_device(x.get_device(), ("x", x), _arg(gamma, "gamma", _F32, shape.C, True),
                         _arg(beta, "beta", _F32, shape.C, True))
     rows = x.shape[:-1]
-    y, mean, rstd = x.new_empty(x.shape), x.new_empty(rows, dtype=_F32), x.new_empty(rows, dtype=_F32)
+    y, mean, rstd = _dense_like(x), torch.empty(rows, dtype=_F32, device=x.device), torch.empty(rows, dtype=_F32, device=x.device)
     kept = _empty_checkpoint(x) if checkpoint else None
     q8, scale = (kept.q8.data_ptr(), kept.scale.data_ptr()) if checkpoint else (None, None)
     rc = load().tri_norm_fwd(shape, x.data_ptr(), _ptr(gamma), _ptr(beta), y.data_ptr(), mean.data_ptr(),
@@ -700,10 +706,10 @@ def norm_backward(x, gamma, mean, rstd, dy, workspace=None, stream=None):
         given = [_rows_arg(x, "x", dy.dtype, n)]
     device = _on_device(dy.get_device(), *given, _arg(gamma, "gamma", _F32, C, True), _arg(mean, "mean", _F32, M),
                         _arg(rstd, "rstd", _F32, M), ("dy", dy), _arg(workspace, "workspace", None, None, True))
-    dx = dy.new_empty(dy.shape)
+    dx = _dense_like(dy)
     dgamma = dbeta = None
     if gamma is not None:
-        dgamma, dbeta = dy.new_empty(C, dtype=_F32), dy.new_empty(C, dtype=_F32)
+        dgamma, dbeta = torch.empty_like(gamma), torch.empty_like(gamma)
         if workspace is None:
             workspace = _workspace(tri_norm_bwd_workspace_size(shape), dy)
     xp, q8, scale = (None, kept[0].data_ptr(), kept[1].data_ptr()) if kept is not None else (x.data_ptr(), None, None)
@@ -752,7 +758,7 @@ def cross_shape_of(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, scale: flo
 
 
 def _workspace(nbytes, like):
-    return like.new_empty(nbytes, dtype=torch.uint8) if nbytes else None
+    return torch.empty(nbytes, dtype=torch.uint8, device=like.device) if nbytes else None
 
 
 def _cross_checked(Q, K, V, mask, kv_lens, scale, *more):
@@ -771,7 +777,7 @@ def cross_forward(Q, K, V, mask=None, kv_lens=None, scale=None, workspace=None, 
     int32 [B]. Returns (O, LSE): O [B, T, H, d] and the FP32 log-sum-exp [B, H, T] that cross_backward reads."""
     shape, device = _cross_checked(Q, K, V, mask, kv_lens, scale, _arg(workspace, "workspace", None, None, True))
     B, T, H, _ = Q.shape
-    O, LSE = Q.new_empty(Q.shape), Q.new_empty((B, H, T), dtype=_F32)
+    O, LSE = _dense_like(Q), torch.empty((B, H, T), dtype=_F32, device=Q.device)
     if workspace is None:
         workspace = _workspace(tri_cross_fwd_workspace_size(shape), Q)
     rc = load().tri_cross_fwd(shape, Q.data_ptr(), K.data_ptr(), V.data_ptr(), _ptr(mask), _ptr(kv_lens),
@@ -787,7 +793,7 @@ def cross_backward(Q, K, V, O, LSE, dO, mask=None, kv_lens=None, scale=None, wor
     rows = n // Q.shape[-1] if n else None
     shape, device = _cross_checked(Q, K, V, mask, kv_lens, scale, _arg(O, "O", _BF16, n), _arg(LSE, "LSE", _F32, rows),
                                    _arg(dO, "dO", _BF16, n), _arg(workspace, "workspace", None, None, True))
-    dQ, dK, dV = Q.new_empty(Q.shape), K.new_empty(K.shape), V.new_empty(V.shape)
+    dQ, dK, dV = _dense_like(Q), _dense_like(K), _dense_like(V)
     if workspace is None:
         workspace = _workspace(tri_cross_bwd_workspace_size(shape), Q)
     rc = load().tri_cross_bwd(shape, Q.data_ptr(), K.data_ptr(), V.data_ptr(), _ptr(mask), _ptr(kv_lens),
