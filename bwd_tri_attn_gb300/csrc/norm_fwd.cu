@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(T > 32 ? T : 256, fwd_ctas<NV>() * (T == 128 ?
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int64_t m = m0 + u * RPC + g;
-        const float r = __frsqrt_rn(fmaf(q[u], inv_c, eps));
+        const float r = rsqrtf(fmaf(q[u], inv_c, eps));
         if (v == 0 && m < M && t == 0) {
           mean[m] = mu[u];
           rstd[m] = r;
@@ -140,9 +140,10 @@ __global__ void __launch_bounds__(T > 32 ? T : 256, fwd_ctas<NV>() * (T == 128 ?
   }
 }
 
-// The forward's geometry: no column sums are kept, so a warp may hold up to 8 chunks a lane and needs
-// no barrier (rows of 2048 BF16 values, with checkpoint: 38.7 us for 8192 rows with a CTA per row).
-enum { kF8, kF16, kF32, kF32x2, kF32x4, kF32x8, kF128x4, kF128x8, kF256x8 };
+// The forward's geometry: no column sums are kept, so rows of up to 128 chunks go to warps and need no
+// barrier. Wider rows go to CTAs of 128 threads: with 8 chunks a lane in a warp, 8192 rows of 2048
+// BF16 values and their checkpoints took 31 us, with 2 chunks a thread 18 us.
+enum { kF8, kF16, kF32, kF32x2, kF32x4, kF128x2, kF128x4, kF128x8, kF256x8 };
 int norm_fwd_geometry(int chunks, bool aligned) {
   if (!aligned && chunks <= 32) return kF32;
   return chunks <= 8     ? kF8
@@ -150,7 +151,7 @@ int norm_fwd_geometry(int chunks, bool aligned) {
          : chunks <= 32  ? kF32
          : chunks <= 64  ? kF32x2
          : chunks <= 128 ? kF32x4
-         : chunks <= 256 ? kF32x8
+         : chunks <= 256 ? kF128x2
          : chunks <= 512 ? kF128x4
          : chunks <= 1024 ? kF128x8
                           : kF256x8;
@@ -162,7 +163,7 @@ int norm_fwd_geometry(int chunks, bool aligned) {
     case kF32: if (aligned) LAUNCH(32, 1, true) else LAUNCH(32, 1, false); break; \
     case kF32x2: if (aligned) LAUNCH(32, 2, true) else LAUNCH(32, 2, false); break; \
     case kF32x4: if (aligned) LAUNCH(32, 4, true) else LAUNCH(32, 4, false); break; \
-    case kF32x8: if (aligned) LAUNCH(32, 8, true) else LAUNCH(32, 8, false); break; \
+    case kF128x2: if (aligned) LAUNCH(128, 2, true) else LAUNCH(128, 2, false); break; \
     case kF128x4: if (aligned) LAUNCH(128, 4, true) else LAUNCH(128, 4, false); break; \
     case kF128x8: if (aligned) LAUNCH(128, 8, true) else LAUNCH(128, 8, false); break; \
     default: if (aligned) LAUNCH(256, 8, true) else LAUNCH(256, 8, false); break; \
