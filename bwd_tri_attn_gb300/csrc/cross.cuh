@@ -153,13 +153,15 @@ __device__ __forceinline__ CrossRun cross_run(const CrossPos &p, int left) {
 }
 
 // ---------------------------------------------------------------- partial results
-// The join kernels' view of one item that several CTAs share: block x looks at the boundary between
-// CTAs x and x + 1 and has work if that is the first boundary inside an item. CTA `first` ended inside the item (its slot 2 first + 1),
-// the CTAs after it, up to `last`, began inside it (slots 2 c); CTAs without units are left out.
+// The join kernels' view of one item that several CTAs share. Block x looks at the boundary between
+// CTAs x and x + 1; if it lies inside an item, the block takes its part of that item's rows: every
+// boundary inside an item brings gridDim.y blocks, of `blocks` in all this is number `block`. The CTA before
+// the item's first boundary ended inside it (slot 2 c + 1), the others began inside it (slot 2 c); CTAs
+// without units are left out.
 constexpr int kMaxCtas = 256;
 struct CrossJoin {
   CrossPos pos;
-  int first, count;
+  int count, block, blocks;
   int slot[kMaxCtas];  // the item's partial slots, in order
 };
 
@@ -173,19 +175,22 @@ __device__ __forceinline__ bool cross_join_setup(const CrossSched &s, int ctas, 
     CrossPos p;
     p.k = 0;
     if (u < units) p = cross_locate(s, u);
-    if (p.k > 0 && cross_bound(units, k - 1, ctas) <= u - p.k) {
-      const int64_t u1 = u - p.k + p.inner;
-      if (lane == 0) j.slot[0] = 2 * k - 1;
+    if (p.k > 0) {
+      // the first and last CTAs that begin inside the item, behind its unit u0: c with u0 < floor(units c / ctas) < u1
+      const int64_t u0 = u - p.k, u1 = u0 + p.inner;
+      const int c0 = (int)div_units((u0 + 1) * ctas + units - 1, units), c1 = (int)div_units(u1 * ctas + units - 1, units) - 1;
+      if (lane == 0) j.slot[0] = 2 * c0 - 1;
       count = 1;
-      for (int c0 = k; c0 < ctas; c0 += 32) {
-        const int c = c0 + lane;
-        const int64_t b0 = c < ctas ? cross_bound(units, c, ctas) : u1;
-        const uint32_t in = __ballot_sync(0xffffffffu, b0 < u1);
-        const bool has = b0 < u1 && cross_bound(units, c + 1, ctas) > b0;
+      for (int b = c0; b <= c1; b += 32) {
+        const int c = b + lane;
+        const bool has = c <= c1 && cross_bound(units, c + 1, ctas) > cross_bound(units, c, ctas);
         const uint32_t take = __ballot_sync(0xffffffffu, has);
         if (has) j.slot[count + __popc(take & ((1u << lane) - 1u))] = 2 * c;
         count += __popc(take);
-        if (in != 0xffffffffu) break;
+      }
+      if (lane == 0) {
+        j.block = (k - c0) * gridDim.y + blockIdx.y;
+        j.blocks = (c1 - c0 + 1) * gridDim.y;
       }
     }
     if (lane == 0) {
@@ -196,6 +201,11 @@ __device__ __forceinline__ bool cross_join_setup(const CrossSched &s, int ctas, 
   __syncthreads();
   return j.count > 0;
 }
+
+// How a join's warps divide an item of `count` partial results: few, and a warp adds those of four rows
+// (all loads in flight together); more, and of one row; many (a few rows over long keys), and the
+// block's eight warps add every eighth of one row's each, the first of them their sums.
+constexpr int kJoinFew = 4, kJoinMany = 16;
 
 // Live keys of the 32 N keys from k0 on, one bit a key. all: every one of them is live and there is no mask. The
 // whole warp calls load() (its reads can be issued early) and then words().
@@ -226,24 +236,20 @@ struct KeyWords {
 // the accumulator otherwise (the whole warp calls it, before the products that read the tile).
 template <int BOXES>
 __device__ __forceinline__ void zero_dead_rows(uint8_t *tile, const uint32_t (&w)[4]) {
-  const int lane = threadIdx.x & 31;
+  // eight lanes (16 bytes each) a row, four rows at a time; a word's 32 rows in eight such steps
+  const int lane = threadIdx.x & 31, sub = lane >> 3;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    for (uint32_t dead = ~w[i]; dead;) {
-      // four rows at a time, eight lanes (16 bytes each) per row
-      int row = -1;
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t dead = ~w[i];
+    if (dead == 0u) continue;
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int r = dead ? __ffs(dead) - 1 : -1;
-        if (r >= 0) dead &= dead - 1;
-        if ((lane >> 3) == g) row = r;
-      }
-      if (row >= 0)
+    for (int s = 0; s < 8; ++s)
+      if ((dead >> (4 * s + sub)) & 1u)
 #pragma unroll
         for (int x = 0; x < BOXES; ++x)
-          *reinterpret_cast<uint4 *>(tile + x * kBoxBytes + (32 * i + row) * 128 + (lane & 7) * 16) =
+          *reinterpret_cast<uint4 *>(tile + x * kBoxBytes + (32 * i + 4 * s + sub) * 128 + (lane & 7) * 16) =
               make_uint4(0u, 0u, 0u, 0u);
-    }
+  }
   sm100::fence_proxy_async_smem();
   __syncwarp();
 }
@@ -287,7 +293,46 @@ __device__ __forceinline__ void warp_arrive(uint32_t bar) {
   if ((threadIdx.x & 31) == 0) sm100::mbar_arrive(bar);
 }
 
+// 32 columns c0 .. c0 + 31 of a row of results: as BF16 to out + c0 (columns past d left out), or as FP32 to
+// part + c0 where out is NULL (columns past `pitch` left out). wide: both start on 32-byte boundaries
+// and d is a multiple of 16. A thread's row is contiguous and its neighbours' are not, so whole sectors
+// are stored at a time: with 16-byte stores the end of a run took 4 to 7 thousand cycles.
+__device__ __forceinline__ void store_cols(const float (&f)[32], int c0, int d, int pitch, bool wide, uint16_t *out, float *part) {
+  if (out) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t w[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] = sm100::pack_bf16x2(f[16 * h + 2 * j], f[16 * h + 2 * j + 1]);
+      const int c = c0 + 16 * h;
+      if (wide) {
+        if (c < d) sm100::st_v8(out + c, w);
+      } else {
+        if (c < d) *reinterpret_cast<uint4 *>(out + c) = make_uint4(w[0], w[1], w[2], w[3]);
+        if (c + 8 < d) *reinterpret_cast<uint4 *>(out + c + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      uint32_t w[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(f[8 * h + j]);
+      const int c = c0 + 8 * h;
+      if (c >= pitch) continue;
+      if (wide) {
+        sm100::st_v8(part + c, w);
+      } else {
+        *reinterpret_cast<uint4 *>(part + c) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4 *>(part + c + 4) = make_uint4(w[4], w[5], w[6], w[7]);
+      }
+    }
+  }
+}
+
 // ---------------------------------------------------------------- host side
+inline bool aligned32(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
+
 // Tensor map of a [B, n, heads, d] BF16 tensor (strides in elements), boxes of 64 channels x `hb` heads
 // x `rows` positions. Channels past d, positions past n: zeros.
 inline cudaError_t make_cross_map(CUtensorMap *m, const void *p, int B, int n, int heads, int d, const int64_t (&st)[3],

@@ -28,6 +28,7 @@ struct CBwdArgs {
   int tiles;        // row tiles of a head block
   float c, scale;   // scale log2(e), scale
   bool clean;       // there may be masked keys
+  bool wide;        // store_cols' rule holds for the gradients and the partial results
   const uint8_t *mask;
   const float *nl, *nd;  // [B][H / GB][tiles][128]: -LSE log2(e) (-inf: row without keys or past T), -D
   uint16_t *dQ, *dK, *dV;
@@ -82,31 +83,18 @@ __global__ void __launch_bounds__(256) cross_bwd_prep_kernel(const CBwdArgs a, c
 }
 
 // ================================================================ shared pieces of the two main kernels
-// 16 kd columns of a thread's accumulator row, chunks [q0, q1) of 16: times f to `out` (BF16, d
-// columns) or `part` (FP32). The whole warp calls it; rows with mine = false write nothing.
-__device__ __forceinline__ void store_row(uint32_t tm, int q0, int q1, int d, float f, bool mine, uint16_t *out, float *part) {
-#pragma unroll 1
-  for (int q = q0; q < q1; ++q) {
-    uint32_t o[16];
-    tmem_ld16(tm + 16 * q, o);
-    tmem_wait_ld(o);
-    float v[16];
+// 32 columns of a thread's accumulator row, from column c0 on, times f (store_cols). The whole warp calls it; rows with
+// mine = false write nothing.
+__device__ __forceinline__ void store_row(uint32_t tm, int c0, const CBwdArgs &a, float f, bool mine, uint16_t *out, float *part) {
+  if (c0 >= 16 * a.kd) return;
+  uint32_t o[32];
+  tmem_ld32(tm + c0, o);
+  tmem_wait_ld(o);
+  float v[32];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(o[j]) * f;
-    if (mine && out) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        if (16 * q + 8 * j < d)
-          *reinterpret_cast<uint4 *>(out + 16 * q + 8 * j) =
-              make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
-                         pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
-    } else if (mine) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        *reinterpret_cast<float4 *>(part + 16 * q + 4 * j) = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-    }
-    __syncwarp();
-  }
+  for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(o[j]) * f;
+  if (mine) store_cols(v, c0, a.d, 16 * a.kd, a.wide, out, part);
+  __syncwarp();
 }
 
 // The element-wise warps of both kernels: four warpgroups, thread = tile row, 32 columns each.
@@ -388,15 +376,17 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         p.next(a.sc);
       }
       if (!ok) break;
-      // the run's sums: warpgroups 0 and 1 store the halves of dV's channels, 2 and 3 dK's
+      // the run's sums: warpgroups 0 and 1 store every other 32 of dV's channels, 2 and 3 of dK's
       ok = wait_bar_warp(bar(C::B_ACC), runs & 1, ab);
       if (!ok) break;
       tc_fence_after();
       const int64_t off = (((int64_t)b * a.sc.S + key) * a.Hk + hk) * a.d;
-      const int pitch = 16 * a.kd, which = part4 >> 1, mid = (a.kd + 1) / 2;
+      const int pitch = 16 * a.kd, which = part4 >> 1;
       float *part = a.part + (((int64_t)max(run.slot, 0) * 2 + which) * kTile + row) * pitch;
-      store_row(tb + lanes + (which ? C::T_DK : C::T_DV), part4 & 1 ? mid : 0, part4 & 1 ? a.kd : mid, a.d, which ? a.scale : 1.f,
-                key < a.sc.S, run.slot < 0 ? (which ? a.dK : a.dV) + off : nullptr, part);
+#pragma unroll 1
+      for (int c0 = 32 * (part4 & 1); c0 < pitch; c0 += 64)
+        store_row(tb + lanes + (which ? C::T_DK : C::T_DV), c0, a, which ? a.scale : 1.f, key < a.sc.S,
+                  run.slot < 0 ? (which ? a.dK : a.dV) + off : nullptr, part);
       tc_fence_before();
     }
   }
@@ -648,18 +638,17 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         p.next(a.sc);
       }
       if (!ok) break;
-      // the run's dQ: the warpgroups take a quarter of the channels each
+      // the run's dQ: the warpgroups take 32 channels each
       ok = wait_bar_warp(bar(C::B_ACC), runs & 1, ab);
       if (!ok) break;
       tc_fence_after();
       // The kernel before, the join of dK and dV, reads the partial results' space: nothing is written
       // before it has ended. (What this kernel reads was complete before that one's predecessor read it.)
       if (runs == 0) wait_previous_kernel();
-      const int t = mt * (kTile >> a.lg) + (row >> a.lg), h = hb * a.GB + (row & (a.GB - 1)), quarter = (a.kd + 3) / 4;
-      const int pitch = 16 * a.kd;
-      store_row(tb + lanes + C::T_DQ, min(part4 * quarter, a.kd), min((part4 + 1) * quarter, a.kd), a.d, a.scale, t < a.T,
+      const int t = mt * (kTile >> a.lg) + (row >> a.lg), h = hb * a.GB + (row & (a.GB - 1));
+      store_row(tb + lanes + C::T_DQ, 32 * part4, a, a.scale, t < a.T,
                 run.slot < 0 ? a.dQ + (((int64_t)b * a.T + t) * a.H + h) * a.d : nullptr,
-                a.part + ((int64_t)max(run.slot, 0) * kTile + row) * pitch);
+                a.part + ((int64_t)max(run.slot, 0) * kTile + row) * 16 * a.kd);
       tc_fence_before();
     }
   }
@@ -673,63 +662,83 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 }
 
 // ================================================================ partial results
-// cross_join_setup says which item a block has. A warp takes four rows of its outputs (dQ: 128 rows;
-// dV, dK: 256) and the partial results in order, or every eighth of many, as in the forward's join.
+// The sum of R rows' partial results first, first + stride, ... (row r0 of dQ; of dV, then dK), as in the
+// forward's join.
+template <int R>
+__device__ __forceinline__ void join_sum(const CBwdArgs &a, const CrossJoin &j, int rows, int r0, int first, int stride, float4 (&acc)[R]) {
+  const int lane = threadIdx.x & 31, pitch = 16 * a.kd;
+#pragma unroll
+  for (int x = 0; x < R; ++x) acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (4 * lane >= pitch) return;
+  constexpr int N = R == 4 ? 2 : 8;  // partial results in flight
+  for (int c0 = first; c0 < j.count; c0 += N * stride) {
+    float4 v[N][R];
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int c = c0 + n * stride;
+      const float *base = a.part + ((int64_t)j.slot[min(c, j.count - 1)] * rows + r0) * pitch + 4 * lane;
+#pragma unroll
+      for (int x = 0; x < R; ++x)
+        v[n][x] = c < j.count ? *reinterpret_cast<const float4 *>(base + x * pitch) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+      for (int x = 0; x < R; ++x) acc[x].x += v[n][x].x, acc[x].y += v[n][x].y, acc[x].z += v[n][x].z, acc[x].w += v[n][x].w;
+  }
+}
+
+__device__ __forceinline__ void join_store(const CBwdArgs &a, const CrossPos &p, int r, const float4 &v) {
+  const int lane = threadIdx.x & 31, row = r % kTile;
+  uint16_t *out;
+  if (a.sc.by_keys) {
+    const int hk = p.item / p.nt, key = (p.item % p.nt) * kTile + row;
+    if (key >= a.sc.S) return;
+    out = (r / kTile ? a.dK : a.dV) + (((int64_t)p.b * a.sc.S + key) * a.Hk + hk) * a.d;
+  } else {
+    const int hb = p.item / a.tiles, t = (p.item % a.tiles) * (kTile >> a.lg) + (row >> a.lg);
+    if (t >= a.T) return;
+    out = a.dQ + (((int64_t)p.b * a.T + t) * a.H + hb * a.GB + (row & (a.GB - 1))) * a.d;
+  }
+  if (4 * lane < a.d) *reinterpret_cast<uint2 *>(out + 4 * lane) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+}
+
 __global__ void __launch_bounds__(256, 4) cross_join_kernel(const CBwdArgs a, int ctas) {
   __shared__ CrossJoin j;
-  __shared__ float4 acc_s[8][4][32];
+  __shared__ float4 acc_s[8][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   allow_next_kernel();
   const bool work = cross_join_setup(a.sc, ctas, j);
   wait_previous_kernel();  // (every block: the next kernel of the stream relies on this one's end alone)
   if (!work) return;
-  const bool many = j.count > 4;
-  const int pitch = 16 * a.kd, rows = (a.sc.by_keys ? 2 : 1) * kTile;
-  const int64_t slot = (int64_t)rows * pitch;
-  const int step = many ? 4 : 32;  // rows a block takes at a time
-  for (int b0 = blockIdx.y * step; b0 < rows; b0 += gridDim.y * step) {
-    const int r0 = b0 + (many ? 0 : 4 * warp);
-    float4 acc[4];
+  const int rows = (a.sc.by_keys ? 2 : 1) * kTile;
+  if (j.count <= kJoinFew) {
+    for (int r = j.block * 32 + 4 * warp; r < rows; r += j.blocks * 32) {
+      float4 acc[4];
+      join_sum<4>(a, j, rows, r, 0, 1, acc);
 #pragma unroll
-    for (int x = 0; x < 4; ++x) acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (4 * lane < pitch)
-#pragma unroll 2
-      for (int c = many ? warp : 0; c < j.count; c += many ? 8 : 1) {
-        const float *base = a.part + j.slot[c] * slot + (int64_t)r0 * pitch + 4 * lane;
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const float4 v = *reinterpret_cast<const float4 *>(base + x * pitch);
-          acc[x].x += v.x, acc[x].y += v.y, acc[x].z += v.z, acc[x].w += v.w;
-        }
-      }
-    if (many) {
-#pragma unroll
-      for (int x = 0; x < 4; ++x) acc_s[warp][x][lane] = acc[x];
-      __syncthreads();
-      if (warp == 0)
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-          for (int y = 1; y < 8; ++y) {
-            const float4 v = acc_s[y][x][lane];
-            acc[x].x += v.x, acc[x].y += v.y, acc[x].z += v.z, acc[x].w += v.w;
-          }
-      __syncthreads();
+      for (int x = 0; x < 4; ++x) join_store(a, j.pos, r + x, acc[x]);
     }
-    if (4 * lane >= a.d || (many && warp > 0)) continue;
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      const int row = (r0 + x) % kTile;
-      uint16_t *out;
-      if (a.sc.by_keys) {
-        const int hk = j.pos.item / j.pos.nt, key = (j.pos.item % j.pos.nt) * kTile + row;
-        if (key >= a.sc.S) continue;
-        out = (r0 / kTile ? a.dK : a.dV) + (((int64_t)j.pos.b * a.sc.S + key) * a.Hk + hk) * a.d;
-      } else {
-        const int hb = j.pos.item / a.tiles, t = (j.pos.item % a.tiles) * (kTile >> a.lg) + (row >> a.lg);
-        if (t >= a.T) continue;
-        out = a.dQ + (((int64_t)j.pos.b * a.T + t) * a.H + hb * a.GB + (row & (a.GB - 1))) * a.d;
+  } else if (j.count <= kJoinMany) {
+    for (int r = j.block * 8 + warp; r < rows; r += j.blocks * 8) {
+      float4 acc[1];
+      join_sum<1>(a, j, rows, r, 0, 1, acc);
+      join_store(a, j.pos, r, acc[0]);
+    }
+  } else {
+    for (int r = j.block; r < rows; r += j.blocks) {
+      float4 acc[1];
+      join_sum<1>(a, j, rows, r, warp, 8, acc);
+      acc_s[warp][lane] = acc[0];
+      __syncthreads();
+      if (warp == 0) {
+        for (int y = 1; y < 8; ++y) {
+          const float4 v = acc_s[y][lane];
+          acc[0].x += v.x, acc[0].y += v.y, acc[0].z += v.z, acc[0].w += v.w;
+        }
+        join_store(a, j.pos, r, acc[0]);
       }
-      *reinterpret_cast<uint2 *>(out + 4 * lane) = make_uint2(pack_bf16x2(acc[x].x, acc[x].y), pack_bf16x2(acc[x].z, acc[x].w));
+      __syncthreads();
     }
   }
 }
@@ -839,6 +848,7 @@ int tri_cross_bwd(tri_cross_shape shape, const tri_attn_bf16 *Q, const tri_attn_
   a.scale = shape.scale;
   a.mask = mask;
   a.clean = mask || kv_lens;
+  a.wide = shape.d % 16 == 0 && aligned32(dQ) && aligned32(dK) && aligned32(dV) && aligned32(ws + g.part);
   float *nl = reinterpret_cast<float *>(ws + g.nl), *nd = reinterpret_cast<float *>(ws + g.nd);
   a.nl = nl;
   a.nd = nd;

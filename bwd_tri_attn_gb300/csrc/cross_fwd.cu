@@ -47,6 +47,7 @@ struct CFwdArgs {
   int two;        // row tiles per item: 1 or 2
   float c;        // |scale| log2(e)
   bool negate;    // scale < 0
+  bool wide;      // store_cols' rule holds for O and the partial results
   bool clean;     // there may be masked keys: warp 10 passes every tile on
   const uint8_t *mask;
   uint16_t *O;
@@ -179,6 +180,16 @@ __global__ void __launch_bounds__(CFwd<DP>::NTHREADS, 1)
           for (int y = 0; y < C::BOXES; ++y)
             tma_load_4d(sb0 + C::TILE + y * kBoxBytes, &mQ, bar(C::B_QF), 64 * y, r1.head0, r1.t0, p.b);
       }
+      if (u + run.n < n && lane == 0) {  // the next run's Q into L2: when Q's place is free it is wanted at once
+        CrossPos next = p;
+        next.skip(a.sc, run.n);
+        const RowTile r0 = row_tile(a, next.item, 0), r1 = row_tile(a, next.item, 1);
+#pragma unroll
+        for (int y = 0; y < C::BOXES; ++y) {
+          tma_prefetch_4d(&mQ, 64 * y, r0.head0, r0.t0, next.b);
+          if (r1.live) tma_prefetch_4d(&mQ, 64 * y, r1.head0, r1.t0, next.b);
+        }
+      }
       __syncwarp();
       for (int k = 0; k < run.n && ok; ++k, ++u) {
         for (int x = 2 * u; a.clean && x < 2 * u + 2 && ok; ++x) {
@@ -278,12 +289,17 @@ __global__ void __launch_bounds__(CFwd<DP>::NTHREADS, 1)
           const bool last = k + 1 == run.n, more = !last || next_pair;
           ok = ok && wait_bar_warp(full + 8 * rv.slot, rv.parity, ab);
           pv(0, par0, k == 0, last);
-          if (more) {
-            wait_k(last);
+          if (!last) {
+            wait_k(false);
             if (ok) qk(0, 0);
           }
           pv(1, par1, k == 0, last);
-          if (more && ok) qk(1, 1);
+          if (!last && ok) qk(1, 1);
+          if (last && more) {  // (Q may still be on its way: nothing of this run waits for it)
+            wait_k(true);
+            if (ok) qk(0, 0);
+            if (ok) qk(1, 1);
+          }
           if (!ok) break;
           v_done();
           if (more) k_done(last ? next_n == 1 : k + 2 == run.n);
@@ -448,31 +464,20 @@ __global__ void __launch_bounds__(CFwd<DP>::NTHREADS, 1)
       w0 *= inv;
       w1 *= inv;
 #pragma unroll 1
-      for (int q = 0; q < a.kd; ++q) {
-        uint32_t o[16];
-        tmem_ld16(to + 16 * q, o);
+      for (int q = 0; 2 * q < a.kd; ++q) {
+        uint32_t o[32];
+        tmem_ld32(to + 32 * q, o);
         tmem_wait_ld(o);
-        float f[16];
+        float f[32];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) f[j] = __uint_as_float(o[j]) * w0;
+        for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(o[j]) * w0;
         if (merge) {
-          tmem_ld16(to + 128 + 16 * q, o);
+          tmem_ld32(to + 128 + 32 * q, o);
           tmem_wait_ld(o);
 #pragma unroll
-          for (int j = 0; j < 16; ++j) f[j] = fmaf(__uint_as_float(o[j]), w1, f[j]);
+          for (int j = 0; j < 32; ++j) f[j] = fmaf(__uint_as_float(o[j]), w1, f[j]);
         }
-        if (mine && run.slot < 0) {
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            if (16 * q + 8 * j < a.d)
-              *reinterpret_cast<uint4 *>(out + 16 * q + 8 * j) =
-                  make_uint4(pack_bf16x2(f[8 * j], f[8 * j + 1]), pack_bf16x2(f[8 * j + 2], f[8 * j + 3]),
-                             pack_bf16x2(f[8 * j + 4], f[8 * j + 5]), pack_bf16x2(f[8 * j + 6], f[8 * j + 7]));
-        } else if (mine) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<float4 *>(part + 16 * q + 4 * j) = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
-        }
+        if (mine) store_cols(f, 32 * q, a.d, pitch, a.wide, run.slot < 0 ? out : nullptr, part);
         __syncwarp();
       }
       if (mine) {
@@ -503,73 +508,97 @@ __device__ __forceinline__ void join_add(float &m, float &l, float4 &acc, float 
   m = m1;
 }
 
-// Adds the partial results of the items that several CTAs share (cross_join_setup says which item a
-// block has). A warp takes four rows; of few partial results (two is the rule) it adds all, in
-// order; of many (few rows over long keys) the eight warps of a block take every eighth, and the first
-// adds the eight sums in order.
-__global__ void __launch_bounds__(256, 4) cross_fwd_join_kernel(const CFwdArgs a, int ctas) {
-  __shared__ CrossJoin j;
-  __shared__ float4 acc_s[8][4][32];
-  __shared__ float2 ml_s[8][4];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const bool work = cross_join_setup(a.sc, ctas, j);
-  wait_previous_kernel();  // (every block: the next kernel of the stream relies on this one's end alone)
-  if (!work) return;
-  const bool many = j.count > 4;
-  const int pitch = 16 * a.kd, tile = kTile * (pitch + 4), rows = a.two * kTile;
-  const int64_t slot = (int64_t)a.two * tile;
-  const int step = many ? 4 : 32;  // rows a block takes at a time
-  for (int b0 = blockIdx.y * step; b0 < rows; b0 += gridDim.y * step) {
-    const int r0 = b0 + (many ? 0 : 4 * warp), i = r0 / kTile, row = r0 % kTile;  // four rows of one tile
-    const RowTile rt = row_tile(a, j.pos.item, i);
-    const bool live = rt.live && rt.t0 + (row >> a.lg) < a.T;
-    float4 acc[4];
-    float m[4], l[4];
+// R rows of an item (four at most from row r0 on, of one tile): the sum over the partial results
+// first, first + stride, ...
+template <int R>
+struct JoinRows {
+  float4 acc[R];
+  float m[R], l[R];
+  __device__ __forceinline__ void add(const CFwdArgs &a, const CrossJoin &j, int r0, int first, int stride) {
+    const int lane = threadIdx.x & 31, pitch = 16 * a.kd, tile = kTile * (pitch + 4);
+    const int i = r0 / kTile, row = r0 % kTile;
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
+    for (int x = 0; x < R; ++x) {
       acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
       m[x] = -INFINITY;
       l[x] = 0.f;
     }
-    if (live)
-#pragma unroll 2
-      for (int c = many ? warp : 0; c < j.count; c += many ? 8 : 1) {
-        const float *base = a.part + j.slot[c] * slot + (int64_t)i * tile;
-        const float4 lse = *reinterpret_cast<const float4 *>(base + kTile * pitch + row);
-        const float ls[4] = {lse.x, lse.y, lse.z, lse.w};
-        float4 v[4];
+    constexpr int N = R == 4 ? 2 : 8;  // partial results in flight
+    for (int c0 = first; c0 < j.count; c0 += N * stride) {
+      float4 v[N][R];
+      float lse[N][R];
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
-          v[x] = 4 * lane < pitch ? *reinterpret_cast<const float4 *>(base + (row + x) * pitch + 4 * lane)
-                                  : make_float4(0.f, 0.f, 0.f, 0.f);
-        // (rows past T hold nothing: whatever comes out for them is not written)
+      for (int n = 0; n < N; ++n) {
+        const int c = c0 + n * stride;
+        const float *base = a.part + (int64_t)j.slot[min(c, j.count - 1)] * (a.two * tile) + (int64_t)i * tile;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) join_add(m[x], l[x], acc[x], ls[x], 1.f, v[x]);
+        for (int x = 0; x < R; ++x) {
+          const bool has = c < j.count;
+          lse[n][x] = has ? base[kTile * pitch + row + x] : -INFINITY;
+          v[n][x] = has && 4 * lane < pitch ? *reinterpret_cast<const float4 *>(base + (row + x) * pitch + 4 * lane)
+                                            : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
       }
-    if (many) {
+      // (rows past T hold nothing: whatever comes out for them is not written)
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        acc_s[warp][x][lane] = acc[x];
-        if (lane == 0) ml_s[warp][x] = make_float2(m[x], l[x]);
-      }
-      __syncthreads();
-      if (warp == 0)
+      for (int n = 0; n < N; ++n)
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
-          for (int y = 1; y < 8; ++y) join_add(m[x], l[x], acc[x], ml_s[y][x].x, ml_s[y][x].y, acc_s[y][x][lane]);
-      __syncthreads();
+        for (int x = 0; x < R; ++x) join_add(m[x], l[x], acc[x], lse[n][x], 1.f, v[n][x]);
     }
-    if (!live || (many && warp > 0)) continue;
+  }
+  __device__ __forceinline__ void store(const CFwdArgs &a, const CrossPos &p, int r0) const {
+    const int lane = threadIdx.x & 31, i = r0 / kTile, row = r0 % kTile;
+    const RowTile rt = row_tile(a, p.item, i);
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
+    for (int x = 0; x < R; ++x) {
       const int t = rt.t0 + ((row + x) >> a.lg), h = rt.head0 + ((row + x) & (a.GB - 1));
       if (t >= a.T) continue;
       const float inv = l[x] > 0.f ? 1.f / l[x] : 0.f;
       if (4 * lane < a.d)
-        *reinterpret_cast<uint2 *>(a.O + (((int64_t)j.pos.b * a.T + t) * a.H + h) * a.d + 4 * lane) =
+        *reinterpret_cast<uint2 *>(a.O + (((int64_t)p.b * a.T + t) * a.H + h) * a.d + 4 * lane) =
             make_uint2(pack_bf16x2(acc[x].x * inv, acc[x].y * inv), pack_bf16x2(acc[x].z * inv, acc[x].w * inv));
       if (lane == 0)
-        a.LSE[((int64_t)j.pos.b * a.H + h) * a.T + t] = l[x] > 0.f ? (m[x] + __log2f(l[x])) * kLn2 : -INFINITY;
+        a.LSE[((int64_t)p.b * a.H + h) * a.T + t] = l[x] > 0.f ? (m[x] + __log2f(l[x])) * kLn2 : -INFINITY;
+    }
+  }
+};
+
+// Adds the partial results of the items that several CTAs share.
+__global__ void __launch_bounds__(256, 3) cross_fwd_join_kernel(const CFwdArgs a, int ctas) {
+  __shared__ CrossJoin j;
+  __shared__ float4 acc_s[8][32];
+  __shared__ float2 ml_s[8];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool work = cross_join_setup(a.sc, ctas, j);
+  wait_previous_kernel();  // (every block: the next kernel of the stream relies on this one's end alone)
+  if (!work) return;
+  // rows that hold queries: the first tile's, and the second one's if it is live
+  const RowTile r0 = row_tile(a, j.pos.item, 0), r1 = row_tile(a, j.pos.item, 1);
+  const int rows = r1.live ? kTile + min(kTile, (a.T - r1.t0) << a.lg) : min(kTile, (a.T - r0.t0) << a.lg);
+  if (j.count <= kJoinFew) {
+    for (int r = j.block * 32 + 4 * warp; r < rows; r += j.blocks * 32) {
+      JoinRows<4> x;
+      x.add(a, j, r, 0, 1);
+      x.store(a, j.pos, r);
+    }
+  } else if (j.count <= kJoinMany) {
+    for (int r = j.block * 8 + warp; r < rows; r += j.blocks * 8) {
+      JoinRows<1> x;
+      x.add(a, j, r, 0, 1);
+      x.store(a, j.pos, r);
+    }
+  } else {
+    for (int r = j.block; r < rows; r += j.blocks) {
+      JoinRows<1> x;
+      x.add(a, j, r, warp, 8);
+      acc_s[warp][lane] = x.acc[0];
+      if (lane == 0) ml_s[warp] = make_float2(x.m[0], x.l[0]);
+      __syncthreads();
+      if (warp == 0) {
+        for (int y = 1; y < 8; ++y) join_add(x.m[0], x.l[0], x.acc[0], ml_s[y].x, ml_s[y].y, acc_s[y][lane]);
+        x.store(a, j.pos, r);
+      }
+      __syncthreads();
     }
   }
 }
@@ -677,6 +706,7 @@ int tri_cross_fwd(tri_cross_shape shape, const tri_attn_bf16 *Q, const tri_attn_
   a.c = fmaxf(fabsf(shape.scale) * kLog2e, 1.17549435e-38f);
   a.negate = shape.scale < 0.f;
   a.clean = mask || kv_lens;
+  a.wide = shape.d % 16 == 0 && aligned32(O) && aligned32(workspace);
   a.mask = mask;
   a.O = O;
   a.LSE = LSE;
