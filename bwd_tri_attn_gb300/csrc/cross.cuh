@@ -293,38 +293,31 @@ __device__ __forceinline__ void warp_arrive(uint32_t bar) {
   if ((threadIdx.x & 31) == 0) sm100::mbar_arrive(bar);
 }
 
-// 32 columns c0 .. c0 + 31 of a row of results: as BF16 to out + c0 (columns past d left out), or as FP32 to
-// part + c0 where out is NULL (columns past `pitch` left out). wide: both start on 32-byte boundaries
-// and d is a multiple of 16. A thread's row is contiguous and its neighbours' are not, so whole sectors
-// are stored at a time: with 16-byte stores the end of a run took 4 to 7 thousand cycles.
-__device__ __forceinline__ void store_cols(const float (&f)[32], int c0, int d, int pitch, bool wide, uint16_t *out, float *part) {
+// 16 columns c0 .. c0 + 15 of a row of results: as BF16 to out + c0 (columns past d left out), or as FP32 to
+// part + c0 where out is NULL. wide: both start on 32-byte boundaries and d is a multiple of 16. A
+// thread's row is contiguous and its neighbours' are not, so whole sectors are stored at a time.
+__device__ __forceinline__ void store_cols(const float (&f)[16], int c0, int d, bool wide, uint16_t *out, float *part) {
   if (out) {
+    uint32_t w[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = sm100::pack_bf16x2(f[2 * j], f[2 * j + 1]);
+    if (wide) {
+      if (c0 < d) sm100::st_v8(out + c0, w);
+    } else {
+      if (c0 < d) *reinterpret_cast<uint4 *>(out + c0) = make_uint4(w[0], w[1], w[2], w[3]);
+      if (c0 + 8 < d) *reinterpret_cast<uint4 *>(out + c0 + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+  } else {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       uint32_t w[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) w[j] = sm100::pack_bf16x2(f[16 * h + 2 * j], f[16 * h + 2 * j + 1]);
-      const int c = c0 + 16 * h;
-      if (wide) {
-        if (c < d) sm100::st_v8(out + c, w);
-      } else {
-        if (c < d) *reinterpret_cast<uint4 *>(out + c) = make_uint4(w[0], w[1], w[2], w[3]);
-        if (c + 8 < d) *reinterpret_cast<uint4 *>(out + c + 8) = make_uint4(w[4], w[5], w[6], w[7]);
-      }
-    }
-  } else {
-#pragma unroll
-    for (int h = 0; h < 4; ++h) {
-      uint32_t w[8];
-#pragma unroll
       for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(f[8 * h + j]);
-      const int c = c0 + 8 * h;
-      if (c >= pitch) continue;
       if (wide) {
-        sm100::st_v8(part + c, w);
+        sm100::st_v8(part + c0 + 8 * h, w);
       } else {
-        *reinterpret_cast<uint4 *>(part + c) = make_uint4(w[0], w[1], w[2], w[3]);
-        *reinterpret_cast<uint4 *>(part + c + 4) = make_uint4(w[4], w[5], w[6], w[7]);
+        *reinterpret_cast<uint4 *>(part + c0 + 8 * h) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4 *>(part + c0 + 8 * h + 4) = make_uint4(w[4], w[5], w[6], w[7]);
       }
     }
   }

@@ -83,17 +83,20 @@ __global__ void __launch_bounds__(256) cross_bwd_prep_kernel(const CBwdArgs a, c
 }
 
 // ================================================================ shared pieces of the two main kernels
-// 32 columns of a thread's accumulator row, from column c0 on, times f (store_cols). The whole warp calls it; rows with
-// mine = false write nothing.
+// 32 columns of a thread's accumulator row, from column c0 on (at most 16 kd in all), times f (store_cols). The whole
+// warp calls it; rows with mine = false write nothing.
 __device__ __forceinline__ void store_row(uint32_t tm, int c0, const CBwdArgs &a, float f, bool mine, uint16_t *out, float *part) {
   if (c0 >= 16 * a.kd) return;
   uint32_t o[32];
   tmem_ld32(tm + c0, o);
   tmem_wait_ld(o);
-  float v[32];
 #pragma unroll
-  for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(o[j]) * f;
-  if (mine) store_cols(v, c0, a.d, 16 * a.kd, a.wide, out, part);
+  for (int h = 0; h < 2; ++h) {
+    float v[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(o[16 * h + j]) * f;
+    if (mine && c0 + 16 * h < 16 * a.kd) store_cols(v, c0 + 16 * h, a.d, a.wide, out, part);
+  }
   __syncwarp();
 }
 

@@ -4,8 +4,8 @@
 // One CTA per SM works through its units; a unit is one 128-key tile against up to two tiles of 128
 // rows. Two streams run side by side, each with a softmax warpgroup (warps 0-3 and 4-7, thread = row): the
 // two row tiles of an item, or, where it has one (single tokens, a last odd tile), its even and odd key tiles,
-// merged at the end of a run. Warp 8 loads K and V through a TMA ring; warp 10 loads Q and zeroes
-// masked rows of V. TMEM: S0, S1 (128 columns each; P, as BF16 pairs, over the first half of S once
+// merged at the end of a run by warps 12-15, which write the run's rows. Warp 8 loads K and V through a TMA
+// ring; warp 10 loads Q and zeroes masked rows of V. TMEM: S0, S1 (128 columns each; P, as BF16 pairs, over the first half of S once
 // S is in registers), O0, O1. Warp 9 issues all products, stream by stream: P V of a stream's step (in two
 // halves, as P comes) and Q K of its next step behind it, so that they run during the softmax of the other
 // stream. (Two issuing warps mixed the streams' products: both softmaxes then ran at the same time, and the
@@ -24,18 +24,19 @@ template <int DP>  // head dimension rounded up to 64 or 128 (the tiles in share
 struct CFwd {
   static constexpr int BOXES = DP / 64, TILE = BOXES * kBoxBytes;
   static constexpr int NST = DP == 128 ? 5 : 10;  // ring of K and V tiles, in turn
-  static constexpr int OFF_RING = 2 * TILE, OFF_BAR = OFF_RING + NST * TILE;
+  static constexpr int OFF_RING = 2 * TILE;
+  static constexpr int OFF_ML = OFF_RING + NST * TILE;  // the streams' maxima and sums at the end of a run
+  static constexpr int OFF_BAR = OFF_ML + 2 * kTile * 8;
   static constexpr int B_FULL = 0, B_EMPTY = NST, B_CLEAN = 2 * NST, B_QF = 3 * NST, B_QE = B_QF + 1, B_S = B_QE + 1,
-                       B_P = B_S + 2, B_O = B_P + 4, B_MERGE = B_O + 2, B_MERGED = B_MERGE + 1,
-                       B_DONE = B_MERGED + 1, NBAR = B_DONE + 1;
+                       B_P = B_S + 2, B_O = B_P + 4, B_ST = B_O + 2, B_SF = B_ST + 2, B_OF = B_SF + 2,
+                       B_DONE = B_OF + 2, NBAR = B_DONE + 1;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int OFF_SHARE = OFF_MISC + 16;
-  static constexpr int OFF_ML = (OFF_SHARE + (int)sizeof(CrossShare) + 15) / 16 * 16;  // stream 1's maxima and sums
-  static constexpr int SMEM = OFF_ML + kTile * 8 + 1024;
-  static constexpr int NTHREADS = 384;
-  // 168 registers a thread at launch: 256 of them take 216, the other 128 give down to 72
-  static constexpr uint32_t REG_LAUNCH = 168, REG_SOFT = 216, REG_OTHER = 72;
-  static_assert(256 * REG_SOFT + (NTHREADS - 256) * REG_OTHER == NTHREADS * REG_LAUNCH, "register split");
+  static constexpr int SMEM = OFF_SHARE + (int)sizeof(CrossShare);
+  static constexpr int NTHREADS = 512;
+  // 128 registers a thread at launch: the softmax warps take 176, the others give down to 88 (output) and 72
+  static constexpr uint32_t REG_LAUNCH = 128, REG_SOFT = 176, REG_OUT = 88, REG_OTHER = 72;
+  static_assert(256 * REG_SOFT + 128 * REG_OUT + 128 * REG_OTHER == NTHREADS * REG_LAUNCH, "register split");
   static constexpr int T_S = 0, T_O = 256;  // TMEM columns; row tile i: + 128 i
   static_assert(SMEM <= 227 * 1024, "shared memory budget");
   static_assert(OFF_SHARE % 4 == 0, "alignment");
@@ -90,11 +91,14 @@ __global__ void __launch_bounds__(CFwd<DP>::NTHREADS, 1)
     cross_fwd_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
                      const __grid_constant__ CUtensorMap mV, const CFwdArgs a) {
   using C = CFwd<DP>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t sm[];
   const uint32_t sb0 = smem_u32(sm);
+  if (sb0 & 1023u) {  // (swizzled tiles need it; the declaration asks for it)
+    if (threadIdx.x == 0) atomicExch(a.sc.status, kStatusTimeout);
+    return;
+  }
   // (the hardware's first four warps, which the schedulers prefer, are those that feed the others)
-  const int warp = ((threadIdx.x >> 5) + 8) % 12, lane = threadIdx.x & 31;
+  const int warp = ((threadIdx.x >> 5) + 8) % 16, lane = threadIdx.x & 31;
   auto bar = [&](int k) { return sb0 + C::OFF_BAR + 8u * (uint32_t)k; };
   volatile uint32_t *misc = reinterpret_cast<volatile uint32_t *>(sm + C::OFF_MISC);
   const Abort ab{reinterpret_cast<volatile int *>(misc + 1), a.sc.status};
@@ -113,11 +117,15 @@ __global__ void __launch_bounds__(CFwd<DP>::NTHREADS, 1)
       mbar_init(bar(C::B_P + 2 + i), 4);
       mbar_init(bar(C::B_O + i), 1);
     }
-    mbar_init(bar(C::B_MERGE), 128);
-    mbar_init(bar(C::B_MERGED), 128);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(C::B_ST + i), 4);
+      mbar_init(bar(C::B_SF + i), 4);
+      mbar_init(bar(C::B_OF + i), 4);
+    }
     misc[1] = 0;
     fence_barrier_init();
   }
+  if (threadIdx.x < 3) tma_prefetch_map(threadIdx.x == 0 ? &mQ : threadIdx.x == 1 ? &mK : &mV);
   if (warp == 9) {
     tmem_alloc(sb0 + C::OFF_MISC, 512);
     tmem_relinquish();
@@ -221,6 +229,7 @@ __global__ void __launch_bounds__(CFwd<DP>::NTHREADS, 1)
     CrossPos p = share.pos;
     uint32_t par0 = 0, par1 = 0;  // phases of the streams' P barriers
     int runs = 0;                 // runs whose Q K has begun
+    int outs0 = 0, outs1 = 0;     // runs in which the streams have had units
     bool ok = true, begun = false;  // the coming run's first Q K is issued
     auto wait_k = [&](bool begins) {  // (and for Q of a run that begins)
       if (begins) {
@@ -243,6 +252,11 @@ __global__ void __launch_bounds__(CFwd<DP>::NTHREADS, 1)
     auto pv = [&](int i, uint32_t &parity, bool begins, bool ends) {
       const uint32_t ds = tb + C::T_S + 128 * i, dO = tb + C::T_O + 128 * i;
       const uint64_t dv = dv0 + rv.slot * kTileStep;
+      if (begins) {  // the stream's O of the run before has been read
+        int &outs = i ? outs1 : outs0;
+        if (outs > 0) ok = ok && wait_bar_warp(bar(C::B_OF + i), (outs - 1) & 1, ab);
+        ++outs;
+      }
       ok = ok && wait_bar_warp(bar(C::B_P + i), parity, ab);  // (P comes in two halves of 64 keys)
       tc_fence_after();
       if (ok) mma_ts_x4_e(dO, ds, dv, kMnStep, id_o, begins ? 0u : 1u);
@@ -326,7 +340,7 @@ __global__ void __launch_bounds__(CFwd<DP>::NTHREADS, 1)
     __syncwarp();
   } else if (warp == 11) {
     reg_dealloc<C::REG_OTHER>();  // (only gives its registers)
-  } else {
+  } else if (warp < 8) {
     reg_alloc<C::REG_SOFT>();
     // ------------------------------------------------------------ softmax of stream i, thread = row
     const int i = warp >> 2, row = (warp & 3) * 32 + lane;
@@ -337,7 +351,6 @@ __global__ void __launch_bounds__(CFwd<DP>::NTHREADS, 1)
     bool ok = true;
     int x = 0;       // units of this stream
     int outs = 0;    // runs in which it has units
-    int merges = 0;  // runs of two streams
     for (int u = 0; u < n && ok;) {
       const CrossRun run = cross_run(p, n - u);
       const bool alt = !row_tile(a, p.item, 1).live;
@@ -422,72 +435,96 @@ __global__ void __launch_bounds__(CFwd<DP>::NTHREADS, 1)
         l += t2.x + t2.y;
       }
       if (!ok) break;
-      // the run's rows: O / l, and the log-sum-exp
-      ok = wait_bar_warp(bar(C::B_O + i), outs & 1, ab);
+      // m and l go to the output warps, which have read those of the run before
+      if (outs > 0) ok = wait_bar_warp(bar(C::B_SF + i), (outs - 1) & 1, ab);
       if (!ok) break;
       ++outs;
-      tc_fence_after();
-      float w0 = 1.f, w1 = 0.f;  // weights of the streams' O
-      const bool merge = alt && run.n > 1;
-      if (merge) {
-        if (i == 1) {  // stream 0's threads of the same rows read O1, and m and l from here
-          ml[row] = make_float2(m, l);
-          tc_fence_before();
-          mbar_arrive(bar(C::B_MERGE));
-          ok = wait_bar_warp(bar(C::B_MERGED), merges & 1, ab);
-          if (!ok) break;
-          tc_fence_after();
-          ++merges;
-          continue;
+      ml[i * kTile + row] = make_float2(m, l);
+      warp_arrive(bar(C::B_ST + i));
+    }
+  } else if (warp >= 12) {
+    reg_dealloc<C::REG_OUT>();
+    // ------------------------------------------------------------ output of a run, thread = row: O / l, and the log-sum-exp
+    // (warps of their own: the softmax goes on with the next run; done by its warps, the end of a run, with
+    // its rarely run code, cost 6 to 8 us)
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const float2 *ml = reinterpret_cast<const float2 *>(sm + C::OFF_ML);
+    const int pitch = 16 * a.kd;
+    CrossPos p = share.pos;
+    bool ok = true;
+    int c0 = 0, c1 = 0;  // runs of the streams
+    for (int u = 0; u < n && ok;) {
+      const CrossRun run = cross_run(p, n - u);
+      const int b = p.b, item = p.item;
+      const bool alt = !row_tile(a, item, 1).live, merge = alt && run.n > 1;
+      u += run.n;
+      p.skip(a.sc, run.n);
+#pragma unroll 1
+      for (int i = 0; i < (alt ? 1 : 2); ++i) {
+        int &c = i ? c1 : c0;
+        ok = wait_bar_warp(bar(C::B_ST + i), c & 1, ab) && wait_bar_warp(bar(C::B_O + i), c & 1, ab);
+        ++c;
+        if (ok && merge) {
+          ok = wait_bar_warp(bar(C::B_ST + 1), c1 & 1, ab) && wait_bar_warp(bar(C::B_O + 1), c1 & 1, ab);
+          ++c1;
         }
-        ok = wait_bar_warp(bar(C::B_MERGE), merges & 1, ab);
         if (!ok) break;
         tc_fence_after();
-        ++merges;
-        const float2 o = ml[row];
-        const float m1 = fmaxf(m, o.x);
-        if (m1 != -INFINITY) {
-          w0 = ex2(m - m1);
-          w1 = ex2(o.x - m1);
-        }
-        l = l * w0 + o.y * w1;
-        m = m1;
-      }
-      const float inv = l > 0.f ? __fdividef(1.f, l) : 0.f;
-      const float lse2 = l > 0.f ? m + __log2f(l) : -INFINITY;
-      const int t = rt.t0 + (row >> a.lg), h = rt.head0 + (row & (a.GB - 1));
-      const bool mine = t < a.T;
-      const int pitch = 16 * a.kd;
-      float *tile = a.part + ((int64_t)max(run.slot, 0) * a.two + (alt ? 0 : i)) * kTile * (pitch + 4);
-      float *part = tile + row * pitch;
-      uint16_t *out = a.O + (((int64_t)b * a.T + t) * a.H + h) * a.d;
-      w0 *= inv;
-      w1 *= inv;
-#pragma unroll 1
-      for (int q = 0; 2 * q < a.kd; ++q) {
-        uint32_t o[32];
-        tmem_ld32(to + 32 * q, o);
-        tmem_wait_ld(o);
-        float f[32];
-#pragma unroll
-        for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(o[j]) * w0;
+        float m = ml[i * kTile + row].x, l = ml[i * kTile + row].y;
+        float w0 = 1.f, w1 = 0.f;  // weights of the streams' O
         if (merge) {
-          tmem_ld32(to + 128 + 32 * q, o);
+          const float2 o = ml[kTile + row];
+          const float m1 = fmaxf(m, o.x);
+          if (m1 != -INFINITY) {
+            w0 = ex2(m - m1);
+            w1 = ex2(o.x - m1);
+          }
+          l = l * w0 + o.y * w1;
+          m = m1;
+          warp_arrive(bar(C::B_SF + 1));
+        }
+        warp_arrive(bar(C::B_SF + i));
+        const float inv = l > 0.f ? __fdividef(1.f, l) : 0.f;
+        w0 *= inv;
+        w1 *= inv;
+        const RowTile rt = row_tile(a, item, i);
+        const int t = rt.t0 + (row >> a.lg), h = rt.head0 + (row & (a.GB - 1));
+        const bool mine = t < a.T;
+        float *tile = a.part + ((int64_t)max(run.slot, 0) * a.two + i) * kTile * (pitch + 4);
+        float *part = tile + row * pitch;
+        uint16_t *out = a.O + (((int64_t)b * a.T + t) * a.H + h) * a.d;
+        const uint32_t to = tb + lanes + C::T_O + 128 * i;
+#pragma unroll 1
+        for (int q = 0; q < a.kd; ++q) {
+          uint32_t o[16];
+          float f[16];
+          tmem_ld16(to + 16 * q, o);
           tmem_wait_ld(o);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) f[j] = fmaf(__uint_as_float(o[j]), w1, f[j]);
+          for (int j = 0; j < 16; ++j) f[j] = __uint_as_float(o[j]) * w0;
+          if (merge) {
+            tmem_ld16(to + 128 + 16 * q, o);
+            tmem_wait_ld(o);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) f[j] = fmaf(__uint_as_float(o[j]), w1, f[j]);
+          }
+          if (q + 1 == a.kd) {  // O is read: the next run's P V may start it again
+            tc_fence_before();
+            warp_arrive(bar(C::B_OF + i));
+            if (merge) warp_arrive(bar(C::B_OF + 1));
+          }
+          if (mine) store_cols(f, 16 * q, a.d, a.wide, run.slot < 0 ? out : nullptr, part);
+          __syncwarp();
         }
-        if (mine) store_cols(f, 32 * q, a.d, pitch, a.wide, run.slot < 0 ? out : nullptr, part);
-        __syncwarp();
+        if (mine) {
+          const float lse2 = l > 0.f ? m + __log2f(l) : -INFINITY;
+          if (run.slot < 0)
+            a.LSE[((int64_t)b * a.H + h) * a.T + t] = lse2 * kLn2;
+          else
+            tile[kTile * pitch + row] = lse2;
+        }
       }
-      if (mine) {
-        if (run.slot < 0)
-          a.LSE[((int64_t)b * a.H + h) * a.T + t] = lse2 * kLn2;
-        else
-          tile[kTile * pitch + row] = lse2;
-      }
-      tc_fence_before();
-      if (merge) mbar_arrive(bar(C::B_MERGED));
     }
   }
   tc_fence_before();
