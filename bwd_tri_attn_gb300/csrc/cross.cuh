@@ -202,10 +202,12 @@ __device__ __forceinline__ bool cross_join_setup(const CrossSched &s, int ctas, 
   return j.count > 0;
 }
 
-// How a join's warps divide an item of `count` partial results: few, and a warp adds those of four rows
-// (all loads in flight together); more, and of one row; many (a few rows over long keys), and the
-// block's eight warps add every eighth of one row's each, the first of them their sums.
-constexpr int kJoinFew = 4, kJoinMany = 16;
+// How a join's warps divide an item of `count` partial results: two (an item between two CTAs, the usual
+// case), and a warp adds those of four rows, all loads in flight together; up to kJoinMany, and of one row;
+// more (a few rows over long keys), and the block's warps add every sixteenth of one row's each, the first
+// of them their sums. Two blocks of 512 threads an SM: what bounds a join is the latency of its loads, and
+// blocks that wait for a place (with smaller ones, which begin with the same arithmetic) cost another such.
+constexpr int kJoinThreads = 512, kJoinMany = 16;
 
 // Live keys of the 32 N keys from k0 on, one bit a key. all: every one of them is live and there is no mask. The
 // whole warp calls load() (its reads can be issued early) and then words().

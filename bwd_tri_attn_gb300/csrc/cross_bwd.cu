@@ -107,8 +107,38 @@ constexpr int kWarpLoad = kEw, kWarpMma = kEw + 1, kWarpRun = kEw + 2;
 
 // D (+)= A B over 128 rows of B, A the BF16 pairs that the four warpgroups wrote over the first half of
 // their 32 columns.
-__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool start) {
-  mma_ts_x8_e<0, 8, 32, 40, 64, 72, 96, 104>(d, a, b, kMnStep, idesc, start ? 0u : 1u);
+__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t start) {
+  mma_ts_x8_e<0, 8, 32, 40, 64, 72, 96, 104>(d, a, b, kMnStep, idesc, start ^ 1u);
+}
+
+// The units of a share, one after the other: whether a unit begins, whether it ends its run.
+struct UnitAhead {
+  CrossPos p;
+  int rest, left = 0;  // units from the coming one on; units left of the run
+  uint32_t first = 0, last = 0;
+  __device__ __forceinline__ UnitAhead(const CrossShare &sh, const CrossSched &sc) : rest(sh.n) {
+    if (rest == 0) return;
+    p = sh.pos;
+    step(sc);
+  }
+  __device__ __forceinline__ void step(const CrossSched &sc) {
+    first = left == 0 ? 1u : 0u;
+    if (first) {
+      left = cross_run(p, rest).n;
+      rest -= left;
+      if (rest > 0) p.skip(sc, left);
+    }
+    --left;
+    last = left == 0 ? 1u : 0u;
+  }
+};
+
+// Keeps the work that leads to these values ahead of what follows.
+__device__ __forceinline__ void pin(uint64_t &a, uint64_t &b, uint64_t &c, uint64_t &d) {
+  asm volatile("" : "+l"(a), "+l"(b), "+l"(c), "+l"(d));
+}
+__device__ __forceinline__ void pin(uint32_t &a, uint32_t &b, uint32_t &c, uint32_t &d) {
+  asm volatile("" : "+r"(a), "+r"(b), "+r"(c), "+r"(d));
 }
 
 // ================================================================ dK and dV
@@ -249,71 +279,74 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const uint64_t dk = desc_k(sb0), dv = desc_k(sb0 + C::TILE), q_k = desc_k(sb0 + C::OFF_Q), q_mn = desc_mn(sb0 + C::OFF_Q),
                    d_k = desc_k(sb0 + C::OFF_D), d_mn = desc_mn(sb0 + C::OFF_D);
     constexpr uint64_t kTileStep = C::TILE >> 4;
-    Ring<C::NQ> q;  // of unit u + 1
+    UnitAhead next(share, a.sc);  // of unit u + 1
+    Ring<C::NQ> q;
     Ring<C::ND> d;
-    int q_slot = 0, d_slot = 0;  // of unit u
+    uint64_t dv_b = 0, dk_b = 0;     // of unit u: dO and Q as the second operands,
+    uint32_t de_bar = 0, qe_bar = 0;  // the barriers that free them,
+    uint32_t first = 0, last = 0;     // whether it begins, ends its run
     int runs = 0;
     bool ok = true;
-    // What a unit needs to know about the next one is worked out ahead: what stands between a wait and
-    // the products behind it is on the critical path.
-    CrossPos p = share.pos;
-    int left = 0;  // units left of unit u + 1's run after it
-    bool first = true, last = false, begin1 = false, end1 = false;
-    auto ahead = [&](int u1) {
-      begin1 = left == 0;
-      if (begin1) left = cross_run(p, n - u1).n;
-      end1 = --left == 0;
-      p.next(a.sc);
-    };
-    if (n > 0) ahead(0);
     // Round u: dV of unit u and S^T of unit u + 1 (its columns are P's) while the warps work on dS; dK of
     // unit u and dP^T of unit u + 1 (its columns are dS's) while they work on the next P. Round -1: S^T
-    // and dP^T of unit 0.
+    // and dP^T of unit 0. This warp gets few issue slots beside four element-wise ones, and between P's
+    // arrival and dV every instruction of it is waited for: all that a unit needs to know is worked out
+    // behind the dV before (512 cycles of the tensor cores), not at the round's end, where it cost 600 cycles of
+    // 2900 a unit.
 #pragma unroll 1
     for (int u = -1; u < n; ++u) {
-      const bool more = u + 1 < n;
       if (u >= 0) {
         ok = wait_bar_warp(bar(C::B_P), u & 1, ab);
         if (!ok) break;
         tc_fence_after();
-        mma_rows(tb + C::T_DV, tb + C::T_S, d_mn + d_slot * kTileStep, id_o, first);
+        mma_rows(tb + C::T_DV, tb + C::T_S, dv_b, id_o, first);
       }
+      const bool more = u + 1 < n;
+      uint64_t s_b = q_k + q.slot * kTileStep, dp_b = d_k + d.slot * kTileStep, dv_b1 = d_mn + d.slot * kTileStep,
+               dk_b1 = q_mn + q.slot * kTileStep;
+      const uint32_t qf_bar = bar(C::B_QF + q.slot), df_bar = bar(C::B_DF + d.slot), q_par = q.parity, d_par = d.parity;
+      uint32_t de_bar1 = bar(C::B_DE + d.slot), qe_bar1 = bar(C::B_QE + q.slot);
+      const uint32_t first1 = next.first, last1 = next.last;
+      q.next();
+      d.next();
+      if (u + 2 < n) next.step(a.sc);
+      pin(s_b, dp_b, dv_b1, dk_b1);
+      pin(de_bar1, qe_bar1, next.first, next.last);
       if (more) {
-        if (begin1) {
+        if (first1) {
           ok = wait_bar_warp(bar(C::B_KF), runs & 1, ab);
           if (!ok) break;
           ++runs;
         }
-        ok = wait_bar_warp(bar(C::B_QF + q.slot), q.parity, ab);
+        ok = wait_bar_warp(qf_bar, q_par, ab);
         if (!ok) break;
         tc_fence_after();
-        mma_channels<C::BOXES>(tb + C::T_S, dk, q_k + q.slot * kTileStep, id_s, a.kd);
+        mma_channels<C::BOXES>(tb + C::T_S, dk, s_b, id_s, a.kd);
         mma_commit_e(bar(C::B_S));
       }
       if (u >= 0) {
-        mma_commit_e(bar(C::B_DE + d_slot));
+        mma_commit_e(de_bar);
         ok = wait_bar_warp(bar(C::B_DS), u & 1, ab);
         if (!ok) break;
         tc_fence_after();
-        mma_rows(tb + C::T_DK, tb + C::T_DP, q_mn + q_slot * kTileStep, id_o, first);
+        mma_rows(tb + C::T_DK, tb + C::T_DP, dk_b, id_o, first);
         if (last) mma_commit_e(bar(C::B_ACC));
       }
       if (more) {
-        ok = wait_bar_warp(bar(C::B_DF + d.slot), d.parity, ab);
+        ok = wait_bar_warp(df_bar, d_par, ab);
         if (!ok) break;
         tc_fence_after();
-        mma_channels<C::BOXES>(tb + C::T_DP, dv, d_k + d.slot * kTileStep, id_s, a.kd);
+        mma_channels<C::BOXES>(tb + C::T_DP, dv, dp_b, id_s, a.kd);
         mma_commit_e(bar(C::B_DP));
-        if (end1) mma_commit_e(bar(C::B_KE));
+        if (last1) mma_commit_e(bar(C::B_KE));
       }
-      if (u >= 0) mma_commit_e(bar(C::B_QE + q_slot));
-      q_slot = q.slot;
-      d_slot = d.slot;
-      q.next();
-      d.next();
-      first = begin1;
-      last = end1;
-      if (u + 2 < n) ahead(u + 2);
+      if (u >= 0) mma_commit_e(qe_bar);
+      dv_b = dv_b1;
+      dk_b = dk_b1;
+      de_bar = de_bar1;
+      qe_bar = qe_bar1;
+      first = first1;
+      last = last1;
     }
     mma_commit_e(bar(C::B_DONE));
     if (lane == 0) drain_bar(bar(C::B_DONE), 0);
@@ -408,11 +441,11 @@ struct CDq {
   static constexpr int NK = DP == 128 ? 3 : 6, NV = DP == 128 ? 2 : 4;
   static constexpr int OFF_K = 2 * TILE, OFF_V = OFF_K + NK * TILE, OFF_BAR = OFF_V + NV * TILE;
   static constexpr int B_KF = 0, B_KE = NK, B_KC = 2 * NK, B_VF = 3 * NK, B_VE = B_VF + NV, B_QF = B_VE + NV, B_QE = B_QF + 1,
-                       B_S = B_QE + 1, B_DP = B_S + 2, B_DPE = B_DP + 1, B_DS = B_DPE + 1, B_ACC = B_DS + 1,
+                       B_S = B_QE + 1, B_DP = B_S + 2, B_DPE = B_DP + 1, B_DS = B_DPE + 1, B_ACC = B_DS + 2,
                        B_DONE = B_ACC + 1, NBAR = B_DONE + 1;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8, OFF_SHARE = OFF_MISC + 16;
   static constexpr int SMEM = OFF_SHARE + (int)sizeof(CrossShare) + 1024;
-  static constexpr int T_S = 0, T_DP = 256, T_DQ = 384;  // (S twice: units in turn)
+  static constexpr int T_S = 0, T_DP = 256, T_DQ = 384;  // (S twice: units in turn, and B_S, B_DS with it)
   static_assert(SMEM <= 227 * 1024 && OFF_SHARE % 4 == 0, "shared memory");
 };
 
@@ -430,7 +463,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   volatile uint32_t *misc = reinterpret_cast<volatile uint32_t *>(sm + C::OFF_MISC);
   const Abort ab{reinterpret_cast<volatile int *>(misc + 1), a.sc.status};
   if (threadIdx.x == 0) {
-    for (int k = 0; k < C::NBAR; ++k) mbar_init(bar(k), k == C::B_DPE || k == C::B_DS ? kEw : 1);
+    for (int k = 0; k < C::NBAR; ++k) mbar_init(bar(k), k >= C::B_DPE && k < C::B_ACC ? kEw : 1);
     misc[1] = 0;
     fence_barrier_init();
   }
@@ -532,60 +565,72 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                    v_k = desc_k(sb0 + C::OFF_V);
     constexpr uint64_t kTileStep = C::TILE >> 4;
     const int full = a.clean ? C::B_KC : C::B_KF;
-    Ring<C::NK> k;  // of unit u + 1
+    UnitAhead next(share, a.sc);  // of unit u + 1
+    Ring<C::NK> k;
     Ring<C::NV> v;
-    int k_slot = 0;  // of unit u
+    uint64_t s_b = k_k, dp_b = v_k, dq_b1 = k_mn;  // of unit u + 1: K, V, and K as dQ's second operand,
+    uint32_t k_bar = bar(full), v_bar = bar(C::B_VF), ke_bar1 = bar(C::B_KE), ve_bar = bar(C::B_VE);  // their barriers
+    uint32_t k_par = 0, v_par = 0;
+    uint64_t dq_b = 0;  // of unit u
+    uint32_t ke_bar = 0, first = 0, last = 0;
     int runs = 0;
     bool ok = true;
-    CrossPos p = share.pos;
-    int left = 0;  // units left of unit u + 1's run after it
-    bool first = true, last = false, begin1 = false, end1 = false;
-    auto ahead = [&](int u1) {
-      begin1 = left == 0;
-      if (begin1) left = cross_run(p, n - u1).n;
-      end1 = --left == 0;
-      p.next(a.sc);
-    };
-    if (n > 0) ahead(0);
     // Round u: S and dP of unit u + 1 while the warps work on dS of unit u, then dQ of unit u. (S of u + 1
-    // takes the columns of S and dS of unit u - 1, whose dQ is issued.)
+    // takes the columns of S and dS of unit u - 1, whose dQ is issued. The warps may be done with dS of u + 1
+    // before dS of u is waited for here, if this warp is held up: hence two barriers.) What the next round needs to know is
+    // worked out before the wait for dS, as in cross_dkv_kernel.
 #pragma unroll 1
     for (int u = -1; u < n; ++u) {
+      const uint32_t first1 = next.first, last1 = next.last;
       if (u + 1 < n) {
         const int odd = (u + 1) & 1;
-        if (begin1) {
+        if (first1) {
           ok = wait_bar_warp(bar(C::B_QF), runs & 1, ab);
           if (!ok) break;
           ++runs;
         }
-        ok = wait_bar_warp(bar(full + k.slot), k.parity, ab);
+        ok = wait_bar_warp(k_bar, k_par, ab);
         if (!ok) break;
         tc_fence_after();
-        mma_channels<C::BOXES>(tb + C::T_S + 128 * odd, dq, k_k + k.slot * kTileStep, id_s, a.kd);
+        mma_channels<C::BOXES>(tb + C::T_S + 128 * odd, dq, s_b, id_s, a.kd);
         mma_commit_e(bar(C::B_S + odd));
         if (u >= 0) ok = wait_bar_warp(bar(C::B_DPE), u & 1, ab);  // dP of unit u is in registers
-        ok = ok && wait_bar_warp(bar(C::B_VF + v.slot), v.parity, ab);
+        ok = ok && wait_bar_warp(v_bar, v_par, ab);
         if (!ok) break;
         tc_fence_after();
-        mma_channels<C::BOXES>(tb + C::T_DP, dd, v_k + v.slot * kTileStep, id_s, a.kd);
+        mma_channels<C::BOXES>(tb + C::T_DP, dd, dp_b, id_s, a.kd);
         mma_commit_e(bar(C::B_DP));
-        mma_commit_e(bar(C::B_VE + v.slot));
-        if (end1) mma_commit_e(bar(C::B_QE));
-        v.next();
+        mma_commit_e(ve_bar);
+        if (last1) mma_commit_e(bar(C::B_QE));
       }
+      const uint64_t dq_b2 = dq_b1;
+      const uint32_t ke_bar2 = ke_bar1;
+      k.next();
+      v.next();
+      s_b = k_k + k.slot * kTileStep;
+      dp_b = v_k + v.slot * kTileStep;
+      dq_b1 = k_mn + k.slot * kTileStep;
+      k_bar = bar(full + k.slot);
+      v_bar = bar(C::B_VF + v.slot);
+      ke_bar1 = bar(C::B_KE + k.slot);
+      ve_bar = bar(C::B_VE + v.slot);
+      k_par = k.parity;
+      v_par = v.parity;
+      if (u + 2 < n) next.step(a.sc);
+      pin(s_b, dp_b, dq_b1, dq_b);
+      pin(k_bar, v_bar, ke_bar1, ve_bar);
       if (u >= 0) {
-        ok = wait_bar_warp(bar(C::B_DS), u & 1, ab);
+        ok = wait_bar_warp(bar(C::B_DS + (u & 1)), (u >> 1) & 1, ab);
         if (!ok) break;
         tc_fence_after();
-        mma_rows(tb + C::T_DQ, tb + C::T_S + 128 * (u & 1), k_mn + k_slot * kTileStep, id_o, first);
-        mma_commit_e(bar(C::B_KE + k_slot));
+        mma_rows(tb + C::T_DQ, tb + C::T_S + 128 * (u & 1), dq_b, id_o, first);
+        mma_commit_e(ke_bar);
         if (last) mma_commit_e(bar(C::B_ACC));
       }
-      k_slot = k.slot;
-      k.next();
-      first = begin1;
-      last = end1;
-      if (u + 2 < n) ahead(u + 2);
+      dq_b = dq_b2;
+      ke_bar = ke_bar2;
+      first = first1;
+      last = last1;
     }
     mma_commit_e(bar(C::B_DONE));
     if (lane == 0) drain_bar(bar(C::B_DONE), 0);
@@ -637,7 +682,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         tmem_st16(ts, pk);
         tmem_wait_st();
         tc_fence_before();
-        warp_arrive(bar(C::B_DS));
+        warp_arrive(bar(C::B_DS + (u & 1)));
         p.next(a.sc);
       }
       if (!ok) break;
@@ -665,30 +710,24 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 }
 
 // ================================================================ partial results
-// The sum of R rows' partial results first, first + stride, ... (row r0 of dQ; of dV, then dK), as in the
-// forward's join.
-template <int R>
-__device__ __forceinline__ void join_sum(const CBwdArgs &a, const CrossJoin &j, int rows, int r0, int first, int stride, float4 (&acc)[R]) {
+// The sum of row r's partial results first, first + stride, ... (a row of dQ; of dV, then dK), as in the forward's join.
+__device__ __forceinline__ float4 join_sum(const CBwdArgs &a, const CrossJoin &j, int rows, int r, int first, int stride) {
   const int lane = threadIdx.x & 31, pitch = 16 * a.kd;
-#pragma unroll
-  for (int x = 0; x < R; ++x) acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (4 * lane >= pitch) return;
-  constexpr int N = R == 4 ? 2 : 8;  // partial results in flight
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (4 * lane >= pitch) return acc;
+  constexpr int N = 8;  // partial results in flight
   for (int c0 = first; c0 < j.count; c0 += N * stride) {
-    float4 v[N][R];
+    float4 v[N];
 #pragma unroll
     for (int n = 0; n < N; ++n) {
       const int c = c0 + n * stride;
-      const float *base = a.part + ((int64_t)j.slot[min(c, j.count - 1)] * rows + r0) * pitch + 4 * lane;
-#pragma unroll
-      for (int x = 0; x < R; ++x)
-        v[n][x] = c < j.count ? *reinterpret_cast<const float4 *>(base + x * pitch) : make_float4(0.f, 0.f, 0.f, 0.f);
+      v[n] = c < j.count ? *reinterpret_cast<const float4 *>(a.part + ((int64_t)j.slot[c] * rows + r) * pitch + 4 * lane)
+                         : make_float4(0.f, 0.f, 0.f, 0.f);
     }
 #pragma unroll
-    for (int n = 0; n < N; ++n)
-#pragma unroll
-      for (int x = 0; x < R; ++x) acc[x].x += v[n][x].x, acc[x].y += v[n][x].y, acc[x].z += v[n][x].z, acc[x].w += v[n][x].w;
+    for (int n = 0; n < N; ++n) acc.x += v[n].x, acc.y += v[n].y, acc.z += v[n].z, acc.w += v[n].w;
   }
+  return acc;
 }
 
 __device__ __forceinline__ void join_store(const CBwdArgs &a, const CrossPos &p, int r, const float4 &v) {
@@ -706,40 +745,46 @@ __device__ __forceinline__ void join_store(const CBwdArgs &a, const CrossPos &p,
   if (4 * lane < a.d) *reinterpret_cast<uint2 *>(out + 4 * lane) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
 }
 
-__global__ void __launch_bounds__(256, 4) cross_join_kernel(const CBwdArgs a, int ctas) {
+__global__ void __launch_bounds__(kJoinThreads, 2) cross_join_kernel(const CBwdArgs a, int ctas) {
+  constexpr int W = kJoinThreads / 32;
   __shared__ CrossJoin j;
-  __shared__ float4 acc_s[8][32];
+  __shared__ float4 acc_s[W][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   allow_next_kernel();
   const bool work = cross_join_setup(a.sc, ctas, j);
   wait_previous_kernel();  // (every block: the next kernel of the stream relies on this one's end alone)
   if (!work) return;
   const int rows = (a.sc.by_keys ? 2 : 1) * kTile;
-  if (j.count <= kJoinFew) {
-    for (int r = j.block * 32 + 4 * warp; r < rows; r += j.blocks * 32) {
-      float4 acc[4];
-      join_sum<4>(a, j, rows, r, 0, 1, acc);
+  if (j.count == 2) {  // (the usual case)
+    const int pitch = 16 * a.kd;
+    const bool has = 4 * lane < pitch;
+    for (int r = 4 * (j.block * W + warp); r < rows; r += 4 * W * j.blocks) {
+      float4 v0[4], v1[4];
 #pragma unroll
-      for (int x = 0; x < 4; ++x) join_store(a, j.pos, r + x, acc[x]);
+      for (int x = 0; x < 4; ++x) {
+        v0[x] = v1[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (has) {
+          v0[x] = *reinterpret_cast<const float4 *>(a.part + ((int64_t)j.slot[0] * rows + r + x) * pitch + 4 * lane);
+          v1[x] = *reinterpret_cast<const float4 *>(a.part + ((int64_t)j.slot[1] * rows + r + x) * pitch + 4 * lane);
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        join_store(a, j.pos, r + x, make_float4(v0[x].x + v1[x].x, v0[x].y + v1[x].y, v0[x].z + v1[x].z, v0[x].w + v1[x].w));
     }
   } else if (j.count <= kJoinMany) {
-    for (int r = j.block * 8 + warp; r < rows; r += j.blocks * 8) {
-      float4 acc[1];
-      join_sum<1>(a, j, rows, r, 0, 1, acc);
-      join_store(a, j.pos, r, acc[0]);
-    }
+    for (int r = j.block * W + warp; r < rows; r += W * j.blocks) join_store(a, j.pos, r, join_sum(a, j, rows, r, 0, 1));
   } else {
     for (int r = j.block; r < rows; r += j.blocks) {
-      float4 acc[1];
-      join_sum<1>(a, j, rows, r, warp, 8, acc);
-      acc_s[warp][lane] = acc[0];
+      float4 acc = join_sum(a, j, rows, r, warp, W);
+      acc_s[warp][lane] = acc;
       __syncthreads();
       if (warp == 0) {
-        for (int y = 1; y < 8; ++y) {
+        for (int y = 1; y < W; ++y) {
           const float4 v = acc_s[y][lane];
-          acc[0].x += v.x, acc[0].y += v.y, acc[0].z += v.z, acc[0].w += v.w;
+          acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
         }
-        join_store(a, j.pos, r, acc[0]);
+        join_store(a, j.pos, r, acc);
       }
       __syncthreads();
     }
@@ -787,13 +832,13 @@ cudaError_t launch_bwd(const CUtensorMap &mq, const CUtensorMap &mdo, const CUte
   }
   cudaError_t e = launch_after(cross_dkv_kernel<DP>, dim3(g.dkv_ctas), dim3(kBwdThreads), CDkv<DP>::SMEM, st, mq, mdo, mk, mv, dkv);
   if (e == cudaSuccess && g.dkv_split && g.dkv_ctas > 1) {
-    e = launch_after(cross_join_kernel, dim3(g.dkv_ctas - 1, 4), dim3(256), 0, st, dkv, g.dkv_ctas);
+    e = launch_after(cross_join_kernel, dim3(g.dkv_ctas - 1, 2), dim3(kJoinThreads), 0, st, dkv, g.dkv_ctas);
   }
   if (e == cudaSuccess) {
     e = launch_after(cross_dq_kernel<DP>, dim3(g.dq_ctas), dim3(kBwdThreads), CDq<DP>::SMEM, st, mq, mdo, mk, mv, dq);
   }
   if (e == cudaSuccess && g.dq_split && g.dq_ctas > 1) {
-    e = launch_after(cross_join_kernel, dim3(g.dq_ctas - 1, 2), dim3(256), 0, st, dq, g.dq_ctas);
+    e = launch_after(cross_join_kernel, dim3(g.dq_ctas - 1, 2), dim3(kJoinThreads), 0, st, dq, g.dq_ctas);
   }
   return e;
 }

@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(CFwd<DP>::NTHREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tb = misc[0];
-  const CrossShare share = *reinterpret_cast<const CrossShare *>(sm + C::OFF_SHARE);
+  const CrossShare &share = *reinterpret_cast<const CrossShare *>(sm + C::OFF_SHARE);
   const int n = share.n;
   // ring positions of unit u: K at 2 u, V at 2 u + 1
   auto stage = [&](int x) { return sb0 + C::OFF_RING + (uint32_t)(x % C::NST) * C::TILE; };
@@ -545,66 +545,73 @@ __device__ __forceinline__ void join_add(float &m, float &l, float4 &acc, float 
   m = m1;
 }
 
-// R rows of an item (four at most from row r0 on, of one tile): the sum over the partial results
-// first, first + stride, ...
-template <int R>
-struct JoinRows {
-  float4 acc[R];
-  float m[R], l[R];
-  __device__ __forceinline__ void add(const CFwdArgs &a, const CrossJoin &j, int r0, int first, int stride) {
-    const int lane = threadIdx.x & 31, pitch = 16 * a.kd, tile = kTile * (pitch + 4);
-    const int i = r0 / kTile, row = r0 % kTile;
-#pragma unroll
-    for (int x = 0; x < R; ++x) {
-      acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-      m[x] = -INFINITY;
-      l[x] = 0.f;
-    }
-    constexpr int N = R == 4 ? 2 : 8;  // partial results in flight
-    for (int c0 = first; c0 < j.count; c0 += N * stride) {
-      float4 v[N][R];
-      float lse[N][R];
-#pragma unroll
-      for (int n = 0; n < N; ++n) {
-        const int c = c0 + n * stride;
-        const float *base = a.part + (int64_t)j.slot[min(c, j.count - 1)] * (a.two * tile) + (int64_t)i * tile;
-#pragma unroll
-        for (int x = 0; x < R; ++x) {
-          const bool has = c < j.count;
-          lse[n][x] = has ? base[kTile * pitch + row + x] : -INFINITY;
-          v[n][x] = has && 4 * lane < pitch ? *reinterpret_cast<const float4 *>(base + (row + x) * pitch + 4 * lane)
-                                            : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-      }
-      // (rows past T hold nothing: whatever comes out for them is not written)
-#pragma unroll
-      for (int n = 0; n < N; ++n)
-#pragma unroll
-        for (int x = 0; x < R; ++x) join_add(m[x], l[x], acc[x], lse[n][x], 1.f, v[n][x]);
-    }
-  }
-  __device__ __forceinline__ void store(const CFwdArgs &a, const CrossPos &p, int r0) const {
-    const int lane = threadIdx.x & 31, i = r0 / kTile, row = r0 % kTile;
-    const RowTile rt = row_tile(a, p.item, i);
-#pragma unroll
-    for (int x = 0; x < R; ++x) {
-      const int t = rt.t0 + ((row + x) >> a.lg), h = rt.head0 + ((row + x) & (a.GB - 1));
-      if (t >= a.T) continue;
-      const float inv = l[x] > 0.f ? 1.f / l[x] : 0.f;
-      if (4 * lane < a.d)
-        *reinterpret_cast<uint2 *>(a.O + (((int64_t)p.b * a.T + t) * a.H + h) * a.d + 4 * lane) =
-            make_uint2(pack_bf16x2(acc[x].x * inv, acc[x].y * inv), pack_bf16x2(acc[x].z * inv, acc[x].w * inv));
-      if (lane == 0)
-        a.LSE[((int64_t)p.b * a.H + h) * a.T + t] = l[x] > 0.f ? (m[x] + __log2f(l[x])) * kLn2 : -INFINITY;
-    }
-  }
-};
+// The result of a row r of an item: (l, m, acc) as join_add leaves them.
+__device__ __forceinline__ void join_store(const CFwdArgs &a, const CrossPos &p, int r, float m, float l, const float4 &acc) {
+  const int lane = threadIdx.x & 31, row = r % kTile;
+  const RowTile rt = row_tile(a, p.item, r / kTile);
+  const int t = rt.t0 + (row >> a.lg), h = rt.head0 + (row & (a.GB - 1));
+  if (t >= a.T) return;
+  const float inv = l > 0.f ? __fdividef(1.f, l) : 0.f;
+  if (4 * lane < a.d)
+    *reinterpret_cast<uint2 *>(a.O + (((int64_t)p.b * a.T + t) * a.H + h) * a.d + 4 * lane) =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+  if (lane == 0) a.LSE[((int64_t)p.b * a.H + h) * a.T + t] = l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
+}
 
-// Adds the partial results of the items that several CTAs share.
-__global__ void __launch_bounds__(256, 3) cross_fwd_join_kernel(const CFwdArgs a, int ctas) {
+// Four rows of an item of two partial results (the usual case): all loads in flight together.
+__device__ __forceinline__ void join_pair(const CFwdArgs &a, const CrossJoin &j, int r0) {
+  const int lane = threadIdx.x & 31, pitch = 16 * a.kd, tile = kTile * (pitch + 4), row = r0 % kTile;
+  const float *base0 = a.part + ((int64_t)j.slot[0] * a.two + r0 / kTile) * tile;
+  const float *base1 = a.part + ((int64_t)j.slot[1] * a.two + r0 / kTile) * tile;
+  const bool has = 4 * lane < pitch;
+  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+  float4 v0[4], v1[4];
+  const float4 l0 = *reinterpret_cast<const float4 *>(base0 + kTile * pitch + row);
+  const float4 l1 = *reinterpret_cast<const float4 *>(base1 + kTile * pitch + row);
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    v0[x] = has ? *reinterpret_cast<const float4 *>(base0 + (row + x) * pitch + 4 * lane) : zero;
+    v1[x] = has ? *reinterpret_cast<const float4 *>(base1 + (row + x) * pitch + 4 * lane) : zero;
+  }
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    float m = x == 0 ? l0.x : x == 1 ? l0.y : x == 2 ? l0.z : l0.w, l = 1.f;
+    join_add(m, l, v0[x], x == 0 ? l1.x : x == 1 ? l1.y : x == 2 ? l1.z : l1.w, 1.f, v1[x]);
+    join_store(a, j.pos, r0 + x, m, l, v0[x]);
+  }
+}
+
+// Row r of an item: the sum of the partial results first, first + stride, ...
+__device__ __forceinline__ void join_sum(const CFwdArgs &a, const CrossJoin &j, int r, int first, int stride, float &m, float &l,
+                                         float4 &acc) {
+  const int lane = threadIdx.x & 31, pitch = 16 * a.kd, tile = kTile * (pitch + 4), row = r % kTile;
+  acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  m = -INFINITY;
+  l = 0.f;
+  constexpr int N = 8;  // partial results in flight
+  for (int c0 = first; c0 < j.count; c0 += N * stride) {
+    float4 v[N];
+    float lse[N];
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int c = c0 + n * stride;
+      const float *base = a.part + ((int64_t)j.slot[min(c, j.count - 1)] * a.two + r / kTile) * tile;
+      lse[n] = c < j.count ? base[kTile * pitch + row] : -INFINITY;
+      v[n] = c < j.count && 4 * lane < pitch ? *reinterpret_cast<const float4 *>(base + row * pitch + 4 * lane)
+                                             : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int n = 0; n < N; ++n) join_add(m, l, acc, lse[n], 1.f, v[n]);
+  }
+}
+
+// Adds the partial results of the items that several CTAs share. (Rows past T hold nothing: whatever comes
+// out for them is not written.)
+__global__ void __launch_bounds__(kJoinThreads, 2) cross_fwd_join_kernel(const CFwdArgs a, int ctas) {
+  constexpr int W = kJoinThreads / 32;
   __shared__ CrossJoin j;
-  __shared__ float4 acc_s[8][32];
-  __shared__ float2 ml_s[8];
+  __shared__ float4 acc_s[W][32];
+  __shared__ float2 ml_s[W];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const bool work = cross_join_setup(a.sc, ctas, j);
   wait_previous_kernel();  // (every block: the next kernel of the stream relies on this one's end alone)
@@ -612,28 +619,24 @@ __global__ void __launch_bounds__(256, 3) cross_fwd_join_kernel(const CFwdArgs a
   // rows that hold queries: the first tile's, and the second one's if it is live
   const RowTile r0 = row_tile(a, j.pos.item, 0), r1 = row_tile(a, j.pos.item, 1);
   const int rows = r1.live ? kTile + min(kTile, (a.T - r1.t0) << a.lg) : min(kTile, (a.T - r0.t0) << a.lg);
-  if (j.count <= kJoinFew) {
-    for (int r = j.block * 32 + 4 * warp; r < rows; r += j.blocks * 32) {
-      JoinRows<4> x;
-      x.add(a, j, r, 0, 1);
-      x.store(a, j.pos, r);
-    }
+  float m, l;
+  float4 acc;
+  if (j.count == 2) {
+    for (int r = 4 * (j.block * W + warp); r < rows; r += 4 * W * j.blocks) join_pair(a, j, r);
   } else if (j.count <= kJoinMany) {
-    for (int r = j.block * 8 + warp; r < rows; r += j.blocks * 8) {
-      JoinRows<1> x;
-      x.add(a, j, r, 0, 1);
-      x.store(a, j.pos, r);
+    for (int r = j.block * W + warp; r < rows; r += W * j.blocks) {
+      join_sum(a, j, r, 0, 1, m, l, acc);
+      join_store(a, j.pos, r, m, l, acc);
     }
   } else {
     for (int r = j.block; r < rows; r += j.blocks) {
-      JoinRows<1> x;
-      x.add(a, j, r, warp, 8);
-      acc_s[warp][lane] = x.acc[0];
-      if (lane == 0) ml_s[warp] = make_float2(x.m[0], x.l[0]);
+      join_sum(a, j, r, warp, W, m, l, acc);
+      acc_s[warp][lane] = acc;
+      if (lane == 0) ml_s[warp] = make_float2(m, l);
       __syncthreads();
       if (warp == 0) {
-        for (int y = 1; y < 8; ++y) join_add(x.m[0], x.l[0], x.acc[0], ml_s[y].x, ml_s[y].y, acc_s[y][lane]);
-        x.store(a, j.pos, r);
+        for (int y = 1; y < W; ++y) join_add(m, l, acc, ml_s[y].x, ml_s[y].y, acc_s[y][lane]);
+        join_store(a, j.pos, r, m, l, acc);
       }
       __syncthreads();
     }
@@ -751,7 +754,7 @@ int tri_cross_fwd(tri_cross_shape shape, const tri_attn_bf16 *Q, const tri_attn_
   const auto st = static_cast<cudaStream_t>(stream);
   cudaError_t e = shape.d <= 64 ? launch_fwd<64>(mq, mk, mv, a, g.ctas, dev, st) : launch_fwd<128>(mq, mk, mv, a, g.ctas, dev, st);
   if (e == cudaSuccess && g.split && g.ctas > 1) {
-    e = launch_after(cross_fwd_join_kernel, dim3(g.ctas - 1, g.two * 2), dim3(256), 0, st, a, g.ctas);
+    e = launch_after(cross_fwd_join_kernel, dim3(g.ctas - 1, g.two), dim3(kJoinThreads), 0, st, a, g.ctas);
   }
   return e == cudaSuccess ? TRI_ATTN_OK : TRI_ATTN_ERR_CUDA;
 }
