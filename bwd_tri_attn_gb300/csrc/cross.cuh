@@ -276,6 +276,13 @@ __device__ __forceinline__ void mma_channels(uint32_t d, uint64_t a, uint64_t b,
   if (BOXES > 1 && kd > 4) sm100::mma_ss_box_e(d, a + kBoxStep, b + kBoxStep, idesc, kd - 4, 1u);
 }
 
+// The same with the first operand in TMEM, BF16 pairs, 8 columns a step.
+template <int BOXES>
+__device__ __forceinline__ void mma_channels_t(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, int kd) {
+  sm100::mma_ts_box_e(d, a, b, idesc, kd, 0u);
+  if (BOXES > 1 && kd > 4) sm100::mma_ts_box_e(d, a + 32u, b + kBoxStep, idesc, kd - 4, 1u);
+}
+
 // A place in a ring of N slots and the phase parity of its barriers.
 template <int N>
 struct Ring {

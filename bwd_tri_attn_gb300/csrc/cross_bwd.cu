@@ -440,12 +440,14 @@ struct CDq {
   static constexpr int BOXES = DP / 64, TILE = BOXES * kBoxBytes;
   static constexpr int NK = DP == 128 ? 3 : 6, NV = DP == 128 ? 2 : 4;
   static constexpr int OFF_K = 2 * TILE, OFF_V = OFF_K + NK * TILE, OFF_BAR = OFF_V + NV * TILE;
-  static constexpr int B_KF = 0, B_KE = NK, B_KC = 2 * NK, B_VF = 3 * NK, B_VE = B_VF + NV, B_QF = B_VE + NV, B_QE = B_QF + 1,
-                       B_S = B_QE + 1, B_DP = B_S + 2, B_DPE = B_DP + 1, B_DS = B_DPE + 1, B_ACC = B_DS + 2,
-                       B_DONE = B_ACC + 1, NBAR = B_DONE + 1;
+  static constexpr int B_KF = 0, B_KE = NK, B_KC = 2 * NK, B_VF = 3 * NK, B_VE = B_VF + NV, B_QF = B_VE + NV,
+                       B_S = B_QF + 1, B_DP = B_S + 1, B_ACC = B_DP + 1, B_DONE = B_ACC + 1,
+                       B_QE = B_DONE + 1, B_QT = B_QE + 1, B_SE = B_QT + 1, B_DS = B_SE + 1, NBAR = B_DS + 1;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8, OFF_SHARE = OFF_MISC + 16;
   static constexpr int SMEM = OFF_SHARE + (int)sizeof(CrossShare) + 1024;
-  static constexpr int T_S = 0, T_DP = 256, T_DQ = 384;  // (S twice: units in turn, and B_S, B_DS with it)
+  // S, dP (and dS over it), dQ; Q and dO of the run as BF16 pairs: as first operands in shared memory they
+  // would take two thirds of its reads, which a product of 128 x 128 from there needs all
+  static constexpr int T_S = 0, T_DP = 128, T_DQ = 256, T_Q = 384, T_DO = 448;
   static_assert(SMEM <= 227 * 1024 && OFF_SHARE % 4 == 0, "shared memory");
 };
 
@@ -463,7 +465,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   volatile uint32_t *misc = reinterpret_cast<volatile uint32_t *>(sm + C::OFF_MISC);
   const Abort ab{reinterpret_cast<volatile int *>(misc + 1), a.sc.status};
   if (threadIdx.x == 0) {
-    for (int k = 0; k < C::NBAR; ++k) mbar_init(bar(k), k >= C::B_DPE && k < C::B_ACC ? kEw : 1);
+    for (int k = 0; k < C::NBAR; ++k) mbar_init(bar(k), k >= C::B_QE ? kEw : 1);
     misc[1] = 0;
     fence_barrier_init();
   }
@@ -561,8 +563,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     // ------------------------------------------------------------ MMA issuer (whole warp, elect.sync)
     const uint32_t id_s = idesc_f16(128, 128, true, true, false, false);
     const uint32_t id_o = idesc_f16(128, 16, true, true, false, true) + ((uint32_t)(2 * (a.kd - 1)) << 17);
-    const uint64_t dq = desc_k(sb0), dd = desc_k(sb0 + C::TILE), k_k = desc_k(sb0 + C::OFF_K), k_mn = desc_mn(sb0 + C::OFF_K),
-                   v_k = desc_k(sb0 + C::OFF_V);
+    const uint64_t k_k = desc_k(sb0 + C::OFF_K), k_mn = desc_mn(sb0 + C::OFF_K), v_k = desc_k(sb0 + C::OFF_V);
     constexpr uint64_t kTileStep = C::TILE >> 4;
     const int full = a.clean ? C::B_KC : C::B_KF;
     UnitAhead next(share, a.sc);  // of unit u + 1
@@ -575,33 +576,45 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     uint32_t ke_bar = 0, first = 0, last = 0;
     int runs = 0;
     bool ok = true;
-    // Round u: S and dP of unit u + 1 while the warps work on dS of unit u, then dQ of unit u. (S of u + 1
-    // takes the columns of S and dS of unit u - 1, whose dQ is issued. The warps may be done with dS of u + 1
-    // before dS of u is waited for here, if this warp is held up: hence two barriers.) What the next round needs to know is
-    // worked out before the wait for dS, as in cross_dkv_kernel.
+    auto s_of_next = [&] {
+      ok = ok && wait_bar_warp(k_bar, k_par, ab);
+      if (!ok) return;
+      tc_fence_after();
+      mma_channels_t<C::BOXES>(tb + C::T_S, tb + C::T_Q, s_b, id_s, a.kd);
+      mma_commit_e(bar(C::B_S));
+    };
+    // Round u: S of unit u + 1 as soon as that of unit u is in registers; dQ of unit u when dS is there; dP of
+    // unit u + 1 (its columns are dS's) while the warps work on P. What the next round needs to know is
+    // worked out before the waits for what the warps do, as in cross_dkv_kernel.
 #pragma unroll 1
     for (int u = -1; u < n; ++u) {
+      const bool more = u + 1 < n;
       const uint32_t first1 = next.first, last1 = next.last;
-      if (u + 1 < n) {
-        const int odd = (u + 1) & 1;
-        if (first1) {
-          ok = wait_bar_warp(bar(C::B_QF), runs & 1, ab);
-          if (!ok) break;
-          ++runs;
-        }
-        ok = wait_bar_warp(k_bar, k_par, ab);
+      if (more && !first1) {
+        ok = wait_bar_warp(bar(C::B_SE), u & 1, ab);
+        s_of_next();
+        if (!ok) break;
+      }
+      if (u >= 0) {
+        ok = wait_bar_warp(bar(C::B_DS), u & 1, ab);
         if (!ok) break;
         tc_fence_after();
-        mma_channels<C::BOXES>(tb + C::T_S + 128 * odd, dq, s_b, id_s, a.kd);
-        mma_commit_e(bar(C::B_S + odd));
-        if (u >= 0) ok = wait_bar_warp(bar(C::B_DPE), u & 1, ab);  // dP of unit u is in registers
+        mma_rows(tb + C::T_DQ, tb + C::T_DP, dq_b, id_o, first);
+        mma_commit_e(ke_bar);
+        if (last) mma_commit_e(bar(C::B_ACC));
+      }
+      if (more) {
+        if (first1) {  // (Q and dO are in TMEM)
+          ok = wait_bar_warp(bar(C::B_QT), runs & 1, ab);
+          ++runs;
+          s_of_next();
+        }
         ok = ok && wait_bar_warp(v_bar, v_par, ab);
         if (!ok) break;
         tc_fence_after();
-        mma_channels<C::BOXES>(tb + C::T_DP, dd, dp_b, id_s, a.kd);
+        mma_channels_t<C::BOXES>(tb + C::T_DP, tb + C::T_DO, dp_b, id_s, a.kd);
         mma_commit_e(bar(C::B_DP));
         mma_commit_e(ve_bar);
-        if (last1) mma_commit_e(bar(C::B_QE));
       }
       const uint64_t dq_b2 = dq_b1;
       const uint32_t ke_bar2 = ke_bar1;
@@ -617,17 +630,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       k_par = k.parity;
       v_par = v.parity;
       if (u + 2 < n) next.step(a.sc);
+      dq_b = dq_b2;
       pin(s_b, dp_b, dq_b1, dq_b);
       pin(k_bar, v_bar, ke_bar1, ve_bar);
-      if (u >= 0) {
-        ok = wait_bar_warp(bar(C::B_DS + (u & 1)), (u >> 1) & 1, ab);
-        if (!ok) break;
-        tc_fence_after();
-        mma_rows(tb + C::T_DQ, tb + C::T_S + 128 * (u & 1), dq_b, id_o, first);
-        mma_commit_e(ke_bar);
-        if (last) mma_commit_e(bar(C::B_ACC));
-      }
-      dq_b = dq_b2;
       ke_bar = ke_bar2;
       first = first1;
       last = last1;
@@ -639,11 +644,35 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     // ------------------------------------------------------------ dS, thread = query row, 32 keys a warpgroup
     const int part4 = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t tdp = tb + lanes + C::T_DP + 32 * part4;
+    const uint32_t ts = tb + lanes + C::T_S + 32 * part4, tdp = tb + lanes + C::T_DP + 32 * part4;
     CrossPos p = share.pos;
     bool ok = true;
     int runs = 0;
     const float2 c2 = make_float2(a.c, a.c);
+    // Q and dO of run q, which has begun, into TMEM: 32 channels a warpgroup, 16-byte chunks where TMA's
+    // swizzle put them
+    auto copy_q = [&](int q) {
+      ok = wait_bar_warp(bar(C::B_QF), q & 1, ab);
+      if (!ok) return;
+      if (32 * part4 < 64 * C::BOXES) {
+        const uint8_t *src = sm + (part4 >> 1) * kBoxBytes + row * 128;
+#pragma unroll
+        for (int o = 0; o < 2; ++o) {
+          uint32_t w[16];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(src + o * C::TILE + (((4 * (part4 & 1) + x) ^ (row & 7)) * 16));
+            w[4 * x] = v.x, w[4 * x + 1] = v.y, w[4 * x + 2] = v.z, w[4 * x + 3] = v.w;
+          }
+          tmem_st16(tb + lanes + (o ? C::T_DO : C::T_Q) + 16 * part4, w);
+        }
+        tmem_wait_st();
+      }
+      tc_fence_before();
+      warp_arrive(bar(C::B_QT));
+      if (lane == 0) mbar_arrive(bar(C::B_QE));
+    };
+    if (n > 0) copy_q(0);
     for (int u = 0; u < n && ok; ++runs) {
       const CrossRun run = cross_run(p, n - u);
       const int b = p.b, hb = p.item / a.tiles, mt = p.item % a.tiles, len = a.sc.len(b);
@@ -655,22 +684,28 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const int key = p.k * kTile + 32 * part4 + lane;
         const bool all = !a.mask && key - lane + 32 <= len;
         const bool live = all || (key < len && (!a.mask || __ldg(a.mask + (int64_t)b * a.sc.S + key) != 0));
-        const uint32_t ts = tb + lanes + C::T_S + 128 * (u & 1) + 32 * part4;
-        ok = wait_bar_warp(bar(C::B_DP), u & 1, ab) && wait_bar_warp(bar(C::B_S + (u & 1)), (u >> 1) & 1, ab);
+        ok = wait_bar_warp(bar(C::B_S), u & 1, ab);
         if (!ok) break;
         tc_fence_after();
-        uint32_t dp[32], s[32], pk[16];
-        tmem_ld32(tdp, dp);
+        float2 pr[16];
+        uint32_t s[32], pk[16];
         tmem_ld32(ts, s);
-        tmem_wait_ld(dp);
         tmem_wait_ld(s);
         tc_fence_before();
-        warp_arrive(bar(C::B_DPE));
+        warp_arrive(bar(C::B_SE));
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
           const float2 y = __ffma2_rn(make_float2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), c2, nl2);
-          const float2 x = __fmul2_rn(make_float2(ex2(y.x), ex2(y.y)),
-                                      __fadd2_rn(make_float2(__uint_as_float(dp[2 * j]), __uint_as_float(dp[2 * j + 1])), nd2));
+          pr[j] = make_float2(ex2(y.x), ex2(y.y));
+        }
+        ok = wait_bar_warp(bar(C::B_DP), u & 1, ab);
+        if (!ok) break;
+        tc_fence_after();
+        tmem_ld32(tdp, s);
+        tmem_wait_ld(s);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const float2 x = __fmul2_rn(pr[j], __fadd2_rn(make_float2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), nd2));
           pk[j] = pack_bf16x2(x.x, x.y);
         }
         if (!all) {
@@ -679,13 +714,17 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           for (int j = 0; j < 16; ++j)
             pk[j] &= ((w >> (2 * j)) & 1u ? 0xffffu : 0u) | ((w >> (2 * j + 1)) & 1u ? 0xffff0000u : 0u);
         }
-        tmem_st16(ts, pk);
+        tmem_st16(tdp, pk);
         tmem_wait_st();
         tc_fence_before();
-        warp_arrive(bar(C::B_DS + (u & 1)));
+        warp_arrive(bar(C::B_DS));
         p.next(a.sc);
       }
       if (!ok) break;
+      if (u < n) {  // (the products with the old Q and dO have gone before dP of the run's last unit)
+        copy_q(runs + 1);
+        if (!ok) break;
+      }
       // the run's dQ: the warpgroups take 32 channels each
       ok = wait_bar_warp(bar(C::B_ACC), runs & 1, ab);
       if (!ok) break;

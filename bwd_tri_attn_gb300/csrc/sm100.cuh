@@ -551,6 +551,24 @@ __device__ __forceinline__ void mma_ss_box_e(uint32_t d_tmem, uint64_t a_desc, u
       : "memory");
 }
 
+// As mma_ss_box_e with A from TMEM (8 columns a step): min(steps, 4) MMAs.
+__device__ __forceinline__ void mma_ts_box_e(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, int steps,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, t, e, q;\n\t.reg .b32 a;\n\t.reg .b64 b;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\tsetp.eq.b32 t, 0, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+      "add.u32 a, %1, 8;\n\tadd.u64 b, %2, 2;\n\tsetp.gt.and.s32 q, %4, 1, e;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+      "add.u32 a, %1, 16;\n\tadd.u64 b, %2, 4;\n\tsetp.gt.and.s32 q, %4, 2, e;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+      "add.u32 a, %1, 24;\n\tadd.u64 b, %2, 6;\n\tsetp.gt.and.s32 q, %4, 3, e;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+      "}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(steps), "r"(accumulate)
+      : "memory");
+}
+
 // Four M=128 MMAs with A from TMEM (8 columns a step) and B from shared memory (b_step a step) into
 // one accumulator, as mma_ts_x8_e.
 __device__ __forceinline__ void mma_ts_x4_e(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint64_t b_step,
