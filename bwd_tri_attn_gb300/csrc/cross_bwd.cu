@@ -83,9 +83,10 @@ __global__ void __launch_bounds__(256) cross_bwd_prep_kernel(const CBwdArgs a, c
 }
 
 // ================================================================ shared pieces of the two main kernels
-// 32 columns of a thread's accumulator row, from column c0 on (at most 16 kd in all), times f (store_cols). The whole
-// warp calls it; rows with mine = false write nothing.
-__device__ __forceinline__ void store_row(uint32_t tm, int c0, const CBwdArgs &a, float f, bool mine, uint16_t *out, float *part) {
+// 32 columns of a thread's accumulator row, from column c0 on (at most 16 kd in all), times f (store_cols), zeros if the row is not
+// live. The whole warp calls it; rows with mine = false write nothing.
+__device__ __forceinline__ void store_row(uint32_t tm, int c0, const CBwdArgs &a, float f, bool live, bool mine, uint16_t *out,
+                                          float *part) {
   if (c0 >= 16 * a.kd) return;
   uint32_t o[32];
   tmem_ld32(tm + c0, o);
@@ -94,7 +95,7 @@ __device__ __forceinline__ void store_row(uint32_t tm, int c0, const CBwdArgs &a
   for (int h = 0; h < 2; ++h) {
     float v[16];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(o[16 * h + j]) * f;
+    for (int j = 0; j < 16; ++j) v[j] = live ? __uint_as_float(o[16 * h + j]) * f : 0.f;
     if (mine && c0 + 16 * h < 16 * a.kd) store_cols(v, c0 + 16 * h, a.d, a.wide, out, part);
   }
   __syncwarp();
@@ -364,8 +365,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     for (int u = 0; u < n && ok; ++runs) {
       const CrossRun run = cross_run(p, n - u);
       const int b = p.b, hk = p.item / p.nt, k0 = (p.item % p.nt) * kTile, key = k0 + row;
+      // (P and dS of a masked key are whatever they are: its row of the sums is its own, and zero when stored)
       const bool live = key < a.sc.len(b) && (!a.mask || __ldg(a.mask + (int64_t)b * a.sc.S + key) != 0);
-      const uint32_t keep = live ? ~0u : 0u;
       for (int k = 0; k < run.n; ++k, ++u) {
         const float4 *nl = reinterpret_cast<const float4 *>(sm + C::OFF_R + r.slot * 1024) + 8 * part4;
         const float4 *nd = nl + 32;
@@ -383,8 +384,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           const float2 y1 = __ffma2_rn(make_float2(__uint_as_float(s[4 * j + 2]), __uint_as_float(s[4 * j + 3])), c2, make_float2(l4.z, l4.w));
           pr[2 * j] = make_float2(ex2(y0.x), ex2(y0.y));
           pr[2 * j + 1] = make_float2(ex2(y1.x), ex2(y1.y));
-          pk[2 * j] = pack_bf16x2(pr[2 * j].x, pr[2 * j].y) & keep;
-          pk[2 * j + 1] = pack_bf16x2(pr[2 * j + 1].x, pr[2 * j + 1].y) & keep;
+          pk[2 * j] = pack_bf16x2(pr[2 * j].x, pr[2 * j].y);
+          pk[2 * j + 1] = pack_bf16x2(pr[2 * j + 1].x, pr[2 * j + 1].y);
         }
         tmem_st16(ts, pk);
         tmem_wait_st();
@@ -400,8 +401,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           const float4 d4 = nd[j];
           const float2 y0 = __fmul2_rn(pr[2 * j], __fadd2_rn(make_float2(__uint_as_float(s[4 * j]), __uint_as_float(s[4 * j + 1])), make_float2(d4.x, d4.y)));
           const float2 y1 = __fmul2_rn(pr[2 * j + 1], __fadd2_rn(make_float2(__uint_as_float(s[4 * j + 2]), __uint_as_float(s[4 * j + 3])), make_float2(d4.z, d4.w)));
-          pk[2 * j] = pack_bf16x2(y0.x, y0.y) & keep;
-          pk[2 * j + 1] = pack_bf16x2(y1.x, y1.y) & keep;
+          pk[2 * j] = pack_bf16x2(y0.x, y0.y);
+          pk[2 * j + 1] = pack_bf16x2(y1.x, y1.y);
         }
         tmem_st16(tdp, pk);
         tmem_wait_st();
@@ -421,7 +422,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       float *part = a.part + (((int64_t)max(run.slot, 0) * 2 + which) * kTile + row) * pitch;
 #pragma unroll 1
       for (int c0 = 32 * (part4 & 1); c0 < pitch; c0 += 64)
-        store_row(tb + lanes + (which ? C::T_DK : C::T_DV), c0, a, which ? a.scale : 1.f, key < a.sc.S,
+        store_row(tb + lanes + (which ? C::T_DK : C::T_DV), c0, a, which ? a.scale : 1.f, live, key < a.sc.S,
                   run.slot < 0 ? (which ? a.dK : a.dV) + off : nullptr, part);
       tc_fence_before();
     }
@@ -733,7 +734,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       // before it has ended. (What this kernel reads was complete before that one's predecessor read it.)
       if (runs == 0) wait_previous_kernel();
       const int t = mt * (kTile >> a.lg) + (row >> a.lg), h = hb * a.GB + (row & (a.GB - 1));
-      store_row(tb + lanes + C::T_DQ, 32 * part4, a, a.scale, t < a.T,
+      store_row(tb + lanes + C::T_DQ, 32 * part4, a, a.scale, true, t < a.T,
                 run.slot < 0 ? a.dQ + (((int64_t)b * a.T + t) * a.H + h) * a.d : nullptr,
                 a.part + ((int64_t)max(run.slot, 0) * kTile + row) * 16 * a.kd);
       tc_fence_before();
