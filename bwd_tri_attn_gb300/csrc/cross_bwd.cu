@@ -134,12 +134,28 @@ struct UnitAhead {
   }
 };
 
-// Keeps the work that leads to these values ahead of what follows.
-__device__ __forceinline__ void pin(uint64_t &a, uint64_t &b, uint64_t &c, uint64_t &d) {
-  asm volatile("" : "+l"(a), "+l"(b), "+l"(c), "+l"(d));
-}
-__device__ __forceinline__ void pin(uint32_t &a, uint32_t &b, uint32_t &c, uint32_t &d) {
-  asm volatile("" : "+r"(a), "+r"(b), "+r"(c), "+r"(d));
+// A place in a ring of N tiles as the issuing warp wants it: its offset in descriptors, its barrier (the
+// barrier that frees it is N further), the phase.
+template <int N>
+struct TileRing {
+  uint32_t off = 0, full, parity = 0;
+  __device__ __forceinline__ explicit TileRing(uint32_t full0) : full(full0) {}
+  __device__ __forceinline__ void next(uint32_t step) {
+    off += step;
+    full += 8u;
+    if (off == N * step) {
+      off = 0;
+      full -= 8u * N;
+      parity ^= 1u;
+    }
+  }
+};
+
+// Two waits, whose latencies (70 cycles and more, beside the other warps) overlap if both are over.
+__device__ __forceinline__ bool wait_two_warp(uint32_t b0, uint32_t p0, uint32_t b1, uint32_t p1, const Abort &ab) {
+  const bool ok0 = mbar_try_wait(b0, p0), ok1 = mbar_try_wait(b1, p1);
+  if (__all_sync(0xffffffffu, ok0 && ok1)) return true;
+  return wait_bar_warp(b0, p0, ab) && wait_bar_warp(b1, p1, ab);
 }
 
 // ================================================================ dK and dV
@@ -279,73 +295,62 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const uint32_t id_o = idesc_f16(128, 16, true, true, false, true) + ((uint32_t)(2 * (a.kd - 1)) << 17);
     const uint64_t dk = desc_k(sb0), dv = desc_k(sb0 + C::TILE), q_k = desc_k(sb0 + C::OFF_Q), q_mn = desc_mn(sb0 + C::OFF_Q),
                    d_k = desc_k(sb0 + C::OFF_D), d_mn = desc_mn(sb0 + C::OFF_D);
-    constexpr uint64_t kTileStep = C::TILE >> 4;
+    constexpr uint32_t kTileStep = C::TILE >> 4;
     UnitAhead next(share, a.sc);  // of unit u + 1
-    Ring<C::NQ> q;
-    Ring<C::ND> d;
-    uint64_t dv_b = 0, dk_b = 0;     // of unit u: dO and Q as the second operands,
-    uint32_t de_bar = 0, qe_bar = 0;  // the barriers that free them,
-    uint32_t first = 0, last = 0;     // whether it begins, ends its run
+    TileRing<C::NQ> q(bar(C::B_QF)), q0 = q;  // of unit u + 1, of unit u
+    TileRing<C::ND> d(bar(C::B_DF)), d0 = d;
+    uint32_t first = 0, last = 0;  // whether unit u begins, ends its run
     int runs = 0;
     bool ok = true;
     // Round u: dV of unit u and S^T of unit u + 1 (its columns are P's) while the warps work on dS; dK of
     // unit u and dP^T of unit u + 1 (its columns are dS's) while they work on the next P. Round -1: S^T
-    // and dP^T of unit 0. This warp gets few issue slots beside four element-wise ones, and between P's
-    // arrival and dV every instruction of it is waited for: all that a unit needs to know is worked out
-    // behind the dV before (512 cycles of the tensor cores), not at the round's end, where it cost 600 cycles of
-    // 2900 a unit.
+    // and dP^T of unit 0. The tensor cores' queue holds about four steps (256 cycles), and this warp gets few
+    // issue slots beside four element-wise ones: what stands between two products is kept short.
 #pragma unroll 1
     for (int u = -1; u < n; ++u) {
+      const bool more = u + 1 < n;
       if (u >= 0) {
-        ok = wait_bar_warp(bar(C::B_P), u & 1, ab);
+        ok = more ? wait_two_warp(bar(C::B_P), u & 1, q.full, q.parity, ab) : wait_bar_warp(bar(C::B_P), u & 1, ab);
         if (!ok) break;
         tc_fence_after();
-        mma_rows(tb + C::T_DV, tb + C::T_S, dv_b, id_o, first);
+        mma_rows(tb + C::T_DV, tb + C::T_S, d_mn + d0.off, id_o, first);
+      } else if (more) {
+        ok = wait_bar_warp(q.full, q.parity, ab);
       }
-      const bool more = u + 1 < n;
-      uint64_t s_b = q_k + q.slot * kTileStep, dp_b = d_k + d.slot * kTileStep, dv_b1 = d_mn + d.slot * kTileStep,
-               dk_b1 = q_mn + q.slot * kTileStep;
-      const uint32_t qf_bar = bar(C::B_QF + q.slot), df_bar = bar(C::B_DF + d.slot), q_par = q.parity, d_par = d.parity;
-      uint32_t de_bar1 = bar(C::B_DE + d.slot), qe_bar1 = bar(C::B_QE + q.slot);
       const uint32_t first1 = next.first, last1 = next.last;
-      q.next();
-      d.next();
-      if (u + 2 < n) next.step(a.sc);
-      pin(s_b, dp_b, dv_b1, dk_b1);
-      pin(de_bar1, qe_bar1, next.first, next.last);
       if (more) {
         if (first1) {
-          ok = wait_bar_warp(bar(C::B_KF), runs & 1, ab);
-          if (!ok) break;
+          ok = ok && wait_bar_warp(bar(C::B_KF), runs & 1, ab);
           ++runs;
         }
-        ok = wait_bar_warp(qf_bar, q_par, ab);
         if (!ok) break;
         tc_fence_after();
-        mma_channels<C::BOXES>(tb + C::T_S, dk, s_b, id_s, a.kd);
+        mma_channels<C::BOXES>(tb + C::T_S, dk, q_k + q.off, id_s, a.kd);
         mma_commit_e(bar(C::B_S));
       }
+      if (u >= 0) mma_commit_e(d0.full + 8 * C::ND);
+      if (u + 2 < n) next.step(a.sc);
       if (u >= 0) {
-        mma_commit_e(de_bar);
-        ok = wait_bar_warp(bar(C::B_DS), u & 1, ab);
+        ok = more ? wait_two_warp(bar(C::B_DS), u & 1, d.full, d.parity, ab) : wait_bar_warp(bar(C::B_DS), u & 1, ab);
         if (!ok) break;
         tc_fence_after();
-        mma_rows(tb + C::T_DK, tb + C::T_DP, dk_b, id_o, first);
+        mma_rows(tb + C::T_DK, tb + C::T_DP, q_mn + q0.off, id_o, first);
         if (last) mma_commit_e(bar(C::B_ACC));
+      } else if (more) {
+        ok = wait_bar_warp(d.full, d.parity, ab);
       }
       if (more) {
-        ok = wait_bar_warp(df_bar, d_par, ab);
         if (!ok) break;
         tc_fence_after();
-        mma_channels<C::BOXES>(tb + C::T_DP, dv, dp_b, id_s, a.kd);
+        mma_channels<C::BOXES>(tb + C::T_DP, dv, d_k + d.off, id_s, a.kd);
         mma_commit_e(bar(C::B_DP));
         if (last1) mma_commit_e(bar(C::B_KE));
       }
-      if (u >= 0) mma_commit_e(qe_bar);
-      dv_b = dv_b1;
-      dk_b = dk_b1;
-      de_bar = de_bar1;
-      qe_bar = qe_bar1;
+      if (u >= 0) mma_commit_e(q0.full + 8 * C::NQ);
+      q0 = q;
+      d0 = d;
+      q.next(kTileStep);
+      d.next(kTileStep);
       first = first1;
       last = last1;
     }
@@ -565,76 +570,57 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const uint32_t id_s = idesc_f16(128, 128, true, true, false, false);
     const uint32_t id_o = idesc_f16(128, 16, true, true, false, true) + ((uint32_t)(2 * (a.kd - 1)) << 17);
     const uint64_t k_k = desc_k(sb0 + C::OFF_K), k_mn = desc_mn(sb0 + C::OFF_K), v_k = desc_k(sb0 + C::OFF_V);
-    constexpr uint64_t kTileStep = C::TILE >> 4;
+    constexpr uint32_t kTileStep = C::TILE >> 4;
     const int full = a.clean ? C::B_KC : C::B_KF;
     UnitAhead next(share, a.sc);  // of unit u + 1
-    Ring<C::NK> k;
-    Ring<C::NV> v;
-    uint64_t s_b = k_k, dp_b = v_k, dq_b1 = k_mn;  // of unit u + 1: K, V, and K as dQ's second operand,
-    uint32_t k_bar = bar(full), v_bar = bar(C::B_VF), ke_bar1 = bar(C::B_KE), ve_bar = bar(C::B_VE);  // their barriers
-    uint32_t k_par = 0, v_par = 0;
-    uint64_t dq_b = 0;  // of unit u
-    uint32_t ke_bar = 0, first = 0, last = 0;
+    TileRing<C::NK> k(bar(full)), k0 = k;  // of unit u + 1, of unit u
+    TileRing<C::NV> v(bar(C::B_VF));
+    const uint32_t k_free = bar(C::B_KE) - bar(full);
+    uint32_t first = 0, last = 0;  // whether unit u begins, ends its run
     int runs = 0;
     bool ok = true;
-    auto s_of_next = [&] {
-      ok = ok && wait_bar_warp(k_bar, k_par, ab);
-      if (!ok) return;
-      tc_fence_after();
-      mma_channels_t<C::BOXES>(tb + C::T_S, tb + C::T_Q, s_b, id_s, a.kd);
-      mma_commit_e(bar(C::B_S));
-    };
     // Round u: S of unit u + 1 as soon as that of unit u is in registers; dQ of unit u when dS is there; dP of
-    // unit u + 1 (its columns are dS's) while the warps work on P. What the next round needs to know is
-    // worked out before the waits for what the warps do, as in cross_dkv_kernel.
+    // unit u + 1 (its columns are dS's) while the warps work on P.
 #pragma unroll 1
     for (int u = -1; u < n; ++u) {
       const bool more = u + 1 < n;
-      const uint32_t first1 = next.first, last1 = next.last;
+      const uint32_t first1 = next.first;
       if (more && !first1) {
-        ok = wait_bar_warp(bar(C::B_SE), u & 1, ab);
-        s_of_next();
-        if (!ok) break;
-      }
-      if (u >= 0) {
-        ok = wait_bar_warp(bar(C::B_DS), u & 1, ab);
+        ok = wait_two_warp(bar(C::B_SE), u & 1, k.full, k.parity, ab);
         if (!ok) break;
         tc_fence_after();
-        mma_rows(tb + C::T_DQ, tb + C::T_DP, dq_b, id_o, first);
-        mma_commit_e(ke_bar);
+        mma_channels_t<C::BOXES>(tb + C::T_S, tb + C::T_Q, k_k + k.off, id_s, a.kd);
+        mma_commit_e(bar(C::B_S));
+      }
+      const uint32_t last1 = next.last;
+      if (u + 2 < n) next.step(a.sc);
+      if (u >= 0) {
+        ok = more ? wait_two_warp(bar(C::B_DS), u & 1, v.full, v.parity, ab) : wait_bar_warp(bar(C::B_DS), u & 1, ab);
+        if (!ok) break;
+        tc_fence_after();
+        mma_rows(tb + C::T_DQ, tb + C::T_DP, k_mn + k0.off, id_o, first);
+        mma_commit_e(k0.full + k_free);
         if (last) mma_commit_e(bar(C::B_ACC));
+      } else if (more) {  // (a CTA may have no units)
+        ok = wait_bar_warp(v.full, v.parity, ab);
+        if (!ok) break;
       }
       if (more) {
         if (first1) {  // (Q and dO are in TMEM)
-          ok = wait_bar_warp(bar(C::B_QT), runs & 1, ab);
+          ok = wait_two_warp(bar(C::B_QT), runs & 1, k.full, k.parity, ab);
+          if (!ok) break;
           ++runs;
-          s_of_next();
+          tc_fence_after();
+          mma_channels_t<C::BOXES>(tb + C::T_S, tb + C::T_Q, k_k + k.off, id_s, a.kd);
+          mma_commit_e(bar(C::B_S));
         }
-        ok = ok && wait_bar_warp(v_bar, v_par, ab);
-        if (!ok) break;
-        tc_fence_after();
-        mma_channels_t<C::BOXES>(tb + C::T_DP, tb + C::T_DO, dp_b, id_s, a.kd);
+        mma_channels_t<C::BOXES>(tb + C::T_DP, tb + C::T_DO, v_k + v.off, id_s, a.kd);
         mma_commit_e(bar(C::B_DP));
-        mma_commit_e(ve_bar);
+        mma_commit_e(v.full + 8 * C::NV);
       }
-      const uint64_t dq_b2 = dq_b1;
-      const uint32_t ke_bar2 = ke_bar1;
-      k.next();
-      v.next();
-      s_b = k_k + k.slot * kTileStep;
-      dp_b = v_k + v.slot * kTileStep;
-      dq_b1 = k_mn + k.slot * kTileStep;
-      k_bar = bar(full + k.slot);
-      v_bar = bar(C::B_VF + v.slot);
-      ke_bar1 = bar(C::B_KE + k.slot);
-      ve_bar = bar(C::B_VE + v.slot);
-      k_par = k.parity;
-      v_par = v.parity;
-      if (u + 2 < n) next.step(a.sc);
-      dq_b = dq_b2;
-      pin(s_b, dp_b, dq_b1, dq_b);
-      pin(k_bar, v_bar, ke_bar1, ve_bar);
-      ke_bar = ke_bar2;
+      k0 = k;
+      k.next(kTileStep);
+      v.next(kTileStep);
       first = first1;
       last = last1;
     }
