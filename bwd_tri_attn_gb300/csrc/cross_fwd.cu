@@ -685,7 +685,10 @@ cudaError_t launch_fwd(const CUtensorMap &mq, const CUtensorMap &mk, const CUten
 int cross_check_shape(const tri_cross_shape &s) {
   if (s.B < 1 || s.T < 1 || s.S < 1 || s.H < 1 || s.Hk < 1 || s.d < 1 || s.H % s.Hk || !isfinite(s.scale))
     return TRI_ATTN_ERR_INVALID_ARG;
-  if (s.d % 8 || s.d > 128 || s.B > 65535 || s.H > 1024 || s.T > (1 << 30) || s.S > (1 << 30)) return TRI_ATTN_ERR_UNSUPPORTED;
+  if (s.d % 8 || s.d > 128 || s.B > 65535 || s.H > 1024) return TRI_ATTN_ERR_UNSUPPORTED;
+  // an item has at most 2^19 units, so that a wait for its end (about 0.8 s at 1.5 us a unit) stays below the
+  // waits' time limit
+  if (s.S > (1 << 26) || (int64_t)s.T * (s.H / s.Hk) > (1 << 26)) return TRI_ATTN_ERR_UNSUPPORTED;
   // a CTA's units, and twice their number, fit 32 bits
   if ((double)s.B * s.H * (s.T / 128 + 1.0) * (s.S / 128 + 1.0) > 0x1p36) return TRI_ATTN_ERR_UNSUPPORTED;
   const int64_t *st[3] = {s.q_stride, s.k_stride, s.v_stride};

@@ -25,8 +25,8 @@
  * two). Products run on the tensor cores with BF16 operands and FP32 accumulation; P and dS are
  * rounded to BF16 as operands of the second products; statistics and sums are FP32.
  *
- * Requirements: B, T, S, H, Hk >= 1; 8 <= d <= 128, a multiple of 8; B <= 65535, H <= 1024, T and S at
- * most 2^30; scale finite; Q, K, V and dO finite wherever they are live; pointers 16-byte aligned
+ * Requirements: B, T, S, H, Hk >= 1; 8 <= d <= 128, a multiple of 8; B <= 65535, H <= 1024; S and
+ * T H / Hk at most 2^26; scale finite; Q, K, V and dO finite wherever they are live; pointers 16-byte aligned
  * (kv_lens: 4, mask: any), buffers not overlapping. Return codes are the TRI_ATTN_* codes of tri_attn.h;
  * a call that returns an error has enqueued nothing (TRI_ATTN_ERR_CUDA from a launch itself
  * excepted). Calls are asynchronous on `stream`, allocate no device memory and keep no state

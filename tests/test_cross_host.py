@@ -39,7 +39,8 @@ def bwd(tb, s, nulls=(), ws=1 << 34, **at):
     (dict(B=0), -1), (dict(T=0), -1), (dict(S=0), -1), (dict(H=0), -1), (dict(Hk=0), -1), (dict(d=0), -1),
     (dict(B=-1), -1), (dict(H=5), -1), (dict(Hk=8), -1), (dict(scale=float("nan")), -1), (dict(scale=float("inf")), -1),
     (dict(d=4), -2), (dict(d=12), -2), (dict(d=136), -2), (dict(B=65536), -2), (dict(H=2048), -2),
-    (dict(T=(1 << 30) + 1), -2), (dict(S=(1 << 30) + 1), -2), (dict(B=60000, T=1 << 29, S=1 << 29), -2),
+    (dict(T=(1 << 30) + 1), -2), (dict(S=(1 << 30) + 1), -2),
+    (dict(S=(1 << 26) + 1), -2), (dict(T=(1 << 25) + 1), -2), (dict(H=1000, Hk=1, T=67109), -2), (dict(B=60000, T=1 << 29, S=1 << 29), -2),
     (dict(q=(7680, 260, 64)), -2), (dict(q=(7680, 256, 0)), -2), (dict(k=(0, 128, 64)), -2), (dict(v=(25600, -128, 64)), -2),
     (dict(k=(25600, 128, 60)), -2), (dict(v=(1 << 40, 128, 64)), -2)])
 def test_bad_shapes(tb, bad, code):
