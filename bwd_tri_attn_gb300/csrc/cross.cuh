@@ -21,7 +21,7 @@
 #include "common.cuh"
 #include "launch.cuh"
 #include "plan.cuh"
-#include "sm100.cuh"
+#include "sm100_box.cuh"
 #include "sync.cuh"
 #include "tmap.cuh"
 #include "tri_cross.h"
