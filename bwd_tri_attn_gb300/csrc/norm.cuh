@@ -5,7 +5,7 @@
 // chunks go to lane groups of 8, 16 or 32 lanes of a 256-thread CTA, rows of up to 64 chunks to a
 // warp with two chunks a lane, and wider rows to a CTA of 128 or 256 threads, so that a thread
 // holds at most 8 chunks and the backward's per-column sums stay in registers. Rows that do not
-// start on 16-byte boundaries use five of the geometries, with shifted loads (two aligned words a
+// start on 16-byte boundaries use seven of the geometries, with shifted loads (two aligned words a
 // chunk) and stores of four bytes. (256, 8) exists for FP32 only: 16-bit rows of TRI_NORM_MAX_C
 // values are 1024 chunks.
 #pragma once
@@ -19,7 +19,9 @@ enum { kNormT8, kNormT16, kNormT32, kNormT32x2, kNormT128, kNormT256, kNormT256x
 // chunks: 16-byte chunks per row (the last one may be partly filled)
 inline int norm_geometry(int chunks, bool aligned) {
   if (!aligned)
-    return chunks <= 32     ? kNormT32
+    return chunks <= 8      ? kNormT8
+           : chunks <= 16   ? kNormT16
+           : chunks <= 32   ? kNormT32
            : chunks <= 128  ? kNormT128
            : chunks <= 512  ? kNormT256x2
            : chunks <= 1024 ? kNormT256x4
@@ -52,6 +54,8 @@ inline int norm_geometry(int chunks, bool aligned) {
       }                                                                    \
     } else {                                                               \
       switch (geo) {                                                       \
+        case kNormT8: LAUNCH(8, 1, false); break;                          \
+        case kNormT16: LAUNCH(16, 1, false); break;                        \
         case kNormT32: LAUNCH(32, 1, false); break;                        \
         case kNormT128: LAUNCH(128, 1, false); break;                      \
         case kNormT256x2: LAUNCH(256, 2, false); break;                    \
@@ -100,7 +104,7 @@ struct RowSum {
 // them again for every row from the first-level cache: its registers are better spent on rows in flight.
 template <typename XT, bool AL>
 __device__ __forceinline__ void row_weights(const float *w, int c, int C, float other, Pairs<XT> &f) {
-  if (AL && w && c < C) {
+  if (w && (AL ? c < C : c + 2 * Pairs<XT>::N <= C && (reinterpret_cast<uintptr_t>(w) & 15u) == 0)) {
 #pragma unroll
     for (int j = 0; j < Pairs<XT>::N; j += 2) {
       const float4 x = __ldg(reinterpret_cast<const float4 *>(w + c + 2 * j));

@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(T > 32 ? T : 256, fwd_ctas<NV>() * (T == 128 ?
 #pragma unroll
         for (int j = 0; j < P; ++j) {
           f[u][v].v[j] = __fadd2_rn(f[u][v].v[j], neg);
-          if constexpr (!AL) {  // (values past C are 0 - mean)
+          if (!AL && c + VEC > C) {  // (values past C are 0 - mean)
             if (c + 2 * j >= C) f[u][v].v[j].x = 0.f;
             if (c + 2 * j + 1 >= C) f[u][v].v[j].y = 0.f;
           }
@@ -146,8 +146,7 @@ __global__ void __launch_bounds__(T > 32 ? T : 256, fwd_ctas<NV>() * (T == 128 ?
 // barrier. Wider rows go to CTAs of 128 threads: with 8 chunks a lane in a warp, 8192 rows of 2048
 // BF16 values and their checkpoints took 31 us, with 2 chunks a thread 18 us.
 enum { kF8, kF16, kF32, kF32x2, kF32x4, kF128x2, kF128x4, kF128x8, kF256x8 };
-int norm_fwd_geometry(int chunks, bool aligned) {
-  if (!aligned && chunks <= 32) return kF32;
+int norm_fwd_geometry(int chunks) {
   return chunks <= 8     ? kF8
          : chunks <= 16  ? kF16
          : chunks <= 32  ? kF32
@@ -160,8 +159,8 @@ int norm_fwd_geometry(int chunks, bool aligned) {
 }
 #define NORM_FWD_DISPATCH(geo, aligned, LAUNCH)                        \
   switch (geo) {                                                       \
-    case kF8: LAUNCH(8, 1, true); break;                               \
-    case kF16: LAUNCH(16, 1, true); break;                             \
+    case kF8: if (aligned) LAUNCH(8, 1, true) else LAUNCH(8, 1, false); break; \
+    case kF16: if (aligned) LAUNCH(16, 1, true) else LAUNCH(16, 1, false); break; \
     case kF32: if (aligned) LAUNCH(32, 1, true) else LAUNCH(32, 1, false); break; \
     case kF32x2: if (aligned) LAUNCH(32, 2, true) else LAUNCH(32, 2, false); break; \
     case kF32x4: if (aligned) LAUNCH(32, 4, true) else LAUNCH(32, 4, false); break; \
@@ -179,7 +178,7 @@ cudaError_t launch_fwd_t(const tri_norm_shape &s, const void *x, const float *ga
   const bool al = s.C % VEC == 0 && ldx % VEC == 0 && ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(y)) & 15u) == 0 &&
                   ((reinterpret_cast<uintptr_t>(gamma) | reinterpret_cast<uintptr_t>(beta)) & 15u) == 0 &&
                   (reinterpret_cast<uintptr_t>(q8) & (VEC - 1)) == 0;
-  const int geo = norm_fwd_geometry((s.C + VEC - 1) / VEC, al);
+  const int geo = norm_fwd_geometry((s.C + VEC - 1) / VEC);
 #define LAUNCH(T, NV, AL)                                                                                          \
   {                                                                                                                \
     if constexpr (T * NV * VEC <= TRI_NORM_MAX_C) {                                                                \
