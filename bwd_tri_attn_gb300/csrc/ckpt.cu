@@ -1,11 +1,12 @@
 // 8-bit activation checkpoints on their own: pack and unpack (include/tri_norm.h states the format).
 //
 // GL lanes hold one group of 128 channels of one row, a 16-byte chunk each (16 lanes for 16-bit
-// types, 32 for FP32); the group's largest magnitude is an xor-shuffle maximum, and nothing is
+// types, 32 for FP32, fewer for short rows); the group's largest magnitude is an xor-shuffle maximum, and nothing is
 // read twice: memory bandwidth bounds both kernels (768 x 768 rows of 128 BF16 values packed and unpacked
 // in 78 us: 5.9 TB/s, 87 % of a copy's rate). U groups per lane group have their loads in
 // flight together.
 #include <algorithm>
+#include <type_traits>
 
 #include "norm.cuh"
 
@@ -20,10 +21,10 @@ __device__ __forceinline__ void group_of(int64_t k, int groups, int64_t &m, int 
   c0 = (int)(k - m * groups) * TRI_CKPT_GROUP;
 }
 
-template <typename XT, bool AL>
+template <typename XT, int GL, bool AL>
 __global__ void __launch_bounds__(256) ckpt_pack_kernel(const XT *__restrict__ x, int64_t ldx, int64_t M, int C,
                                                         int groups, int8_t *__restrict__ q8, float *__restrict__ s8) {
-  constexpr int VEC = Chunk<XT>::VEC, GL = TRI_CKPT_GROUP / VEC, PER = 256 / GL;
+  constexpr int VEC = Chunk<XT>::VEC, PER = 256 / GL;
   const int t = threadIdx.x % GL, g = threadIdx.x / GL;
   const Span span = span_of(x, M, ldx, C);
   const int64_t n = M * groups, step = (int64_t)gridDim.x * PER * kU;
@@ -58,11 +59,12 @@ __global__ void __launch_bounds__(256) ckpt_pack_kernel(const XT *__restrict__ x
   }
 }
 
-template <typename XT, bool AL>
+template <typename XT, int GL, bool AL>
 __global__ void __launch_bounds__(256) ckpt_unpack_kernel(const int8_t *__restrict__ q8, const float *__restrict__ s8,
                                                           int64_t M, int C, int groups, XT *__restrict__ x) {
-  constexpr int VEC = Chunk<XT>::VEC, GL = TRI_CKPT_GROUP / VEC, PER = 256 / GL;
+  constexpr int VEC = Chunk<XT>::VEC, PER = 256 / GL;
   const int t = threadIdx.x % GL, g = threadIdx.x / GL;
+  const Span span = span_of(q8, M, C, C);
   const int64_t n = M * groups, step = (int64_t)gridDim.x * PER * kU;
   for (int64_t k0 = (int64_t)blockIdx.x * PER * kU; k0 < n; k0 += step) {
     uint32_t w[kU][VEC / 4];
@@ -74,7 +76,7 @@ __global__ void __launch_bounds__(256) ckpt_unpack_kernel(const int8_t *__restri
       const int64_t k = min(k0 + u * PER + g, n - 1);
       group_of(k, groups, m[u], c[u]);
       c[u] += t * VEC;
-      q8_load<VEC, AL>(q8 + m[u] * C, c[u], C, w[u]);
+      q8_load<VEC, AL>(q8 + m[u] * C, c[u], C, span, w[u]);
       sc[u] = __ldg(s8 + k);
     }
 #pragma unroll
@@ -86,34 +88,55 @@ __global__ void __launch_bounds__(256) ckpt_unpack_kernel(const int8_t *__restri
   }
 }
 
+// Calls f with the lanes of a group: 128 channels' worth, or fewer where a row is shorter than that
+// (100000 rows of 27 FP32 values: 30 us both ways with 32 lanes, seven of them with values).
+template <typename XT, typename F>
+void with_lanes(int C, F f) {
+  constexpr int VEC = Chunk<XT>::VEC;
+  if (C <= 4 * VEC)
+    f(std::integral_constant<int, 4>());
+  else if (C <= 8 * VEC)
+    f(std::integral_constant<int, 8>());
+  else if (VEC == 8 || C <= 16 * VEC)
+    f(std::integral_constant<int, 16>());
+  else
+    f(std::integral_constant<int, TRI_CKPT_GROUP / VEC>());
+}
+
 template <typename XT>
 cudaError_t launch_pack(const tri_norm_shape &s, const void *x, int8_t *q8, float *s8, cudaStream_t st) {
-  constexpr int VEC = Chunk<XT>::VEC, PER = 256 / (TRI_CKPT_GROUP / VEC) * kU;
+  constexpr int VEC = Chunk<XT>::VEC;
   const int64_t ldx = s.ldx ? s.ldx : s.C;
   const int groups = (s.C + TRI_CKPT_GROUP - 1) / TRI_CKPT_GROUP;
   const bool al = s.C % VEC == 0 && ldx % VEC == 0 && (reinterpret_cast<uintptr_t>(x) & 15u) == 0 &&
                   (reinterpret_cast<uintptr_t>(q8) & (VEC - 1)) == 0;
-  const int grid = (int)std::min<int64_t>((s.M * groups + PER - 1) / PER, 152 * 32);
   const XT *xp = static_cast<const XT *>(x);
-  if (al)
-    ckpt_pack_kernel<XT, true><<<grid, 256, 0, st>>>(xp, ldx, s.M, s.C, groups, q8, s8);
-  else
-    ckpt_pack_kernel<XT, false><<<grid, 256, 0, st>>>(xp, ldx, s.M, s.C, groups, q8, s8);
+  with_lanes<XT>(s.C, [&](auto lanes) {
+    constexpr int GL = lanes.value, PER = 256 / GL * kU;
+    const int grid = (int)std::min<int64_t>((s.M * groups + PER - 1) / PER, 152 * 32);
+    if (al)
+      ckpt_pack_kernel<XT, GL, true><<<grid, 256, 0, st>>>(xp, ldx, s.M, s.C, groups, q8, s8);
+    else
+      ckpt_pack_kernel<XT, GL, false><<<grid, 256, 0, st>>>(xp, ldx, s.M, s.C, groups, q8, s8);
+  });
   return cudaGetLastError();
 }
 
 template <typename XT>
 cudaError_t launch_unpack(const tri_norm_shape &s, const int8_t *q8, const float *s8, void *x, cudaStream_t st) {
-  constexpr int VEC = Chunk<XT>::VEC, PER = 256 / (TRI_CKPT_GROUP / VEC) * kU;
+  constexpr int VEC = Chunk<XT>::VEC;
   const int groups = (s.C + TRI_CKPT_GROUP - 1) / TRI_CKPT_GROUP;
   const bool al = s.C % VEC == 0 && (reinterpret_cast<uintptr_t>(x) & 15u) == 0 &&
                   (reinterpret_cast<uintptr_t>(q8) & (VEC - 1)) == 0;
-  const int grid = (int)std::min<int64_t>((s.M * groups + PER - 1) / PER, 152 * 32);
   XT *xp = static_cast<XT *>(x);
-  if (al)
-    ckpt_unpack_kernel<XT, true><<<grid, 256, 0, st>>>(q8, s8, s.M, s.C, groups, xp);
-  else
-    ckpt_unpack_kernel<XT, false><<<grid, 256, 0, st>>>(q8, s8, s.M, s.C, groups, xp);
+  with_lanes<XT>(s.C, [&](auto lanes) {
+    constexpr int GL = lanes.value, PER = 256 / GL * kU;
+    const int grid = (int)std::min<int64_t>((s.M * groups + PER - 1) / PER, 152 * 32);
+    if (al)
+      ckpt_unpack_kernel<XT, GL, true><<<grid, 256, 0, st>>>(q8, s8, s.M, s.C, groups, xp);
+    else
+      ckpt_unpack_kernel<XT, GL, false><<<grid, 256, 0, st>>>(q8, s8, s.M, s.C, groups, xp);
+  });
   return cudaGetLastError();
 }
 

@@ -34,7 +34,7 @@ __global__ void __launch_bounds__(T > 32 ? T : 256, bwd_ctas<NV>() * (T == 128 ?
   __shared__ __align__(8) float col[T > 32 ? 2 : 2 * NV * T * VEC];
   RowSum<T, 2> row_sum{red, 0};
   allow_next_kernel();  // (the sum of the partial results waits for all of this one before it reads)
-  const Span span_x = span_of(x, M, ldx, C), span_dy = span_of(dy, M, lddy, C);
+  const Span span_x = span_of(x, M, ldx, C), span_dy = span_of(dy, M, lddy, C), span_q = span_of(q8, M, C, C);
   const int t = threadIdx.x % T, g = threadIdx.x / T;
   const float inv_c = 1.f / (float)C;
   const int groups = (C + TRI_CKPT_GROUP - 1) / TRI_CKPT_GROUP;
@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(T > 32 ? T : 256, bwd_ctas<NV>() * (T == 128 ?
       if (live) {
         if constexpr (Q8) {
           uint32_t w[VEC / 4];
-          q8_load<VEC, AL>(q8 + m * C, c, C, w);
+          q8_load<VEC, AL>(q8 + m * C, c, C, span_q, w);
           rx[v].x = w[0];
           if constexpr (VEC == 8) rx[v].y = w[1];
           if (c < C) sc[v] = __ldg(s8 + m * groups + c / TRI_CKPT_GROUP);

@@ -168,9 +168,11 @@ __device__ __forceinline__ void chunk_store(XT *row, int c, int C, const uint4 &
   }
 }
 
-// VEC 8-bit values of a row, packed into VEC / 4 words (zeros past C).
+// VEC 8-bit values of a row, packed into VEC / 4 words (zeros past C). Unaligned rows: eight values in aligned words
+// (10007 rows of 1003 FP16 values packed and unpacked: 27 -> 25 us), four byte by byte (100000 rows of 27
+// FP32 values: 14 us, 16 with words).
 template <int VEC, bool AL>
-__device__ __forceinline__ void q8_load(const int8_t *row, int c, int C, uint32_t (&w)[VEC / 4]) {
+__device__ __forceinline__ void q8_load(const int8_t *row, int c, int C, const Span &span, uint32_t (&w)[VEC / 4]) {
 #pragma unroll
   for (int i = 0; i < VEC / 4; ++i) w[i] = 0u;
   if constexpr (AL) {
@@ -183,9 +185,22 @@ __device__ __forceinline__ void q8_load(const int8_t *row, int c, int C, uint32_
       }
     }
   } else {
+    const uintptr_t addr = reinterpret_cast<uintptr_t>(row + c), at = addr & ~uintptr_t(3);
+    if (VEC == 8 && c < C && at >= span.begin && at + VEC + 4 <= span.end) {  // aligned words and a shift
+      uint32_t r[VEC / 4 + 1];
 #pragma unroll
-    for (int j = 0; j < VEC; ++j)
-      if (c + j < C) w[j / 4] |= (uint32_t)(uint8_t)row[c + j] << (8 * (j & 3));
+      for (int i = 0; i <= VEC / 4; ++i) r[i] = __ldg(reinterpret_cast<const uint32_t *>(at) + i);
+#pragma unroll
+      for (int i = 0; i < VEC / 4; ++i) {
+        const int n = C - c - 4 * i;  // values of this word
+        w[i] = __funnelshift_r(r[i], r[i + 1], 8 * (uint32_t)(addr & 3));
+        if (n < 4) w[i] &= n > 0 ? (1u << (8 * n)) - 1u : 0u;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < VEC; ++j)
+        if (c + j < C) w[j / 4] |= (uint32_t)(uint8_t)row[c + j] << (8 * (j & 3));
+    }
   }
 }
 
@@ -198,6 +213,22 @@ __device__ __forceinline__ void q8_store(int8_t *row, int c, int C, const uint32
       else
         *reinterpret_cast<uint32_t *>(row + c) = w[0];
     }
+  } else if (VEC == 8 && c + VEC <= C) {  // whole words where they are aligned, the bytes before and after them
+    constexpr int N = VEC / 4;
+    uint8_t *p = reinterpret_cast<uint8_t *>(row + c);
+    const uint32_t head = (4 - (uint32_t)reinterpret_cast<uintptr_t>(p)) & 3, top = w[N - 1];
+    if (head == 0) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) reinterpret_cast<uint32_t *>(p)[i] = w[i];
+      return;
+    }
+    if (head & 1) p[0] = (uint8_t)w[0];
+    if (head & 2) *reinterpret_cast<uint16_t *>(p + (head & 1)) = (uint16_t)(w[0] >> (8 * (head & 1)));
+#pragma unroll
+    for (int i = 0; i + 1 < N; ++i) *reinterpret_cast<uint32_t *>(p + head + 4 * i) = __funnelshift_r(w[i], w[i + 1], 8 * head);
+    // (4 - head bytes are left, the first of them at a multiple of 4)
+    if (head != 3) *reinterpret_cast<uint16_t *>(p + head + 4 * (N - 1)) = (uint16_t)(top >> (8 * head));
+    if (head & 1) p[VEC - 1] = (uint8_t)(top >> 24);
   } else {
 #pragma unroll
     for (int j = 0; j < VEC; ++j)
