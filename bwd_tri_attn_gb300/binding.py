@@ -264,6 +264,19 @@ def _stream_on(device, stream):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _used_on(stream, device, *tensors):
+    """What a call allocated on the current stream and uses on `stream`: its memory is not given out again before
+    that stream has passed the call, whenever the tensors are dropped."""
+    handle = _stream_on(device, stream)
+    if handle == _stream_on(device, None):
+        return
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -683,6 +696,8 @@ def norm_forward(x, gamma=None, beta=None, eps=1e-5, checkpoint=False, stream=No
     rc = load().tri_norm_fwd(shape, x.data_ptr(), _ptr(gamma), _ptr(beta), y.data_ptr(), mean.data_ptr(),
                              rstd.data_ptr(), q8, scale, _stream_on(device, stream))
     _check("tri_norm_fwd", rc)
+    if stream is not None:
+        _used_on(stream, device, y, mean, rstd, *(kept or ()))
     return (y, mean, rstd, kept) if checkpoint else (y, mean, rstd)
 
 
@@ -717,6 +732,8 @@ def norm_backward(x, gamma, mean, rstd, dy, workspace=None, stream=None):
                              dx.data_ptr(), _ptr(dgamma), _ptr(dbeta), _ptr(workspace), _nbytes(workspace),
                              _stream_on(device, stream))
     _check("tri_norm_bwd", rc)
+    if stream is not None:
+        _used_on(stream, device, dx, dgamma, dbeta, workspace)
     return dx, dgamma, dbeta
 
 
@@ -728,6 +745,8 @@ def checkpoint_pack(x, stream=None) -> Checkpoint:
     rc = load().tri_ckpt_pack(shape, x.data_ptr(), kept.q8.data_ptr(), kept.scale.data_ptr(),
                               _stream_on(device, stream))
     _check("tri_ckpt_pack", rc)
+    if stream is not None:
+        _used_on(stream, device, *kept)
     return kept
 
 
@@ -740,6 +759,8 @@ def checkpoint_unpack(kept, dtype=torch.bfloat16, stream=None) -> torch.Tensor:
     device = _on_device(x.get_device(), _arg(q8, "q8", torch.int8, n), _arg(scale, "scale", _F32, ng))
     rc = load().tri_ckpt_unpack(shape, q8.data_ptr(), scale.data_ptr(), x.data_ptr(), _stream_on(device, stream))
     _check("tri_ckpt_unpack", rc)
+    if stream is not None:
+        _used_on(stream, device, x)
     return x
 
 
@@ -784,6 +805,8 @@ def cross_forward(Q, K, V, mask=None, kv_lens=None, scale=None, workspace=None, 
                               O.data_ptr(), LSE.data_ptr(), _ptr(workspace), _nbytes(workspace),
                               _stream_on(device, stream))
     _check("tri_cross_fwd", rc)
+    if stream is not None:
+        _used_on(stream, device, O, LSE, workspace)
     return O, LSE
 
 
@@ -800,4 +823,6 @@ def cross_backward(Q, K, V, O, LSE, dO, mask=None, kv_lens=None, scale=None, wor
                               O.data_ptr(), LSE.data_ptr(), dO.data_ptr(), dQ.data_ptr(), dK.data_ptr(),
                               dV.data_ptr(), _ptr(workspace), _nbytes(workspace), _stream_on(device, stream))
     _check("tri_cross_bwd", rc)
+    if stream is not None:
+        _used_on(stream, device, dQ, dK, dV, workspace)
     return dQ, dK, dV

@@ -153,3 +153,32 @@ def test_layer_behind_the_triangle_attention_block():
     for t in (x, z, *block.parameters()):
         assert t.grad.isfinite().all() and t.grad.abs().max() > 0
     assert tb.tri_attn_device_status() == 0
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_memory_of_calls_on_another_stream(handle):
+    """A call's results and workspace may be dropped while the stream that it was given has not begun it."""
+    side = torch.cuda.Stream()
+    stream = side.cuda_stream if handle else side
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    q, k, v, do = (torch.randn((2, n, 4, 64), generator=gen, device="cuda").bfloat16() for n in (300, 600, 600, 300))
+    x, g = torch.randn((600, 256), generator=gen, device="cuda"), torch.ones(256, device="cuda")
+    O, LSE = tb.cross_forward(q, k, v)
+    y, mean, rstd = tb.norm_forward(x, g, g)
+    kept = tb.checkpoint_pack(x)
+    calls = [lambda s: tb.cross_forward(q, k, v, stream=s), lambda s: tb.cross_backward(q, k, v, O, LSE, do, stream=s),
+             lambda s: tb.norm_forward(x, g, g, checkpoint=True, stream=s)[:3], lambda s: tb.norm_backward(x, g, mean, rstd, y, stream=s),
+             lambda s: tb.checkpoint_pack(x, stream=s), lambda s: (tb.checkpoint_unpack(kept, torch.float32, stream=s),)]
+    for call in calls:
+        want = [t.clone() for t in call(None)]
+        sizes = [t.numel() * t.element_size() for t in want] + [tb.tri_cross_bwd_workspace_size(tb.cross_shape_of(q, k, v))]
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)  # (about 10 ms)
+        call(stream)  # (the results are dropped at once)
+        others = [torch.full((n,), 7, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(3)]
+        got = call(stream)
+        torch.cuda.synchronize()
+        assert all((o == 7).all() for o in others)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert tb.tri_attn_device_status() == 0
