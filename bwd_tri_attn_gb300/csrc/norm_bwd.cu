@@ -6,7 +6,7 @@
 // second kernel in a fixed order, without atomics, so the same call gives the same bits. The next
 // row's loads are issued before the current row's sums (memory bandwidth bounds the kernel).
 // 768 x 768 rows of 128 BF16 values: 88 us with the sum of the partials (5.2 TB/s, 77 % of a copy's
-// rate); 8192 rows of 2048 from the checkpoint: 26 us. Rows that do not start on 16-byte boundaries
+// rate); 8192 rows of 2048 from the checkpoint: 25 us. Rows that do not start on 16-byte boundaries
 // take more instructions than memory time: 10007 rows of 1003 FP16 values 28 us, where the bytes
 // want 9 (stores of 16 bytes made of neighbouring lanes' chunks took 32).
 #include <algorithm>
@@ -17,22 +17,23 @@
 namespace triattn {
 namespace {
 
+// Rows that a CTA which holds a row takes at a time: they share the barriers of their sums (10007 rows of
+// 1024 FP16 values: 21 us one by one, 18 in pairs). Unaligned rows, which want the issue slots, go one by
+// one (of 1003 values: 28 us, 30 in pairs).
+constexpr int bwd_rows(int T, int NV, bool AL) { return T > 32 && NV == 1 && AL ? 2 : 1; }
 // CTAs of 256 threads per SM that the registers are kept to.
-template <int NV>
-constexpr int bwd_ctas() {
-  return NV == 1 ? 3 : NV == 2 ? 2 : 1;
-}
+constexpr int bwd_ctas(int T, int NV, bool AL) { return NV == 1 ? (bwd_rows(T, NV, AL) == 2 ? 2 : 3) : NV == 2 ? 2 : 1; }
 
 template <typename XT, int T, int NV, bool AL, bool Q8>
-__global__ void __launch_bounds__(T > 32 ? T : 256, bwd_ctas<NV>() * (T == 128 ? 2 : 1))
+__global__ void __launch_bounds__(T > 32 ? T : 256, bwd_ctas(T, NV, AL) * (T == 128 ? 2 : 1))
     norm_bwd_kernel(const XT *__restrict__ x, int64_t ldx, const int8_t *__restrict__ q8, const float *__restrict__ s8,
                     const float *__restrict__ gamma, const float *__restrict__ mean, const float *__restrict__ rstd,
                     const XT *__restrict__ dy, int64_t lddy, int64_t M, int C, int64_t rpc, XT *__restrict__ dx,
                     float *__restrict__ part) {
-  constexpr int VEC = Chunk<XT>::VEC, P = VEC / 2, NT = T > 32 ? T : 256, RPC = NT / T;
-  __shared__ float red[T > 32 ? 2 * T / 32 : 1][2];
+  constexpr int VEC = Chunk<XT>::VEC, P = VEC / 2, NT = T > 32 ? T : 256, RPC = NT / T, U = bwd_rows(T, NV, AL);
+  __shared__ float red[T > 32 ? 2 * T / 32 : 1][2 * U];
   __shared__ __align__(8) float col[T > 32 ? 2 : 2 * NV * T * VEC];
-  RowSum<T, 2> row_sum{red, 0};
+  RowSum<T, 2 * U> row_sum{red, 0};
   allow_next_kernel();  // (the sum of the partial results waits for all of this one before it reads)
   const Span span_x = span_of(x, M, ldx, C), span_dy = span_of(dy, M, lddy, C), span_q = span_of(q8, M, C, C);
   const int t = threadIdx.x % T, g = threadIdx.x / T;
@@ -48,81 +49,91 @@ __global__ void __launch_bounds__(T > 32 ? T : 256, bwd_ctas<NV>() * (T == 128 ?
   const int64_t r0 = (int64_t)blockIdx.x * rpc, r1 = min(M, r0 + rpc);
   // rows past the chunk are zeros, which add nothing and are not written (their threads still
   // join the sums)
-  auto load = [&](int64_t m, uint4(&rx)[NV], uint4(&rd)[NV], float(&sc)[NV], float &mu, float &rs) {
+  struct Row {
+    uint4 x[NV], d[NV];
+    float sc[NV], mu, rs;
+  };
+  auto load = [&](int64_t m, Row &r) {
     const bool live = m < r1;
-    mu = live ? __ldg(mean + m) : 0.f;
-    rs = live ? __ldg(rstd + m) : 0.f;
+    r.mu = live ? __ldg(mean + m) : 0.f;
+    r.rs = live ? __ldg(rstd + m) : 0.f;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int c = (v * T + t) * VEC;
-      rx[v] = rd[v] = make_uint4(0u, 0u, 0u, 0u);
-      sc[v] = 0.f;
+      r.x[v] = r.d[v] = make_uint4(0u, 0u, 0u, 0u);
+      r.sc[v] = 0.f;
       if (live) {
         if constexpr (Q8) {
           uint32_t w[VEC / 4];
           q8_load<VEC, AL>(q8 + m * C, c, C, span_q, w);
-          rx[v].x = w[0];
-          if constexpr (VEC == 8) rx[v].y = w[1];
-          if (c < C) sc[v] = __ldg(s8 + m * groups + c / TRI_CKPT_GROUP);
+          r.x[v].x = w[0];
+          if constexpr (VEC == 8) r.x[v].y = w[1];
+          if (c < C) r.sc[v] = __ldg(s8 + m * groups + c / TRI_CKPT_GROUP);
         } else {
-          rx[v] = chunk_load<XT, AL>(x + m * ldx, c, C, span_x);
+          r.x[v] = chunk_load<XT, AL>(x + m * ldx, c, C, span_x);
         }
-        rd[v] = chunk_load<XT, AL>(dy + m * lddy, c, C, span_dy);
+        r.d[v] = chunk_load<XT, AL>(dy + m * lddy, c, C, span_dy);
       }
     }
   };
-  uint4 rx[NV], rd[NV];
-  float sc[NV], mu, rs;
-  load(r0 + g, rx, rd, sc, mu, rs);
-  for (int64_t b0 = r0; b0 < r1; b0 += RPC) {
-    uint4 nx[NV], nd[NV];
-    float nsc[NV], nmu, nrs;
-    load(b0 + RPC + g, nx, nd, nsc, nmu, nrs);
-    Pairs<XT> xh[NV], dz[NV];
-    float2 s0 = make_float2(0.f, 0.f), s1 = s0;
-    const float2 neg = make_float2(-mu, -mu), rs2 = make_float2(rs, rs);
+  Row row[U];
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      if constexpr (Q8) {
-        uint32_t w[VEC / 4];
-        w[0] = rx[v].x;
-        if constexpr (VEC == 8) w[1] = rx[v].y;
-        q8_values<XT>(w, sc[v], xh[v]);
-      } else {
-        chunk_unpack(rx[v], xh[v]);
-      }
-      Pairs<XT> d;
-      chunk_unpack(rd[v], d);
+  for (int u = 0; u < U; ++u) load(r0 + u * RPC + g, row[u]);
+  for (int64_t b0 = r0; b0 < r1; b0 += RPC * U) {
+    Row next[U];
 #pragma unroll
-      for (int j = 0; j < P; ++j) {
-        // (columns past C: dy is zero there, so they add nothing to any sum)
-        xh[v].v[j] = __fmul2_rn(__fadd2_rn(xh[v].v[j], neg), rs2);
-        ag[v].v[j] = __ffma2_rn(d.v[j], xh[v].v[j], ag[v].v[j]);
-        ab[v].v[j] = __fadd2_rn(ab[v].v[j], d.v[j]);
-        dz[v].v[j] = __fmul2_rn(d.v[j], gm[v].v[j]);
-        s0 = __fadd2_rn(s0, dz[v].v[j]);
-        s1 = __ffma2_rn(dz[v].v[j], xh[v].v[j], s1);
-      }
-    }
-    float s[2] = {s0.x + s0.y, s1.x + s1.y};
-    row_sum(s);
-    const float a = -s[0] * inv_c, b = -s[1] * inv_c;
-    const float2 a2 = make_float2(a, a), b2 = make_float2(b, b);
-    const int64_t m = b0 + g;
-    if (m < r1) {
+    for (int u = 0; u < U; ++u) load(b0 + (U + u) * RPC + g, next[u]);
+    Pairs<XT> xh[U][NV], dz[U][NV];
+    float s[2 * U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float2 s0 = make_float2(0.f, 0.f), s1 = s0;
+      const float2 neg = make_float2(-row[u].mu, -row[u].mu), rs2 = make_float2(row[u].rs, row[u].rs);
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
-        Pairs<XT> o;
+        if constexpr (Q8) {
+          uint32_t w[VEC / 4];
+          w[0] = row[u].x[v].x;
+          if constexpr (VEC == 8) w[1] = row[u].x[v].y;
+          q8_values<XT>(w, row[u].sc[v], xh[u][v]);
+        } else {
+          chunk_unpack(row[u].x[v], xh[u][v]);
+        }
+        Pairs<XT> d;
+        chunk_unpack(row[u].d[v], d);
 #pragma unroll
-        for (int j = 0; j < P; ++j)
-          o.v[j] = __fmul2_rn(rs2, __ffma2_rn(xh[v].v[j], b2, __fadd2_rn(dz[v].v[j], a2)));
-        chunk_store<XT, AL>(dx + m * C, (v * T + t) * VEC, C, chunk_pack(o));
+        for (int j = 0; j < P; ++j) {
+          // (columns past C: dy is zero there, so they add nothing to any sum)
+          xh[u][v].v[j] = __fmul2_rn(__fadd2_rn(xh[u][v].v[j], neg), rs2);
+          ag[v].v[j] = __ffma2_rn(d.v[j], xh[u][v].v[j], ag[v].v[j]);
+          ab[v].v[j] = __fadd2_rn(ab[v].v[j], d.v[j]);
+          dz[u][v].v[j] = __fmul2_rn(d.v[j], gm[v].v[j]);
+          s0 = __fadd2_rn(s0, dz[u][v].v[j]);
+          s1 = __ffma2_rn(dz[u][v].v[j], xh[u][v].v[j], s1);
+        }
+      }
+      s[2 * u] = s0.x + s0.y;
+      s[2 * u + 1] = s1.x + s1.y;
+    }
+    row_sum(s);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float a = -s[2 * u] * inv_c, b = -s[2 * u + 1] * inv_c;
+      const float2 a2 = make_float2(a, a), b2 = make_float2(b, b), rs2 = make_float2(row[u].rs, row[u].rs);
+      const int64_t m = b0 + u * RPC + g;
+      if (m < r1) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          Pairs<XT> o;
+#pragma unroll
+          for (int j = 0; j < P; ++j)
+            o.v[j] = __fmul2_rn(rs2, __ffma2_rn(xh[u][v].v[j], b2, __fadd2_rn(dz[u][v].v[j], a2)));
+          chunk_store<XT, AL>(dx + m * C, (v * T + t) * VEC, C, chunk_pack(o));
+        }
       }
     }
 #pragma unroll
-    for (int v = 0; v < NV; ++v) rx[v] = nx[v], rd[v] = nd[v], sc[v] = nsc[v];
-    mu = nmu;
-    rs = nrs;
+    for (int u = 0; u < U; ++u) row[u] = next[u];
   }
   if (!part) return;
   float *out = part + (int64_t)blockIdx.x * 2 * C;
@@ -217,9 +228,10 @@ struct BwdSplitRows {
 // The split of the rows over CTAs, from the shape alone: the CTAs that 152 SMs hold at once (a second,
 // shorter wave of them took as long as the first: 102 against 77 us for 768 x 768 rows of 128),
 // at least two rows for each group of threads that holds a row.
-BwdSplitRows split_rows(const tri_norm_shape &s, int geo) {
+BwdSplitRows split_rows(const tri_norm_shape &s, int geo, bool aligned) {
   const int T = norm_threads_per_row(geo), RPC = T > 32 ? 1 : 256 / T;
-  const int per_sm = geo == kNormT32x2 || geo == kNormT256x2 ? 2 : geo == kNormT256x4 || geo == kNormT256x8 ? 1 : T == 128 ? 6 : 3;
+  const int nv = geo == kNormT32x2 || geo == kNormT256x2 ? 2 : geo == kNormT256x4 ? 4 : geo == kNormT256x8 ? 8 : 1;
+  const int per_sm = bwd_ctas(T, nv, aligned) * (T == 128 ? 2 : 1);
   const int64_t target = 152 * per_sm;
   int64_t rpc = (s.M + target - 1) / target;
   rpc = std::max<int64_t>((rpc + RPC - 1) / RPC * RPC, 2 * RPC);
@@ -245,7 +257,7 @@ cudaError_t launch_bwd_t(const tri_norm_shape &s, const void *x, const int8_t *q
   constexpr int VEC = Chunk<XT>::VEC;
   bool al;
   const int geo = geometry_of<XT>(s, x, q8, gamma, dy, dx, &al);
-  const BwdSplitRows sp = split_rows(s, geo);
+  const BwdSplitRows sp = split_rows(s, geo, al);
   const int64_t ldx = s.ldx ? s.ldx : s.C, lddy = s.lddy ? s.lddy : s.C;
   const XT *dyp = static_cast<const XT *>(dy);
   XT *dxp = static_cast<XT *>(dx);
@@ -272,7 +284,7 @@ cudaError_t launch_bwd_t(const tri_norm_shape &s, const void *x, const int8_t *q
 // The largest number of partial sums any alignment of the call's pointers can lead to.
 size_t workspace_bytes_of(const tri_norm_shape &s) {
   const int vec = s.dtype == TRI_DTYPE_FP32 ? 4 : 8, chunks = (s.C + vec - 1) / vec;
-  const int parts = std::max(split_rows(s, norm_geometry(chunks, true)).parts, split_rows(s, norm_geometry(chunks, false)).parts);
+  const int parts = std::max(split_rows(s, norm_geometry(chunks, true), true).parts, split_rows(s, norm_geometry(chunks, false), false).parts);
   return sizeof(float) * (size_t)parts * 2 * s.C;
 }
 
