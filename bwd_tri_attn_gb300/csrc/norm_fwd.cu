@@ -4,8 +4,8 @@
 // A row is read once into registers; its mean and then the mean of the squared differences are
 // summed from there (no cancellation for rows far from zero), and y, the statistics and the
 // checkpoint leave in the same pass: the kernel reads x and writes y (plus one byte and 1/32 of an
-// FP32 scale per value for the checkpoint), and memory bandwidth bounds it: 31 us for 384 x 384 rows
-// of 128 FP32 values (4.8 TB/s, 71 % of a copy's rate), 19 us for 8192 rows of 2048 BF16 values with their
+// FP32 scale per value for the checkpoint), and memory bandwidth bounds it: 24 us for 384 x 384 rows
+// of 128 FP32 values (6.3 TB/s, 93 % of a copy's rate), 57 us for 768 x 768 rows of 128 BF16 values (78 %), 19 us for 8192 rows of 2048 BF16 values with their
 // checkpoint (4.5 TB/s); 3 us for 384 rows, a launch.
 #include <math.h>
 
@@ -29,6 +29,14 @@ constexpr int fwd_ctas() {
   return NV <= 2 ? 3 : NV == 4 ? 2 : 1;
 }
 
+// Whether the CTAs stay (one wave of them) and load their next rows while they sum these. It pays where a thread
+// holds many chunks or wide values: 147456 rows of 128 FP32 values 28.8 -> 24.2 us, 50000 of 768 BF16 values 48 ->
+// 36 us; short 16-bit rows are faster in many CTAs (589824 of 128 BF16 values: 57 us, 65 so).
+template <typename XT>
+constexpr bool fwd_ahead(int NV, bool AL) {
+  return NV >= 4 || (sizeof(XT) == 4 && NV == 1 && AL);
+}
+
 template <typename XT, int T, int NV, bool AL>
 __global__ void __launch_bounds__(T > 32 ? T : 256, fwd_ctas<NV>() * (T == 128 ? 2 : 1))
     norm_fwd_kernel(const XT *__restrict__ x, int64_t ldx, const float *__restrict__ gamma,
@@ -46,17 +54,21 @@ __global__ void __launch_bounds__(T > 32 ? T : 256, fwd_ctas<NV>() * (T == 128 ?
   // (every thread of a warp, and of a CTA that holds a row, makes the same number of iterations:
   // rows past the last one are zeros that are not written)
   const int64_t step = (int64_t)gridDim.x * RPC * U;
+  uint4 raw[U][NV];
+  auto load = [&](int64_t m0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t m = m0 + u * RPC + g;
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+        raw[u][v] = m < M ? chunk_load<XT, AL>(x + m * ldx, (v * T + t) * VEC, C, span) : make_uint4(0u, 0u, 0u, 0u);
+    }
+  };
+  if (fwd_ahead<XT>(NV, AL)) load((int64_t)blockIdx.x * RPC * U);
   for (int64_t m0 = (int64_t)blockIdx.x * RPC * U; m0 < M; m0 += step) {
     Pairs<XT> f[U][NV];
+    if (!fwd_ahead<XT>(NV, AL)) load(m0);
     {
-      uint4 raw[U][NV];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int64_t m = m0 + u * RPC + g;
-#pragma unroll
-        for (int v = 0; v < NV; ++v)
-          raw[u][v] = m < M ? chunk_load<XT, AL>(x + m * ldx, (v * T + t) * VEC, C, span) : make_uint4(0u, 0u, 0u, 0u);
-      }
 #pragma unroll
       for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -85,6 +97,7 @@ __global__ void __launch_bounds__(T > 32 ? T : 256, fwd_ctas<NV>() * (T == 128 ?
         }
       }
     }
+    if (fwd_ahead<XT>(NV, AL)) load(m0 + step);
     float mu[U], q[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -183,7 +196,8 @@ cudaError_t launch_fwd_t(const tri_norm_shape &s, const void *x, const float *ga
   {                                                                                                                \
     if constexpr (T * NV * VEC <= TRI_NORM_MAX_C) {                                                                \
       constexpr int NT = T > 32 ? T : 256, per = NT / T * fwd_rows<NV>();                                          \
-      const int grid = (int)std::min<int64_t>((s.M + per - 1) / per, 152 * 32);                                    \
+      constexpr int most = 152 * (fwd_ahead<XT>(NV, AL) ? fwd_ctas<NV>() * (T == 128 ? 2 : 1) : 32);                 \
+      const int grid = (int)std::min<int64_t>((s.M + per - 1) / per, most);                                        \
       norm_fwd_kernel<XT, T, NV, AL><<<grid, NT, 0, st>>>(static_cast<const XT *>(x), ldx, gamma, beta, s.eps, s.M, \
                                                           s.C, static_cast<XT *>(y), mean, rstd, q8, s8);          \
     }                                                                                                              \
