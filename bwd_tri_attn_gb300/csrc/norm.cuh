@@ -15,7 +15,7 @@
 
 namespace triattn {
 
-enum { kNormT8, kNormT16, kNormT32, kNormT32x2, kNormT128, kNormT256, kNormT256x2, kNormT256x4, kNormT256x8 };
+enum { kNormT8, kNormT16, kNormT32, kNormT32x2, kNormT128, kNormT256, kNormT256x2, kNormT512x2, kNormT512x4 };
 
 // chunks: 16-byte chunks per row (the last one may be partly filled)
 inline int norm_geometry(int chunks, bool aligned) {
@@ -26,8 +26,8 @@ inline int norm_geometry(int chunks, bool aligned) {
            : chunks <= 64   ? kNormT32x2
            : chunks <= 128  ? kNormT128
            : chunks <= 512  ? kNormT256x2
-           : chunks <= 1024 ? kNormT256x4
-                            : kNormT256x8;
+           : chunks <= 1024 ? kNormT512x2
+                            : kNormT512x4;
   return chunks <= 8     ? kNormT8
          : chunks <= 16  ? kNormT16
          : chunks <= 32  ? kNormT32
@@ -35,8 +35,8 @@ inline int norm_geometry(int chunks, bool aligned) {
          : chunks <= 128 ? kNormT128
          : chunks <= 256 ? kNormT256
          : chunks <= 512 ? kNormT256x2
-         : chunks <= 1024 ? kNormT256x4
-                          : kNormT256x8;
+         : chunks <= 1024 ? kNormT512x2
+                          : kNormT512x4;
 }
 
 // LAUNCH(T, NV, aligned) of a geometry.
@@ -51,8 +51,8 @@ inline int norm_geometry(int chunks, bool aligned) {
         case kNormT128: LAUNCH(128, 1, true); break;                       \
         case kNormT256: LAUNCH(256, 1, true); break;                       \
         case kNormT256x2: LAUNCH(256, 2, true); break;                     \
-        case kNormT256x4: LAUNCH(256, 4, true); break;                     \
-        default: LAUNCH(256, 8, true); break;                              \
+        case kNormT512x2: LAUNCH(512, 2, true); break;                     \
+        default: LAUNCH(512, 4, true); break;                              \
       }                                                                    \
     } else {                                                               \
       switch (geo) {                                                       \
@@ -62,14 +62,14 @@ inline int norm_geometry(int chunks, bool aligned) {
         case kNormT32x2: LAUNCH(32, 2, false); break;                      \
         case kNormT128: LAUNCH(128, 1, false); break;                      \
         case kNormT256x2: LAUNCH(256, 2, false); break;                    \
-        case kNormT256x4: LAUNCH(256, 4, false); break;                    \
-        default: LAUNCH(256, 8, false); break;                             \
+        case kNormT512x2: LAUNCH(512, 2, false); break;                    \
+        default: LAUNCH(512, 4, false); break;                             \
       }                                                                    \
     }                                                                      \
   } while (0)
 
 inline int norm_threads_per_row(int geo) {
-  return geo == kNormT8 ? 8 : geo == kNormT16 ? 16 : geo <= kNormT32x2 ? 32 : geo == kNormT128 ? 128 : 256;
+  return geo == kNormT8 ? 8 : geo == kNormT16 ? 16 : geo <= kNormT32x2 ? 32 : geo == kNormT128 ? 128 : geo < kNormT512x2 ? 256 : 512;
 }
 
 // Sums of W values over the T threads that hold a row, the same bits in every one of them: an xor

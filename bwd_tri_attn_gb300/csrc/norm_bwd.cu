@@ -21,11 +21,13 @@ namespace {
 // 1024 FP16 values: 21 us one by one, 18 in pairs). Unaligned rows, which want the issue slots, go one by
 // one (of 1003 values: 28 us, 30 in pairs).
 constexpr int bwd_rows(int T, int NV, bool AL) { return T > 32 && NV == 1 && AL ? 2 : 1; }
-// CTAs of 256 threads per SM that the registers are kept to.
-constexpr int bwd_ctas(int T, int NV, bool AL) { return NV == 1 ? (bwd_rows(T, NV, AL) == 2 ? 2 : 3) : NV == 2 ? 2 : 1; }
+// CTAs per SM that the registers are kept to: 768 threads, 512 where a thread holds more, at least one CTA.
+constexpr int bwd_ctas(int T, int NV, bool AL) {
+  return T == 512 ? 1 : (NV == 1 ? (bwd_rows(T, NV, AL) == 2 ? 2 : 3) : 2) * (T == 128 ? 2 : 1);
+}
 
 template <typename XT, int T, int NV, bool AL, bool Q8>
-__global__ void __launch_bounds__(T > 32 ? T : 256, bwd_ctas(T, NV, AL) * (T == 128 ? 2 : 1))
+__global__ void __launch_bounds__(T > 32 ? T : 256, bwd_ctas(T, NV, AL))
     norm_bwd_kernel(const XT *__restrict__ x, int64_t ldx, const int8_t *__restrict__ q8, const float *__restrict__ s8,
                     const float *__restrict__ gamma, const float *__restrict__ mean, const float *__restrict__ rstd,
                     const XT *__restrict__ dy, int64_t lddy, int64_t M, int C, int64_t rpc, XT *__restrict__ dx,
@@ -230,8 +232,8 @@ struct BwdSplitRows {
 // at least two rows for each group of threads that holds a row.
 BwdSplitRows split_rows(const tri_norm_shape &s, int geo, bool aligned) {
   const int T = norm_threads_per_row(geo), RPC = T > 32 ? 1 : 256 / T;
-  const int nv = geo == kNormT32x2 || geo == kNormT256x2 ? 2 : geo == kNormT256x4 ? 4 : geo == kNormT256x8 ? 8 : 1;
-  const int per_sm = bwd_ctas(T, nv, aligned) * (T == 128 ? 2 : 1);
+  const int nv = geo == kNormT32x2 || geo == kNormT256x2 || geo == kNormT512x2 ? 2 : geo == kNormT512x4 ? 4 : 1;
+  const int per_sm = bwd_ctas(T, nv, aligned);
   const int64_t target = 152 * per_sm;
   int64_t rpc = (s.M + target - 1) / target;
   rpc = std::max<int64_t>((rpc + RPC - 1) / RPC * RPC, 2 * RPC);
