@@ -3,11 +3,11 @@
 //
 // T threads hold one row, each NV chunks of 16 bytes (chunk v T + t of the row): rows of up to 32
 // chunks go to lane groups of 8, 16 or 32 lanes of a 256-thread CTA, rows of up to 64 chunks to a
-// warp with two chunks a lane, and wider rows to a CTA of 128 or 256 threads, so that a thread
-// holds at most 8 chunks and the backward's per-column sums stay in registers. Rows that do not
-// start on 16-byte boundaries use eight of the geometries, with shifted loads (two aligned words a
-// chunk) and stores of four bytes. (256, 8) exists for FP32 only: 16-bit rows of TRI_NORM_MAX_C
-// values are 1024 chunks. Fewer lanes than a row has chunks cost registers, more of them idle: 109876 rows of 59
+// warp with two chunks a lane, and wider rows to a CTA of 128, 256 or 512 threads, so that a thread
+// holds at most 4 chunks and the backward's per-column sums stay in registers. Rows that begin anywhere
+// use eight of the geometries, with shifted loads (two aligned words a chunk) and stores of four
+// bytes. (512, 4) exists for FP32 only: 16-bit rows of TRI_NORM_MAX_C values are 1024 chunks.
+// Fewer lanes than a row has chunks cost registers, more of them idle: 109876 rows of 59
 // BF16 values took the backward 64 us in 32 lanes and 19 in 8, 20000 rows of 505 33 us in 128 and 25 in 32.
 #pragma once
 

@@ -26,13 +26,95 @@ constexpr int bwd_ctas(int T, int NV, bool AL) {
   return T == 512 ? 1 : (NV == 1 ? (bwd_rows(T, NV, AL) == 2 ? 2 : 3) : 2) * (T == 128 ? 2 : 1);
 }
 
-template <typename XT, int T, int NV, bool AL, bool Q8>
-__global__ void __launch_bounds__(T > 32 ? T : 256, bwd_ctas(T, NV, AL))
+// How the rows of a tensor lie. In step: not all of them start on a 16-byte boundary, but those of x, dy
+// and dx are equally far from one. A CTA then takes every VEC-th row, which all are the same way off, and its chunks
+// begin at the boundaries: a column stays with its thread, and all accesses but those at the rows' ends are
+// aligned 16 bytes.
+enum { kAnyRows, kAlignedRows, kRowsInStep };
+
+// The chunk at row + c (a 16-byte boundary; c may be negative): at a row's ends the
+// whole chunk is read too, where it lies inside the tensor. in_row() then makes zeros of what lies outside the row,
+// when the values are used: done here it would wait for loads that are to be in flight.
+template <typename XT>
+__device__ __forceinline__ uint4 chunk_load_in_step(const XT *row, int c, int C, const Span &span) {
+  constexpr int VEC = Chunk<XT>::VEC;
+  if (c >= 0 && c + VEC <= C) return ld_stream(reinterpret_cast<const uint4 *>(row + c));
+  uint32_t w[4] = {0u, 0u, 0u, 0u};
+  const uintptr_t at = reinterpret_cast<uintptr_t>(row) + (uintptr_t)((intptr_t)c * (intptr_t)sizeof(XT));
+  if (c < C && c + VEC > 0) {
+    if (at >= span.begin && at + 16 <= span.end) return ld_stream(reinterpret_cast<const uint4 *>(at));
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      if ((unsigned)(c + j) >= (unsigned)C) continue;
+      if constexpr (sizeof(XT) == 2)
+        w[j / 2] |= (uint32_t)reinterpret_cast<const uint16_t *>(row)[c + j] << (16 * (j & 1));
+      else
+        w[j] = reinterpret_cast<const uint32_t *>(row)[c + j];
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <typename XT>
+__device__ __forceinline__ void in_row(uint4 &v, int c, int C) {
+  constexpr int VEC = Chunk<XT>::VEC;
+  if (c >= 0 && c + VEC <= C) return;
+  uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int j = 0; j < VEC; ++j)
+    if ((unsigned)(c + j) >= (unsigned)C) {
+      if constexpr (sizeof(XT) == 2)
+        w[j / 2] &= (j & 1) ? 0x0000ffffu : 0xffff0000u;
+      else
+        w[j] = 0u;
+    }
+  v = make_uint4(w[0], w[1], w[2], w[3]);
+}
+// The 8-bit values of that chunk (at a multiple of VEC bytes, too).
+template <int VEC>
+__device__ __forceinline__ void q8_load_in_step(const int8_t *row, int c, int C, const Span &span, uint32_t (&w)[VEC / 4]) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(row) + (uintptr_t)(intptr_t)c;
+#pragma unroll
+  for (int i = 0; i < VEC / 4; ++i) w[i] = 0u;
+  if (c >= C || c + VEC <= 0) return;
+  if ((c >= 0 && c + VEC <= C) || (at >= span.begin && at + VEC <= span.end)) {
+    if constexpr (VEC == 8) {
+      const uint2 v = __ldg(reinterpret_cast<const uint2 *>(at));
+      w[0] = v.x, w[1] = v.y;
+    } else {
+      w[0] = __ldg(reinterpret_cast<const uint32_t *>(at));
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < VEC; ++j)
+    if ((unsigned)(c + j) < (unsigned)C) w[j / 4] |= (uint32_t)(uint8_t)row[c + j] << (8 * (j & 3));
+}
+template <typename XT>
+__device__ __forceinline__ void chunk_store_in_step(XT *row, int c, int C, const uint4 &v) {
+  constexpr int VEC = Chunk<XT>::VEC;
+  if (c >= 0 && c + VEC <= C) {
+    *reinterpret_cast<uint4 *>(row + c) = v;
+    return;
+  }
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) {
+    if ((unsigned)(c + j) >= (unsigned)C) continue;
+    if constexpr (sizeof(XT) == 2)
+      reinterpret_cast<uint16_t *>(row)[c + j] = (uint16_t)(w[j / 2] >> (16 * (j & 1)));
+    else
+      reinterpret_cast<uint32_t *>(row)[c + j] = w[j];
+  }
+}
+
+template <typename XT, int T, int NV, int ROWS, bool Q8>
+__global__ void __launch_bounds__(T > 32 ? T : 256, bwd_ctas(T, NV, ROWS != kAnyRows))
     norm_bwd_kernel(const XT *__restrict__ x, int64_t ldx, const int8_t *__restrict__ q8, const float *__restrict__ s8,
                     const float *__restrict__ gamma, const float *__restrict__ mean, const float *__restrict__ rstd,
-                    const XT *__restrict__ dy, int64_t lddy, int64_t M, int C, int64_t rpc, XT *__restrict__ dx,
-                    float *__restrict__ part) {
-  constexpr int VEC = Chunk<XT>::VEC, P = VEC / 2, NT = T > 32 ? T : 256, RPC = NT / T, U = bwd_rows(T, NV, AL);
+                    const XT *__restrict__ dy, int64_t lddy, int64_t M, int C, int64_t rpc, int per_class,
+                    XT *__restrict__ dx, float *__restrict__ part) {
+  constexpr bool AL = ROWS == kAlignedRows, STEP = ROWS == kRowsInStep;
+  constexpr int VEC = Chunk<XT>::VEC, P = VEC / 2, NT = T > 32 ? T : 256, RPC = NT / T, U = bwd_rows(T, NV, ROWS != kAnyRows);
   __shared__ float red[T > 32 ? 2 * T / 32 : 1][2 * U];
   __shared__ __align__(8) float col[T > 32 ? 2 : 2 * NV * T * VEC];
   RowSum<T, 2 * U> row_sum{red, 0};
@@ -42,39 +124,63 @@ __global__ void __launch_bounds__(T > 32 ? T : 256, bwd_ctas(T, NV, AL))
   const float inv_c = 1.f / (float)C;
   const int groups = (C + TRI_CKPT_GROUP - 1) / TRI_CKPT_GROUP;
   Pairs<XT> gm[NV], ag[NV], ab[NV];
+  // rows first + stride i, i in [r0, r1); sh values before the first one's first lies a boundary
+  const int cls = STEP ? (int)blockIdx.x / per_class : 0;
+  const int64_t stride = STEP ? VEC : 1, first = cls;
+  const int sh = STEP ? (int)((reinterpret_cast<uintptr_t>(dx + first * C) & 15) / sizeof(XT)) : 0;
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
-    row_weights<XT, AL>(gamma, (v * T + t) * VEC, C, 1.f, gm[v]);
+    if constexpr (STEP) {
+#pragma unroll
+      for (int j = 0; j < P; ++j) {
+        const int c = (v * T + t) * VEC - sh + 2 * j;
+        gm[v].v[j] = make_float2(gamma && (unsigned)c < (unsigned)C ? __ldg(gamma + c) : 1.f,
+                                 gamma && (unsigned)(c + 1) < (unsigned)C ? __ldg(gamma + c + 1) : 1.f);
+      }
+    } else {
+      row_weights<XT, AL>(gamma, (v * T + t) * VEC, C, 1.f, gm[v]);
+    }
 #pragma unroll
     for (int j = 0; j < P; ++j) ag[v].v[j] = ab[v].v[j] = make_float2(0.f, 0.f);
   }
-  const int64_t r0 = (int64_t)blockIdx.x * rpc, r1 = min(M, r0 + rpc);
+  const int64_t rows = (M - first + stride - 1) / stride;  // (of the class; M < first: none)
+  const int64_t r0 = (STEP ? (int64_t)blockIdx.x - (int64_t)cls * per_class : (int64_t)blockIdx.x) * rpc, r1 = min(rows, r0 + rpc);
   // rows past the chunk are zeros, which add nothing and are not written (their threads still
   // join the sums)
   struct Row {
     uint4 x[NV], d[NV];
-    float sc[NV], mu, rs;
+    float sc[NV], sc2[NV], mu, rs;  // (in step a chunk may reach into the next group, with another scale)
   };
-  auto load = [&](int64_t m, Row &r) {
-    const bool live = m < r1;
+  auto load = [&](int64_t i, Row &r) {
+    const bool live = i < r1;
+    const int64_t m = first + stride * i;
     r.mu = live ? __ldg(mean + m) : 0.f;
     r.rs = live ? __ldg(rstd + m) : 0.f;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int c = (v * T + t) * VEC;
+      const int c = (v * T + t) * VEC - sh;
       r.x[v] = r.d[v] = make_uint4(0u, 0u, 0u, 0u);
-      r.sc[v] = 0.f;
+      r.sc[v] = r.sc2[v] = 0.f;
       if (live) {
         if constexpr (Q8) {
           uint32_t w[VEC / 4];
-          q8_load<VEC, AL>(q8 + m * C, c, C, span_q, w);
+          if constexpr (STEP)
+            q8_load_in_step<VEC>(q8 + m * C, c, C, span_q, w);
+          else
+            q8_load<VEC, AL>(q8 + m * C, c, C, span_q, w);
           r.x[v].x = w[0];
           if constexpr (VEC == 8) r.x[v].y = w[1];
-          if (c < C) r.sc[v] = __ldg(s8 + m * groups + c / TRI_CKPT_GROUP);
+          if (c < C) r.sc[v] = __ldg(s8 + m * groups + max(c, 0) / TRI_CKPT_GROUP);
+          if (STEP && c < C) r.sc2[v] = __ldg(s8 + m * groups + min(max(c, 0) / TRI_CKPT_GROUP + 1, groups - 1));
+        } else if constexpr (STEP) {
+          r.x[v] = chunk_load_in_step<XT>(x + m * ldx, c, C, span_x);
         } else {
           r.x[v] = chunk_load<XT, AL>(x + m * ldx, c, C, span_x);
         }
-        r.d[v] = chunk_load<XT, AL>(dy + m * lddy, c, C, span_dy);
+        if constexpr (STEP)
+          r.d[v] = chunk_load_in_step<XT>(dy + m * lddy, c, C, span_dy);
+        else
+          r.d[v] = chunk_load<XT, AL>(dy + m * lddy, c, C, span_dy);
       }
     }
   };
@@ -93,11 +199,29 @@ __global__ void __launch_bounds__(T > 32 ? T : 256, bwd_ctas(T, NV, AL))
       const float2 neg = make_float2(-row[u].mu, -row[u].mu), rs2 = make_float2(row[u].rs, row[u].rs);
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
+        if constexpr (STEP) {
+          if constexpr (!Q8) in_row<XT>(row[u].x[v], (v * T + t) * VEC - sh, C);  // (8-bit values are finite all the same)
+          in_row<XT>(row[u].d[v], (v * T + t) * VEC - sh, C);
+        }
         if constexpr (Q8) {
           uint32_t w[VEC / 4];
           w[0] = row[u].x[v].x;
           if constexpr (VEC == 8) w[1] = row[u].x[v].y;
-          q8_values<XT>(w, row[u].sc[v], xh[u][v]);
+          if constexpr (STEP) {
+            const int c = (v * T + t) * VEC - sh, n = (max(c, 0) / TRI_CKPT_GROUP + 1) * TRI_CKPT_GROUP - c;  // of the first group
+            q8_values<XT>(w, row[u].sc[v], xh[u][v]);
+            if (n < VEC) {
+              Pairs<XT> other;
+              q8_values<XT>(w, row[u].sc2[v], other);
+#pragma unroll
+              for (int j = 0; j < P; ++j) {
+                if (2 * j >= n) xh[u][v].v[j].x = other.v[j].x;
+                if (2 * j + 1 >= n) xh[u][v].v[j].y = other.v[j].y;
+              }
+            }
+          } else {
+            q8_values<XT>(w, row[u].sc[v], xh[u][v]);
+          }
         } else {
           chunk_unpack(row[u].x[v], xh[u][v]);
         }
@@ -122,15 +246,18 @@ __global__ void __launch_bounds__(T > 32 ? T : 256, bwd_ctas(T, NV, AL))
     for (int u = 0; u < U; ++u) {
       const float a = -s[2 * u] * inv_c, b = -s[2 * u + 1] * inv_c;
       const float2 a2 = make_float2(a, a), b2 = make_float2(b, b), rs2 = make_float2(row[u].rs, row[u].rs);
-      const int64_t m = b0 + u * RPC + g;
-      if (m < r1) {
+      const int64_t i = b0 + u * RPC + g, m = first + stride * i;
+      if (i < r1) {
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
           Pairs<XT> o;
 #pragma unroll
           for (int j = 0; j < P; ++j)
             o.v[j] = __fmul2_rn(rs2, __ffma2_rn(xh[u][v].v[j], b2, __fadd2_rn(dz[u][v].v[j], a2)));
-          chunk_store<XT, AL>(dx + m * C, (v * T + t) * VEC, C, chunk_pack(o));
+          if constexpr (STEP)
+            chunk_store_in_step<XT>(dx + m * C, (v * T + t) * VEC - sh, C, chunk_pack(o));
+          else
+            chunk_store<XT, AL>(dx + m * C, (v * T + t) * VEC, C, chunk_pack(o));
         }
       }
     }
@@ -144,12 +271,12 @@ __global__ void __launch_bounds__(T > 32 ? T : 256, bwd_ctas(T, NV, AL))
     for (int v = 0; v < NV; ++v)
 #pragma unroll
       for (int j = 0; j < P; ++j) {
-        const int c = (v * T + t) * VEC + 2 * j;
-        if (c < C) {
+        const int c = (v * T + t) * VEC - sh + 2 * j;
+        if ((unsigned)c < (unsigned)C) {
           out[c] = ag[v].v[j].x;
           out[C + c] = ab[v].v[j].x;
         }
-        if (c + 1 < C) {
+        if ((unsigned)(c + 1) < (unsigned)C) {
           out[c + 1] = ag[v].v[j].y;
           out[C + c + 1] = ab[v].v[j].y;
         }
@@ -184,8 +311,8 @@ __global__ void __launch_bounds__(T > 32 ? T : 256, bwd_ctas(T, NV, AL))
       __syncthreads();
     }
     for (int c = threadIdx.x; c < C; c += NT) {
-      out[c] = col[c];
-      out[C + c] = col[W + c];
+      out[c] = col[c + sh];
+      out[C + c] = col[W + c + sh];
     }
   }
 }
@@ -223,33 +350,49 @@ __global__ void __launch_bounds__(1024) norm_reduce_kernel(const float *__restri
 }
 
 struct BwdSplitRows {
-  int64_t rpc;  // rows per CTA
-  int parts;    // CTAs
+  int64_t rpc;             // rows per CTA
+  int parts, per_class;    // CTAs; of a class of rows in step (else all of them)
 };
 
 // The split of the rows over CTAs, from the shape alone: the CTAs that 152 SMs hold at once (a second,
 // shorter wave of them took as long as the first: 102 against 77 us for 768 x 768 rows of 128),
 // at least two rows for each group of threads that holds a row.
-BwdSplitRows split_rows(const tri_norm_shape &s, int geo, bool aligned) {
+BwdSplitRows split_rows(const tri_norm_shape &s, int geo, int rows_are) {
   const int T = norm_threads_per_row(geo), RPC = T > 32 ? 1 : 256 / T;
   const int nv = geo == kNormT32x2 || geo == kNormT256x2 || geo == kNormT512x2 ? 2 : geo == kNormT512x4 ? 4 : 1;
-  const int per_sm = bwd_ctas(T, nv, aligned);
-  const int64_t target = 152 * per_sm;
-  int64_t rpc = (s.M + target - 1) / target;
+  const int classes = rows_are == kRowsInStep ? (s.dtype == TRI_DTYPE_FP32 ? 4 : 8) : 1;
+  const int64_t target = 152 * bwd_ctas(T, nv, rows_are != kAnyRows) / classes, M = (s.M + classes - 1) / classes;
+  int64_t rpc = (M + target - 1) / target;
   rpc = std::max<int64_t>((rpc + RPC - 1) / RPC * RPC, 2 * RPC);
-  return {rpc, (int)((s.M + rpc - 1) / rpc)};
+  const int per_class = (int)((M + rpc - 1) / rpc);
+  return {rpc, classes * per_class, per_class};
 }
 
+// How the rows of a call lie, and its geometry. (In step the row's chunks can be one more.)
+struct BwdRows {
+  int rows, geo;
+};
+int step_chunks(int C, int vec) { return (C + 2 * vec - 2) / vec; }
+// 8000 rows of 4001 BF16 values take 110 us one by one and 48 in step, 10007 of 1003 FP16 values 28 and 24; but not
+// where the one chunk more is held by twice the threads: 50000 of 250 BF16 values 29 and 34.
+bool step_pays(int C, int vec) {
+  const int n = step_chunks(C, vec);
+  return n * vec <= TRI_NORM_MAX_C && (n > 128 || norm_geometry(n, true) == norm_geometry((C + vec - 1) / vec, true));
+}
 template <typename XT>
-int geometry_of(const tri_norm_shape &s, const void *x, const int8_t *q8, const float *gamma, const void *dy,
-                const void *dx, bool *al) {
+BwdRows rows_of(const tri_norm_shape &s, const void *x, const int8_t *q8, const float *gamma, const void *dy, const void *dx) {
   constexpr int VEC = Chunk<XT>::VEC;
   const int64_t ldx = s.ldx ? s.ldx : s.C, lddy = s.lddy ? s.lddy : s.C;
-  *al = s.C % VEC == 0 && (q8 || ldx % VEC == 0) && lddy % VEC == 0 &&
-        ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(gamma) | reinterpret_cast<uintptr_t>(dy) |
-          reinterpret_cast<uintptr_t>(dx)) & 15u) == 0 &&
-        (reinterpret_cast<uintptr_t>(q8) & (VEC - 1)) == 0;
-  return norm_geometry((s.C + VEC - 1) / VEC, *al);
+  const uintptr_t xa = reinterpret_cast<uintptr_t>(x), da = reinterpret_cast<uintptr_t>(dy), oa = reinterpret_cast<uintptr_t>(dx);
+  const bool al = s.C % VEC == 0 && (q8 || ldx % VEC == 0) && lddy % VEC == 0 &&
+                  ((xa | reinterpret_cast<uintptr_t>(gamma) | da | oa) & 15u) == 0 && (reinterpret_cast<uintptr_t>(q8) & (VEC - 1)) == 0;
+  const int chunks = (s.C + VEC - 1) / VEC;
+  if (al) return {kAlignedRows, norm_geometry(chunks, true)};
+  // (the checkpoint's rows are in step if its start is as many values from a multiple of VEC as dx's)
+  const bool step = (q8 ? (reinterpret_cast<uintptr_t>(q8) - oa / sizeof(XT)) % VEC == 0 : ldx % VEC == s.C % VEC && ((xa ^ oa) & 15u) == 0) &&
+                    lddy % VEC == s.C % VEC && ((da ^ oa) & 15u) == 0 && oa % sizeof(XT) == 0;
+  if (step && step_pays(s.C, VEC)) return {kRowsInStep, norm_geometry(step_chunks(s.C, VEC), true)};
+  return {kAnyRows, norm_geometry(chunks, false)};
 }
 
 template <typename XT>
@@ -257,24 +400,27 @@ cudaError_t launch_bwd_t(const tri_norm_shape &s, const void *x, const int8_t *q
                          const float *mean, const float *rstd, const void *dy, void *dx, float *dgamma, float *dbeta,
                          float *part, cudaStream_t st) {
   constexpr int VEC = Chunk<XT>::VEC;
-  bool al;
-  const int geo = geometry_of<XT>(s, x, q8, gamma, dy, dx, &al);
-  const BwdSplitRows sp = split_rows(s, geo, al);
+  const BwdRows r = rows_of<XT>(s, x, q8, gamma, dy, dx);
+  const BwdSplitRows sp = split_rows(s, r.geo, r.rows);
   const int64_t ldx = s.ldx ? s.ldx : s.C, lddy = s.lddy ? s.lddy : s.C;
   const XT *dyp = static_cast<const XT *>(dy);
   XT *dxp = static_cast<XT *>(dx);
-#define LAUNCH(T, NV, AL)                                                                                                \
-  if constexpr (T * NV * VEC <= TRI_NORM_MAX_C) {                                                                        \
-    constexpr int NT = T > 32 ? T : 256;                                                                                 \
-    if (q8)                                                                                                              \
-      norm_bwd_kernel<XT, T, NV, AL, true><<<sp.parts, NT, 0, st>>>(nullptr, 0, q8, s8, gamma, mean, rstd, dyp, lddy, s.M, \
-                                                                    s.C, sp.rpc, dxp, part);                             \
-    else                                                                                                                 \
-      norm_bwd_kernel<XT, T, NV, AL, false><<<sp.parts, NT, 0, st>>>(static_cast<const XT *>(x), ldx, nullptr, nullptr,  \
-                                                                     gamma, mean, rstd, dyp, lddy, s.M, s.C, sp.rpc, dxp, \
-                                                                     part);                                              \
+#define LAUNCH_ROWS(T, NV, ROWS, Q8)                                                                                   \
+  norm_bwd_kernel<XT, T, NV, ROWS, Q8><<<sp.parts, (T > 32 ? T : 256), 0, st>>>(                                       \
+      static_cast<const XT *>(x), ldx, q8, s8, gamma, mean, rstd, dyp, lddy, s.M, s.C, sp.rpc, sp.per_class, dxp, part)
+#define LAUNCH(T, NV, AL)                                                                                              \
+  if constexpr (T * NV * VEC <= TRI_NORM_MAX_C) {                                                                      \
+    if (AL && r.rows == kRowsInStep && q8)                                                                             \
+      LAUNCH_ROWS(T, NV, (AL ? kRowsInStep : kAnyRows), true);                                                         \
+    else if (AL && r.rows == kRowsInStep)                                                                              \
+      LAUNCH_ROWS(T, NV, (AL ? kRowsInStep : kAnyRows), false);                                                        \
+    else if (q8)                                                                                                       \
+      LAUNCH_ROWS(T, NV, (AL ? kAlignedRows : kAnyRows), true);                                                        \
+    else                                                                                                               \
+      LAUNCH_ROWS(T, NV, (AL ? kAlignedRows : kAnyRows), false);                                                       \
   }
-  NORM_DISPATCH(geo, al, LAUNCH);
+  NORM_DISPATCH(r.geo, r.rows != kAnyRows, LAUNCH);
+#undef LAUNCH_ROWS
 #undef LAUNCH
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess && part) {
@@ -286,7 +432,10 @@ cudaError_t launch_bwd_t(const tri_norm_shape &s, const void *x, const int8_t *q
 // The largest number of partial sums any alignment of the call's pointers can lead to.
 size_t workspace_bytes_of(const tri_norm_shape &s) {
   const int vec = s.dtype == TRI_DTYPE_FP32 ? 4 : 8, chunks = (s.C + vec - 1) / vec;
-  const int parts = std::max(split_rows(s, norm_geometry(chunks, true), true).parts, split_rows(s, norm_geometry(chunks, false), false).parts);
+  int parts = std::max(split_rows(s, norm_geometry(chunks, true), kAlignedRows).parts,
+                       split_rows(s, norm_geometry(chunks, false), kAnyRows).parts);
+  if (step_pays(s.C, vec))
+    parts = std::max(parts, split_rows(s, norm_geometry(step_chunks(s.C, vec), true), kRowsInStep).parts);
   return sizeof(float) * (size_t)parts * 2 * s.C;
 }
 

@@ -24,7 +24,7 @@ DTYPES = [torch.bfloat16, torch.float16, torch.float32]
 # (rows, channels): every launch geometry, aligned and not, one row, one channel, group tails
 SIZES = [(1, 1), (5, 1), (1, 8), (3, 5), (7, 64), (33, 128), (100, 130), (17, 256), (9, 384), (40, 512), (64, 768),
          (5, 1003), (3, 1024), (12, 2048), (5, 4099), (2, 8192), (3, 8191), (2000, 16), (50, 27), (61, 59), (40, 121),
-         (300, 30)]
+         (300, 30), (700, 1003), (150, 4001), (77, 259)]
 
 
 def _u(dtype):
