@@ -79,60 +79,86 @@ __host__ __device__ __forceinline__ Span span_of(const T *p, int64_t rows, int64
   return Span{reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p + (rows - 1) * ld + C)};
 }
 
-// The 16 bytes at any address, from the two aligned 16-byte words around them (both inside the tensor).
-__device__ __forceinline__ uint4 ld_shifted(uintptr_t addr) {
-  const uint4 *at = reinterpret_cast<const uint4 *>(addr & ~uintptr_t(15));
-  const uint4 lo = __ldg(at), hi = __ldg(at + 1);
-  const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-  const bool one = (addr & 4) != 0, two = (addr & 8) != 0;
-  const uint32_t bits = 8 * (uint32_t)(addr & 3);
-  uint32_t t[7], u[5];
-#pragma unroll
-  for (int i = 0; i < 7; ++i) t[i] = one ? w[i + 1] : w[i];
-#pragma unroll
-  for (int i = 0; i < 5; ++i) u[i] = two ? t[i + 2] : t[i];
-  return make_uint4(__funnelshift_r(u[0], u[1], bits), __funnelshift_r(u[1], u[2], bits),
-                    __funnelshift_r(u[2], u[3], bits), __funnelshift_r(u[3], u[4], bits));
+// A chunk on its way: the values c .. c + VEC - 1 of a row. AL: the row starts on a 16-byte boundary and C is a
+// multiple of VEC, so a chunk is whole or absent. Else the two aligned 16-byte words around it (both inside
+// the tensor), or, at the tensor's ends, the values one by one; chunk_settle shifts the words and makes zeros of
+// what lies past C. The two are apart so that a thread's loads are in flight together: the shift waits for its words.
+template <bool AL>
+struct Fetched {
+  uint4 lo;
+};
+template <>
+struct Fetched<false> {
+  uint4 lo, hi;
+};
+__device__ __forceinline__ bool words_inside(uintptr_t addr, const Span &span) {
+  const uintptr_t at = addr & ~uintptr_t(15);
+  return at >= span.begin && at + 32 <= span.end;
 }
-
-// The chunk of values c .. c + VEC - 1 of a row (zeros past C). AL: the row starts on a 16-byte
-// boundary and C is a multiple of VEC, so a chunk is whole or absent. Else two aligned words and a
-// shift, or value by value at the ends of the tensor.
 template <typename XT, bool AL>
-__device__ __forceinline__ uint4 chunk_load(const XT *row, int c, int C, const Span &span) {
+__device__ __forceinline__ void chunk_fetch(Fetched<AL> &f, const XT *row, int c, int C, const Span &span) {
   constexpr int VEC = Chunk<XT>::VEC;
+  f.lo = make_uint4(0u, 0u, 0u, 0u);
   if constexpr (AL) {
-    return c < C ? ld_stream(reinterpret_cast<const uint4 *>(row + c)) : make_uint4(0u, 0u, 0u, 0u);
+    if (c < C) f.lo = ld_stream(reinterpret_cast<const uint4 *>(row + c));
   } else {
-    if (c >= C) return make_uint4(0u, 0u, 0u, 0u);
+    f.hi = f.lo;
+    if (c >= C) return;
+    const uintptr_t addr = reinterpret_cast<uintptr_t>(row + c);
+    if (words_inside(addr, span)) {
+      const uint4 *at = reinterpret_cast<const uint4 *>(addr & ~uintptr_t(15));
+      f.lo = __ldg(at);
+      f.hi = __ldg(at + 1);
+      return;
+    }
     uint32_t w[4] = {0u, 0u, 0u, 0u};
-    const uintptr_t addr = reinterpret_cast<uintptr_t>(row + c), at = addr & ~uintptr_t(15);
-    if (at >= span.begin && at + 32 <= span.end) {
-      const uint4 v = ld_shifted(addr);
-      w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-      if (c + VEC > C) {
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          if constexpr (sizeof(XT) == 2) {
-            if (c + j >= C) w[j / 2] &= (j & 1) ? 0x0000ffffu : 0xffff0000u;
-          } else {
-            if (c + j >= C) w[j] = 0u;
-          }
+    for (int j = 0; j < VEC; ++j) {
+      if (c + j >= C) continue;
+      if constexpr (sizeof(XT) == 2)
+        w[j / 2] |= (uint32_t)reinterpret_cast<const uint16_t *>(row)[c + j] << (16 * (j & 1));
+      else
+        w[j] = reinterpret_cast<const uint32_t *>(row)[c + j];
+    }
+    f.lo = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+template <typename XT, bool AL>
+__device__ __forceinline__ uint4 chunk_settle(const Fetched<AL> &f, const XT *row, int c, int C, const Span &span) {
+  if constexpr (AL) {
+    return f.lo;
+  } else {
+    constexpr int VEC = Chunk<XT>::VEC;
+    const uintptr_t addr = reinterpret_cast<uintptr_t>(row + c);
+    if (c >= C || !words_inside(addr, span)) return f.lo;
+    const uint32_t v[8] = {f.lo.x, f.lo.y, f.lo.z, f.lo.w, f.hi.x, f.hi.y, f.hi.z, f.hi.w};
+    const bool one = (addr & 4) != 0, two = (addr & 8) != 0;
+    const uint32_t bits = 8 * (uint32_t)(addr & 3);
+    uint32_t t[7], u[5], w[4];
+#pragma unroll
+    for (int i = 0; i < 7; ++i) t[i] = one ? v[i + 1] : v[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) u[i] = two ? t[i + 2] : t[i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(u[i], u[i + 1], bits);
+    if (c + VEC > C) {
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        if constexpr (sizeof(XT) == 2) {
+          if (c + j >= C) w[j / 2] &= (j & 1) ? 0x0000ffffu : 0xffff0000u;
+        } else {
+          if (c + j >= C) w[j] = 0u;
         }
       }
-    } else if constexpr (sizeof(XT) == 2) {
-      const uint16_t *p = reinterpret_cast<const uint16_t *>(row);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j)
-        if (c + j < C) w[j / 2] |= (uint32_t)p[c + j] << (16 * (j & 1));
-    } else {
-      const uint32_t *p = reinterpret_cast<const uint32_t *>(row);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j)
-        if (c + j < C) w[j] = p[c + j];
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
   }
+}
+template <typename XT, bool AL>
+__device__ __forceinline__ uint4 chunk_load(const XT *row, int c, int C, const Span &span) {
+  Fetched<AL> f;
+  chunk_fetch<XT, AL>(f, row, c, C, span);
+  return chunk_settle<XT, AL>(f, row, c, C, span);
 }
 
 template <typename XT, bool AL>
