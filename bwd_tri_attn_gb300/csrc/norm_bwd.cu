@@ -6,9 +6,8 @@
 // second kernel in a fixed order, without atomics, so the same call gives the same bits. The next
 // row's loads are issued before the current row's sums (memory bandwidth bounds the kernel).
 // 768 x 768 rows of 128 BF16 values: 88 us with the sum of the partials (5.2 TB/s, 77 % of a copy's
-// rate); 8192 rows of 2048 from the checkpoint: 25 us. Rows that do not start on 16-byte boundaries
-// take more instructions than memory time: 10007 rows of 1003 FP16 values 28 us, where the bytes
-// want 9 (stores of 16 bytes made of neighbouring lanes' chunks took 32).
+// rate); 8192 rows of 2048 from the checkpoint: 25 us; 10007 rows of 1003 FP16 values 24 us (of 1024: 18,
+// where the bytes want 9: few rows a CTA, and 7 MB of partial sums).
 #include <algorithm>
 
 #include "launch.cuh"
@@ -18,8 +17,8 @@ namespace triattn {
 namespace {
 
 // Rows that a CTA which holds a row takes at a time: they share the barriers of their sums (10007 rows of
-// 1024 FP16 values: 21 us one by one, 18 in pairs). Unaligned rows, which want the issue slots, go one by
-// one (of 1003 values: 28 us, 30 in pairs).
+// 1024 FP16 values: 21 us one by one, 18 in pairs). Rows that begin anywhere, which want the issue slots,
+// go one by one (of 1003 values: 28 us, 30 in pairs).
 constexpr int bwd_rows(int T, int NV, bool AL) { return T > 32 && NV == 1 && AL ? 2 : 1; }
 // CTAs per SM that the registers are kept to: 768 threads, 512 where a thread holds more, at least one CTA.
 constexpr int bwd_ctas(int T, int NV, bool AL) {

@@ -154,6 +154,34 @@ def test_spaced_and_unaligned_rows(C, width, start, dtype):
         assert torch.equal(k.q8, q) and torch.equal(k.scale, s)
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float32], ids=str)
+@pytest.mark.parametrize("M,C,off", [(50, 259, 3), (9, 64, 1), (300, 1001, 2)])
+def test_backward_into_buffers_equally_far_from_a_boundary(M, C, off, dtype):
+    """x, dy and dx (and the checkpoint) that start the same number of values behind a 16-byte boundary; nothing is
+    written before or behind dx."""
+    x, dy = _normal((M, C), dtype, 20), _normal((M, C), dtype, 21, 1.0, 0.0)
+    gamma, _ = _weights(C, 22)
+    _, mean, rstd, kept = tb.norm_forward(x, gamma, checkpoint=True)
+    vec = 16 // x.element_size()
+    shape = tb.norm_shape_of(x, dy=dy)
+    ws = torch.empty(tb.tri_norm_bwd_workspace_size(shape), dtype=torch.uint8, device="cuda")
+
+    def shifted(t):
+        wide = torch.full((t.numel() + 2 * vec,), 7, dtype=t.dtype, device="cuda")
+        part = wide[off:off + t.numel()].view(t.shape)
+        part.copy_(t)
+        return wide, part
+
+    (_, xs), (_, ds), (wide, dx), (_, q8) = shifted(x), shifted(dy), shifted(x), shifted(kept.q8)
+    dgamma, dbeta = torch.empty_like(gamma), torch.empty_like(gamma)
+    for eight_bits in (False, True):
+        wide.fill_(7)
+        tb.tri_norm_bwd(shape, None if eight_bits else xs, q8 if eight_bits else None, kept.scale if eight_bits else None, gamma,
+                        mean, rstd, ds, dx, dgamma, dbeta, ws)
+        assert (wide[:off] == 7).all() and (wide[off + M * C:] == 7).all()
+        _check_backward(tb.checkpoint_unpack(kept, torch.float32) if eight_bits else x, gamma, mean, rstd, dy, (dx, dgamma, dbeta))
+
+
 def test_rows_far_from_zero():
     """A common offset of 1000: the variance is of the differences, not a difference of squares."""
     x = _normal((50, 384), torch.float32, 11, 0.5, 1000.0)
