@@ -114,6 +114,7 @@ __global__ void __launch_bounds__(T > 32 ? T : 256, bwd_ctas(T, NV, ROWS != kAny
                     XT *__restrict__ dx, float *__restrict__ part) {
   constexpr bool AL = ROWS == kAlignedRows, STEP = ROWS == kRowsInStep;
   constexpr int VEC = Chunk<XT>::VEC, P = VEC / 2, NT = T > 32 ? T : 256, RPC = NT / T, U = bwd_rows(T, NV, ROWS != kAnyRows);
+  constexpr bool kZeros = STEP && !Q8, kAgain = !kZeros && !(AL && NV == 1);  // (how columns outside the row are kept out)
   __shared__ float red[T > 32 ? 2 * T / 32 : 1][2 * U];
   __shared__ __align__(8) float col[T > 32 ? 2 : 2 * NV * T * VEC];
   RowSum<T, 2 * U> row_sum{red, 0};
@@ -144,6 +145,8 @@ __global__ void __launch_bounds__(T > 32 ? T : 256, bwd_ctas(T, NV, ROWS != kAny
   }
   const int64_t rows = (M - first + stride - 1) / stride;  // (of the class; M < first: none)
   const int64_t r0 = (STEP ? (int64_t)blockIdx.x - (int64_t)cls * per_class : (int64_t)blockIdx.x) * rpc, r1 = min(rows, r0 + rpc);
+  // (a thread of an aligned row with its one chunk past the row's end: the mean too is 0, and so is xh)
+  const bool idle = AL && NV == 1 && t * VEC >= C;
   // rows past the chunk are zeros, which add nothing and are not written (their threads still
   // join the sums)
   struct Row {
@@ -153,7 +156,7 @@ __global__ void __launch_bounds__(T > 32 ? T : 256, bwd_ctas(T, NV, ROWS != kAny
   auto load = [&](int64_t i, Row &r) {
     const bool live = i < r1;
     const int64_t m = first + stride * i;
-    r.mu = live ? __ldg(mean + m) : 0.f;
+    r.mu = live && !idle ? __ldg(mean + m) : 0.f;
     r.rs = live ? __ldg(rstd + m) : 0.f;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
@@ -199,7 +202,6 @@ __global__ void __launch_bounds__(T > 32 ? T : 256, bwd_ctas(T, NV, ROWS != kAny
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
         if constexpr (STEP) {
-          if constexpr (!Q8) in_row<XT>(row[u].x[v], (v * T + t) * VEC - sh, C);  // (8-bit values are finite all the same)
           in_row<XT>(row[u].d[v], (v * T + t) * VEC - sh, C);
         }
         if constexpr (Q8) {
@@ -227,9 +229,20 @@ __global__ void __launch_bounds__(T > 32 ? T : 256, bwd_ctas(T, NV, ROWS != kAny
         Pairs<XT> d;
         chunk_unpack(row[u].d[v], d);
 #pragma unroll
+        for (int j = 0; j < P; ++j) xh[u][v].v[j] = __fmul2_rn(__fadd2_rn(xh[u][v].v[j], neg), rs2);
+        if constexpr (kZeros) {  // (what was loaded there is a neighbour's)
+          const int c = (v * T + t) * VEC - sh;
+          if (c < 0 || c + VEC > C) {
+#pragma unroll
+            for (int j = 0; j < P; ++j) {
+              if ((unsigned)(c + 2 * j) >= (unsigned)C) xh[u][v].v[j].x = 0.f;
+              if ((unsigned)(c + 2 * j + 1) >= (unsigned)C) xh[u][v].v[j].y = 0.f;
+            }
+          }
+        }
+#pragma unroll
         for (int j = 0; j < P; ++j) {
-          // (columns past C: dy is zero there, so they add nothing to any sum)
-          xh[u][v].v[j] = __fmul2_rn(__fadd2_rn(xh[u][v].v[j], neg), rs2);
+          // (columns outside the row: dy is zero there, so they add nothing to a sum but for the NaN seen to below)
           ag[v].v[j] = __ffma2_rn(d.v[j], xh[u][v].v[j], ag[v].v[j]);
           ab[v].v[j] = __fadd2_rn(ab[v].v[j], d.v[j]);
           dz[u][v].v[j] = __fmul2_rn(d.v[j], gm[v].v[j]);
@@ -241,6 +254,31 @@ __global__ void __launch_bounds__(T > 32 ? T : 256, bwd_ctas(T, NV, ROWS != kAny
       s[2 * u + 1] = s1.x + s1.y;
     }
     row_sum(s);
+    // Outside the row xh is (0 - mean) rstd, an infinity where |mean| rstd passes the largest number, and 0 x inf a
+    // NaN: such a row's sum is taken again over its own columns. (The lanes of a warp, and a CTA that holds a
+    // row, go there together.) Zeros for xh out there, in every row, were slower: 8192 x 8192 BF16 88 us, 112 so, 87 as it is.
+    bool lost = false;
+#pragma unroll
+    for (int u = 0; u < U; ++u) lost |= isnan(s[2 * u + 1]);
+    if (kAgain && (T > 32 ? lost : __any_sync(0xffffffffu, lost))) {
+      float own[2 * U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        own[2 * u] = own[2 * u + 1] = 0.f;
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+          for (int j = 0; j < P; ++j) {
+            const int c = (v * T + t) * VEC - sh + 2 * j;
+            if ((unsigned)c < (unsigned)C) own[2 * u + 1] = fmaf(dz[u][v].v[j].x, xh[u][v].v[j].x, own[2 * u + 1]);
+            if ((unsigned)(c + 1) < (unsigned)C) own[2 * u + 1] = fmaf(dz[u][v].v[j].y, xh[u][v].v[j].y, own[2 * u + 1]);
+          }
+      }
+      row_sum(own);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (isnan(s[2 * u + 1])) s[2 * u + 1] = own[2 * u + 1];
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const float a = -s[2 * u] * inv_c, b = -s[2 * u + 1] * inv_c;
