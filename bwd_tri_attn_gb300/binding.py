@@ -257,24 +257,44 @@ def _on_device(device, *checked):
     return device
 
 
-def _stream_on(device, stream):
-    """The raw handle of `stream`, or of the device's current stream (as _stream, with less work on the host)."""
+def _raw_stream(device):
+    """The raw handle of the device's current stream (as _stream, with less work on the host)."""
+    return _raw_stream_of(device) if _raw_stream_of is not None else torch.cuda.current_stream().cuda_stream
+
+
+def _other_stream(stream):
+    """The stream that an allocating helper was given (a torch stream or a raw handle), if it is not the current one."""
     if stream is None:
-        return _raw_stream_of(device) if _raw_stream_of is not None else torch.cuda.current_stream().cuda_stream
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        return None
+    if isinstance(stream, torch.cuda.Stream) and stream.device_index != torch.cuda.current_device():
+        raise ValueError(f"stream must be one of the current device's, got {stream}")
+    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    current = torch.cuda.current_stream().cuda_stream
+    if handle == current or (handle, current) == (1, 0):
+        return None
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    if handle == 2:  # cudaStreamPerThread: torch can make no stream object of it, and so cannot keep its memory
+        raise ValueError("the per-thread default stream cannot be given to a call that allocates")
+    return torch.cuda.ExternalStream(handle) if handle > 1 else torch.cuda.default_stream()  # (1: cudaStreamLegacy)
 
 
-def _used_on(stream, device, *tensors):
-    """What a call allocated on the current stream and uses on `stream`: its memory is not given out again before
-    that stream has passed the call, whenever the tensors are dropped."""
-    handle = _stream_on(device, stream)
-    if handle == _stream_on(device, None):
-        return
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
-    for t in tensors:
-        if t is not None:
-            t.record_stream(stream)
+def _called_on(stream, call, *args, workspace=None, **kwargs):
+    """call(*args) with `stream` in the place of the caller's current one. What it allocates is that stream's memory:
+    memory that the caller's stream has been given back may still be in use by what runs there. The results are not
+    given out again before the caller's stream has passed whatever it does with them until they are dropped."""
+    caller = torch.cuda.current_stream()
+    if workspace is not None:
+        kwargs["workspace"] = workspace
+    with torch.cuda.stream(stream):
+        out = call(*args, **kwargs)
+    if workspace is not None:
+        workspace.record_stream(stream)
+    for t in out if isinstance(out, tuple) else (out,):
+        for r in t if isinstance(t, tuple) else (t,):
+            if r is not None:
+                r.record_stream(caller)
+    return out
 
 
 def _ptr(t):
@@ -565,12 +585,15 @@ def tri_attn_set_timing_events(events) -> None:
 
 
 # ----------------------------------------------------------------------------
-# Allocating conveniences (outputs are fresh torch tensors on Q's device).
+# Allocating conveniences (outputs are fresh torch tensors on Q's device; those of a call that is given a
+# stream belong to that stream).
 # ----------------------------------------------------------------------------
 
 def forward(Q, K, V, bias, mask=None, scale=None, residual=True, stream=None, node=NODE_STARTING):
     """Returns (O, LSE, Ores); Ores is None when ``residual`` is False. O and Ores have Q's
     layout; LSE is [B, S, H, N] in terms of the attention's slices and positions."""
+    if (other := _other_stream(stream)) is not None:
+        return _called_on(other, forward, Q, K, V, bias, mask, scale, residual, node=node)
     shape = shape_of(Q, scale, node)
     B, S, N, H = shape.B, shape.S, shape.N, shape.H
     O = torch.empty_like(Q)
@@ -588,6 +611,8 @@ def workspace_for(shape: Shape, device) -> torch.Tensor:
 def backward(Q, K, V, bias, mask, O, Ores, LSE, dO, scale=None, workspace=None, stream=None,
              node=NODE_STARTING):
     """Returns (dQ, dK, dV, dBias)."""
+    if (other := _other_stream(stream)) is not None:
+        return _called_on(other, backward, Q, K, V, bias, mask, O, Ores, LSE, dO, scale, workspace=workspace, node=node)
     shape = shape_of(Q, scale, node)
     if workspace is None:
         workspace = workspace_for(shape, Q.device)
@@ -612,6 +637,8 @@ def mul_shape_of(Pa: torch.Tensor, incoming: bool = False, layout: int = LAYOUT_
 def mul_forward(Pa, Ga, Pb, Gb, incoming=False, layout=LAYOUT_PAIR, stream=None):
     """Returns (X, A, Bm): X [B, C, N, N] channel-major, and the gated operands A, Bm
     [B, C, N, N] that mul_backward reads."""
+    if (other := _other_stream(stream)) is not None:
+        return _called_on(other, mul_forward, Pa, Ga, Pb, Gb, incoming, layout)
     shape = mul_shape_of(Pa, incoming, layout)
     B, N, C = shape.B, shape.N, shape.C
     A, Bm, X = (torch.empty((B, C, N, N), dtype=torch.bfloat16, device=Pa.device) for _ in range(3))
@@ -621,6 +648,8 @@ def mul_forward(Pa, Ga, Pb, Gb, incoming=False, layout=LAYOUT_PAIR, stream=None)
 
 def mul_backward(Pa, Ga, Pb, Gb, A, Bm, dX, incoming=False, layout=LAYOUT_PAIR, workspace=None, stream=None):
     """Returns (dPa, dGa, dPb, dGb) in the projections' layout; dX is channel-major."""
+    if (other := _other_stream(stream)) is not None:
+        return _called_on(other, mul_backward, Pa, Ga, Pb, Gb, A, Bm, dX, incoming, layout, workspace=workspace)
     shape = mul_shape_of(Pa, incoming, layout)
     if workspace is None:
         workspace = torch.empty(max(tri_mul_bwd_workspace_size(shape), 16), dtype=torch.uint8, device=Pa.device)
@@ -639,6 +668,8 @@ def module_shape_of(z: torch.Tensor, H: int, d: int, node: int = NODE_STARTING, 
 
 def module_forward(z, gamma, beta, W, wb, Wo, mask, H, d, node=NODE_STARTING, eps=1e-5, stream=None):
     """Returns (out, saved): out [B, N, N, c] and the activations module_backward reads."""
+    if (other := _other_stream(stream)) is not None:
+        return _called_on(other, module_forward, z, gamma, beta, W, wb, Wo, mask, H, d, node, eps)
     shape = module_shape_of(z, H, d, node, eps)
     saved = torch.empty(max(tri_module_saved_size(shape), 16), dtype=torch.uint8, device=z.device)
     out = torch.empty_like(z)
@@ -649,6 +680,8 @@ def module_forward(z, gamma, beta, W, wb, Wo, mask, H, d, node=NODE_STARTING, ep
 def module_backward(z, gamma, beta, W, wb, Wo, mask, saved, dout, H, d, node=NODE_STARTING, eps=1e-5,
                     workspace=None, stream=None):
     """Returns (dz, dgamma, dbeta, dW, dwb, dWo); the weight gradients are FP32."""
+    if (other := _other_stream(stream)) is not None:
+        return _called_on(other, module_backward, z, gamma, beta, W, wb, Wo, mask, saved, dout, H, d, node, eps, workspace=workspace)
     shape = module_shape_of(z, H, d, node, eps)
     if workspace is None:
         workspace = torch.empty(max(tri_module_bwd_workspace_size(shape), 16), dtype=torch.uint8, device=z.device)
@@ -686,6 +719,8 @@ def _empty_checkpoint(x):
 def norm_forward(x, gamma=None, beta=None, eps=1e-5, checkpoint=False, stream=None):
     """LayerNorm over the last axis of x [..., C]: returns (y, mean, rstd), y in x's dtype and the FP32 statistics
     [...]; with ``checkpoint`` also the 8-bit checkpoint of x, written in the same pass."""
+    if (other := _other_stream(stream)) is not None:
+        return _called_on(other, norm_forward, x, gamma, beta, eps, checkpoint)
     shape = norm_shape_of(x, eps)
     device = _on_device(x.get_device(), ("x", x), _arg(gamma, "gamma", _F32, shape.C, True),
                         _arg(beta, "beta", _F32, shape.C, True))
@@ -694,16 +729,16 @@ def norm_forward(x, gamma=None, beta=None, eps=1e-5, checkpoint=False, stream=No
     kept = _empty_checkpoint(x) if checkpoint else None
     q8, scale = (kept.q8.data_ptr(), kept.scale.data_ptr()) if checkpoint else (None, None)
     rc = load().tri_norm_fwd(shape, x.data_ptr(), _ptr(gamma), _ptr(beta), y.data_ptr(), mean.data_ptr(),
-                             rstd.data_ptr(), q8, scale, _stream_on(device, stream))
+                             rstd.data_ptr(), q8, scale, _raw_stream(device))
     _check("tri_norm_fwd", rc)
-    if stream is not None:
-        _used_on(stream, device, y, mean, rstd, *(kept or ()))
     return (y, mean, rstd, kept) if checkpoint else (y, mean, rstd)
 
 
 def norm_backward(x, gamma, mean, rstd, dy, workspace=None, stream=None):
     """Returns (dx, dgamma, dbeta): dx in dy's dtype, the weight gradients FP32 (None when gamma is None, the
     LayerNorm without weights). ``x`` is the forward's input or its ``Checkpoint``; mean and rstd are the forward's."""
+    if (other := _other_stream(stream)) is not None:
+        return _called_on(other, norm_backward, x, gamma, mean, rstd, dy, workspace=workspace)
     dtype = _norm_dtype(dy, "dy")
     kept = x if isinstance(x, tuple) else None
     like = kept[0] if kept is not None else x
@@ -730,37 +765,35 @@ def norm_backward(x, gamma, mean, rstd, dy, workspace=None, stream=None):
     xp, q8, scale = (None, kept[0].data_ptr(), kept[1].data_ptr()) if kept is not None else (x.data_ptr(), None, None)
     rc = load().tri_norm_bwd(shape, xp, q8, scale, _ptr(gamma), mean.data_ptr(), rstd.data_ptr(), dy.data_ptr(),
                              dx.data_ptr(), _ptr(dgamma), _ptr(dbeta), _ptr(workspace), _nbytes(workspace),
-                             _stream_on(device, stream))
+                             _raw_stream(device))
     _check("tri_norm_bwd", rc)
-    if stream is not None:
-        _used_on(stream, device, dx, dgamma, dbeta, workspace)
     return dx, dgamma, dbeta
 
 
 def checkpoint_pack(x, stream=None) -> Checkpoint:
     """x [..., C] kept in 8 bits: int8 values and one FP32 scale for every 128 channels of a row."""
+    if (other := _other_stream(stream)) is not None:
+        return _called_on(other, checkpoint_pack, x)
     shape = norm_shape_of(x)
     device = _on_device(x.get_device(), ("x", x))
     kept = _empty_checkpoint(x)
     rc = load().tri_ckpt_pack(shape, x.data_ptr(), kept.q8.data_ptr(), kept.scale.data_ptr(),
-                              _stream_on(device, stream))
+                              _raw_stream(device))
     _check("tri_ckpt_pack", rc)
-    if stream is not None:
-        _used_on(stream, device, *kept)
     return kept
 
 
 def checkpoint_unpack(kept, dtype=torch.bfloat16, stream=None) -> torch.Tensor:
     """The values a checkpoint stands for, rounded once to ``dtype``."""
+    if (other := _other_stream(stream)) is not None:
+        return _called_on(other, checkpoint_unpack, kept, dtype)
     q8, scale = kept
     x = torch.empty(q8.shape, dtype=dtype, device=q8.device)
     shape = norm_shape_of(x)
     n, ng = _norm_counts(shape)
     device = _on_device(x.get_device(), _arg(q8, "q8", torch.int8, n), _arg(scale, "scale", _F32, ng))
-    rc = load().tri_ckpt_unpack(shape, q8.data_ptr(), scale.data_ptr(), x.data_ptr(), _stream_on(device, stream))
+    rc = load().tri_ckpt_unpack(shape, q8.data_ptr(), scale.data_ptr(), x.data_ptr(), _raw_stream(device))
     _check("tri_ckpt_unpack", rc)
-    if stream is not None:
-        _used_on(stream, device, x)
     return x
 
 
@@ -796,6 +829,8 @@ def cross_forward(Q, K, V, mask=None, kv_lens=None, scale=None, workspace=None, 
     """Cross attention of the queries Q [B, T, H, d] to the encoder states K, V [B, S, Hk, d] (BF16; heads, positions
     and batches may be spaced apart). mask: bool or uint8 [B, S], False where a key is not to be attended; kv_lens:
     int32 [B]. Returns (O, LSE): O [B, T, H, d] and the FP32 log-sum-exp [B, H, T] that cross_backward reads."""
+    if (other := _other_stream(stream)) is not None:
+        return _called_on(other, cross_forward, Q, K, V, mask, kv_lens, scale, workspace=workspace)
     shape, device = _cross_checked(Q, K, V, mask, kv_lens, scale, _arg(workspace, "workspace", None, None, True))
     B, T, H, _ = Q.shape
     O, LSE = _dense_like(Q), torch.empty((B, H, T), dtype=_F32, device=Q.device)
@@ -803,15 +838,15 @@ def cross_forward(Q, K, V, mask=None, kv_lens=None, scale=None, workspace=None, 
         workspace = _workspace(tri_cross_fwd_workspace_size(shape), Q)
     rc = load().tri_cross_fwd(shape, Q.data_ptr(), K.data_ptr(), V.data_ptr(), _ptr(mask), _ptr(kv_lens),
                               O.data_ptr(), LSE.data_ptr(), _ptr(workspace), _nbytes(workspace),
-                              _stream_on(device, stream))
+                              _raw_stream(device))
     _check("tri_cross_fwd", rc)
-    if stream is not None:
-        _used_on(stream, device, O, LSE, workspace)
     return O, LSE
 
 
 def cross_backward(Q, K, V, O, LSE, dO, mask=None, kv_lens=None, scale=None, workspace=None, stream=None):
     """Returns (dQ, dK, dV), without gaps, for the gradient dO of cross_forward's O."""
+    if (other := _other_stream(stream)) is not None:
+        return _called_on(other, cross_backward, Q, K, V, O, LSE, dO, mask, kv_lens, scale, workspace=workspace)
     n = Q.numel() if isinstance(Q, torch.Tensor) else None
     rows = n // Q.shape[-1] if n else None
     shape, device = _cross_checked(Q, K, V, mask, kv_lens, scale, _arg(O, "O", _BF16, n), _arg(LSE, "LSE", _F32, rows),
@@ -821,8 +856,6 @@ def cross_backward(Q, K, V, O, LSE, dO, mask=None, kv_lens=None, scale=None, wor
         workspace = _workspace(tri_cross_bwd_workspace_size(shape), Q)
     rc = load().tri_cross_bwd(shape, Q.data_ptr(), K.data_ptr(), V.data_ptr(), _ptr(mask), _ptr(kv_lens),
                               O.data_ptr(), LSE.data_ptr(), dO.data_ptr(), dQ.data_ptr(), dK.data_ptr(),
-                              dV.data_ptr(), _ptr(workspace), _nbytes(workspace), _stream_on(device, stream))
+                              dV.data_ptr(), _ptr(workspace), _nbytes(workspace), _raw_stream(device))
     _check("tri_cross_bwd", rc)
-    if stream is not None:
-        _used_on(stream, device, dQ, dK, dV, workspace)
     return dQ, dK, dV
