@@ -854,16 +854,20 @@ BwdGeo bwd_geo(const tri_cross_shape &s, int nsm) {
   return g;
 }
 
+// The main kernels' one-time set-up on the device: before the call's first launch, so that nothing is enqueued if it fails.
+template <int DP>
+cudaError_t prepare_bwd(int dev) {
+  static DeviceOnce ready;
+  if (ready.done(dev)) return cudaSuccess;
+  cudaError_t e = cudaFuncSetAttribute(cross_dkv_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, CDkv<DP>::SMEM);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(cross_dq_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, CDq<DP>::SMEM);
+  if (e == cudaSuccess) ready.mark(dev);
+  return e;
+}
+
 template <int DP>
 cudaError_t launch_bwd(const CUtensorMap &mq, const CUtensorMap &mdo, const CUtensorMap &mk, const CUtensorMap &mv,
-                       const CBwdArgs &dkv, const CBwdArgs &dq, const BwdGeo &g, int dev, cudaStream_t st) {
-  static DeviceOnce ready;
-  if (!ready.done(dev)) {
-    cudaError_t e = cudaFuncSetAttribute(cross_dkv_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, CDkv<DP>::SMEM);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(cross_dq_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, CDq<DP>::SMEM);
-    if (e != cudaSuccess) return e;
-    ready.mark(dev);
-  }
+                       const CBwdArgs &dkv, const CBwdArgs &dq, const BwdGeo &g, cudaStream_t st) {
   cudaError_t e = launch_after(cross_dkv_kernel<DP>, dim3(g.dkv_ctas), dim3(kBwdThreads), CDkv<DP>::SMEM, st, mq, mdo, mk, mv, dkv);
   if (e == cudaSuccess && g.dkv_split && g.dkv_ctas > 1) {
     e = launch_after(cross_join_kernel, dim3(g.dkv_ctas - 1, 2), dim3(kJoinThreads), 0, st, dkv, g.dkv_ctas);
@@ -941,12 +945,13 @@ int tri_cross_bwd(tri_cross_shape shape, const tri_attn_bf16 *Q, const tri_attn_
   CBwdArgs dkv = a, dq = a;
   dkv.sc = CrossSched{shape.B, shape.S, kv_lens, true, shape.Hk, (z.G / z.GB) * g.tiles, status};
   dq.sc = CrossSched{shape.B, shape.S, kv_lens, false, shape.H / z.GB, g.tiles, status};
+  if ((shape.d <= 64 ? prepare_bwd<64>(dev) : prepare_bwd<128>(dev)) != cudaSuccess) return TRI_ATTN_ERR_CUDA;
   const auto st = static_cast<cudaStream_t>(stream);
   const int row_blocks = (int)std::min<int64_t>((g.rows + 15) / 16, 152 * 16);
   cross_bwd_prep_kernel<<<row_blocks + (kv_lens ? 16 * shape.B : 0), 256, 0, st>>>(dkv, O, LSE, dO, nl, nd, row_blocks);
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess)
-    e = shape.d <= 64 ? launch_bwd<64>(mq, mdo, mk, mv, dkv, dq, g, dev, st) : launch_bwd<128>(mq, mdo, mk, mv, dkv, dq, g, dev, st);
+    e = shape.d <= 64 ? launch_bwd<64>(mq, mdo, mk, mv, dkv, dq, g, st) : launch_bwd<128>(mq, mdo, mk, mv, dkv, dq, g, st);
   return e == cudaSuccess ? TRI_ATTN_OK : TRI_ATTN_ERR_CUDA;
 }
 
