@@ -9,17 +9,26 @@
 
 namespace triattn {
 
-// cuTensorMapEncodeTiled through the runtime's driver entry point (no libcuda link).
+// A driver function through the runtime's entry points (no libcuda link).
+template <typename F>
+F driver_function(const char *name, unsigned version) {
+  void *p = nullptr;
+  cudaDriverEntryPointQueryResult q;
+  if (cudaGetDriverEntryPointByVersion(name, &p, version, cudaEnableDefault, &q) != cudaSuccess || q != cudaDriverEntryPointSuccess)
+    p = nullptr;
+  return reinterpret_cast<F>(p);
+}
+
+// cuTensorMapEncodeTiled, which wants a current context: a host thread (autograd's, say) has none before its
+// first runtime call that needs one, and gets its device's here. NULL: not to be had.
 inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-    void *p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) !=
-            cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      p = nullptr;
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  }();
+  static const auto fn = driver_function<PFN_cuTensorMapEncodeTiled_v12000>("cuTensorMapEncodeTiled", 12000);
+  static const auto current = driver_function<PFN_cuCtxGetCurrent_v4000>("cuCtxGetCurrent", 4000);
+  CUcontext ctx = nullptr;
+  if (!current || current(&ctx) != CUDA_SUCCESS || !ctx) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess) return nullptr;
+  }
   return fn;
 }
 

@@ -1,5 +1,5 @@
 // A stand-in for the CUDA runtime under the library's own objects: no GPU, every launch counted and none run, and a
-// chosen call made to fail. Entry points that the tests' calls only need to return take no parameters here (C linkage;
+// chosen call made to fail. The thread has no context before cudaSetDevice, as a fresh one. Entry points that the tests' calls only need to return take no parameters here (C linkage;
 // what the caller passes is left where it is).
 #include <driver_types.h>
 
@@ -9,7 +9,13 @@ namespace {
 int launches = 0;
 char failing[64] = "";
 int answer(const char *name) { return std::strcmp(name, failing) ? 0 : (int)cudaErrorInvalidValue; }
-int encode() { return answer("cuTensorMapEncodeTiled"); }
+bool has_context = false;
+int get_current(void **context) {
+  static int one;
+  *context = has_context ? &one : nullptr;
+  return 0;
+}
+int encode() { return has_context ? answer("cuTensorMapEncodeTiled") : 201; }  // (CUDA_ERROR_INVALID_CONTEXT)
 alignas(256) char device_memory[256];
 }  // namespace
 
@@ -41,6 +47,10 @@ int cudaGetDevice(int *device) {
   *device = 0;
   return answer("cudaGetDevice");
 }
+int cudaSetDevice() {
+  has_context = true;
+  return answer("cudaSetDevice");
+}
 int cudaDeviceGetAttribute(int *value) {
   *value = 152;
   return answer("cudaDeviceGetAttribute");
@@ -55,8 +65,8 @@ int cudaFuncGetAttributes(cudaFuncAttributes *a) {
   a->numRegs = 128;
   return answer("cudaFuncGetAttributes");
 }
-int cudaGetDriverEntryPointByVersion(const char *, void **p, unsigned, unsigned long long, int *status) {
-  *p = reinterpret_cast<void *>(&encode);
+int cudaGetDriverEntryPointByVersion(const char *name, void **p, unsigned, unsigned long long, int *status) {
+  *p = std::strcmp(name, "cuTensorMapEncodeTiled") ? reinterpret_cast<void *>(&get_current) : reinterpret_cast<void *>(&encode);
   *status = 0;
   return 0;
 }
