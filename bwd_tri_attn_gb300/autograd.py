@@ -2,9 +2,10 @@
 
 Every forward and backward step runs in the library's kernels through ``binding``; these classes
 only keep the tensors the backward pass needs and hand gradients back in the dtypes autograd
-expects. There is no CPU path: the library raises if it is missing or a call fails. Inputs are
-made contiguous (a no-op for contiguous tensors); dtypes and sizes are checked by the binding. The
-backward passes are differentiable once (no second derivatives).
+expects. There is no CPU path: the library raises if it is missing or a call fails. Inputs and
+gradients are made contiguous, and copied to a 16-byte boundary where the library wants one (a no-op
+for fresh tensors); dtypes and sizes are checked by the binding. The backward passes are
+differentiable once (no second derivatives).
 
 - ``triangle_attention(Q, K, V, bias, mask=None, node=NODE_STARTING)``: the attention core
   (include/tri_attn.h) with its residual-compensated backward; gradients for Q, K, V and bias.
@@ -31,11 +32,18 @@ from torch.autograd.function import once_differentiable
 from . import binding as tb
 
 
+def _dense(t):
+    """t contiguous from a 16-byte boundary on: t itself where it is (a contiguous view, such as a concatenation's
+    gradient, may begin anywhere), else a copy."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 class _TriangleAttention(torch.autograd.Function):
     @staticmethod
     def forward(ctx, Q, K, V, bias, mask, node):
-        Q, K, V, bias = (t.contiguous() for t in (Q, K, V, bias))
-        mask = None if mask is None else mask.contiguous()
+        Q, K, V, bias = (_dense(t) for t in (Q, K, V, bias))
+        mask = None if mask is None else _dense(mask)
         O, LSE, Ores = tb.forward(Q, K, V, bias, mask, node=node)
         ctx.node = node
         ctx.save_for_backward(Q, K, V, bias, mask, O, Ores, LSE)
@@ -46,7 +54,7 @@ class _TriangleAttention(torch.autograd.Function):
     def backward(ctx, dO):
         Q, K, V, bias, mask, O, Ores, LSE = ctx.saved_tensors
         dQ, dK, dV, dBias = tb.backward(Q, K, V, bias, mask, O, Ores, LSE,
-                                        dO.to(torch.bfloat16).contiguous(), node=ctx.node)
+                                        _dense(dO.to(torch.bfloat16)), node=ctx.node)
         return dQ, dK, dV, dBias, None, None
 
 
@@ -59,7 +67,7 @@ def triangle_attention(Q, K, V, bias, mask=None, node=tb.NODE_STARTING):
 class _TriangleMultiplication(torch.autograd.Function):
     @staticmethod
     def forward(ctx, Pa, Ga, Pb, Gb, incoming, layout):
-        Pa, Ga, Pb, Gb = (t.contiguous() for t in (Pa, Ga, Pb, Gb))
+        Pa, Ga, Pb, Gb = (_dense(t) for t in (Pa, Ga, Pb, Gb))
         X, A, Bm = tb.mul_forward(Pa, Ga, Pb, Gb, incoming=incoming, layout=layout)
         ctx.cfg = (incoming, layout)
         ctx.save_for_backward(Pa, Ga, Pb, Gb, A, Bm)
@@ -70,7 +78,7 @@ class _TriangleMultiplication(torch.autograd.Function):
     def backward(ctx, dX):
         Pa, Ga, Pb, Gb, A, Bm = ctx.saved_tensors
         incoming, layout = ctx.cfg
-        grads = tb.mul_backward(Pa, Ga, Pb, Gb, A, Bm, dX.to(torch.bfloat16).contiguous(), incoming=incoming,
+        grads = tb.mul_backward(Pa, Ga, Pb, Gb, A, Bm, _dense(dX.to(torch.bfloat16)), incoming=incoming,
                                 layout=layout)
         return (*grads, None, None)
 
@@ -84,10 +92,10 @@ def triangle_multiplication(Pa, Ga, Pb, Gb, incoming=False, layout=tb.LAYOUT_PAI
 class _TriangleAttentionBlock(torch.autograd.Function):
     @staticmethod
     def forward(ctx, z, gamma, beta, W, wb, Wo, mask, H, d, node, eps, checkpoint):
-        z = z.contiguous()
-        mask = None if mask is None else mask.contiguous()
-        bf = [t.to(torch.bfloat16).contiguous() for t in (W, wb, Wo)]
-        g32, b32 = gamma.float().contiguous(), beta.float().contiguous()
+        z = _dense(z)
+        mask = None if mask is None else _dense(mask)
+        bf = [_dense(t.to(torch.bfloat16)) for t in (W, wb, Wo)]
+        g32, b32 = _dense(gamma.float()), _dense(beta.float())
         out, saved = tb.module_forward(z, g32, b32, *bf, mask, H, d, node=node, eps=eps)
         ctx.meta = (H, d, node, eps, [t.dtype for t in (gamma, beta, W, wb, Wo)])
         ctx.kept_in_8_bits = checkpoint
@@ -104,7 +112,7 @@ class _TriangleAttentionBlock(torch.autograd.Function):
             _, saved = tb.module_forward(z, g32, b32, W, wb, Wo, mask, H, d, node=node, eps=eps)
         else:
             z, saved = kept
-        grads = tb.module_backward(z, g32, b32, W, wb, Wo, mask, saved, dout.to(torch.bfloat16).contiguous(),
+        grads = tb.module_backward(z, g32, b32, W, wb, Wo, mask, saved, _dense(dout.to(torch.bfloat16)),
                                    H, d, node=node, eps=eps)
         dz = grads[0]
         wgrads = [g.to(dt) for g, dt in zip(grads[1:], dtypes)]
@@ -166,7 +174,7 @@ class _CrossAttention(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dO):
         Q, K, V, mask, kv_lens, O, LSE = ctx.saved_tensors
-        grads = tb.cross_backward(Q, K, V, O, LSE, dO.to(torch.bfloat16).contiguous(), mask, kv_lens, ctx.scale)
+        grads = tb.cross_backward(Q, K, V, O, LSE, _dense(dO.to(torch.bfloat16)), mask, kv_lens, ctx.scale)
         return (*grads, None, None, None)
 
 
@@ -175,10 +183,7 @@ def _spaced(t):
     zero, a 16-byte aligned start), else a contiguous copy."""
     fits = t.dim() == 4 and (t.stride(3) == 1 or t.shape[3] == 1) and t.data_ptr() % 16 == 0 and all(
         n == 1 or (s >= t.shape[3] and s % 8 == 0) for n, s in zip(t.shape[:3], t.stride()[:3]))
-    if fits:
-        return t
-    t = t.contiguous()
-    return t if t.data_ptr() % 16 == 0 else t.clone()
+    return t if fits else _dense(t)
 
 
 def cross_attention(Q, K, V, mask=None, kv_lens=None, scale=None):
