@@ -76,6 +76,7 @@ class ModuleShape(ctypes.Structure):
 
 DTYPE_BF16, DTYPE_FP16, DTYPE_FP32 = 0, 1, 2  # tri_norm_shape.dtype
 CKPT_GROUP = 128  # channels that share a scale in an 8-bit checkpoint
+MAX_CHANNELS = 2 ** 31 - 128  # of a checkpointed row (TRI_CKPT_MAX_C; ctypes would cut a wider one to 32 bits)
 
 
 class NormShape(ctypes.Structure):
@@ -453,6 +454,13 @@ def _rows_arg(t, name, dtype, numel):
     return (name, t)
 
 
+def _channels(t, name):
+    C = t.shape[-1]
+    if C > MAX_CHANNELS:
+        raise ValueError(f"{name} has rows of {C} channels, of which there may be {MAX_CHANNELS}")
+    return C
+
+
 def _norm_counts(shape):
     return shape.M * shape.C, shape.M * ((shape.C + CKPT_GROUP - 1) // CKPT_GROUP)
 
@@ -699,7 +707,7 @@ def norm_shape_of(x: torch.Tensor, eps: float = 1e-5, dy: torch.Tensor | None = 
     dtype = _norm_dtype(x, "x")
     if x.dim() < 1 or x.numel() == 0:
         raise ValueError(f"x must have at least one row and one channel, got shape {tuple(x.shape)}")
-    C = x.shape[-1]
+    C = _channels(x, "x")
     return NormShape(x.numel() // C, _row_stride(x, "x"), C if dy is None else _row_stride(dy, "dy"), C, dtype,
                      float(eps))
 
@@ -747,7 +755,7 @@ def norm_backward(x, gamma, mean, rstd, dy, workspace=None, stream=None):
     n = dy.numel()
     if dy.dim() < 1 or n == 0:
         raise ValueError(f"dy must have at least one row and one channel, got shape {tuple(dy.shape)}")
-    C = dy.shape[-1]
+    C = _channels(dy, "dy")
     M = n // C
     shape = NormShape(M, C if kept is not None else _row_stride(x, "x"), _row_stride(dy, "dy"), C, dtype, 0.0)
     if kept is not None:

@@ -229,6 +229,7 @@ int norm_check_shape(const tri_norm_shape &s) {
     return TRI_ATTN_ERR_INVALID_ARG;
   if (s.dtype != TRI_DTYPE_BF16 && s.dtype != TRI_DTYPE_FP16 && s.dtype != TRI_DTYPE_FP32)
     return TRI_ATTN_ERR_INVALID_ARG;
+  if (s.C > TRI_CKPT_MAX_C) return TRI_ATTN_ERR_UNSUPPORTED;  // (a row's channels rounded up to whole groups fit an int)
   // every element offset (the largest row stride included) fits 62 bits
   const int64_t ld = std::max<int64_t>(std::max<int64_t>(s.ldx, s.lddy), s.C);
   if (s.M > (int64_t{1} << 40) || ld > (int64_t{1} << 62) / s.M) return TRI_ATTN_ERR_UNSUPPORTED;

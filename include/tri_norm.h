@@ -25,8 +25,9 @@
  * and all sums are FP32; the variance is the mean of the squared differences from the mean
  * (two passes over registers), and each 16-bit output is rounded once, to nearest even.
  *
- * Requirements: M >= 1, 1 <= C <= TRI_NORM_MAX_C, eps >= 0 finite, pointers aligned to their element
- * (16-byte aligned pointers and row strides take the wide loads), buffers not overlapping.
+ * Requirements: M >= 1, 1 <= C <= TRI_NORM_MAX_C (checkpoints alone: TRI_CKPT_MAX_C), eps >= 0 finite,
+ * pointers aligned to their element (16-byte aligned pointers and row strides take the wide loads),
+ * buffers not overlapping.
  * Return codes are the TRI_ATTN_* codes of tri_attn.h; a call that returns an error has enqueued
  * nothing (TRI_ATTN_ERR_CUDA from a launch itself excepted). Calls are asynchronous on `stream`
  * (a cudaStream_t, NULL = the legacy default stream), allocate nothing, keep no state between
@@ -44,6 +45,7 @@ extern "C" {
 
 #define TRI_NORM_MAX_C 8192
 #define TRI_CKPT_GROUP 128
+#define TRI_CKPT_MAX_C 2147483520 /* 2^31 - 128 */
 
 #define TRI_DTYPE_BF16 0
 #define TRI_DTYPE_FP16 1
@@ -77,7 +79,7 @@ int tri_norm_bwd(tri_norm_shape shape, const void *x, const int8_t *q8, const fl
                  const float *mean, const float *rstd, const void *dy, void *dx, float *dgamma, float *dbeta,
                  void *workspace, size_t workspace_bytes, void *stream);
 
-/* Checkpoint of x [M, C] (row stride ldx); C may be of any size here. */
+/* Checkpoint of x [M, C] (row stride ldx); C may be up to TRI_CKPT_MAX_C here. */
 int tri_ckpt_pack(tri_norm_shape shape, const void *x, int8_t *q8, float *scale8, void *stream);
 
 /* The values a checkpoint stands for, rounded once to shape.dtype: x [M, C] without gaps. */

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from bwd_tri_attn_gb300 import binding as tb
-from tests.test_norm_gpu import F, _normal, _u, _weights
+from tests.test_norm_gpu import F, _normal, _u, _values, _weights
 
 pytestmark = pytest.mark.gpu
 
@@ -34,3 +34,20 @@ def test_backward_of_constant_rows_far_from_zero(M, C, dtype, eight_bits):
     assert ((dx.double() - want).abs() <= _u(dtype) * want.abs() + 2 * F * mag).all()
     assert (dgamma == 0).all()
     assert ((dbeta.double() - dy.double().sum(0)).abs() <= 2 * F * dy.double().abs().sum(0)).all()
+
+
+@pytest.mark.parametrize("M,C,dtype", [(1, 2 ** 31 - 128, torch.bfloat16), (3, 2 ** 29 + 5, torch.float16)], ids=str)
+def test_checkpoints_of_the_widest_rows(M, C, dtype):
+    """Rows of billions of channels, checked group by group at their ends and on either side of 2^31 bytes."""
+    x = torch.empty((M, C), dtype=dtype, device="cuda").normal_()
+    kept = tb.checkpoint_pack(x)
+    back = tb.checkpoint_unpack(kept, dtype)
+    assert kept.scale.shape == (M, (C + 127) // 128)
+    for m in range(M):
+        for g in (0, 2 ** 22 - 64, 2 ** 23 - 64, 2 ** 24 - 2 ** 10, (C - 1) // 128 - 63):
+            a, b = 128 * g, min(128 * (g + 64), C)
+            if a >= C:
+                continue
+            q, s, v = _values(x[m:m + 1, a:b])
+            assert torch.equal(kept.q8[m:m + 1, a:b], q) and torch.equal(kept.scale[m:m + 1, g:g + s.shape[1]], s)
+            assert torch.equal(back[m:m + 1, a:b], v.to(dtype))
