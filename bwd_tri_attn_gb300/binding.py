@@ -814,6 +814,8 @@ def cross_shape_of(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, scale: flo
             raise ValueError(f"{name} must have four axes (batch, position, head, channel), got shape {tuple(t.shape)}")
     B, T, H, d = Q.shape
     _, S, Hk, _ = K.shape
+    if max(B, T, S, H, Hk, d) >= 1 << 31:  # (ctypes would cut it to 32 bits)
+        raise ValueError(f"an axis is too long: Q has shape {tuple(Q.shape)}, K {tuple(K.shape)}")
     if scale is None:
         scale = 1.0 / math.sqrt(d) if d else 0.0
     return CrossShape(B, T, S, H, Hk, d, scale, Q.stride()[:3], K.stride()[:3], V.stride()[:3])

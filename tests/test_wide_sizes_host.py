@@ -37,3 +37,15 @@ def test_channels_of_the_c_calls(C):
     three = [ctypes.c_void_p(FAKE)] * 3
     assert tb.load().tri_ckpt_pack(shape, *three, None) == -2
     assert tb.load().tri_ckpt_unpack(shape, *three, None) == -2
+
+
+@pytest.mark.parametrize("q,k", [((1, 2, 4, 64), (1, 2 ** 32 + 8, 2, 64)), ((1, 2 ** 32 + 1, 4, 64), (1, 5, 2, 64)),
+                                 ((2 ** 32 + 1, 1, 1, 8), (2 ** 32 + 1, 1, 1, 8)), ((1, 2, 2 ** 32 + 4, 64), (1, 5, 2, 64)),
+                                 ((1, 2, 4, 64), (1, 5, 2 ** 31, 64)), ((1, 2, 4, 2 ** 32 + 64), (1, 5, 2, 2 ** 32 + 64))])
+def test_axes_of_cross_attention(q, k):
+    Q, K = meta(*q), meta(*k)
+    lse = meta(q[0], q[2], q[1], dtype=torch.float32)
+    for call in (lambda: tb.cross_shape_of(Q, K, K), lambda: tb.cross_forward(Q, K, K),
+                 lambda: tb.cross_backward(Q, K, K, Q, lse, Q)):
+        with pytest.raises(ValueError, match="too long"):
+            call()
