@@ -692,6 +692,7 @@ int cross_check_shape(const tri_cross_shape &s) {
   if (s.B < 1 || s.T < 1 || s.S < 1 || s.H < 1 || s.Hk < 1 || s.d < 1 || s.H % s.Hk || !isfinite(s.scale))
     return TRI_ATTN_ERR_INVALID_ARG;
   if (s.d % 8 || s.d > 128 || s.B > 65535 || s.H > 1024) return TRI_ATTN_ERR_UNSUPPORTED;
+  if (!isfinite(s.scale * kLog2e)) return TRI_ATTN_ERR_UNSUPPORTED;  // (what scores are multiplied by)
   // an item has at most 2^19 units, so that a wait for its end (about 0.8 s at 1.5 us a unit) stays below the
   // waits' time limit
   if (s.S > (1 << 26) || (int64_t)s.T * (s.H / s.Hk) > (1 << 26)) return TRI_ATTN_ERR_UNSUPPORTED;

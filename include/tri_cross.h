@@ -26,13 +26,17 @@
  * rounded to BF16 as operands of the second products; statistics and sums are FP32.
  *
  * Requirements: B, T, S, H, Hk >= 1; 8 <= d <= 128, a multiple of 8; B <= 65535, H <= 1024; S and
- * T H / Hk at most 2^26; scale finite; Q, K, V and dO finite wherever they are live; pointers 16-byte aligned
- * (kv_lens: 4, mask: any), buffers not overlapping. Return codes are the TRI_ATTN_* codes of tri_attn.h;
- * a call that returns an error has enqueued nothing (TRI_ATTN_ERR_CUDA from a launch itself
- * excepted). Calls are asynchronous on `stream`, allocate no device memory and keep no state
- * between calls; a workspace may be used again once the call that uses it has finished. No
- * floating-point atomics: for the same shape, lengths and GPU model a call gives the same bits.
- * Kernels never trap; a bounded device wait that expires records TRI_ATTN_ERR_TIMEOUT for
+ * T H / Hk at most 2^26; scale log2(e) finite; Q, K, V and dO finite wherever they are live; pointers
+ * 16-byte aligned (kv_lens: 4, mask: any), buffers not overlapping. Range: products are summed in FP32 and the scale
+ * multiplies <Q, K> when it has been summed, so sum_e |Q K| must stay below 3.4e38 both before and after
+ * it, and sum_e |dO V|, sum_e |dO O| and the sums behind the gradients likewise; beyond, results are
+ * infinite or NaN. An exponent of magnitude s is accurate to s 2^-23.
+ *
+ * Return codes are the TRI_ATTN_* codes of tri_attn.h; a call that returns an error has enqueued nothing
+ * (TRI_ATTN_ERR_CUDA from a launch itself excepted). Calls are asynchronous on `stream`, allocate no device
+ * memory and keep no state between calls; a workspace may be used again once the call that uses it
+ * has finished. No floating-point atomics: for the same shape, lengths and GPU model a call gives the
+ * same bits. Kernels never trap; a bounded device wait that expires records TRI_ATTN_ERR_TIMEOUT for
  * tri_attn_device_status(). The first call of each entry point on a device does one-time host
  * set-up; make it before any stream capture.
  */
