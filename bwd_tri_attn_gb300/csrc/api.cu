@@ -192,9 +192,9 @@ extern "C" {
 const char *tri_attn_strerror(int code) {
   switch (code) {
     case TRI_ATTN_OK: return "success";
-    case TRI_ATTN_ERR_INVALID_ARG: return "invalid argument (NULL pointer, non-positive size, non-finite scale or unknown node)";
-    case TRI_ATTN_ERR_UNSUPPORTED: return "unsupported configuration (d must be 16 or 32, N <= TRI_ATTN_MAX_N, H <= TRI_ATTN_MAX_H, pointers 16-byte aligned)";
-    case TRI_ATTN_ERR_WORKSPACE: return "workspace missing or smaller than tri_attn_bwd_workspace_size()";
+    case TRI_ATTN_ERR_INVALID_ARG: return "invalid argument (NULL pointer, non-positive size, non-finite scale or eps, or unknown node, layout or dtype)";
+    case TRI_ATTN_ERR_UNSUPPORTED: return "unsupported configuration (a size, stride or pointer alignment outside the limits in the operator's header)";
+    case TRI_ATTN_ERR_WORKSPACE: return "workspace missing or smaller than the operator's workspace size function says";
     case TRI_ATTN_ERR_CUDA: return "CUDA runtime error";
     case TRI_ATTN_ERR_TIMEOUT: return "a bounded device-side wait expired";
     case TRI_ATTN_ERR_STATIC_TOO_SMALL:

@@ -103,8 +103,8 @@ typedef struct tri_attn_shape {
 enum {
     TRI_ATTN_OK = 0,
     TRI_ATTN_ERR_INVALID_ARG = -1,  /* NULL where required, non-positive or non-finite sizes, bad node */
-    TRI_ATTN_ERR_UNSUPPORTED = -2,  /* d not 16/32, N above the limit, misaligned pointer */
-    TRI_ATTN_ERR_WORKSPACE = -3,    /* workspace NULL or smaller than tri_attn_bwd_workspace_size */
+    TRI_ATTN_ERR_UNSUPPORTED = -2,  /* outside the operator's limits (here: d not 16/32, N above the limit), misaligned pointer */
+    TRI_ATTN_ERR_WORKSPACE = -3,    /* workspace NULL or smaller than the operator's workspace size */
     TRI_ATTN_ERR_CUDA = -4,         /* a CUDA runtime/driver call or launch failed */
     TRI_ATTN_ERR_TIMEOUT = -5,      /* a bounded device wait expired (see tri_attn_device_status) */
     TRI_ATTN_ERR_STATIC_TOO_SMALL = -6 /* tri_attn_bwd_static: shape needs more than the static workspace */
