@@ -4,7 +4,8 @@
 // Rows. GB query heads that share a key head (the largest power of two that divides H / Hk, at
 // most 128) are rows of one tile: row r of a tile that starts at query t0 is query t0 + r / GB of
 // head head0 + r mod GB, which is how a TMA box (64 channels, GB heads, 128 / GB queries) lands in shared memory.
-// One query of grouped heads so fills GB rows and reads K and V once.
+// One query of grouped heads so fills GB rows and reads K and V once; a group that is no power of two is
+// several such blocks, each of which reads them (28 heads over 4: seven of one head each).
 //
 // Work. An item is a set of output rows (a row tile of a head block for the forward and dQ, a key tile
 // of a key head for dK and dV), a unit one step of its inner loop (a key tile, or a query tile). The

@@ -15,12 +15,12 @@
 // first products read, through MN-major descriptors.
 //
 // Bounds and figures. A unit of 128 x 128 x 128 takes cross_dkv_kernel 1.5 us and cross_dq_kernel 1.1 us, where
-// the tensor cores alone take 1.07 and 0.8. In the first, shared memory is busy most of that time: 1536
+// the tensor cores alone take 1.34 and 1.01 at the rate of a large library product (1.07 and 0.8 nominally). In the first, shared memory is busy most of that time: 1536
 // cycles for the products' operands, 500 for the copies into it, 900 for reading -LSE and -D, which every
 // warp needs for all its columns; in the second the chain from dS over dQ and dP to the next dS. With 64
 // channels and fewer both are bound by the element-wise warps' work (a second buffer for S or dP there
 // changed nothing). 2048 queries x 4096 keys (lengths of 88 % on average), 2 x 16 heads of 128 over 4 key
-// heads: 290 us, of which the joins and the preparation 25.
+// heads: 296 us, of which the joins and the preparation 25.
 #include <math.h>
 
 #include "cross.cuh"

@@ -13,10 +13,10 @@
 // than 2^8: the reference value cancels in O / l, and P up to 2^8 costs no precision.
 //
 // Bounds and figures. Long rows are bound by the tensor cores: a unit (four products of 128 x 128 x 128) takes
-// 1.45 to 1.55 us where they alone take 1.07; 4096 queries x 4096 keys, 2 x 16 heads of 128: 175 us
-// (1570 TFLOP/s, 83 % of the rate of a large library product), 3 us of it the join. Single tokens are
-// bound by the memory: 8 x 16384 keys, 8 key heads of 128: 72 us (5.6 TB/s, 83 % of a copy's rate). Small
-// calls are one launch, 6 us.
+// 1.45 to 1.55 us where they alone take 1.34 at the rate of a large library product (1.07 at the nominal one); 4096
+// queries x 4096 keys, 2 x 16 heads of 128: 177 us (1554 TFLOP/s, 82 % of that product's rate), 3 us of it the
+// join. Single tokens are bound by the memory: 8 sequences of 16384 down to 9216 keys, 8 key heads of 128: 72 us (5.8
+// TB/s, 86 % of a copy's rate). Small calls are one launch, 6 us.
 #include <math.h>
 
 #include "cross.cuh"
@@ -59,7 +59,9 @@ struct CFwdArgs {
   const uint8_t *mask;
   uint16_t *O;
   float *LSE;
-  float *part;    // partial results: [2 CTAs][two 128][16 kd + 1] (O normalised, then LSE in log2 units)
+  // partial results: [2 CTAs][two] tiles of 128 rows of 16 kd values (O normalised), then the 128 rows' LSE in log2
+  // units; a tile has room for 128 (16 kd + 4) values, so that it begins on a 16-byte boundary
+  float *part;
 };
 
 // Row tile i of item `item`: its first query, and its head block's first head.

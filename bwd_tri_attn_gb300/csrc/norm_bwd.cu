@@ -5,9 +5,10 @@
 // into registers: dgamma and dbeta cost no second pass. The CTAs' partial sums are added by a
 // second kernel in a fixed order, without atomics, so the same call gives the same bits. The next
 // row's loads are issued before the current row's sums (memory bandwidth bounds the kernel).
-// 768 x 768 rows of 128 BF16 values: 88 us with the sum of the partials (5.2 TB/s, 77 % of a copy's
-// rate); 8192 rows of 2048 from the checkpoint: 25 us; 10007 rows of 1003 FP16 values 24 us (of 1024: 18,
-// where the bytes want 9: few rows a CTA, and 7 MB of partial sums).
+// 768 x 768 rows of 128 BF16 values: 91 us with the sum of the partials (5.0 TB/s, 74 % of a copy's
+// rate); 8192 rows of 2048 from the checkpoint: 27 us; 8192 x 8192 FP32 values 132 us, from the checkpoint 110;
+// 10007 rows of 1003 FP16 values 26 us (of 1024: 18.5; the bytes want 9): 592 CTAs of 17 rows, two at a time one
+// behind another, with too few bytes in flight, and 4.8 MB of partial sums written and read again.
 #include <algorithm>
 
 #include "launch.cuh"
@@ -32,8 +33,8 @@ constexpr int bwd_ctas(int T, int NV, bool AL) {
 enum { kAnyRows, kAlignedRows, kRowsInStep };
 
 // The chunk at row + c (a 16-byte boundary; c may be negative): at a row's ends the
-// whole chunk is read too, where it lies inside the tensor. in_row() then makes zeros of what lies outside the row,
-// when the values are used: done here it would wait for loads that are to be in flight.
+// whole chunk is read too, where it lies inside the tensor. What lies outside the row becomes zeros when the values are
+// used (dy's by in_row(), x's as xh): done here it would wait for loads that are to be in flight.
 template <typename XT>
 __device__ __forceinline__ uint4 chunk_load_in_step(const XT *row, int c, int C, const Span &span) {
   constexpr int VEC = Chunk<XT>::VEC;
@@ -410,7 +411,7 @@ struct BwdRows {
   int rows, geo;
 };
 int step_chunks(int C, int vec) { return (C + 2 * vec - 2) / vec; }
-// 8000 rows of 4001 BF16 values take 110 us one by one and 48 in step, 10007 of 1003 FP16 values 28 and 24; but not
+// 8000 rows of 4001 BF16 values take 110 us one by one and 50 in step, 10007 of 1003 FP16 values 28 and 25; but not
 // where the one chunk more is held by twice the threads: 50000 of 250 BF16 values 29 and 34.
 bool step_pays(int C, int vec) {
   const int n = step_chunks(C, vec);

@@ -4,8 +4,8 @@
 // A row is read once into registers; its mean and then the mean of the squared differences are
 // summed from there (no cancellation for rows far from zero), and y, the statistics and the
 // checkpoint leave in the same pass: the kernel reads x and writes y (plus one byte and 1/32 of an
-// FP32 scale per value for the checkpoint), and memory bandwidth bounds it: 24 us for 384 x 384 rows
-// of 128 FP32 values (6.3 TB/s, 93 % of a copy's rate), 57 us for 768 x 768 rows of 128 BF16 values (78 %), 19 us for 8192 rows of 2048 BF16 values with their
+// FP32 scale per value for the checkpoint), and memory bandwidth bounds it: 27 us for 384 x 384 rows
+// of 128 FP32 values (5.6 TB/s, 83 % of a copy's rate), 57 us for 768 x 768 rows of 128 BF16 values (78 %), 19 us for 8192 rows of 2048 BF16 values with their
 // checkpoint (4.5 TB/s); 3 us for 384 rows, a launch.
 #include <math.h>
 

@@ -11,8 +11,9 @@
  * Key j of sequence b is live if j < kv_lens[b] (kv_lens NULL: S) and mask[b,j] is not 0 (mask NULL:
  * all). Keys that are not live have no effect at all, whatever K and V hold there (padding may be
  * uninitialised, infinite or NaN). A sequence without live keys has O = 0 and LSE = -inf. The same
- * entry points serve single new tokens (T = 1): heads that share a key head are rows of one tile,
- * so K and V are read once, and the keys are split over the GPU.
+ * entry points serve single new tokens (T = 1): heads that share a key head are rows of one tile, in blocks
+ * of the largest power of two (at most 128) that divides H / Hk, so K and V are read once a block (groups
+ * of 1, 2, 4, 8, ...: once; groups of 7: seven times), and the keys are split over the GPU.
  *
  * Backward, with the gradient dO of O: D[t] = sum_e dO[t,e] O[t,e], dV = P^T dO,
  * dS = P (dO V^T - D), dQ = scale dS K, dK = scale dS^T Q; the gradients of a shared key head are

@@ -23,7 +23,10 @@
  * the scales FP32; q8 signed 8-bit, [M, C] without gaps; scales [M, (C + 127) / 128]. x and dy may
  * have a row stride (ldx, lddy elements, at least C); y and dx are written without gaps. Statistics
  * and all sums are FP32; the variance is the mean of the squared differences from the mean
- * (two passes over registers), and each 16-bit output is rounded once, to nearest even.
+ * (two passes over registers), and each 16-bit output is rounded once, to nearest even. Range: a row
+ * whose sum or sum of squared differences passes the largest FP32 number (|x - mean| about 2e17 in every
+ * one of 8192 channels, 1e18 in 256) has an infinite mean or variance: NaN, or rstd = 0 and y = beta. The
+ * mean is an FP32 sum and number, off by some 2^-22 of the row's magnitudes: y by that times rstd gamma.
  *
  * Requirements: M >= 1, 1 <= C <= TRI_NORM_MAX_C (checkpoints alone: TRI_CKPT_MAX_C), eps >= 0 finite,
  * pointers aligned to their element (16-byte aligned pointers and row strides take the wide loads),
