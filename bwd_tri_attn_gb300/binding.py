@@ -1,5 +1,5 @@
 """Thin ctypes binding of the C ABI in ``include/tri_attn.h``, ``include/tri_mul.h``,
-``include/tri_module.h``, ``include/tri_norm.h`` and ``include/tri_cross.h``.
+``include/tri_module.h``, ``include/tri_norm.h``, ``include/tri_cross.h`` and ``include/tri_ffn.h``.
 
 Argument marshalling only: PyTorch tensors supply device pointers and the
 current CUDA stream; every step of the computation runs in the library's
@@ -47,7 +47,8 @@ EXPORTS = ("tri_attn_strerror", "tri_attn_fwd", "tri_attn_bwd_workspace_size", "
            "tri_mul_bwd_workspace_size", "tri_mul_bwd", "tri_module_saved_size", "tri_module_bwd_workspace_size",
            "tri_module_fwd", "tri_module_bwd", "tri_norm_fwd", "tri_norm_bwd_workspace_size", "tri_norm_bwd",
            "tri_ckpt_pack", "tri_ckpt_unpack", "tri_cross_fwd_workspace_size", "tri_cross_fwd",
-           "tri_cross_bwd_workspace_size", "tri_cross_bwd")
+           "tri_cross_bwd_workspace_size", "tri_cross_bwd", "tri_ffn_fwd_workspace_size", "tri_ffn_fwd",
+           "tri_ffn_bwd_workspace_size", "tri_ffn_bwd")
 
 
 LAYOUT_PAIR, LAYOUT_CHANNEL_MAJOR = 0, 1  # tri_mul_shape.layout
@@ -107,6 +108,20 @@ class CrossShape(ctypes.Structure):
         return (f"CrossShape(B={self.B}, T={self.T}, S={self.S}, H={self.H}, Hk={self.Hk}, d={self.d}, "
                 f"scale={self.scale}, q_stride={list(self.q_stride)}, k_stride={list(self.k_stride)}, "
                 f"v_stride={list(self.v_stride)})")
+
+
+ACTIVATIONS = {"silu": 0, "gelu": 1, "sigmoid": 2}  # tri_ffn_shape.act
+
+
+class FfnShape(ctypes.Structure):
+    """tri_ffn_shape: rows, row strides of x and dout in elements (0: C), channels, hidden features, activation,
+    weight gradients in FP32 (else BF16)."""
+    _fields_ = [("M", ctypes.c_int64), ("ldx", ctypes.c_int64), ("lddout", ctypes.c_int64), ("C", ctypes.c_int),
+                ("F", ctypes.c_int), ("act", ctypes.c_int), ("wgrad_fp32", ctypes.c_int)]
+
+    def __repr__(self):
+        return (f"FfnShape(M={self.M}, ldx={self.ldx}, lddout={self.lddout}, C={self.C}, F={self.F}, act={self.act}, "
+                f"wgrad_fp32={self.wgrad_fp32})")
 
 
 def lib_path() -> str:
@@ -174,6 +189,14 @@ def load(path: str | None = None):
         lib.tri_cross_bwd_workspace_size.restype = ctypes.c_size_t
         lib.tri_cross_bwd.argtypes = [CrossShape] + [_VP] * 12 + [ctypes.c_size_t, _VP]
         lib.tri_cross_bwd.restype = ctypes.c_int
+        lib.tri_ffn_fwd_workspace_size.argtypes = [FfnShape]
+        lib.tri_ffn_fwd_workspace_size.restype = ctypes.c_size_t
+        lib.tri_ffn_fwd.argtypes = [FfnShape] + [_VP] * 8 + [ctypes.c_size_t, _VP]
+        lib.tri_ffn_fwd.restype = ctypes.c_int
+        lib.tri_ffn_bwd_workspace_size.argtypes = [FfnShape]
+        lib.tri_ffn_bwd_workspace_size.restype = ctypes.c_size_t
+        lib.tri_ffn_bwd.argtypes = [FfnShape] + [_VP] * 12 + [ctypes.c_size_t, _VP]
+        lib.tri_ffn_bwd.restype = ctypes.c_int
         _lib = lib
     return _lib
 
@@ -573,6 +596,39 @@ def tri_cross_bwd(shape: CrossShape, Q, K, V, mask, kv_lens, O, LSE, dO, dQ, dK,
     _check("tri_cross_bwd", rc)
 
 
+def _ffn_args(shape, x, Wg, Wu, Wd):
+    n = shape.C * shape.F
+    return [_spaced_arg(x, "x", _BF16, shape, shape.ldx), _arg(Wg, "Wg", _BF16, n), _arg(Wu, "Wu", _BF16, n),
+            _arg(Wd, "Wd", _BF16, n)]
+
+
+def tri_ffn_fwd_workspace_size(shape: FfnShape) -> int:
+    return int(load().tri_ffn_fwd_workspace_size(shape))
+
+
+def tri_ffn_fwd(shape: FfnShape, x, Wg, Wu, Wd, out, a, u, workspace, stream=None):
+    hidden = shape.M * shape.F
+    ptrs = _ptrs(*_ffn_args(shape, x, Wg, Wu, Wd), _arg(out, "out", _BF16, shape.M * shape.C),
+                 _arg(a, "a", _BF16, hidden, True), _arg(u, "u", _BF16, hidden, True),
+                 _arg(workspace, "workspace", None, None, True))
+    rc = load().tri_ffn_fwd(shape, *ptrs, _nbytes(workspace), _stream(stream))
+    _check("tri_ffn_fwd", rc)
+
+
+def tri_ffn_bwd_workspace_size(shape: FfnShape) -> int:
+    return int(load().tri_ffn_bwd_workspace_size(shape))
+
+
+def tri_ffn_bwd(shape: FfnShape, x, Wg, Wu, Wd, a, u, dout, dx, dWg, dWu, dWd, workspace, stream=None):
+    n, hidden, wd = shape.C * shape.F, shape.M * shape.F, _F32 if shape.wgrad_fp32 else _BF16
+    ptrs = _ptrs(*_ffn_args(shape, x, Wg, Wu, Wd), _arg(a, "a", _BF16, hidden), _arg(u, "u", _BF16, hidden),
+                 _spaced_arg(dout, "dout", _BF16, shape, shape.lddout), _arg(dx, "dx", _BF16, shape.M * shape.C, True),
+                 _arg(dWg, "dWg", wd, n, True), _arg(dWu, "dWu", wd, n, True), _arg(dWd, "dWd", wd, n, True),
+                 _arg(workspace, "workspace", None, None, True))
+    rc = load().tri_ffn_bwd(shape, *ptrs, _nbytes(workspace), _stream(stream))
+    _check("tri_ffn_bwd", rc)
+
+
 def tri_attn_device_status(stream=None) -> int:
     return int(load().tri_attn_device_status(_stream(stream)))
 
@@ -869,3 +925,81 @@ def cross_backward(Q, K, V, O, LSE, dO, mask=None, kv_lens=None, scale=None, wor
                               dV.data_ptr(), _ptr(workspace), _nbytes(workspace), _raw_stream(device))
     _check("tri_cross_bwd", rc)
     return dQ, dK, dV
+
+
+def ffn_shape_of(x: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, Wd: torch.Tensor, act: str = "silu",
+                 dout: torch.Tensor | None = None, wgrad_fp32: bool = False) -> FfnShape:
+    """Shape of the gated feed-forward block on the last axis of x [..., C] with Wg, Wu [F, C] and Wd [C, F]."""
+    for t, name in ((x, "x"), (Wg, "Wg"), (Wu, "Wu"), (Wd, "Wd"), *(() if dout is None else ((dout, "dout"),))):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
+        if t.dtype != _BF16:
+            raise TypeError(f"{name} must be {_BF16}, got {t.dtype}")
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {', '.join(ACTIVATIONS)}, got {act!r}")
+    if x.dim() < 1 or x.numel() == 0:
+        raise ValueError(f"x must have at least one row and one channel, got shape {tuple(x.shape)}")
+    C = x.shape[-1]
+    if Wg.dim() != 2 or Wg.shape[1] != C:
+        raise ValueError(f"Wg must have shape [F, {C}], got {tuple(Wg.shape)}")
+    F = Wg.shape[0]
+    if Wu.shape != (F, C):
+        raise ValueError(f"Wu must have shape {(F, C)}, got {tuple(Wu.shape)}")
+    if Wd.shape != (C, F):
+        raise ValueError(f"Wd must have shape {(C, F)}, got {tuple(Wd.shape)}")
+    if max(C, F) >= 1 << 31:  # (ctypes would cut it to 32 bits)
+        raise ValueError(f"an axis is too long: Wg has shape {tuple(Wg.shape)}")
+    if dout is not None and dout.shape != x.shape:
+        raise ValueError(f"dout {tuple(dout.shape)} must have x's shape {tuple(x.shape)}")
+    return FfnShape(x.numel() // C, _row_stride(x, "x"), C if dout is None else _row_stride(dout, "dout"), C, F,
+                    ACTIVATIONS[act], int(wgrad_fp32))
+
+
+def _weights_args(Wg, Wu, Wd):
+    return [_arg(Wg, "Wg", _BF16, None), _arg(Wu, "Wu", _BF16, None), _arg(Wd, "Wd", _BF16, None)]
+
+
+def ffn_forward(x, Wg, Wu, Wd, act="silu", keep=False, workspace=None, stream=None):
+    """The gated feed-forward block act(x Wg^T) (x Wu^T) Wd^T on x [..., C] with Wg, Wu [F, C] and Wd [C, F] (BF16; rows
+    of x may be spaced apart); act: "silu", "gelu" or "sigmoid". Returns out [..., C], with ``keep`` (out, a, u): also
+    the two projections [..., F], which ffn_backward reads."""
+    if (other := _other_stream(stream)) is not None:
+        return _called_on(other, ffn_forward, x, Wg, Wu, Wd, act, keep, workspace=workspace)
+    shape = ffn_shape_of(x, Wg, Wu, Wd, act)
+    device = _on_device(x.get_device(), ("x", x), *_weights_args(Wg, Wu, Wd), _arg(workspace, "workspace", None, None, True))
+    out = _dense_like(x)
+    a = u = None
+    if keep:
+        a, u = (torch.empty((*x.shape[:-1], shape.F), dtype=_BF16, device=x.device) for _ in range(2))
+    if workspace is None:
+        workspace = _workspace(tri_ffn_fwd_workspace_size(shape), x)
+    rc = load().tri_ffn_fwd(shape, x.data_ptr(), Wg.data_ptr(), Wu.data_ptr(), Wd.data_ptr(), out.data_ptr(), _ptr(a),
+                            _ptr(u), _ptr(workspace), _nbytes(workspace), _raw_stream(device))
+    _check("tri_ffn_fwd", rc)
+    return (out, a, u) if keep else out
+
+
+def ffn_backward(x, Wg, Wu, Wd, a, u, dout, act="silu", weight_dtype=_BF16, need_dx=True, need_dw=True, workspace=None,
+                 stream=None):
+    """Returns (dx, dWg, dWu, dWd) for the gradient dout of ffn_forward's out; a and u are what it kept. The weight
+    gradients are BF16 or FP32 (``weight_dtype``); what is not needed is None."""
+    if (other := _other_stream(stream)) is not None:
+        return _called_on(other, ffn_backward, x, Wg, Wu, Wd, a, u, dout, act, weight_dtype, need_dx, need_dw,
+                          workspace=workspace)
+    if weight_dtype not in (_BF16, _F32):
+        raise TypeError(f"weight_dtype must be {_BF16} or {_F32}, got {weight_dtype}")
+    if not (need_dx or need_dw):
+        raise ValueError("no gradient is asked for")
+    shape = ffn_shape_of(x, Wg, Wu, Wd, act, dout, weight_dtype == _F32)
+    hidden = shape.M * shape.F
+    device = _on_device(x.get_device(), ("x", x), *_weights_args(Wg, Wu, Wd), _arg(a, "a", _BF16, hidden),
+                        _arg(u, "u", _BF16, hidden), ("dout", dout), _arg(workspace, "workspace", None, None, True))
+    dx = _dense_like(x) if need_dx else None
+    dWg, dWu, dWd = (torch.empty(w.shape, dtype=weight_dtype, device=w.device) if need_dw else None for w in (Wg, Wu, Wd))
+    if workspace is None:
+        workspace = _workspace(tri_ffn_bwd_workspace_size(shape), x)
+    rc = load().tri_ffn_bwd(shape, x.data_ptr(), Wg.data_ptr(), Wu.data_ptr(), Wd.data_ptr(), a.data_ptr(), u.data_ptr(),
+                            dout.data_ptr(), _ptr(dx), _ptr(dWg), _ptr(dWu), _ptr(dWd), _ptr(workspace),
+                            _nbytes(workspace), _raw_stream(device))
+    _check("tri_ffn_bwd", rc)
+    return dx, dWg, dWu, dWd

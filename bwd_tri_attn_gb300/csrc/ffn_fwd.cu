@@ -1,0 +1,83 @@
+// Gated feed-forward block, forward (include/tri_ffn.h states the formulas): both projections, the activation and the
+// product of the two in one kernel, then the output's product. ffn.cuh has the kernels.
+#include "ffn.cuh"
+
+namespace triattn {
+namespace {
+
+using namespace ffn;
+
+struct FwdWorkspace {
+  int64_t h, part, bytes;
+};
+FwdWorkspace fwd_workspace(const tri_ffn_shape &s) {
+  FwdWorkspace w;
+  w.h = 0;
+  w.part = aligned256(2 * s.M * s.F);
+  w.bytes = w.part + (int64_t)share_bytes(256);
+  return w;
+}
+
+template <int BN>
+cudaError_t launch_fwd(const tri_ffn_shape &s, const void *x, const void *Wg, const void *Wu, const void *Wd, void *out, void *a,
+                       void *u, char *ws, int *status, cudaStream_t st) {
+  const FwdWorkspace w = fwd_workspace(s);
+  int dev = 0, nsm = 0;
+  cudaError_t e = device_and_sms(&dev, &nsm);
+  if (e != cudaSuccess) return e;
+  float *part = reinterpret_cast<float *>(ws + w.part);
+  const int64_t C = s.C, F = s.F, ldx = s.ldx ? s.ldx : C;
+  Args io{};
+  io.act = s.act;
+  io.rows[0] = io.rows[1] = (int)s.M;
+  io.cols[0] = io.cols[1] = s.F;
+  io.nk = io.nk0 = ceil_div(C, kBlock);
+  io.o[0] = ws + w.h;
+  io.o[1] = a;
+  io.o[2] = u;
+  const Matrix mx{x, C, s.M, ldx}, mw[2] = {{Wg, C, F, C}, {Wu, C, F, C}};
+  Product<kHidden, 256> hidden;
+  e = hidden.plan(io, &mx, 1, mw, 2, part, status, dev, nsm);
+  if (e != cudaSuccess) return e;
+  Args io2{};
+  io2.rows[0] = io2.rows[1] = (int)s.M;
+  io2.cols[0] = io2.cols[1] = s.C;
+  io2.nk = io2.nk0 = ceil_div(F, kBlock);
+  io2.o[0] = out;
+  const Matrix mh{ws + w.h, F, s.M, F}, md{Wd, F, C, F};
+  Product<kOut, BN> down;
+  e = down.plan(io2, &mh, 1, &md, 1, part, status, dev, nsm);
+  if (e != cudaSuccess) return e;
+  e = hidden.launch(st);
+  return e == cudaSuccess ? down.launch(st) : e;
+}
+
+}  // namespace
+}  // namespace triattn
+
+using namespace triattn;
+
+extern "C" {
+
+size_t tri_ffn_fwd_workspace_size(tri_ffn_shape shape) { return ffn::check_shape(shape) ? 0 : (size_t)fwd_workspace(shape).bytes; }
+
+int tri_ffn_fwd(tri_ffn_shape shape, const tri_attn_bf16 *x, const tri_attn_bf16 *Wg, const tri_attn_bf16 *Wu,
+                const tri_attn_bf16 *Wd, tri_attn_bf16 *out, tri_attn_bf16 *a, tri_attn_bf16 *u, void *workspace,
+                size_t workspace_bytes, void *stream) {
+  const int rc = ffn::check_shape(shape);
+  if (rc) return rc;
+  if (!x || !Wg || !Wu || !Wd || !out || (a != nullptr) != (u != nullptr)) return TRI_ATTN_ERR_INVALID_ARG;
+  for (const void *p : {(const void *)x, (const void *)Wg, (const void *)Wu, (const void *)Wd, (const void *)out, (const void *)a,
+                        (const void *)u, (const void *)workspace})
+    if (reinterpret_cast<uintptr_t>(p) & 15u) return TRI_ATTN_ERR_UNSUPPORTED;
+  if (!workspace || workspace_bytes < (size_t)fwd_workspace(shape).bytes) return TRI_ATTN_ERR_WORKSPACE;
+  int *status = device_status_word();
+  if (!status) return TRI_ATTN_ERR_CUDA;
+  const auto st = static_cast<cudaStream_t>(stream);
+  char *ws = static_cast<char *>(workspace);
+  const cudaError_t e = shape.C <= 128 ? launch_fwd<128>(shape, x, Wg, Wu, Wd, out, a, u, ws, status, st)
+                                       : launch_fwd<256>(shape, x, Wg, Wu, Wd, out, a, u, ws, status, st);
+  return e == cudaSuccess ? TRI_ATTN_OK : TRI_ATTN_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -1,0 +1,94 @@
+"""The gated feed-forward block (include/tri_ffn.h) against its formulas in 64 bits.
+
+Tolerances, from the arithmetic. U = 2^-8 is half a step of BF16, relative. An output is a sum of n products of a
+rounded operand (h, da or du: off by at most U each, and by the activation's FP32 error, a few 2^-22, below) with an
+exact one, added in FP32 (sums of at most 2^15 terms here, in blocks of 16 inside the tensor cores: under 2^12
+roundings or cut-offs of 2^-23, and usually far less: F = 2^-11), then rounded once: |error| <= U |result| + (U + F) sum |products|.
+a and u have exact operands: U |result| + F sum |products|. h in the backward pass is formed from the kept, rounded a
+and u, and so is the oracle's. erff's own bound is 2 ulp; 1 + erf cancels for negative a, which the absolute error
+2^-22 |a u| of h covers: small against U times the magnitudes, as sums of products with |h| near its size show, but
+not element by element, so every product counts |h| + 2^-20 |a u| in the sum of magnitudes.
+"""
+import math
+
+import pytest
+import torch
+
+from bwd_tri_attn_gb300 import binding as tb
+
+pytestmark = pytest.mark.gpu
+
+U, F = 2.0 ** -8, 2.0 ** -11
+ACTS = ["silu", "gelu", "sigmoid"]
+# (rows, channels, features): tiles filled and not, one row, one block of channels, shares of a tile over many pairs
+SIZES = [(1, 8, 8), (1, 64, 128), (7, 72, 200), (128, 64, 64), (129, 128, 512), (256, 256, 256), (300, 136, 1032), (513, 384, 1536),
+         (1000, 264, 264), (4001, 392, 1032), (9, 2048, 8192), (20000, 128, 512), (64, 4096, 520)]
+
+
+def normal(gen, *shape, std=1.0):
+    return (torch.randn(shape, generator=gen, device="cuda") * std).bfloat16()
+
+
+def inputs(M, C, Fh, seed=0):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    return (normal(gen, M, C), normal(gen, Fh, C, std=C ** -0.5), normal(gen, Fh, C, std=C ** -0.5),
+            normal(gen, C, Fh, std=Fh ** -0.5), normal(gen, M, C))
+
+
+def act64(a, act):
+    """act(a) and its derivative."""
+    if act == "gelu":
+        phi = 0.5 * torch.erfc(-a * math.sqrt(0.5))
+        return a * phi, phi + a * torch.exp(-0.5 * a * a) / math.sqrt(2 * math.pi)
+    s = torch.sigmoid(a)
+    return (a * s, s * (1 + a * (1 - s))) if act == "silu" else (s, s * (1 - s))
+
+
+def close(got, want, mag, operand=U, out=U):
+    assert got.isfinite().all()
+    err = (got.double() - want).abs()
+    tol = out * want.abs() + (operand + F) * mag
+    assert (err <= tol).all(), f"{(err / tol).max().item()} of the tolerance, {(err > tol).sum().item()} places"
+
+
+def check_forward(x, wg, wu, wd, act, out, a, u):
+    x, wg, wu, wd = (t.double() for t in (x, wg, wu, wd))
+    a64, u64 = x @ wg.T, x @ wu.T
+    if a is not None:
+        close(a, a64, x.abs() @ wg.abs().T, 0.0)
+        close(u, u64, x.abs() @ wu.abs().T, 0.0)
+    h = act64(a64, act)[0] * u64
+    # (FP32 sums behind a and u: at most F of their magnitudes through act's slope, at most 1.13, and u)
+    da, du = F * (x.abs() @ wg.abs().T), F * (x.abs() @ wu.abs().T)
+    mag = h.abs() + 2.0 ** -20 * (a64 * u64).abs() + (1.2 * da * u64.abs() + act64(a64, act)[0].abs() * du) / U
+    close(out, h @ wd.T, mag @ wd.abs().T)
+
+
+def check_backward(x, wg, wu, wd, a, u, dout, act, got, out=U):
+    x, wg, wu, wd, a, u, dout = (t.double() for t in (x, wg, wu, wd, a, u, dout))
+    f, df = act64(a, act)
+    dh, mh = dout @ wd, F * (dout.abs() @ wd.abs())
+    da, du, h = dh * u * df, dh * f, f * u
+    ma = da.abs() + (mh * (u * df).abs() + 2.0 ** -20 * (dh * u).abs() * (1 + a.abs())) / U
+    mu = du.abs() + (mh * f.abs() + 2.0 ** -20 * (dh * a).abs()) / U
+    mw = h.abs() + 2.0 ** -20 * (a * u).abs() / U
+    dx, dwg, dwu, dwd = got
+    if dx is not None:
+        close(dx, da @ wg + du @ wu, ma @ wg.abs() + mu @ wu.abs())
+    if dwg is not None:
+        close(dwg, da.T @ x, ma.T @ x.abs(), out=out)
+        close(dwu, du.T @ x, mu.T @ x.abs(), out=out)
+        close(dwd, dout.T @ h, dout.abs().T @ mw, out=out)
+
+
+@pytest.mark.parametrize("M,C,Fh", SIZES)
+def test_forward_and_backward(M, C, Fh):
+    act = ACTS[(M + C + Fh) % 3]
+    x, wg, wu, wd, dout = inputs(M, C, Fh)
+    out, a, u = tb.ffn_forward(x, wg, wu, wd, act=act, keep=True)
+    assert tb.tri_attn_device_status() == 0
+    check_forward(x, wg, wu, wd, act, out, a, u)
+    assert torch.equal(out, tb.ffn_forward(x, wg, wu, wd, act=act))
+    got = tb.ffn_backward(x, wg, wu, wd, a, u, dout, act=act)
+    assert tb.tri_attn_device_status() == 0
+    check_backward(x, wg, wu, wd, a, u, dout, act, got)
