@@ -1,5 +1,6 @@
 """Thin ctypes binding of the C ABI in ``include/tri_attn.h``, ``include/tri_mul.h``,
-``include/tri_module.h``, ``include/tri_norm.h``, ``include/tri_cross.h`` and ``include/tri_ffn.h``.
+``include/tri_module.h``, ``include/tri_norm.h``, ``include/tri_cross.h``, ``include/tri_ffn.h``,
+``include/tri_rms.h``, ``include/tri_clip.h`` and ``include/tri_relpos.h``.
 
 Argument marshalling only: PyTorch tensors supply device pointers and the
 current CUDA stream; every step of the computation runs in the library's
@@ -48,7 +49,8 @@ EXPORTS = ("tri_attn_strerror", "tri_attn_fwd", "tri_attn_bwd_workspace_size", "
            "tri_module_fwd", "tri_module_bwd", "tri_norm_fwd", "tri_norm_bwd_workspace_size", "tri_norm_bwd",
            "tri_ckpt_pack", "tri_ckpt_unpack", "tri_cross_fwd_workspace_size", "tri_cross_fwd",
            "tri_cross_bwd_workspace_size", "tri_cross_bwd", "tri_ffn_fwd_workspace_size", "tri_ffn_fwd",
-           "tri_ffn_bwd_workspace_size", "tri_ffn_bwd")
+           "tri_ffn_bwd_workspace_size", "tri_ffn_bwd", "tri_rms_fwd", "tri_rms_bwd_workspace_size", "tri_rms_bwd",
+           "tri_grad_norm", "tri_clip", "tri_relpos_fwd", "tri_relpos_bwd_workspace_size", "tri_relpos_bwd")
 
 
 LAYOUT_PAIR, LAYOUT_CHANNEL_MAJOR = 0, 1  # tri_mul_shape.layout
@@ -124,6 +126,49 @@ class FfnShape(ctypes.Structure):
                 f"wgrad_fp32={self.wgrad_fp32})")
 
 
+class RmsShape(ctypes.Structure):
+    """tri_rms_shape: rows, row strides in elements (0: C) of x or r, of the residual or dr, and of dy, channels, dtype, eps."""
+    _fields_ = [("M", ctypes.c_int64), ("ldx", ctypes.c_int64), ("ldres", ctypes.c_int64), ("lddy", ctypes.c_int64),
+                ("C", ctypes.c_int), ("dtype", ctypes.c_int), ("eps", ctypes.c_float)]
+
+    def __repr__(self):
+        return (f"RmsShape(M={self.M}, ldx={self.ldx}, ldres={self.ldres}, lddy={self.lddy}, C={self.C}, "
+                f"dtype={self.dtype}, eps={self.eps})")
+
+
+class RmsOutput(NamedTuple):
+    """What rms_forward returns; what was not asked for is None."""
+    y: torch.Tensor | None  # the normalised rows
+    rstd: torch.Tensor      # FP32 [...]
+    r: torch.Tensor | None  # x + residual
+    y8: Checkpoint | None   # the normalised rows in 8 bits
+
+
+CLIP_WORKSPACE_BYTES = 16384
+
+
+class ClipTensor(ctypes.Structure):
+    """tri_clip_tensor: a gradient, where its clipped values go, its elements and dtype."""
+    _fields_ = [("g", ctypes.c_void_p), ("out", ctypes.c_void_p), ("n", ctypes.c_int64), ("dtype", ctypes.c_int64)]
+
+
+MAX_BUCKETS = 128  # of a side of the relative position bias (TRI_RELPOS_MAX_K)
+
+
+class RelposShape(ctypes.Structure):
+    """tri_relpos_shape: batch, heads, queries, keys, buckets of a side, whether keys ahead have buckets of their own."""
+    _fields_ = [("B", ctypes.c_int), ("H", ctypes.c_int), ("Nq", ctypes.c_int), ("Nk", ctypes.c_int),
+                ("K", ctypes.c_int), ("two_sided", ctypes.c_int)]
+
+    def __repr__(self):
+        return (f"RelposShape(B={self.B}, H={self.H}, Nq={self.Nq}, Nk={self.Nk}, K={self.K}, "
+                f"two_sided={self.two_sided})")
+
+    @property
+    def rows(self):
+        return self.K * (2 if self.two_sided else 1)
+
+
 def lib_path() -> str:
     return _build.LIB
 
@@ -197,6 +242,22 @@ def load(path: str | None = None):
         lib.tri_ffn_bwd_workspace_size.restype = ctypes.c_size_t
         lib.tri_ffn_bwd.argtypes = [FfnShape] + [_VP] * 12 + [ctypes.c_size_t, _VP]
         lib.tri_ffn_bwd.restype = ctypes.c_int
+        lib.tri_rms_fwd.argtypes = [RmsShape] + [_VP] * 9
+        lib.tri_rms_fwd.restype = ctypes.c_int
+        lib.tri_rms_bwd_workspace_size.argtypes = [RmsShape]
+        lib.tri_rms_bwd_workspace_size.restype = ctypes.c_size_t
+        lib.tri_rms_bwd.argtypes = [RmsShape] + [_VP] * 8 + [ctypes.c_size_t, _VP]
+        lib.tri_rms_bwd.restype = ctypes.c_int
+        lib.tri_grad_norm.argtypes = [ctypes.c_int, _VP, _VP, _VP, ctypes.c_size_t, _VP]
+        lib.tri_grad_norm.restype = ctypes.c_int
+        lib.tri_clip.argtypes = [ctypes.c_int, _VP, ctypes.c_float, _VP, _VP, ctypes.c_size_t, _VP]
+        lib.tri_clip.restype = ctypes.c_int
+        lib.tri_relpos_fwd.argtypes = [RelposShape] + [_VP] * 7
+        lib.tri_relpos_fwd.restype = ctypes.c_int
+        lib.tri_relpos_bwd_workspace_size.argtypes = [RelposShape]
+        lib.tri_relpos_bwd_workspace_size.restype = ctypes.c_size_t
+        lib.tri_relpos_bwd.argtypes = [RelposShape] + [_VP] * 6 + [ctypes.c_size_t, _VP]
+        lib.tri_relpos_bwd.restype = ctypes.c_int
         _lib = lib
     return _lib
 
@@ -629,6 +690,84 @@ def tri_ffn_bwd(shape: FfnShape, x, Wg, Wu, Wd, a, u, dout, dx, dWg, dWu, dWd, w
     _check("tri_ffn_bwd", rc)
 
 
+def tri_rms_fwd(shape: RmsShape, x, residual, gamma, r, y, rstd, q8=None, scale=None, stream=None):
+    n, ng = _norm_counts(shape)
+    dt = _TORCH_DTYPES.get(shape.dtype)
+    ptrs = _ptrs(_spaced_arg(x, "x", dt, shape, shape.ldx),
+                 None if residual is None else _spaced_arg(residual, "residual", dt, shape, shape.ldres),
+                 _arg(gamma, "gamma", _F32, shape.C, True), _arg(r, "r", dt, n, True), _arg(y, "y", dt, n, True),
+                 _arg(rstd, "rstd", _F32, shape.M), _arg(q8, "q8", torch.int8, n, True), _arg(scale, "scale", _F32, ng, True))
+    rc = load().tri_rms_fwd(shape, *ptrs, _stream(stream))
+    _check("tri_rms_fwd", rc)
+
+
+def tri_rms_bwd_workspace_size(shape: RmsShape) -> int:
+    return int(load().tri_rms_bwd_workspace_size(shape))
+
+
+def tri_rms_bwd(shape: RmsShape, r, gamma, rstd, dy, dr, dx, dgamma, workspace, stream=None):
+    n, _ = _norm_counts(shape)
+    dt = _TORCH_DTYPES.get(shape.dtype)
+    ptrs = _ptrs(_spaced_arg(r, "r", dt, shape, shape.ldx), _arg(gamma, "gamma", _F32, shape.C, True),
+                 _arg(rstd, "rstd", _F32, shape.M), _spaced_arg(dy, "dy", dt, shape, shape.lddy),
+                 None if dr is None else _spaced_arg(dr, "dr", dt, shape, shape.ldres), _arg(dx, "dx", dt, n),
+                 _arg(dgamma, "dgamma", _F32, shape.C, True), _arg(workspace, "workspace", None, None, True))
+    rc = load().tri_rms_bwd(shape, *ptrs, _nbytes(workspace), _stream(stream))
+    _check("tri_rms_bwd", rc)
+
+
+def tri_grad_norm(tensors, norm, workspace, stream=None):
+    """``tensors``: a ctypes array of ClipTensor (device pointers that the caller answers for)."""
+    ptrs = _ptrs(_arg(norm, "norm", _F32, 1), _arg(workspace, "workspace", None, None, True))
+    rc = load().tri_grad_norm(len(tensors), tensors, *ptrs, _nbytes(workspace), _stream(stream))
+    _check("tri_grad_norm", rc)
+
+
+def tri_clip(tensors, max_norm, norm, workspace, stream=None):
+    """As tri_grad_norm, and the clipped gradients."""
+    ptrs = _ptrs(_arg(norm, "norm", _F32, 1), _arg(workspace, "workspace", None, None, True))
+    rc = load().tri_clip(len(tensors), tensors, max_norm, *ptrs, _nbytes(workspace), _stream(stream))
+    _check("tri_clip", rc)
+
+
+_I32 = torch.int32
+
+
+def _starts_array(shape, starts):
+    """The buckets' first distances as the library reads them (from host memory)."""
+    if len(starts) != shape.K or not len(starts):
+        raise ValueError(f"starts has {len(starts)} buckets, the shape {shape.K}")
+    starts = [int(s) for s in starts]
+    if starts[0] != 0 or any(b <= a for a, b in zip(starts, starts[1:])) or starts[-1] >= 1 << 31:
+        raise ValueError(f"starts must begin with 0 and rise, below 2^31, got {starts}")
+    return (ctypes.c_int32 * shape.K)(*starts)
+
+
+def _positions_args(shape, positions, key_positions):
+    return [_arg(positions, "positions", _I32, shape.B * shape.Nq, True),
+            _arg(key_positions, "key_positions", _I32, shape.B * shape.Nk, True)]
+
+
+def tri_relpos_fwd(shape: RelposShape, starts, table, positions, key_positions, base, bias, stream=None):
+    n = shape.B * shape.H * shape.Nq * shape.Nk
+    ptrs = _ptrs(_arg(table, "table", _F32, shape.rows * shape.H), *_positions_args(shape, positions, key_positions),
+                 _arg(base, "base", _BF16, n, True), _arg(bias, "bias", _BF16, n))
+    rc = load().tri_relpos_fwd(shape, _starts_array(shape, starts), *ptrs, _stream(stream))
+    _check("tri_relpos_fwd", rc)
+
+
+def tri_relpos_bwd_workspace_size(shape: RelposShape) -> int:
+    return int(load().tri_relpos_bwd_workspace_size(shape))
+
+
+def tri_relpos_bwd(shape: RelposShape, starts, positions, key_positions, dbias, dtable, workspace, stream=None):
+    ptrs = _ptrs(*_positions_args(shape, positions, key_positions),
+                 _arg(dbias, "dbias", _BF16, shape.B * shape.H * shape.Nq * shape.Nk),
+                 _arg(dtable, "dtable", _F32, shape.rows * shape.H), _arg(workspace, "workspace", None, None, True))
+    rc = load().tri_relpos_bwd(shape, _starts_array(shape, starts), *ptrs, _nbytes(workspace), _stream(stream))
+    _check("tri_relpos_bwd", rc)
+
+
 def tri_attn_device_status(stream=None) -> int:
     return int(load().tri_attn_device_status(_stream(stream)))
 
@@ -1003,3 +1142,222 @@ def ffn_backward(x, Wg, Wu, Wd, a, u, dout, act="silu", weight_dtype=_BF16, need
                             _nbytes(workspace), _raw_stream(device))
     _check("tri_ffn_bwd", rc)
     return dx, dWg, dWu, dWd
+
+
+def rms_shape_of(x: torch.Tensor, residual: torch.Tensor | None = None, eps: float = 1e-5,
+                 dy: torch.Tensor | None = None) -> RmsShape:
+    """Shape of the RMS norm over the last axis of x [..., C] (r in the backward pass) and the row strides of it, of the
+    residual (dr) and of dy."""
+    dtype = _norm_dtype(x, "x")
+    if x.dim() < 1 or x.numel() == 0:
+        raise ValueError(f"x must have at least one row and one channel, got shape {tuple(x.shape)}")
+    C = _channels(x, "x")
+    for t, name in ((residual, "residual"), (dy, "dy")):
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
+        if t.shape != x.shape:
+            raise ValueError(f"{name} {tuple(t.shape)} must have x's shape {tuple(x.shape)}")
+        if t.dtype != x.dtype:
+            raise TypeError(f"{name} must be {x.dtype}, got {t.dtype}")
+    return RmsShape(x.numel() // C, _row_stride(x, "x"), C if residual is None else _row_stride(residual, "residual"),
+                    C if dy is None else _row_stride(dy, "dy"), C, dtype, float(eps))
+
+
+def rms_forward(x, gamma=None, residual=None, eps=1e-5, eight_bits=False, stream=None) -> RmsOutput:
+    """RMS norm over the last axis of r = x + residual (of x without a residual), x [..., C] in BF16, FP16 or FP32: returns
+    RmsOutput(y, rstd, r, y8). eight_bits: also y8, y as a ``Checkpoint`` (checkpoint_unpack reads it); "only": y8 in the
+    place of y. r is None without a residual."""
+    if (other := _other_stream(stream)) is not None:
+        return RmsOutput(*_called_on(other, rms_forward, x, gamma, residual, eps, eight_bits))
+    if eight_bits not in (False, True, "only"):
+        raise ValueError(f"eight_bits must be False, True or \"only\", got {eight_bits!r}")
+    shape = rms_shape_of(x, residual, eps)
+    device = _on_device(x.get_device(), ("x", x), None if residual is None else ("residual", residual),
+                        _arg(gamma, "gamma", _F32, shape.C, True))
+    r = None if residual is None else _dense_like(x)
+    y = None if eight_bits == "only" else _dense_like(x)
+    rstd = torch.empty(x.shape[:-1], dtype=_F32, device=x.device)
+    y8 = _empty_checkpoint(x) if eight_bits else None
+    q8, scale = (y8.q8.data_ptr(), y8.scale.data_ptr()) if eight_bits else (None, None)
+    rc = load().tri_rms_fwd(shape, x.data_ptr(), _ptr(residual), _ptr(gamma), _ptr(r), _ptr(y), rstd.data_ptr(), q8, scale,
+                            _raw_stream(device))
+    _check("tri_rms_fwd", rc)
+    return RmsOutput(y, rstd, r, y8)
+
+
+def rms_backward(r, gamma, rstd, dy, dr=None, workspace=None, stream=None):
+    """Returns (dx, dgamma): dx, the gradient of x and of the residual alike, and dgamma in FP32 (None when gamma is None).
+    r and rstd are the forward's (r: x where there was no residual); dr is the gradient that reaches r past the norm."""
+    if (other := _other_stream(stream)) is not None:
+        return _called_on(other, rms_backward, r, gamma, rstd, dy, dr, workspace=workspace)
+    shape = rms_shape_of(r, dr, 0.0, dy)
+    device = _on_device(r.get_device(), ("r", r), ("dy", dy), None if dr is None else ("dr", dr),
+                        _arg(gamma, "gamma", _F32, shape.C, True), _arg(rstd, "rstd", _F32, shape.M),
+                        _arg(workspace, "workspace", None, None, True))
+    dx = _dense_like(dy)
+    dgamma = None
+    if gamma is not None:
+        dgamma = torch.empty_like(gamma)
+        if workspace is None:
+            workspace = _workspace(tri_rms_bwd_workspace_size(shape), dy)
+    rc = load().tri_rms_bwd(shape, r.data_ptr(), _ptr(gamma), rstd.data_ptr(), dy.data_ptr(), _ptr(dr), dx.data_ptr(),
+                            _ptr(dgamma), _ptr(workspace), _nbytes(workspace), _raw_stream(device))
+    _check("tri_rms_bwd", rc)
+    return dx, dgamma
+
+
+def _clip_array(grads, out):
+    """The gradients' descriptions for the library, and the device's index: every tensor checked, no output twice."""
+    device = torch.cuda.current_device()
+    rows = []
+    for i, g in enumerate(grads):
+        code = _norm_dtype(g, f"gradient {i}")
+        o = g if out is None else out[i]
+        if o is not g:
+            if not isinstance(o, torch.Tensor) or o.dtype != g.dtype or o.shape != g.shape:
+                raise ValueError(f"out {i} must be a tensor of gradient {i}'s shape and type")
+            if not o.is_contiguous() or o.get_device() != device:
+                raise ValueError(f"out {i} must be contiguous and on the current device")
+        if not g.is_contiguous():
+            raise ValueError(f"gradient {i} must be contiguous")
+        if g.get_device() != device:
+            raise ValueError(f"gradient {i} must be a CUDA tensor on the current device, got {g.device}")
+        n = g.numel()
+        if n:
+            rows.append((g.data_ptr(), o.data_ptr(), n, code))
+    if len({r[1] for r in rows}) != len(rows):
+        raise ValueError("a tensor stands twice among the gradients that are written")
+    return (ClipTensor * len(rows))(*rows), device
+
+
+def _clip(call, grads, out, workspace, *more):
+    grads = list(grads)
+    if out is not None:
+        out = list(out)
+        if len(out) != len(grads):
+            raise ValueError(f"{len(out)} outputs for {len(grads)} gradients")
+    rows, device = _clip_array(grads, out)
+    norm = torch.empty((), dtype=_F32, device=torch.device("cuda", device))
+    if workspace is None:
+        workspace = torch.empty(CLIP_WORKSPACE_BYTES, dtype=torch.uint8, device=norm.device)
+    _on_device(device, _arg(workspace, "workspace", None, None))
+    rc = getattr(load(), call)(len(rows), rows, *more, norm.data_ptr(), workspace.data_ptr(), _nbytes(workspace),
+                               _raw_stream(device))
+    _check(call, rc)
+    return norm
+
+
+def gradient_norm(grads, workspace=None, stream=None) -> torch.Tensor:
+    """The 2-norm of all elements of the gradients (BF16, FP16 and FP32 tensors of any number and shapes): an FP32 number
+    on the device."""
+    if (other := _other_stream(stream)) is not None:
+        return _called_on(other, gradient_norm, grads, workspace=workspace)
+    return _clip("tri_grad_norm", grads, None, workspace)
+
+
+def clip_gradients(grads, max_norm, out=None, workspace=None, stream=None) -> torch.Tensor:
+    """Multiplies the gradients by min(1, max_norm / (norm + 1e-6)), in place or into the tensors ``out``, and returns
+    their norm before, an FP32 number on the device."""
+    max_norm = float(max_norm)
+    if not max_norm >= 0.0:
+        raise ValueError(f"max_norm must not be negative, got {max_norm}")
+    if (other := _other_stream(stream)) is not None:
+        return _called_on(other, clip_gradients, grads, max_norm, out, workspace=workspace)
+    return _clip("tri_clip", grads, out, workspace, max_norm)
+
+
+def relpos_starts(buckets: int, max_distance: int, two_sided: bool = True) -> tuple[int, ...]:
+    """The first distances of logarithmic buckets: of ``buckets`` in all (half of them on each side if two-sided, K on a
+    side) the first e = (K + 1) // 2 of a side hold one distance each, the others equal steps of the logarithm up to
+    max_distance: bucket e + k holds the distances n with (n / e)^(K - e) >= (max_distance / e)^k (in whole numbers,
+    so that no rounding moves a border; at least one distance a bucket)."""
+    K = buckets // 2 if two_sided else buckets
+    if K < 1 or (two_sided and buckets % 2):
+        raise ValueError(f"there must be at least one bucket on a side, and as many on both: got {buckets}")
+    if max_distance < K:
+        raise ValueError(f"max_distance must be at least the {K} buckets of a side, got {max_distance}")
+    e = (K + 1) // 2
+    m, starts = K - e, list(range(e))
+    for k in range(m):
+        low, high = starts[-1] + 1 if starts else 0, max(max_distance, starts[-1] + 1)
+        while low < high:
+            mid = (low + high) // 2
+            if mid ** m * e ** k >= max_distance ** k * e ** m:
+                high = mid
+            else:
+                low = mid + 1
+        starts.append(low)
+    return tuple(starts)
+
+
+def _positions_of(shape, positions, key_positions):
+    if positions is None and key_positions is not None:
+        raise ValueError("key_positions come with positions")
+    if positions is not None and key_positions is None:
+        if shape.Nq != shape.Nk:
+            raise ValueError(f"{shape.Nk} keys need positions of their own, there are {shape.Nq} queries")
+        key_positions = positions
+    for t, name, n in ((positions, "positions", shape.Nq), (key_positions, "key_positions", shape.Nk)):
+        if isinstance(t, torch.Tensor) and t.shape != (shape.B, n):
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, the call needs {(shape.B, n)}")
+    return positions, key_positions
+
+
+def _axes(*axes):
+    if max(axes) >= 1 << 31:  # (ctypes would cut it to 32 bits)
+        raise ValueError(f"an axis is too long: {axes}")
+
+
+def relpos_forward(table, starts, Nq, Nk=None, B=1, two_sided=True, base=None, positions=None, key_positions=None,
+                   stream=None) -> torch.Tensor:
+    """The pair bias [B, H, Nq, Nk] (BF16) base + table[bucket(key's position - query's)]: table FP32 [rows, H], 2 K rows
+    for K two-sided buckets or K; ``starts``: the buckets' first distances (relpos_starts makes logarithmic ones); base BF16
+    [B, H, Nq, Nk] or None; positions int32 [B, Nq], key_positions [B, Nk] (None: 0, 1, 2, ...; the queries')."""
+    if (other := _other_stream(stream)) is not None:
+        return _called_on(other, relpos_forward, table, starts, Nq, Nk, B, two_sided, base, positions, key_positions)
+    if not isinstance(table, torch.Tensor):
+        raise TypeError(f"table must be a torch.Tensor, got {type(table).__name__}")
+    Nk = Nq if Nk is None else Nk
+    K = len(starts)
+    if table.dim() != 2 or table.shape[0] != K * (2 if two_sided else 1):
+        raise ValueError(f"table must have shape [{K * (2 if two_sided else 1)}, H], got {tuple(table.shape)}")
+    H = table.shape[1]
+    _axes(B, H, Nq, Nk)
+    shape = RelposShape(B, H, Nq, Nk, K, int(bool(two_sided)))
+    if isinstance(base, torch.Tensor) and base.shape != (B, H, Nq, Nk):
+        raise ValueError(f"base has shape {tuple(base.shape)}, the call needs {(B, H, Nq, Nk)}")
+    positions, key_positions = _positions_of(shape, positions, key_positions)
+    rows = _starts_array(shape, starts)
+    device = _on_device(table.get_device(), _arg(table, "table", _F32, None),
+                        *_positions_args(shape, positions, key_positions), _arg(base, "base", _BF16, None, True))
+    bias = torch.empty((B, H, Nq, Nk), dtype=_BF16, device=table.device)
+    rc = load().tri_relpos_fwd(shape, rows, table.data_ptr(), _ptr(positions), _ptr(key_positions), _ptr(base),
+                               bias.data_ptr(), _raw_stream(device))
+    _check("tri_relpos_fwd", rc)
+    return bias
+
+
+def relpos_backward(dbias, starts, two_sided=True, positions=None, key_positions=None, workspace=None,
+                    stream=None) -> torch.Tensor:
+    """The table's gradient (FP32 [rows, H]) for the gradient dbias [B, H, Nq, Nk] (BF16) of relpos_forward's result."""
+    if (other := _other_stream(stream)) is not None:
+        return _called_on(other, relpos_backward, dbias, starts, two_sided, positions, key_positions, workspace=workspace)
+    if not isinstance(dbias, torch.Tensor):
+        raise TypeError(f"dbias must be a torch.Tensor, got {type(dbias).__name__}")
+    if dbias.dim() != 4:
+        raise ValueError(f"dbias must have four axes (batch, head, query, key), got shape {tuple(dbias.shape)}")
+    _axes(*dbias.shape)
+    shape = RelposShape(*dbias.shape, len(starts), int(bool(two_sided)))
+    positions, key_positions = _positions_of(shape, positions, key_positions)
+    rows = _starts_array(shape, starts)
+    device = _on_device(dbias.get_device(), _arg(dbias, "dbias", _BF16, None),
+                        *_positions_args(shape, positions, key_positions), _arg(workspace, "workspace", None, None, True))
+    dtable = torch.empty((shape.rows, shape.H), dtype=_F32, device=dbias.device)
+    if workspace is None:
+        workspace = _workspace(tri_relpos_bwd_workspace_size(shape), dbias)
+    rc = load().tri_relpos_bwd(shape, rows, _ptr(positions), _ptr(key_positions), dbias.data_ptr(), dtable.data_ptr(),
+                               _ptr(workspace), _nbytes(workspace), _raw_stream(device))
+    _check("tri_relpos_bwd", rc)
+    return dtable

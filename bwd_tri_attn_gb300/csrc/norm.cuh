@@ -121,7 +121,34 @@ __device__ __forceinline__ void row_weights(const float *w, int c, int C, float 
   }
 }
 
+// The forward's geometry: no column sums are kept, so rows of up to 128 chunks go to warps and need no
+// barrier. Wider rows go to CTAs of 128 threads: with 8 chunks a lane in a warp, 8192 rows of 2048
+// BF16 values and their checkpoints took 31 us, with 2 chunks a thread 18 us.
+enum { kF8, kF16, kF32, kF32x2, kF32x4, kF128x2, kF128x4, kF128x8, kF256x8 };
+inline int norm_fwd_geometry(int chunks) {
+  return chunks <= 8     ? kF8
+         : chunks <= 16  ? kF16
+         : chunks <= 32  ? kF32
+         : chunks <= 64  ? kF32x2
+         : chunks <= 128 ? kF32x4
+         : chunks <= 256 ? kF128x2
+         : chunks <= 512 ? kF128x4
+         : chunks <= 1024 ? kF128x8
+                          : kF256x8;
+}
+#define NORM_FWD_DISPATCH(geo, aligned, LAUNCH)                        \
+  switch (geo) {                                                       \
+    case kF8: if (aligned) LAUNCH(8, 1, true) else LAUNCH(8, 1, false); break; \
+    case kF16: if (aligned) LAUNCH(16, 1, true) else LAUNCH(16, 1, false); break; \
+    case kF32: if (aligned) LAUNCH(32, 1, true) else LAUNCH(32, 1, false); break; \
+    case kF32x2: if (aligned) LAUNCH(32, 2, true) else LAUNCH(32, 2, false); break; \
+    case kF32x4: if (aligned) LAUNCH(32, 4, true) else LAUNCH(32, 4, false); break; \
+    case kF128x2: if (aligned) LAUNCH(128, 2, true) else LAUNCH(128, 2, false); break; \
+    case kF128x4: if (aligned) LAUNCH(128, 4, true) else LAUNCH(128, 4, false); break; \
+    case kF128x8: if (aligned) LAUNCH(128, 8, true) else LAUNCH(128, 8, false); break; \
+    default: if (aligned) LAUNCH(256, 8, true) else LAUNCH(256, 8, false); break; \
+  }
+
 int norm_check_shape(const tri_norm_shape &s);
-cudaError_t launch_norm_reduce(const float *part, int parts, int C, float *dgamma, float *dbeta, cudaStream_t st);
 
 }  // namespace triattn

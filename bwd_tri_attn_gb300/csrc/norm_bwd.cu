@@ -9,66 +9,11 @@
 // rate); 8192 rows of 2048 from the checkpoint: 27 us; 8192 x 8192 FP32 values 132 us, from the checkpoint 110;
 // 10007 rows of 1003 FP16 values 26 us (of 1024: 18.5; the bytes want 9): 592 CTAs of 17 rows, two at a time one
 // behind another, with too few bytes in flight, and 4.8 MB of partial sums written and read again.
-#include <algorithm>
-
-#include "launch.cuh"
-#include "norm.cuh"
+#include "norm_bwd.cuh"
 
 namespace triattn {
 namespace {
 
-// Rows that a CTA which holds a row takes at a time: they share the barriers of their sums (10007 rows of
-// 1024 FP16 values: 21 us one by one, 18 in pairs). Rows that begin anywhere, which want the issue slots,
-// go one by one (of 1003 values: 28 us, 30 in pairs).
-constexpr int bwd_rows(int T, int NV, bool AL) { return T > 32 && NV == 1 && AL ? 2 : 1; }
-// CTAs per SM that the registers are kept to: 768 threads, 512 where a thread holds more, at least one CTA.
-constexpr int bwd_ctas(int T, int NV, bool AL) {
-  return T == 512 ? 1 : (NV == 1 ? (bwd_rows(T, NV, AL) == 2 ? 2 : 3) : 2) * (T == 128 ? 2 : 1);
-}
-
-// How the rows of a tensor lie. In step: not all of them start on a 16-byte boundary, but those of x, dy
-// and dx are equally far from one. A CTA then takes every VEC-th row, which all are the same way off, and its chunks
-// begin at the boundaries: a column stays with its thread, and all accesses but those at the rows' ends are
-// aligned 16 bytes.
-enum { kAnyRows, kAlignedRows, kRowsInStep };
-
-// The chunk at row + c (a 16-byte boundary; c may be negative): at a row's ends the
-// whole chunk is read too, where it lies inside the tensor. What lies outside the row becomes zeros when the values are
-// used (dy's by in_row(), x's as xh): done here it would wait for loads that are to be in flight.
-template <typename XT>
-__device__ __forceinline__ uint4 chunk_load_in_step(const XT *row, int c, int C, const Span &span) {
-  constexpr int VEC = Chunk<XT>::VEC;
-  if (c >= 0 && c + VEC <= C) return ld_stream(reinterpret_cast<const uint4 *>(row + c));
-  uint32_t w[4] = {0u, 0u, 0u, 0u};
-  const uintptr_t at = reinterpret_cast<uintptr_t>(row) + (uintptr_t)((intptr_t)c * (intptr_t)sizeof(XT));
-  if (c < C && c + VEC > 0) {
-    if (at >= span.begin && at + 16 <= span.end) return ld_stream(reinterpret_cast<const uint4 *>(at));
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      if ((unsigned)(c + j) >= (unsigned)C) continue;
-      if constexpr (sizeof(XT) == 2)
-        w[j / 2] |= (uint32_t)reinterpret_cast<const uint16_t *>(row)[c + j] << (16 * (j & 1));
-      else
-        w[j] = reinterpret_cast<const uint32_t *>(row)[c + j];
-    }
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-template <typename XT>
-__device__ __forceinline__ void in_row(uint4 &v, int c, int C) {
-  constexpr int VEC = Chunk<XT>::VEC;
-  if (c >= 0 && c + VEC <= C) return;
-  uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int j = 0; j < VEC; ++j)
-    if ((unsigned)(c + j) >= (unsigned)C) {
-      if constexpr (sizeof(XT) == 2)
-        w[j / 2] &= (j & 1) ? 0x0000ffffu : 0xffff0000u;
-      else
-        w[j] = 0u;
-    }
-  v = make_uint4(w[0], w[1], w[2], w[3]);
-}
 // The 8-bit values of that chunk (at a multiple of VEC bytes, too).
 template <int VEC>
 __device__ __forceinline__ void q8_load_in_step(const int8_t *row, int c, int C, const Span &span, uint32_t (&w)[VEC / 4]) {
@@ -88,23 +33,6 @@ __device__ __forceinline__ void q8_load_in_step(const int8_t *row, int c, int C,
 #pragma unroll
   for (int j = 0; j < VEC; ++j)
     if ((unsigned)(c + j) < (unsigned)C) w[j / 4] |= (uint32_t)(uint8_t)row[c + j] << (8 * (j & 3));
-}
-template <typename XT>
-__device__ __forceinline__ void chunk_store_in_step(XT *row, int c, int C, const uint4 &v) {
-  constexpr int VEC = Chunk<XT>::VEC;
-  if (c >= 0 && c + VEC <= C) {
-    *reinterpret_cast<uint4 *>(row + c) = v;
-    return;
-  }
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int j = 0; j < VEC; ++j) {
-    if ((unsigned)(c + j) >= (unsigned)C) continue;
-    if constexpr (sizeof(XT) == 2)
-      reinterpret_cast<uint16_t *>(row)[c + j] = (uint16_t)(w[j / 2] >> (16 * (j & 1)));
-    else
-      reinterpret_cast<uint32_t *>(row)[c + j] = w[j];
-  }
 }
 
 template <typename XT, int T, int NV, int ROWS, bool Q8>
@@ -355,68 +283,10 @@ __global__ void __launch_bounds__(T > 32 ? T : 256, bwd_ctas(T, NV, ROWS != kAny
   }
 }
 
-// dgamma and dbeta: the sums over the CTAs' partials part[p][2][C]. A CTA takes 32 of the 2 C
-// columns; lane row y adds p = y, y + 32, ... in order, then the 32 sums are added in order.
-__global__ void __launch_bounds__(1024) norm_reduce_kernel(const float *__restrict__ part, int parts, int C,
-                                                           float *__restrict__ dgamma, float *__restrict__ dbeta) {
-  __shared__ float acc[32][33];
-  const int i = blockIdx.x * 32 + threadIdx.x, n = 2 * C;
-  float s = 0.f;
-  wait_previous_kernel();
-  if (i < n) {
-    int p = threadIdx.y;
-    for (; p + 96 < parts; p += 128) {  // four loads in flight, added in order
-      const float a0 = part[(int64_t)p * n + i], a1 = part[(int64_t)(p + 32) * n + i];
-      const float a2 = part[(int64_t)(p + 64) * n + i], a3 = part[(int64_t)(p + 96) * n + i];
-      s = (((s + a0) + a1) + a2) + a3;
-    }
-    for (; p < parts; p += 32) s += part[(int64_t)p * n + i];
-  }
-  acc[threadIdx.y][threadIdx.x] = s;
-  __syncthreads();
-  // row y of the transposed sums: an xor tree over 32 lanes
-  float r = acc[threadIdx.x][threadIdx.y];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
-  const int k = blockIdx.x * 32 + threadIdx.y;
-  if (threadIdx.x == 0 && k < n) {
-    if (k < C)
-      dgamma[k] = r;
-    else
-      dbeta[k - C] = r;
-  }
-}
-
-struct BwdSplitRows {
-  int64_t rpc;             // rows per CTA
-  int parts, per_class;    // CTAs; of a class of rows in step (else all of them)
-};
-
-// The split of the rows over CTAs, from the shape alone: the CTAs that 152 SMs hold at once (a second,
-// shorter wave of them took as long as the first: 102 against 77 us for 768 x 768 rows of 128),
-// at least two rows for each group of threads that holds a row.
-BwdSplitRows split_rows(const tri_norm_shape &s, int geo, int rows_are) {
-  const int T = norm_threads_per_row(geo), RPC = T > 32 ? 1 : 256 / T;
-  const int nv = geo == kNormT32x2 || geo == kNormT256x2 || geo == kNormT512x2 ? 2 : geo == kNormT512x4 ? 4 : 1;
-  const int classes = rows_are == kRowsInStep ? (s.dtype == TRI_DTYPE_FP32 ? 4 : 8) : 1;
-  const int64_t target = 152 * bwd_ctas(T, nv, rows_are != kAnyRows) / classes, M = (s.M + classes - 1) / classes;
-  int64_t rpc = (M + target - 1) / target;
-  rpc = std::max<int64_t>((rpc + RPC - 1) / RPC * RPC, 2 * RPC);
-  const int per_class = (int)((M + rpc - 1) / rpc);
-  return {rpc, classes * per_class, per_class};
-}
-
 // How the rows of a call lie, and its geometry. (In step the row's chunks can be one more.)
 struct BwdRows {
   int rows, geo;
 };
-int step_chunks(int C, int vec) { return (C + 2 * vec - 2) / vec; }
-// 8000 rows of 4001 BF16 values take 110 us one by one and 50 in step, 10007 of 1003 FP16 values 28 and 25; but not
-// where the one chunk more is held by twice the threads: 50000 of 250 BF16 values 29 and 34.
-bool step_pays(int C, int vec) {
-  const int n = step_chunks(C, vec);
-  return n * vec <= TRI_NORM_MAX_C && (n > 128 || norm_geometry(n, true) == norm_geometry((C + vec - 1) / vec, true));
-}
 template <typename XT>
 BwdRows rows_of(const tri_norm_shape &s, const void *x, const int8_t *q8, const float *gamma, const void *dy, const void *dx) {
   constexpr int VEC = Chunk<XT>::VEC;
@@ -462,7 +332,7 @@ cudaError_t launch_bwd_t(const tri_norm_shape &s, const void *x, const int8_t *q
 #undef LAUNCH
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess && part) {
-    e = launch_after(norm_reduce_kernel, dim3((2 * s.C + 31) / 32), dim3(32, 32), 0, st, part, sp.parts, s.C, dgamma, dbeta);
+    e = launch_after(norm_reduce_kernel, dim3((2 * s.C + 31) / 32), dim3(32, 32), 0, st, part, sp.parts, 2 * s.C, s.C, dgamma, dbeta);
   }
   return e;
 }
