@@ -9,6 +9,7 @@ an exception is raised.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import math
 import os
@@ -1209,27 +1210,35 @@ def rms_backward(r, gamma, rstd, dy, dr=None, workspace=None, stream=None):
 
 
 def _clip_array(grads, out):
-    """The gradients' descriptions for the library, and the device's index: every tensor checked, no output twice."""
+    """The gradients' descriptions for the library (as ClipTensor's fields one behind another), their number and the
+    device's index: every tensor checked, no output twice."""
     device = torch.cuda.current_device()
-    rows = []
+    codes, rows, written = _NORM_DTYPES, [], set()
     for i, g in enumerate(grads):
-        code = _norm_dtype(g, f"gradient {i}")
-        o = g if out is None else out[i]
-        if o is not g:
-            if not isinstance(o, torch.Tensor) or o.dtype != g.dtype or o.shape != g.shape:
-                raise ValueError(f"out {i} must be a tensor of gradient {i}'s shape and type")
-            if not o.is_contiguous() or o.get_device() != device:
-                raise ValueError(f"out {i} must be contiguous and on the current device")
+        try:
+            code, at = codes[g.dtype], g.get_device()
+        except (AttributeError, KeyError):
+            _norm_dtype(g, f"gradient {i}")  # (names what is wrong)
+            raise
+        if at != device:
+            raise ValueError(f"gradient {i} must be a CUDA tensor on the current device, got {g.device}")
         if not g.is_contiguous():
             raise ValueError(f"gradient {i} must be contiguous")
-        if g.get_device() != device:
-            raise ValueError(f"gradient {i} must be a CUDA tensor on the current device, got {g.device}")
-        n = g.numel()
+        n, p = g.numel(), g.data_ptr()
+        o = p
+        if out is not None:
+            t = out[i]
+            if not isinstance(t, torch.Tensor) or t.dtype != g.dtype or t.shape != g.shape:
+                raise ValueError(f"out {i} must be a tensor of gradient {i}'s shape and type")
+            if t.get_device() != device or not t.is_contiguous():
+                raise ValueError(f"out {i} must be contiguous and on the current device")
+            o = t.data_ptr()
         if n:
-            rows.append((g.data_ptr(), o.data_ptr(), n, code))
-    if len({r[1] for r in rows}) != len(rows):
+            rows += (p, o, n, code)
+            written.add(o)
+    if 4 * len(written) != len(rows):
         raise ValueError("a tensor stands twice among the gradients that are written")
-    return (ClipTensor * len(rows))(*rows), device
+    return array.array("q", rows), len(written), device
 
 
 def _clip(call, grads, out, workspace, *more):
@@ -1238,12 +1247,12 @@ def _clip(call, grads, out, workspace, *more):
         out = list(out)
         if len(out) != len(grads):
             raise ValueError(f"{len(out)} outputs for {len(grads)} gradients")
-    rows, device = _clip_array(grads, out)
+    rows, count, device = _clip_array(grads, out)
     norm = torch.empty((), dtype=_F32, device=torch.device("cuda", device))
     if workspace is None:
         workspace = torch.empty(CLIP_WORKSPACE_BYTES, dtype=torch.uint8, device=norm.device)
     _on_device(device, _arg(workspace, "workspace", None, None))
-    rc = getattr(load(), call)(len(rows), rows, *more, norm.data_ptr(), workspace.data_ptr(), _nbytes(workspace),
+    rc = getattr(load(), call)(count, rows.buffer_info()[0], *more, norm.data_ptr(), workspace.data_ptr(), _nbytes(workspace),
                                _raw_stream(device))
     _check(call, rc)
     return norm

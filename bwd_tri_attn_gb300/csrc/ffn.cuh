@@ -40,10 +40,12 @@ struct Cfg {
   static constexpr bool AMN = OP == kDW, BMN = OP == kDHidden || OP == kDx || OP == kDW;
   static constexpr int COLS = OP == kHidden ? BN / 2 : BN;  // columns of the result in a tile
   static constexpr int A_BYTES = kHalf * 128, B_BYTES = BN / 2 * 128, STAGE = A_BYTES + B_BYTES;
-  static constexpr int NST = BN == 256 ? 6 : 8;
+  static constexpr int NST = OP == kDHidden ? (BN == 128 ? 6 : 5) : BN == 128 ? 8 : 6;
   static constexpr int EPI_WARPS = 8, NTHREADS = 32 * (4 + EPI_WARPS);
+  // 32 x 32 pieces of the results on their way out, a ring for each of these warps (FP32 pieces take two places)
+  static constexpr int PIECE = 32 * 64, RING = OP == kDHidden ? 4 : 2;
   static constexpr int B_FULL = 0, B_EMPTY = NST, B_ACCF = 2 * NST, B_ACCE = B_ACCF + 2, B_DONE = B_ACCE + 2, NBAR = B_DONE + 1;
-  static constexpr int OFF_BAR = NST * STAGE, OFF_MISC = OFF_BAR + 8 * NBAR, SMEM = OFF_MISC + 16, SMEM_ALLOC = SMEM + 1024;
+  static constexpr int OFF_EPI = NST * STAGE, OFF_BAR = OFF_EPI + EPI_WARPS * RING * PIECE, OFF_MISC = OFF_BAR + 8 * NBAR, SMEM = OFF_MISC + 16, SMEM_ALLOC = SMEM + 1024;
   static_assert(SMEM_ALLOC <= 227 * 1024, "shared memory");
 };
 
@@ -52,7 +54,8 @@ struct Args {
   int mt[2], nt[2];      // tiles
   int nk, nk0;           // 64-channel blocks; those of the first of kDx's two projections
   int full, tail, pairs; // tiles of whole waves, the others, and the pairs that share those (0: nobody does)
-  int act, f32;          // TRI_FFN_*; FP32 results (kDW)
+  int act, f32, wide;    // TRI_FFN_*; FP32 results (kDW); a and u are read 32 bytes at a time
+  int box;               // rows of a CTA's box of A (not kDW): 128, or fewer where all rows are in the first CTA's
   int64_t units;         // tail * nk
   const uint16_t *a, *u; // kDHidden
   void *o[3];            // kHidden: h, a, u (the last two may be NULL); kDHidden: da, du, h (may be NULL); kDW: the three
@@ -119,77 +122,187 @@ __device__ __forceinline__ Tile tile_at(const Args &a, int t) {
 }
 
 // ------------------------------------------------------------------------------------------------ activation
-// f = act(a) and, where asked, its derivative. (The quotient of 1 + 2^x is an approximate reciprocal, 2 ulp; it is 0 where
-// 2^x overflows.)
-template <bool kSlope>
-__device__ __forceinline__ void activation(int act, float a, float &f, float &df) {
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+__device__ __forceinline__ float reciprocal(float x) {  // (1 ulp; 0 for what is above 2^126)
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// sigmoid(a) of N pairs, with one approximate reciprocal (1 ulp) for both of a pair: 1 / (p q) times p and q. Where p q passes
+// what it can take (a below -40 or so, or no number), one for each.
+template <int N>
+__device__ __forceinline__ void sigmoids(const float2 (&a)[N], float2 (&s)[N]) {
+  float2 d[N];
+  uint32_t top = 0;  // (as unsigned numbers the bits of numbers >= 1 order as they do, a NaN above them)
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const float2 x = __fmul2_rn(a[j], both(-kLog2e));
+    d[j] = __fadd2_rn(make_float2(ex2(x.x), ex2(x.y)), both(1.f));
+    const float pq = d[j].x * d[j].y;
+    top = max(top, __float_as_uint(pq));
+    s[j] = __fmul2_rn(both(reciprocal(pq)), make_float2(d[j].y, d[j].x));
+  }
+  if (top > __float_as_uint(0x1p120f)) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) s[j] = make_float2(reciprocal(d[j].x), reciprocal(d[j].y));
+  }
+}
+
+// f = act(a) and, where asked, its derivative.
+template <bool kSlope, int N>
+__device__ __forceinline__ void activation(int act, const float2 (&a)[N], float2 (&f)[N], float2 (&df)[N]) {
   if (act == TRI_FFN_GELU) {
-    const float phi = fmaf(0.5f, erff(a * 0.70710678f), 0.5f);
-    f = a * phi;
-    if constexpr (kSlope) df = fmaf(a * 0.39894228f, ex2(a * a * (-0.5f * kLog2e)), phi);
-  } else {
-    const float s = __fdividef(1.f, 1.f + ex2(-a * kLog2e));
+    // Phi(-|a|) = (c1 t + ... + c5 t^5) exp(-a^2 / 2) with t = 1 / (1 + p |a|): Hastings' approximation of the error function
+    // (Abramowitz and Stegun 7.1.26, off by at most 1.5e-7), halved and at a / sqrt(2); the slope takes the same exponential.
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const float2 m = make_float2(fabsf(a[j].x), fabsf(a[j].y)), d = __ffma2_rn(m, both(0.3275911f * 0.70710678f), both(1.f));
+      const float2 t = make_float2(reciprocal(d.x), reciprocal(d.y)), q = __fmul2_rn(__fmul2_rn(a[j], a[j]), both(-0.5f * kLog2e));
+      const float2 e = make_float2(ex2(q.x), ex2(q.y));
+      float2 c = __ffma2_rn(t, both(0.5f * 1.061405429f), both(-0.5f * 1.453152027f));
+      c = __ffma2_rn(c, t, both(0.5f * 1.421413741f));
+      c = __ffma2_rn(c, t, both(-0.5f * 0.284496736f));
+      c = __ffma2_rn(c, t, both(0.5f * 0.254829592f));
+      c = __fmul2_rn(__fmul2_rn(c, t), e);
+      const float2 phi = make_float2(a[j].x < 0.f ? c.x : 1.f - c.x, a[j].y < 0.f ? c.y : 1.f - c.y);
+      f[j] = __fmul2_rn(a[j], phi);
+      if constexpr (kSlope) df[j] = __ffma2_rn(__fmul2_rn(a[j], both(0.39894228f)), e, phi);
+    }
+    return;
+  }
+  float2 s[N];
+  sigmoids(a, s);
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const float2 rest = __ffma2_rn(s[j], both(-1.f), both(1.f));
     if (act == TRI_FFN_SILU) {
-      f = a * s;
-      if constexpr (kSlope) df = s * fmaf(a, 1.f - s, 1.f);
+      f[j] = __fmul2_rn(a[j], s[j]);
+      if constexpr (kSlope) df[j] = __fmul2_rn(s[j], __ffma2_rn(a[j], rest, both(1.f)));
     } else {
-      f = s;
-      if constexpr (kSlope) df = s * (1.f - s);
+      f[j] = s[j];
+      if constexpr (kSlope) df[j] = __fmul2_rn(s[j], rest);
     }
   }
 }
 
-__device__ __forceinline__ float low(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ float2 unpack2(uint32_t w) { return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)); }
+__device__ __forceinline__ uint32_t pack2(float2 v) { return pack_bf16x2(v.x, v.y); }
 
-__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
-  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-}
-
-// Eight finished sums of row m, columns n .. n + 7 (kHidden: v of the gate, w of the up projection), the row and the
-// columns inside the result. ra, ru: kDHidden's a and u there.
-template <int OP>
-__device__ __forceinline__ void finish8(const Args &a, const Tile &x, int m, int n, const float (&v)[8], const float (&w)[8],
-                                        const uint4 &ra, const uint4 &ru) {
-  const int64_t off = (int64_t)m * x.cols + n;
-  if constexpr (OP == kOut || OP == kDx) {
-    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.o[0]) + off) = pack8(v);
-  } else if constexpr (OP == kDW) {
-    void *o = x.prod == 0 ? a.o[0] : x.prod == 1 ? a.o[1] : a.o[2];
-    if (a.f32) {
-      float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(o) + off);
-      p[0] = make_float4(v[0], v[1], v[2], v[3]);
-      p[1] = make_float4(v[4], v[5], v[6], v[7]);
-    } else {
-      *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(o) + off) = pack8(v);
-    }
-  } else if constexpr (OP == kHidden) {
-    float h[8], none;
+// 2 N sums in consecutive columns of a row (kHidden: v of the gate, w of the up projection; kDHidden: ra and ru, the kept a and
+// u there) to the BF16 results there: o[0], and h, a, u of kHidden, da, du, h of kDHidden.
+template <int OP, int N>
+__device__ __forceinline__ void results(int act, const float2 (&v)[N], const float2 (&w)[N], const uint32_t (&ra)[N], const uint32_t (&ru)[N],
+                                        uint32_t (&o0)[N], uint32_t (&o1)[N], uint32_t (&o2)[N]) {
+  if constexpr (OP == kHidden) {
+    float2 f[N], none[N];
+    activation<false>(act, v, f, none);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      activation<false>(a.act, v[j], h[j], none);
-      h[j] *= w[j];
+    for (int j = 0; j < N; ++j) {
+      o0[j] = pack2(__fmul2_rn(f[j], w[j]));
+      o1[j] = pack2(v[j]);
+      o2[j] = pack2(w[j]);
     }
-    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.o[0]) + off) = pack8(h);
-    if (a.o[1]) {
-      *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.o[1]) + off) = pack8(v);
-      *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.o[2]) + off) = pack8(w);
+  } else if constexpr (OP == kDHidden) {
+    float2 g[N], f[N], df[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) g[j] = unpack2(ra[j]);
+    activation<true>(act, g, f, df);
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const float2 up = unpack2(ru[j]);
+      o0[j] = pack2(__fmul2_rn(__fmul2_rn(v[j], up), df[j]));
+      o1[j] = pack2(__fmul2_rn(v[j], f[j]));
+      o2[j] = pack2(__fmul2_rn(f[j], up));
     }
   } else {
-    const uint32_t wa[4] = {ra.x, ra.y, ra.z, ra.w}, wu[4] = {ru.x, ru.y, ru.z, ru.w};
-    float da[8], du[8], h[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float g = j & 1 ? high(wa[j / 2]) : low(wa[j / 2]), up = j & 1 ? high(wu[j / 2]) : low(wu[j / 2]);
-      float f, df;
-      activation<true>(a.act, g, f, df);
-      da[j] = v[j] * up * df;
-      du[j] = v[j] * f;
-      h[j] = f * up;
+    for (int j = 0; j < N; ++j) o0[j] = pack2(v[j]);
+  }
+}
+
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, uint32_t src, int c0, int c1) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(reinterpret_cast<uint64_t>(map)),
+               "r"(src), "r"(c0), "r"(c1)
+               : "memory");
+}
+__device__ __forceinline__ void st_shared_v4(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+// A warp's ring of pieces in shared memory: 32 columns of 32 rows (row = lane), in the store map's swizzle.
+template <int RING, int BYTES>
+struct Pieces {
+  uint32_t base;
+  int next, used;
+  __device__ __forceinline__ uint32_t begin() {
+    if (used >= RING) {  // the store that used the place before has read it
+      if ((threadIdx.x & 31) == 0) bulk_wait_group_read<RING - 1>();
+      __syncwarp();
+    } else {
+      ++used;
     }
-    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.o[0]) + off) = pack8(da);
-    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.o[1]) + off) = pack8(du);
-    if (a.o[2]) *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.o[2]) + off) = pack8(h);
+    const uint32_t at = base + next * BYTES;
+    next = next + 1 == RING ? 0 : next + 1;
+    return at;
+  }
+  __device__ __forceinline__ void send(const CUtensorMap *map, uint32_t at, int col, int row) {
+    fence_proxy_async_smem();  // the generic-proxy writes before the async-proxy read
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) {
+      tma_store_2d(map, at, col, row);
+      bulk_commit_group();
+    }
+  }
+  // `n` pieces at once: places that the pieces sent before the last one have left (RING > n)
+  template <int n>
+  __device__ __forceinline__ void begin(uint32_t (&at)[n]) {
+    static_assert(RING == n + 1, "places");
+    if (used) {
+      if ((threadIdx.x & 31) == 0) bulk_wait_group_read<1>();
+      __syncwarp();
+    }
+    used = 1;
+#pragma unroll
+    for (int k = 0; k < n; ++k) {
+      at[k] = base + next * BYTES;
+      next = next + 1 == RING ? 0 : next + 1;
+    }
+  }
+  // 16-bit values: rows of 64 bytes, 16-byte part c at c ^ ((row / 2) mod 4)
+  __device__ __forceinline__ void put(const CUtensorMap *map, const uint32_t (&w)[16], int col, int row) {
+    const uint32_t at = begin(), lane = threadIdx.x & 31;
+#pragma unroll
+    for (uint32_t c = 0; c < 4; ++c)
+      st_shared_v4(at + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4), w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+    send(map, at, col, row);
+  }
+  // FP32 values: rows of 128 bytes, 16-byte part c at c ^ (row mod 8)
+  __device__ __forceinline__ void put(const CUtensorMap *map, const uint32_t (&w)[32], int col, int row) {
+    const uint32_t at = begin(), lane = threadIdx.x & 31;
+#pragma unroll
+    for (uint32_t c = 0; c < 8; ++c)
+      st_shared_v4(at + lane * 128 + ((c ^ (lane & 7)) << 4), w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+    send(map, at, col, row);
+  }
+};
+
+// 32 BF16 values of a row from column `col` on (zeros past the last column; the row is inside).
+__device__ __forceinline__ void load_row32(const uint16_t *p, int col, int cols, int wide, uint32_t (&w)[16]) {
+  if (wide && col + 32 <= cols) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                   : "=r"(w[8 * j]), "=r"(w[8 * j + 1]), "=r"(w[8 * j + 2]), "=r"(w[8 * j + 3]), "=r"(w[8 * j + 4]), "=r"(w[8 * j + 5]),
+                     "=r"(w[8 * j + 6]), "=r"(w[8 * j + 7])
+                   : "l"(p + col + 16 * j));
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint4 v = col + 8 * j < cols ? ld_stream(reinterpret_cast<const uint4 *>(p + col + 8 * j)) : make_uint4(0u, 0u, 0u, 0u);
+    w[4 * j] = v.x, w[4 * j + 1] = v.y, w[4 * j + 2] = v.z, w[4 * j + 3] = v.w;
   }
 }
 
@@ -198,7 +311,9 @@ template <int OP, int BN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<OP, BN>::NTHREADS, 1)
     product_kernel(const __grid_constant__ CUtensorMap mA0, const __grid_constant__ CUtensorMap mA1,
                    const __grid_constant__ CUtensorMap mA2, const __grid_constant__ CUtensorMap mB0,
-                   const __grid_constant__ CUtensorMap mB1, const __grid_constant__ CUtensorMap mB2, const Args a) {
+                   const __grid_constant__ CUtensorMap mB1, const __grid_constant__ CUtensorMap mB2,
+                   const __grid_constant__ CUtensorMap mO0, const __grid_constant__ CUtensorMap mO1,
+                   const __grid_constant__ CUtensorMap mO2, const Args a) {
   using C = Cfg<OP, BN>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -236,6 +351,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<OP, BN>::NTHREAD
   int tile, k0, k1, slot;
   if (warp == 0) {
     // ------------------------------------------------------------ TMA: both CTAs load, all bytes count on the first one's barriers
+    // (rows that are not loaded leave what they like in accumulator rows that nobody reads)
+    const bool few = !C::AMN && a.box < kHalf, loads = !few || rank == 0;
+    const uint32_t bytes = few ? a.box * 128 + 2 * C::B_BYTES : 2 * C::STAGE;
     bool ok = true;
     int it = 0;
     if (lane == 0) {
@@ -253,7 +371,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<OP, BN>::NTHREAD
         if (!ok) break;
         if (lane == 0) {
           const uint32_t dst = sb0 + st * C::STAGE, fb = mapa_shared(bar(C::B_FULL + st), 0);
-          if (rank == 0) mbar_arrive_expect_tx(bar(C::B_FULL + st), 2 * C::STAGE);
+          if (rank == 0) mbar_arrive_expect_tx(bar(C::B_FULL + st), bytes);
           int k = kb * kBlock;
           if (OP == kDx) {
             const bool second = kb >= a.nk0;
@@ -264,7 +382,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<OP, BN>::NTHREAD
           if constexpr (C::AMN) {
             pair_load_2d(dst, pA, fb, am, k);
             pair_load_2d(dst + kBox, pA, fb, am + 64, k);
-          } else {
+          } else if (loads) {
             pair_load_2d(dst, pA, fb, k, am);
           }
           if constexpr (C::BMN) {
@@ -310,15 +428,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<OP, BN>::NTHREAD
     __syncwarp();
   } else if (warp >= 4) {
     // ------------------------------------------------------------ finished sums, thread = row: half of the columns
+    // (pieces of 32 columns leave by TMA: a thread's own stores, a line for each lane, took four times as long)
     const int q = warp & 3, half = (warp - 4) >> 2, row = 32 * q + lane;
-    const uint32_t lanes = (uint32_t)(32 * q) << 16;
+    const uint32_t lanes = (uint32_t)(32 * q) << 16, ring = sb0 + C::OFF_EPI + (warp - 4) * C::RING * C::PIECE;
+    Pieces<C::RING, C::PIECE> out{ring, 0, 0};
+    Pieces<C::RING / 2, 2 * C::PIECE> out32{ring, 0, 0};
     constexpr int CH = C::COLS / 64;  // 32-column chunks of a warp
     int tl = 0;
     while (items.next(a, pair, pairs, tile, k0, k1, slot)) {
       const Tile x = tile_at<OP, BN>(a, tile);
-      const int acc = tl & 1, m = x.m0 + kHalf * rank + row, c0 = half * (C::COLS / 2);
-      const int cols = x.cols;
+      const int acc = tl & 1, mw = x.m0 + kHalf * rank + 32 * q, m = mw + lane, c0 = half * (C::COLS / 2);
       const bool mine = m < x.rows;
+      uint32_t ra[16], ru[16];
+      auto fetch = [&](int i) {
+        if (mine && slot < 0) {
+          load_row32(a.a + (int64_t)m * x.cols, x.n0 + c0 + 32 * i, x.cols, a.wide, ra);
+          load_row32(a.u + (int64_t)m * x.cols, x.n0 + c0 + 32 * i, x.cols, a.wide, ru);
+        }
+      };
+      if constexpr (OP == kDHidden) fetch(0);
       if (!wait_bar_warp(bar(C::B_ACCF + acc), (tl >> 1) & 1, ab)) break;
       ++tl;
       tc_fence_after();
@@ -326,18 +454,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<OP, BN>::NTHREAD
       float *part = a.part + ((int64_t)max(slot, 0) * 2 + rank) * BN * kHalf + row;
 #pragma unroll 1
       for (int i = 0; i < CH; ++i) {
-        const int c = c0 + 32 * i;
+        const int c = c0 + 32 * i, n = x.n0 + c;
         uint32_t v[32], w[32];
-        uint4 ra[4], ru[4];
-        if constexpr (OP == kDHidden) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (mine && slot < 0 && x.n0 + c + 8 * j < cols) {
-              const int64_t off = (int64_t)m * cols + x.n0 + c + 8 * j;
-              ra[j] = ld_stream(reinterpret_cast<const uint4 *>(a.a + off));
-              ru[j] = ld_stream(reinterpret_cast<const uint4 *>(a.u + off));
-            }
-        }
         tmem_ld32(tacc + c, v);
         if constexpr (OP == kHidden) tmem_ld32(tacc + BN / 2 + c, w);
         tmem_wait_ld(v);
@@ -347,28 +465,78 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<OP, BN>::NTHREAD
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(mapa_shared(bar(C::B_ACCE + acc), 0));
         }
-        if (mine && slot >= 0) {
+        if (slot >= 0) {
+          if (mine) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            part[(c + j) * kHalf] = __uint_as_float(v[j]);
-            if constexpr (OP == kHidden) part[(BN / 2 + c + j) * kHalf] = __uint_as_float(w[j]);
-          }
-        } else if (mine) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if (x.n0 + c + 8 * j >= cols) break;
-            float f[8], g[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              f[e] = __uint_as_float(v[8 * j + e]);
-              if constexpr (OP == kHidden) g[e] = __uint_as_float(w[8 * j + e]);
+            for (int j = 0; j < 32; ++j) {
+              part[(c + j) * kHalf] = __uint_as_float(v[j]);
+              if constexpr (OP == kHidden) part[(BN / 2 + c + j) * kHalf] = __uint_as_float(w[j]);
             }
-            finish8<OP>(a, x, m, x.n0 + c + 8 * j, f, g, ra[j], ru[j]);
+          }
+        } else if (mw < x.rows && n < x.cols) {  // (the whole warp; rows and columns outside are not stored)
+          const CUtensorMap *mo = OP != kDW || x.prod == 0 ? &mO0 : x.prod == 1 ? &mO1 : &mO2;
+          if constexpr (OP == kDHidden) {
+            uint32_t at[3];
+            out.begin(at);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              float2 f[8];
+              uint32_t ga[8], gu[8], o[3][8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                f[j] = make_float2(__uint_as_float(v[16 * h + 2 * j]), __uint_as_float(v[16 * h + 2 * j + 1]));
+                ga[j] = ra[8 * h + j];
+                gu[j] = ru[8 * h + j];
+              }
+              results<OP>(a.act, f, f, ga, gu, o[0], o[1], o[2]);
+#pragma unroll
+              for (int k = 0; k < 3; ++k)
+#pragma unroll
+                for (uint32_t e = 0; e < 2; ++e)
+                  st_shared_v4(at[k] + lane * 64 + (((2 * h + e) ^ ((lane >> 1) & 3)) << 4), o[k][4 * e], o[k][4 * e + 1], o[k][4 * e + 2], o[k][4 * e + 3]);
+            }
+            if (i + 1 < CH) fetch(i + 1);
+            out.send(&mO0, at[0], n, mw);
+            out.send(&mO1, at[1], n, mw);
+            if (a.o[2])
+              out.send(&mO2, at[2], n, mw);
+            else if (lane == 0)
+              bulk_commit_group();  // (an empty one: begin() counts three)
+          } else if (OP == kDW && a.f32) {
+            out32.put(mo, v, n, mw);
+          } else {
+            uint32_t o[16];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              float2 f[8], g[8];
+              uint32_t o0[8], none[8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const int k = 16 * h + 2 * j;
+                f[j] = make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1]));
+                if constexpr (OP == kHidden) g[j] = make_float2(__uint_as_float(w[k]), __uint_as_float(w[k + 1]));
+              }
+              results<OP>(a.act, f, g, o0, o0, o0, none, none);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) o[8 * h + j] = o0[j];
+            }
+            out.put(mo, o, n, mw);
+            if (OP == kHidden && a.o[1]) {
+              auto keep = [&](const CUtensorMap *map, const uint32_t (&y)[32]) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) o[j] = pack_bf16x2(__uint_as_float(y[2 * j]), __uint_as_float(y[2 * j + 1]));
+                out.put(map, o, n, mw);
+              };
+              keep(&mO1, v);
+              keep(&mO2, w);
+            }
           }
         }
         __syncwarp();  // (the next chunk is read by the whole warp)
       }
     }
+    if (lane == 0) bulk_wait_group<0>();  // every store has been performed before the CTA exits
+    __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
@@ -394,24 +562,39 @@ __global__ void __launch_bounds__(256) join_kernel(const Args a) {
   wait_previous_kernel();
   allow_next_kernel();
   if (!mine) return;
-  uint4 ra = make_uint4(0u, 0u, 0u, 0u), ru = ra;
+  const int64_t off = (int64_t)m * x.cols + n;
+  uint32_t ra[4] = {}, ru[4] = {};
   if constexpr (OP == kDHidden) {
-    const int64_t off = (int64_t)m * x.cols + n;
-    ra = *reinterpret_cast<const uint4 *>(a.a + off);
-    ru = *reinterpret_cast<const uint4 *>(a.u + off);
+    *reinterpret_cast<uint4 *>(ra) = *reinterpret_cast<const uint4 *>(a.a + off);
+    *reinterpret_cast<uint4 *>(ru) = *reinterpret_cast<const uint4 *>(a.u + off);
   }
-  float v[8] = {}, w[8] = {};
+  float2 v[4] = {}, w[4] = {};
 #pragma unroll 2
   for (int p = p0; p <= p1; ++p) {
     const int slot = 2 * p + (a.units * p / a.pairs < lo ? 1 : 0);
     const float *part = a.part + ((int64_t)slot * 2 + rank) * BN * kHalf + row;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      v[j] += part[(c + j) * kHalf];
-      if constexpr (OP == kHidden) w[j] += part[(BN / 2 + c + j) * kHalf];
+    for (int j = 0; j < 4; ++j) {
+      v[j] = __fadd2_rn(v[j], make_float2(part[(c + 2 * j) * kHalf], part[(c + 2 * j + 1) * kHalf]));
+      if constexpr (OP == kHidden)
+        w[j] = __fadd2_rn(w[j], make_float2(part[(BN / 2 + c + 2 * j) * kHalf], part[(BN / 2 + c + 2 * j + 1) * kHalf]));
     }
   }
-  finish8<OP>(a, x, m, n, v, w, ra, ru);
+  void *o = OP != kDW || x.prod == 0 ? a.o[0] : x.prod == 1 ? a.o[1] : a.o[2];
+  if (OP == kDW && a.f32) {
+    float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(o) + off);
+    p[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+    p[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
+    return;
+  }
+  uint32_t o0[4], o1[4], o2[4];
+  results<OP>(a.act, v, w, ra, ru, o0, o1, o2);
+  auto put = [&](void *to, const uint32_t (&y)[4]) {
+    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(to) + off) = make_uint4(y[0], y[1], y[2], y[3]);
+  };
+  put(o, o0);
+  if (OP == kDHidden || (OP == kHidden && a.o[1])) put(a.o[1], o1);
+  if ((OP == kDHidden || OP == kHidden) && a.o[2]) put(a.o[2], o2);
 }
 
 // ------------------------------------------------------------------------------------------------ host
@@ -426,19 +609,36 @@ inline cudaError_t make_matrix_map(CUtensorMap *m, const void *ptr, int64_t inne
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
+// Row-major [rows][cols] without gaps, in pieces of 32 x 32 to be stored: BF16 (64-byte swizzle) or FP32 (128-byte).
+inline cudaError_t make_result_map(CUtensorMap *m, void *ptr, int64_t cols, int64_t rows, bool f32) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return cudaErrorNotSupported;
+  cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)((f32 ? 4 : 2) * cols)};
+  cuuint32_t box[2] = {32, 32}, es[2] = {1, 1};
+  CUresult r = enc(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, ptr, dims, strides, box, es,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                   CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
 
 inline int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
-// How many pairs share the tiles that fill no whole wave (0: each goes to one pair). In units of a 64-channel block of
-// a tile (0.27 us): what sharing saves against the joining kernel (3 us) and its traffic at 6.5 TB/s.
-inline int sharing_pairs(int tiles, int nk, int64_t rows, int bn, int pairs) {
+// How many pairs share the tiles that fill no whole wave (0: each goes to one pair), and the time of it all, in units of a
+// 64-channel block of a 256-column tile (0.27 us): sharing costs the joining kernel (3 us) and its traffic at 6.5 TB/s.
+struct Split {
+  int pairs;
+  double time;
+};
+inline Split split_of(int tiles, int nk, int64_t rows, int bn, int pairs) {
+  const double unit = bn == 256 ? 1.0 : 0.58;  // (a block of 128 columns has half of the products and three quarters of the loads)
   const int tail = tiles % pairs;
-  if (!tail) return 0;
+  const double whole = (double)(tiles / pairs) * nk * unit, alone = tail ? nk * unit : 0.0;
   const int64_t units = (int64_t)tail * nk;
   const int by = (int)std::min<int64_t>(pairs, units / 4);
-  if (by <= tail) return 0;
+  if (by <= tail) return {0, whole + alone};
   const double segments = std::min(2 * by, by + tail), bytes = segments * (double)std::min<int64_t>(rows, kRows) * bn * 8;
-  return nk - (double)ceil_div(units, by) > 12 + bytes / 6.5e12 / 0.27e-6 ? by : 0;
+  const double shared = ceil_div(units, by) * unit + 12 + bytes / 6.5e12 / 0.27e-6;
+  return shared < alone ? Split{by, whole + shared} : Split{0, whole + alone};
 }
 // (what any number of pairs can need)
 inline size_t share_bytes(int64_t bn) { return (size_t)2 * kMaxPairs * kRows * bn * sizeof(float); }
@@ -449,22 +649,29 @@ struct Matrix {
   int64_t inner, outer, pitch;
 };
 
+// One product in tiles of BN columns.
 template <int OP, int BN>
 struct Product {
-  CUtensorMap mA[3], mB[3];
+  CUtensorMap mA[3], mB[3], mO[3];
   Args a;
-  int grid, tiles;
-  // a's sizes, pointers and nk are set; nA, nB operands
-  cudaError_t plan(const Args &io, const Matrix *A, int nA, const Matrix *B, int nB, float *part, int *status, int dev, int nsm) {
+  int grid;
+  static int tiles(const Args &io, int i) { return ceil_div(io.rows[i], kRows) * ceil_div(io.cols[i], Cfg<OP, BN>::COLS); }
+  static Split split(const Args &io, int pairs, int *count) {
+    *count = OP == kDW ? 2 * tiles(io, 0) + tiles(io, 1) : tiles(io, 0);
+    return split_of(*count, io.nk, std::max(io.rows[0], io.rows[1]), BN, pairs);
+  }
+  cudaError_t plan(const Args &io, const Matrix *A, int nA, const Matrix *B, int nB, int pairs, int dev) {
     using C = Cfg<OP, BN>;
     a = io;
-    a.part = part;
-    a.status = status;
+    a.box = io.rows[0] < kHalf ? (io.rows[0] + 7) / 8 * 8 : kHalf;
+    a.wide = a.cols[0] % 16 == 0 && ((reinterpret_cast<uintptr_t>(a.a) | reinterpret_cast<uintptr_t>(a.u)) & 31u) == 0;
     cudaError_t e = cudaSuccess;
     for (int i = 0; i < 3 && e == cudaSuccess; ++i) {
       const Matrix &x = A[i < nA ? i : 0], &y = B[i < nB ? i : 0];
-      e = make_matrix_map(&mA[i], x.p, x.inner, x.outer, x.pitch, C::AMN ? 64 : kHalf);
+      e = make_matrix_map(&mA[i], x.p, x.inner, x.outer, x.pitch, C::AMN ? 64 : a.box);
       if (e == cudaSuccess) e = make_matrix_map(&mB[i], y.p, y.inner, y.outer, y.pitch, C::BMN ? 64 : BN / 2);
+      const int k = a.o[i] ? i : 0, sizes = OP == kDW && k == 2 ? 1 : 0;
+      if (e == cudaSuccess) e = make_result_map(&mO[i], a.o[k], a.cols[sizes], a.rows[sizes], OP == kDW && a.f32);
     }
     if (e != cudaSuccess) return e;
     static DeviceOnce ready;
@@ -477,12 +684,10 @@ struct Product {
       a.mt[i] = ceil_div(a.rows[i], kRows);
       a.nt[i] = ceil_div(a.cols[i], C::COLS);
     }
-    tiles = a.mt[0] * a.nt[0];
-    if (OP == kDW) tiles = 2 * tiles + a.mt[1] * a.nt[1];
-    const int pairs = std::max(1, std::min(nsm / 2, kMaxPairs));
-    a.pairs = sharing_pairs(tiles, a.nk, std::max(a.rows[0], a.rows[1]), BN, pairs);
-    a.tail = a.pairs ? tiles % pairs : 0;
-    a.full = tiles - a.tail;
+    int count;
+    a.pairs = split(io, pairs, &count).pairs;
+    a.tail = a.pairs ? count % pairs : 0;
+    a.full = count - a.tail;
     a.units = (int64_t)a.tail * a.nk;
     grid = 2 * std::min(pairs, std::max(a.pairs, a.full));
     return cudaSuccess;
@@ -490,15 +695,36 @@ struct Product {
   cudaError_t launch(cudaStream_t st) const {
     using C = Cfg<OP, BN>;
     cudaError_t e = launch_after(product_kernel<OP, BN>, dim3(grid), dim3(C::NTHREADS), C::SMEM_ALLOC, st, mA[0], mA[1], mA[2], mB[0],
-                                 mB[1], mB[2], a);
+                                 mB[1], mB[2], mO[0], mO[1], mO[2], a);
     if (e == cudaSuccess && a.pairs) e = launch_after(join_kernel<OP, BN>, dim3(a.tail, 2 * (C::COLS / 16)), dim3(256), 0, st, a);
     return e;
   }
 };
 
-inline cudaError_t device_and_sms(int *dev, int *nsm) {
+// A product in tiles of 256 columns, or of 128 where these fill the pairs better or waste fewer columns.
+template <int OP>
+struct AnyProduct {
+  union {
+    Product<OP, 256> wide;
+    Product<OP, 128> narrow;
+  };
+  bool use_narrow;
+  AnyProduct() {}
+  cudaError_t plan(const Args &io, const Matrix *A, int nA, const Matrix *B, int nB, int pairs, int dev) {
+    int count;
+    use_narrow = Product<OP, 128>::split(io, pairs, &count).time < Product<OP, 256>::split(io, pairs, &count).time;
+    return use_narrow ? narrow.plan(io, A, nA, B, nB, pairs, dev) : wide.plan(io, A, nA, B, nB, pairs, dev);
+  }
+  cudaError_t launch(cudaStream_t st) const { return use_narrow ? narrow.launch(st) : wide.launch(st); }
+};
+
+// The current device and its pairs of SMs (kMaxPairs at most: workspaces are sized for them).
+inline cudaError_t device_and_pairs(int *dev, int *pairs) {
+  int nsm = 0;
   cudaError_t e = current_device(dev);
-  return e != cudaSuccess ? e : cudaDeviceGetAttribute(nsm, cudaDevAttrMultiProcessorCount, *dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, *dev);
+  *pairs = std::max(1, std::min(nsm / 2, kMaxPairs));
+  return e;
 }
 
 inline int64_t aligned256(int64_t n) { return (n + 255) / 256 * 256; }

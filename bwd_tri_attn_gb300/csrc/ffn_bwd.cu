@@ -27,15 +27,16 @@ struct BwdCall {
   void *dx, *dW[3];
 };
 
-template <int BN>
 cudaError_t launch_bwd(const tri_ffn_shape &s, const BwdCall &c, char *ws, int *status, cudaStream_t st) {
   const BwdWorkspace w = bwd_workspace(s);
-  int dev = 0, nsm = 0;
-  cudaError_t e = device_and_sms(&dev, &nsm);
+  int dev = 0, pairs = 0;
+  cudaError_t e = device_and_pairs(&dev, &pairs);
   if (e != cudaSuccess) return e;
   float *part = reinterpret_cast<float *>(ws + w.part);
   const int64_t C = s.C, F = s.F, M = s.M, ldx = s.ldx ? s.ldx : C, ldd = s.lddout ? s.lddout : C;
   Args io{};
+  io.part = part;
+  io.status = status;
   io.act = s.act;
   io.rows[0] = io.rows[1] = (int)M;
   io.cols[0] = io.cols[1] = s.F;
@@ -46,32 +47,36 @@ cudaError_t launch_bwd(const tri_ffn_shape &s, const BwdCall &c, char *ws, int *
   io.o[1] = ws + w.du;
   io.o[2] = c.dW[0] ? ws + w.h : nullptr;
   const Matrix mdout{c.dout, C, M, ldd}, mwd{c.Wd, F, C, F};
-  Product<kDHidden, 256> hidden;
-  e = hidden.plan(io, &mdout, 1, &mwd, 1, part, status, dev, nsm);
+  AnyProduct<kDHidden> hidden;
+  e = hidden.plan(io, &mdout, 1, &mwd, 1, pairs, dev);
   if (e != cudaSuccess) return e;
   const Matrix features[3] = {{ws + w.da, F, M, F}, {ws + w.du, F, M, F}, {ws + w.h, F, M, F}};
-  Product<kDx, BN> dx;
+  AnyProduct<kDx> dx;
   if (c.dx) {
     const Matrix weights[2] = {{c.Wg, C, F, C}, {c.Wu, C, F, C}};
     Args o{};
+    o.part = part;
+    o.status = status;
     o.rows[0] = o.rows[1] = (int)M;
     o.cols[0] = o.cols[1] = s.C;
     o.nk0 = ceil_div(F, kBlock);
     o.nk = 2 * o.nk0;
     o.o[0] = c.dx;
-    e = dx.plan(o, features, 2, weights, 2, part, status, dev, nsm);
+    e = dx.plan(o, features, 2, weights, 2, pairs, dev);
     if (e != cudaSuccess) return e;
   }
-  Product<kDW, BN> dW;
+  AnyProduct<kDW> dW;
   if (c.dW[0]) {
     const Matrix left[3] = {features[0], features[1], mdout}, right[3] = {{c.x, C, M, ldx}, {c.x, C, M, ldx}, features[2]};
     Args o{};
+    o.part = part;
+    o.status = status;
     o.rows[0] = o.cols[1] = s.F;
     o.cols[0] = o.rows[1] = s.C;
     o.nk = o.nk0 = ceil_div(M, kBlock);
     o.f32 = s.wgrad_fp32 != 0;
     for (int i = 0; i < 3; ++i) o.o[i] = c.dW[i];
-    e = dW.plan(o, left, 3, right, 3, part, status, dev, nsm);
+    e = dW.plan(o, left, 3, right, 3, pairs, dev);
     if (e != cudaSuccess) return e;
   }
   e = hidden.launch(st);
@@ -108,7 +113,7 @@ int tri_ffn_bwd(tri_ffn_shape shape, const tri_attn_bf16 *x, const tri_attn_bf16
   const auto st = static_cast<cudaStream_t>(stream);
   const BwdCall c{x, Wg, Wu, Wd, a, u, dout, dx, {dWg, dWu, dWd}};
   char *ws = static_cast<char *>(workspace);
-  const cudaError_t e = shape.C <= 128 ? launch_bwd<128>(shape, c, ws, status, st) : launch_bwd<256>(shape, c, ws, status, st);
+  const cudaError_t e = launch_bwd(shape, c, ws, status, st);
   return e == cudaSuccess ? TRI_ATTN_OK : TRI_ATTN_ERR_CUDA;
 }
 

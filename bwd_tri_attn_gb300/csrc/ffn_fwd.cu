@@ -18,16 +18,17 @@ FwdWorkspace fwd_workspace(const tri_ffn_shape &s) {
   return w;
 }
 
-template <int BN>
 cudaError_t launch_fwd(const tri_ffn_shape &s, const void *x, const void *Wg, const void *Wu, const void *Wd, void *out, void *a,
                        void *u, char *ws, int *status, cudaStream_t st) {
   const FwdWorkspace w = fwd_workspace(s);
-  int dev = 0, nsm = 0;
-  cudaError_t e = device_and_sms(&dev, &nsm);
+  int dev = 0, pairs = 0;
+  cudaError_t e = device_and_pairs(&dev, &pairs);
   if (e != cudaSuccess) return e;
   float *part = reinterpret_cast<float *>(ws + w.part);
   const int64_t C = s.C, F = s.F, ldx = s.ldx ? s.ldx : C;
   Args io{};
+  io.part = part;
+  io.status = status;
   io.act = s.act;
   io.rows[0] = io.rows[1] = (int)s.M;
   io.cols[0] = io.cols[1] = s.F;
@@ -36,17 +37,19 @@ cudaError_t launch_fwd(const tri_ffn_shape &s, const void *x, const void *Wg, co
   io.o[1] = a;
   io.o[2] = u;
   const Matrix mx{x, C, s.M, ldx}, mw[2] = {{Wg, C, F, C}, {Wu, C, F, C}};
-  Product<kHidden, 256> hidden;
-  e = hidden.plan(io, &mx, 1, mw, 2, part, status, dev, nsm);
+  AnyProduct<kHidden> hidden;
+  e = hidden.plan(io, &mx, 1, mw, 2, pairs, dev);
   if (e != cudaSuccess) return e;
   Args io2{};
+  io2.part = part;
+  io2.status = status;
   io2.rows[0] = io2.rows[1] = (int)s.M;
   io2.cols[0] = io2.cols[1] = s.C;
   io2.nk = io2.nk0 = ceil_div(F, kBlock);
   io2.o[0] = out;
   const Matrix mh{ws + w.h, F, s.M, F}, md{Wd, F, C, F};
-  Product<kOut, BN> down;
-  e = down.plan(io2, &mh, 1, &md, 1, part, status, dev, nsm);
+  AnyProduct<kOut> down;
+  e = down.plan(io2, &mh, 1, &md, 1, pairs, dev);
   if (e != cudaSuccess) return e;
   e = hidden.launch(st);
   return e == cudaSuccess ? down.launch(st) : e;
@@ -75,8 +78,7 @@ int tri_ffn_fwd(tri_ffn_shape shape, const tri_attn_bf16 *x, const tri_attn_bf16
   if (!status) return TRI_ATTN_ERR_CUDA;
   const auto st = static_cast<cudaStream_t>(stream);
   char *ws = static_cast<char *>(workspace);
-  const cudaError_t e = shape.C <= 128 ? launch_fwd<128>(shape, x, Wg, Wu, Wd, out, a, u, ws, status, st)
-                                       : launch_fwd<256>(shape, x, Wg, Wu, Wd, out, a, u, ws, status, st);
+  const cudaError_t e = launch_fwd(shape, x, Wg, Wu, Wd, out, a, u, ws, status, st);
   return e == cudaSuccess ? TRI_ATTN_OK : TRI_ATTN_ERR_CUDA;
 }
 

@@ -1,6 +1,7 @@
 // Relative position bias by buckets and its gradient (include/tri_relpos.h states the formulas).
 //
-// A CTA takes a piece of one head's plane of Nq x Nk values, in 16-byte vectors between 16-byte boundaries whatever Nk is. What a
+// A warp takes 512 consecutive values of one head's plane of Nq x Nk at a time, eight pairs a lane, neighbouring lanes
+// neighbouring pairs, so that accesses are whole lines whatever Nk is and the distances that meet in a lookup are consecutive too. What a
 // distance d leads to (the table's value forward, its row backward) stands in shared memory for every d from -L to L, L the
 // last bucket's start, so an element costs a subtraction, a clamp and a lookup; beyond L on either side all d share a row. Where
 // that table would not fit (L above kLookup), the bucket is searched for element by element. Memory bandwidth bounds the
@@ -20,13 +21,16 @@ namespace {
 
 constexpr int kLookup = 4096;
 constexpr int kFwdThreads = 256, kBwdThreads = 128;
+constexpr int kFwdCtas = 152 * 16, kBwdCtas = 152 * 6;  // about one wave of the backward's, whose ends cost it
 
 struct RelArgs {
   int B, H, Nq, Nk, K, two, rows;
   int L;          // the last bucket's start, or 1: from there on either side all differences share a row
   int64_t plane;  // Nq Nk
-  int piece;      // vectors of a CTA
+  int64_t units;  // of 512 values, of a plane
+  int piece;      // units of a CTA
   int pieces;     // CTAs of a plane
+  int step_i, step_j;  // 64 values further on: rows and columns
   const float *table;
   const int32_t *posq, *posk;
   const uint16_t *base;
@@ -56,31 +60,64 @@ __device__ __forceinline__ int sub_sat(int x, int y) {
   return max(r, -0x7fffffff);
 }
 
-// Values begin .. end - 1 of the vector that starts at value e0 of a plane are the plane's; their differences, d[].
-struct Vector {
-  int64_t e0;
-  int begin, end;
-};
-__device__ __forceinline__ Vector vector_at(const RelArgs &a, int64_t plane0, int64_t k) {
-  Vector v;
-  v.e0 = 8 * k - (plane0 & 7);
-  v.begin = (int)max((int64_t)0, -v.e0);
-  v.end = (int)min((int64_t)8, a.plane - v.e0);
-  return v;
-}
-__device__ __forceinline__ void differences(const RelArgs &a, int b, const Vector &v, int (&d)[8]) {
-  const uint32_t e = (uint32_t)(v.e0 + v.begin), nk = (uint32_t)a.Nk;
-  int i = (int)(e / nk), j = (int)(e - (uint32_t)i * nk);
-#pragma unroll
-  for (int x = 0; x < 8; ++x) {
-    d[x] = 0;
-    if (x < v.begin || x >= v.end) continue;
-    d[x] = a.posq ? sub_sat(__ldg(a.posk + (int64_t)b * a.Nk + j), __ldg(a.posq + (int64_t)b * a.Nq + i)) : j - i;
-    if (++j == a.Nk) {
-      j = 0;
+// A lane's walk over its pairs: values e and e + 1 of a plane, at an even index of the tensor (so e may be -1), 64 apart.
+struct Walk {
+  int64_t e;
+  int i, j;  // of value e
+  __device__ __forceinline__ Walk(const RelArgs &a, int64_t plane0, int64_t k) {
+    e = 512 * k - (plane0 & 1) + 2 * (threadIdx.x & 31);
+    const uint32_t at = (uint32_t)max(e, (int64_t)0), nk = (uint32_t)a.Nk;
+    i = (int)(at / nk);
+    j = (int)(at - (uint32_t)i * nk) - (e < 0 ? 1 : 0);
+  }
+  __device__ __forceinline__ void step(const RelArgs &a) {
+    e += 64;
+    i += a.step_i;
+    j += a.step_j;
+    if (j < 0) {  // (from e = -1 on by whole rows)
+      j += a.Nk;
+      --i;
+    }
+    if (j >= a.Nk) {
+      j -= a.Nk;
       ++i;
     }
   }
+  // Which of the two belong to the plane, and their differences (of the others: anything).
+  __device__ __forceinline__ void pair(const RelArgs &a, int b, bool &first, bool &second, int &d0, int &d1) const {
+    first = e >= 0 && e < a.plane;
+    second = e + 1 < a.plane;
+    const bool turn = j + 1 == a.Nk;  // (the second one begins the next row)
+    const int i1 = turn ? i + 1 : i, j1 = turn ? 0 : j + 1;
+    if (!a.posq) {
+      d0 = j - i;
+      d1 = j1 - i1;
+      return;
+    }
+    const int32_t *pq = a.posq + (int64_t)b * a.Nq, *pk = a.posk + (int64_t)b * a.Nk;
+    const int q0 = first ? __ldg(pq + i) : 0, q1 = turn && second ? __ldg(pq + i1) : first ? q0 : second ? __ldg(pq + i1) : 0;
+    int k0 = 0, k1 = 0;
+    if (first && second && !turn && (reinterpret_cast<uintptr_t>(pk + j) & 7) == 0) {
+      const int2 both = __ldg(reinterpret_cast<const int2 *>(pk + j));
+      k0 = both.x;
+      k1 = both.y;
+    } else {
+      if (first) k0 = __ldg(pk + j);
+      if (second) k1 = __ldg(pk + j1);
+    }
+    d0 = sub_sat(k0, q0);
+    d1 = sub_sat(k1, q1);
+  }
+};
+constexpr int kPairs = 8;  // of a lane at a time
+
+// Values at and at + 1 of a tensor (at even), zeros for those that are not asked for.
+__device__ __forceinline__ uint32_t load_pair(const uint16_t *p, int64_t at, bool first, bool second) {
+  if (first && second) return __ldcs(reinterpret_cast<const unsigned int *>(p + at));
+  uint32_t w = 0u;
+  if (first) w = p[at];
+  if (second) w = (uint32_t)p[at + 1] << 16;
+  return w;
 }
 
 template <bool kNear>  // L <= kLookup
@@ -91,43 +128,38 @@ __global__ void __launch_bounds__(kFwdThreads) relpos_fwd_kernel(const __grid_co
   for (int x = threadIdx.x; x < (kNear ? 2 * a.L + 1 : a.rows); x += kFwdThreads)
     value[x] = __ldg(a.table + (int64_t)(kNear ? row_of(a, x - a.L) : x) * a.H + h);
   __syncthreads();
-  const int64_t plane0 = bh * a.plane;  // (a multiple of 8 values is a 16-byte boundary)
-  const int64_t k1 = min((int64_t)(blockIdx.x + 1) * a.piece, (a.plane + (plane0 & 7) + 7) / 8);
-  for (int64_t k = (int64_t)blockIdx.x * a.piece + threadIdx.x; k < k1; k += kFwdThreads) {
-    const Vector v = vector_at(a, plane0, k);
-    const int64_t at = plane0 + v.e0;
-    const bool whole = v.begin == 0 && v.end == 8;
-    Pairs<__nv_bfloat16> f;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) f.v[j] = make_float2(0.f, 0.f);
+  const int64_t plane0 = bh * a.plane;
+  constexpr int W = kFwdThreads / 32;
+  for (int64_t k = (int64_t)blockIdx.x * a.piece + (threadIdx.x >> 5); k < min((int64_t)(blockIdx.x + 1) * a.piece, a.units); k += W) {
+    Walk w(a, plane0, k);
+    uint32_t base[kPairs];
     if (a.base) {
-      uint4 w = make_uint4(0u, 0u, 0u, 0u);
-      if (whole) {
-        w = *reinterpret_cast<const uint4 *>(a.base + at);
-      } else {
-        uint32_t p[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-        for (int x = 0; x < 8; ++x)
-          if (x >= v.begin && x < v.end) p[x / 2] |= (uint32_t)a.base[at + x] << (16 * (x & 1));
-        w = make_uint4(p[0], p[1], p[2], p[3]);
+      for (int p = 0; p < kPairs; ++p) {
+        const int64_t e = w.e + 64 * p;
+        base[p] = load_pair(a.base, plane0 + e, e >= 0 && e < a.plane, e + 1 < a.plane);
       }
-      chunk_unpack(w, f);
     }
-    int d[8];
-    differences(a, b, v, d);
-    float t[8];
 #pragma unroll
-    for (int x = 0; x < 8; ++x) t[x] = value[kNear ? min(max(d[x], -a.L), a.L) + a.L : row_of(a, d[x])];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) f.v[j] = __fadd2_rn(f.v[j], make_float2(t[2 * j], t[2 * j + 1]));
-    const uint4 o = chunk_pack(f);
-    if (whole) {
-      *reinterpret_cast<uint4 *>(a.bias + at) = o;
-    } else {
-      const uint32_t p[4] = {o.x, o.y, o.z, o.w};
-#pragma unroll
-      for (int x = 0; x < 8; ++x)
-        if (x >= v.begin && x < v.end) a.bias[at + x] = (uint16_t)(p[x / 2] >> (16 * (x & 1)));
+    for (int p = 0; p < kPairs; ++p) {
+      bool first, second;
+      int d0, d1;
+      w.pair(a, b, first, second, d0, d1);
+      const int64_t at = plane0 + w.e;
+      w.step(a);
+      float2 t;
+      if (kNear)
+        t = make_float2(value[min(max(d0, -a.L), a.L) + a.L], value[min(max(d1, -a.L), a.L) + a.L]);
+      else
+        t = make_float2(value[row_of(a, d0)], value[row_of(a, d1)]);
+      if (a.base) t = __fadd2_rn(t, make_float2(__uint_as_float(base[p] << 16), __uint_as_float(base[p] & 0xffff0000u)));
+      const uint32_t o = sm100::pack_bf16x2(t.x, t.y);
+      if (first && second) {
+        *reinterpret_cast<uint32_t *>(a.bias + at) = o;
+      } else {
+        if (first) a.bias[at] = (uint16_t)o;
+        if (second) a.bias[at + 1] = (uint16_t)(o >> 16);
+      }
     }
   }
 }
@@ -148,48 +180,42 @@ __global__ void __launch_bounds__(kBwdThreads) relpos_bwd_kernel(const __grid_co
   __syncthreads();
   float *mine = sums + warp * a.rows * 33 + lane;
   const int64_t plane0 = bh * a.plane;
-  const int64_t k1 = min((int64_t)(blockIdx.x + 1) * a.piece, (a.plane + (plane0 & 7) + 7) / 8);
   float behind = 0.f, ahead = 0.f;  // d <= -L, d >= L
-  for (int64_t k = (int64_t)blockIdx.x * a.piece + threadIdx.x; k < k1; k += kBwdThreads) {
-    const Vector v = vector_at(a, plane0, k);
-    const int64_t at = plane0 + v.e0;
-    uint4 w;
-    if (v.begin == 0 && v.end == 8) {
-      w = ld_stream(reinterpret_cast<const uint4 *>(a.dbias + at));
-    } else {
-      uint32_t p[4] = {0u, 0u, 0u, 0u};
+  for (int64_t k = (int64_t)blockIdx.x * a.piece + warp; k < min((int64_t)(blockIdx.x + 1) * a.piece, a.units); k += W) {
+    Walk w(a, plane0, k);
+    uint32_t g[kPairs];
 #pragma unroll
-      for (int x = 0; x < 8; ++x)
-        if (x >= v.begin && x < v.end) p[x / 2] |= (uint32_t)a.dbias[at + x] << (16 * (x & 1));
-      w = make_uint4(p[0], p[1], p[2], p[3]);
+    for (int p = 0; p < kPairs; ++p) {
+      const int64_t e = w.e + 64 * p;
+      g[p] = load_pair(a.dbias, plane0 + e, e >= 0 && e < a.plane, e + 1 < a.plane);
     }
-    Pairs<__nv_bfloat16> f;
-    chunk_unpack(w, f);
-    int d[8];
-    differences(a, b, v, d);
 #pragma unroll
-    for (int x = 0; x < 8; ++x) {
-      const float g = x & 1 ? f.v[x / 2].y : f.v[x / 2].x;
-      if (x < v.begin || x >= v.end) continue;
-      if (d[x] <= -a.L)
-        behind += g;
-      else if (d[x] >= a.L)
-        ahead += g;
-      else
-        mine[(kNear ? row_at[d[x] + a.L] : row_of(a, d[x])) * 33] += g;
+    for (int p = 0; p < kPairs; ++p) {
+      bool first, second;
+      int d0, d1;
+      w.pair(a, b, first, second, d0, d1);
+      w.step(a);
+      const float g0 = __uint_as_float(g[p] << 16), g1 = __uint_as_float(g[p] & 0xffff0000u);
+      if (min(d0, d1) >= a.L) {  // (what is outside the plane is 0)
+        ahead += g0 + g1;
+      } else if (max(d0, d1) <= -a.L) {
+        behind += g0 + g1;
+      } else {
+        if (first) mine[(kNear ? row_at[min(max(d0, -a.L), a.L) + a.L] : row_of(a, d0)) * 33] += g0;
+        if (second) mine[(kNear ? row_at[min(max(d1, -a.L), a.L) + a.L] : row_of(a, d1)) * 33] += g1;
+      }
     }
   }
   mine[row_of(a, -0x7fffffff) * 33] += behind;
   mine[row_of(a, 0x7fffffff) * 33] += ahead;
   __syncthreads();
-  for (int r = threadIdx.x; r < a.rows; r += kBwdThreads) {
+  for (int r = warp; r < a.rows; r += W) {  // the warps' columns in turn, then the lanes by an xor tree
     float s = 0.f;
-    for (int i = 0; i < W; ++i) {
-      float t = 0.f;
-      for (int l = 0; l < 32; ++l) t += sums[(i * a.rows + r) * 33 + l];
-      s += t;
-    }
-    a.part[((int64_t)bh * a.pieces + blockIdx.x) * a.rows + r] = s;
+#pragma unroll
+    for (int i = 0; i < W; ++i) s += sums[(i * a.rows + r) * 33 + lane];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0) a.part[((int64_t)bh * a.pieces + blockIdx.x) * a.rows + r] = s;
   }
 }
 
@@ -222,17 +248,16 @@ int starts_check(const tri_relpos_shape &s, const int32_t *starts) {
   return TRI_ATTN_OK;
 }
 
-// A plane's pieces: some 16 CTAs per SM over all planes, of at least four vectors a thread.
-void cut(RelArgs &a, int threads) {
-  const int64_t vectors = (a.plane + 14) / 8, planes = (int64_t)a.B * a.H;
-  const int64_t want = std::max<int64_t>(1, 152 * 16 / planes);
-  int64_t piece = std::max<int64_t>((vectors + want - 1) / want, 4 * threads);
-  piece = (piece + threads - 1) / threads * threads;
-  a.piece = (int)piece;
-  a.pieces = (int)((vectors + piece - 1) / piece);
+// A plane's pieces: about as many CTAs over all planes as are given, each of at least two units a warp.
+void cut(RelArgs &a, int warps, int ctas) {
+  a.units = (a.plane + 1 + 511) / 512;
+  const int64_t planes = (int64_t)a.B * a.H, want = std::max<int64_t>(1, ctas / planes);
+  const int64_t piece = std::max<int64_t>((a.units + want - 1) / want, 2 * warps);
+  a.piece = (int)((piece + warps - 1) / warps * warps);
+  a.pieces = (int)((a.units + a.piece - 1) / a.piece);
 }
 
-RelArgs rel_args(const tri_relpos_shape &s, int threads) {
+RelArgs rel_args(const tri_relpos_shape &s, int warps, int ctas) {
   RelArgs a{};
   a.B = s.B;
   a.H = s.H;
@@ -242,7 +267,9 @@ RelArgs rel_args(const tri_relpos_shape &s, int threads) {
   a.two = s.two_sided;
   a.rows = s.K << s.two_sided;
   a.plane = (int64_t)s.Nq * s.Nk;
-  cut(a, threads);
+  a.step_i = 64 / a.Nk;
+  a.step_j = 64 % a.Nk;
+  cut(a, warps, ctas);
   return a;
 }
 void set_starts(RelArgs &a, const int32_t *starts) {
@@ -282,7 +309,7 @@ int tri_relpos_fwd(tri_relpos_shape shape, const int32_t *starts, const float *t
   if ((reinterpret_cast<uintptr_t>(base) | reinterpret_cast<uintptr_t>(bias)) & 15u) return TRI_ATTN_ERR_UNSUPPORTED;
   if ((reinterpret_cast<uintptr_t>(table) | reinterpret_cast<uintptr_t>(positions) | reinterpret_cast<uintptr_t>(key_positions)) & 3u)
     return TRI_ATTN_ERR_UNSUPPORTED;
-  RelArgs a = rel_args(shape, kFwdThreads);
+  RelArgs a = rel_args(shape, kFwdThreads / 32, kFwdCtas);
   set_starts(a, starts);
   a.table = table;
   a.posq = positions;
@@ -299,7 +326,7 @@ int tri_relpos_fwd(tri_relpos_shape shape, const int32_t *starts, const float *t
 
 size_t tri_relpos_bwd_workspace_size(tri_relpos_shape shape) {
   if (relpos_check(shape)) return 0;
-  const RelArgs a = rel_args(shape, kBwdThreads);
+  const RelArgs a = rel_args(shape, kBwdThreads / 32, kBwdCtas);
   return sizeof(float) * (size_t)a.B * a.H * a.pieces * a.rows;
 }
 
@@ -314,7 +341,7 @@ int tri_relpos_bwd(tri_relpos_shape shape, const int32_t *starts, const int32_t 
        reinterpret_cast<uintptr_t>(workspace)) & 3u)
     return TRI_ATTN_ERR_UNSUPPORTED;
   if (!workspace || workspace_bytes < tri_relpos_bwd_workspace_size(shape)) return TRI_ATTN_ERR_WORKSPACE;
-  RelArgs a = rel_args(shape, kBwdThreads);
+  RelArgs a = rel_args(shape, kBwdThreads / 32, kBwdCtas);
   set_starts(a, starts);
   a.posq = positions;
   a.posk = key_positions;
