@@ -27,7 +27,7 @@ struct RelArgs {
   int B, H, Nq, Nk, K, two, rows;
   int L;          // the last bucket's start, or 1: from there on either side all differences share a row
   int64_t plane;  // Nq Nk
-  int64_t units;  // of 512 values, of a plane
+  int units;      // of 512 values, of a plane
   int piece;      // units of a CTA
   int pieces;     // CTAs of a plane
   int step_i, step_j;  // 64 values further on: rows and columns
@@ -60,67 +60,58 @@ __device__ __forceinline__ int sub_sat(int x, int y) {
   return max(r, -0x7fffffff);
 }
 
-// A lane's walk over its pairs: values e and e + 1 of a plane, at an even index of the tensor (so e may be -1), 64 apart.
-struct Walk {
-  int64_t e;
-  int i, j;  // of value e
-  __device__ __forceinline__ Walk(const RelArgs &a, int64_t plane0, int64_t k) {
-    e = 512 * k - (plane0 & 1) + 2 * (threadIdx.x & 31);
-    const uint32_t at = (uint32_t)max(e, (int64_t)0), nk = (uint32_t)a.Nk;
-    i = (int)(at / nk);
-    j = (int)(at - (uint32_t)i * nk) - (e < 0 ? 1 : 0);
-  }
-  __device__ __forceinline__ void step(const RelArgs &a) {
-    e += 64;
-    i += a.step_i;
-    j += a.step_j;
-    if (j < 0) {  // (from e = -1 on by whole rows)
-      j += a.Nk;
-      --i;
-    }
-    if (j >= a.Nk) {
-      j -= a.Nk;
-      ++i;
-    }
-  }
-  // Which of the two belong to the plane, and their differences (of the others: anything).
-  __device__ __forceinline__ void pair(const RelArgs &a, int b, bool &first, bool &second, int &d0, int &d1) const {
-    first = e >= 0 && e < a.plane;
-    second = e + 1 < a.plane;
-    const bool turn = j + 1 == a.Nk;  // (the second one begins the next row)
-    const int i1 = turn ? i + 1 : i, j1 = turn ? 0 : j + 1;
-    if (!a.posq) {
-      d0 = j - i;
-      d1 = j1 - i1;
-      return;
-    }
-    const int32_t *pq = a.posq + (int64_t)b * a.Nq, *pk = a.posk + (int64_t)b * a.Nk;
-    const int q0 = first ? __ldg(pq + i) : 0, q1 = turn && second ? __ldg(pq + i1) : first ? q0 : second ? __ldg(pq + i1) : 0;
-    int k0 = 0, k1 = 0;
-    if (first && second && !turn && (reinterpret_cast<uintptr_t>(pk + j) & 7) == 0) {
-      const int2 both = __ldg(reinterpret_cast<const int2 *>(pk + j));
-      k0 = both.x;
-      k1 = both.y;
-    } else {
-      if (first) k0 = __ldg(pk + j);
-      if (second) k1 = __ldg(pk + j1);
-    }
-    d0 = sub_sat(k0, q0);
-    d1 = sub_sat(k1, q1);
-  }
-};
-constexpr int kPairs = 8;  // of a lane at a time
-
-// Values at and at + 1 of a tensor (at even), zeros for those that are not asked for.
-__device__ __forceinline__ uint32_t load_pair(const uint16_t *p, int64_t at, bool first, bool second) {
-  if (first && second) return __ldcs(reinterpret_cast<const unsigned int *>(p + at));
-  uint32_t w = 0u;
-  if (first) w = p[at];
-  if (second) w = (uint32_t)p[at + 1] << 16;
-  return w;
+// The difference of value e of a plane.
+template <bool kPos>
+__device__ __forceinline__ int difference(const RelArgs &a, int b, int e) {
+  const int i = (int)((uint32_t)e / (uint32_t)a.Nk), j = e - i * a.Nk;
+  return kPos ? sub_sat(__ldg(a.posk + (int64_t)b * a.Nk + j), __ldg(a.posq + (int64_t)b * a.Nq + i)) : j - i;
 }
 
-template <bool kNear>  // L <= kLookup
+// A lane's walk over its pairs of a unit that lies inside the plane: values e and e + 1, 64 further on with each step.
+template <bool kPos>
+struct Walk {
+  int j, d, i, q;  // of value e: column, j - i; kPos: row and its position
+  const int32_t *pq, *pk;
+  __device__ __forceinline__ Walk(const RelArgs &a, int b, int e) : q(0), pq(nullptr), pk(nullptr) {
+    i = (int)((uint32_t)e / (uint32_t)a.Nk);
+    j = e - i * a.Nk;
+    d = j - i;
+    if (kPos) {
+      pq = a.posq + (int64_t)b * a.Nq;
+      pk = a.posk + (int64_t)b * a.Nk;
+      q = __ldg(pq + i);
+    }
+  }
+  __device__ __forceinline__ void step(const RelArgs &a) {
+    j += a.step_j;
+    d += a.step_j - a.step_i;
+    const bool wrap = j >= a.Nk;
+    if (wrap) {
+      j -= a.Nk;
+      d -= a.Nk + 1;
+    }
+    if (kPos) {
+      i += a.step_i + (wrap ? 1 : 0);
+      if (wrap || a.step_i) q = __ldg(pq + min(i, a.Nq - 1));  // (one step past the unit's end is made)
+    }
+  }
+  __device__ __forceinline__ void pair(const RelArgs &a, int &d0, int &d1) const {
+    const bool turn = j + 1 == a.Nk;  // (the second one begins the next row)
+    if (!kPos) {
+      d0 = d;
+      d1 = d + (turn ? -a.Nk : 1);
+    } else {
+      d0 = sub_sat(__ldg(pk + j), q);
+      d1 = sub_sat(__ldg(pk + (turn ? 0 : j + 1)), turn ? __ldg(pq + i + 1) : q);
+    }
+  }
+};
+constexpr int kUnit = 512, kPairs = kUnit / 64;  // values of a warp at a time, pairs of a lane
+
+// First value (an even index of the tensor; -1 in the first unit where the plane begins at an odd one) of unit k.
+__device__ __forceinline__ int unit_start(int64_t plane0, int k) { return kUnit * k - (int)(plane0 & 1); }
+
+template <bool kNear, bool kPos>  // L <= kLookup; positions
 __global__ void __launch_bounds__(kFwdThreads) relpos_fwd_kernel(const __grid_constant__ RelArgs a) {
   extern __shared__ float value[];  // kNear: by distance; else by row
   const int bh = blockIdx.y + gridDim.y * blockIdx.z, b = bh / a.H, h = bh - b * a.H;
@@ -128,44 +119,40 @@ __global__ void __launch_bounds__(kFwdThreads) relpos_fwd_kernel(const __grid_co
   for (int x = threadIdx.x; x < (kNear ? 2 * a.L + 1 : a.rows); x += kFwdThreads)
     value[x] = __ldg(a.table + (int64_t)(kNear ? row_of(a, x - a.L) : x) * a.H + h);
   __syncthreads();
+  auto value_of = [&](int d) { return value[kNear ? min(max(d, -a.L), a.L) + a.L : row_of(a, d)]; };
   const int64_t plane0 = bh * a.plane;
-  constexpr int W = kFwdThreads / 32;
-  for (int64_t k = (int64_t)blockIdx.x * a.piece + (threadIdx.x >> 5); k < min((int64_t)(blockIdx.x + 1) * a.piece, a.units); k += W) {
-    Walk w(a, plane0, k);
-    uint32_t base[kPairs];
+  const int lane = threadIdx.x & 31, k1 = min((blockIdx.x + 1) * a.piece, a.units);
+  for (int k = blockIdx.x * a.piece + (threadIdx.x >> 5); k < k1; k += kFwdThreads / 32) {
+    const int u0 = unit_start(plane0, k);
+    if (u0 < 0 || u0 + kUnit > a.plane) {  // a plane's ends, value by value
+      for (int e = u0 + lane + (u0 + lane < 0 ? 32 : 0); e < min(u0 + kUnit, (int)a.plane); e += 32) {
+        const uint16_t w = a.base ? a.base[plane0 + e] : 0;
+        a.bias[plane0 + e] = f32_to_bf16_rn(value_of(difference<kPos>(a, b, e)) + bf16_to_f32(w));
+      }
+      continue;
+    }
+    const int64_t at = plane0 + u0 + 2 * lane;
+    const uint32_t *base = reinterpret_cast<const uint32_t *>(a.base + at);
+    uint32_t *bias = reinterpret_cast<uint32_t *>(a.bias + at), in[kPairs];
     if (a.base) {
 #pragma unroll
-      for (int p = 0; p < kPairs; ++p) {
-        const int64_t e = w.e + 64 * p;
-        base[p] = load_pair(a.base, plane0 + e, e >= 0 && e < a.plane, e + 1 < a.plane);
-      }
+      for (int p = 0; p < kPairs; ++p) in[p] = __ldcs(base + 32 * p);
     }
+    Walk<kPos> w(a, b, u0 + 2 * lane);
 #pragma unroll
     for (int p = 0; p < kPairs; ++p) {
-      bool first, second;
       int d0, d1;
-      w.pair(a, b, first, second, d0, d1);
-      const int64_t at = plane0 + w.e;
+      w.pair(a, d0, d1);
       w.step(a);
-      float2 t;
-      if (kNear)
-        t = make_float2(value[min(max(d0, -a.L), a.L) + a.L], value[min(max(d1, -a.L), a.L) + a.L]);
-      else
-        t = make_float2(value[row_of(a, d0)], value[row_of(a, d1)]);
-      if (a.base) t = __fadd2_rn(t, make_float2(__uint_as_float(base[p] << 16), __uint_as_float(base[p] & 0xffff0000u)));
-      const uint32_t o = sm100::pack_bf16x2(t.x, t.y);
-      if (first && second) {
-        *reinterpret_cast<uint32_t *>(a.bias + at) = o;
-      } else {
-        if (first) a.bias[at] = (uint16_t)o;
-        if (second) a.bias[at + 1] = (uint16_t)(o >> 16);
-      }
+      float2 t = make_float2(value_of(d0), value_of(d1));
+      if (a.base) t = __fadd2_rn(t, make_float2(__uint_as_float(in[p] << 16), __uint_as_float(in[p] & 0xffff0000u)));
+      bias[32 * p] = sm100::pack_bf16x2(t.x, t.y);
     }
   }
 }
 
 // part[bh][piece][row]: a CTA's sums.
-template <bool kNear>
+template <bool kNear, bool kPos>
 __global__ void __launch_bounds__(kBwdThreads) relpos_bwd_kernel(const __grid_constant__ RelArgs a) {
   extern __shared__ float sums[];  // [warp][row][33], then (kNear) the rows by distance, one byte each
   constexpr int W = kBwdThreads / 32;
@@ -179,30 +166,35 @@ __global__ void __launch_bounds__(kBwdThreads) relpos_bwd_kernel(const __grid_co
     for (int x = threadIdx.x; x < 2 * a.L + 1; x += kBwdThreads) row_at[x] = (uint8_t)row_of(a, x - a.L);
   __syncthreads();
   float *mine = sums + warp * a.rows * 33 + lane;
+  auto add = [&](int d, float g) { mine[(kNear ? row_at[min(max(d, -a.L), a.L) + a.L] : row_of(a, d)) * 33] += g; };
   const int64_t plane0 = bh * a.plane;
+  const int k1 = min((blockIdx.x + 1) * a.piece, a.units);
   float behind = 0.f, ahead = 0.f;  // d <= -L, d >= L
-  for (int64_t k = (int64_t)blockIdx.x * a.piece + warp; k < min((int64_t)(blockIdx.x + 1) * a.piece, a.units); k += W) {
-    Walk w(a, plane0, k);
+  for (int k = blockIdx.x * a.piece + warp; k < k1; k += W) {
+    const int u0 = unit_start(plane0, k);
+    if (u0 < 0 || u0 + kUnit > a.plane) {  // a plane's ends, value by value
+      for (int e = u0 + lane + (u0 + lane < 0 ? 32 : 0); e < min(u0 + kUnit, (int)a.plane); e += 32)
+        add(difference<kPos>(a, b, e), bf16_to_f32(a.dbias[plane0 + e]));
+      continue;
+    }
+    const uint32_t *dbias = reinterpret_cast<const uint32_t *>(a.dbias + plane0 + u0 + 2 * lane);
     uint32_t g[kPairs];
 #pragma unroll
-    for (int p = 0; p < kPairs; ++p) {
-      const int64_t e = w.e + 64 * p;
-      g[p] = load_pair(a.dbias, plane0 + e, e >= 0 && e < a.plane, e + 1 < a.plane);
-    }
+    for (int p = 0; p < kPairs; ++p) g[p] = __ldcs(dbias + 32 * p);
+    Walk<kPos> w(a, b, u0 + 2 * lane);
 #pragma unroll
     for (int p = 0; p < kPairs; ++p) {
-      bool first, second;
       int d0, d1;
-      w.pair(a, b, first, second, d0, d1);
+      w.pair(a, d0, d1);
       w.step(a);
       const float g0 = __uint_as_float(g[p] << 16), g1 = __uint_as_float(g[p] & 0xffff0000u);
-      if (min(d0, d1) >= a.L) {  // (what is outside the plane is 0)
+      if (min(d0, d1) >= a.L) {
         ahead += g0 + g1;
       } else if (max(d0, d1) <= -a.L) {
         behind += g0 + g1;
       } else {
-        if (first) mine[(kNear ? row_at[min(max(d0, -a.L), a.L) + a.L] : row_of(a, d0)) * 33] += g0;
-        if (second) mine[(kNear ? row_at[min(max(d1, -a.L), a.L) + a.L] : row_of(a, d1)) * 33] += g1;
+        add(d0, g0);
+        add(d1, g1);
       }
     }
   }
@@ -238,7 +230,7 @@ __global__ void __launch_bounds__(256) relpos_reduce_kernel(const float *__restr
 
 int relpos_check(const tri_relpos_shape &s) {
   if (s.B < 1 || s.H < 1 || s.Nq < 1 || s.Nk < 1 || s.K < 1 || (s.two_sided != 0 && s.two_sided != 1)) return TRI_ATTN_ERR_INVALID_ARG;
-  if (s.K > TRI_RELPOS_MAX_K || (int64_t)s.B * s.H > (1 << 20) || (int64_t)s.Nq * s.Nk >= (int64_t{1} << 31)) return TRI_ATTN_ERR_UNSUPPORTED;
+  if (s.K > TRI_RELPOS_MAX_K || (int64_t)s.B * s.H > (1 << 20) || (int64_t)s.Nq * s.Nk > TRI_RELPOS_MAX_PLANE) return TRI_ATTN_ERR_UNSUPPORTED;
   return TRI_ATTN_OK;
 }
 int starts_check(const tri_relpos_shape &s, const int32_t *starts) {
@@ -250,7 +242,7 @@ int starts_check(const tri_relpos_shape &s, const int32_t *starts) {
 
 // A plane's pieces: about as many CTAs over all planes as are given, each of at least two units a warp.
 void cut(RelArgs &a, int warps, int ctas) {
-  a.units = (a.plane + 1 + 511) / 512;
+  a.units = (int)((a.plane + 1 + kUnit - 1) / kUnit);
   const int64_t planes = (int64_t)a.B * a.H, want = std::max<int64_t>(1, ctas / planes);
   const int64_t piece = std::max<int64_t>((a.units + want - 1) / want, 2 * warps);
   a.piece = (int)((piece + warps - 1) / warps * warps);
@@ -281,16 +273,18 @@ dim3 grid_of(const RelArgs &a) {
   return dim3(a.pieces, y, (planes + y - 1) / y);
 }
 
-// More than 48 KB of shared memory: once per device and kernel.
-template <bool kNear>
-cudaError_t bwd_ready() {
-  static DeviceOnce ready;
+template <bool kNear, bool kPos>
+cudaError_t launch_relpos_bwd(const RelArgs &a, size_t smem, cudaStream_t st) {
+  static DeviceOnce ready;  // (more than 48 KB of shared memory)
   int dev = 0;
   cudaError_t e = current_device(&dev);
-  if (e != cudaSuccess || ready.done(dev)) return e;
-  e = cudaFuncSetAttribute(relpos_bwd_kernel<kNear>, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
-  if (e == cudaSuccess) ready.mark(dev);
-  return e;
+  if (e == cudaSuccess && !ready.done(dev)) {
+    e = cudaFuncSetAttribute(relpos_bwd_kernel<kNear, kPos>, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+    if (e == cudaSuccess) ready.mark(dev);
+  }
+  if (e != cudaSuccess) return e;
+  relpos_bwd_kernel<kNear, kPos><<<grid_of(a), kBwdThreads, smem, st>>>(a);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -317,10 +311,16 @@ int tri_relpos_fwd(tri_relpos_shape shape, const int32_t *starts, const float *t
   a.base = reinterpret_cast<const uint16_t *>(base);
   a.bias = reinterpret_cast<uint16_t *>(bias);
   const auto st = static_cast<cudaStream_t>(stream);
-  if (a.L <= kLookup)
-    relpos_fwd_kernel<true><<<grid_of(a), kFwdThreads, sizeof(float) * (2 * a.L + 1), st>>>(a);
+  const bool near = a.L <= kLookup;
+  const size_t smem = sizeof(float) * (near ? 2 * a.L + 1 : a.rows);
+  if (near && positions)
+    relpos_fwd_kernel<true, true><<<grid_of(a), kFwdThreads, smem, st>>>(a);
+  else if (near)
+    relpos_fwd_kernel<true, false><<<grid_of(a), kFwdThreads, smem, st>>>(a);
+  else if (positions)
+    relpos_fwd_kernel<false, true><<<grid_of(a), kFwdThreads, smem, st>>>(a);
   else
-    relpos_fwd_kernel<false><<<grid_of(a), kFwdThreads, sizeof(float) * a.rows, st>>>(a);
+    relpos_fwd_kernel<false, false><<<grid_of(a), kFwdThreads, smem, st>>>(a);
   return cudaGetLastError() == cudaSuccess ? TRI_ATTN_OK : TRI_ATTN_ERR_CUDA;
 }
 
@@ -348,14 +348,12 @@ int tri_relpos_bwd(tri_relpos_shape shape, const int32_t *starts, const int32_t 
   a.dbias = reinterpret_cast<const uint16_t *>(dbias);
   a.part = static_cast<float *>(workspace);
   const bool near = a.L <= kLookup;
-  if ((near ? bwd_ready<true>() : bwd_ready<false>()) != cudaSuccess) return TRI_ATTN_ERR_CUDA;
   const size_t smem = sizeof(float) * (kBwdThreads / 32) * a.rows * 33 + (near ? 2 * a.L + 1 : 0);
   const auto st = static_cast<cudaStream_t>(stream);
-  if (near)
-    relpos_bwd_kernel<true><<<grid_of(a), kBwdThreads, smem, st>>>(a);
-  else
-    relpos_bwd_kernel<false><<<grid_of(a), kBwdThreads, smem, st>>>(a);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = near && positions ? launch_relpos_bwd<true, true>(a, smem, st)
+                  : near            ? launch_relpos_bwd<true, false>(a, smem, st)
+                  : positions       ? launch_relpos_bwd<false, true>(a, smem, st)
+                                    : launch_relpos_bwd<false, false>(a, smem, st);
   if (e == cudaSuccess)
     e = launch_after(relpos_reduce_kernel, dim3((a.rows * a.H + 7) / 8), dim3(256), 0, st, a.part, a.B, a.H, a.pieces, a.rows, dtable);
   return e == cudaSuccess ? TRI_ATTN_OK : TRI_ATTN_ERR_CUDA;
