@@ -727,6 +727,10 @@ inline cudaError_t device_and_pairs(int *dev, int *pairs) {
   return e;
 }
 
+// The forward of few channels in one kernel (ffn_block.cu; C <= 256; ka, ku: both or neither).
+cudaError_t launch_block(const tri_ffn_shape &s, const void *x, const void *Wg, const void *Wu, const void *Wd, void *out, void *ka,
+                         void *ku, int *status, int dev, int pairs, cudaStream_t st);
+
 inline int64_t aligned256(int64_t n) { return (n + 255) / 256 * 256; }
 
 inline int check_shape(const tri_ffn_shape &s) {

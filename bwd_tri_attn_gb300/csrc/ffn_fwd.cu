@@ -18,6 +18,8 @@ FwdWorkspace fwd_workspace(const tri_ffn_shape &s) {
   return w;
 }
 
+bool block_pays(const tri_ffn_shape &s, int pairs) { return s.C <= 256 && ceil_div(s.M, kRows) >= pairs; }
+
 cudaError_t launch_fwd(const tri_ffn_shape &s, const void *x, const void *Wg, const void *Wu, const void *Wd, void *out, void *a,
                        void *u, char *ws, int *status, cudaStream_t st) {
   const FwdWorkspace w = fwd_workspace(s);
@@ -51,6 +53,7 @@ cudaError_t launch_fwd(const tri_ffn_shape &s, const void *x, const void *Wg, co
   AnyProduct<kOut> down;
   e = down.plan(io2, &mh, 1, &md, 1, pairs, dev);
   if (e != cudaSuccess) return e;
+  if (block_pays(s, pairs)) return launch_block(s, x, Wg, Wu, Wd, out, a, u, status, dev, pairs, st);
   e = hidden.launch(st);
   return e == cudaSuccess ? down.launch(st) : e;
 }

@@ -46,6 +46,22 @@ __device__ __forceinline__ void pair_mma_x4_e(uint32_t d_tmem, uint64_t a_desc, 
       : "memory");
 }
 
+// Four MMAs with A from TMEM (its 16-channel steps at a_tmem + 0, 8, A2 and A3 columns, in both CTAs' rows) and B from
+// shared memory (K-major, 32 bytes a step).
+template <int A2, int A3>
+__device__ __forceinline__ void pair_mma_ts_x4_e(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, t, e;\n\t.reg .b32 a;\n\t.reg .b64 b;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+      "add.u32 a, %1, 8;\n\tadd.u64 b, %2, 2;\n\t@e tcgen05.mma.cta_group::2.kind::f16 [%0], [a], b, %3, t;\n\t"
+      "add.u32 a, %1, %5;\n\tadd.u64 b, %2, 4;\n\t@e tcgen05.mma.cta_group::2.kind::f16 [%0], [a], b, %3, t;\n\t"
+      "add.u32 a, %1, %6;\n\tadd.u64 b, %2, 6;\n\t@e tcgen05.mma.cta_group::2.kind::f16 [%0], [a], b, %3, t;\n\t"
+      "}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "n"(A2), "n"(A3)
+      : "memory");
+}
+
 // Arrives once on the mbarrier at this offset in both CTAs when every MMA issued so far by this thread is done.
 __device__ __forceinline__ void pair_commit_e(uint32_t bar) {
   asm volatile(
