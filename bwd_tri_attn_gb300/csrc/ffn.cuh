@@ -40,12 +40,11 @@ struct Cfg {
   static constexpr bool AMN = OP == kDW, BMN = OP == kDHidden || OP == kDx || OP == kDW;
   static constexpr int COLS = OP == kHidden ? BN / 2 : BN;  // columns of the result in a tile
   static constexpr int A_BYTES = kHalf * 128, B_BYTES = BN / 2 * 128, STAGE = A_BYTES + B_BYTES;
-  static constexpr int NST = OP == kDHidden ? (BN == 128 ? 6 : 5) : BN == 128 ? 8 : 6;
+  static constexpr int NST = OP == kDHidden ? (BN == 128 ? 7 : 5) : BN == 128 ? 8 : 6;
   static constexpr int EPI_WARPS = 8, NTHREADS = 32 * (4 + EPI_WARPS);
-  // 32 x 32 pieces of the results on their way out, a ring for each of these warps (FP32 pieces take two places)
-  static constexpr int PIECE = 32 * 64, RING = OP == kDHidden ? 4 : 2;
+  static constexpr int PIECE = 32 * 64, PIECES = OP == kDHidden ? 3 : OP == kDW ? 2 : 1;  // of a warp (FP32: one of twice the size)
   static constexpr int B_FULL = 0, B_EMPTY = NST, B_ACCF = 2 * NST, B_ACCE = B_ACCF + 2, B_DONE = B_ACCE + 2, NBAR = B_DONE + 1;
-  static constexpr int OFF_EPI = NST * STAGE, OFF_BAR = OFF_EPI + EPI_WARPS * RING * PIECE, OFF_MISC = OFF_BAR + 8 * NBAR, SMEM = OFF_MISC + 16, SMEM_ALLOC = SMEM + 1024;
+  static constexpr int OFF_EPI = NST * STAGE, OFF_BAR = OFF_EPI + EPI_WARPS * PIECES * PIECE, OFF_MISC = OFF_BAR + 8 * NBAR, SMEM = OFF_MISC + 16, SMEM_ALLOC = SMEM + 1024;
   static_assert(SMEM_ALLOC <= 227 * 1024, "shared memory");
 };
 
@@ -54,7 +53,7 @@ struct Args {
   int mt[2], nt[2];      // tiles
   int nk, nk0;           // 64-channel blocks; those of the first of kDx's two projections
   int full, tail, pairs; // tiles of whole waves, the others, and the pairs that share those (0: nobody does)
-  int act, f32, wide;    // TRI_FFN_*; FP32 results (kDW); a and u are read 32 bytes at a time
+  int act, f32;          // TRI_FFN_*; FP32 results (kDW)
   int box;               // rows of a CTA's box of A (not kDW): 128, or fewer where all rows are in the first CTA's
   int64_t units;         // tail * nk
   const uint16_t *a, *u; // kDHidden
@@ -140,9 +139,9 @@ __device__ __forceinline__ void sigmoids(const float2 (&a)[N], float2 (&s)[N]) {
   for (int j = 0; j < N; ++j) {
     const float2 x = __fmul2_rn(a[j], both(-kLog2e));
     d[j] = __fadd2_rn(make_float2(ex2(x.x), ex2(x.y)), both(1.f));
-    const float pq = d[j].x * d[j].y;
+    const float pq = d[j].x * d[j].y, r = reciprocal(pq);
     top = max(top, __float_as_uint(pq));
-    s[j] = __fmul2_rn(both(reciprocal(pq)), make_float2(d[j].y, d[j].x));
+    s[j] = make_float2(r * d[j].y, r * d[j].x);
   }
   if (top > __float_as_uint(0x1p120f)) {
 #pragma unroll
@@ -151,9 +150,9 @@ __device__ __forceinline__ void sigmoids(const float2 (&a)[N], float2 (&s)[N]) {
 }
 
 // f = act(a) and, where asked, its derivative.
-template <bool kSlope, int N>
-__device__ __forceinline__ void activation(int act, const float2 (&a)[N], float2 (&f)[N], float2 (&df)[N]) {
-  if (act == TRI_FFN_GELU) {
+template <int ACT, bool kSlope, int N>
+__device__ __forceinline__ void activation(const float2 (&a)[N], float2 (&f)[N], float2 (&df)[N]) {
+  if constexpr (ACT == TRI_FFN_GELU) {
     // Phi(-|a|) = (c1 t + ... + c5 t^5) exp(-a^2 / 2) with t = 1 / (1 + p |a|): Hastings' approximation of the error function
     // (Abramowitz and Stegun 7.1.26, off by at most 1.5e-7), halved and at a / sqrt(2); the slope takes the same exponential.
 #pragma unroll
@@ -170,21 +169,35 @@ __device__ __forceinline__ void activation(int act, const float2 (&a)[N], float2
       f[j] = __fmul2_rn(a[j], phi);
       if constexpr (kSlope) df[j] = __ffma2_rn(__fmul2_rn(a[j], both(0.39894228f)), e, phi);
     }
-    return;
-  }
-  float2 s[N];
-  sigmoids(a, s);
+  } else {
+    float2 s[N];
+    sigmoids(a, s);
 #pragma unroll
-  for (int j = 0; j < N; ++j) {
-    const float2 rest = __ffma2_rn(s[j], both(-1.f), both(1.f));
-    if (act == TRI_FFN_SILU) {
-      f[j] = __fmul2_rn(a[j], s[j]);
-      if constexpr (kSlope) df[j] = __fmul2_rn(s[j], __ffma2_rn(a[j], rest, both(1.f)));
-    } else {
-      f[j] = s[j];
-      if constexpr (kSlope) df[j] = __fmul2_rn(s[j], rest);
+    for (int j = 0; j < N; ++j) {
+      if constexpr (ACT == TRI_FFN_SILU) {
+        f[j] = __fmul2_rn(a[j], s[j]);
+        if constexpr (kSlope) df[j] = __fmul2_rn(s[j], __ffma2_rn(a[j], __ffma2_rn(s[j], both(-1.f), both(1.f)), both(1.f)));
+      } else {
+        f[j] = s[j];
+        if constexpr (kSlope) df[j] = __fmul2_rn(s[j], __ffma2_rn(s[j], both(-1.f), both(1.f)));
+      }
     }
   }
+}
+
+// work(Const<ACT>) for the call's activation: the choice is made outside of what loops over values.
+template <int V>
+struct Const {
+  static constexpr int value = V;
+};
+template <typename F>
+__device__ __forceinline__ void for_activation(int act, F &&work) {
+  if (act == TRI_FFN_SILU)
+    work(Const<TRI_FFN_SILU>{});
+  else if (act == TRI_FFN_GELU)
+    work(Const<TRI_FFN_GELU>{});
+  else
+    work(Const<TRI_FFN_SIGMOID>{});
 }
 
 __device__ __forceinline__ float2 unpack2(uint32_t w) { return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)); }
@@ -192,12 +205,12 @@ __device__ __forceinline__ uint32_t pack2(float2 v) { return pack_bf16x2(v.x, v.
 
 // 2 N sums in consecutive columns of a row (kHidden: v of the gate, w of the up projection; kDHidden: ra and ru, the kept a and
 // u there) to the BF16 results there: o[0], and h, a, u of kHidden, da, du, h of kDHidden.
-template <int OP, int N>
-__device__ __forceinline__ void results(int act, const float2 (&v)[N], const float2 (&w)[N], const uint32_t (&ra)[N], const uint32_t (&ru)[N],
+template <int OP, int ACT, int N>
+__device__ __forceinline__ void results(const float2 (&v)[N], const float2 (&w)[N], const uint32_t (&ra)[N], const uint32_t (&ru)[N],
                                         uint32_t (&o0)[N], uint32_t (&o1)[N], uint32_t (&o2)[N]) {
   if constexpr (OP == kHidden) {
     float2 f[N], none[N];
-    activation<false>(act, v, f, none);
+    activation<ACT, false>(v, f, none);
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       o0[j] = pack2(__fmul2_rn(f[j], w[j]));
@@ -208,7 +221,7 @@ __device__ __forceinline__ void results(int act, const float2 (&v)[N], const flo
     float2 g[N], f[N], df[N];
 #pragma unroll
     for (int j = 0; j < N; ++j) g[j] = unpack2(ra[j]);
-    activation<true>(act, g, f, df);
+    activation<ACT, true>(g, f, df);
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       const float2 up = unpack2(ru[j]);
@@ -222,88 +235,87 @@ __device__ __forceinline__ void results(int act, const float2 (&v)[N], const flo
   }
 }
 
-__device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, uint32_t src, int c0, int c1) {
-  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(reinterpret_cast<uint64_t>(map)),
-               "r"(src), "r"(c0), "r"(c1)
-               : "memory");
+// h of 2 N features of a row, from the sums of the gate and of the up projection, packed.
+template <int ACT, int N>
+__device__ __forceinline__ void hidden(const uint32_t *v, const uint32_t *w, uint32_t *o) {
+  float2 f[N], g[N];
+  uint32_t o0[N], none[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    f[j] = make_float2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+    g[j] = make_float2(__uint_as_float(w[2 * j]), __uint_as_float(w[2 * j + 1]));
+  }
+  results<kHidden, ACT>(f, g, o0, o0, o0, none, none);
+#pragma unroll
+  for (int j = 0; j < N; ++j) o[j] = o0[j];
 }
+// 8 packed values of 16 sums.
+__device__ __forceinline__ void pack16(const uint32_t *v, uint32_t *o) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) o[j] = pack_bf16x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+}
+
 __device__ __forceinline__ void st_shared_v4(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
 
-// A warp's ring of pieces in shared memory: 32 columns of 32 rows (row = lane), in the store map's swizzle.
-template <int RING, int BYTES>
-struct Pieces {
-  uint32_t base;
-  int next, used;
-  __device__ __forceinline__ uint32_t begin() {
-    if (used >= RING) {  // the store that used the place before has read it
-      if ((threadIdx.x & 31) == 0) bulk_wait_group_read<RING - 1>();
-      __syncwarp();
-    } else {
-      ++used;
-    }
-    const uint32_t at = base + next * BYTES;
-    next = next + 1 == RING ? 0 : next + 1;
-    return at;
+// A warp's piece of 32 rows of PARTS x 16 bytes on its way between the threads' rows and memory's: in shared memory part c of
+// row r lies at c ^ (r PARTS / 8 mod PARTS) of the row's place, which keeps both directions free of bank conflicts. (By
+// TMA a row of 64 bytes took ten cycles: 147456 x 512 features 87 us.)
+template <int PARTS>
+struct Piece {
+  static_assert(PARTS == 2 || PARTS == 4 || PARTS == 8, "parts");
+  static constexpr int ROWS = 32 / PARTS, BYTES = 16 * PARTS;  // rows of an access by the warp, bytes of a row
+  static __device__ __forceinline__ uint32_t place(uint32_t at, int r, int c) {
+    return at + r * BYTES + ((c ^ (r / (8 / PARTS) % PARTS)) << 4);
   }
-  __device__ __forceinline__ void send(const CUtensorMap *map, uint32_t at, int col, int row) {
-    fence_proxy_async_smem();  // the generic-proxy writes before the async-proxy read
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) {
-      tma_store_2d(map, at, col, row);
-      bulk_commit_group();
-    }
+  // The thread's own row.
+  static __device__ __forceinline__ void put(uint32_t at, int c, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    st_shared_v4(place(at, threadIdx.x & 31, c), x, y, z, w);
   }
-  // `n` pieces at once: places that the pieces sent before the last one have left (RING > n)
-  template <int n>
-  __device__ __forceinline__ void begin(uint32_t (&at)[n]) {
-    static_assert(RING == n + 1, "places");
-    if (used) {
-      if ((threadIdx.x & 31) == 0) bulk_wait_group_read<1>();
-      __syncwarp();
-    }
-    used = 1;
+  static __device__ __forceinline__ uint4 get(uint32_t at, int c) { return ld_shared_v4(place(at, threadIdx.x & 31, c)); }
+  // The whole piece to or from memory: `p` its first value (16-byte aligned), `pitch` bytes between rows, rows and parts of a row
+  // that are inside. (Between the two views __syncwarp().)
+  static __device__ __forceinline__ void store(uint32_t at, void *p, int64_t pitch, int rows, int parts) {
+    const int lane = threadIdx.x & 31, c = lane % PARTS;
+    uint4 v[PARTS];
 #pragma unroll
-    for (int k = 0; k < n; ++k) {
-      at[k] = base + next * BYTES;
-      next = next + 1 == RING ? 0 : next + 1;
+    for (int i = 0; i < PARTS; ++i) v[i] = ld_shared_v4(place(at, lane / PARTS + ROWS * i, c));
+#pragma unroll
+    for (int i = 0; i < PARTS; ++i) {
+      const int r = lane / PARTS + ROWS * i;
+      if (r < rows && c < parts) *reinterpret_cast<uint4 *>(static_cast<char *>(p) + r * pitch + 16 * c) = v[i];
     }
   }
-  // 16-bit values: rows of 64 bytes, 16-byte part c at c ^ ((row / 2) mod 4)
-  __device__ __forceinline__ void put(const CUtensorMap *map, const uint32_t (&w)[16], int col, int row) {
-    const uint32_t at = begin(), lane = threadIdx.x & 31;
+  static __device__ __forceinline__ void load(uint4 (&v)[PARTS], const void *p, int64_t pitch, int rows, int parts) {
+    const int lane = threadIdx.x & 31, c = lane % PARTS;
 #pragma unroll
-    for (uint32_t c = 0; c < 4; ++c)
-      st_shared_v4(at + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4), w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
-    send(map, at, col, row);
+    for (int i = 0; i < PARTS; ++i) {
+      const int r = lane / PARTS + ROWS * i;
+      v[i] = r < rows && c < parts ? ld_stream(reinterpret_cast<const uint4 *>(static_cast<const char *>(p) + r * pitch + 16 * c))
+                                   : make_uint4(0u, 0u, 0u, 0u);
+    }
   }
-  // FP32 values: rows of 128 bytes, 16-byte part c at c ^ (row mod 8)
-  __device__ __forceinline__ void put(const CUtensorMap *map, const uint32_t (&w)[32], int col, int row) {
-    const uint32_t at = begin(), lane = threadIdx.x & 31;
+  static __device__ __forceinline__ void keep(uint32_t at, const uint4 (&v)[PARTS]) {
+    const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (uint32_t c = 0; c < 8; ++c)
-      st_shared_v4(at + lane * 128 + ((c ^ (lane & 7)) << 4), w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
-    send(map, at, col, row);
+    for (int i = 0; i < PARTS; ++i) st_shared_v4(place(at, lane / PARTS + ROWS * i, lane % PARTS), v[i].x, v[i].y, v[i].z, v[i].w);
   }
 };
 
-// 32 BF16 values of a row from column `col` on (zeros past the last column; the row is inside).
-__device__ __forceinline__ void load_row32(const uint16_t *p, int col, int cols, int wide, uint32_t (&w)[16]) {
-  if (wide && col + 32 <= cols) {
+// 2 N packed values of each row of a warp to memory.
+template <int N>
+__device__ __forceinline__ void store_rows(uint32_t at, const uint32_t (&w)[N], uint16_t *p, int64_t cols, int rows, int parts) {
+  __syncwarp();  // (the piece before has left)
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-      asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                   : "=r"(w[8 * j]), "=r"(w[8 * j + 1]), "=r"(w[8 * j + 2]), "=r"(w[8 * j + 3]), "=r"(w[8 * j + 4]), "=r"(w[8 * j + 5]),
-                     "=r"(w[8 * j + 6]), "=r"(w[8 * j + 7])
-                   : "l"(p + col + 16 * j));
-    return;
-  }
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint4 v = col + 8 * j < cols ? ld_stream(reinterpret_cast<const uint4 *>(p + col + 8 * j)) : make_uint4(0u, 0u, 0u, 0u);
-    w[4 * j] = v.x, w[4 * j + 1] = v.y, w[4 * j + 2] = v.z, w[4 * j + 3] = v.w;
-  }
+  for (int c = 0; c < N / 4; ++c) Piece<N / 4>::put(at, c, w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+  __syncwarp();
+  Piece<N / 4>::store(at, p, 2 * cols, rows, parts);
 }
 
 // ------------------------------------------------------------------------------------------------ the product
@@ -311,9 +323,7 @@ template <int OP, int BN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<OP, BN>::NTHREADS, 1)
     product_kernel(const __grid_constant__ CUtensorMap mA0, const __grid_constant__ CUtensorMap mA1,
                    const __grid_constant__ CUtensorMap mA2, const __grid_constant__ CUtensorMap mB0,
-                   const __grid_constant__ CUtensorMap mB1, const __grid_constant__ CUtensorMap mB2,
-                   const __grid_constant__ CUtensorMap mO0, const __grid_constant__ CUtensorMap mO1,
-                   const __grid_constant__ CUtensorMap mO2, const Args a) {
+                   const __grid_constant__ CUtensorMap mB1, const __grid_constant__ CUtensorMap mB2, const Args a) {
   using C = Cfg<OP, BN>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -406,7 +416,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<OP, BN>::NTHREAD
     int it = 0, tl = 0;
     while (ok && items.next(a, pair, pairs, tile, k0, k1, slot)) {
       const int acc = tl & 1;
-      if (tl >= 2) ok = __all_sync(0xffffffffu, wait_bar_cluster(bar(C::B_ACCE + acc), ((tl >> 1) - 1) & 1, ab));
+      if (tl >= 2) ok = wait_bar_warp(bar(C::B_ACCE + acc), ((tl >> 1) - 1) & 1, ab);
       if (!ok) break;
       tc_fence_after();
       for (int kb = k0; kb < k1; ++kb, ++it) {
@@ -428,22 +438,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<OP, BN>::NTHREAD
     __syncwarp();
   } else if (warp >= 4) {
     // ------------------------------------------------------------ finished sums, thread = row: half of the columns
-    // (pieces of 32 columns leave by TMA: a thread's own stores, a line for each lane, took four times as long)
     const int q = warp & 3, half = (warp - 4) >> 2, row = 32 * q + lane;
-    const uint32_t lanes = (uint32_t)(32 * q) << 16, ring = sb0 + C::OFF_EPI + (warp - 4) * C::RING * C::PIECE;
-    Pieces<C::RING, C::PIECE> out{ring, 0, 0};
-    Pieces<C::RING / 2, 2 * C::PIECE> out32{ring, 0, 0};
+    const uint32_t lanes = (uint32_t)(32 * q) << 16, st0 = sb0 + C::OFF_EPI + (warp - 4) * C::PIECES * C::PIECE;
     constexpr int CH = C::COLS / 64;  // 32-column chunks of a warp
     int tl = 0;
     while (items.next(a, pair, pairs, tile, k0, k1, slot)) {
       const Tile x = tile_at<OP, BN>(a, tile);
       const int acc = tl & 1, mw = x.m0 + kHalf * rank + 32 * q, m = mw + lane, c0 = half * (C::COLS / 2);
       const bool mine = m < x.rows;
-      uint32_t ra[16], ru[16];
+      const int64_t cols = x.cols, pitch = 2 * cols;
+      uint4 ra[4], ru[4];  // kDHidden: a and u of the next chunk
       auto fetch = [&](int i) {
-        if (mine && slot < 0) {
-          load_row32(a.a + (int64_t)m * x.cols, x.n0 + c0 + 32 * i, x.cols, a.wide, ra);
-          load_row32(a.u + (int64_t)m * x.cols, x.n0 + c0 + 32 * i, x.cols, a.wide, ru);
+        if (slot < 0) {
+          const int64_t off = mw * cols + x.n0 + c0 + 32 * i;
+          const int rows = x.rows - mw, parts = (x.cols - (x.n0 + c0 + 32 * i)) / 8;
+          Piece<4>::load(ra, a.a + off, pitch, rows, parts);
+          Piece<4>::load(ru, a.u + off, pitch, rows, parts);
         }
       };
       if constexpr (OP == kDHidden) fetch(0);
@@ -463,7 +473,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<OP, BN>::NTHREAD
         if (i + 1 == CH) {  // all of it is read: the next but one tile may start there
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(mapa_shared(bar(C::B_ACCE + acc), 0));
+          // (nothing but TMEM goes by this barrier, and the tcgen05 fences order that: a release would wait for the stores)
+          if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(bar(C::B_ACCE + acc), 0));
         }
         if (slot >= 0) {
           if (mine) {
@@ -474,69 +485,65 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<OP, BN>::NTHREAD
             }
           }
         } else if (mw < x.rows && n < x.cols) {  // (the whole warp; rows and columns outside are not stored)
-          const CUtensorMap *mo = OP != kDW || x.prod == 0 ? &mO0 : x.prod == 1 ? &mO1 : &mO2;
+          const int rows = x.rows - mw, parts = (x.cols - n) / 8;
+          const int64_t off = mw * cols + n;
+          auto to = [&](int k) { return static_cast<uint16_t *>(a.o[k]) + off; };
           if constexpr (OP == kDHidden) {
-            uint32_t at[3];
-            out.begin(at);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              float2 f[8];
-              uint32_t ga[8], gu[8], o[3][8];
-#pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                f[j] = make_float2(__uint_as_float(v[16 * h + 2 * j]), __uint_as_float(v[16 * h + 2 * j + 1]));
-                ga[j] = ra[8 * h + j];
-                gu[j] = ru[8 * h + j];
-              }
-              results<OP>(a.act, f, f, ga, gu, o[0], o[1], o[2]);
-#pragma unroll
-              for (int k = 0; k < 3; ++k)
-#pragma unroll
-                for (uint32_t e = 0; e < 2; ++e)
-                  st_shared_v4(at[k] + lane * 64 + (((2 * h + e) ^ ((lane >> 1) & 3)) << 4), o[k][4 * e], o[k][4 * e + 1], o[k][4 * e + 2], o[k][4 * e + 3]);
-            }
+            __syncwarp();  // (the chunk before has left)
+            Piece<4>::keep(st0, ra);
+            Piece<4>::keep(st0 + C::PIECE, ru);
             if (i + 1 < CH) fetch(i + 1);
-            out.send(&mO0, at[0], n, mw);
-            out.send(&mO1, at[1], n, mw);
-            if (a.o[2])
-              out.send(&mO2, at[2], n, mw);
-            else if (lane == 0)
-              bulk_commit_group();  // (an empty one: begin() counts three)
+            __syncwarp();
+            for_activation(a.act, [&](auto which) {
+#pragma unroll
+              for (int h = 0; h < 4; ++h) {  // (a part of the thread's row is read, and written with the results)
+                float2 f[4];
+                uint32_t o[3][4];
+                const uint4 wa = Piece<4>::get(st0, h), wu = Piece<4>::get(st0 + C::PIECE, h);
+                const uint32_t ga[4] = {wa.x, wa.y, wa.z, wa.w}, gu[4] = {wu.x, wu.y, wu.z, wu.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) f[j] = make_float2(__uint_as_float(v[8 * h + 2 * j]), __uint_as_float(v[8 * h + 2 * j + 1]));
+                results<OP, decltype(which)::value>(f, f, ga, gu, o[0], o[1], o[2]);
+#pragma unroll
+                for (int k = 0; k < 3; ++k) Piece<4>::put(st0 + k * C::PIECE, h, o[k][0], o[k][1], o[k][2], o[k][3]);
+              }
+            });
+            __syncwarp();
+            Piece<4>::store(st0, to(0), pitch, rows, parts);
+            Piece<4>::store(st0 + C::PIECE, to(1), pitch, rows, parts);
+            if (a.o[2]) Piece<4>::store(st0 + 2 * C::PIECE, to(2), pitch, rows, parts);
           } else if (OP == kDW && a.f32) {
-            out32.put(mo, v, n, mw);
+            __syncwarp();
+#pragma unroll
+            for (int c = 0; c < 8; ++c) Piece<8>::put(st0, c, v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+            __syncwarp();
+            Piece<8>::store(st0, static_cast<float *>(x.prod == 0 ? a.o[0] : x.prod == 1 ? a.o[1] : a.o[2]) + off, 4 * cols, rows, 2 * parts);
           } else {
             uint32_t o[16];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              float2 f[8], g[8];
-              uint32_t o0[8], none[8];
-#pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                const int k = 16 * h + 2 * j;
-                f[j] = make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1]));
-                if constexpr (OP == kHidden) g[j] = make_float2(__uint_as_float(w[k]), __uint_as_float(w[k + 1]));
-              }
-              results<OP>(a.act, f, g, o0, o0, o0, none, none);
-#pragma unroll
-              for (int j = 0; j < 8; ++j) o[8 * h + j] = o0[j];
+            if constexpr (OP == kHidden) {
+              for_activation(a.act, [&](auto which) {
+                hidden<decltype(which)::value, 8>(v, w, o);
+                hidden<decltype(which)::value, 8>(v + 16, w + 16, o + 8);
+              });
+            } else {
+              pack16(v, o);
+              pack16(v + 16, o + 8);
             }
-            out.put(mo, o, n, mw);
+            store_rows(st0, o, OP != kDW || x.prod == 0 ? to(0) : x.prod == 1 ? to(1) : to(2), cols, rows, parts);
             if (OP == kHidden && a.o[1]) {
-              auto keep = [&](const CUtensorMap *map, const uint32_t (&y)[32]) {
-#pragma unroll
-                for (int j = 0; j < 16; ++j) o[j] = pack_bf16x2(__uint_as_float(y[2 * j]), __uint_as_float(y[2 * j + 1]));
-                out.put(map, o, n, mw);
+              auto keep = [&](int k, const uint32_t (&y)[32]) {
+                pack16(y, o);
+                pack16(y + 16, o + 8);
+                store_rows(st0, o, to(k), cols, rows, parts);
               };
-              keep(&mO1, v);
-              keep(&mO2, w);
+              keep(1, v);
+              keep(2, w);
             }
           }
         }
         __syncwarp();  // (the next chunk is read by the whole warp)
       }
     }
-    if (lane == 0) bulk_wait_group<0>();  // every store has been performed before the CTA exits
-    __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
@@ -588,7 +595,7 @@ __global__ void __launch_bounds__(256) join_kernel(const Args a) {
     return;
   }
   uint32_t o0[4], o1[4], o2[4];
-  results<OP>(a.act, v, w, ra, ru, o0, o1, o2);
+  for_activation(a.act, [&](auto which) { results<OP, decltype(which)::value>(v, w, ra, ru, o0, o1, o2); });
   auto put = [&](void *to, const uint32_t (&y)[4]) {
     *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(to) + off) = make_uint4(y[0], y[1], y[2], y[3]);
   };
@@ -609,18 +616,6 @@ inline cudaError_t make_matrix_map(CUtensorMap *m, const void *ptr, int64_t inne
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
-// Row-major [rows][cols] without gaps, in pieces of 32 x 32 to be stored: BF16 (64-byte swizzle) or FP32 (128-byte).
-inline cudaError_t make_result_map(CUtensorMap *m, void *ptr, int64_t cols, int64_t rows, bool f32) {
-  auto enc = tensor_map_encoder();
-  if (!enc) return cudaErrorNotSupported;
-  cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)((f32 ? 4 : 2) * cols)};
-  cuuint32_t box[2] = {32, 32}, es[2] = {1, 1};
-  CUresult r = enc(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, ptr, dims, strides, box, es,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                   CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
 inline int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
 // How many pairs share the tiles that fill no whole wave (0: each goes to one pair), and the time of it all, in units of a
@@ -652,7 +647,7 @@ struct Matrix {
 // One product in tiles of BN columns.
 template <int OP, int BN>
 struct Product {
-  CUtensorMap mA[3], mB[3], mO[3];
+  CUtensorMap mA[3], mB[3];
   Args a;
   int grid;
   static int tiles(const Args &io, int i) { return ceil_div(io.rows[i], kRows) * ceil_div(io.cols[i], Cfg<OP, BN>::COLS); }
@@ -664,14 +659,11 @@ struct Product {
     using C = Cfg<OP, BN>;
     a = io;
     a.box = io.rows[0] < kHalf ? (io.rows[0] + 7) / 8 * 8 : kHalf;
-    a.wide = a.cols[0] % 16 == 0 && ((reinterpret_cast<uintptr_t>(a.a) | reinterpret_cast<uintptr_t>(a.u)) & 31u) == 0;
     cudaError_t e = cudaSuccess;
     for (int i = 0; i < 3 && e == cudaSuccess; ++i) {
       const Matrix &x = A[i < nA ? i : 0], &y = B[i < nB ? i : 0];
       e = make_matrix_map(&mA[i], x.p, x.inner, x.outer, x.pitch, C::AMN ? 64 : a.box);
       if (e == cudaSuccess) e = make_matrix_map(&mB[i], y.p, y.inner, y.outer, y.pitch, C::BMN ? 64 : BN / 2);
-      const int k = a.o[i] ? i : 0, sizes = OP == kDW && k == 2 ? 1 : 0;
-      if (e == cudaSuccess) e = make_result_map(&mO[i], a.o[k], a.cols[sizes], a.rows[sizes], OP == kDW && a.f32);
     }
     if (e != cudaSuccess) return e;
     static DeviceOnce ready;
@@ -695,7 +687,7 @@ struct Product {
   cudaError_t launch(cudaStream_t st) const {
     using C = Cfg<OP, BN>;
     cudaError_t e = launch_after(product_kernel<OP, BN>, dim3(grid), dim3(C::NTHREADS), C::SMEM_ALLOC, st, mA[0], mA[1], mA[2], mB[0],
-                                 mB[1], mB[2], mO[0], mO[1], mO[2], a);
+                                 mB[1], mB[2], a);
     if (e == cudaSuccess && a.pairs) e = launch_after(join_kernel<OP, BN>, dim3(a.tail, 2 * (C::COLS / 16)), dim3(256), 0, st, a);
     return e;
   }
