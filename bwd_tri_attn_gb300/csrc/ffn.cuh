@@ -40,9 +40,11 @@ struct Cfg {
   static constexpr bool AMN = OP == kDW, BMN = OP == kDHidden || OP == kDx || OP == kDW;
   static constexpr int COLS = OP == kHidden ? BN / 2 : BN;  // columns of the result in a tile
   static constexpr int A_BYTES = kHalf * 128, B_BYTES = BN / 2 * 128, STAGE = A_BYTES + B_BYTES;
-  static constexpr int NST = OP == kDHidden ? (BN == 128 ? 7 : 5) : BN == 128 ? 8 : 6;
-  static constexpr int EPI_WARPS = 8, NTHREADS = 32 * (4 + EPI_WARPS);
-  static constexpr int PIECE = 32 * 64, PIECES = OP == kDHidden ? 3 : OP == kDW ? 2 : 1;  // of a warp (FP32: one of twice the size)
+  static constexpr int NST = OP == kDHidden ? (BN == 128 ? 5 : 4) : BN == 128 ? 8 : 6;
+  // Warps that take the sums, half of the columns each, and the columns that they write at a time: 64, whole lines of memory
+  // (the features' gradients of 8192 x 2048 x 8192, five tensors: 16 columns 336 us, 32 220, 64 the figure at ffn_bwd.cu).
+  static constexpr int EPI_WARPS = 8, NTHREADS = 32 * (4 + EPI_WARPS), CW = COLS / 2 < 64 ? COLS / 2 : 64;
+  static constexpr int PIECE = 32 * 128, PIECES = OP == kDHidden ? 3 : 1;  // of a warp
   static constexpr int B_FULL = 0, B_EMPTY = NST, B_ACCF = 2 * NST, B_ACCE = B_ACCF + 2, B_DONE = B_ACCE + 2, NBAR = B_DONE + 1;
   static constexpr int OFF_EPI = NST * STAGE, OFF_BAR = OFF_EPI + EPI_WARPS * PIECES * PIECE, OFF_MISC = OFF_BAR + 8 * NBAR, SMEM = OFF_MISC + 16, SMEM_ALLOC = SMEM + 1024;
   static_assert(SMEM_ALLOC <= 227 * 1024, "shared memory");
@@ -438,22 +440,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<OP, BN>::NTHREAD
     __syncwarp();
   } else if (warp >= 4) {
     // ------------------------------------------------------------ finished sums, thread = row: half of the columns
-    const int q = warp & 3, half = (warp - 4) >> 2, row = 32 * q + lane;
+    constexpr int CW = C::CW, PARTS = CW / 8, CH = C::COLS / 2 / CW;  // columns at a time, their 16-byte parts; a warp's chunks
+    using Rows = Piece<PARTS>;
+    const int q = warp & 3, c0 = ((warp - 4) >> 2) * (C::COLS / 2), row = 32 * q + lane;
     const uint32_t lanes = (uint32_t)(32 * q) << 16, st0 = sb0 + C::OFF_EPI + (warp - 4) * C::PIECES * C::PIECE;
-    constexpr int CH = C::COLS / 64;  // 32-column chunks of a warp
     int tl = 0;
     while (items.next(a, pair, pairs, tile, k0, k1, slot)) {
       const Tile x = tile_at<OP, BN>(a, tile);
-      const int acc = tl & 1, mw = x.m0 + kHalf * rank + 32 * q, m = mw + lane, c0 = half * (C::COLS / 2);
+      const int acc = tl & 1, mw = x.m0 + kHalf * rank + 32 * q, m = mw + lane;
       const bool mine = m < x.rows;
       const int64_t cols = x.cols, pitch = 2 * cols;
-      uint4 ra[4], ru[4];  // kDHidden: a and u of the next chunk
+      uint4 ra[PARTS], ru[PARTS];  // kDHidden: a and u of the next chunk
       auto fetch = [&](int i) {
         if (slot < 0) {
-          const int64_t off = mw * cols + x.n0 + c0 + 32 * i;
-          const int rows = x.rows - mw, parts = (x.cols - (x.n0 + c0 + 32 * i)) / 8;
-          Piece<4>::load(ra, a.a + off, pitch, rows, parts);
-          Piece<4>::load(ru, a.u + off, pitch, rows, parts);
+          const int64_t off = mw * cols + x.n0 + c0 + CW * i;
+          const int rows = x.rows - mw, parts = (x.cols - (x.n0 + c0 + CW * i)) / 8;
+          Rows::load(ra, a.a + off, pitch, rows, parts);
+          Rows::load(ru, a.u + off, pitch, rows, parts);
         }
       };
       if constexpr (OP == kDHidden) fetch(0);
@@ -464,60 +467,64 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<OP, BN>::NTHREAD
       float *part = a.part + ((int64_t)max(slot, 0) * 2 + rank) * BN * kHalf + row;
 #pragma unroll 1
       for (int i = 0; i < CH; ++i) {
-        const int c = c0 + 32 * i, n = x.n0 + c;
-        uint32_t v[32], w[32];
-        tmem_ld32(tacc + c, v);
-        if constexpr (OP == kHidden) tmem_ld32(tacc + BN / 2 + c, w);
-        tmem_wait_ld(v);
-        if constexpr (OP == kHidden) tmem_wait_ld(w);
-        if (i + 1 == CH) {  // all of it is read: the next but one tile may start there
-          tc_fence_before();
-          __syncwarp();
-          // (nothing but TMEM goes by this barrier, and the tcgen05 fences order that: a release would wait for the stores)
-          if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(bar(C::B_ACCE + acc), 0));
-        }
-        if (slot >= 0) {
-          if (mine) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              part[(c + j) * kHalf] = __uint_as_float(v[j]);
-              if constexpr (OP == kHidden) part[(BN / 2 + c + j) * kHalf] = __uint_as_float(w[j]);
-            }
+        const int n = x.n0 + c0 + CW * i, rows = x.rows - mw, parts = (x.cols - n) / 8;
+        const int64_t off = mw * cols + n;
+        const bool inside = slot < 0 && rows > 0 && parts > 0;  // (of the whole warp; what is outside of the result is not stored)
+        auto to = [&](int k) { return static_cast<uint16_t *>(a.o[k]) + off; };
+        __syncwarp();  // (the chunk before has left)
+        if constexpr (OP == kDHidden) {
+          if (inside) {
+            Rows::keep(st0, ra);
+            Rows::keep(st0 + C::PIECE, ru);
           }
-        } else if (mw < x.rows && n < x.cols) {  // (the whole warp; rows and columns outside are not stored)
-          const int rows = x.rows - mw, parts = (x.cols - n) / 8;
-          const int64_t off = mw * cols + n;
-          auto to = [&](int k) { return static_cast<uint16_t *>(a.o[k]) + off; };
-          if constexpr (OP == kDHidden) {
-            __syncwarp();  // (the chunk before has left)
-            Piece<4>::keep(st0, ra);
-            Piece<4>::keep(st0 + C::PIECE, ru);
-            if (i + 1 < CH) fetch(i + 1);
+          if (i + 1 < CH) fetch(i + 1);
+          __syncwarp();
+        }
+#pragma unroll
+        for (int s = 0; s < CW / 32; ++s) {
+          const int c = c0 + CW * i + 32 * s;
+          uint32_t v[32], w[32];
+          tmem_ld32(tacc + c, v);
+          if constexpr (OP == kHidden) tmem_ld32(tacc + BN / 2 + c, w);
+          tmem_wait_ld(v);
+          if constexpr (OP == kHidden) tmem_wait_ld(w);
+          if (i + 1 == CH && s + 1 == CW / 32) {  // all of it is read: the next but one tile may start there
+            tc_fence_before();
             __syncwarp();
+            // (nothing but TMEM goes by this barrier, and the tcgen05 fences order that: a release would wait for the stores)
+            if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(bar(C::B_ACCE + acc), 0));
+          }
+          if (slot >= 0) {
+            if (mine) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) {
+                part[(c + j) * kHalf] = __uint_as_float(v[j]);
+                if constexpr (OP == kHidden) part[(BN / 2 + c + j) * kHalf] = __uint_as_float(w[j]);
+              }
+            }
+          } else if (!inside) {
+          } else if constexpr (OP == kDHidden) {
             for_activation(a.act, [&](auto which) {
 #pragma unroll
               for (int h = 0; h < 4; ++h) {  // (a part of the thread's row is read, and written with the results)
                 float2 f[4];
                 uint32_t o[3][4];
-                const uint4 wa = Piece<4>::get(st0, h), wu = Piece<4>::get(st0 + C::PIECE, h);
+                const uint4 wa = Rows::get(st0, 4 * s + h), wu = Rows::get(st0 + C::PIECE, 4 * s + h);
                 const uint32_t ga[4] = {wa.x, wa.y, wa.z, wa.w}, gu[4] = {wu.x, wu.y, wu.z, wu.w};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) f[j] = make_float2(__uint_as_float(v[8 * h + 2 * j]), __uint_as_float(v[8 * h + 2 * j + 1]));
                 results<OP, decltype(which)::value>(f, f, ga, gu, o[0], o[1], o[2]);
 #pragma unroll
-                for (int k = 0; k < 3; ++k) Piece<4>::put(st0 + k * C::PIECE, h, o[k][0], o[k][1], o[k][2], o[k][3]);
+                for (int k = 0; k < 3; ++k) Rows::put(st0 + k * C::PIECE, 4 * s + h, o[k][0], o[k][1], o[k][2], o[k][3]);
               }
             });
-            __syncwarp();
-            Piece<4>::store(st0, to(0), pitch, rows, parts);
-            Piece<4>::store(st0 + C::PIECE, to(1), pitch, rows, parts);
-            if (a.o[2]) Piece<4>::store(st0 + 2 * C::PIECE, to(2), pitch, rows, parts);
           } else if (OP == kDW && a.f32) {
             __syncwarp();
 #pragma unroll
-            for (int c = 0; c < 8; ++c) Piece<8>::put(st0, c, v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+            for (int k = 0; k < 8; ++k) Piece<8>::put(st0, k, v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
             __syncwarp();
-            Piece<8>::store(st0, static_cast<float *>(x.prod == 0 ? a.o[0] : x.prod == 1 ? a.o[1] : a.o[2]) + off, 4 * cols, rows, 2 * parts);
+            Piece<8>::store(st0, static_cast<float *>(x.prod == 0 ? a.o[0] : x.prod == 1 ? a.o[1] : a.o[2]) + off + 32 * s, 4 * cols, rows,
+                            2 * parts - 8 * s);
           } else {
             uint32_t o[16];
             if constexpr (OP == kHidden) {
@@ -525,20 +532,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<OP, BN>::NTHREAD
                 hidden<decltype(which)::value, 8>(v, w, o);
                 hidden<decltype(which)::value, 8>(v + 16, w + 16, o + 8);
               });
+              if (a.o[1]) {  // (a and u are kept, too: one after another, 32 columns at a time)
+                store_rows(st0, o, to(0) + 32 * s, cols, rows, parts - 4 * s);
+                pack16(v, o);
+                pack16(v + 16, o + 8);
+                store_rows(st0, o, to(1) + 32 * s, cols, rows, parts - 4 * s);
+                pack16(w, o);
+                pack16(w + 16, o + 8);
+                store_rows(st0, o, to(2) + 32 * s, cols, rows, parts - 4 * s);
+                continue;
+              }
             } else {
               pack16(v, o);
               pack16(v + 16, o + 8);
             }
-            store_rows(st0, o, OP != kDW || x.prod == 0 ? to(0) : x.prod == 1 ? to(1) : to(2), cols, rows, parts);
-            if (OP == kHidden && a.o[1]) {
-              auto keep = [&](int k, const uint32_t (&y)[32]) {
-                pack16(y, o);
-                pack16(y + 16, o + 8);
-                store_rows(st0, o, to(k), cols, rows, parts);
-              };
-              keep(1, v);
-              keep(2, w);
-            }
+#pragma unroll
+            for (int h = 0; h < 4; ++h) Rows::put(st0, 4 * s + h, o[4 * h], o[4 * h + 1], o[4 * h + 2], o[4 * h + 3]);
+          }
+        }
+        if (inside && !(OP == kDW && a.f32) && !(OP == kHidden && a.o[1])) {
+          __syncwarp();
+          Rows::store(st0, OP != kDW || x.prod == 0 ? to(0) : x.prod == 1 ? to(1) : to(2), pitch, rows, parts);
+          if constexpr (OP == kDHidden) {
+            Rows::store(st0 + C::PIECE, to(1), pitch, rows, parts);
+            if (a.o[2]) Rows::store(st0 + 2 * C::PIECE, to(2), pitch, rows, parts);
           }
         }
         __syncwarp();  // (the next chunk is read by the whole warp)

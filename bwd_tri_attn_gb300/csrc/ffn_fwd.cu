@@ -18,7 +18,13 @@ FwdWorkspace fwd_workspace(const tri_ffn_shape &s) {
   return w;
 }
 
-bool block_pays(const tri_ffn_shape &s, int pairs) { return s.C <= 256 && ceil_div(s.M, kRows) >= pairs; }
+// Whether one kernel is faster, in us: rounds of 256 rows a pair, 64 features in 0.65 us (up to 128 channels) or 1.13,
+// against two kernels and the features' way through memory. (20480 rows of 64 and 2048 features: 46 and 50 us, 10240 of 256
+// and 1024: 24 and 22, 40960 of 128 and 512: 23 and 29, 2560: 10 and 10, 5120 of 256 and 8192: 149 and 64.)
+bool block_pays(const tri_ffn_shape &s, int pairs) {
+  const double rounds = ceil_div(ceil_div(s.M, kRows), pairs);
+  return s.C <= 256 && 4.3 + rounds * ceil_div(s.F, 64) * (s.C <= 128 ? 0.65 : 1.13) < 8 + 1.1e-6 * (double)s.M * s.F;
+}
 
 cudaError_t launch_fwd(const tri_ffn_shape &s, const void *x, const void *Wg, const void *Wu, const void *Wd, void *out, void *a,
                        void *u, char *ws, int *status, cudaStream_t st) {
