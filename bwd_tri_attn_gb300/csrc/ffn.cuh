@@ -42,7 +42,8 @@ struct Cfg {
   static constexpr int A_BYTES = kHalf * 128, B_BYTES = BN / 2 * 128, STAGE = A_BYTES + B_BYTES;
   static constexpr int NST = OP == kDHidden ? (BN == 128 ? 5 : 4) : BN == 128 ? 8 : 6;
   // Warps that take the sums, half of the columns each, and the columns that they write at a time: 64, whole lines of memory
-  // (the features' gradients of 8192 x 2048 x 8192, five tensors: 16 columns 336 us, 32 220, 64 the figure at ffn_bwd.cu).
+  // (kDHidden of 8192 x 2048 x 8192, five tensors: 16 columns 336 us, 32 or 64 220 to 230; of 4001 x 392 x 1032, whose rows begin
+  // anywhere, 64 columns 19 us, a thread's own 16-byte accesses 25).
   static constexpr int EPI_WARPS = 8, NTHREADS = 32 * (4 + EPI_WARPS), CW = COLS / 2 < 64 ? COLS / 2 : 64;
   static constexpr int PIECE = 32 * 128, PIECES = OP == kDHidden ? 3 : 1;  // of a warp
   static constexpr int B_FULL = 0, B_EMPTY = NST, B_ACCF = 2 * NST, B_ACCE = B_ACCF + 2, B_DONE = B_ACCE + 2, NBAR = B_DONE + 1;
