@@ -1213,32 +1213,45 @@ def _clip_array(grads, out):
     """The gradients' descriptions for the library (as ClipTensor's fields one behind another), their number and the
     device's index: every tensor checked, no output twice."""
     device = torch.cuda.current_device()
-    codes, rows, written = _NORM_DTYPES, [], set()
-    for i, g in enumerate(grads):
-        try:
-            code, at = codes[g.dtype], g.get_device()
-        except (AttributeError, KeyError):
-            _norm_dtype(g, f"gradient {i}")  # (names what is wrong)
-            raise
-        if at != device:
-            raise ValueError(f"gradient {i} must be a CUDA tensor on the current device, got {g.device}")
-        if not g.is_contiguous():
-            raise ValueError(f"gradient {i} must be contiguous")
-        n, p = g.numel(), g.data_ptr()
-        o = p
+    try:
+        types = [g.dtype for g in grads]
+        codes = [_NORM_DTYPES[t] for t in types]
+        sizes = [g.numel() for g in grads]
+        at = [g.data_ptr() for g in grads]
+        fine = all([g.get_device() == device for g in grads]) and all([g.is_contiguous() for g in grads])
+        to = at
         if out is not None:
-            t = out[i]
-            if not isinstance(t, torch.Tensor) or t.dtype != g.dtype or t.shape != g.shape:
-                raise ValueError(f"out {i} must be a tensor of gradient {i}'s shape and type")
-            if t.get_device() != device or not t.is_contiguous():
-                raise ValueError(f"out {i} must be contiguous and on the current device")
-            o = t.data_ptr()
-        if n:
-            rows += (p, o, n, code)
-            written.add(o)
-    if 4 * len(written) != len(rows):
+            to = [t.data_ptr() for t in out]
+            fine = (fine and [t.dtype for t in out] == types and [t.numel() for t in out] == sizes
+                    and all([t.get_device() == device for t in out]) and all([t.is_contiguous() for t in out]))
+    except (AttributeError, KeyError):
+        fine = False
+    if not fine:
+        _clip_refusal(device, grads, out)
+    if 0 in sizes:
+        some = [i for i, n in enumerate(sizes) if n]
+        codes, sizes, at, to = ([v[i] for i in some] for v in (codes, sizes, at, to))
+    n = len(at)
+    if len(set(to)) != n:
         raise ValueError("a tensor stands twice among the gradients that are written")
-    return array.array("q", rows), len(written), device
+    rows = array.array("q", bytes(32 * n))
+    for k, v in enumerate((at, to, sizes, codes)):
+        rows[k::4] = array.array("q", v)
+    return rows, n, device
+
+
+def _clip_refusal(device, grads, out):
+    """Names what is wrong with one of the tensors."""
+    for i, g in enumerate(grads):
+        _norm_dtype(g, f"gradient {i}")
+        for t, name in ((g, f"gradient {i}"), *(() if out is None else ((out[i], f"out {i}"),))):
+            if not isinstance(t, torch.Tensor) or t.dtype != g.dtype or t.numel() != g.numel():
+                raise ValueError(f"{name} must be a tensor of gradient {i}'s size and type")
+            if not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+            if t.get_device() != device:
+                raise ValueError(f"{name} must be a CUDA tensor on the current device, got {t.device}")
+    raise ValueError("the gradients' tensors do not fit together")
 
 
 def _clip(call, grads, out, workspace, *more):

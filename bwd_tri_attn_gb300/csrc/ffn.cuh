@@ -679,9 +679,14 @@ struct Product {
     a.box = io.rows[0] < kHalf ? (io.rows[0] + 7) / 8 * 8 : kHalf;
     cudaError_t e = cudaSuccess;
     for (int i = 0; i < 3 && e == cudaSuccess; ++i) {
-      const Matrix &x = A[i < nA ? i : 0], &y = B[i < nB ? i : 0];
-      e = make_matrix_map(&mA[i], x.p, x.inner, x.outer, x.pitch, C::AMN ? 64 : a.box);
-      if (e == cudaSuccess) e = make_matrix_map(&mB[i], y.p, y.inner, y.outer, y.pitch, C::BMN ? 64 : BN / 2);
+      if (i < nA)
+        e = make_matrix_map(&mA[i], A[i].p, A[i].inner, A[i].outer, A[i].pitch, C::AMN ? 64 : a.box);
+      else
+        mA[i] = mA[0];
+      if (i >= nB)
+        mB[i] = mB[0];
+      else if (e == cudaSuccess)
+        e = make_matrix_map(&mB[i], B[i].p, B[i].inner, B[i].outer, B[i].pitch, C::BMN ? 64 : BN / 2);
     }
     if (e != cudaSuccess) return e;
     static DeviceOnce ready;

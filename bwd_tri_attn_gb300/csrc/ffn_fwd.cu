@@ -32,6 +32,7 @@ cudaError_t launch_fwd(const tri_ffn_shape &s, const void *x, const void *Wg, co
   int dev = 0, pairs = 0;
   cudaError_t e = device_and_pairs(&dev, &pairs);
   if (e != cudaSuccess) return e;
+  if (block_pays(s, pairs)) return launch_block(s, x, Wg, Wu, Wd, out, a, u, status, dev, pairs, st);
   float *part = reinterpret_cast<float *>(ws + w.part);
   const int64_t C = s.C, F = s.F, ldx = s.ldx ? s.ldx : C;
   Args io{};
@@ -59,7 +60,6 @@ cudaError_t launch_fwd(const tri_ffn_shape &s, const void *x, const void *Wg, co
   AnyProduct<kOut> down;
   e = down.plan(io2, &mh, 1, &md, 1, pairs, dev);
   if (e != cudaSuccess) return e;
-  if (block_pays(s, pairs)) return launch_block(s, x, Wg, Wu, Wd, out, a, u, status, dev, pairs, st);
   e = hidden.launch(st);
   return e == cudaSuccess ? down.launch(st) : e;
 }
