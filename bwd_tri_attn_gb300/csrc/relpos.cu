@@ -30,7 +30,8 @@ struct RelArgs {
   int units;      // of 512 values, of a plane
   int piece;      // units of a CTA
   int pieces;     // CTAs of a plane
-  int step_i, step_j;  // 64 values further on: rows and columns
+  uint32_t nk4, step_j4;  // four times Nk; 64 values further on: four times the columns,
+  int step_i, step_d;     // the rows, and columns less rows
   const float *table;
   const int32_t *posq, *posk;
   const uint16_t *base;
@@ -40,13 +41,13 @@ struct RelArgs {
   int32_t starts[TRI_RELPOS_MAX_K];
 };
 
-// The table's row for the difference d (of at most 2^31 - 1 either way).
+// The table's row for the difference d.
 __device__ __forceinline__ int row_of(const RelArgs &a, int d) {
-  const int n = a.two ? abs(d) : max(-d, 0);
+  const uint32_t n = d < 0 ? 0u - (uint32_t)d : a.two ? (uint32_t)d : 0u;
   int lo = 0, hi = a.K - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (a.starts[mid] <= n)
+    if ((uint32_t)a.starts[mid] <= n)
       lo = mid;
     else
       hi = mid - 1;
@@ -54,10 +55,10 @@ __device__ __forceinline__ int row_of(const RelArgs &a, int d) {
   return a.two && d > 0 ? a.K + lo : lo;
 }
 
+// x - y, the ends of int32 where it passes them. (There is no such instruction any more.)
 __device__ __forceinline__ int sub_sat(int x, int y) {
-  int r;
-  asm("sub.sat.s32 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
-  return max(r, -0x7fffffff);
+  const int r = (int)((uint32_t)x - (uint32_t)y);
+  return ((x ^ y) & (x ^ r)) < 0 ? (x < 0 ? (int)0x80000000 : 0x7fffffff) : r;
 }
 
 // The difference of value e of a plane.
@@ -70,43 +71,62 @@ __device__ __forceinline__ int difference(const RelArgs &a, int b, int e) {
 // A lane's walk over its pairs of a unit that lies inside the plane: values e and e + 1, 64 further on with each step.
 template <bool kPos>
 struct Walk {
-  int j, d, i, q;  // of value e: column, j - i; kPos: row and its position
-  const int32_t *pq, *pk;
+  uint32_t j4;  // of value e: four times its column
+  int d, i, q;  // j - i; kPos: row and its position
+  const char *pq, *pk;
   __device__ __forceinline__ Walk(const RelArgs &a, int b, int e) : q(0), pq(nullptr), pk(nullptr) {
     i = (int)((uint32_t)e / (uint32_t)a.Nk);
-    j = e - i * a.Nk;
+    const int j = e - i * a.Nk;
+    j4 = 4u * (uint32_t)j;
     d = j - i;
     if (kPos) {
-      pq = a.posq + (int64_t)b * a.Nq;
-      pk = a.posk + (int64_t)b * a.Nk;
-      q = __ldg(pq + i);
+      pq = reinterpret_cast<const char *>(a.posq + (int64_t)b * a.Nq);
+      pk = reinterpret_cast<const char *>(a.posk + (int64_t)b * a.Nk);
+      q = at(pq, 4u * (uint32_t)i);
     }
   }
+  static __device__ __forceinline__ int at(const char *p, uint32_t offset) { return __ldg(reinterpret_cast<const int *>(p + offset)); }
   __device__ __forceinline__ void step(const RelArgs &a) {
-    j += a.step_j;
-    d += a.step_j - a.step_i;
-    const bool wrap = j >= a.Nk;
+    j4 += a.step_j4;
+    d += a.step_d;
+    const bool wrap = j4 >= a.nk4;
     if (wrap) {
-      j -= a.Nk;
+      j4 -= a.nk4;
       d -= a.Nk + 1;
     }
-    if (kPos) {
+    if (kPos && (wrap || a.step_i)) {
       i += a.step_i + (wrap ? 1 : 0);
-      if (wrap || a.step_i) q = __ldg(pq + min(i, a.Nq - 1));  // (one step past the unit's end is made)
+      q = at(pq, 4u * (uint32_t)min(i, a.Nq - 1));  // (one step past the unit's end is made)
     }
   }
   __device__ __forceinline__ void pair(const RelArgs &a, int &d0, int &d1) const {
-    const bool turn = j + 1 == a.Nk;  // (the second one begins the next row)
+    const bool turn = j4 + 4 == a.nk4;  // (the second one begins the next row)
     if (!kPos) {
       d0 = d;
       d1 = d + (turn ? -a.Nk : 1);
-    } else {
-      d0 = sub_sat(__ldg(pk + j), q);
-      d1 = sub_sat(__ldg(pk + (turn ? 0 : j + 1)), turn ? __ldg(pq + i + 1) : q);
+      return;
+    }
+    const int k0 = at(pk, j4), k1 = at(pk, turn ? 0u : j4 + 4), q1 = turn ? at(pq, 4u * (uint32_t)(i + 1)) : q;
+    d0 = (int)((uint32_t)k0 - (uint32_t)q);
+    d1 = (int)((uint32_t)k1 - (uint32_t)q1);
+    if ((((k0 ^ q) & (k0 ^ d0)) | ((k1 ^ q1) & (k1 ^ d1))) < 0) {  // (differences that int32 does not hold: rarely)
+      d0 = sub_sat(k0, q);
+      d1 = sub_sat(k1, q1);
     }
   }
 };
 constexpr int kUnit = 512, kPairs = kUnit / 64;  // values of a warp at a time, pairs of a lane
+
+// The differences of a lane's pairs from value e on.
+template <bool kPos>
+__device__ __forceinline__ void differences(const RelArgs &a, int b, int e, int (&d)[kPairs][2]) {
+  Walk<kPos> w(a, b, e);
+#pragma unroll
+  for (int p = 0; p < kPairs; ++p) {
+    w.pair(a, d[p][0], d[p][1]);
+    w.step(a);
+  }
+}
 
 // First value (an even index of the tensor; -1 in the first unit where the plane begins at an odd one) of unit k.
 __device__ __forceinline__ int unit_start(int64_t plane0, int k) { return kUnit * k - (int)(plane0 & 1); }
@@ -138,13 +158,11 @@ __global__ void __launch_bounds__(kFwdThreads) relpos_fwd_kernel(const __grid_co
 #pragma unroll
       for (int p = 0; p < kPairs; ++p) in[p] = __ldcs(base + 32 * p);
     }
-    Walk<kPos> w(a, b, u0 + 2 * lane);
+    int d[kPairs][2];  // (all first: their loads are in flight together)
+    differences<kPos>(a, b, u0 + 2 * lane, d);
 #pragma unroll
     for (int p = 0; p < kPairs; ++p) {
-      int d0, d1;
-      w.pair(a, d0, d1);
-      w.step(a);
-      float2 t = make_float2(value_of(d0), value_of(d1));
+      float2 t = make_float2(value_of(d[p][0]), value_of(d[p][1]));
       if (a.base) t = __fadd2_rn(t, make_float2(__uint_as_float(in[p] << 16), __uint_as_float(in[p] & 0xffff0000u)));
       bias[32 * p] = sm100::pack_bf16x2(t.x, t.y);
     }
@@ -154,47 +172,53 @@ __global__ void __launch_bounds__(kFwdThreads) relpos_fwd_kernel(const __grid_co
 // part[bh][piece][row]: a CTA's sums.
 template <bool kNear, bool kPos>
 __global__ void __launch_bounds__(kBwdThreads) relpos_bwd_kernel(const __grid_constant__ RelArgs a) {
-  extern __shared__ float sums[];  // [warp][row][33], then (kNear) the rows by distance, one byte each
+  extern __shared__ float sums[];  // [warp][row][33], then (kNear) where a distance's row begins
   constexpr int W = kBwdThreads / 32;
-  uint8_t *row_at = reinterpret_cast<uint8_t *>(sums + W * a.rows * 33);
+  uint16_t *row_at = reinterpret_cast<uint16_t *>(sums + W * a.rows * 33);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int bh = blockIdx.y + gridDim.y * blockIdx.z, b = bh / a.H;
   if (b >= a.B) return;
   allow_next_kernel();
   for (int x = threadIdx.x; x < W * a.rows * 33; x += kBwdThreads) sums[x] = 0.f;
   if (kNear)
-    for (int x = threadIdx.x; x < 2 * a.L + 1; x += kBwdThreads) row_at[x] = (uint8_t)row_of(a, x - a.L);
+    for (int x = threadIdx.x; x < 2 * a.L + 1; x += kBwdThreads) row_at[x] = (uint16_t)(33 * row_of(a, x - a.L));
   __syncthreads();
   float *mine = sums + warp * a.rows * 33 + lane;
-  auto add = [&](int d, float g) { mine[(kNear ? row_at[min(max(d, -a.L), a.L) + a.L] : row_of(a, d)) * 33] += g; };
+  auto add = [&](int d, float g) { mine[kNear ? row_at[min(max(d, -a.L), a.L) + a.L] : 33 * row_of(a, d)] += g; };
   const int64_t plane0 = bh * a.plane;
   const int k1 = min((blockIdx.x + 1) * a.piece, a.units);
   float behind = 0.f, ahead = 0.f;  // d <= -L, d >= L
+  auto inner = [&](int k) { return unit_start(plane0, k) >= 0 && unit_start(plane0, k) + kUnit <= a.plane; };
+  auto load = [&](int k, uint32_t (&g)[kPairs]) {  // (a unit ahead: a warp has 1 KB on its way, 24 warps of an SM alone too little)
+    if (k >= k1 || !inner(k)) return;
+    const uint32_t *dbias = reinterpret_cast<const uint32_t *>(a.dbias + plane0 + unit_start(plane0, k) + 2 * lane);
+#pragma unroll
+    for (int p = 0; p < kPairs; ++p) g[p] = __ldcs(dbias + 32 * p);
+  };
+  uint32_t next[kPairs];
+  load(blockIdx.x * a.piece + warp, next);
   for (int k = blockIdx.x * a.piece + warp; k < k1; k += W) {
     const int u0 = unit_start(plane0, k);
-    if (u0 < 0 || u0 + kUnit > a.plane) {  // a plane's ends, value by value
+    uint32_t g[kPairs];
+#pragma unroll
+    for (int p = 0; p < kPairs; ++p) g[p] = next[p];
+    load(k + W, next);
+    if (!inner(k)) {  // a plane's ends, value by value
       for (int e = u0 + lane + (u0 + lane < 0 ? 32 : 0); e < min(u0 + kUnit, (int)a.plane); e += 32)
         add(difference<kPos>(a, b, e), bf16_to_f32(a.dbias[plane0 + e]));
       continue;
     }
-    const uint32_t *dbias = reinterpret_cast<const uint32_t *>(a.dbias + plane0 + u0 + 2 * lane);
-    uint32_t g[kPairs];
-#pragma unroll
-    for (int p = 0; p < kPairs; ++p) g[p] = __ldcs(dbias + 32 * p);
-    Walk<kPos> w(a, b, u0 + 2 * lane);
+    int d[kPairs][2];
+    differences<kPos>(a, b, u0 + 2 * lane, d);
 #pragma unroll
     for (int p = 0; p < kPairs; ++p) {
-      int d0, d1;
-      w.pair(a, d0, d1);
-      w.step(a);
       const float g0 = __uint_as_float(g[p] << 16), g1 = __uint_as_float(g[p] & 0xffff0000u);
-      if (min(d0, d1) >= a.L) {
-        ahead += g0 + g1;
-      } else if (max(d0, d1) <= -a.L) {
-        behind += g0 + g1;
-      } else {
-        add(d0, g0);
-        add(d1, g1);
+      const bool up = min(d[p][0], d[p][1]) >= a.L, down = max(d[p][0], d[p][1]) <= -a.L;
+      if (up) ahead += g0 + g1;
+      if (down) behind += g0 + g1;
+      if (!up && !down) {
+        add(d[p][0], g0);
+        add(d[p][1], g1);
       }
     }
   }
@@ -230,7 +254,7 @@ __global__ void __launch_bounds__(256) relpos_reduce_kernel(const float *__restr
 
 int relpos_check(const tri_relpos_shape &s) {
   if (s.B < 1 || s.H < 1 || s.Nq < 1 || s.Nk < 1 || s.K < 1 || (s.two_sided != 0 && s.two_sided != 1)) return TRI_ATTN_ERR_INVALID_ARG;
-  if (s.K > TRI_RELPOS_MAX_K || (int64_t)s.B * s.H > (1 << 20) || (int64_t)s.Nq * s.Nk > TRI_RELPOS_MAX_PLANE) return TRI_ATTN_ERR_UNSUPPORTED;
+  if (s.K > TRI_RELPOS_MAX_K || (int64_t)s.B * s.H > (1 << 20) || (int64_t)s.Nq * s.Nk > TRI_RELPOS_MAX_PLANE || s.Nk >= (1 << 30)) return TRI_ATTN_ERR_UNSUPPORTED;
   return TRI_ATTN_OK;
 }
 int starts_check(const tri_relpos_shape &s, const int32_t *starts) {
@@ -259,8 +283,10 @@ RelArgs rel_args(const tri_relpos_shape &s, int warps, int ctas) {
   a.two = s.two_sided;
   a.rows = s.K << s.two_sided;
   a.plane = (int64_t)s.Nq * s.Nk;
+  a.nk4 = 4u * (uint32_t)a.Nk;
   a.step_i = 64 / a.Nk;
-  a.step_j = 64 % a.Nk;
+  a.step_j4 = 4u * (uint32_t)(64 % a.Nk);
+  a.step_d = 64 % a.Nk - a.step_i;
   cut(a, warps, ctas);
   return a;
 }
@@ -348,7 +374,7 @@ int tri_relpos_bwd(tri_relpos_shape shape, const int32_t *starts, const int32_t 
   a.dbias = reinterpret_cast<const uint16_t *>(dbias);
   a.part = static_cast<float *>(workspace);
   const bool near = a.L <= kLookup;
-  const size_t smem = sizeof(float) * (kBwdThreads / 32) * a.rows * 33 + (near ? 2 * a.L + 1 : 0);
+  const size_t smem = sizeof(float) * (kBwdThreads / 32) * a.rows * 33 + (near ? 2 * (2 * a.L + 1) : 0);
   const auto st = static_cast<cudaStream_t>(stream);
   cudaError_t e = near && positions ? launch_relpos_bwd<true, true>(a, smem, st)
                   : near            ? launch_relpos_bwd<true, false>(a, smem, st)

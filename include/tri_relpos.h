@@ -16,7 +16,7 @@
  * [B, Nk], both or neither; base, bias, dbias BF16 [B, H, Nq, Nk]; all on the device without gaps. starts: K
  * numbers in host memory, read during the call: 0 = starts[0] < starts[1] < ...
  *
- * Requirements: B, H, Nq, Nk >= 1; 1 <= K <= TRI_RELPOS_MAX_K; B H <= 2^20, Nq Nk <= TRI_RELPOS_MAX_PLANE; bias, base and dbias 16-byte aligned,
+ * Requirements: B, H, Nq, Nk >= 1; 1 <= K <= TRI_RELPOS_MAX_K; B H <= 2^20, Nk < 2^30, Nq Nk <= TRI_RELPOS_MAX_PLANE; bias, base and dbias 16-byte aligned,
  * the others 4; buffers not overlapping (bias may be base: in place). Differences of positions saturate at the ends of int32.
  * Return codes are the TRI_ATTN_* codes of tri_attn.h; a call that returns an error has enqueued nothing
  * (TRI_ATTN_ERR_CUDA from a launch itself excepted). Calls are asynchronous on `stream`, allocate nothing, keep
