@@ -746,6 +746,11 @@ inline cudaError_t device_and_pairs(int *dev, int *pairs) {
 cudaError_t launch_block(const tri_ffn_shape &s, const void *x, const void *Wg, const void *Wu, const void *Wd, void *out, void *ka,
                          void *ku, int *status, int dev, int pairs, cudaStream_t st);
 
+// The forward of at most kFewRows rows (ffn_few.cu; ka, ku: both or neither; h: room for the features).
+constexpr int kFewRows = 32;
+cudaError_t launch_few(const tri_ffn_shape &s, const void *x, const void *Wg, const void *Wu, const void *Wd, void *out, void *ka,
+                       void *ku, void *h, cudaStream_t st);
+
 inline int64_t aligned256(int64_t n) { return (n + 255) / 256 * 256; }
 
 inline int check_shape(const tri_ffn_shape &s) {

@@ -26,12 +26,17 @@ bool block_pays(const tri_ffn_shape &s, int pairs) {
   return s.C <= 256 && 4.3 + rounds * ceil_div(s.F, 64) * (s.C <= 128 ? 0.65 : 1.13) < 8 + 1.1e-6 * (double)s.M * s.F;
 }
 
+// Whether the few rows' kernels are faster: up to 16 rows always (8 of 4096 and 16384: 62 us, 85 in tiles; of 1024 and 4096: 9 and
+// 19), up to 32 where the weights are small (32 of 1024 and 4096: 16 and 19, of 512 and 16384: 38 and 26).
+bool few_rows_pay(const tri_ffn_shape &s) { return s.M <= 16 || (s.M <= kFewRows && (int64_t)s.C * s.F <= (1 << 22)); }
+
 cudaError_t launch_fwd(const tri_ffn_shape &s, const void *x, const void *Wg, const void *Wu, const void *Wd, void *out, void *a,
                        void *u, char *ws, int *status, cudaStream_t st) {
   const FwdWorkspace w = fwd_workspace(s);
   int dev = 0, pairs = 0;
   cudaError_t e = device_and_pairs(&dev, &pairs);
   if (e != cudaSuccess) return e;
+  if (few_rows_pay(s)) return launch_few(s, x, Wg, Wu, Wd, out, a, u, ws + w.h, st);
   if (block_pays(s, pairs)) return launch_block(s, x, Wg, Wu, Wd, out, a, u, status, dev, pairs, st);
   float *part = reinterpret_cast<float *>(ws + w.part);
   const int64_t C = s.C, F = s.F, ldx = s.ldx ? s.ldx : C;

@@ -23,7 +23,8 @@ ACTS = ["silu", "gelu", "sigmoid"]
 # (rows, channels, features): tiles filled and not, one row, one block of channels, shares of a tile over many pairs
 SIZES = [(1, 8, 8), (1, 64, 128), (7, 72, 200), (128, 64, 64), (129, 128, 512), (256, 256, 256), (300, 136, 1032), (513, 384, 1536),
          (1000, 264, 264), (4001, 392, 1032), (9, 2048, 8192), (20000, 128, 512), (64, 4096, 520),
-         (19500, 64, 200), (39999, 200, 264), (60001, 256, 64), (19457, 8, 8), (50000, 136, 328), (80000, 128, 64)]
+         (19500, 64, 200), (39999, 200, 264), (60001, 256, 64), (19457, 8, 8), (50000, 136, 328), (80000, 128, 64),
+         (2, 1000, 3000), (8, 4096, 1032), (15, 264, 72), (16, 2048, 520), (17, 72, 4104), (31, 520, 264), (32, 1032, 2048), (33, 1032, 2048)]
 
 
 def normal(gen, *shape, std=1.0):
