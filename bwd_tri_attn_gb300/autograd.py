@@ -212,3 +212,172 @@ class TriangleAttentionBlock(torch.nn.Module):
     def forward(self, z, mask=None):
         return triangle_attention_block(z, self.gamma, self.beta, self.W, self.wb, self.Wo, mask, self.H, self.d,
                                         self.node, self.eps, self.checkpoint)
+
+
+class _RelativePositionBias(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, table, base, starts, Nq, Nk, B, two_sided, positions, key_positions):
+        base = None if base is None else _dense(base)
+        positions, key_positions = (None if t is None else t.contiguous() for t in (positions, key_positions))
+        ctx.cfg = (starts, two_sided, table.dtype)
+        ctx.save_for_backward(positions, key_positions)
+        return tb.relpos_forward(table.float().contiguous(), starts, Nq, Nk, B, two_sided, base, positions, key_positions)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dbias):
+        positions, key_positions = ctx.saved_tensors
+        starts, two_sided, dtype = ctx.cfg
+        dtable = None
+        if ctx.needs_input_grad[0]:
+            dtable = tb.relpos_backward(_dense(dbias.to(torch.bfloat16)), starts, two_sided, positions, key_positions).to(dtype)
+        return (dtable, dbias if ctx.needs_input_grad[1] else None, *[None] * 7)
+
+
+def relative_position_bias(table, starts, Nq, Nk=None, B=1, base=None, two_sided=True, positions=None, key_positions=None):
+    """The BF16 pair bias [B, H, Nq, Nk] that triangle_attention takes: base + table[bucket(key's position - query's)].
+    table [2 K, H] (one-sided: [K, H]); starts: the buckets' first distances (binding.relpos_starts makes logarithmic ones);
+    base BF16 [B, H, Nq, Nk] or None; positions int32 [B, Nq] and key_positions [B, Nk] (None: 0, 1, 2, ...)."""
+    return _RelativePositionBias.apply(table, base, tuple(int(s) for s in starts), Nq, Nk, B, two_sided, positions, key_positions)
+
+
+class _RmsNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, gamma, residual, eps):
+        x = x.contiguous()
+        g32 = None if gamma is None else gamma.float().contiguous()
+        got = tb.rms_forward(x, g32, None if residual is None else residual.contiguous(), eps=eps)
+        ctx.dtype = None if gamma is None else gamma.dtype
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(x if got.r is None else got.r, g32, got.rstd)
+        return got.y if got.r is None else (got.y, got.r)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dr=None):
+        r, g32, rstd = ctx.saved_tensors
+        if dy is None:  # (only the sum was used)
+            return dr, None, dr, None
+        dx, dgamma = tb.rms_backward(r, g32, rstd, dy.contiguous(), None if dr is None else dr.contiguous())
+        return dx, None if dgamma is None else dgamma.to(ctx.dtype), dx if ctx.needs_input_grad[2] else None, None
+
+
+def rms_norm(x, gamma=None, residual=None, eps=1e-5):
+    """RMS norm over the last axis of x [..., C] (BF16, FP16 or FP32; FP32 statistics and weights): y, and with a
+    residual (y, r), the norm of r = x + residual and r, which goes on past the layer."""
+    return _RmsNorm.apply(x, gamma, residual, eps)
+
+
+class _GatedFeedForward(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, Wg, Wu, Wd, act, checkpoint):
+        x = _dense(x)
+        bf = [_dense(w.to(torch.bfloat16)) for w in (Wg, Wu, Wd)]
+        out, *kept = (tb.ffn_forward(x, *bf, act=act), *tb.checkpoint_pack(x)) if checkpoint else (
+            *tb.ffn_forward(x, *bf, act=act, keep=True), x)
+        ctx.cfg = (act, checkpoint, [w.dtype for w in (Wg, Wu, Wd)])
+        ctx.save_for_backward(*bf, *kept)
+        return out
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dout):
+        act, checkpoint, dtypes = ctx.cfg
+        Wg, Wu, Wd, *kept = ctx.saved_tensors
+        if checkpoint:
+            x = tb.checkpoint_unpack(kept)
+            a, u = tb.ffn_forward(x, Wg, Wu, Wd, act=act, keep="only")
+        else:
+            a, u, x = kept
+        return (*_ffn_gradients(ctx.needs_input_grad[:4], x, (Wg, Wu, Wd), a, u, dout, act, dtypes), None, None)
+
+
+def _ffn_gradients(needs, x, weights, a, u, dout, act, dtypes):
+    """The gradients of x and the three weights (None where needs says so), in the weights' masters' dtypes: from FP32 ones
+    where a master is not BF16."""
+    exact = torch.bfloat16 if all(d == torch.bfloat16 for d in dtypes) else torch.float32
+    dx, *dw = tb.ffn_backward(x, *weights, a, u, _dense(dout.to(torch.bfloat16)), act=act, weight_dtype=exact,
+                              need_dx=needs[0], need_dw=any(needs[1:]))
+    return (dx, *(g.to(d) if n else None for g, d, n in zip(dw, dtypes, needs[1:])))
+
+
+def _wants_gradients(*tensors):
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+
+
+def gated_feed_forward(x, Wg, Wu, Wd, act="silu", checkpoint=False):
+    """The gated feed-forward block act(x Wg^T) (x Wu^T) Wd^T on BF16 rows x [..., C]: Wg, Wu [F, C] and Wd [C, F], BF16 or
+    masters of another type (the forward uses their BF16 rounding); act "silu", "gelu" or "sigmoid". With ``checkpoint``
+    it keeps x in 8 bits in the place of x and both projections, and its gradients are those at the checkpoint's values."""
+    if not _wants_gradients(x, Wg, Wu, Wd):
+        return tb.ffn_forward(_dense(x), *(_dense(w.to(torch.bfloat16)) for w in (Wg, Wu, Wd)), act=act)
+    return _GatedFeedForward.apply(x, Wg, Wu, Wd, act, checkpoint)
+
+
+class _FeedForwardLayer(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, residual, gamma, Wg, Wu, Wd, act, eps, checkpoint):
+        x, residual = x.contiguous(), residual.contiguous()
+        bf = [_dense(w.to(torch.bfloat16)) for w in (Wg, Wu, Wd)]
+        g32 = gamma.float().contiguous()
+        got = tb.rms_forward(x, g32, residual, eps=eps, eight_bits=checkpoint)
+        out, *kept = (tb.ffn_forward(got.y, *bf, act=act), *got.y8) if checkpoint else (
+            *tb.ffn_forward(got.y, *bf, act=act, keep=True), got.y)
+        ctx.cfg = (act, checkpoint, gamma.dtype, [w.dtype for w in (Wg, Wu, Wd)])
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(*bf, g32, got.r, got.rstd, *kept)
+        return out, got.r
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dout, dr):
+        act, checkpoint, dtype, dtypes = ctx.cfg
+        Wg, Wu, Wd, g32, r, rstd, *kept = ctx.saved_tensors
+        if dout is None:  # (only the sum was used)
+            return dr, dr, *[None] * 7
+        if checkpoint:
+            y = tb.checkpoint_unpack(kept)
+            a, u = tb.ffn_forward(y, Wg, Wu, Wd, act=act, keep="only")
+        else:
+            a, u, y = kept
+        needs = (any(ctx.needs_input_grad[:3]), *ctx.needs_input_grad[3:6])
+        dy, *dw = _ffn_gradients(needs, y, (Wg, Wu, Wd), a, u, dout, act, dtypes)
+        dx = dgamma = None
+        if dy is not None:
+            dx, dgamma = tb.rms_backward(r, g32, rstd, dy, None if dr is None else dr.contiguous())
+            dgamma = dgamma.to(dtype)
+        return (dx, dx, dgamma, *dw, None, None, None)
+
+
+def feed_forward_layer(x, residual, gamma, Wg, Wu, Wd, act="silu", eps=1e-5, checkpoint=False):
+    """A pre-norm feed-forward layer on BF16 rows: r = x + residual, the gated feed-forward block of r's RMS norm (weights
+    gamma [C]); returns (out, r), of which the next layer takes the sum. With ``checkpoint`` the block's input is kept in 8 bits,
+    written by the norm, in the place of the normalised rows and both projections, which the backward pass recomputes."""
+    if not _wants_gradients(x, residual, gamma, Wg, Wu, Wd):
+        got = tb.rms_forward(x.contiguous(), gamma.float().contiguous(), residual.contiguous(), eps=eps)
+        return tb.ffn_forward(got.y, *(_dense(w.to(torch.bfloat16)) for w in (Wg, Wu, Wd)), act=act), got.r
+    return _FeedForwardLayer.apply(x, residual, gamma, Wg, Wu, Wd, act, eps, checkpoint)
+
+
+class FeedForwardLayer(torch.nn.Module):
+    """The pre-norm feed-forward layer as a module with FP32 master parameters: gamma 1, the weights normal / sqrt of
+    their input's width. forward(x, residual) returns (out, r)."""
+
+    def __init__(self, C: int = 128, F: int = 512, act: str = "silu", eps: float = 1e-5, device=None, checkpoint: bool = False):
+        super().__init__()
+        self.act, self.eps, self.checkpoint = act, eps, checkpoint
+        f32 = dict(dtype=torch.float32, device=device)
+        self.gamma = torch.nn.Parameter(torch.ones(C, **f32))
+        self.Wg = torch.nn.Parameter(torch.randn(F, C, **f32) / math.sqrt(C))
+        self.Wu = torch.nn.Parameter(torch.randn(F, C, **f32) / math.sqrt(C))
+        self.Wd = torch.nn.Parameter(torch.randn(C, F, **f32) / math.sqrt(F))
+
+    def forward(self, x, residual):
+        return feed_forward_layer(x, residual, self.gamma, self.Wg, self.Wu, self.Wd, self.act, self.eps, self.checkpoint)
+
+
+def clip_grad_norm_(parameters, max_norm):
+    """Clips the gradients of the parameters (those that have one) in place to the 2-norm max_norm of all of them together
+    and returns their norm before, an FP32 number on the device."""
+    parameters = [parameters] if isinstance(parameters, torch.Tensor) else list(parameters)
+    return tb.clip_gradients([p.grad for p in parameters if p.grad is not None], max_norm)

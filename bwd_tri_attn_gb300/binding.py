@@ -670,7 +670,7 @@ def tri_ffn_fwd_workspace_size(shape: FfnShape) -> int:
 
 def tri_ffn_fwd(shape: FfnShape, x, Wg, Wu, Wd, out, a, u, workspace, stream=None):
     hidden = shape.M * shape.F
-    ptrs = _ptrs(*_ffn_args(shape, x, Wg, Wu, Wd), _arg(out, "out", _BF16, shape.M * shape.C),
+    ptrs = _ptrs(*_ffn_args(shape, x, Wg, Wu, Wd), _arg(out, "out", _BF16, shape.M * shape.C, True),
                  _arg(a, "a", _BF16, hidden, True), _arg(u, "u", _BF16, hidden, True),
                  _arg(workspace, "workspace", None, None, True))
     rc = load().tri_ffn_fwd(shape, *ptrs, _nbytes(workspace), _stream(stream))
@@ -1102,21 +1102,23 @@ def _weights_args(Wg, Wu, Wd):
 def ffn_forward(x, Wg, Wu, Wd, act="silu", keep=False, workspace=None, stream=None):
     """The gated feed-forward block act(x Wg^T) (x Wu^T) Wd^T on x [..., C] with Wg, Wu [F, C] and Wd [C, F] (BF16; rows
     of x may be spaced apart); act: "silu", "gelu" or "sigmoid". Returns out [..., C], with ``keep`` (out, a, u): also
-    the two projections [..., F], which ffn_backward reads."""
+    the two projections [..., F], which ffn_backward reads; keep="only": (a, u) alone."""
     if (other := _other_stream(stream)) is not None:
         return _called_on(other, ffn_forward, x, Wg, Wu, Wd, act, keep, workspace=workspace)
+    if keep not in (False, True, "only"):
+        raise ValueError(f"keep must be False, True or \"only\", got {keep!r}")
     shape = ffn_shape_of(x, Wg, Wu, Wd, act)
     device = _on_device(x.get_device(), ("x", x), *_weights_args(Wg, Wu, Wd), _arg(workspace, "workspace", None, None, True))
-    out = _dense_like(x)
+    out = None if keep == "only" else _dense_like(x)
     a = u = None
     if keep:
         a, u = (torch.empty((*x.shape[:-1], shape.F), dtype=_BF16, device=x.device) for _ in range(2))
     if workspace is None:
         workspace = _workspace(tri_ffn_fwd_workspace_size(shape), x)
-    rc = load().tri_ffn_fwd(shape, x.data_ptr(), Wg.data_ptr(), Wu.data_ptr(), Wd.data_ptr(), out.data_ptr(), _ptr(a),
+    rc = load().tri_ffn_fwd(shape, x.data_ptr(), Wg.data_ptr(), Wu.data_ptr(), Wd.data_ptr(), _ptr(out), _ptr(a),
                             _ptr(u), _ptr(workspace), _nbytes(workspace), _raw_stream(device))
     _check("tri_ffn_fwd", rc)
-    return (out, a, u) if keep else out
+    return (a, u) if out is None else (out, a, u) if keep else out
 
 
 def ffn_backward(x, Wg, Wu, Wd, a, u, dout, act="silu", weight_dtype=_BF16, need_dx=True, need_dw=True, workspace=None,

@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) few_kernel(const FewArgs a) {
 template <int T>
 cudaError_t launch(const FewArgs &hidden, const FewArgs &out, cudaStream_t st) {
   cudaError_t e = launch_after(few_kernel<true, T>, dim3(ceil_div(hidden.rows, 16)), dim3(32 * kWarps), 0, st, hidden);
-  if (e == cudaSuccess) e = launch_after(few_kernel<false, T>, dim3(ceil_div(out.rows, 16)), dim3(32 * kWarps), 0, st, out);
+  if (e == cudaSuccess && out.o) e = launch_after(few_kernel<false, T>, dim3(ceil_div(out.rows, 16)), dim3(32 * kWarps), 0, st, out);
   return e;
 }
 

@@ -37,7 +37,7 @@ cudaError_t launch_fwd(const tri_ffn_shape &s, const void *x, const void *Wg, co
   cudaError_t e = device_and_pairs(&dev, &pairs);
   if (e != cudaSuccess) return e;
   if (few_rows_pay(s)) return launch_few(s, x, Wg, Wu, Wd, out, a, u, ws + w.h, st);
-  if (block_pays(s, pairs)) return launch_block(s, x, Wg, Wu, Wd, out, a, u, status, dev, pairs, st);
+  if (out && block_pays(s, pairs)) return launch_block(s, x, Wg, Wu, Wd, out, a, u, status, dev, pairs, st);
   float *part = reinterpret_cast<float *>(ws + w.part);
   const int64_t C = s.C, F = s.F, ldx = s.ldx ? s.ldx : C;
   Args io{};
@@ -54,19 +54,21 @@ cudaError_t launch_fwd(const tri_ffn_shape &s, const void *x, const void *Wg, co
   AnyProduct<kHidden> hidden;
   e = hidden.plan(io, &mx, 1, mw, 2, pairs, dev);
   if (e != cudaSuccess) return e;
-  Args io2{};
-  io2.part = part;
-  io2.status = status;
-  io2.rows[0] = io2.rows[1] = (int)s.M;
-  io2.cols[0] = io2.cols[1] = s.C;
-  io2.nk = io2.nk0 = ceil_div(F, kBlock);
-  io2.o[0] = out;
-  const Matrix mh{ws + w.h, F, s.M, F}, md{Wd, F, C, F};
   AnyProduct<kOut> down;
-  e = down.plan(io2, &mh, 1, &md, 1, pairs, dev);
-  if (e != cudaSuccess) return e;
+  if (out) {
+    Args io2{};
+    io2.part = part;
+    io2.status = status;
+    io2.rows[0] = io2.rows[1] = (int)s.M;
+    io2.cols[0] = io2.cols[1] = s.C;
+    io2.nk = io2.nk0 = ceil_div(F, kBlock);
+    io2.o[0] = out;
+    const Matrix mh{ws + w.h, F, s.M, F}, md{Wd, F, C, F};
+    e = down.plan(io2, &mh, 1, &md, 1, pairs, dev);
+    if (e != cudaSuccess) return e;
+  }
   e = hidden.launch(st);
-  return e == cudaSuccess ? down.launch(st) : e;
+  return e == cudaSuccess && out ? down.launch(st) : e;
 }
 
 }  // namespace
@@ -83,7 +85,7 @@ int tri_ffn_fwd(tri_ffn_shape shape, const tri_attn_bf16 *x, const tri_attn_bf16
                 size_t workspace_bytes, void *stream) {
   const int rc = ffn::check_shape(shape);
   if (rc) return rc;
-  if (!x || !Wg || !Wu || !Wd || !out || (a != nullptr) != (u != nullptr)) return TRI_ATTN_ERR_INVALID_ARG;
+  if (!x || !Wg || !Wu || !Wd || (!out && !a) || (a != nullptr) != (u != nullptr)) return TRI_ATTN_ERR_INVALID_ARG;
   for (const void *p : {(const void *)x, (const void *)Wg, (const void *)Wu, (const void *)Wd, (const void *)out, (const void *)a,
                         (const void *)u, (const void *)workspace})
     if (reinterpret_cast<uintptr_t>(p) & 15u) return TRI_ATTN_ERR_UNSUPPORTED;

@@ -56,7 +56,10 @@ typedef struct tri_ffn_shape {
 /* Bytes of workspace tri_ffn_fwd needs (0 for a bad shape). */
 size_t tri_ffn_fwd_workspace_size(tri_ffn_shape shape);
 
-/* Forward. a and u are both given (kept for the backward pass) or both NULL. */
+/*
+ * Forward. a and u are both given (kept for the backward pass) or both NULL; where they are given out may be NULL (a pass
+ * that recomputes them).
+ */
 int tri_ffn_fwd(tri_ffn_shape shape, const tri_attn_bf16 *x, const tri_attn_bf16 *Wg, const tri_attn_bf16 *Wu,
                 const tri_attn_bf16 *Wd, tri_attn_bf16 *out, tri_attn_bf16 *a, tri_attn_bf16 *u, void *workspace,
                 size_t workspace_bytes, void *stream);
