@@ -24,7 +24,8 @@ ACTS = ["silu", "gelu", "sigmoid"]
 SIZES = [(1, 8, 8), (1, 64, 128), (7, 72, 200), (128, 64, 64), (129, 128, 512), (256, 256, 256), (300, 136, 1032), (513, 384, 1536),
          (1000, 264, 264), (4001, 392, 1032), (9, 2048, 8192), (20000, 128, 512), (64, 4096, 520),
          (19500, 64, 200), (39999, 200, 264), (60001, 256, 64), (19457, 8, 8), (50000, 136, 328), (80000, 128, 64),
-         (2, 1000, 3000), (8, 4096, 1032), (15, 264, 72), (16, 2048, 520), (17, 72, 4104), (31, 520, 264), (32, 1032, 2048), (33, 1032, 2048)]
+         (2, 1000, 3000), (8, 4096, 1032), (15, 264, 72), (16, 2048, 520), (17, 72, 4104), (31, 520, 264), (32, 1032, 2048), (33, 1032, 2048),
+         (10000, 1032, 2056)]
 
 
 def normal(gen, *shape, std=1.0):
@@ -94,3 +95,49 @@ def test_forward_and_backward(M, C, Fh):
     got = tb.ffn_backward(x, wg, wu, wd, a, u, dout, act=act)
     assert tb.tri_attn_device_status() == 0
     check_backward(x, wg, wu, wd, a, u, dout, act, got)
+
+
+@pytest.mark.parametrize("M,C,Fh", [(1, 8, 8), (300, 136, 1032), (2000, 72, 40), (5000, 264, 520)])
+def test_weight_gradients_in_32_bits(M, C, Fh):
+    """Their own rounding is FP32's: what is left is that of h, da and du."""
+    x, wg, wu, wd, dout = inputs(M, C, Fh, 2)
+    _, a, u = tb.ffn_forward(x, wg, wu, wd, keep=True)
+    got = tb.ffn_backward(x, wg, wu, wd, a, u, dout, weight_dtype=torch.float32)
+    assert all(t.dtype == torch.float32 for t in got[1:])
+    check_backward(x, wg, wu, wd, a, u, dout, "silu", got, out=2.0 ** -24)
+    some = tb.ffn_backward(x, wg, wu, wd, a, u, dout, need_dw=False)
+    assert torch.equal(some[0], got[0]) and some[1:] == (None, None, None)
+    some = tb.ffn_backward(x, wg, wu, wd, a, u, dout, need_dx=False, weight_dtype=torch.float32)
+    assert some[0] is None and all(torch.equal(p, q) for p, q in zip(some[1:], got[1:]))
+
+
+@pytest.mark.parametrize("M,C,Fh", [(5, 128, 256), (100, 72, 200), (20000, 64, 128)])
+def test_projections_alone(M, C, Fh):
+    """What a pass that recomputes them asks for: the bits of the whole forward, in each of its forms but the one kernel's,
+    whose sums run in the same order too."""
+    x, wg, wu, wd, _ = inputs(M, C, Fh, 3)
+    _, a, u = tb.ffn_forward(x, wg, wu, wd, keep=True)
+    a2, u2 = tb.ffn_forward(x, wg, wu, wd, keep="only")
+    assert torch.equal(a, a2) and torch.equal(u, u2)
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("M", [3, 200, 20000])
+def test_activations_far_out(act, M):
+    """Gates from -1e30 to 1e30 (sums of one product each): finite, and as the formulas have it."""
+    C = Fh = 64
+    gates = torch.tensor([0.0, -0.0, 1e-30, -1e-30, 1.0, -1.0, -20.0, -39.0, -41.0, -80.0, -87.0, -88.0, -89.0, -120.0, -1e4, -1e30, 20.0, 89.0, 1e4, 1e30])
+    x = torch.zeros(M, C, device="cuda")
+    x[:, 0] = 1.0
+    x = x.bfloat16()
+    wg, wu = torch.zeros(Fh, C, device="cuda"), torch.zeros(Fh, C, device="cuda")
+    wg[:, 0] = gates.repeat(4)[:Fh].cuda()
+    wu[:, 0] = 2.0
+    wg, wu, wd = wg.bfloat16(), wu.bfloat16(), torch.eye(Fh, device="cuda").bfloat16()
+    out, a, u = tb.ffn_forward(x, wg, wu, wd, act=act, keep=True)
+    f, df = act64(a[0].double(), act)
+    assert torch.equal(a[0], wg[:, 0]) and ((out.double() - 2 * f).abs() <= 3 * U * (2 * f).abs() + 2.0 ** -19 * (1 + a[0].double().abs().clamp(max=6))).all()
+    dx, dwg, dwu, _ = tb.ffn_backward(x, wg, wu, wd, a, u, x, act=act)
+    assert dx.isfinite().all() and dwg.isfinite().all() and dwu.isfinite().all()
+    want = M * 2 * df[0]  # (dout = x reaches feature 0 alone)
+    assert abs(dwg[0, 0].item() - want.item()) <= 3 * U * abs(want.item()) + M * 2.0 ** -18
