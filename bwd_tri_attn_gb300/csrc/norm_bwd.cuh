@@ -88,13 +88,14 @@ static __global__ void __launch_bounds__(1024) norm_reduce_kernel(const float *_
   float s = 0.f;
   wait_previous_kernel();
   if (i < n) {
-    int p = threadIdx.y;
-    for (; p + 96 < parts; p += 128) {  // four loads in flight, added in order
-      const float a0 = part[(int64_t)p * n + i], a1 = part[(int64_t)(p + 32) * n + i];
-      const float a2 = part[(int64_t)(p + 64) * n + i], a3 = part[(int64_t)(p + 96) * n + i];
-      s = (((s + a0) + a1) + a2) + a3;
+    for (int p = threadIdx.y; p < parts; p += 256) {  // eight loads in flight, added in order
+      float a[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) a[k] = p + 32 * k < parts ? part[(int64_t)(p + 32 * k) * n + i] : 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (p + 32 * k < parts) s += a[k];
     }
-    for (; p < parts; p += 32) s += part[(int64_t)p * n + i];
   }
   acc[threadIdx.y][threadIdx.x] = s;
   __syncthreads();
