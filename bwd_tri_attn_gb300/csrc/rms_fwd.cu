@@ -2,12 +2,14 @@
 // the formulas).
 //
 // A row is read once into registers, added, rounded and squared there, and everything leaves in the same pass: memory
-// bandwidth bounds the kernel. Rows are spread over threads as in the LayerNorm's forward (norm.cuh).
+// bandwidth bounds the kernel. Rows are spread over threads as in the LayerNorm's forward (norm.cuh). Rows of odd width that
+// begin equally far from a boundary in all tensors are taken in step (rows_step.cuh), with aligned accesses and the weights,
+// shifted as the CTA's rows are, in shared memory (not with the 8-bit output, whose groups of channels no chunk may cut).
 #include <math.h>
 
 #include <algorithm>
 
-#include "norm.cuh"
+#include "rows_step.cuh"
 #include "tri_rms.h"
 
 namespace triattn {
@@ -33,12 +35,14 @@ struct RmsFwdArgs {
   int8_t *q8;
 };
 
-template <typename XT, int T, int NV, bool AL>
+template <typename XT, int T, int NV, int ROWS>
 __global__ void __launch_bounds__(T > 32 ? T : 256, rms_ctas<NV>() * (T == 128 ? 2 : 1))
     rms_fwd_kernel(const RmsFwdArgs a, const XT *__restrict__ x, const XT *__restrict__ res, XT *__restrict__ r, XT *__restrict__ y) {
+  constexpr bool AL = ROWS == kAlignedRows, STEP = ROWS == kRowsInStep;
   constexpr int VEC = Chunk<XT>::VEC, P = VEC / 2, NT = T > 32 ? T : 256, RPC = NT / T, U = rms_rows<NV>();
   constexpr int GL = (TRI_CKPT_GROUP / VEC) < T ? (TRI_CKPT_GROUP / VEC) : T;  // lanes per checkpoint group
   __shared__ float red[T > 32 ? 2 * T / 32 : 1][U];
+  __shared__ __align__(16) float weights[STEP ? T * NV * VEC : 4];
   RowSum<T, U> row_sum{red, 0};
   const int64_t M = a.M;
   const int C = a.C;
@@ -46,30 +50,49 @@ __global__ void __launch_bounds__(T > 32 ? T : 256, rms_ctas<NV>() * (T == 128 ?
   const int t = threadIdx.x % T, g = threadIdx.x / T;
   const float inv_c = 1.f / (float)C;
   const int groups = (C + TRI_CKPT_GROUP - 1) / TRI_CKPT_GROUP;
+  // rows first + stride i; sh values before the first one's first lies a boundary
+  const int cls = STEP ? (int)(blockIdx.x % VEC) : 0;
+  const int64_t stride = STEP ? VEC : 1, first = cls, rows = (M - first + stride - 1) / stride;
+  const int64_t cta = STEP ? blockIdx.x / VEC : blockIdx.x, ctas = STEP ? gridDim.x / VEC : gridDim.x;
+  const int sh = STEP ? (int)((reinterpret_cast<uintptr_t>(y + first * C) & 15) / sizeof(XT)) : 0;
+  if constexpr (STEP) {
+    for (int c = threadIdx.x; c < T * NV * VEC; c += NT)
+      weights[c] = a.gamma && (unsigned)(c - sh) < (unsigned)C ? __ldg(a.gamma + c - sh) : 1.f;
+    __syncthreads();
+  }
+  auto fetch = [&](const XT *p, int64_t ld, int64_t i, int v, const Span &s) {
+    const int c = (v * T + t) * VEC - sh;
+    if (i >= rows) return make_uint4(0u, 0u, 0u, 0u);
+    if constexpr (STEP)
+      return chunk_load_in_step<XT>(p + (first + stride * i) * ld, c, C, s);
+    else
+      return chunk_load<XT, AL>(p + i * ld, c, C, s);
+  };
+  auto put = [&](XT *p, int64_t i, int v, const uint4 &w) {
+    const int c = (v * T + t) * VEC - sh;
+    if (i >= rows) return;
+    if constexpr (STEP)
+      chunk_store_in_step<XT>(p + (first + stride * i) * C, c, C, w);
+    else
+      chunk_store<XT, AL>(p + i * C, c, C, w);
+  };
   // (every thread of a warp, and of a CTA that holds a row, makes the same number of iterations:
   // rows past the last one are zeros that are not written)
-  for (int64_t m0 = (int64_t)blockIdx.x * RPC * U; m0 < M; m0 += (int64_t)gridDim.x * RPC * U) {
+  for (int64_t m0 = cta * RPC * U; m0 < rows; m0 += ctas * RPC * U) {
     Pairs<XT> f[U][NV];
     uint4 val[U][NV];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t m = m0 + u * RPC + g;
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int v = 0; v < NV; ++v)
-        val[u][v] = m < M ? chunk_load<XT, AL>(x + m * a.ldx, (v * T + t) * VEC, C, span) : make_uint4(0u, 0u, 0u, 0u);
-    }
+      for (int v = 0; v < NV; ++v) val[u][v] = fetch(x, a.ldx, m0 + u * RPC + g, v, span);
     if (res) {  // (uniform: a kernel argument)
       uint4 more[U][NV];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int64_t m = m0 + u * RPC + g;
+      for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int v = 0; v < NV; ++v)
-          more[u][v] = m < M ? chunk_load<XT, AL>(res + m * a.ldres, (v * T + t) * VEC, C, span_res) : make_uint4(0u, 0u, 0u, 0u);
-      }
+        for (int v = 0; v < NV; ++v) more[u][v] = fetch(res, a.ldres, m0 + u * RPC + g, v, span_res);
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int64_t m = m0 + u * RPC + g;
+      for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
           Pairs<XT> o;
@@ -78,9 +101,8 @@ __global__ void __launch_bounds__(T > 32 ? T : 256, rms_ctas<NV>() * (T == 128 ?
 #pragma unroll
           for (int j = 0; j < P; ++j) f[u][v].v[j] = __fadd2_rn(f[u][v].v[j], o.v[j]);
           val[u][v] = chunk_pack(f[u][v]);  // (the norm is that of the rounded sum, which the backward pass reads)
-          if (m < M) chunk_store<XT, AL>(r + m * C, (v * T + t) * VEC, C, val[u][v]);
+          put(r, m0 + u * RPC + g, v, val[u][v]);
         }
-      }
     }
     float q[U];
 #pragma unroll
@@ -88,6 +110,7 @@ __global__ void __launch_bounds__(T > 32 ? T : 256, rms_ctas<NV>() * (T == 128 ?
       float2 s = make_float2(0.f, 0.f);
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
+        if constexpr (STEP) in_row<XT>(val[u][v], (v * T + t) * VEC - sh, C);  // (what was loaded there is a neighbour's)
         chunk_unpack(val[u][v], f[u][v]);
 #pragma unroll
         for (int j = 0; j < P; ++j) s = __ffma2_rn(f[u][v].v[j], f[u][v].v[j], s);
@@ -97,24 +120,32 @@ __global__ void __launch_bounds__(T > 32 ? T : 256, rms_ctas<NV>() * (T == 128 ?
     row_sum(q);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t m = m0 + u * RPC + g;
+      const int64_t i = m0 + u * RPC + g;
       q[u] = rsqrtf(fmaf(q[u], inv_c, a.eps));
-      if (m < M && t == 0) a.rstd[m] = q[u];
+      if (i < rows && t == 0) a.rstd[first + stride * i] = q[u];
     }
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int c = (v * T + t) * VEC;
       Pairs<XT> gm;
-      row_weights<XT, AL>(a.gamma, c, C, 1.f, gm);
+      if constexpr (STEP) {
+#pragma unroll
+        for (int j = 0; j < P; j += 2) {
+          const float4 w = *reinterpret_cast<const float4 *>(weights + (v * T + t) * VEC + 2 * j);
+          gm.v[j] = make_float2(w.x, w.y);
+          gm.v[j + 1] = make_float2(w.z, w.w);
+        }
+      } else {
+        row_weights<XT, AL>(a.gamma, (v * T + t) * VEC, C, 1.f, gm);
+      }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int64_t m = m0 + u * RPC + g;
         const float2 r2 = make_float2(q[u], q[u]);
 #pragma unroll
         for (int j = 0; j < P; ++j) f[u][v].v[j] = __fmul2_rn(__fmul2_rn(f[u][v].v[j], r2), gm.v[j]);
-        if (y && m < M) chunk_store<XT, AL>(y + m * C, c, C, chunk_pack(f[u][v]));
+        if (y) put(y, m0 + u * RPC + g, v, chunk_pack(f[u][v]));
       }
     }
+    if constexpr (STEP) continue;
     if (!a.q8) continue;
     uint32_t top[U * NV];
     float sc[U * NV], inv[U * NV];
@@ -156,18 +187,31 @@ cudaError_t launch_rms_fwd(const tri_rms_shape &s, const void *x, const void *re
   const bool al = s.C % VEC == 0 && ldx % VEC == 0 && (!res || ldres % VEC == 0) && (at & 15u) == 0 &&
                   (reinterpret_cast<uintptr_t>(q8) & (VEC - 1)) == 0;
   const RmsFwdArgs a{ldx, ldres, s.M, s.C, s.eps, gamma, rstd, s8, q8};
-  const int geo = norm_fwd_geometry((s.C + VEC - 1) / VEC);
+  // (in step: all tensors' rows equally far from a boundary)
+  auto off = [&](const void *p) { return p ? ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(y)) & 15u) : 0u; };
+  const int chunks = (s.C + VEC - 1) / VEC, in_step = step_chunks(s.C, VEC);
+  const bool step = !al && !q8 && ldx % VEC == s.C % VEC && (!res || ldres % VEC == s.C % VEC) && !off(x) && !off(res) && !off(r) &&
+                    in_step * VEC <= TRI_NORM_MAX_C && s.M >= 2 * VEC;
+  const int geo = norm_fwd_geometry(step ? in_step : chunks);
+#define LAUNCH_ROWS(T, NV, ROWS)                                                                                         \
+  rms_fwd_kernel<XT, T, NV, ROWS><<<grid, NT, 0, st>>>(a, static_cast<const XT *>(x), static_cast<const XT *>(res),        \
+                                                       static_cast<XT *>(r), static_cast<XT *>(y))
 #define LAUNCH(T, NV, AL)                                                                                               \
   {                                                                                                                     \
     if constexpr (T * NV * VEC <= TRI_NORM_MAX_C) {                                                                     \
       constexpr int NT = T > 32 ? T : 256, per = NT / T * rms_rows<NV>();                                               \
-      const int grid = (int)std::min<int64_t>((s.M + per - 1) / per, 152 * 32);                                         \
-      rms_fwd_kernel<XT, T, NV, AL><<<grid, NT, 0, st>>>(a, static_cast<const XT *>(x), static_cast<const XT *>(res),   \
-                                                         static_cast<XT *>(r), static_cast<XT *>(y));                   \
+      const int64_t rows = step ? (s.M + VEC - 1) / VEC : s.M;                                                          \
+      int grid = (int)std::min<int64_t>((rows + per - 1) / per, step ? 152 * 32 / VEC : 152 * 32);                      \
+      if (step) grid *= VEC;                                                                                            \
+      if (AL && step)                                                                                                   \
+        LAUNCH_ROWS(T, NV, (AL ? kRowsInStep : kAnyRows));                                                              \
+      else                                                                                                              \
+        LAUNCH_ROWS(T, NV, (AL ? kAlignedRows : kAnyRows));                                                             \
     }                                                                                                                   \
   }
-  NORM_FWD_DISPATCH(geo, al, LAUNCH);
+  NORM_FWD_DISPATCH(geo, (al || step), LAUNCH);
 #undef LAUNCH
+#undef LAUNCH_ROWS
   return cudaGetLastError();
 }
 

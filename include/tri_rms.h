@@ -27,7 +27,7 @@
  * nothing (TRI_ATTN_ERR_CUDA from a launch itself excepted). Calls are asynchronous on `stream`
  * (a cudaStream_t, NULL = the legacy default stream), allocate nothing, keep no state between
  * calls and may be captured into a graph. Every reduction runs in an order fixed by the shape, the
- * type and the alignment: the same call gives the same bits.
+ * type, the alignment and what the call asks for: the same call gives the same bits.
  */
 #ifndef TRI_RMS_H
 #define TRI_RMS_H

@@ -89,7 +89,8 @@ def test_forward_and_backward(M, C, dtype):
         only = tb.rms_forward(x, gamma, residual, eight_bits="only")
         assert only.y is None and torch.equal(only.y8.q8, got.y8.q8) and torch.equal(only.y8.scale, got.y8.scale)
         plain = tb.rms_forward(x, gamma, residual)
-        assert plain.y8 is None and torch.equal(plain.y, got.y) and torch.equal(plain.rstd, got.rstd)
+        assert plain.y8 is None
+        _check_forward(x, residual, gamma, 1e-5, plain)  # (rows of odd width without the 8-bit output are added in another order)
         r = x if residual is None else got.r
         _check_backward(r, gamma, got.rstd, dy, past, tb.rms_backward(r, gamma, got.rstd, dy, past))
 
