@@ -38,6 +38,8 @@ struct RelArgs {
   uint16_t *bias;
   const uint16_t *dbias;
   float *part;
+  uint8_t *index;       // the rows as bytes, and a copy's pitch
+  int64_t index_pitch;  // (even; a multiple of 16)
   int32_t starts[TRI_RELPOS_MAX_K];
 };
 
@@ -169,15 +171,39 @@ __global__ void __launch_bounds__(kFwdThreads) relpos_fwd_kernel(const __grid_co
   }
 }
 
+// Which row of the table each value of a sequence's plane belongs to, a byte each, for the heads that share the positions: two
+// copies, the second one a place further on, so that a pair's bytes lie at an even address wherever the head's plane begins.
+template <bool kNear>
+__global__ void __launch_bounds__(kFwdThreads) relpos_rows_kernel(const __grid_constant__ RelArgs a) {
+  extern __shared__ uint8_t row_by[];  // kNear: by distance
+  const int b = blockIdx.y;
+  allow_next_kernel();
+  if (kNear) {
+    for (int x = threadIdx.x; x < 2 * a.L + 1; x += kFwdThreads) row_by[x] = (uint8_t)row_of(a, x - a.L);
+    __syncthreads();
+  }
+  uint8_t *first = a.index + (int64_t)b * 2 * a.index_pitch, *second = first + a.index_pitch + 1;
+  for (int64_t e = (int64_t)blockIdx.x * kFwdThreads + threadIdx.x; e < a.plane; e += (int64_t)gridDim.x * kFwdThreads) {
+    const int d = difference<true>(a, b, (int)e);
+    const uint8_t r = kNear ? row_by[min(max(d, -a.L), a.L) + a.L] : (uint8_t)row_of(a, d);
+    first[e] = r;
+    second[e] = r;
+  }
+}
+
 // part[bh][piece][row]: a CTA's sums.
-template <bool kNear, bool kPos>
+enum { kSearch, kLookUp, kIndex };  // how a value's row is found: among the starts, by its distance, from relpos_rows_kernel's bytes
+
+template <int HOW, bool kPos>
 __global__ void __launch_bounds__(kBwdThreads) relpos_bwd_kernel(const __grid_constant__ RelArgs a) {
   extern __shared__ float sums[];  // [warp][row][33], then (kNear) where a distance's row begins
+  constexpr bool kNear = HOW == kLookUp;
   constexpr int W = kBwdThreads / 32;
   uint16_t *row_at = reinterpret_cast<uint16_t *>(sums + W * a.rows * 33);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int bh = blockIdx.y + gridDim.y * blockIdx.z, b = bh / a.H;
   if (b >= a.B) return;
+  if (HOW == kIndex) wait_previous_kernel();
   allow_next_kernel();
   for (int x = threadIdx.x; x < W * a.rows * 33; x += kBwdThreads) sums[x] = 0.f;
   if (kNear)
@@ -188,6 +214,7 @@ __global__ void __launch_bounds__(kBwdThreads) relpos_bwd_kernel(const __grid_co
   const int64_t plane0 = bh * a.plane;
   const int k1 = min((blockIdx.x + 1) * a.piece, a.units);
   float behind = 0.f, ahead = 0.f;  // d <= -L, d >= L
+  const uint32_t far_ahead = 257u * row_of(a, 0x7fffffff), far_behind = 257u * row_of(a, -0x7fffffff);  // (kIndex: both of a pair)
   auto inner = [&](int k) { return unit_start(plane0, k) >= 0 && unit_start(plane0, k) + kUnit <= a.plane; };
   auto load = [&](int k, uint32_t (&g)[kPairs]) {  // (a unit ahead: a warp has 1 KB on its way, 24 warps of an SM alone too little)
     if (k >= k1 || !inner(k)) return;
@@ -205,20 +232,41 @@ __global__ void __launch_bounds__(kBwdThreads) relpos_bwd_kernel(const __grid_co
     load(k + W, next);
     if (!inner(k)) {  // a plane's ends, value by value
       for (int e = u0 + lane + (u0 + lane < 0 ? 32 : 0); e < min(u0 + kUnit, (int)a.plane); e += 32)
-        add(difference<kPos>(a, b, e), bf16_to_f32(a.dbias[plane0 + e]));
+        if constexpr (HOW == kIndex)
+          mine[a.index[(int64_t)b * 2 * a.index_pitch + e] * 33] += bf16_to_f32(a.dbias[plane0 + e]);
+        else
+          add(difference<kPos>(a, b, e), bf16_to_f32(a.dbias[plane0 + e]));
       continue;
     }
-    int d[kPairs][2];
-    differences<kPos>(a, b, u0 + 2 * lane, d);
+    if constexpr (HOW == kIndex) {
+      const uint8_t *index = a.index + (int64_t)b * 2 * a.index_pitch + (plane0 & 1) * (a.index_pitch + 1) + u0 + 2 * lane;
+      uint32_t r[kPairs];
 #pragma unroll
-    for (int p = 0; p < kPairs; ++p) {
-      const float g0 = __uint_as_float(g[p] << 16), g1 = __uint_as_float(g[p] & 0xffff0000u);
-      const bool up = min(d[p][0], d[p][1]) >= a.L, down = max(d[p][0], d[p][1]) <= -a.L;
-      if (up) ahead += g0 + g1;
-      if (down) behind += g0 + g1;
-      if (!up && !down) {
-        add(d[p][0], g0);
-        add(d[p][1], g1);
+      for (int p = 0; p < kPairs; ++p) r[p] = __ldg(reinterpret_cast<const uint16_t *>(index + 64 * p));
+#pragma unroll
+      for (int p = 0; p < kPairs; ++p) {
+        const float g0 = __uint_as_float(g[p] << 16), g1 = __uint_as_float(g[p] & 0xffff0000u);
+        const bool up = r[p] == far_ahead, down = !up && r[p] == far_behind;
+        if (up) ahead += g0 + g1;
+        if (down) behind += g0 + g1;
+        if (!up && !down) {
+          mine[(r[p] & 255u) * 33] += g0;
+          mine[(r[p] >> 8) * 33] += g1;
+        }
+      }
+    } else {
+      int d[kPairs][2];
+      differences<kPos>(a, b, u0 + 2 * lane, d);
+#pragma unroll
+      for (int p = 0; p < kPairs; ++p) {
+        const float g0 = __uint_as_float(g[p] << 16), g1 = __uint_as_float(g[p] & 0xffff0000u);
+        const bool up = min(d[p][0], d[p][1]) >= a.L, down = max(d[p][0], d[p][1]) <= -a.L;
+        if (up) ahead += g0 + g1;
+        if (down) behind += g0 + g1;
+        if (!up && !down) {
+          add(d[p][0], g0);
+          add(d[p][1], g1);
+        }
       }
     }
   }
@@ -294,22 +342,45 @@ void set_starts(RelArgs &a, const int32_t *starts) {
   std::copy(starts, starts + a.K, a.starts);
   a.L = std::max(starts[a.K - 1], 1);  // (0 is on neither side)
 }
+// Eight heads and more with positions: the rows are worked out once for all of them (2 x 16 heads of 1003 x 1003: 50 us
+// head by head).
+constexpr int kIndexHeads = 8;
+size_t part_bytes(const RelArgs &a) { return (sizeof(float) * (size_t)a.B * a.H * a.pieces * a.rows + 15) / 16 * 16; }
+int64_t index_pitch_of(const RelArgs &a) { return (a.plane + 1 + 15) / 16 * 16; }
+size_t bwd_bytes(const RelArgs &a) { return part_bytes(a) + (a.H >= kIndexHeads ? (size_t)a.B * 2 * index_pitch_of(a) + 16 : 0); }
+
 dim3 grid_of(const RelArgs &a) {
   const unsigned planes = (unsigned)a.B * a.H, y = std::min(planes, 32768u);
   return dim3(a.pieces, y, (planes + y - 1) / y);
 }
 
-template <bool kNear, bool kPos>
-cudaError_t launch_relpos_bwd(const RelArgs &a, size_t smem, cudaStream_t st) {
+template <int HOW, bool kPos>
+cudaError_t relpos_bwd_ready() {
   static DeviceOnce ready;  // (more than 48 KB of shared memory)
   int dev = 0;
   cudaError_t e = current_device(&dev);
   if (e == cudaSuccess && !ready.done(dev)) {
-    e = cudaFuncSetAttribute(relpos_bwd_kernel<kNear, kPos>, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+    e = cudaFuncSetAttribute(relpos_bwd_kernel<HOW, kPos>, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
     if (e == cudaSuccess) ready.mark(dev);
   }
+  return e;
+}
+template <int HOW, bool kPos>
+cudaError_t launch_relpos_bwd(const RelArgs &a, cudaStream_t st) {
+  const bool near = a.L <= kLookup;
+  const size_t smem = sizeof(float) * (kBwdThreads / 32) * a.rows * 33 + (HOW == kLookUp ? 2 * (2 * a.L + 1) : 0);
+  cudaError_t e = relpos_bwd_ready<HOW, kPos>();
   if (e != cudaSuccess) return e;
-  relpos_bwd_kernel<kNear, kPos><<<grid_of(a), kBwdThreads, smem, st>>>(a);
+  if constexpr (HOW == kIndex) {
+    const dim3 grid((unsigned)std::min<int64_t>((a.plane + kFwdThreads - 1) / kFwdThreads, 152 * 8 / std::min(a.B, 8)), a.B);
+    if (near)
+      relpos_rows_kernel<true><<<grid, kFwdThreads, 2 * a.L + 1, st>>>(a);
+    else
+      relpos_rows_kernel<false><<<grid, kFwdThreads, 0, st>>>(a);
+    e = cudaGetLastError();
+    return e == cudaSuccess ? launch_after(relpos_bwd_kernel<HOW, kPos>, grid_of(a), dim3(kBwdThreads), smem, st, a) : e;
+  }
+  relpos_bwd_kernel<HOW, kPos><<<grid_of(a), kBwdThreads, smem, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -353,7 +424,7 @@ int tri_relpos_fwd(tri_relpos_shape shape, const int32_t *starts, const float *t
 size_t tri_relpos_bwd_workspace_size(tri_relpos_shape shape) {
   if (relpos_check(shape)) return 0;
   const RelArgs a = rel_args(shape, kBwdThreads / 32, kBwdCtas);
-  return sizeof(float) * (size_t)a.B * a.H * a.pieces * a.rows;
+  return bwd_bytes(a);
 }
 
 int tri_relpos_bwd(tri_relpos_shape shape, const int32_t *starts, const int32_t *positions, const int32_t *key_positions,
@@ -373,13 +444,15 @@ int tri_relpos_bwd(tri_relpos_shape shape, const int32_t *starts, const int32_t 
   a.posk = key_positions;
   a.dbias = reinterpret_cast<const uint16_t *>(dbias);
   a.part = static_cast<float *>(workspace);
+  a.index = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(workspace) + part_bytes(a) + 15) & ~uintptr_t(15));
+  a.index_pitch = index_pitch_of(a);
   const bool near = a.L <= kLookup;
-  const size_t smem = sizeof(float) * (kBwdThreads / 32) * a.rows * 33 + (near ? 2 * (2 * a.L + 1) : 0);
   const auto st = static_cast<cudaStream_t>(stream);
-  cudaError_t e = near && positions ? launch_relpos_bwd<true, true>(a, smem, st)
-                  : near            ? launch_relpos_bwd<true, false>(a, smem, st)
-                  : positions       ? launch_relpos_bwd<false, true>(a, smem, st)
-                                    : launch_relpos_bwd<false, false>(a, smem, st);
+  cudaError_t e = positions && a.H >= kIndexHeads && a.B <= 65535 ? launch_relpos_bwd<kIndex, false>(a, st)
+                  : near && positions                             ? launch_relpos_bwd<kLookUp, true>(a, st)
+                  : near                                          ? launch_relpos_bwd<kLookUp, false>(a, st)
+                  : positions                                     ? launch_relpos_bwd<kSearch, true>(a, st)
+                                                                  : launch_relpos_bwd<kSearch, false>(a, st);
   if (e == cudaSuccess)
     e = launch_after(relpos_reduce_kernel, dim3((a.rows * a.H + 7) / 8), dim3(256), 0, st, a.part, a.B, a.H, a.pieces, a.rows, dtable);
   return e == cudaSuccess ? TRI_ATTN_OK : TRI_ATTN_ERR_CUDA;

@@ -21,7 +21,9 @@ CASES = [  # B, H, Nq, Nk, starts, two-sided
     (2, 2, 100, 33, LOG16, False), (1, 2, 129, 131, tuple(range(33)), True), (1, 3, 1, 1003, LOG16, True), (3, 1, 1003, 1, LOG16, False),
     (1, 16, 384, 384, LOG16, True), (2, 2, 300, 301, (0, 5, 9), True), (1, 2, 200, 6000, (0, 1, 50, 4096), True),
     (1, 2, 200, 6000, (0, 1, 50, 4097), True), (1, 1, 50, 9000, (0, 3, 5000, 8000), False), (1, 2, 64, 64, tuple(range(128)), True),
-    (1, 1, 40, 5000, tuple(40 * k for k in range(128)), True), (1, 2, 40, 40, (0,), False), (1, 2, 40, 40, (0,), True)]
+    (1, 1, 40, 5000, tuple(40 * k for k in range(128)), True), (1, 2, 40, 40, (0,), False), (1, 2, 40, 40, (0,), True),
+    (2, 9, 61, 63, LOG16, True), (3, 8, 50, 70, LOG16, False), (1, 10, 33, 31, (0,), False), (1, 8, 100, 101, (0, 2), True),
+    (1, 8, 30, 4000, tuple(40 * k for k in range(128)), True)]
 
 
 def rows_of(starts, two, q, k):
