@@ -268,8 +268,7 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t at) {
 }
 
 // A warp's piece of 32 rows of PARTS x 16 bytes on its way between the threads' rows and memory's: in shared memory part c of
-// row r lies at c ^ (r PARTS / 8 mod PARTS) of the row's place, which keeps both directions free of bank conflicts. (By
-// TMA a row of 64 bytes took ten cycles: 147456 x 512 features 87 us.)
+// row r lies at c ^ (r PARTS / 8 mod PARTS) of the row's place, which keeps both directions free of bank conflicts.
 template <int PARTS>
 struct Piece {
   static_assert(PARTS == 2 || PARTS == 4 || PARTS == 8, "parts");

@@ -4,11 +4,11 @@
 // A pair of CTAs takes 256 rows and goes over the features 64 at a time: the products of x with 64 rows of Wg (the first
 // CTA's) and of Wu (the second's) come side by side in TMEM; sixteen warps of each CTA make h of them and write it back, as
 // BF16, over the gate's columns, from where it is the first operand of the product with Wd's 64 columns, which adds up in
-// TMEM over all features. NS such blocks are in flight, so that products and activations overlap. Two warps issue, one the
-// first products and one the second: a wait costs an issuing warp 200 to 300 cycles even where nothing is to be waited for, as long as four
-// of a block's twelve MMAs, and one warp with all waits took 1780 cycles a block (65 us for 147456 x 128 x 512). Weights
-// stream through a ring from L2, which holds them. With h in memory the features' traffic bounds the block (131 us; 302 MB
-// written and read again).
+// TMEM over all features. NS such blocks are in flight, so that products and activations overlap. Three warps issue, two
+// the first products in turn and one the second: a wait costs an issuing warp some 180 cycles even where nothing is to be
+// waited for, and one warp with all waits took 1780 cycles a block, twice its twelve MMAs (65 us for 147456 x 128 x 512;
+// two warps 57). Weights stream through a ring from L2, which holds them. With h in memory the features' traffic bounds the
+// block (131 us; 302 MB written and read again).
 #include "ffn.cuh"
 
 namespace triattn {
@@ -52,7 +52,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BCfg<CB>::NTHREADS, 
   volatile uint32_t *misc = reinterpret_cast<volatile uint32_t *>(sm + C::OFF_MISC);
   const Abort ab{reinterpret_cast<volatile int *>(misc + 1), a.status};
   if (threadIdx.x == 0) {
-    for (int k = 0; k < C::NBAR; ++k) mbar_init(bar(k), k >= C::B_H && k < C::B_OF ? C::EPI_WARPS : k == C::B_OE ? 2 * C::EPI_WARPS : k == C::B_DONE ? 2 : 1);  // (a block has half of both CTAs' warps)
+    for (int k = 0; k < C::NBAR; ++k) mbar_init(bar(k), k >= C::B_H && k < C::B_OF ? C::EPI_WARPS : k == C::B_OE ? 2 * C::EPI_WARPS : k == C::B_DONE ? 3 : k >= C::B_XE && k < C::B_WF ? 2 : 1);  // (a block has half of both CTAs' warps)
     misc[1] = 0;
     fence_barrier_init();
   }
@@ -106,14 +106,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BCfg<CB>::NTHREADS, 
       for (int x = max(0, xs - C::XB); x < xs; ++x) drain_bar(bar(C::B_XF + x % C::XB), (x / C::XB) & 1);
       for (int x = max(0, ws - C::NW); x < ws; ++x) drain_bar(bar(C::B_WF + x % C::NW), (x / C::NW) & 1);
     }
-  } else if (warp == 1 && rank == 0) {
-    // ------------------------------------------------------------ issues x Wg^T and x Wu^T, block by block
+  } else if ((warp == 1 || warp == 3) && rank == 0) {
+    // ------------------------------------------------------------ issue x Wg^T and x Wu^T, every second block each
     constexpr uint32_t idesc = idesc_f16(kRows, 128, true, true, false, false);
-    bool ok = true;
-    int f = 0, t = 0;
-    for (int n = 0; n < total; ++n) {
+    bool ok = true, here = false;
+    int t = 0, f = warp == 1 ? 0 : 1;  // tile and feature block of block n; whether the tile's x is known to be there
+    auto arrive_x = [&]() {
+      if (!here) ok = wait_bar_warp(bar(C::B_XF + t % C::XB), (t / C::XB) & 1, ab);
+      here = true;
+    };
+    // Both warps say of every tile that they are done with it, and not before it has come, even where they have no block of it:
+    // said earlier, it would count for the tile that had the place before.
+    auto leave_x = [&]() {
+      arrive_x();
+      if (ok) pair_commit_e(bar(C::B_XE + t % C::XB));
+      ++t;
+      here = false;
+    };
+    for (int n = f; n < total && ok; n += 2, f += 2) {
+      for (; f >= a.blocks && ok; f -= a.blocks) leave_x();
+      if (!ok) break;
       const int b = n % C::NS, s = n % C::NW, xs = t % C::XB, p = n - C::NS;
-      if (f == 0) ok = wait_bar_warp(bar(C::B_XF + xs), (t / C::XB) & 1, ab);
+      arrive_x();
       // (the block that had the buffer is done when its weights' place is free again)
       ok = ok && (p < 0 || wait_bar_warp(bar(C::B_WE + p % C::NW), (p / C::NW) & 1, ab)) && wait_bar_warp(bar(C::B_WF + s), (n / C::NW) & 1, ab);
       if (!ok) break;
@@ -123,12 +137,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BCfg<CB>::NTHREADS, 
       for (int k = 0; k < a.kc; ++k)
         pair_mma_x4_e(tb + 128 * b, dx + (uint64_t)(k * (kHalf * 128 >> 4)), 2, dw + (uint64_t)(k * (kBox >> 4)), 2, idesc, k > 0 ? 1u : 0u);
       pair_commit_e(bar(C::B_S + b));
-      if (++f == a.blocks) {
-        pair_commit_e(bar(C::B_XE + xs));
-        f = 0;
-        ++t;
-      }
     }
+    while (ok && t < mine) leave_x();
     pair_commit_e(bar(C::B_DONE));
     if (lane == 0) drain_bar(bar(C::B_DONE), 0);
     __syncwarp();
@@ -193,6 +203,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BCfg<CB>::NTHREADS, 
         f -= a.blocks;
         ++t;
       }
+      // (the tile before is read out before a block that is not its tile's first one, whose products it would hold up, and
+      // after one that is, while which its last products run)
+      for (; f > 0 && stored < t && ok; ++stored) ok = store_tile(stored);
+      if (!ok) break;
       const int b = n % C::NS, m = row_of_tile(t);
       ok = wait_bar_warp(bar(C::B_S + b), (n / C::NS) & 1, ab);
       if (!ok) break;
@@ -222,7 +236,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BCfg<CB>::NTHREADS, 
         }
         __syncwarp();
       }
-      for (; stored < t && ok; ++stored) ok = store_tile(stored);  // (its last products ran during this block's first ones)
+      for (; stored < t && ok; ++stored) ok = store_tile(stored);
     }
     for (; stored < mine && ok; ++stored) ok = store_tile(stored);
   }

@@ -25,7 +25,7 @@ SIZES = [(1, 8, 8), (1, 64, 128), (7, 72, 200), (128, 64, 64), (129, 128, 512), 
          (1000, 264, 264), (4001, 392, 1032), (9, 2048, 8192), (20000, 128, 512), (64, 4096, 520),
          (19500, 64, 200), (39999, 200, 264), (60001, 256, 64), (19457, 8, 8), (50000, 136, 328), (80000, 128, 64),
          (2, 1000, 3000), (8, 4096, 1032), (15, 264, 72), (16, 2048, 520), (17, 72, 4104), (31, 520, 264), (32, 1032, 2048), (33, 1032, 2048),
-         (10000, 1032, 2056)]
+         (10000, 1032, 2056), (150000, 72, 64), (150001, 128, 48), (100000, 200, 40), (120000, 128, 72), (99999, 256, 136)]
 
 
 def normal(gen, *shape, std=1.0):
