@@ -380,4 +380,7 @@ def clip_grad_norm_(parameters, max_norm):
     """Clips the gradients of the parameters (those that have one) in place to the 2-norm max_norm of all of them together
     and returns their norm before, an FP32 number on the device."""
     parameters = [parameters] if isinstance(parameters, torch.Tensor) else list(parameters)
-    return tb.clip_gradients([p.grad for p in parameters if p.grad is not None], max_norm)
+    grads = [p.grad for p in parameters if p.grad is not None]
+    norm = tb.clip_gradients(grads, max_norm)
+    torch.autograd.graph.increment_version(grads)  # (written where autograd does not see it)
+    return norm

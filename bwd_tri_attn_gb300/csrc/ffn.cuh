@@ -8,6 +8,13 @@
 // Tiles of whole waves go to the pairs in turn. The rest is divided evenly over the pairs by 64-channel blocks: a
 // pair's share of a tile that it does not have alone goes to the workspace in FP32, and a second kernel adds the
 // shares in the order of the channels (no atomics: the same bits every time) and finishes the tile.
+//
+// The tensor cores bound the large products. 8192 rows of 4096 channels and 16384 features, forward: 1694 us, 1.95 PFLOP/s
+// (1926 us in a loop of seconds, at the clock that the power limit leaves: 1.71); 8192 of 2048 and 8192, backward: 990 us, 1.67
+// PFLOP/s. There dx has the tensor cores 90 % active, the weights' gradients 86 %, the features' gradients 53 %: their five
+// tensors of M F values, 0.67 GB, cross the L2's way to the SMs beside the operands (without products 117 us, without results
+// 145, together 217 to 237). Between kernels 7 us are spent on starting, filling the stages and the last tile's results, which is
+// most of a small call: 4001 rows of 392 and 1032, backward: 51 us for three kernels, 10 at the tensor cores' rate.
 #pragma once
 
 #include <algorithm>

@@ -7,7 +7,9 @@
 // TMEM over all features. NS such blocks are in flight, so that products and activations overlap. Three warps issue, two
 // the first products in turn and one the second: a wait costs an issuing warp some 180 cycles even where nothing is to be
 // waited for, and one warp with all waits took 1780 cycles a block, twice its twelve MMAs (65 us for 147456 x 128 x 512;
-// two warps 57). Weights stream through a ring from L2, which holds them. With h in memory the features' traffic bounds the
+// two warps 57). What bounds it now is a block's way through its buffer, some 4400 cycles for three buffers: first products 550,
+// activation 1600, second products, and four hand-overs in between; all sixteen warps on one block, 16 features each, took as long.
+// The tensor cores are 45 % active. Weights stream through a ring from L2, which holds them. With h in memory the features' traffic bounds the
 // block (131 us; 302 MB written and read again).
 #include "ffn.cuh"
 
@@ -52,7 +54,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BCfg<CB>::NTHREADS, 
   volatile uint32_t *misc = reinterpret_cast<volatile uint32_t *>(sm + C::OFF_MISC);
   const Abort ab{reinterpret_cast<volatile int *>(misc + 1), a.status};
   if (threadIdx.x == 0) {
-    for (int k = 0; k < C::NBAR; ++k) mbar_init(bar(k), k >= C::B_H && k < C::B_OF ? C::EPI_WARPS : k == C::B_OE ? 2 * C::EPI_WARPS : k == C::B_DONE ? 3 : k >= C::B_XE && k < C::B_WF ? 2 : 1);  // (a block has half of both CTAs' warps)
+    for (int k = 0; k < C::NBAR; ++k)  // (a block has half of both CTAs' warps; two warps leave an x, three end)
+      mbar_init(bar(k), k >= C::B_H && k < C::B_OF    ? C::EPI_WARPS
+                        : k == C::B_OE                ? 2 * C::EPI_WARPS
+                        : k == C::B_DONE              ? 3
+                        : k >= C::B_XE && k < C::B_WF ? 2
+                                                      : 1);
     misc[1] = 0;
     fence_barrier_init();
   }
@@ -268,7 +275,18 @@ cudaError_t launch(const tri_ffn_shape &s, const void *x, const void *Wg, const 
     if (e != cudaSuccess) return e;
     ready.mark(dev);
   }
-  BArgs a{(int)s.M, s.C, s.F, s.act, static_cast<uint16_t *>(out), static_cast<uint16_t *>(ka), static_cast<uint16_t *>(ku), ceil_div(s.M, kRows), ceil_div(s.F, 64), ceil_div(s.C, 64), status};
+  BArgs a{};
+  a.M = (int)s.M;
+  a.C = s.C;
+  a.F = s.F;
+  a.act = s.act;
+  a.out = static_cast<uint16_t *>(out);
+  a.ka = static_cast<uint16_t *>(ka);
+  a.ku = static_cast<uint16_t *>(ku);
+  a.tiles = ceil_div(s.M, kRows);
+  a.blocks = ceil_div(s.F, 64);
+  a.kc = ceil_div(s.C, 64);
+  a.status = status;
   return launch_after(block_kernel<CB>, dim3(2 * std::min(pairs, a.tiles)), dim3(C::NTHREADS), C::SMEM_ALLOC, st, mX, mWg, mWu, mWd, a);
 }
 

@@ -1,6 +1,7 @@
 // Gated feed-forward block, backward (include/tri_ffn.h states the formulas): the features' gradient and, from it and
 // the kept a and u, da, du and h in one kernel; then dx as one product over both projections' features; then the three
-// weights' gradients as one launch. ffn.cuh has the kernels.
+// weights' gradients as one launch. ffn.cuh has the kernels and what they measured. (dx and the weights' gradients side by side,
+// the second waiting for the features' gradient alone, took as long as one behind the other.)
 #include "ffn.cuh"
 
 namespace triattn {

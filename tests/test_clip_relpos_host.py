@@ -105,6 +105,15 @@ def test_relpos(tb):
     assert need and relpos(tb, shape(), which=2, ws=need - 1) == -3 and relpos(tb, shape(), which=2, bwd=("workspace",)) == -3
 
 
+def test_relpos_long_planes_are_split(tb):
+    """However many planes there are, a lane (of 128 of a CTA) adds up at most 2^14 values in one FP32 sum: every CTA of a
+    plane has its own row of partial sums in the workspace."""
+    for B, H, Nq, Nk in ((152, 7, 4096, 4096), (1 << 17, 7, 2048, 2048), (1, 1, 46340, 46340), (152, 6, 1 << 16, 32767)):
+        need = tb.tri_relpos_bwd_workspace_size(tb.RelposShape(B, H, Nq, Nk, 4, 1))
+        ctas = need // (4 * 8 * B * H)
+        assert ctas * 128 * (1 << 14) >= Nq * Nk, (B, H, Nq, Nk)
+
+
 def test_relpos_binding(tb):
     t, starts = torch.zeros(8, 2), STARTS
     d = torch.zeros(1, 2, 5, 7, dtype=torch.bfloat16)

@@ -97,6 +97,17 @@ def test_gradients_of_a_step(B, N, C, F, H, d, act, fused, checkpoint):
         assert ((t.grad - 0.5 * g).abs() <= 2.0 ** -19 * g.abs()).all()
 
 
+def test_clipping_shows_as_a_write():
+    """What autograd keeps of a gradient may not be read after it was clipped in place."""
+    w = torch.ones(40, device="cuda", requires_grad=True)
+    other = torch.ones(40, device="cuda", requires_grad=True)
+    w.grad = torch.full((40,), 3.0, device="cuda")
+    y = other * w.grad
+    ag.clip_grad_norm_([w, other], 1.0)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.sum().backward()
+
+
 def test_step_in_a_graph():
     """Forward, backward and clipping captured, replayed on other data."""
     B, N, C, F, H, d = 1, 36, 64, 192, 2, 32
