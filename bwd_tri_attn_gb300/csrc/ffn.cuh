@@ -642,21 +642,26 @@ inline cudaError_t make_matrix_map(CUtensorMap *m, const void *ptr, int64_t inne
 }
 inline int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
-// How many pairs share the tiles that fill no whole wave (0: each goes to one pair), and the time of it all, in units of a
-// 64-channel block of a 256-column tile (0.27 us): sharing costs the joining kernel (3 us) and its traffic at 6.5 TB/s.
+// How many pairs share the tiles that fill no whole wave (0: each goes to one pair), and the time of it all in us: 0.33 for a
+// 64-channel block of 256 columns, 0.25 of 128 (half of the products, three quarters of the loads); `results` for those of a
+// tile as far as the next tile's products do not hide them, and 3 or 1.5 for the last tile's; sharing costs the joining kernel and
+// its traffic at 6.5 TB/s. Over 23 sizes from 64 to 40000 rows it chooses the faster width of each product but for two that
+// are 3 % apart. (20000 rows of 640 and 2560, backward: 391 us in 256 columns, dx in 128 418, the weights' gradients in 128 429; 4001
+// of 392 and 1032: 64 in 256 columns, 50 in 128, 60 with the features' gradients alone in 128.)
 struct Split {
   int pairs;
   double time;
 };
-inline Split split_of(int tiles, int nk, int64_t rows, int bn, int pairs) {
-  const double unit = bn == 256 ? 1.0 : 0.58;  // (a block of 128 columns has half of the products and three quarters of the loads)
+inline Split split_of(int tiles, int nk, int64_t rows, int bn, double results, int pairs) {
+  const bool wide = bn == 256;
+  const double block = wide ? 0.33 : 0.25, one = nk * block + results, last = wide ? 3.0 : 1.5;
   const int tail = tiles % pairs;
-  const double whole = (double)(tiles / pairs) * nk * unit, alone = tail ? nk * unit : 0.0;
+  const double whole = tiles / pairs * one + last, alone = tail ? one : 0.0;
   const int64_t units = (int64_t)tail * nk;
   const int by = (int)std::min<int64_t>(pairs, units / 4);
   if (by <= tail) return {0, whole + alone};
   const double segments = std::min(2 * by, by + tail), bytes = segments * (double)std::min<int64_t>(rows, kRows) * bn * 8;
-  const double shared = ceil_div(units, by) * unit + 12 + bytes / 6.5e12 / 0.27e-6;
+  const double shared = ceil_div(units, by) * block + 4 + bytes / 6.5e6;
   return shared < alone ? Split{by, whole + shared} : Split{0, whole + alone};
 }
 // (what any number of pairs can need)
@@ -677,7 +682,8 @@ struct Product {
   static int tiles(const Args &io, int i) { return ceil_div(io.rows[i], kRows) * ceil_div(io.cols[i], Cfg<OP, BN>::COLS); }
   static Split split(const Args &io, int pairs, int *count) {
     *count = OP == kDW ? 2 * tiles(io, 0) + tiles(io, 1) : tiles(io, 0);
-    return split_of(*count, io.nk, std::max(io.rows[0], io.rows[1]), BN, pairs);
+    const double results = OP != kDHidden ? 0.0 : BN == 256 ? 7.0 : 2.5;  // (five tensors; alone they take 8.7 and 4.4 us)
+    return split_of(*count, io.nk, std::max(io.rows[0], io.rows[1]), BN, results, pairs);
   }
   cudaError_t plan(const Args &io, const Matrix *A, int nA, const Matrix *B, int nB, int pairs, int dev) {
     using C = Cfg<OP, BN>;
