@@ -9,9 +9,9 @@
 //
 // Backward: the two far rows, to which most elements belong, are summed in registers; the others go to a histogram
 // in shared memory with a column for each lane, so that no two threads add to one number and the order of all sums is fixed.
-// The CTAs' sums are added in order by a second kernel. 2 x 16 heads of 1003 x 1003 with positions: 31 us, of which the rows' bytes
-// (relpos_rows_kernel) 6, the sum of the CTAs' sums 4, and the rest, 64 MB at 3 TB/s, is bound by shared memory: two reads and
-// writes a pair that is not far, one behind the other where both fall to one row.
+// The CTAs' sums are added in order by a second kernel. 2 x 16 heads of 1003 x 1003 with positions: 26 us for 64 MB, of which the
+// rows' bytes (relpos_rows_kernel) and the sum of the CTAs' sums are 8; the rest waits for memory and shared memory in turn, with the
+// six CTAs of an SM that the histograms leave room for (five 29 us; units two ahead, in more registers, 28.6).
 #include <algorithm>
 
 #include "launch.cuh"
@@ -185,12 +185,31 @@ __global__ void __launch_bounds__(kFwdThreads) relpos_rows_kernel(const __grid_c
     for (int x = threadIdx.x; x < 2 * a.L + 1; x += kFwdThreads) row_by[x] = (uint8_t)row_of(a, x - a.L);
     __syncthreads();
   }
-  uint8_t *first = a.index + (int64_t)b * 2 * a.index_pitch, *second = first + a.index_pitch + 1;
-  for (int64_t e = (int64_t)blockIdx.x * kFwdThreads + threadIdx.x; e < a.plane; e += (int64_t)gridDim.x * kFwdThreads) {
-    const int d = difference<true>(a, b, (int)e);
-    const uint8_t r = kNear ? row_by[min(max(d, -a.L), a.L) + a.L] : (uint8_t)row_of(a, d);
-    first[e] = r;
-    second[e] = r;
+  uint8_t *first = a.index + (int64_t)b * 2 * a.index_pitch, *second = first + a.index_pitch;
+  const int *pq = a.posq + (int64_t)b * a.Nq, *pk = a.posk + (int64_t)b * a.Nk;
+  auto row = [&](int i, int j) {
+    const int d = sub_sat(__ldg(pk + j), __ldg(pq + i));
+    return (uint32_t)(kNear ? row_by[min(max(d, -a.L), a.L) + a.L] : (uint8_t)row_of(a, d));
+  };
+  // Four values a thread, a word of each copy; the second copy's begins with the value before. (A copy's room is a multiple of 16
+  // bytes that the plane does not fill: what stands behind the plane belongs to no value.)
+  const int words = (int)((a.plane + 4) / 4);
+  for (int w = blockIdx.x * kFwdThreads + threadIdx.x; w < words; w += gridDim.x * kFwdThreads) {
+    const uint32_t e = 4u * (uint32_t)w;
+    int i = (int)((e ? e - 1 : 0u) / (uint32_t)a.Nk), j = (int)((e ? e - 1 : 0u) - (uint32_t)i * (uint32_t)a.Nk);
+    uint32_t r[5];
+#pragma unroll
+    for (int k = 0; k < 5; ++k) {
+      r[k] = row(i, j);
+      if ((e || k) && i < a.Nq - 1 + (j + 1 < a.Nk)) {  // (on to the next value, as far as there is one; value 0 twice)
+        if (++j == a.Nk) {
+          j = 0;
+          ++i;
+        }
+      }
+    }
+    *reinterpret_cast<uint32_t *>(first + e) = r[1] | r[2] << 8 | r[3] << 16 | r[4] << 24;
+    *reinterpret_cast<uint32_t *>(second + e) = r[0] | r[1] << 8 | r[2] << 16 | r[3] << 24;
   }
 }
 
@@ -206,11 +225,11 @@ __global__ void __launch_bounds__(kBwdThreads) relpos_bwd_kernel(const __grid_co
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int bh = blockIdx.y + gridDim.y * blockIdx.z, b = bh / a.H;
   if (b >= a.B) return;
-  if (HOW == kIndex) wait_previous_kernel();
-  allow_next_kernel();
   for (int x = threadIdx.x; x < W * a.rows * 33; x += kBwdThreads) sums[x] = 0.f;
   if (kNear)
     for (int x = threadIdx.x; x < 2 * a.L + 1; x += kBwdThreads) row_at[x] = (uint16_t)(33 * row_of(a, x - a.L));
+  if (HOW == kIndex) wait_previous_kernel();
+  allow_next_kernel();
   __syncthreads();
   float *mine = sums + warp * a.rows * 33 + lane;
   auto add = [&](int d, float g) { mine[kNear ? row_at[min(max(d, -a.L), a.L) + a.L] : 33 * row_of(a, d)] += g; };
@@ -219,20 +238,29 @@ __global__ void __launch_bounds__(kBwdThreads) relpos_bwd_kernel(const __grid_co
   float behind = 0.f, ahead = 0.f;  // d <= -L, d >= L
   const uint32_t far_ahead = 257u * row_of(a, 0x7fffffff), far_behind = 257u * row_of(a, -0x7fffffff);  // (kIndex: both of a pair)
   auto inner = [&](int k) { return unit_start(plane0, k) >= 0 && unit_start(plane0, k) + kUnit <= a.plane; };
-  auto load = [&](int k, uint32_t (&g)[kPairs]) {  // (a unit ahead: a warp has 1 KB on its way, 24 warps of an SM alone too little)
+  const uint8_t *index = HOW == kIndex ? a.index + (int64_t)b * 2 * a.index_pitch + (plane0 & 1) * (a.index_pitch + 1) + 2 * lane : nullptr;
+  auto load = [&](int k, uint32_t (&g)[kPairs], uint16_t (&r)[kPairs]) {  // (a unit ahead: a warp has 1 KB on its way, 24 warps of an SM alone too little)
     if (k >= k1 || !inner(k)) return;
     const uint32_t *dbias = reinterpret_cast<const uint32_t *>(a.dbias + plane0 + unit_start(plane0, k) + 2 * lane);
 #pragma unroll
     for (int p = 0; p < kPairs; ++p) g[p] = __ldcs(dbias + 32 * p);
+    if constexpr (HOW == kIndex) {
+#pragma unroll
+      for (int p = 0; p < kPairs; ++p) r[p] = __ldg(reinterpret_cast<const uint16_t *>(index + unit_start(plane0, k) + 64 * p));
+    }
   };
   uint32_t next[kPairs];
-  load(blockIdx.x * a.piece + warp, next);
+  uint16_t next_r[kPairs];
+  load(blockIdx.x * a.piece + warp, next, next_r);
   for (int k = blockIdx.x * a.piece + warp; k < k1; k += W) {
     const int u0 = unit_start(plane0, k);
-    uint32_t g[kPairs];
+    uint32_t g[kPairs], r[kPairs];
 #pragma unroll
-    for (int p = 0; p < kPairs; ++p) g[p] = next[p];
-    load(k + W, next);
+    for (int p = 0; p < kPairs; ++p) {
+      g[p] = next[p];
+      if constexpr (HOW == kIndex) r[p] = next_r[p];
+    }
+    load(k + W, next, next_r);
     if (!inner(k)) {  // a plane's ends, value by value
       for (int e = u0 + lane + (u0 + lane < 0 ? 32 : 0); e < min(u0 + kUnit, (int)a.plane); e += 32)
         if constexpr (HOW == kIndex)
@@ -242,10 +270,6 @@ __global__ void __launch_bounds__(kBwdThreads) relpos_bwd_kernel(const __grid_co
       continue;
     }
     if constexpr (HOW == kIndex) {
-      const uint8_t *index = a.index + (int64_t)b * 2 * a.index_pitch + (plane0 & 1) * (a.index_pitch + 1) + u0 + 2 * lane;
-      uint32_t r[kPairs];
-#pragma unroll
-      for (int p = 0; p < kPairs; ++p) r[p] = __ldg(reinterpret_cast<const uint16_t *>(index + 64 * p));
 #pragma unroll
       for (int p = 0; p < kPairs; ++p) {
         const float g0 = __uint_as_float(g[p] << 16), g1 = __uint_as_float(g[p] & 0xffff0000u);
@@ -346,7 +370,7 @@ void set_starts(RelArgs &a, const int32_t *starts) {
   a.L = std::max(starts[a.K - 1], 1);  // (0 is on neither side)
 }
 // Eight heads and more with positions: the rows are worked out once for all of them (2 x 16 heads of 1003 x 1003: 50 us
-// head by head).
+// head by head, 26 so).
 constexpr int kIndexHeads = 8;
 size_t part_bytes(const RelArgs &a) { return (sizeof(float) * (size_t)a.B * a.H * a.pieces * a.rows + 15) / 16 * 16; }
 int64_t index_pitch_of(const RelArgs &a) { return (a.plane + 1 + 15) / 16 * 16; }
@@ -375,7 +399,7 @@ cudaError_t launch_relpos_bwd(const RelArgs &a, cudaStream_t st) {
   cudaError_t e = relpos_bwd_ready<HOW, kPos>();
   if (e != cudaSuccess) return e;
   if constexpr (HOW == kIndex) {
-    const dim3 grid((unsigned)std::min<int64_t>((a.plane + kFwdThreads - 1) / kFwdThreads, 152 * 8 / std::min(a.B, 8)), a.B);
+    const dim3 grid((unsigned)std::min<int64_t>((a.plane / 4 + kFwdThreads) / kFwdThreads, 152 * 8 / std::min(a.B, 8)), a.B);
     if (near)
       relpos_rows_kernel<true><<<grid, kFwdThreads, 2 * a.L + 1, st>>>(a);
     else

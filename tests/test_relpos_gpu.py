@@ -23,7 +23,8 @@ CASES = [  # B, H, Nq, Nk, starts, two-sided
     (1, 2, 200, 6000, (0, 1, 50, 4097), True), (1, 1, 50, 9000, (0, 3, 5000, 8000), False), (1, 2, 64, 64, tuple(range(128)), True),
     (1, 1, 40, 5000, tuple(40 * k for k in range(128)), True), (1, 2, 40, 40, (0,), False), (1, 2, 40, 40, (0,), True),
     (2, 9, 61, 63, LOG16, True), (3, 8, 50, 70, LOG16, False), (1, 10, 33, 31, (0,), False), (1, 8, 100, 101, (0, 2), True),
-    (1, 8, 30, 4000, tuple(40 * k for k in range(128)), True)]
+    (1, 8, 30, 4000, tuple(40 * k for k in range(128)), True), (2, 8, 1, 1, (0, 1), True), (2, 9, 3, 1, LOG16, True),
+    (2, 8, 1, 5, LOG16, False), (3, 8, 2, 3, (0, 2), True), (1, 9, 700, 2, LOG16, True)]
 
 
 def rows_of(starts, two, q, k):
