@@ -57,12 +57,12 @@ struct BwdSplitRows {
 
 // The split of the rows over CTAs, from the shape alone: the CTAs that 152 SMs hold at once (a second,
 // shorter wave of them took as long as the first: 102 against 77 us for 768 x 768 rows of 128),
-// at least two rows for each group of threads that holds a row.
-inline BwdSplitRows split_rows(const tri_norm_shape &s, int geo, int rows_are) {
+// at least two rows for each group of threads that holds a row. `ctas`: of an SM, where a kernel has not bwd_ctas() of them.
+inline BwdSplitRows split_rows(const tri_norm_shape &s, int geo, int rows_are, int ctas = 0) {
   const int T = norm_threads_per_row(geo), RPC = T > 32 ? 1 : 256 / T;
   const int nv = geo == kNormT32x2 || geo == kNormT256x2 || geo == kNormT512x2 ? 2 : geo == kNormT512x4 ? 4 : 1;
   const int classes = rows_are == kRowsInStep ? (s.dtype == TRI_DTYPE_FP32 ? 4 : 8) : 1;
-  const int64_t target = 152 * bwd_ctas(T, nv, rows_are != kAnyRows) / classes, M = (s.M + classes - 1) / classes;
+  const int64_t target = 152 * (ctas ? ctas : bwd_ctas(T, nv, rows_are != kAnyRows)) / classes, M = (s.M + classes - 1) / classes;
   int64_t rpc = (M + target - 1) / target;
   rpc = std::max<int64_t>((rpc + RPC - 1) / RPC * RPC, 2 * RPC);
   const int per_class = (int)((M + rpc - 1) / rpc);

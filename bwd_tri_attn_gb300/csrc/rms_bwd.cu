@@ -4,8 +4,7 @@
 // row's sum from there and adds dy r rstd of its own columns in registers; a second kernel adds the CTAs' partial
 // sums in a fixed order. The next row's loads are in flight meanwhile. Rows that begin anywhere are taken in step where it pays
 // (norm_bwd.cuh). Outside a row r and dy are zeros, so nothing from there reaches a sum. 20011 rows of 1003 FP16 values with dr:
-// 41 us for 160 MB (3.9 TB/s), 5 of them the second kernel; a row's sum stands between its loads and its stores, and registers
-// hold no more than two rows a CTA in flight.
+// 33 us for 160 MB (4.8 TB/s), 5 of them the second kernel; aligned rows of 1024 28 us (5.9 TB/s).
 #include "norm_bwd.cuh"
 #include "tri_rms.h"
 
@@ -15,12 +14,18 @@ int rms_check_shape(const tri_rms_shape &s);
 
 namespace {
 
+// Rows in step of up to 128 chunks: three CTAs an SM with the registers for all of the next rows, dr too, and one way to load a
+// chunk (20011 rows of 1003 FP16 values: 33 us; four CTAs and dr when its row's turn comes 41, with one way 43; three CTAs with
+// two ways 38. Aligned rows of 1024, which are at 5.8 TB/s, take 28 us in four CTAs and 29 in three).
+constexpr bool rms_ahead(int T, int NV, int ROWS) { return T == 128 && NV == 1 && ROWS == kRowsInStep; }
+constexpr int kAheadCtas = 3;
+
 template <typename XT, int T, int NV, int ROWS>
-__global__ void __launch_bounds__(T > 32 ? T : 256, bwd_ctas(T, NV, ROWS != kAnyRows))
+__global__ void __launch_bounds__(T > 32 ? T : 256, rms_ahead(T, NV, ROWS) ? kAheadCtas : bwd_ctas(T, NV, ROWS != kAnyRows))
     rms_bwd_kernel(const XT *__restrict__ r, int64_t ldr, const float *__restrict__ gamma, const float *__restrict__ rstd,
                    const XT *__restrict__ dy, int64_t lddy, const XT *__restrict__ dr, int64_t lddr, int64_t M, int C, int64_t rpc,
                    int per_class, XT *__restrict__ dx, float *__restrict__ part) {
-  constexpr bool AL = ROWS == kAlignedRows, STEP = ROWS == kRowsInStep;
+  constexpr bool AL = ROWS == kAlignedRows, STEP = ROWS == kRowsInStep, AHEAD = rms_ahead(T, NV, ROWS);
   constexpr int VEC = Chunk<XT>::VEC, P = VEC / 2, NT = T > 32 ? T : 256, RPC = NT / T, U = bwd_rows(T, NV, ROWS != kAnyRows);
   __shared__ float red[T > 32 ? 2 * T / 32 : 1][U];
   __shared__ __align__(8) float col[T > 32 ? 2 : NV * T * VEC];
@@ -53,14 +58,21 @@ __global__ void __launch_bounds__(T > 32 ? T : 256, bwd_ctas(T, NV, ROWS != kAny
   const int64_t r0 = (STEP ? (int64_t)blockIdx.x - (int64_t)cls * per_class : (int64_t)blockIdx.x) * rpc, r1 = min(rows, r0 + rpc);
   auto chunk = [&](const XT *row, int c, const Span &span) {
     if constexpr (STEP)
-      return chunk_load_in_step<XT>(row, c, C, span);
+      return chunk_load_in_step<XT, AHEAD>(row, c, C, span);
     else
       return chunk_load<XT, AL>(row, c, C, span);
   };
   // (rows past the chunk are zeros, which add nothing and are not written; their threads still join the sums)
   struct Row {
-    uint4 r[NV], d[NV];
+    uint4 r[NV], d[NV], p[NV];  // (p: dr's)
     float rs;
+  };
+  auto load_past = [&](int64_t i, Row &w) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      w.p[v] = make_uint4(0u, 0u, 0u, 0u);
+      if (i < r1) w.p[v] = chunk(dr + (first + stride * i) * lddr, (v * T + t) * VEC - sh, span_dr);
+    }
   };
   auto load = [&](int64_t i, Row &w) {
     const bool live = i < r1;
@@ -75,23 +87,16 @@ __global__ void __launch_bounds__(T > 32 ? T : 256, bwd_ctas(T, NV, ROWS != kAny
         w.d[v] = chunk(dy + m * lddy, c, span_dy);
       }
     }
+    if (AHEAD && dr) load_past(i, w);  // (uniform: a kernel argument)
   };
   Row row[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) load(r0 + u * RPC + g, row[u]);
   for (int64_t b0 = r0; b0 < r1; b0 += RPC * U) {
     Row next[U];
-    uint4 past[U][NV];
-    if (dr) {  // (uniform: a kernel argument)
+    if (!AHEAD && dr) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int64_t i = b0 + u * RPC + g, m = first + stride * i;
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-          past[u][v] = make_uint4(0u, 0u, 0u, 0u);
-          if (i < r1) past[u][v] = chunk(dr + m * lddr, (v * T + t) * VEC - sh, span_dr);
-        }
-      }
+      for (int u = 0; u < U; ++u) load_past(b0 + u * RPC + g, row[u]);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) load(b0 + (U + u) * RPC + g, next[u]);
@@ -132,7 +137,7 @@ __global__ void __launch_bounds__(T > 32 ? T : 256, bwd_ctas(T, NV, ROWS != kAny
           Pairs<XT> o, p;
 #pragma unroll
           for (int j = 0; j < P; ++j) p.v[j] = make_float2(0.f, 0.f);
-          if (dr) chunk_unpack(past[u][v], p);
+          if (dr) chunk_unpack(row[u].p[v], p);
 #pragma unroll
           for (int j = 0; j < P; ++j) o.v[j] = __ffma2_rn(rs2, __ffma2_rn(rh[u][v].v[j], b2, dz[u][v].v[j]), p.v[j]);
           if constexpr (STEP)
@@ -187,6 +192,10 @@ __global__ void __launch_bounds__(T > 32 ? T : 256, bwd_ctas(T, NV, ROWS != kAny
 
 tri_norm_shape norm_shape(const tri_rms_shape &s) { return tri_norm_shape{s.M, 0, 0, s.C, s.dtype, 0.f}; }
 
+BwdSplitRows rms_split(const tri_rms_shape &s, int geo, int are) {
+  return split_rows(norm_shape(s), geo, are, geo == kNormT128 && are == kRowsInStep ? kAheadCtas : 0);
+}
+
 template <typename XT>
 cudaError_t launch_rms_bwd(const tri_rms_shape &s, const void *r, const float *gamma, const float *rstd, const void *dy, const void *dr,
                            void *dx, float *dgamma, float *part, cudaStream_t st) {
@@ -201,7 +210,7 @@ cudaError_t launch_rms_bwd(const tri_rms_shape &s, const void *r, const float *g
                     (((ra ^ oa) | (da ^ oa) | (pa ^ oa)) & 15u) == 0 && step_pays(s.C, VEC);
   const int are = al ? kAlignedRows : step ? kRowsInStep : kAnyRows;
   const int geo = norm_geometry(are == kRowsInStep ? step_chunks(s.C, VEC) : chunks, are != kAnyRows);
-  const BwdSplitRows sp = split_rows(norm_shape(s), geo, are);
+  const BwdSplitRows sp = rms_split(s, geo, are);
 #define LAUNCH_ROWS(T, NV, ROWS)                                                                                          \
   rms_bwd_kernel<XT, T, NV, ROWS><<<sp.parts, (T > 32 ? T : 256), 0, st>>>(                                               \
       static_cast<const XT *>(r), ldr, gamma, rstd, static_cast<const XT *>(dy), lddy, static_cast<const XT *>(dr), lddr, \
@@ -224,10 +233,9 @@ cudaError_t launch_rms_bwd(const tri_rms_shape &s, const void *r, const float *g
 
 // The largest number of partial sums any alignment of the call's pointers can lead to.
 size_t rms_workspace_bytes(const tri_rms_shape &s) {
-  const tri_norm_shape n = norm_shape(s);
   const int vec = s.dtype == TRI_DTYPE_FP32 ? 4 : 8, chunks = (s.C + vec - 1) / vec;
-  int parts = std::max(split_rows(n, norm_geometry(chunks, true), kAlignedRows).parts, split_rows(n, norm_geometry(chunks, false), kAnyRows).parts);
-  if (step_pays(s.C, vec)) parts = std::max(parts, split_rows(n, norm_geometry(step_chunks(s.C, vec), true), kRowsInStep).parts);
+  int parts = std::max(rms_split(s, norm_geometry(chunks, true), kAlignedRows).parts, rms_split(s, norm_geometry(chunks, false), kAnyRows).parts);
+  if (step_pays(s.C, vec)) parts = std::max(parts, rms_split(s, norm_geometry(step_chunks(s.C, vec), true), kRowsInStep).parts);
   return sizeof(float) * (size_t)parts * s.C;
 }
 

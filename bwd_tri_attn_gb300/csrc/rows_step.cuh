@@ -14,10 +14,12 @@ enum { kAnyRows, kAlignedRows, kRowsInStep };
 // The chunk at row + c (a 16-byte boundary; c may be negative): at a row's ends the
 // whole chunk is read too, where it lies inside the tensor. What lies outside the row becomes zeros when the values are
 // used (dy's by in_row(), x's as xh): done here it would wait for loads that are to be in flight.
-template <typename XT>
+// ONE_WAY: without a way of their own for chunks inside the row, which costs a warp at a row's ends both ways, and saves
+// registers elsewhere.
+template <typename XT, bool ONE_WAY = false>
 __device__ __forceinline__ uint4 chunk_load_in_step(const XT *row, int c, int C, const Span &span) {
   constexpr int VEC = Chunk<XT>::VEC;
-  if (c >= 0 && c + VEC <= C) return ld_stream(reinterpret_cast<const uint4 *>(row + c));
+  if (!ONE_WAY && c >= 0 && c + VEC <= C) return ld_stream(reinterpret_cast<const uint4 *>(row + c));
   uint32_t w[4] = {0u, 0u, 0u, 0u};
   const uintptr_t at = reinterpret_cast<uintptr_t>(row) + (uintptr_t)((intptr_t)c * (intptr_t)sizeof(XT));
   if (c < C && c + VEC > 0) {
