@@ -5,8 +5,9 @@
 // bandwidth bounds the kernel. Rows are spread over threads as in the LayerNorm's forward (norm.cuh). Rows of odd width that
 // begin equally far from a boundary in all tensors are taken in step (rows_step.cuh), with aligned accesses and the weights,
 // shifted as the CTA's rows are, in shared memory (not with the 8-bit output, whose groups of channels no chunk may cut).
-// 8192 rows of 4096 BF16 values with a residual, y in 8 bits alone: 46 us for 236 MB (5.1 TB/s); 20011 rows of 1003 FP16 values
-// with a residual, in step: 35 us for 160 MB (4.6 TB/s), chunk by chunk from wherever a row begins 72.
+// 8192 rows of 4096 BF16 values with a residual, y in 8 bits alone: 45 us for 236 MB (5.2 TB/s); 20011 rows of 1003 FP16 values
+// with a residual, in step: 34 us for 160 MB (4.7 TB/s; with two ways to load a chunk 35), chunk by chunk from wherever a row
+// begins 72.
 #include <math.h>
 
 #include <algorithm>
@@ -22,10 +23,11 @@ template <int NV>
 constexpr int rms_rows() {
   return NV == 1 ? 4 : NV == 2 ? 2 : 1;
 }
-// CTAs of 256 threads per SM that the registers are kept to.
+// CTAs of 256 threads per SM that the registers are kept to. (8192 rows of 4096 BF16 values with a residual, into 8 bits: 45 us in
+// three, 49 in two.)
 template <int NV>
 constexpr int rms_ctas() {
-  return NV <= 2 ? 3 : NV == 4 ? 2 : 1;
+  return NV <= 4 ? 3 : 1;
 }
 
 struct RmsFwdArgs {
@@ -66,7 +68,7 @@ __global__ void __launch_bounds__(T > 32 ? T : 256, rms_ctas<NV>() * (T == 128 ?
     const int c = (v * T + t) * VEC - sh;
     if (i >= rows) return make_uint4(0u, 0u, 0u, 0u);
     if constexpr (STEP)
-      return chunk_load_in_step<XT>(p + (first + stride * i) * ld, c, C, s);
+      return chunk_load_in_step<XT, true>(p + (first + stride * i) * ld, c, C, s);
     else
       return chunk_load<XT, AL>(p + i * ld, c, C, s);
   };
