@@ -12,6 +12,7 @@
 // The tensor cores are 45 % active. Weights stream through a ring from L2, which holds them. With h in memory the features' traffic bounds the
 // block (131 us; 302 MB written and read again).
 #include "ffn.cuh"
+#include "ffn_schedule.cuh"
 
 namespace triattn {
 namespace ffn {
@@ -24,9 +25,10 @@ struct BCfg {
   static constexpr int XB = CB == 128 ? 2 : 1, X_BYTES = KB * kHalf * 128;  // x's tiles
   static constexpr int W1_BYTES = KB * kBox, W_BYTES = W1_BYTES + CB / 2 * 128;  // of a feature block: 64 rows of Wg or Wu, CB / 2 of Wd
   static constexpr int NW = CB == 128 ? 5 : 3;
+  using Order = BlockSchedule<NS, NW>;
   static constexpr int T_OUT = NS * 128;
   static constexpr int EPI_WARPS = 16, NTHREADS = 32 * (4 + EPI_WARPS), PIECE = 32 * 32;
-  static constexpr int B_XF = 0, B_XE = B_XF + XB, B_WF = B_XE + XB, B_WE = B_WF + NW, B_S = B_WE + NW, B_H = B_S + NS, B_OF = B_H + NS,
+  static constexpr int B_XF = 0, B_XE = B_XF + XB, B_WF = B_XE + XB, B_WE = B_WF + NW, B_S = B_WE + NW, B_H = B_S + Order::kSums, B_OF = B_H + NS,
                        B_OE = B_OF + 1, B_DONE = B_OE + 1, NBAR = B_DONE + 1;
   static constexpr int OFF_X = 0, OFF_W = XB * X_BYTES, OFF_EPI = OFF_W + NW * W_BYTES, OFF_BAR = OFF_EPI + EPI_WARPS * PIECE,
                        OFF_MISC = OFF_BAR + 8 * NBAR, SMEM_ALLOC = OFF_MISC + 16 + 1024;
@@ -45,6 +47,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BCfg<CB>::NTHREADS, 
     block_kernel(const __grid_constant__ CUtensorMap mX, const __grid_constant__ CUtensorMap mWg, const __grid_constant__ CUtensorMap mWu,
                  const __grid_constant__ CUtensorMap mWd, const BArgs a) {
   using C = BCfg<CB>;
+  using Order = typename C::Order;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sb0 = smem_u32(sm);
@@ -95,8 +98,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BCfg<CB>::NTHREADS, 
     load_x();
     for (int t = 0; t < mine && ok; ++t) {
       for (int f = 0; f < a.blocks && ok; ++f) {
-        const int s = ws % C::NW;
-        if (ws >= C::NW) ok = wait_bar_warp(bar(C::B_WE + s), ((ws / C::NW) - 1) & 1, ab);
+        const int s = Order::slot(ws);
+        if (ws >= C::NW) ok = wait_bar_warp(bar(C::B_WE + s), Order::slot_phase(ws - C::NW) & 1, ab);
         if (!ok) break;
         if (lane == 0) {
           const uint32_t fb = mapa_shared(bar(C::B_WF + s), 0), dst = sb0 + C::OFF_W + s * C::W_BYTES;
@@ -111,7 +114,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BCfg<CB>::NTHREADS, 
     }
     if (!ok && lane == 0 && rank == 0) {  // let the copies in flight land before the CTAs exit
       for (int x = max(0, xs - C::XB); x < xs; ++x) drain_bar(bar(C::B_XF + x % C::XB), (x / C::XB) & 1);
-      for (int x = max(0, ws - C::NW); x < ws; ++x) drain_bar(bar(C::B_WF + x % C::NW), (x / C::NW) & 1);
+      for (int x = max(0, ws - C::NW); x < ws; ++x) drain_bar(bar(C::B_WF + Order::slot(x)), Order::slot_phase(x) & 1);
     }
   } else if ((warp == 1 || warp == 3) && rank == 0) {
     // ------------------------------------------------------------ issue x Wg^T and x Wu^T, every second block each
@@ -133,17 +136,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BCfg<CB>::NTHREADS, 
     for (int n = f; n < total && ok; n += 2, f += 2) {
       for (; f >= a.blocks && ok; f -= a.blocks) leave_x();
       if (!ok) break;
-      const int b = n % C::NS, s = n % C::NW, xs = t % C::XB, p = n - C::NS;
+      const int b = Order::buffer(n), s = Order::slot(n), xs = t % C::XB, p = n - C::NS;
       arrive_x();
       // (the block that had the buffer is done when its weights' place is free again)
-      ok = ok && (p < 0 || wait_bar_warp(bar(C::B_WE + p % C::NW), (p / C::NW) & 1, ab)) && wait_bar_warp(bar(C::B_WF + s), (n / C::NW) & 1, ab);
+      ok = ok && (p < 0 || wait_bar_warp(bar(C::B_WE + Order::slot(p)), Order::slot_phase(p) & 1, ab)) &&
+           wait_bar_warp(bar(C::B_WF + s), Order::slot_phase(n) & 1, ab);
       if (!ok) break;
       tc_fence_after();
       const uint64_t dx = smem_desc(sb0 + C::OFF_X + xs * C::X_BYTES, 16, 1024, kSwizzle128B);
       const uint64_t dw = smem_desc(sb0 + C::OFF_W + s * C::W_BYTES, 16, 1024, kSwizzle128B);
       for (int k = 0; k < a.kc; ++k)
         pair_mma_x4_e(tb + 128 * b, dx + (uint64_t)(k * (kHalf * 128 >> 4)), 2, dw + (uint64_t)(k * (kBox >> 4)), 2, idesc, k > 0 ? 1u : 0u);
-      pair_commit_e(bar(C::B_S + b));
+      pair_commit_e(bar(C::B_S + Order::sums(n)));
     }
     while (ok && t < mine) leave_x();
     pair_commit_e(bar(C::B_DONE));
@@ -155,9 +159,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BCfg<CB>::NTHREADS, 
     bool ok = true;
     int f = 0, t = 0;
     for (int n = 0; n < total; ++n) {
-      const int b = n % C::NS, s = n % C::NW;
+      const int b = Order::buffer(n), s = Order::slot(n);
       if (f == 0 && t > 0) ok = wait_bar_warp(bar(C::B_OE), (t - 1) & 1, ab);
-      ok = ok && wait_bar_warp(bar(C::B_WF + s), (n / C::NW) & 1, ab) && wait_bar_warp(bar(C::B_H + b), (n / C::NS) & 1, ab);
+      ok = ok && wait_bar_warp(bar(C::B_WF + s), Order::slot_phase(n) & 1, ab) &&
+           wait_bar_warp(bar(C::B_H + b), Order::hidden_phase(n) & 1, ab);
       if (!ok) break;
       tc_fence_after();
       const uint64_t dw = smem_desc(sb0 + C::OFF_W + s * C::W_BYTES + C::W1_BYTES, 16, 1024, kSwizzle128B);
@@ -214,8 +219,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BCfg<CB>::NTHREADS, 
       // after one that is, while which its last products run)
       for (; f > 0 && stored < t && ok; ++stored) ok = store_tile(stored);
       if (!ok) break;
-      const int b = n % C::NS, m = row_of_tile(t);
-      ok = wait_bar_warp(bar(C::B_S + b), (n / C::NS) & 1, ab);
+      const int b = Order::buffer(n), m = row_of_tile(t);
+      ok = wait_bar_warp(bar(C::B_S + Order::sums(n)), Order::sums_phase(n) & 1, ab);
       if (!ok) break;
       tc_fence_after();
       const uint32_t ts = tb + lanes + 128 * b + 32 * half;
