@@ -135,7 +135,7 @@ __device__ __forceinline__ double chunk_squares(const Tensor &t, int64_t chunk) 
 }
 
 // part[cta]: the sum over the CTA's chunks, on top of what the launches before left there.
-__global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ Batch b, int more, double *__restrict__ part) {
+__global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ Batch b, int more, double *part) {
   __shared__ double red[kThreads / 32];
   wait_previous_kernel();
   allow_next_kernel();
@@ -186,8 +186,8 @@ __device__ __forceinline__ void chunk_scale(const Tensor &t, int64_t chunk, floa
 }
 
 // The norm from the CTAs' sums, and a batch's clipped tensors.
-__global__ void __launch_bounds__(kThreads) clip_kernel(const __grid_constant__ Batch b, const double *__restrict__ part, int parts,
-                                                        float max_norm, float *__restrict__ norm) {
+__global__ void __launch_bounds__(kThreads) clip_kernel(const __grid_constant__ Batch b, const double *part, int parts,
+                                                        float max_norm, float *norm) {
   __shared__ double red[kThreads / 32];
   wait_previous_kernel();
   allow_next_kernel();

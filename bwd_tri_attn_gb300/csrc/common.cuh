@@ -134,6 +134,16 @@ __device__ __forceinline__ uint4 ld_stream(const uint4 *p) {
   return v;
 }
 
+// The same of what the stream's kernel before may still have been writing when this one began (launch_after): a coherent load,
+// since the one above is for what nobody writes while the kernel lives, from its start on.
+__device__ __forceinline__ uint4 ld_stream_after(const uint4 *p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
 
 // Device status codes written by bounded waits (host reads them lazily).
 constexpr int kStatusTimeout = 1;

@@ -306,7 +306,7 @@ struct Piece {
 #pragma unroll
     for (int i = 0; i < PARTS; ++i) {
       const int r = lane / PARTS + ROWS * i;
-      v[i] = r < rows && c < parts ? ld_stream(reinterpret_cast<const uint4 *>(static_cast<const char *>(p) + r * pitch + 16 * c))
+      v[i] = r < rows && c < parts ? ld_stream_after(reinterpret_cast<const uint4 *>(static_cast<const char *>(p) + r * pitch + 16 * c))
                                    : make_uint4(0u, 0u, 0u, 0u);
     }
   }

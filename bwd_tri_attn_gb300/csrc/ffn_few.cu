@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) few_kernel(const FewArgs a) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int k = k0 + 32 * s + 8 * t;
-          raw[s][m][h] = k < a.K ? ld_stream(reinterpret_cast<const uint4 *>(w[m][h] + k)) : make_uint4(0u, 0u, 0u, 0u);
+          raw[s][m][h] = k < a.K ? ld_stream_after(reinterpret_cast<const uint4 *>(w[m][h] + k)) : make_uint4(0u, 0u, 0u, 0u);
         }
   };
   // The weights are no kernel's results but of those before the whole call: the second kernel asks for its first ones before the

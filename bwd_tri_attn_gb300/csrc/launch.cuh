@@ -34,7 +34,9 @@ struct DeviceValue {
 };
 
 // Launch of a kernel that may be set up while the stream's previous kernel still runs (programmatic
-// dependent launch): it calls wait_previous_kernel() before it reads what that kernel wrote.
+// dependent launch): it calls wait_previous_kernel() before it reads what that kernel wrote, and reads it by ordinary loads.
+// (Non-coherent ones, __ldg(), ld_stream() and what the compiler makes of const __restrict__ pointers, are for memory that
+// nobody writes from the kernel's start on, which may be before that one's end.)
 template <typename... P, typename... A>
 cudaError_t launch_after(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, const A &...args) {
   cudaLaunchConfig_t cfg = {};

@@ -19,8 +19,8 @@ constexpr int bwd_ctas(int T, int NV, bool AL) {
 
 // dgamma and dbeta: the sums over the CTAs' partials part[p][n], n = 2 C (n = C: dgamma alone). A CTA takes 32 of the n
 // columns; lane row y adds p = y, y + 32, ... in order, then the 32 sums are added in order.
-static __global__ void __launch_bounds__(1024) norm_reduce_kernel(const float *__restrict__ part, int parts, int n, int C,
-                                                           float *__restrict__ dgamma, float *__restrict__ dbeta) {
+static __global__ void __launch_bounds__(1024) norm_reduce_kernel(const float *part, int parts, int n, int C,
+                                                           float *dgamma, float *dbeta) {
   __shared__ float acc[32][33];
   const int i = blockIdx.x * 32 + threadIdx.x;
   float s = 0.f;

@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kBwdThreads) relpos_bwd_kernel(const __grid_co
     for (int p = 0; p < kPairs; ++p) g[p] = __ldcs(dbias + 32 * p);
     if constexpr (HOW == kIndex) {
 #pragma unroll
-      for (int p = 0; p < kPairs; ++p) r[p] = __ldg(reinterpret_cast<const uint16_t *>(index + unit_start(plane0, k) + 64 * p));
+      for (int p = 0; p < kPairs; ++p) r[p] = *reinterpret_cast<const uint16_t *>(index + unit_start(plane0, k) + 64 * p);
     }
   };
   uint32_t next[kPairs];
@@ -311,8 +311,8 @@ __global__ void __launch_bounds__(kBwdThreads) relpos_bwd_kernel(const __grid_co
 }
 
 // dtable[t][h]: a warp for each, its lanes the sequences' and pieces' sums in turn, then an xor tree.
-__global__ void __launch_bounds__(256) relpos_reduce_kernel(const float *__restrict__ part, int B, int H, int pieces, int rows,
-                                                            float *__restrict__ dtable) {
+__global__ void __launch_bounds__(256) relpos_reduce_kernel(const float *part, int B, int H, int pieces, int rows,
+                                                            float *dtable) {
   const int x = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   wait_previous_kernel();
   if (x >= rows * H) return;
