@@ -5,7 +5,7 @@ only keep the tensors the backward pass needs and hand gradients back in the dty
 expects. There is no CPU path: the library raises if it is missing or a call fails. Inputs and
 gradients are made contiguous, and copied to a 16-byte boundary where the library wants one (a no-op
 for fresh tensors); dtypes and sizes are checked by the binding. The backward passes are
-differentiable once (no second derivatives).
+differentiable once (no second derivatives); forward-mode derivatives are refused.
 
 - ``triangle_attention(Q, K, V, bias, mask=None, node=NODE_STARTING)``: the attention core
   (include/tri_attn.h) with its residual-compensated backward; gradients for Q, K, V and bias.
@@ -21,12 +21,22 @@ differentiable once (no second derivatives).
   for x and the weights; with ``checkpoint`` it keeps x in 8 bits for the backward pass.
 - ``cross_attention(Q, K, V, mask=None, kv_lens=None, scale=None)``: cross attention to an encoder's
   states of another length (include/tri_cross.h), gradients for Q, K and V.
+- ``relative_position_bias(table, starts, Nq, ...)``: the pair bias from a learned table of distances
+  (include/tri_relpos.h), gradients for the table and the base.
+- ``rms_norm(x, gamma=None, residual=None, eps=1e-5)``: RMS norm, with the residual's addition
+  (include/tri_rms.h).
+- ``gated_feed_forward(x, Wg, Wu, Wd, act, checkpoint=False)``: the gated feed-forward block
+  (include/tri_ffn.h), weights as in the block above; ``feed_forward_layer`` and ``FeedForwardLayer``: it
+  behind the norm of a residual sum.
+- ``clip_grad_norm_(parameters, max_norm)``: clips gradients in place to a norm of all of them together
+  (include/tri_clip.h).
 """
 from __future__ import annotations
 
 import math
 
 import torch
+from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
 from . import binding as tb
@@ -302,7 +312,12 @@ def _ffn_gradients(needs, x, weights, a, u, dout, act, dtypes):
 
 
 def _wants_gradients(*tensors):
-    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+    """Whether the call belongs to a derivative: a backward pass, or a forward-mode one, which the autograd functions refuse
+    (passed by, the outputs would come without a tangent: a derivative of zero)."""
+    tensors = [t for t in tensors if t is not None]
+    if torch.is_grad_enabled() and any(t.requires_grad for t in tensors):
+        return True
+    return any(forward_ad.unpack_dual(t).tangent is not None for t in tensors)
 
 
 def gated_feed_forward(x, Wg, Wu, Wd, act="silu", checkpoint=False):
