@@ -1211,9 +1211,9 @@ def rms_backward(r, gamma, rstd, dy, dr=None, workspace=None, stream=None):
     return dx, dgamma
 
 
-def _clip_array(grads, out):
+def _clip_array(grads, out, written):
     """The gradients' descriptions for the library (as ClipTensor's fields one behind another), their number and the
-    device's index: every tensor checked, no output twice."""
+    device's index: every tensor checked, none twice among those that are written."""
     device = torch.cuda.current_device()
     try:
         types = [g.dtype for g in grads]
@@ -1234,7 +1234,7 @@ def _clip_array(grads, out):
         some = [i for i, n in enumerate(sizes) if n]
         codes, sizes, at, to = ([v[i] for i in some] for v in (codes, sizes, at, to))
     n = len(at)
-    if len(set(to)) != n:
+    if written and len(set(to)) != n:
         raise ValueError("a tensor stands twice among the gradients that are written")
     rows = array.array("q", bytes(32 * n))
     for k, v in enumerate((at, to, sizes, codes)):
@@ -1256,13 +1256,13 @@ def _clip_refusal(device, grads, out):
     raise ValueError("the gradients' tensors do not fit together")
 
 
-def _clip(call, grads, out, workspace, *more):
+def _clip(call, grads, out, workspace, *more, written=True):
     grads = list(grads)
     if out is not None:
         out = list(out)
         if len(out) != len(grads):
             raise ValueError(f"{len(out)} outputs for {len(grads)} gradients")
-    rows, count, device = _clip_array(grads, out)
+    rows, count, device = _clip_array(grads, out, written)
     norm = torch.empty((), dtype=_F32, device=torch.device("cuda", device))
     if workspace is None:
         workspace = torch.empty(CLIP_WORKSPACE_BYTES, dtype=torch.uint8, device=norm.device)
@@ -1274,11 +1274,11 @@ def _clip(call, grads, out, workspace, *more):
 
 
 def gradient_norm(grads, workspace=None, stream=None) -> torch.Tensor:
-    """The 2-norm of all elements of the gradients (BF16, FP16 and FP32 tensors of any number and shapes): an FP32 number
-    on the device."""
+    """The 2-norm of all elements of the gradients (BF16, FP16 and FP32 tensors of any number and shapes; one that is named
+    twice counts twice): an FP32 number on the device."""
     if (other := _other_stream(stream)) is not None:
         return _called_on(other, gradient_norm, grads, workspace=workspace)
-    return _clip("tri_grad_norm", grads, None, workspace)
+    return _clip("tri_grad_norm", grads, None, workspace, written=False)
 
 
 def clip_gradients(grads, max_norm, out=None, workspace=None, stream=None) -> torch.Tensor:
