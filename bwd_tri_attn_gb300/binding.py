@@ -21,6 +21,7 @@ import torch
 from . import _build
 
 TRI_ATTN_OK = 0
+TRI_ATTN_ERR_INVALID_ARG = -1
 _lock = threading.Lock()
 _lib = None
 
@@ -1269,6 +1270,8 @@ def _clip(call, grads, out, workspace, *more, written=True):
     _on_device(device, _arg(workspace, "workspace", None, None))
     rc = getattr(load(), call)(count, rows.buffer_info()[0], *more, norm.data_ptr(), workspace.data_ptr(), _nbytes(workspace),
                                _raw_stream(device))
+    if rc == TRI_ATTN_ERR_INVALID_ARG:  # (the rest is checked)
+        raise ValueError("a tensor that is written shares memory with another one")
     _check(call, rc)
     return norm
 
@@ -1283,7 +1286,7 @@ def gradient_norm(grads, workspace=None, stream=None) -> torch.Tensor:
 
 def clip_gradients(grads, max_norm, out=None, workspace=None, stream=None) -> torch.Tensor:
     """Multiplies the gradients by min(1, max_norm / (norm + 1e-6)), in place or into the tensors ``out``, and returns
-    their norm before, an FP32 number on the device."""
+    their norm before, an FP32 number on the device. No tensor that is written shares memory with another one."""
     max_norm = float(max_norm)
     if not max_norm >= 0.0:
         raise ValueError(f"max_norm must not be negative, got {max_norm}")

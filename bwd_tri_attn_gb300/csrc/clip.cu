@@ -9,6 +9,8 @@
 #include <math.h>
 
 #include <algorithm>
+#include <memory>
+#include <new>
 
 #include "launch.cuh"
 #include "rows.cuh"
@@ -223,6 +225,37 @@ void next_batch(int n, const tri_clip_tensor *tensors, int &at, Batch &b) {
   }
 }
 
+// Whether a tensor that is written shares memory with another one, or with its own input unless it is that (CTAs read and
+// write chunks of all tensors in any order). By the ranges' starts in order: one that is written may not begin before all earlier
+// ones have ended, one that is read not before all written ones have. TRI_ATTN_OK: none does.
+int check_overlap(int n, const tri_clip_tensor *tensors) {
+  struct Range {
+    uintptr_t begin, end;
+    bool written;
+  };
+  constexpr int kFew = 256;
+  Range few[kFew];
+  std::unique_ptr<Range[]> many(2 * (int64_t)n > kFew ? new (std::nothrow) Range[2 * (size_t)n] : nullptr);
+  Range *ranges = 2 * (int64_t)n > kFew ? many.get() : few;
+  if (!ranges) return TRI_ATTN_ERR_UNSUPPORTED;
+  int64_t count = 0;
+  for (int i = 0; i < n; ++i) {
+    const tri_clip_tensor &x = tensors[i];
+    if (x.n == 0) continue;
+    const uintptr_t g = reinterpret_cast<uintptr_t>(x.g), out = reinterpret_cast<uintptr_t>(x.out), bytes = x.n * element_bytes(x.dtype);
+    ranges[count++] = {out, out + bytes, true};
+    if (g != out) ranges[count++] = {g, g + bytes, false};
+  }
+  std::sort(ranges, ranges + count, [](const Range &a, const Range &b) { return a.begin < b.begin; });
+  uintptr_t written = 0, any = 0;
+  for (const Range *r = ranges; r != ranges + count; ++r) {
+    if (r->begin < (r->written ? any : written)) return TRI_ATTN_ERR_INVALID_ARG;
+    any = std::max(any, r->end);
+    if (r->written) written = std::max(written, r->end);
+  }
+  return TRI_ATTN_OK;
+}
+
 int clip(int n, const tri_clip_tensor *tensors, bool scale, float max_norm, float *norm, void *workspace, size_t workspace_bytes,
          cudaStream_t st) {
   if (n < 0 || (n && !tensors) || !norm || !(max_norm >= 0.f)) return TRI_ATTN_ERR_INVALID_ARG;
@@ -238,6 +271,8 @@ int clip(int n, const tri_clip_tensor *tensors, bool scale, float max_norm, floa
   }
   if (!workspace || workspace_bytes < TRI_CLIP_WORKSPACE_BYTES) return TRI_ATTN_ERR_WORKSPACE;
   if (reinterpret_cast<uintptr_t>(workspace) & 15u) return TRI_ATTN_ERR_UNSUPPORTED;
+  const int rc = scale ? check_overlap(n, tensors) : TRI_ATTN_OK;
+  if (rc) return rc;
   double *part = static_cast<double *>(workspace);
   Batch b;
   // as many sums as the largest batch has CTAs (the first launch writes them all)

@@ -13,9 +13,9 @@
  *
  * Requirements: pointers aligned to their element (of one tensor: g and out equally far from a 16-byte boundary take
  * the wide accesses); max_norm >= 0, infinity included; no output overlaps another tensor or output (out may be g: in
- * place); n <= 2^20. workspace: TRI_CLIP_WORKSPACE_BYTES, 16-byte aligned.
+ * place), which tri_clip refuses (TRI_ATTN_ERR_INVALID_ARG); n <= 2^20. workspace: TRI_CLIP_WORKSPACE_BYTES, 16-byte aligned.
  * Return codes are the TRI_ATTN_* codes of tri_attn.h; a call that returns an error has enqueued nothing
- * (TRI_ATTN_ERR_CUDA from a launch itself excepted). Calls are asynchronous on `stream`, allocate nothing, keep
+ * (TRI_ATTN_ERR_CUDA from a launch itself excepted). Calls are asynchronous on `stream`, allocate no device memory, keep
  * no state between calls and may be captured into a graph (the descriptions are part of what is captured). No
  * floating-point atomics: the same call gives the same bits.
  */
