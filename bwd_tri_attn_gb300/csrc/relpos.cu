@@ -78,16 +78,17 @@ template <bool kPos>
 struct Walk {
   uint32_t j4;  // of value e: four times its column
   int d, i, q;  // j - i; kPos: row and its position
-  const char *pq, *pk;
+  const int *pq;  // (rows go up to 2^31: four times a row is no 32-bit offset)
+  const char *pk;
   __device__ __forceinline__ Walk(const RelArgs &a, int b, int e) : q(0), pq(nullptr), pk(nullptr) {
     i = (int)((uint32_t)e / (uint32_t)a.Nk);
     const int j = e - i * a.Nk;
     j4 = 4u * (uint32_t)j;
     d = j - i;
     if (kPos) {
-      pq = reinterpret_cast<const char *>(a.posq + (int64_t)b * a.Nq);
+      pq = a.posq + (int64_t)b * a.Nq;
       pk = reinterpret_cast<const char *>(a.posk + (int64_t)b * a.Nk);
-      q = at(pq, 4u * (uint32_t)i);
+      q = __ldg(pq + i);
     }
   }
   static __device__ __forceinline__ int at(const char *p, uint32_t offset) { return __ldg(reinterpret_cast<const int *>(p + offset)); }
@@ -101,7 +102,7 @@ struct Walk {
     }
     if (kPos && (wrap || a.step_i)) {
       i += a.step_i + (wrap ? 1 : 0);
-      q = at(pq, 4u * (uint32_t)min(i, a.Nq - 1));  // (one step past the unit's end is made)
+      q = __ldg(pq + min(i, a.Nq - 1));  // (one step past the unit's end is made)
     }
   }
   __device__ __forceinline__ void pair(const RelArgs &a, int &d0, int &d1) const {
@@ -111,7 +112,7 @@ struct Walk {
       d1 = d + (turn ? -a.Nk : 1);
       return;
     }
-    const int k0 = at(pk, j4), k1 = at(pk, turn ? 0u : j4 + 4), q1 = turn ? at(pq, 4u * (uint32_t)(i + 1)) : q;
+    const int k0 = at(pk, j4), k1 = at(pk, turn ? 0u : j4 + 4), q1 = turn ? __ldg(pq + i + 1) : q;
     d0 = (int)((uint32_t)k0 - (uint32_t)q);
     d1 = (int)((uint32_t)k1 - (uint32_t)q1);
     if ((((k0 ^ q) & (k0 ^ d0)) | ((k1 ^ q1) & (k1 ^ d1))) < 0) {  // (differences that int32 does not hold: rarely)
