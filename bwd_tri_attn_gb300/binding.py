@@ -1212,6 +1212,21 @@ def rms_backward(r, gamma, rstd, dy, dr=None, workspace=None, stream=None):
     return dx, dgamma
 
 
+def _gapless(t):
+    """Whether a tensor's elements fill its memory, in whatever order of its axes."""
+    want = 1
+    for stride, n in sorted((s, n) for n, s in zip(t.shape, t.stride()) if n != 1):
+        if stride != want:
+            return False
+        want *= n
+    return True
+
+
+def _same_order(g, t):
+    """Whether a value of g and its product, in t, are equally far from the tensors' first elements."""
+    return (g.is_contiguous() and t.is_contiguous()) or (g.shape == t.shape and g.stride() == t.stride())
+
+
 def _clip_array(grads, out, written):
     """The gradients' descriptions for the library (as ClipTensor's fields one behind another), their number and the
     device's index: every tensor checked, none twice among those that are written."""
@@ -1221,12 +1236,12 @@ def _clip_array(grads, out, written):
         codes = [_NORM_DTYPES[t] for t in types]
         sizes = [g.numel() for g in grads]
         at = [g.data_ptr() for g in grads]
-        fine = all([g.get_device() == device for g in grads]) and all([g.is_contiguous() for g in grads])
+        fine = all([g.get_device() == device for g in grads]) and all([g.is_contiguous() or _gapless(g) for g in grads])
         to = at
         if out is not None:
             to = [t.data_ptr() for t in out]
             fine = (fine and [t.dtype for t in out] == types and [t.numel() for t in out] == sizes
-                    and all([t.get_device() == device for t in out]) and all([t.is_contiguous() for t in out]))
+                    and all([t.get_device() == device for t in out]) and all([_same_order(g, t) for g, t in zip(grads, out)]))
     except (AttributeError, KeyError):
         fine = False
     if not fine:
@@ -1250,10 +1265,13 @@ def _clip_refusal(device, grads, out):
         for t, name in ((g, f"gradient {i}"), *(() if out is None else ((out[i], f"out {i}"),))):
             if not isinstance(t, torch.Tensor) or t.dtype != g.dtype or t.numel() != g.numel():
                 raise ValueError(f"{name} must be a tensor of gradient {i}'s size and type")
-            if not t.is_contiguous():
-                raise ValueError(f"{name} must be contiguous")
+            if not (t.is_contiguous() or _gapless(t)):
+                raise ValueError(f"{name} must be contiguous, in whatever order of its axes")
             if t.get_device() != device:
                 raise ValueError(f"{name} must be a CUDA tensor on the current device, got {t.device}")
+        if out is not None and not _same_order(g, out[i]):
+            raise ValueError(f"out {i} must have gradient {i}'s shape and strides, {tuple(g.shape)} and {g.stride()}, "
+                             f"got {tuple(out[i].shape)} and {out[i].stride()}")
     raise ValueError("the gradients' tensors do not fit together")
 
 
@@ -1277,8 +1295,8 @@ def _clip(call, grads, out, workspace, *more, written=True):
 
 
 def gradient_norm(grads, workspace=None, stream=None) -> torch.Tensor:
-    """The 2-norm of all elements of the gradients (BF16, FP16 and FP32 tensors of any number and shapes; one that is named
-    twice counts twice): an FP32 number on the device."""
+    """The 2-norm of all elements of the gradients (BF16, FP16 and FP32 tensors of any number and shapes, without gaps in whatever
+    order of their axes; one that is named twice counts twice): an FP32 number on the device."""
     if (other := _other_stream(stream)) is not None:
         return _called_on(other, gradient_norm, grads, workspace=workspace)
     return _clip("tri_grad_norm", grads, None, workspace, written=False)
@@ -1286,7 +1304,8 @@ def gradient_norm(grads, workspace=None, stream=None) -> torch.Tensor:
 
 def clip_gradients(grads, max_norm, out=None, workspace=None, stream=None) -> torch.Tensor:
     """Multiplies the gradients by min(1, max_norm / (norm + 1e-6)), in place or into the tensors ``out``, and returns
-    their norm before, an FP32 number on the device. No tensor that is written shares memory with another one."""
+    their norm before, an FP32 number on the device. No tensor that is written shares memory with another one; one that is
+    transposed or permuted has an ``out`` of the same strides."""
     max_norm = float(max_norm)
     if not max_norm >= 0.0:
         raise ValueError(f"max_norm must not be negative, got {max_norm}")
