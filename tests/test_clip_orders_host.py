@@ -12,7 +12,8 @@ def cpu_tensors(monkeypatch):
 
 def shapes():
     t = torch.zeros(2, 3, 4, 5)
-    return [t[0, 0].t(), t.permute(3, 1, 0, 2), t.contiguous(memory_format=torch.channels_last), torch.zeros(1, 7, 1).permute(2, 1, 0), torch.zeros(5).as_strided((1, 5), (77, 1)), torch.zeros(3, 0).t()]
+    return [t[0, 0].t(), t.permute(3, 1, 0, 2), t.contiguous(memory_format=torch.channels_last),
+            torch.zeros(1, 7, 1).permute(2, 1, 0), torch.zeros(5).as_strided((1, 5), (77, 1)), torch.zeros(3, 0).t()]
 
 
 @pytest.mark.parametrize("i", range(6))
@@ -26,7 +27,8 @@ def test_any_order(i):
 def test_refused():
     t = torch.zeros(6, 8)
     four = torch.zeros(2, 3, 4, 5)
-    for bad in (four[:, :1].reshape(2, 1, 20).transpose(1, 2), t[:, :4], t[::2], t.t()[:3], t.expand(2, 6, 8), torch.zeros(4).expand(3, 4).t(), t.as_strided((4, 4), (1, 1))):
+    for bad in (four[:, :1].reshape(2, 1, 20).transpose(1, 2), t[:, :4], t[::2], t.t()[:3], t.expand(2, 6, 8), torch.zeros(4).expand(3, 4).t(),
+                t.as_strided((4, 4), (1, 1))):
         with pytest.raises(ValueError, match="gradient 1 must be contiguous"):
             tb._clip_array([t, bad], None, written=False)
         with pytest.raises(ValueError, match="out 0 must be contiguous"):
