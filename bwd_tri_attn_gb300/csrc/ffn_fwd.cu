@@ -7,6 +7,10 @@ namespace {
 
 using namespace ffn;
 
+// Whether the few rows' kernels are faster: up to 16 rows always (8 of 4096 and 16384: 67 us, 88 in tiles; of 1024 and 4096: 9 and
+// 19), up to 32 where the weights are small (32 of 1024 and 4096: 15 and 19, of 512 and 16384: 38 and 26).
+bool few_rows_pay(const tri_ffn_shape &s) { return s.M <= 16 || (s.M <= kFewRows && (int64_t)s.C * s.F <= (1 << 22)); }
+
 struct FwdWorkspace {
   int64_t h, part, bytes;
 };
@@ -14,7 +18,7 @@ FwdWorkspace fwd_workspace(const tri_ffn_shape &s) {
   FwdWorkspace w;
   w.h = 0;
   w.part = aligned256(2 * s.M * s.F);
-  w.bytes = w.part + (int64_t)share_bytes(256);
+  w.bytes = w.part + (few_rows_pay(s) ? 0 : (int64_t)share_bytes(256));  // (few rows' kernels share no tiles)
   return w;
 }
 
@@ -25,10 +29,6 @@ bool block_pays(const tri_ffn_shape &s, int pairs) {
   const double rounds = ceil_div(ceil_div(s.M, kRows), pairs);
   return s.C <= 256 && 4.3 + rounds * ceil_div(s.F, 64) * (s.C <= 128 ? 0.65 : 1.13) < 8 + 1.1e-6 * (double)s.M * s.F;
 }
-
-// Whether the few rows' kernels are faster: up to 16 rows always (8 of 4096 and 16384: 62 us, 85 in tiles; of 1024 and 4096: 9 and
-// 19), up to 32 where the weights are small (32 of 1024 and 4096: 16 and 19, of 512 and 16384: 38 and 26).
-bool few_rows_pay(const tri_ffn_shape &s) { return s.M <= 16 || (s.M <= kFewRows && (int64_t)s.C * s.F <= (1 << 22)); }
 
 cudaError_t launch_fwd(const tri_ffn_shape &s, const void *x, const void *Wg, const void *Wu, const void *Wd, void *out, void *a,
                        void *u, char *ws, int *status, cudaStream_t st) {
