@@ -1214,6 +1214,8 @@ def rms_backward(r, gamma, rstd, dy, dr=None, workspace=None, stream=None):
 
 def _gapless(t):
     """Whether a tensor's elements fill its memory, in whatever order of its axes."""
+    if t.is_contiguous():  # (without elements, too)
+        return True
     want = 1
     for stride, n in sorted((s, n) for n, s in zip(t.shape, t.stride()) if n != 1):
         if stride != want:
@@ -1236,12 +1238,14 @@ def _clip_array(grads, out, written):
         codes = [_NORM_DTYPES[t] for t in types]
         sizes = [g.numel() for g in grads]
         at = [g.data_ptr() for g in grads]
-        fine = all([g.get_device() == device for g in grads]) and all([g.is_contiguous() or _gapless(g) for g in grads])
+        plain = all([g.is_contiguous() for g in grads])
+        fine = all([g.get_device() == device for g in grads]) and (plain or all(map(_gapless, grads)))
         to = at
         if out is not None:
             to = [t.data_ptr() for t in out]
             fine = (fine and [t.dtype for t in out] == types and [t.numel() for t in out] == sizes
-                    and all([t.get_device() == device for t in out]) and all([_same_order(g, t) for g, t in zip(grads, out)]))
+                    and all([t.get_device() == device for t in out])
+                    and ((plain and all([t.is_contiguous() for t in out])) or all(map(_same_order, grads, out))))
     except (AttributeError, KeyError):
         fine = False
     if not fine:
@@ -1265,7 +1269,7 @@ def _clip_refusal(device, grads, out):
         for t, name in ((g, f"gradient {i}"), *(() if out is None else ((out[i], f"out {i}"),))):
             if not isinstance(t, torch.Tensor) or t.dtype != g.dtype or t.numel() != g.numel():
                 raise ValueError(f"{name} must be a tensor of gradient {i}'s size and type")
-            if not (t.is_contiguous() or _gapless(t)):
+            if not _gapless(t):
                 raise ValueError(f"{name} must be contiguous, in whatever order of its axes")
             if t.get_device() != device:
                 raise ValueError(f"{name} must be a CUDA tensor on the current device, got {t.device}")
