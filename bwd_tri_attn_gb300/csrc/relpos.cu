@@ -5,13 +5,15 @@
 // distance d leads to (the table's value forward, its row backward) stands in shared memory for every d from -L to L, L the
 // last bucket's start, so an element costs a subtraction, a clamp and a lookup; beyond L on either side all d share a row. Where
 // that table would not fit (L above kLookup), the bucket is searched for element by element. Memory bandwidth bounds the
-// forward: 2 x 16 heads of 1024 x 1024 with a base take 24 us (134 MB, 5.5 TB/s; with one value a lane and a division for each 47).
+// forward: 2 x 16 heads of 1024 x 1024 with a base take 24 us (134 MB, 5.5 TB/s; with one value a lane and a division for each 47);
+// with positions, whose loads and saturating differences every value pays for, 38.
 //
 // Backward: the two far rows, to which most elements belong, are summed in registers; the others go to a histogram
 // in shared memory with a column for each lane, so that no two threads add to one number and the order of all sums is fixed.
-// The CTAs' sums are added in order by a second kernel. 2 x 16 heads of 1003 x 1003 with positions: 26 us for 64 MB, of which the
-// rows' bytes (relpos_rows_kernel) and the sum of the CTAs' sums are 8; the rest waits for memory and shared memory in turn, with the
-// six CTAs of an SM that the histograms leave room for (five 29 us; units two ahead, in more registers, 28.6).
+// The CTAs' sums are added in order by a second kernel. 2 x 16 heads of 1003 x 1003 with positions, 33 buckets: 26 us for 64 MB (27
+// where the input is another one each time), of which the rows' bytes (relpos_rows_kernel) and the sum of the CTAs' sums are 8; the
+// rest waits for memory and shared memory in turn, with the six CTAs of an SM that the histograms leave room for (five 29 us;
+// units two ahead, in more registers, 28.6). With 16 logarithmic buckets to 128, another input each time: 33 us, without positions 30.
 #include <algorithm>
 
 #include "launch.cuh"

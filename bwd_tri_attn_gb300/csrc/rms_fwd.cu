@@ -191,7 +191,9 @@ cudaError_t launch_rms_fwd(const tri_rms_shape &s, const void *x, const void *re
   const bool al = s.C % VEC == 0 && ldx % VEC == 0 && (!res || ldres % VEC == 0) && (at & 15u) == 0 &&
                   (reinterpret_cast<uintptr_t>(q8) & (VEC - 1)) == 0;
   const RmsFwdArgs a{ldx, ldres, s.M, s.C, s.eps, gamma, rstd, s8, q8};
-  // (in step: all tensors' rows equally far from a boundary)
+  // In step: all tensors' rows equally far from a boundary. (With a residual, in step and chunk by chunk: 30000 x 1003 BF16 43 and 89
+  // us, 50000 x 500 37 and 62, 30000 x 509 FP32 39 and 72; where the one chunk more takes twice the threads, too, 30000 x 1021 62 and
+  // 91, 50000 x 511 52 and 74, 100000 x 127 35 and 43, 109876 x 59 21 and 23, 8000 x 4093, the one that does not gain, 90 and 88.)
   auto off = [&](const void *p) { return p ? ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(y)) & 15u) : 0u; };
   const int chunks = (s.C + VEC - 1) / VEC, in_step = step_chunks(s.C, VEC);
   const bool step = !al && !q8 && ldx % VEC == s.C % VEC && (!res || ldres % VEC == s.C % VEC) && !off(x) && !off(res) && !off(r) &&
