@@ -393,7 +393,8 @@ class FeedForwardLayer(torch.nn.Module):
 
 def clip_grad_norm_(parameters, max_norm):
     """Clips the gradients of the parameters (those that have one) in place to the 2-norm max_norm of all of them together
-    and returns their norm before, an FP32 number on the device."""
+    and returns their norm before, an FP32 number on the device. They are on the current device, dense and without gaps, and
+    share no memory."""
     parameters = [parameters] if isinstance(parameters, torch.Tensor) else list(parameters)
     grads = [p.grad for p in parameters if p.grad is not None]
     norm = tb.clip_gradients(grads, max_norm)
