@@ -7,7 +7,8 @@
  * Tensors: n descriptions in host memory, read during the call; each tensor lies in device memory without gaps, in BF16,
  * FP16 or FP32, with any number of elements (none, too). norm: one FP32 number in device memory. The squares
  * are summed in FP32 within 16 elements and in FP64 across them; where FP32 squares would overflow or vanish they are taken in FP64, so that
- * norm is right to FP32 rounding wherever it is an FP32 number. A product is rounded once. An infinity or a NaN among the
+ * norm is right to FP32 rounding wherever it is an FP32 number. A product is rounded once; the factor is an FP32 number, with fewer bits below 2^-126 and
+ * 0 below 2^-150 (max_norm so far below norm). An infinity or a NaN among the
  * gradients shows in norm and, as the formula has it, in the outputs (NaN where norm is NaN; where norm is
  * infinite 0 for the finite ones). A tensor clipped in place that the factor 1 leaves as it is is not written.
  *
